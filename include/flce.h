@@ -346,6 +346,45 @@ flce_status_t flce_f32_to_bf16(const float* src, void* dst, int64_t count, flce_
 flce_status_t flce_forward_noalloc(const flce_problem_t* p, const void* X, const void* W,
                                    const int32_t* labels, float* loss, float* lse, flce_stream_t stream);
 
+/* ----------------------------------------------------------------------------
+ * Layer norm: the norm that makes the head's input.  For each of n rows of h
+ * elements,
+ *   mean = sum_j x_j / h,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / h + eps),
+ *   xhat_j = (x_j - mean) rstd,  y_j = xhat_j weight_j + bias_j,
+ * and backward, with u_j = dy_j weight_j,
+ *   dx_j = rstd (u_j - sum_k u_k / h - xhat_j sum_k u_k xhat_k / h),
+ *   dweight_j = sum_rows dy_j xhat_j,  dbias_j = sum_rows dy_j.
+ *   - x, y, dy and dx share one type, weight, bias and their gradients another
+ *     (flce_dtype_t each); mean and rstd are fp32 [n].  All sums are fp32.
+ *   - Any n >= 0 and h >= 1.  x has a row pitch of x_pitch elements (>= h), so
+ *     rows of a larger tensor (each sequence's last position) are read in
+ *     place; y, dy and dx are dense.  Pointers need the alignment of their type.
+ *   - bias NULL: none is added.  dbias NULL: none is written.  With n = 0
+ *     dweight and dbias are zeros.
+ *   - The sums over rows have a fixed order: the same inputs give the same bits.
+ *   - Non-finite elements make their own row non-finite (and, backward, the
+ *     sums they enter), no other row. */
+typedef enum { FLCE_BF16 = 0, FLCE_F32 = 1 } flce_dtype_t;
+
+typedef struct {
+  int64_t n;        /* rows */
+  int64_t h;        /* elements of a row */
+  int64_t x_pitch;  /* elements from one row of x to the next, >= h */
+  float eps;        /* >= 0 */
+  int32_t x_dtype;  /* flce_dtype_t of x, y, dy, dx */
+  int32_t w_dtype;  /* flce_dtype_t of weight, bias, dweight, dbias */
+} flce_norm_t;
+
+flce_status_t flce_layernorm_forward(const flce_norm_t* q, const void* x, const void* weight, const void* bias,
+                                     void* y, float* mean, float* rstd, flce_stream_t stream);
+
+/* Workspace of flce_layernorm_backward (0 if q is invalid): fp32 partial sums of
+ * dweight and dbias, one row of 2h for each slice of rows.  256-byte aligned. */
+size_t flce_layernorm_workspace_bytes(const flce_norm_t* q);
+flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, const void* x, const void* weight,
+                                      const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                                      void* ws, size_t ws_bytes, flce_stream_t stream);
+
 /* Static description of a status code. */
 const char* flce_status_string(flce_status_t s);
 

@@ -10,6 +10,7 @@ from .binding import (  # noqa: F401
     fwd_bwd, read_device_status, status_string, linear_cross_entropy, logits_footprint_bytes,
     profile_enable, profile_read, KERNEL_KINDS, scale_grads, topk, topk_workspace_bytes, soft_fwd_bwd,
     host_buffer_bytes, fwd_bwd_host, sparse_kl_divergence, shard_workspace_bytes, shard_forward, shard_combine,
-    shard_backward, valid_count, f32_to_bf16,
+    shard_backward, valid_count, f32_to_bf16, layer_norm, layernorm_forward, layernorm_backward,
+    layernorm_workspace_bytes,
 )
 from .sharded import sharded_cross_entropy  # noqa: F401

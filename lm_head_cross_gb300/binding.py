@@ -23,7 +23,8 @@ EXPORTED = ("flce_workspace_bytes", "flce_workspace_bytes_rowchunk", "flce_forwa
             "flce_profile_read", "flce_forward_noalloc", "flce_scale_grads", "flce_topk_workspace_bytes", "flce_topk",
             "flce_soft_fwd_bwd", "flce_soft_fwd_bwd_rowchunk", "flce_host_buffer_bytes", "flce_fwd_bwd_host", "flce_shard_workspace_bytes",
             "flce_shard_forward", "flce_shard_combine", "flce_shard_backward", "flce_valid_count",
-            "flce_f32_to_bf16", "flce_debug_checks", "flce_selftest_bounds", "flce_status_string")
+            "flce_f32_to_bf16", "flce_layernorm_forward", "flce_layernorm_workspace_bytes", "flce_layernorm_backward",
+            "flce_debug_checks", "flce_selftest_bounds", "flce_status_string")
 KERNEL_KINDS = ("forward", "grad", "dxdw", "small")
 
 
@@ -42,6 +43,11 @@ class Problem(ctypes.Structure):
 
 class VocabShard(ctypes.Structure):
     _fields_ = [("v_offset", ctypes.c_int64), ("v_rows", ctypes.c_int64)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("h", ctypes.c_int64), ("x_pitch", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32)]
 
 
 def lib_path() -> str:
@@ -77,6 +83,13 @@ def lib():
     L.flce_valid_count.restype = ctypes.c_int
     L.flce_f32_to_bf16.argtypes = [vp, vp, ctypes.c_int64, vp]
     L.flce_f32_to_bf16.restype = ctypes.c_int
+    Q = ctypes.POINTER(Norm)
+    L.flce_layernorm_forward.argtypes = [Q, vp, vp, vp, vp, vp, vp, vp]
+    L.flce_layernorm_forward.restype = ctypes.c_int
+    L.flce_layernorm_workspace_bytes.argtypes = [Q]
+    L.flce_layernorm_workspace_bytes.restype = sz
+    L.flce_layernorm_backward.argtypes = [Q, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.flce_layernorm_backward.restype = ctypes.c_int
     L.flce_forward_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp]
     L.flce_forward_noalloc.restype = ctypes.c_int
     L.flce_forward.argtypes = [P, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -625,3 +638,119 @@ def sparse_kl_divergence(x, w, tgt_idx, tgt_prob, reduction: str = "mean", rowch
     idx = tgt_idx.reshape(-1, k).to(torch.int32).contiguous()
     q = tgt_prob.reshape(-1, k).to(torch.float32).contiguous()
     return _SparseKL.get().apply(x2, w.contiguous(), idx, q, reduction, bool(rowchunk))
+
+
+def _dtype(t, name):
+    """flce_dtype_t of a tensor: 0 bf16, 1 fp32."""
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _allocating(stream):
+    """Allocations inside belong to ``stream`` (the current one when None): the caching
+    allocator then reuses them only after that stream's work."""
+    import contextlib
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _norm(x, weight, bias, eps):
+    if x.dim() != 2 or weight.dim() != 1 or weight.shape[0] != x.shape[1]:
+        raise ValueError(f"x must be [N, H] and weight [H], got {tuple(x.shape)} and {tuple(weight.shape)}")
+    if bias is not None and (bias.shape != weight.shape or bias.dtype != weight.dtype):
+        raise ValueError("bias must have weight's shape and dtype")
+    n, h = x.shape
+    if h < 1:
+        raise ValueError("x has no columns")
+    if not (x.is_cuda and weight.is_cuda and (bias is None or bias.is_cuda)):
+        raise ValueError("x, weight and bias must be CUDA tensors")
+    if (h > 1 and x.stride(1) != 1) or (n > 1 and x.stride(0) < h):
+        raise ValueError("the rows of x must be contiguous and must not overlap")
+    if not (weight.is_contiguous() and (bias is None or bias.is_contiguous())):
+        raise ValueError("weight and bias must be contiguous")
+    return Norm(n, h, x.stride(0) if n > 1 else h, float(eps), _dtype(x, "x"), _dtype(weight, "weight"))
+
+
+def layernorm_forward(x, weight, bias=None, eps=1e-5, stream=None):
+    """Layer norm of the rows of x [N, H] (bf16 or fp32; the rows may be those of a larger
+    tensor).  weight, bias: [H], bf16 or fp32.  Returns (y [N, H] of x's type, mean [N],
+    rstd [N] fp32)."""
+    torch = _torch()
+    q = _norm(x, weight, bias, eps)
+    with _allocating(stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        mean = torch.empty(q.n, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(q.n, dtype=torch.float32, device=x.device)
+    _call("flce_layernorm_forward", lib().flce_layernorm_forward(
+        ctypes.byref(q), x.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(), y.data_ptr(),
+        mean.data_ptr(), rstd.data_ptr(), _stream_ptr(stream)))
+    return y, mean, rstd
+
+
+def layernorm_workspace_bytes(n, h) -> int:
+    return int(lib().flce_layernorm_workspace_bytes(ctypes.byref(Norm(int(n), int(h), int(h), 0.0, 0, 0))))
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, bias=True, ws=None, stream=None):
+    """Gradients of layernorm_forward.  Returns (dx of x's type, dweight, dbias of weight's
+    type, ws); ``bias=False``: dbias is None."""
+    torch = _torch()
+    q = _norm(x, weight, None, 0.0)
+    if dy.shape != x.shape or dy.dtype != x.dtype or not dy.is_contiguous() or not dy.is_cuda:
+        raise ValueError("dy must be a contiguous CUDA tensor of x's shape and dtype")
+    _f32(mean, (q.n,), "mean")
+    _f32(rstd, (q.n,), "rstd")
+    with _allocating(stream):
+        if ws is None:
+            ws = torch.empty(int(lib().flce_layernorm_workspace_bytes(ctypes.byref(q))), dtype=torch.uint8,
+                             device=x.device)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dweight = torch.empty_like(weight)
+        dbias = torch.empty_like(weight) if bias else None
+    _call("flce_layernorm_backward", lib().flce_layernorm_backward(
+        ctypes.byref(q), dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr() if bias else None, ws.data_ptr(), ws.numel(),
+        _stream_ptr(stream)))
+    return dx, dweight, dbias, ws
+
+
+class _LayerNorm:
+    """torch.autograd.Function over layernorm_forward / layernorm_backward."""
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            torch = _torch()
+
+            class Fn(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, x2, weight, bias, eps):
+                    y, mean, rstd = layernorm_forward(x2, weight, bias, eps)
+                    ctx.save_for_backward(x2, weight, mean, rstd)
+                    ctx.has_bias = bias is not None
+                    return y
+
+                @staticmethod
+                def backward(ctx, dy):
+                    x2, weight, mean, rstd = ctx.saved_tensors
+                    dx, dweight, dbias, _ = layernorm_backward(dy.contiguous(), x2, weight, mean, rstd,
+                                                               bias=ctx.has_bias)
+                    return dx, dweight, dbias, None
+
+            cls.fn = Fn
+        return cls.fn
+
+
+def layer_norm(x, weight, bias=None, eps: float = 1e-5):
+    """Layer norm over the last dimension of x [..., H] (bf16 or fp32 CUDA); weight and bias
+    [H], bf16 or fp32.  Autograd flows to x, weight and bias."""
+    h = x.shape[-1]
+    x2 = x.reshape(-1, h)
+    if h > 1 and x2.stride(1) != 1 or (x2.shape[0] > 1 and x2.stride(0) < h):
+        x2 = x2.contiguous()
+    y = _LayerNorm.get().apply(x2, weight.contiguous(), None if bias is None else bias.contiguous(), float(eps))
+    return y.reshape(x.shape)

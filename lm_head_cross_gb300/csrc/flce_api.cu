@@ -1307,6 +1307,77 @@ flce_status_t flce_f32_to_bf16(const float* src, void* dst, int64_t count, flce_
   return cuda_status(timed(3, 0.0, s, [&] { return launch_f32_to_bf16(src, dst, count, s); }));
 }
 
+// ----------------------------------------------------------------------------- layer norm
+
+namespace {
+
+size_t dtype_bytes(int32_t dtype) { return dtype == FLCE_F32 ? 4 : 2; }
+bool known_dtype(int32_t dtype) { return dtype == FLCE_BF16 || dtype == FLCE_F32; }
+
+flce_status_t check_norm(const flce_norm_t* q, NormParams* out) {
+  if (!q || q->n < 0 || q->h < 1 || q->x_pitch < q->h || !(q->eps >= 0.f)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!known_dtype(q->x_dtype) || !known_dtype(q->w_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
+  // columns are 32-bit; element offsets are 64-bit
+  if (q->h > (int64_t{1} << 20) || q->n > (int64_t{1} << 40) / q->x_pitch) return FLCE_ERR_UNSUPPORTED_SHAPE;
+  *out = NormParams{q->n, static_cast<int>(q->h), q->x_pitch, q->eps, q->x_dtype == FLCE_F32, q->w_dtype == FLCE_F32};
+  return FLCE_OK;
+}
+
+}  // namespace
+
+flce_status_t flce_layernorm_forward(const flce_norm_t* q, const void* x, const void* weight, const void* bias,
+                                     void* y, float* mean, float* rstd, flce_stream_t stream) {
+  NormParams np;
+  flce_status_t st = check_norm(q, &np);
+  if (st != FLCE_OK) return st;
+  if (!weight || (q->n > 0 && (!x || !y || !mean || !rstd))) return FLCE_ERR_INVALID_ARGUMENT;
+  const size_t xa = dtype_bytes(q->x_dtype), wa = dtype_bytes(q->w_dtype);
+  if (!aligned(x, xa) || !aligned(y, xa) || !aligned(weight, wa) || !aligned(bias, wa) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return FLCE_ERR_MISALIGNED;
+  if (q->n == 0) return FLCE_OK;
+  Device dev;
+  st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(
+      timed(3, 0.0, s, [&] { return launch_norm_forward(np, x, weight, bias, y, mean, rstd, s); }));
+}
+
+size_t flce_layernorm_workspace_bytes(const flce_norm_t* q) {
+  NormParams np;
+  if (check_norm(q, &np) != FLCE_OK) return 0;
+  return align_up(static_cast<size_t>(norm_slices(np.n)) * 2 * static_cast<size_t>(np.h) * sizeof(float));
+}
+
+flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, const void* x, const void* weight,
+                                      const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                                      void* ws, size_t ws_bytes, flce_stream_t stream) {
+  NormParams np;
+  flce_status_t st = check_norm(q, &np);
+  if (st != FLCE_OK) return st;
+  if (!weight || !dweight || !ws || (q->n > 0 && (!dy || !x || !mean || !rstd || !dx)))
+    return FLCE_ERR_INVALID_ARGUMENT;
+  const size_t xa = dtype_bytes(q->x_dtype), wa = dtype_bytes(q->w_dtype);
+  if (!aligned(dy, xa) || !aligned(x, xa) || !aligned(dx, xa) || !aligned(weight, wa) || !aligned(dweight, wa) ||
+      !aligned(dbias, wa) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(ws, kAlign))
+    return FLCE_ERR_MISALIGNED;
+  if (ws_bytes < flce_layernorm_workspace_bytes(q)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (q->n == 0) {
+    const size_t bytes = wa * static_cast<size_t>(q->h);
+    if (cudaMemsetAsync(dweight, 0, bytes, s) != cudaSuccess) return FLCE_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, bytes, s) != cudaSuccess) return FLCE_ERR_CUDA;
+    return FLCE_OK;
+  }
+  Device dev;
+  st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  return cuda_status(timed(3, 0.0, s, [&] {
+    return launch_norm_backward(np, dy, x, weight, mean, rstd, dx, dweight, dbias, static_cast<float*>(ws), s);
+  }));
+}
+
 flce_status_t flce_profile_enable(int mask) {
   Profiler& P = profiler();
   std::lock_guard<std::mutex> lock(P.mu);

@@ -227,6 +227,21 @@ cudaError_t launch_timeout_selftest(int* status, uint64_t limit_ns, cudaStream_t
 // FLCE_DEBUG_CHECKS record kErrBounds (and touch no memory), release builds nothing.
 cudaError_t launch_bounds_selftest(int* status, cudaStream_t stream);
 
+// Layer norm (flce_norm.cu).
+struct NormParams {
+  int64_t n;
+  int h;
+  int64_t x_pitch;
+  float eps;
+  bool x_f32, w_f32;  // else bf16
+};
+int norm_slices(int64_t n);  // rows of partial sums the backward pass keeps in its workspace
+cudaError_t launch_norm_forward(const NormParams& q, const void* x, const void* weight, const void* bias, void* y,
+                                float* mean, float* rstd, cudaStream_t stream);
+cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void* x, const void* weight,
+                                 const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                                 float* part, cudaStream_t stream);
+
 // Limit of every bounded wait in the kernels, in nanoseconds: FLCE_TIMEOUT_NS
 // from the environment (read once), else 4 s.
 uint64_t timeout_ns();

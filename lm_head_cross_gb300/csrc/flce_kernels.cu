@@ -36,6 +36,7 @@
 
 #include "flce_device.cuh"
 #include "flce_internal.h"
+#include "flce_launch.cuh"
 
 namespace flce {
 
@@ -1838,24 +1839,6 @@ __global__ void bounds_selftest_kernel(int* status) {
 
 int tc_smem_bytes() { return Cfg<kModeForward>::kSmemBytes; }
 int tc_topk_subranges() { return Cfg<kModeTopk>::kEpiWarps / 4; }
-
-// Every launch carries the programmatic-stream-serialization attribute (see
-// griddep_begin): a kernel may be scheduled while its predecessor drains.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                     Args&&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
 
 template <int MODE>
 static cudaError_t launch_mode(const TcMaps& maps, const TcParams& p, int grid, cudaStream_t stream) {
