@@ -385,6 +385,57 @@ flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, cons
                                       const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
                                       void* ws, size_t ws_bytes, flce_stream_t stream);
 
+/* ----------------------------------------------------------------------------
+ * AdamW: one step over many tensors.  For every element, with the gradient
+ * g = grad * grad_scale (a device fp32 scalar; NULL: 1),
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr wd) - (lr / (1 - beta1^step)) m / (sqrt(v / (1 - beta2^step)) + eps).
+ * All arithmetic is fp32.
+ *   - param and grad: bf16 or fp32 each.  With `master` (fp32) the step is taken
+ *     on the master weights and param receives their rounding; without it on
+ *     param itself.
+ *   - state_bits 32: exp_avg (m) and exp_avg_sq (v) are fp32 [count].
+ *   - state_bits 8: exp_avg holds m and exp_avg_sq holds r = sqrt(v), each as one
+ *     e4m3 byte an element with an fp32 scale for each FLCE_ADAMW_BLOCK elements
+ *     (the last block of a tensor may be shorter): value = byte * scale, scale =
+ *     the block's largest magnitude / 448.  m is rounded to nearest.  r is rounded
+ *     up with a probability equal to the fraction of the step it has passed, by
+ *     a hash of (step, element), so that a running mean that moves by less than
+ *     an 8-bit step moves at all; a non-zero r never becomes zero.  The same
+ *     step on the same inputs gives the same bits.  A block that holds a
+ *     non-finite moment becomes NaN as a whole; one whose moments are all below
+ *     1e-35 becomes zero.
+ *   - Tensors are updated in place and must not overlap.  Pointers need the
+ *     alignment of their type.  lr and weight_decay are per tensor.
+ *   - tensors is a HOST array, read before the call returns; the step holds no
+ *     device memory of its own. */
+#define FLCE_ADAMW_BLOCK 256
+
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;            /* or NULL */
+  void* exp_avg;            /* m */
+  void* exp_avg_sq;         /* v, or in 8 bits r = sqrt(v) */
+  float* exp_avg_scale;     /* 8-bit states: [ceil(count / FLCE_ADAMW_BLOCK)], else ignored */
+  float* exp_avg_sq_scale;
+  int64_t count;            /* elements; 0 is skipped */
+  float lr;
+  float weight_decay;
+  int32_t param_dtype;      /* flce_dtype_t */
+  int32_t grad_dtype;
+} flce_adamw_tensor_t;
+
+typedef struct {
+  double beta1, beta2;      /* in [0, 1) */
+  double eps;               /* >= 0 */
+  int64_t step;             /* this step's number, from 1 */
+  int32_t state_bits;       /* 32 or 8, for every tensor of the call */
+} flce_adamw_t;
+
+flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count, const flce_adamw_t* opt,
+                              const float* grad_scale, flce_stream_t stream);
+
 /* Static description of a status code. */
 const char* flce_status_string(flce_status_t s);
 

@@ -2,8 +2,9 @@
 
 Python binding over the C-ABI library ``libflce.so`` (declared in
 ``include/flce.h``).  Every step of the computation runs in the library's CUDA
-kernels; this module only marshals arguments.  See ``binding`` for the calls
-and ``sharded`` for the vocabulary- and sequence-sharded loss across ranks.
+kernels; this module only marshals arguments.  See ``binding`` for the calls,
+``optim`` for AdamW and ``sharded`` for the vocabulary- and sequence-sharded loss
+across ranks.
 """
 from .binding import (  # noqa: F401
     FlceError, Problem, VocabShard, lib, lib_path, workspace_bytes, workspace_bytes_rowchunk, forward, backward,
@@ -13,4 +14,5 @@ from .binding import (  # noqa: F401
     shard_backward, valid_count, f32_to_bf16, layer_norm, layernorm_forward, layernorm_backward,
     layernorm_workspace_bytes,
 )
+from .optim import AdamW, adamw_plan, adamw_step  # noqa: F401
 from .sharded import sharded_cross_entropy  # noqa: F401

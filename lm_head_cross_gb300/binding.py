@@ -24,6 +24,7 @@ EXPORTED = ("flce_workspace_bytes", "flce_workspace_bytes_rowchunk", "flce_forwa
             "flce_soft_fwd_bwd", "flce_soft_fwd_bwd_rowchunk", "flce_host_buffer_bytes", "flce_fwd_bwd_host", "flce_shard_workspace_bytes",
             "flce_shard_forward", "flce_shard_combine", "flce_shard_backward", "flce_valid_count",
             "flce_f32_to_bf16", "flce_layernorm_forward", "flce_layernorm_workspace_bytes", "flce_layernorm_backward",
+            "flce_adamw_step",
             "flce_debug_checks", "flce_selftest_bounds", "flce_status_string")
 KERNEL_KINDS = ("forward", "grad", "dxdw", "small")
 
@@ -48,6 +49,18 @@ class VocabShard(ctypes.Structure):
 class Norm(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("h", ctypes.c_int64), ("x_pitch", ctypes.c_int64), ("eps", ctypes.c_float),
                 ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("count", ctypes.c_int64), ("lr", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class AdamwOptions(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("state_bits", ctypes.c_int32)]
 
 
 def lib_path() -> str:
@@ -90,6 +103,8 @@ def lib():
     L.flce_layernorm_workspace_bytes.restype = sz
     L.flce_layernorm_backward.argtypes = [Q, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.flce_layernorm_backward.restype = ctypes.c_int
+    L.flce_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), ctypes.c_int32, ctypes.POINTER(AdamwOptions), vp, vp]
+    L.flce_adamw_step.restype = ctypes.c_int
     L.flce_forward_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp]
     L.flce_forward_noalloc.restype = ctypes.c_int
     L.flce_forward.argtypes = [P, vp, vp, vp, vp, vp, vp, sz, vp]

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
@@ -873,6 +874,68 @@ flce_status_t copy_events(CopyEvents** out) {
   return FLCE_OK;
 }
 
+size_t dtype_bytes(int32_t dtype) { return dtype == FLCE_F32 ? 4 : 2; }
+bool known_dtype(int32_t dtype) { return dtype == FLCE_BF16 || dtype == FLCE_F32; }
+
+flce_status_t check_adamw_tensor(const flce_adamw_tensor_t& t, bool eight) {
+  if (t.count < 0 || !known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (t.count == 0) return FLCE_OK;
+  if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return FLCE_ERR_INVALID_ARGUMENT;
+  if (eight && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (t.count > int64_t{kAdamwChunk} << 30) return FLCE_ERR_UNSUPPORTED_SHAPE;
+  const size_t sa = eight ? 1 : 4;
+  if (!aligned(t.param, dtype_bytes(t.param_dtype)) || !aligned(t.grad, dtype_bytes(t.grad_dtype)) ||
+      !aligned(t.master, 4) || !aligned(t.exp_avg, sa) || !aligned(t.exp_avg_sq, sa) ||
+      (eight && (!aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4))))
+    return FLCE_ERR_MISALIGNED;
+  return FLCE_OK;
+}
+
+// Launches over tensors [0, count), as many of them at a time as one kernel argument
+// holds (and as 32-bit chunk numbers reach).
+template <int N>
+flce_status_t adamw_launches(const flce_adamw_tensor_t* tensors, int count, const flce_adamw_t& o,
+                             const float* grad_scale, cudaStream_t stream) {
+  const double bc1 = 1.0 - std::pow(o.beta1, static_cast<double>(o.step));
+  const double bc2 = 1.0 - std::pow(o.beta2, static_cast<double>(o.step));
+  const bool eight = o.state_bits == 8;
+  AdamwArgs<N> a;
+  a.beta1 = static_cast<float>(o.beta1);
+  a.omb1 = static_cast<float>(1.0 - o.beta1);
+  a.beta2 = static_cast<float>(o.beta2);
+  a.omb2 = static_cast<float>(1.0 - o.beta2);
+  a.inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
+  a.eps = static_cast<float>(o.eps);
+  a.step_key = static_cast<uint32_t>(static_cast<uint64_t>(o.step) * 0xA511E9B3ull);
+  a.grad_scale = grad_scale;
+  for (int i = 0; i < count;) {
+    a.tensors = 0;
+    int64_t chunks = 0;
+    for (; i < count && a.tensors < N; ++i) {
+      const flce_adamw_tensor_t& t = tensors[i];
+      if (t.count == 0) continue;
+      const int64_t c = (t.count + kAdamwChunk - 1) / kAdamwChunk;
+      if (chunks + c > 0x7fffffff) break;
+      const bool vec = aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.master, 16) &&
+                       aligned(t.exp_avg, 16) && aligned(t.exp_avg_sq, 16);
+      a.t[a.tensors++] = AdamwTensor{t.param, t.grad, t.master, t.exp_avg, t.exp_avg_sq,
+                                     eight ? t.exp_avg_scale : nullptr, eight ? t.exp_avg_sq_scale : nullptr, t.count,
+                                     static_cast<float>(1.0 - static_cast<double>(t.lr) * t.weight_decay),
+                                     static_cast<float>(t.lr / bc1),
+                                     (t.param_dtype == FLCE_F32 ? kAdamwParamF32 : 0u) |
+                                         (t.grad_dtype == FLCE_F32 ? kAdamwGradF32 : 0u) |
+                                         (vec ? kAdamwAligned : 0u),
+                                     static_cast<uint32_t>(chunks)};
+      chunks += c;
+    }
+    if (a.tensors == 0) break;
+    a.chunks = static_cast<uint32_t>(chunks);
+    flce_status_t st = cuda_status(timed(3, 0.0, stream, [&] { return launch_adamw<N>(a, o.state_bits, stream); }));
+    if (st != FLCE_OK) return st;
+  }
+  return FLCE_OK;
+}
+
 }  // namespace
 
 int chunk_width(int64_t n) { return n <= 16384 ? 8192 : 4096; }
@@ -1311,9 +1374,6 @@ flce_status_t flce_f32_to_bf16(const float* src, void* dst, int64_t count, flce_
 
 namespace {
 
-size_t dtype_bytes(int32_t dtype) { return dtype == FLCE_F32 ? 4 : 2; }
-bool known_dtype(int32_t dtype) { return dtype == FLCE_BF16 || dtype == FLCE_F32; }
-
 flce_status_t check_norm(const flce_norm_t* q, NormParams* out) {
   if (!q || q->n < 0 || q->h < 1 || q->x_pitch < q->h || !(q->eps >= 0.f)) return FLCE_ERR_INVALID_ARGUMENT;
   if (!known_dtype(q->x_dtype) || !known_dtype(q->w_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
@@ -1376,6 +1436,30 @@ flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, cons
   return cuda_status(timed(3, 0.0, s, [&] {
     return launch_norm_backward(np, dy, x, weight, mean, rstd, dx, dweight, dbias, static_cast<float*>(ws), s);
   }));
+}
+
+// ----------------------------------------------------------------------------- AdamW
+
+flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count, const flce_adamw_t* opt,
+                              const float* grad_scale, flce_stream_t stream) {
+  if (!opt || count < 0 || (count > 0 && !tensors)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!(opt->beta1 >= 0.0 && opt->beta1 < 1.0) || !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) || !(opt->eps >= 0.0) ||
+      opt->step < 1 || (opt->state_bits != 32 && opt->state_bits != 8))
+    return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(grad_scale, 4)) return FLCE_ERR_MISALIGNED;
+  int live = 0;
+  for (int i = 0; i < count; ++i) {
+    flce_status_t st = check_adamw_tensor(tensors[i], opt->state_bits == 8);
+    if (st != FLCE_OK) return st;
+    live += tensors[i].count > 0;
+  }
+  if (live == 0) return FLCE_OK;
+  Device dev;
+  flce_status_t st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return live <= kAdamwFewTensors ? adamw_launches<kAdamwFewTensors>(tensors, count, *opt, grad_scale, s)
+                                  : adamw_launches<kAdamwManyTensors>(tensors, count, *opt, grad_scale, s);
 }
 
 flce_status_t flce_profile_enable(int mask) {

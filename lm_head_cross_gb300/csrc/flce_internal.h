@@ -242,6 +242,42 @@ cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void
                                  const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
                                  float* part, cudaStream_t stream);
 
+// AdamW (flce_adamw.cu).  The tensors travel as a kernel argument, so a step needs no
+// table in device memory; an argument holds at most 32764 bytes.
+constexpr int kAdamwBlock = 256;   // elements of one 8-bit scale
+constexpr int kAdamwChunk = 4096;  // elements of one thread block
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t count;
+  float decay;     // 1 - lr wd
+  float rate;      // lr / (1 - beta1^step)
+  uint32_t flags;  // kAdamwParamF32 | ...
+  uint32_t chunk0; // chunks of the tensors before this one
+};
+enum : uint32_t { kAdamwParamF32 = 1, kAdamwGradF32 = 2, kAdamwAligned = 4 };
+constexpr int kAdamwManyTensors = 400;
+constexpr int kAdamwFewTensors = 16;
+template <int N>
+struct AdamwArgs {
+  AdamwTensor t[N];
+  int tensors;
+  uint32_t chunks;
+  float beta1, omb1, beta2, omb2;  // omb = 1 - beta
+  float inv_root_bc2;              // 1 / sqrt(1 - beta2^step)
+  float eps;
+  uint32_t step_key;               // of the 8-bit rounding's hash
+  const float* grad_scale;
+};
+static_assert(sizeof(AdamwArgs<kAdamwManyTensors>) <= 32764, "kernel argument limit");
+template <int N>
+cudaError_t launch_adamw(const AdamwArgs<N>& a, int state_bits, cudaStream_t stream);
+
 // Limit of every bounded wait in the kernels, in nanoseconds: FLCE_TIMEOUT_NS
 // from the environment (read once), else 4 s.
 uint64_t timeout_ns();
