@@ -347,6 +347,37 @@ flce_status_t flce_forward_noalloc(const flce_problem_t* p, const void* X, const
                                    const int32_t* labels, float* loss, float* lse, flce_stream_t stream);
 
 /* ----------------------------------------------------------------------------
+ * Token log probabilities: the distribution softmax(x_i W^T / T) of each row, as
+ * scoring, sampling with reported alternatives and policy-gradient training read
+ * it, without the [N,V] logits.  With z_ij = x_i . w_j / T (T = temperature > 0):
+ *   lse_i = log sum_j exp(z_ij),   p_ij = exp(z_ij - lse_i)
+ *   logprob_i = z_{i,t_i} - lse_i, t_i = tokens[i]; 0 where t_i = ignore_index
+ *   entropy_i = -sum_j p_ij log p_ij   (of every row, ignored or not)
+ *   top_ids[i, :]: the k ids with the largest x_i . w_j, high to low (equal: lower
+ *   id first), top_logprobs[i, :] = z_ij - lse_i there.  0 <= k <= 16.  With k > V the
+ *   ids past V are -1 and their log probabilities minus infinity.
+ * p->shift scores row i against tokens[i + 1] as labels are; p->reduction is not
+ * used.  tokens NULL: no token is given (logprob must be NULL too).  logprob and
+ * entropy may be NULL; top_ids and top_logprobs are not used when k = 0. */
+size_t flce_token_logprobs_workspace_bytes(const flce_problem_t* p, int32_t k);
+flce_status_t flce_token_logprobs(const flce_problem_t* p, int32_t k, float temperature, const void* X, const void* W,
+                                  const int32_t* tokens, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                                  float* top_logprobs, void* ws, size_t ws_bytes, flce_stream_t stream);
+
+/* Gradients of sum_i (gl_i logprob_i + ge_i entropy_i), gl = grad_logprob and
+ * ge = grad_entropy (fp32 [N]; NULL: zeros), given lse and entropy from the call
+ * above on the same X, W, tokens and temperature:
+ *   dz_ij = gl_i ([j = t_i] - p_ij) - ge_i p_ij (log p_ij + entropy_i),
+ *   dX = dz W / T,  dW = dz^T X / T   (bf16, fp32 accumulation).
+ * Rows whose token is ignored take gl_i = 0.  Runs on the bounded workspace of
+ * flce_workspace_bytes(p): the logits are recomputed chunk by chunk, dz is held in
+ * bf16.  entropy may be NULL where grad_entropy is. */
+flce_status_t flce_token_logprobs_backward(const flce_problem_t* p, float temperature, const void* X, const void* W,
+                                           const int32_t* tokens, const float* lse, const float* entropy,
+                                           const float* grad_logprob, const float* grad_entropy, void* dX, void* dW,
+                                           void* ws, size_t ws_bytes, flce_stream_t stream);
+
+/* ----------------------------------------------------------------------------
  * Layer norm: the norm that makes the head's input.  For each of n rows of h
  * elements,
  *   mean = sum_j x_j / h,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / h + eps),

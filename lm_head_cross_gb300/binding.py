@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -24,7 +25,8 @@ EXPORTED = ("flce_workspace_bytes", "flce_workspace_bytes_rowchunk", "flce_forwa
             "flce_soft_fwd_bwd", "flce_soft_fwd_bwd_rowchunk", "flce_host_buffer_bytes", "flce_fwd_bwd_host", "flce_shard_workspace_bytes",
             "flce_shard_forward", "flce_shard_combine", "flce_shard_backward", "flce_valid_count",
             "flce_f32_to_bf16", "flce_layernorm_forward", "flce_layernorm_workspace_bytes", "flce_layernorm_backward",
-            "flce_adamw_step",
+            "flce_adamw_step", "flce_token_logprobs", "flce_token_logprobs_workspace_bytes",
+            "flce_token_logprobs_backward",
             "flce_debug_checks", "flce_selftest_bounds", "flce_status_string")
 KERNEL_KINDS = ("forward", "grad", "dxdw", "small")
 
@@ -105,6 +107,12 @@ def lib():
     L.flce_layernorm_backward.restype = ctypes.c_int
     L.flce_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), ctypes.c_int32, ctypes.POINTER(AdamwOptions), vp, vp]
     L.flce_adamw_step.restype = ctypes.c_int
+    L.flce_token_logprobs_workspace_bytes.argtypes = [P, ctypes.c_int32]
+    L.flce_token_logprobs_workspace_bytes.restype = sz
+    L.flce_token_logprobs.argtypes = [P, ctypes.c_int32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.flce_token_logprobs.restype = ctypes.c_int
+    L.flce_token_logprobs_backward.argtypes = [P, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.flce_token_logprobs_backward.restype = ctypes.c_int
     L.flce_forward_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp]
     L.flce_forward_noalloc.restype = ctypes.c_int
     L.flce_forward.argtypes = [P, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -769,3 +777,152 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5):
         x2 = x2.contiguous()
     y = _LayerNorm.get().apply(x2, weight.contiguous(), None if bias is None else bias.contiguous(), float(eps))
     return y.reshape(x.shape)
+
+
+class TokenLogprobs(NamedTuple):
+    """What logprobs_forward and token_logprobs return for each row: the given token's log
+    probability (None without tokens), the entropy, the log-sum-exp, and the top alternatives'
+    ids and log probabilities (None when top = 0)."""
+    logprob: object
+    entropy: object
+    lse: object
+    top_ids: object
+    top_logprobs: object
+
+
+def _check_head(x, w, tokens):
+    torch = _torch()
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"x must be [N, H] and w [V, H], got {tuple(x.shape)} and {tuple(w.shape)}")
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise TypeError("x and w must be bfloat16")
+    if not (x.is_cuda and w.is_cuda and x.is_contiguous() and w.is_contiguous()):
+        raise ValueError("x and w must be contiguous CUDA tensors")
+    if tokens is not None:
+        if tokens.dtype != torch.int32:
+            raise TypeError("tokens must be int32")
+        if tokens.shape != (x.shape[0],) or not tokens.is_cuda or not tokens.is_contiguous():
+            raise ValueError("tokens must be a contiguous CUDA tensor [N]")
+
+
+def token_logprobs_workspace_bytes(n, h, v, top=0) -> int:
+    return int(lib().flce_token_logprobs_workspace_bytes(ctypes.byref(_problem(n, h, v, -100, "none")), int(top)))
+
+
+def logprobs_forward(x, w, tokens=None, top=0, temperature=1.0, ignore_index=-100, shift=0, seq_len=0, ws=None,
+                     stream=None, check=False):
+    """Log probabilities of ``tokens`` [N] int32 under softmax(x @ w.T / temperature), with each
+    row's entropy, log-sum-exp and ``top`` (at most 16) alternatives.  Returns (TokenLogprobs, ws)."""
+    torch = _torch()
+    _check_head(x, w, tokens)
+    n, h = x.shape
+    p = _problem(n, h, w.shape[0], ignore_index, "none", shift, seq_len)
+    top, dev, f32 = int(top), x.device, torch.float32
+    with _allocating(stream):
+        if ws is None:
+            nbytes = int(lib().flce_token_logprobs_workspace_bytes(ctypes.byref(p), top))
+            if nbytes == 0:
+                raise FlceError(1, "flce_token_logprobs_workspace_bytes")
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        lp = None if tokens is None else torch.empty(n, dtype=f32, device=dev)
+        entropy, lse = torch.empty(n, dtype=f32, device=dev), torch.empty(n, dtype=f32, device=dev)
+        ids = torch.empty(n, top, dtype=torch.int32, device=dev) if top > 0 else None
+        tlp = torch.empty(n, top, dtype=f32, device=dev) if top > 0 else None
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _call("flce_token_logprobs", lib().flce_token_logprobs(
+        ctypes.byref(p), top, float(temperature), x.data_ptr(), w.data_ptr(), ptr(tokens), ptr(lp), entropy.data_ptr(),
+        lse.data_ptr(), ptr(ids), ptr(tlp), ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
+    if check:
+        _call("device", read_device_status(ws, stream))
+    return TokenLogprobs(lp, entropy, lse, ids, tlp), ws
+
+
+def logprobs_backward(x, w, tokens, lse, entropy, grad_logprob=None, grad_entropy=None, temperature=1.0,
+                      ignore_index=-100, shift=0, seq_len=0, ws=None, stream=None, check=False):
+    """Gradients of sum(grad_logprob * logprob + grad_entropy * entropy) given logprobs_forward's
+    lse and entropy.  grad_logprob, grad_entropy: fp32 [N], or None.  Returns (dX, dW, ws)."""
+    torch = _torch()
+    _check_head(x, w, tokens)
+    n, h = x.shape
+    _f32(lse, (n,), "lse")
+    if grad_logprob is not None:
+        _f32(grad_logprob, (n,), "grad_logprob")
+        if tokens is None:
+            raise ValueError("grad_logprob needs tokens")
+    if grad_entropy is not None:
+        _f32(grad_entropy, (n,), "grad_entropy")
+        if entropy is None:
+            raise ValueError("grad_entropy needs entropy")
+    if entropy is not None:
+        _f32(entropy, (n,), "entropy")
+    p = _problem(n, h, w.shape[0], ignore_index, "none", shift, seq_len)
+    with _allocating(stream):
+        if ws is None:
+            ws = _alloc_ws(n, h, w.shape[0], ignore_index, "none", x.device)
+        dX, dW = torch.empty_like(x), torch.empty_like(w)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _call("flce_token_logprobs_backward", lib().flce_token_logprobs_backward(
+        ctypes.byref(p), float(temperature), x.data_ptr(), w.data_ptr(), ptr(tokens), lse.data_ptr(), ptr(entropy),
+        ptr(grad_logprob), ptr(grad_entropy), dX.data_ptr(), dW.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream_ptr(stream)))
+    if check:
+        _call("device", read_device_status(ws, stream))
+    return dX, dW, ws
+
+
+class _TokenLogprobs:
+    """torch.autograd.Function over logprobs_forward / logprobs_backward; gradients flow through
+    the log probabilities and the entropies."""
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            torch = _torch()
+
+            class Fn(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, x2, w, tokens, top, kw):
+                    r, _ = logprobs_forward(x2, w, tokens, top=top, **kw)
+                    ctx.save_for_backward(x2, w, r.lse, r.entropy, *(() if tokens is None else (tokens,)))
+                    ctx.kw = kw
+                    ctx.mark_non_differentiable(*(t for t in (r.lse, r.top_ids, r.top_logprobs) if t is not None))
+                    ctx.set_materialize_grads(False)
+                    return tuple(r)
+
+                @staticmethod
+                def backward(ctx, g_logprob, g_entropy, *_):
+                    x2, w, lse, entropy, *rest = ctx.saved_tensors
+                    if g_logprob is None and g_entropy is None:
+                        return None, None, None, None, None
+                    g = [None if t is None else t.to(torch.float32).contiguous() for t in (g_logprob, g_entropy)]
+                    dX, dW, _ = logprobs_backward(x2, w, rest[0] if rest else None, lse, entropy, *g, **ctx.kw)
+                    return dX, dW, None, None, None
+
+            cls.fn = Fn
+        return cls.fn
+
+
+def token_logprobs(x, w, tokens=None, top: int = 0, temperature: float = 1.0, ignore_index: int = -100,
+                   shift: int = 0):
+    """Log probabilities of given tokens under softmax(x @ w.T / temperature), with entropies and
+    top alternatives, without materialising the logits.
+
+    x: [..., H] bf16 CUDA, w: [V, H] bf16, tokens: [...] integer (same leading shape as x), or
+    None.  Rows whose token is ignore_index have log probability 0 and pass no gradient through
+    it; their entropy and alternatives are those of any row.  top: alternatives per row (at most
+    16), by logit, the lower id first among equals.  shift=1 scores position t of each sequence
+    against the token at t + 1.  Returns TokenLogprobs shaped like x's leading dimensions;
+    autograd flows from logprob and entropy to x and w.
+    """
+    torch = _torch()
+    h, lead = x.shape[-1], x.shape[:-1]
+    seq_len = 0
+    if shift:
+        if x.dim() < 3:
+            raise ValueError("shift=1 needs x shaped [B, S, H]")
+        seq_len = int(x.shape[-2])
+    tok = None if tokens is None else tokens.reshape(-1).to(torch.int32).contiguous()
+    kw = dict(temperature=float(temperature), ignore_index=int(ignore_index), shift=int(shift), seq_len=seq_len)
+    r = _TokenLogprobs.get().apply(x.reshape(-1, h).contiguous(), w.contiguous(), tok, int(top), kw)
+    return TokenLogprobs(*(None if t is None else t.reshape(lead + t.shape[1:]) for t in r))

@@ -18,6 +18,7 @@ namespace flce {
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int32_t kMaxShardParts = 1 << 16;  // most vocabulary shards flce_shard_combine takes
 #ifdef FLCE_DEBUG_CHECKS
 constexpr int kDebugChecksBuild = 1;
@@ -258,20 +259,23 @@ int choose_vsplit_uncached(int row_tiles, int vocab_tiles, int grid, int cap, in
   return best;
 }
 
+// The last few answers are kept: a training step and an evaluation alternate shapes.
 int choose_vsplit(int row_tiles, int vocab_tiles, int grid, int cap, int group) {
+  constexpr int kKept = 16;
   static std::mutex mu;
-  static int key[5] = {-1, -1, -1, -1, -1};
-  static int val = 1;
+  static int key[kKept][5];
+  static int val[kKept];
+  static int used = 0, next = 0;
   std::lock_guard<std::mutex> lock(mu);
-  if (key[0] != row_tiles || key[1] != vocab_tiles || key[2] != grid || key[3] != cap || key[4] != group) {
-    val = choose_vsplit_uncached(row_tiles, vocab_tiles, grid, cap, group);
-    key[0] = row_tiles;
-    key[1] = vocab_tiles;
-    key[2] = grid;
-    key[3] = cap;
-    key[4] = group;
-  }
-  return val;
+  const int want[5] = {row_tiles, vocab_tiles, grid, cap, group};
+  for (int i = 0; i < used; ++i)
+    if (std::equal(want, want + 5, key[i])) return val[i];
+  const int v = choose_vsplit_uncached(row_tiles, vocab_tiles, grid, cap, group);
+  std::copy(want, want + 5, key[next]);
+  val[next] = v;
+  next = (next + 1) % kKept;
+  used = std::min(used + 1, kKept);
+  return v;
 }
 
 struct Ctx {
@@ -496,6 +500,14 @@ flce_status_t run_forward(const Ctx& c, const void* X, const void* W, const int3
   }));
 }
 
+// Gradients of token log probabilities and entropies: what the grad launches need besides
+// the log probabilities' upstream gradients (grad_rows).
+struct ScoreGrad {
+  float inv_temp;
+  const float* grad_ent;
+  const float* entropy;
+};
+
 // Backward given lse and the scale already in the workspace.  dX accumulates
 // in fp32 in `dx_acc` (the workspace's accumulator, or a caller buffer) and is
 // written as bf16 to dX unless dX is null.
@@ -504,7 +516,7 @@ flce_status_t run_forward(const Ctx& c, const void* X, const void* W, const int3
 // its dX/dW launch.
 flce_status_t run_backward(const Ctx& c, const void* X, const void* W, const int32_t* labels, const float* lse,
                            const float* grad_rows, void* dX, void* dW, float* dx_acc,
-                           const LabelView* soft = nullptr) {
+                           const LabelView* soft = nullptr, const ScoreGrad* score = nullptr) {
   const flce_problem_t& p = *c.p;
   const int chunk = c.L.chunk;
   TcParams tp{};
@@ -519,6 +531,12 @@ flce_status_t run_backward(const Ctx& c, const void* X, const void* W, const int
   tp.seq_len = p.shift ? p.seq_len : 1;
   tp.grad_rows = grad_rows;
   tp.soft_grad = soft ? 1 : 0;
+  if (score) {
+    tp.inv_temp = score->inv_temp;
+    tp.zscale = kLog2e * score->inv_temp;
+    tp.grad_ent = score->grad_ent;
+    tp.entropy = score->entropy;
+  }
   tp.lse = lse;
   tp.scale = c.scale();
   tp.row_tiles = static_cast<int>((p.n + kPairRows - 1) / kPairRows);
@@ -545,7 +563,7 @@ flce_status_t run_backward(const Ctx& c, const void* X, const void* W, const int
     const long long gtiles = static_cast<long long>(tp.row_tiles) * tp.grad_n_tiles;
     const double gflops = 2.0 * static_cast<double>(p.n) * cw * static_cast<double>(p.h);
     flce_status_t st = cuda_status(timed(1, gflops, c.stream, [&] {
-      return launch_tc(kModeGrad, gm, tp, pair_grid(c.dev.sms, gtiles), c.stream);
+      return launch_tc(score ? kModeGradScore : kModeGrad, gm, tp, pair_grid(c.dev.sms, gtiles), c.stream);
     }));
     if (st != FLCE_OK) return st;
     if (soft) {
@@ -823,6 +841,89 @@ flce_status_t run_topk(const Ctx& c, int k, const void* X, const void* W, int32_
   return cuda_status(timed(3, 0.0, c.stream, [&] {
     return launch_topk_finalize(tp.n, tc_topk_subranges() * tp.vsplit, k, c.part_m(), c.part_l(), cand_val, cand_idx,
                                 lse, out_val, out_idx, c.stream);
+  }));
+}
+
+// Token log probabilities.  Workspace: the header every layout starts with, then per
+// (split, row) the partial maximum, sum and entropy sum, the rows' target logits and, for
+// the alternatives, shared thresholds and the splits' candidates.
+struct ScoreLayout {
+  size_t part_m, part_l, part_s, tgt, thr, cand_val, cand_idx, total;
+  int splits;
+};
+
+ScoreLayout score_layout(const flce_problem_t& p, int k) {
+  ScoreLayout L{};
+  const size_t n = static_cast<size_t>(p.n);
+  L.splits = score_splits(p.n);
+  const size_t part = align_up(sizeof(float) * static_cast<size_t>(L.splits) * n);
+  size_t off = kAlign;
+  L.part_m = off;
+  L.part_l = (off += part);
+  L.part_s = (off += part);
+  L.tgt = (off += part);
+  L.thr = (off += align_up(sizeof(float) * n));
+  if (k > 0) off += align_up(sizeof(unsigned) * n);
+  const size_t cand = k > 0 ? align_up(sizeof(float) * static_cast<size_t>(L.splits) * n * kTopkMax) : 0;
+  L.cand_val = off;
+  L.cand_idx = (off += cand);
+  L.total = off + cand;
+  if (p.n == 0) L.total = kAlign;
+  return L;
+}
+
+flce_status_t run_score(const flce_problem_t& p, int k, float inv_temp, const void* X, const void* W,
+                        const int32_t* tokens, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                        float* top_logprobs, uint8_t* ws, cudaStream_t stream, const Device& dev) {
+  const ScoreLayout L = score_layout(p, k);
+  if (cudaMemsetAsync(ws, 0, kAlign, stream) != cudaSuccess) return FLCE_ERR_CUDA;  // status word, counters
+  if (k > 0 && cudaMemsetAsync(ws + L.thr, 0, sizeof(unsigned) * static_cast<size_t>(p.n), stream) != cudaSuccess)
+    return FLCE_ERR_CUDA;
+  TcMaps maps;
+  if (!make_map(&maps.a, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.n, p.h * 2, kBK, kBM)) return FLCE_ERR_CUDA;
+  if (!make_map(&maps.b, W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.v, p.h * 2, kBK, kBoxB)) return FLCE_ERR_CUDA;
+  maps.out = maps.a2 = maps.b2 = maps.out2 = maps.a;  // unused in these modes
+  TcParams tp{};
+  tp.n = static_cast<int>(p.n);
+  tp.h = static_cast<int>(p.h);
+  tp.v = static_cast<int>(p.v);
+  tp.ignore_index = p.ignore_index;
+  tp.timeout_ns = timeout_ns();
+  tp.status = reinterpret_cast<int*>(ws);
+  tp.row_tiles = static_cast<int>((p.n + kPairRows - 1) / kPairRows);
+  tp.vocab_tiles = static_cast<int>((p.v + kBN - 1) / kBN);
+  tp.units_group = units_group_rows(tp.row_tiles, p.h);
+  tp.vsplit = choose_vsplit(tp.row_tiles, tp.vocab_tiles, dev.sms / 2, L.splits, tp.units_group);
+  tp.part_m = reinterpret_cast<float*>(ws + L.part_m);
+  tp.part_l = reinterpret_cast<float*>(ws + L.part_l);
+  tp.part_s = reinterpret_cast<float*>(ws + L.part_s);
+  tp.tgt = reinterpret_cast<float*>(ws + L.tgt);
+  tp.labels = tokens;
+  tp.shift = p.shift;
+  tp.seq_len = p.shift ? p.seq_len : 1;
+  tp.row_end = tp.n;
+  tp.zscale = kLog2e * inv_temp;
+  tp.inv_temp = inv_temp;
+  tp.tile_counter = reinterpret_cast<int*>(ws) + 1;
+  tp.part_count = static_cast<int64_t>(L.splits) * p.n;
+  if (k > 0) {
+    tp.topk_thr = reinterpret_cast<unsigned*>(ws + L.thr);
+    tp.topk_val = reinterpret_cast<float*>(ws + L.cand_val);
+    tp.topk_idx = reinterpret_cast<int32_t*>(ws + L.cand_idx);
+    tp.topk_k = k;
+    tp.topk_count = static_cast<int64_t>(L.splits) * p.n * kTopkMax;
+  }
+  const double flops = 2.0 * static_cast<double>(p.n) * static_cast<double>(p.v) * static_cast<double>(p.h);
+  const int grid = pair_grid(dev.sms, static_cast<long long>(tp.row_tiles) * tp.vsplit);
+  flce_status_t st = cuda_status(timed(0, flops, stream, [&] {
+    return launch_tc(k > 0 ? kModeScoreTop : kModeScore, maps, tp, grid, stream);
+  }));
+  if (st != FLCE_OK) return st;
+  const LabelView lv{tokens, p.ignore_index, p.shift, p.shift ? p.seq_len : 1, nullptr, nullptr, 0};
+  return cuda_status(timed(3, 0.0, stream, [&] {
+    return launch_score_finalize(tp.n, tp.v, tp.vsplit, k, lv, tp.zscale, tp.part_m, tp.part_l, tp.part_s, tp.tgt,
+                                 tp.topk_val, tp.topk_idx, logprob, entropy, lse, top_ids, top_logprobs, tp.status,
+                                 stream);
   }));
 }
 
@@ -1191,6 +1292,66 @@ flce_status_t flce_soft_fwd_bwd_rowchunk(const flce_problem_t* p, int32_t k, con
                                          const int32_t* tgt_idx, const float* tgt_prob, float* loss, float* lse,
                                          void* dX, void* dW, void* ws, size_t ws_bytes, flce_stream_t stream) {
   return soft_fwd_bwd(p, k, X, W, tgt_idx, tgt_prob, loss, lse, dX, dW, ws, ws_bytes, stream, true);
+}
+
+// ----------------------------------------------------------------------------- token log probabilities
+
+namespace {
+bool temperature_ok(float t) { return t > 0.f && t <= 1e30f && 1.f / t <= 1e30f; }
+}  // namespace
+
+size_t flce_token_logprobs_workspace_bytes(const flce_problem_t* p, int32_t k) {
+  if (check_problem(p) != FLCE_OK || k < 0 || k > kTopkMax) return 0;
+  return score_layout(*p, k).total;
+}
+
+flce_status_t flce_token_logprobs(const flce_problem_t* p, int32_t k, float temperature, const void* X, const void* W,
+                                  const int32_t* tokens, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                                  float* top_logprobs, void* ws, size_t ws_bytes, flce_stream_t stream) {
+  if (!p || !W || !ws || !rows_ok(p, X) || !rows_ok(p, lse)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (k < 0 || k > kTopkMax || !temperature_ok(temperature)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (logprob && !tokens && p->n > 0) return FLCE_ERR_INVALID_ARGUMENT;
+  if (k > 0 && (!rows_ok(p, top_ids) || !rows_ok(p, top_logprobs))) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(X, 16) || !aligned(W, 16) || !aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
+      !aligned(lse, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4) || !aligned(ws, kAlign))
+    return FLCE_ERR_MISALIGNED;
+  flce_status_t st = check_problem(p);
+  if (st != FLCE_OK) return st;
+  if (p->n == 0) return run_empty(p, nullptr, nullptr, ws, ws_bytes, stream);
+  if (ws_bytes < score_layout(*p, k).total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  Device dev;
+  st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  if (!encode_fn()) return FLCE_ERR_CUDA;
+  return run_score(*p, k, 1.f / temperature, X, W, tokens, logprob, entropy, lse, top_ids, top_logprobs,
+                   static_cast<uint8_t*>(ws), reinterpret_cast<cudaStream_t>(stream), dev);
+}
+
+flce_status_t flce_token_logprobs_backward(const flce_problem_t* p, float temperature, const void* X, const void* W,
+                                           const int32_t* tokens, const float* lse, const float* entropy,
+                                           const float* grad_logprob, const float* grad_entropy, void* dX, void* dW,
+                                           void* ws, size_t ws_bytes, flce_stream_t stream) {
+  if (!p || !W || !dW || !rows_ok(p, X) || !rows_ok(p, lse) || !rows_ok(p, dX)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!temperature_ok(temperature)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (p->n > 0 && ((grad_logprob && !tokens) || (grad_entropy && !entropy))) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(X, 16) || !aligned(W, 16) || !aligned(dX, 16) || !aligned(dW, 16) || !aligned(tokens, 4) ||
+      !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(grad_logprob, 4) || !aligned(grad_entropy, 4))
+    return FLCE_ERR_MISALIGNED;
+  flce_status_t st = check_problem(p);
+  if (st != FLCE_OK) return st;
+  if (p->n == 0) return run_empty(p, nullptr, dW, ws, ws_bytes, stream);
+  Ctx c;
+  st = prepare(&c, p, ws, ws_bytes, stream);
+  if (st != FLCE_OK) return st;
+  if (tokens) {  // out-of-range tokens are reported as in the forward pass
+    st = cuda_status(timed(3, 0.0, c.stream, [&] {
+      return launch_label_scan_view(static_cast<int>(p->n), static_cast<int>(p->v), c.labels_of(tokens), c.blk_loss(),
+                                    c.blk_valid(), c.status(), c.stream);
+    }));
+    if (st != FLCE_OK) return st;
+  }
+  const ScoreGrad sg{1.f / temperature, grad_entropy, entropy};
+  return run_backward(c, X, W, tokens, lse, grad_logprob, dX, dW, c.dx_acc(), nullptr, &sg);
 }
 
 // ----------------------------------------------------------------------------- vocabulary / sequence shards

@@ -38,7 +38,16 @@ inline int pair_grid(int sms, long long pair_work) {
 // workspace holds one chunk of G, N x chunk bf16.
 int chunk_width(int64_t n);
 
-enum Mode : int { kModeForward = 0, kModeGrad = 1, kModeBwd = 2, kModeFwdStore = 3, kModeTopk = 4 };
+enum Mode : int {
+  kModeForward = 0,
+  kModeGrad = 1,
+  kModeBwd = 2,
+  kModeFwdStore = 3,
+  kModeTopk = 4,
+  kModeScore = 5,      // forward with the entropy's sum, at a temperature
+  kModeScoreTop = 6,   // the same with each row's best logits
+  kModeGradScore = 7,  // G of the gradients of token log probabilities and entropies
+};
 
 // Forward-store: a row's p~ is stored relative to its reference logit (log2
 // units) unless a tile's p~ sum exceeds 2^kRefSpan; then relative to the
@@ -47,6 +56,7 @@ constexpr float kRefSpan = 64.f;
 
 constexpr int kTopkMax = 16;     // largest k of flce_topk / of soft targets per row
 constexpr int kTopkSplit = 16;   // most vocabulary splits of the top-k pass (bounds its partial buffer)
+constexpr int kScoreSplitMax = 80;  // most vocabulary splits of the score pass (see score_splits)
 
 // Output format of the dX / dW tiles of a kModeBwd launch.
 enum OutMode : int {
@@ -101,6 +111,13 @@ struct TcParams {
   // element counts of the buffers above that are indexed by computed offsets (checked in
   // builds with FLCE_DEBUG_CHECKS): part_m / part_l, mtile, topk_val / topk_idx, rowscale
   int64_t part_count, mtile_count, topk_count, rowscale_count;
+  // score modes and their gradient: log2 e / temperature, 1 / temperature, the third
+  // partial of each (split, row), per-row upstream gradients (either may be null; those of
+  // the log probabilities are in grad_rows) and entropies
+  float zscale, inv_temp;
+  float* part_s;        // sum of 2^(t - m) (t - m)
+  const float* grad_ent;
+  const float* entropy;
   int soft_grad;        // grad: soft targets (every row valid, no one-hot; grad_rows carries s Q_i)
 };
 
@@ -204,6 +221,22 @@ cudaError_t launch_soft_rowcoef(int n, int k, const float* soft_prob, const floa
 cudaError_t launch_soft_chunk_targets(int n, int k, const int32_t* soft_idx, const float* soft_prob,
                                       const float* scale, int c0, int cw, int64_t pitch, void* G, int v, int* status,
                                       cudaStream_t stream);
+
+// Token log probabilities: per row, from the splits' partials, lse, the log probability of
+// its label (0 where ignored), the entropy (any but lse may be null) and, for k > 0, the k
+// best of the candidates with their log probabilities.  zscale, inv_temp as in TcParams.
+//
+// Most splits of an n-row score pass: enough that one row tile's ranges occupy every CTA
+// pair (76 on this GPU), 16 (as for the top-k pass) from ten row tiles on.
+inline int score_splits(int64_t n) {
+  const int64_t row_tiles = (n + kPairRows - 1) / kPairRows;
+  const int64_t s = row_tiles > 0 ? 2 * kScoreSplitMax / row_tiles : kScoreSplitMax;
+  return static_cast<int>(s < 16 ? 16 : s > kScoreSplitMax ? kScoreSplitMax : s);
+}
+cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv, float zscale, const float* part_m,
+                                  const float* part_l, const float* part_s, const float* tgt, const float* cand_val,
+                                  const int32_t* cand_idx, float* logprob, float* entropy, float* lse,
+                                  int32_t* top_ids, float* top_logprobs, int* status, cudaStream_t stream);
 
 // Vocabulary shards.  A shard's kernels read labels in shard-local form: -1 for an
 // ignored row (the shard calls run with ignore_index -1), y - v0 for a label the

@@ -13,8 +13,11 @@
 //                  reference (its target logit) or, past a span, the tile max.
 //   kModeTopk      the forward's log-sum-exp plus each row's best 16 logits
 //                  and their ids per vocabulary range.
+//   kModeScore     the forward with the entropy's sum beside the sum of exponentials,
+//                  at a temperature; kModeScoreTop also keeps each row's best logits.
 //   kModeGrad      recomputes S for one vocabulary chunk and writes
-//                  G = s (exp(S - lse) - onehot) valid as bf16.
+//                  G = s (exp(S - lse) - onehot) valid as bf16; kModeGradScore the G of
+//                  token log probabilities and entropies.
 //   kModeBwd       dX and dW tiles of one chunk of G (or of p~ with per-row
 //                  factors) in one launch, handed out longest-first by a
 //                  global counter.
@@ -106,7 +109,13 @@ struct Pair {
 };
 
 template <int MODE>
-constexpr bool kUnits = (MODE == kModeForward || MODE == kModeFwdStore || MODE == kModeTopk);
+constexpr bool kScoring = (MODE == kModeScore || MODE == kModeScoreTop);
+template <int MODE>
+constexpr bool kTop = (MODE == kModeTopk || MODE == kModeScoreTop);
+template <int MODE>
+constexpr bool kGrad = (MODE == kModeGrad || MODE == kModeGradScore);
+template <int MODE>
+constexpr bool kUnits = (MODE == kModeForward || MODE == kModeFwdStore || kTop<MODE> || kScoring<MODE>);
 
 // Dynamic schedules hand out work through a global counter (p.tile_counter,
 // zero at launch): the backward's tiles one by one, the forward modes' units
@@ -158,7 +167,7 @@ __device__ __forceinline__ bool sched_get(const TcParams& p, const Pair& pr, con
     t.last = (s.vt == s.ve - 1);
     t.split = s.sp;
     return true;
-  } else if (MODE == kModeGrad) {
+  } else if (kGrad<MODE>) {
     if (s.t >= p.row_tiles * p.grad_n_tiles) return false;
     t.m0 = (s.t / p.grad_n_tiles) * kPairM + half;
     t.n0 = (s.t % p.grad_n_tiles) * kBN;  // chunk-local vocabulary column
@@ -535,6 +544,18 @@ __device__ __forceinline__ float exp_pack_group(const uint32_t (&v)[64], uint32_
   return sum;
 }
 
+// Below every finite logit's distance from the maximum, in log2 units: 2^it is 0, and 0
+// times it is 0, where a logit of minus infinity (a column past V, an infinite weight)
+// would make 0 * infinity.
+constexpr float kNoLogit = -1e30f;
+
+// max(a, b) that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 template <int MODE>
 __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& pr, uint8_t* staging, uint64_t* tfull,
                              uint64_t* tempty, uint32_t tmem_base, TileRing ring, uint64_t* ebar,
@@ -570,18 +591,19 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
   tk.shared_thr = nullptr;
   float gthr = -INFINITY;  // top-k: the row's shared threshold as last read
   static_assert(kTopkCand * 32 * 8 <= kStagingPerWarp, "top-k candidates fit the staging area");
-  float run_m = -INFINITY, run_l = 0.f, z_tgt = 0.f;
+  float run_m = -INFINITY, run_l = 0.f, run_s = 0.f, z_tgt = 0.f;
   bool found = false;
   int y_fwd = p.ignore_index;
   float ref_row = 0.f;  // forward-store: the row's reference exponent, log2 units
   const float scale = (MODE == kModeGrad) ? *p.scale : 0.f;
+  const float zs = (kScoring<MODE> || MODE == kModeGradScore) ? p.zscale : kLog2e;  // log2 units per logit
   const int row_end = p.row_end > 0 ? p.row_end : p.n;
 
   while (sched_get<MODE>(p, pr, s, t)) {
     // top-k: the row's shared threshold, loaded before the wait so that the wait
     // hides its latency (an older value only keeps more candidates)
     unsigned thr_key = 0u;
-    if (MODE == kModeTopk) {
+    if (kTop<MODE>) {
       const int row = p.r0 + t.m0 + r;
       if (p.topk_thr && row < row_end) thr_key = *reinterpret_cast<volatile unsigned*>(p.topk_thr + row);
     }
@@ -599,17 +621,18 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
       if (t.first) {
         run_m = -INFINITY;
         run_l = 0.f;
+        if (kScoring<MODE>) run_s = 0.f;
         found = false;
         y_fwd = (row < row_end) ? label_at(p.labels, row, p.shift, p.seq_len, p.ignore_index) : p.ignore_index;
         if (MODE == kModeFwdStore) ref_row = (row < p.n) ? p.mref[row] : 0.f;
-        if (MODE == kModeTopk) {
+        if (kTop<MODE>) {
           tk.count = 0;
           tk.thr = -INFINITY;
           tk.shared_thr = (p.topk_thr && row < row_end) ? p.topk_thr + row : nullptr;
         }
       }
-      if (MODE == kModeTopk && tk.shared_thr) gthr = topk_unkey(thr_key);
-      if (MODE == kModeTopk && t.first) {
+      if (kTop<MODE> && tk.shared_thr) gthr = topk_unkey(thr_key);
+      if (kTop<MODE> && t.first) {
         // Before a range's first tile fills the candidate buffer from nothing: each of
         // the tile's 16 disjoint 16-column groups holds its max, so at least kTopkMax
         // values of the row are >= the smallest of those maxima, and nothing below it
@@ -640,7 +663,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
           if (tk.shared_thr) atomicMax(tk.shared_thr, topk_key(t0));
         }
       }
-      if (MODE == kModeForward || MODE == kModeTopk) {
+      if (MODE == kModeForward || kTop<MODE> || kScoring<MODE>) {
         // 32 columns per TMEM load (64 measured the same for the forward and ran
         // slower for top-k, whose candidate code then unrolls over 64 columns)
         constexpr int kW = 32;
@@ -676,13 +699,30 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
           float cmax = gmax[0];
 #pragma unroll
           for (int hh = 1; hh < kBlocks; ++hh) cmax = fmaxf(cmax, gmax[hh]);
-          const float new_m = fmaxf(run_m, cmax * kLog2e);
+          const float new_m = fmaxf(run_m, cmax * zs);
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
+          if (kScoring<MODE>) {
+            // beside sum e = sum 2^(t - m), the entropy's sum e (t - m): entropy = ln l - ln 2 (that / l),
+            // two terms of like sign, where lse - sum p z would cancel
+            float e4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < kW; ++j) s4[j & 3] += fast_exp2(fmaf(__uint_as_float(v[j]), kLog2e, -new_m));
-          run_l = run_l * fast_exp2(run_m - new_m) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+            for (int j = 0; j < kW; ++j) {
+              const float u = max_nan(fmaf(__uint_as_float(v[j]), zs, -new_m), kNoLogit);
+              const float w = fast_exp2(u);
+              s4[j & 3] += w;
+              e4[j & 3] = fmaf(w, u, e4[j & 3]);
+            }
+            const float d = max_nan(run_m - new_m, kNoLogit);
+            const float f = fast_exp2(d);
+            run_s = f * fmaf(run_l, d, run_s) + ((e4[0] + e4[1]) + (e4[2] + e4[3]));
+            run_l = run_l * f + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < kW; ++j) s4[j & 3] += fast_exp2(fmaf(__uint_as_float(v[j]), kLog2e, -new_m));
+            run_l = run_l * fast_exp2(run_m - new_m) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+          }
           run_m = new_m;
-          if (MODE == kModeTopk) {
+          if (kTop<MODE>) {
             // blocks of 8: a buffer holding at most kTopkCand - 8 never overflows, and a
             // lane is compacted only once it has gathered more than that
             // a value must beat this range's own 16th best (ids grow along the range, so an
@@ -779,7 +819,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
         run_l = run_l * fast_exp2(run_m - new_m) + sum * fast_exp2(ref - new_m);
         run_m = new_m;
       }
-      if (MODE == kModeTopk && t.last)
+      if (kTop<MODE> && t.last)
         topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > p.topk_k), p.topk_k);
       if (t.last && row < row_end) {
         const int osplit = (Cfg<MODE>::kEpiWarps == 8) ? 2 * t.split + ehalf : t.split;
@@ -787,9 +827,10 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
         if (in_bounds(pi, p.part_count, p.status)) {
           p.part_m[pi] = run_m;
           p.part_l[pi] = run_l;
+          if (kScoring<MODE>) p.part_s[pi] = run_s;
         }
         if (found && in_bounds(row, p.n, p.status)) p.tgt[row] = z_tgt;
-        if (MODE == kModeTopk) {
+        if (kTop<MODE>) {
           const int kept = tk.count;  // at most k (the merge does not need them sorted)
           const int64_t base = (static_cast<int64_t>(osplit) * p.n + row) * kTopkMax;
           for (int i = 0; i < kTopkMax; ++i) {
@@ -826,6 +867,37 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
           w[j] = pack_bf16x2(a, b);
         }
         // columns at or beyond the chunk width fall outside the store box's tensor and are dropped by TMA
+        stage_and_store(&maps.out, stg, sbuf, lane, w, t.n0 + g * 64, t.m0 + quarter * 32, p.status);
+      }
+      release_accumulator(&tempty[acc], lane);
+    } else if (MODE == kModeGradScore) {
+      // G_ij = gl_i ([j = y_i] - p_ij) - ge_i p_ij (log p_ij + entropy_i), times 1 / temperature:
+      // p (a + b log2 p) with a = -(gl + ge entropy), b = -ge ln 2, and gl at the label.  Rounded
+      // to bf16 for the two contractions that follow, like every G.
+      const int row = t.m0 + r;
+      const int y = (row >= p.n) ? p.ignore_index : label_at(p.labels, row, p.shift, p.seq_len, p.ignore_index);
+      const float gl = (y != p.ignore_index && p.grad_rows) ? p.grad_rows[row] * p.inv_temp : 0.f;
+      const float ge = (row < p.n && p.grad_ent) ? p.grad_ent[row] * p.inv_temp : 0.f;
+      const float a = (row < p.n && p.grad_ent) ? -fmaf(ge, p.entropy[row], gl) : -gl;
+      const float b = -ge * kLn2;
+      const float lse2 = (row < p.n) ? p.lse[row] * kLog2e : 0.f;
+      const int ycol = (y != p.ignore_index) ? y - (p.c0 + t.n0) : -1;  // label position inside this tile (if any)
+#pragma unroll 1
+      for (int g = 0; g < kBN / 64; ++g) {
+        if (t.n0 + g * 64 >= p.cw) break;
+        __syncwarp();
+        uint32_t v[64];
+        tmem_ld_32x64(tbase + g * 64, v);
+        uint32_t w[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int c = g * 64 + 2 * j;
+          const float u0 = max_nan(fmaf(__uint_as_float(v[2 * j]), zs, -lse2), kNoLogit);
+          const float u1 = max_nan(fmaf(__uint_as_float(v[2 * j + 1]), zs, -lse2), kNoLogit);
+          const float g0 = fmaf(fast_exp2(u0), fmaf(b, u0, a), c == ycol ? gl : 0.f);
+          const float g1 = fmaf(fast_exp2(u1), fmaf(b, u1, a), c + 1 == ycol ? gl : 0.f);
+          w[j] = pack_bf16x2(g0, g1);
+        }
         stage_and_store(&maps.out, stg, sbuf, lane, w, t.n0 + g * 64, t.m0 + quarter * 32, p.status);
       }
       release_accumulator(&tempty[acc], lane);
@@ -1019,9 +1091,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<MODE>::kThreads,
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   // Wait for the previous kernel before touching memory it may write.  In the
-  // forward modes the producer and MMA threads read only X and W, which no
-  // kernel of the library writes, so they start the contraction at once and
-  // only the epilogue (which reads the row state and writes the outputs) waits.
+  // forward modes the producer and MMA threads read only X and W.  Every call
+  // clears its workspace's header first, a memory operation that waits for all
+  // earlier work on the stream (the layer norm that wrote X, the optimizer step
+  // that wrote W), and no kernel of the call itself writes X or W, so they start
+  // the contraction at once and only the epilogue (which reads the row state and
+  // writes the outputs) waits.
   if (!kUnits<MODE> || warp >= 2) griddep_wait();
   griddep_launch();
   if (p.zero_words && blockIdx.x == 0 && threadIdx.x == 64) {  // an epilogue thread: after the wait
@@ -1642,6 +1717,100 @@ __global__ void __launch_bounds__(256) topk_finalize_kernel(int n, int nsub, int
   }
 }
 
+// One warp per row: merges the splits' (max, sum, entropy sum), reads off the label's log
+// probability, and for k > 0 picks the best k of the splits' candidates (kPer of them in
+// each lane's registers).
+template <int kPer>
+__global__ void __launch_bounds__(256) score_finalize_kernel(
+    int n, int v, int nsplit, int k, LabelView lv, float zscale, const float* __restrict__ part_m,
+    const float* __restrict__ part_l, const float* __restrict__ part_s, const float* __restrict__ tgt,
+    const float* __restrict__ cand_val, const int32_t* __restrict__ cand_idx, float* __restrict__ logprob,
+    float* __restrict__ entropy, float* __restrict__ lse_out, int32_t* __restrict__ top_ids,
+    float* __restrict__ top_logprobs, int* __restrict__ status) {
+  griddep_begin();
+  const int row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (row >= n) return;  // whole warps
+  float m = -INFINITY;
+  for (int s = lane; s < nsplit; s += 32) m = fmaxf(m, part_m[static_cast<int64_t>(s) * n + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, es = 0.f;
+  for (int s = lane; s < nsplit; s += 32) {
+    const int64_t at = static_cast<int64_t>(s) * n + row;
+    const float d = max_nan(part_m[at] - m, kNoLogit), pl = part_l[at];
+    const float f = exp2f(d);
+    l += pl * f;
+    es += f * fmaf(pl, d, part_s[at]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, o);
+    es += __shfl_xor_sync(0xffffffffu, es, o);
+  }
+  const float log2l = log2f(l);
+  if (lane == 0) {
+    lse_out[row] = (m + log2l) * kLn2;
+    if (entropy) entropy[row] = (log2l - es / l) * kLn2;
+    if (lv.labels) {
+      const int y = label_at(lv.labels, row, lv.shift, lv.seq_len, lv.ignore_index);
+      float lp = 0.f;
+      if (y != lv.ignore_index) {
+        // relative to the same m as l: exact where the label holds the largest logit
+        if (y >= 0 && y < v) lp = (fmaf(tgt[row], zscale, -m) - log2l) * kLn2;
+        else atomicCAS(status, 0, kErrLabel);
+      }
+      if (logprob) logprob[row] = lp;
+    }
+  }
+  if (k == 0) return;
+  const int total = nsplit * kTopkMax;
+  float cv[kPer];
+  int ci[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int c = lane + 32 * q;
+    const bool ok = c < total;
+    const int64_t at = (static_cast<int64_t>(c / kTopkMax) * n + row) * kTopkMax + c % kTopkMax;
+    cv[q] = ok ? cand_val[at] : -INFINITY;
+    ci[q] = ok ? cand_idx[at] : -1;
+  }
+  for (int r = 0; r < k; ++r) {
+    float bv = -INFINITY;
+    int bi = -1, bq = -1;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      if (topk_better(cv[q], ci[q], bv, bi)) {
+        bv = cv[q];
+        bi = ci[q];
+        bq = q;
+      }
+    float wv = bv;
+    int wi = bi;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float ov = __shfl_xor_sync(0xffffffffu, wv, o);
+      const int oi = __shfl_xor_sync(0xffffffffu, wi, o);
+      if (topk_better(ov, oi, wv, wi)) {
+        wv = ov;
+        wi = oi;
+      }
+    }
+    if (bq >= 0 && wi >= 0 && bi == wi) {  // ids are unique within a row: one lane holds the winner
+#pragma unroll
+      for (int q = 0; q < kPer; ++q)
+        if (q == bq) {
+          cv[q] = -INFINITY;
+          ci[q] = -1;
+        }
+    }
+    if (lane == 0) {
+      top_ids[static_cast<int64_t>(row) * k + r] = wi;
+      top_logprobs[static_cast<int64_t>(row) * k + r] = (fmaf(wv, zscale, -m) - log2l) * kLn2;
+    }
+  }
+}
+
 __global__ void convert_bf16_kernel(const float* __restrict__ src, __nv_bfloat16* __restrict__ dst, int64_t count8) {
   griddep_begin();
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < count8;
@@ -1861,6 +2030,9 @@ cudaError_t launch_tc(int mode, const TcMaps& maps, const TcParams& p, int grid,
     case kModeBwd: return launch_mode<kModeBwd>(maps, p, grid, stream);
     case kModeFwdStore: return launch_mode<kModeFwdStore>(maps, p, grid, stream);
     case kModeTopk: return launch_mode<kModeTopk>(maps, p, grid, stream);
+    case kModeScore: return launch_mode<kModeScore>(maps, p, grid, stream);
+    case kModeScoreTop: return launch_mode<kModeScoreTop>(maps, p, grid, stream);
+    case kModeGradScore: return launch_mode<kModeGradScore>(maps, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1975,6 +2147,16 @@ cudaError_t launch_topk_finalize(int n, int nsub, int k, const float* part_m, co
                                  int32_t* out_idx, cudaStream_t stream) {
   return launch_k(topk_finalize_kernel, dim3((n + 7) / 8), dim3(256), 0, stream,
                   n, nsub, k, part_m, part_l, cand_val, cand_idx, lse, out_val, out_idx);
+}
+
+cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv, float zscale, const float* part_m,
+                                  const float* part_l, const float* part_s, const float* tgt, const float* cand_val,
+                                  const int32_t* cand_idx, float* logprob, float* entropy, float* lse,
+                                  int32_t* top_ids, float* top_logprobs, int* status, cudaStream_t stream) {
+  auto* kernel = nsplit <= 16 ? score_finalize_kernel<16 * kTopkMax / 32>
+                              : score_finalize_kernel<kScoreSplitMax * kTopkMax / 32>;
+  return launch_k(kernel, dim3((n + 7) / 8), dim3(256), 0, stream, n, v, nsplit, k, lv, zscale, part_m, part_l, part_s,
+                  tgt, cand_val, cand_idx, logprob, entropy, lse, top_ids, top_logprobs, status);
 }
 
 cudaError_t launch_scale_bf16(void* x, int64_t count, const float* g, cudaStream_t stream) {
