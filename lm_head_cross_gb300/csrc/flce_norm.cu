@@ -11,6 +11,8 @@ namespace flce {
 namespace {
 
 constexpr int kNormThreads = 256;
+constexpr int kNormSms = 152;                // SMs of the GPU this is written for
+constexpr int kNormSlices = 3 * kNormSms;    // most blocks of the one-pass backward
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -229,10 +231,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(int64_t n, int h
   }
 }
 
-template <typename T, typename W>
+template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_dx_kernel(int64_t n, int h, int64_t pitch,
                                                                const T* __restrict__ dy, const T* __restrict__ x,
-                                                               const W* __restrict__ weight,
+                                                               const void* __restrict__ weight, bool w_f32,
                                                                const float* __restrict__ mean,
                                                                const float* __restrict__ rstd, T* __restrict__ dx) {
   griddep_begin();
@@ -244,14 +246,18 @@ __global__ void __launch_bounds__(kNormThreads) norm_dx_kernel(int64_t n, int h,
     const float mu = mean[row], rs = rstd[row];
     float2 s = make_float2(0.f, 0.f);
     for (int j = threadIdx.x; j < h; j += kNormThreads) {
-      const float u = to_f32(dr[j]) * to_f32(weight[j]);
+      float w[1];
+      load_w<1>(weight, w_f32, j, w);
+      const float u = to_f32(dr[j]) * w[0];
       s.x += u;
       s.y += u * ((to_f32(xr[j]) - mu) * rs);
     }
     s = block_sum(s, red);
     const float a = s.x / h, b = s.y / h;
     for (int j = threadIdx.x; j < h; j += kNormThreads) {
-      const float u = to_f32(dr[j]) * to_f32(weight[j]);
+      float w[1];
+      load_w<1>(weight, w_f32, j, w);
+      const float u = to_f32(dr[j]) * w[0];
       or_[j] = from_f32<T>(rs * (u - a - (to_f32(xr[j]) - mu) * rs * b));
     }
   }
@@ -281,20 +287,278 @@ __global__ void __launch_bounds__(kNormThreads) norm_dw_partial_kernel(int64_t n
   out[h + j] = b;
 }
 
+// dweight, dbias: column sums of `slices` rows of partial sums.  32 columns a block, the rows
+// dealt over its 32 warps (about ten loads each, all in flight) and joined in warp order.
+constexpr int kFinalWarps = 32;
 template <typename W>
-__global__ void __launch_bounds__(kNormThreads) norm_dw_final_kernel(int h, int slices, const float* __restrict__ part,
-                                                                     W* __restrict__ dweight, W* __restrict__ dbias) {
+__global__ void __launch_bounds__(32 * kFinalWarps) norm_dw_final_kernel(int h, int slices,
+                                                                         const float* __restrict__ part,
+                                                                         W* __restrict__ dweight,
+                                                                         W* __restrict__ dbias) {
   griddep_begin();
-  const int j = blockIdx.x * kNormThreads + threadIdx.x;
-  if (j >= h) return;
-  float a = 0.f, b = 0.f;
-  for (int s = 0; s < slices; ++s) {
-    const float* p = part + static_cast<int64_t>(s) * 2 * h;
-    a += p[j];
-    b += p[h + j];
+  __shared__ float red[kFinalWarps][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t j = blockIdx.x * int64_t{32} + lane;  // column of [dweight | dbias]
+  float a = 0.f;
+  if (j < 2 * static_cast<int64_t>(h)) {
+#pragma unroll 10
+    for (int s = warp; s < slices; s += kFinalWarps) a += part[static_cast<int64_t>(s) * 2 * h + j];
   }
-  dweight[j] = from_f32<W>(a);
-  if (dbias) dbias[j] = from_f32<W>(b);
+  red[warp][lane] = a;
+  __syncthreads();
+  if (warp != 0 || j >= 2 * static_cast<int64_t>(h)) return;
+  float t = 0.f;
+#pragma unroll
+  for (int w = 0; w < kFinalWarps; ++w) t += red[w][lane];
+  if (j < h) dweight[j] = from_f32<W>(t);
+  else if (dbias) dbias[j - h] = from_f32<W>(t);
+}
+
+// ----------------------------------------------------------------------------- backward in one pass
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* smem, const void* gmem) {
+  static_assert(BYTES == 16, "one size is used");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t as_u64(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
+__device__ __forceinline__ float2 as_f2(uint64_t v) { return *reinterpret_cast<float2*>(&v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Shape of the one-pass backward: GW warps share a row, VPL accesses of N elements a lane,
+// kGroups rows in a block at a time.
+template <int N, int GW, int VPL>
+struct BwdShape {
+  static constexpr int kWarps = N == 1 && GW <= 8 ? 8 : 16;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kGroups = kWarps / GW;
+  static constexpr int kPairs = N * VPL / 2;  // column pairs of a lane
+  static constexpr int kBlocks = N == 1 ? (GW <= 8 ? 3 : 1) : kPairs <= 4 ? 2 : 1;  // on one SM
+  static constexpr int kStages = VPL == 1 ? 5 : VPL == 2 ? 3 : 2;  // rows in flight for each group
+  static constexpr int kStageBytes = kThreads * VPL * 32;  // x and dy, 16 bytes an access
+  static constexpr int kWeightBytes = N == 1 ? 0 : 32 * GW * VPL * N * 4;  // fp32, in the lanes' order
+  static constexpr int kRingBytes = N == 1 ? 0 : kStages * kStageBytes;
+};
+
+// dx, and the rows' share of dweight and dbias, in one pass over x and dy.  A lane owns the
+// same columns of every row, so the column sums are registers; the two sums over a row
+// (u and u xhat) are shuffles and, with GW > 1, one exchange through shared memory.  Blocks
+// stay for the whole grid's rows: each ends with one row of partial sums.
+//   N > 1: rows stream through shared memory by asynchronous copies, kStages of them in
+//   flight; a lane reads back only what it copied, so no barrier guards the ring.
+//   N = 1 (rows that no 16-byte access fits): the next row waits in registers.
+// Columns past h are zeros throughout.
+template <typename T, int N, int GW, int VPL>
+__global__ void __launch_bounds__(BwdShape<N, GW, VPL>::kThreads, BwdShape<N, GW, VPL>::kBlocks)
+    norm_bwd_rows_kernel(int n, int h, int64_t pitch, const T* __restrict__ dy, const T* __restrict__ x,
+                         const void* __restrict__ weight, bool w_f32, const float* __restrict__ mean,
+                         const float* __restrict__ rstd, T* __restrict__ dx, float* __restrict__ part) {
+  using S = BwdShape<N, GW, VPL>;
+  constexpr int kPairs = S::kPairs;
+  static_assert(N > 1 || VPL % 2 == 0, "columns come in pairs");
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) float2 red[2][S::kWarps];
+  griddep_begin();
+  const int group = static_cast<int>(threadIdx.x) / (32 * GW);
+  const int lane = static_cast<int>(threadIdx.x) % (32 * GW);
+  const int first = blockIdx.x + group * gridDim.x;
+  const int step = gridDim.x * S::kGroups;  // (row + step fits 32 bits: see norm_backward)
+  constexpr int kAcross = 32 * GW * N;  // columns one access of the group covers
+  const auto column = [&](int k) { return k * kAcross + lane * N; };
+
+  // The weight: registers, or in fp32 behind the ring, where every group finds it in the
+  // lanes' order (16 bytes a lane).
+  float2 w[N == 1 ? kPairs : 1], aw[kPairs], ab[kPairs];
+  float4* const ws = reinterpret_cast<float4*>(ring + S::kRingBytes);
+#pragma unroll
+  for (int k = 0; k < VPL; ++k) {
+    float t[N] = {};
+    if (column(k) < h) load_w<N>(weight, w_f32, column(k), t);
+    if constexpr (N == 1) {
+      reinterpret_cast<float*>(w)[k] = t[0];
+    } else if (group == 0) {
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q)
+        ws[(k * (N / 4) + q) * 32 * GW + lane] = make_float4(t[4 * q], t[4 * q + 1], t[4 * q + 2], t[4 * q + 3]);
+    }
+  }
+  if constexpr (N > 1) __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) aw[i] = ab[i] = make_float2(0.f, 0.f);
+
+  const auto slot = [&](int stage, int k, int which) {  // this lane's x or dy of one access
+    return ring + stage * S::kStageBytes + ((2 * k + which) * S::kThreads + threadIdx.x) * 16;
+  };
+  Pack<T, N> px[VPL], pd[VPL];  // N = 1: the prefetched row
+  const auto fetch = [&](int row, int stage) {
+    if (row < n) {
+      const T* xr = x + static_cast<int64_t>(row) * pitch + lane * N;
+      const T* dr = dy + static_cast<int64_t>(row) * h + lane * N;
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) {
+        if (column(k) >= h) continue;
+        if constexpr (N > 1) {
+          cp_async<16>(slot(stage, k, 0), xr + k * kAcross);
+          cp_async<16>(slot(stage, k, 1), dr + k * kAcross);
+        } else {
+          px[k].v[0] = xr[k * kAcross];
+          pd[k].v[0] = dr[k * kAcross];
+        }
+      }
+    }
+    if constexpr (N > 1) cp_async_commit();
+  };
+  constexpr int kAhead = N > 1 ? S::kStages : 1;
+#pragma unroll
+  for (int k = 0; k < VPL; ++k) {
+    if constexpr (N > 1) {
+      if (column(k) >= h)
+        for (int s = 0; s < 2 * kAhead; ++s) *reinterpret_cast<uint4*>(slot(s >> 1, k, s & 1)) = make_uint4(0, 0, 0, 0);
+    } else {
+      px[k].v[0] = pd[k].v[0] = from_f32<T>(0.f);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) fetch(first + s * step, s);
+  float mu_next = 0.f, rs_next = 0.f;
+  if (first < n) {
+    mu_next = mean[first];
+    rs_next = rstd[first];
+  }
+
+  const float inv_h = 1.f / h;
+  int stage = 0, parity = 0;
+  for (int row = first; row < n; row += step) {
+    const float mu = mu_next, rs = rs_next;
+    if (row + step < n) {
+      mu_next = mean[row + step];
+      rs_next = rstd[row + step];
+    }
+    float2 xh[kPairs], u[kPairs];  // x then xhat; dy then u
+    if constexpr (N > 1) {
+      cp_async_wait<S::kStages - 1>();
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) {
+        const auto vx = *reinterpret_cast<const Pack<T, N>*>(slot(stage, k, 0));
+        const auto vd = *reinterpret_cast<const Pack<T, N>*>(slot(stage, k, 1));
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          xh[k * (N / 2) + e] = make_float2(element(vx, 2 * e), element(vx, 2 * e + 1));
+          u[k * (N / 2) + e] = make_float2(element(vd, 2 * e), element(vd, 2 * e + 1));
+        }
+      }
+      fetch(row + S::kStages * step, stage);  // into the slots just read
+      if (++stage == S::kStages) stage = 0;
+    } else {
+#pragma unroll
+      for (int k = 0; k < VPL; k += 2) {
+        xh[k / 2] = make_float2(to_f32(px[k].v[0]), to_f32(px[k + 1].v[0]));
+        u[k / 2] = make_float2(to_f32(pd[k].v[0]), to_f32(pd[k + 1].v[0]));
+      }
+      fetch(row + step, 0);
+    }
+    float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      xh[i] = mul2(add2(xh[i], both(-mu)), both(rs));
+      aw[i] = fma2(u[i], xh[i], aw[i]);
+      ab[i] = add2(ab[i], u[i]);
+      if constexpr (N == 1) {
+        u[i] = mul2(u[i], w[i]);
+      } else {
+        const float4 wq = ws[(i / 2) * 32 * GW + lane];
+        u[i] = mul2(u[i], (i & 1) ? make_float2(wq.z, wq.w) : make_float2(wq.x, wq.y));
+      }
+      s1 = add2(s1, u[i]);
+      s2 = fma2(u[i], xh[i], s2);
+    }
+    float2 sum = make_float2(s1.x + s1.y, s2.x + s2.y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      sum = add2(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
+    if constexpr (GW > 1) {
+      // the other half of red[] is rewritten only after the next row's barrier
+      if ((threadIdx.x & 31) == 0) red[parity][threadIdx.x >> 5] = sum;
+      if constexpr (S::kGroups == 1) __syncthreads();
+      else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * GW) : "memory");
+      sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < GW; q += 2) {
+        const float4 t = *reinterpret_cast<const float4*>(&red[parity][group * GW + q]);
+        sum = add2(sum, add2(make_float2(t.x, t.y), make_float2(t.z, t.w)));
+      }
+      parity ^= 1;
+    }
+    // dx = rstd (u - mean u - xhat mean(u xhat))
+    const float2 c0 = both(-rs * (sum.x * inv_h)), c1 = both(-rs * (sum.y * inv_h));
+    T* or_ = dx + static_cast<int64_t>(row) * h + lane * N;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) {
+      if constexpr (N > 1) {
+        float o[N];
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          const int i = k * (N / 2) + e;
+          const float2 d = fma2(xh[i], c1, fma2(u[i], both(rs), c0));
+          o[2 * e] = d.x;
+          o[2 * e + 1] = d.y;
+        }
+        Pack<T, N> out;
+        pack_f32(out, o);
+        if (column(k) < h) *reinterpret_cast<Pack<T, N>*>(or_ + k * kAcross) = out;
+      } else if (k % 2 == 0) {
+        const float2 d = fma2(xh[k / 2], c1, fma2(u[k / 2], both(rs), c0));
+        if (column(k) < h) or_[k * kAcross] = from_f32<T>(d.x);
+        if (column(k + 1) < h) or_[(k + 1) * kAcross] = from_f32<T>(d.y);
+      }
+    }
+  }
+
+  // one row of partial sums a block; its groups join in order
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * h;
+  float* to = out;
+  if constexpr (S::kGroups > 1) {
+    if constexpr (N > 1) cp_async_wait<0>();
+    to = reinterpret_cast<float*>(ring);
+  }
+#pragma unroll 1
+  for (int g = 0; g < S::kGroups; ++g) {
+    if constexpr (S::kGroups > 1) __syncthreads();
+    if (g != group) continue;
+#pragma unroll
+    for (int i = 0; i < VPL * N; ++i) {
+      const int j = column(i / N) + i % N;
+      if (j >= h) continue;
+      to[j] = (g ? to[j] : 0.f) + reinterpret_cast<const float*>(aw)[i];
+      to[h + j] = (g ? to[h + j] : 0.f) + reinterpret_cast<const float*>(ab)[i];
+    }
+  }
+  if constexpr (S::kGroups > 1) {
+    __syncthreads();
+    for (int j = threadIdx.x; j < 2 * h; j += S::kThreads) out[j] = to[j];
+  }
 }
 
 struct NormForwardArgs {
@@ -356,27 +620,80 @@ cudaError_t norm_forward(const NormForwardArgs& a) {
                   static_cast<const T*>(a.x), a.weight, a.bias, a.q.w_f32, static_cast<T*>(a.y), a.mean, a.rstd);
 }
 
-template <typename T, typename W>
-cudaError_t norm_backward(const NormParams& q, const void* dy, const void* x, const void* weight, const float* mean,
-                          const float* rstd, void* dx, void* dweight, void* dbias, float* part, cudaStream_t stream) {
-  const int grid = static_cast<int>(std::min<int64_t>(q.n, 1 << 20));
-  cudaError_t e = launch_k(norm_dx_kernel<T, W>, dim3(grid), dim3(kNormThreads), 0, stream, q.n, q.h, q.x_pitch,
-                           static_cast<const T*>(dy), static_cast<const T*>(x), static_cast<const W*>(weight), mean,
-                           rstd, static_cast<T*>(dx));
+struct NormBackwardArgs {
+  NormParams q;
+  const void *dy, *x, *weight;
+  const float *mean, *rstd;
+  void* dx;
+  float* part;
+  cudaStream_t stream;
+};
+
+// The one-pass backward; returns the rows of partial sums it leaves through *slices.
+template <typename T, int N, int GW, int VPL>
+cudaError_t norm_backward_rows(const NormBackwardArgs& a, int* slices) {
+  using S = BwdShape<N, GW, VPL>;
+  // the ring (N > 1), or the joining of the groups' column sums
+  const size_t join = S::kGroups > 1 ? 2 * sizeof(float) * static_cast<size_t>(a.q.h) : 0;
+  const size_t smem = std::max<size_t>(S::kRingBytes + S::kWeightBytes, join);
+  auto* kernel = norm_bwd_rows_kernel<T, N, GW, VPL>;
+  if (smem > 40 * 1024) {  // 48 KB with the static part needs no leave
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t blocks = (a.q.n + S::kGroups - 1) / S::kGroups;
+  *slices = static_cast<int>(std::min<int64_t>(blocks, S::kBlocks * kNormSms));
+  return launch_k(kernel, dim3(*slices), dim3(S::kThreads), smem, a.stream, static_cast<int>(a.q.n), a.q.h, a.q.x_pitch,
+                  static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.weight, a.q.w_f32, a.mean, a.rstd,
+                  static_cast<T*>(a.dx), a.part);
+}
+
+// Two passes for rows past every one-pass shape: dx row by row, then the column sums over
+// slices of rows.
+template <typename T>
+cudaError_t norm_backward_wide(const NormBackwardArgs& a, int* slices) {
+  const int grid = static_cast<int>(std::min<int64_t>(a.q.n, 1 << 20));
+  cudaError_t e = launch_k(norm_dx_kernel<T>, dim3(grid), dim3(kNormThreads), 0, a.stream, a.q.n, a.q.h, a.q.x_pitch,
+                           static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.weight, a.q.w_f32, a.mean,
+                           a.rstd, static_cast<T*>(a.dx));
   if (e != cudaSuccess) return e;
-  const int slices = norm_slices(q.n);
-  const int64_t rows = (q.n + slices - 1) / slices;
-  const int cols = (q.h + kNormThreads - 1) / kNormThreads;
-  e = launch_k(norm_dw_partial_kernel<T>, dim3(cols, slices), dim3(kNormThreads), 0, stream, q.n, q.h, q.x_pitch, rows,
-               static_cast<const T*>(dy), static_cast<const T*>(x), mean, rstd, part);
-  if (e != cudaSuccess) return e;
-  return launch_k(norm_dw_final_kernel<W>, dim3(cols), dim3(kNormThreads), 0, stream, q.h, slices, part,
-                  static_cast<W*>(dweight), static_cast<W*>(dbias));
+  *slices = std::min(norm_slices(a.q.n), 128);
+  const int64_t rows = (a.q.n + *slices - 1) / *slices;
+  const int cols = (a.q.h + kNormThreads - 1) / kNormThreads;
+  return launch_k(norm_dw_partial_kernel<T>, dim3(cols, *slices), dim3(kNormThreads), 0, a.stream, a.q.n, a.q.h,
+                  a.q.x_pitch, rows, static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.mean, a.rstd, a.part);
+}
+
+template <typename T>
+cudaError_t norm_backward(const NormBackwardArgs& a, int* slices) {
+  constexpr int kVec = 16 / sizeof(T);
+  const size_t row = sizeof(T) * static_cast<size_t>(a.q.x_pitch);
+  const auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  const int h = a.q.h;
+  if (a.q.n > (1 << 30)) return norm_backward_wide<T>(a, slices);  // 32-bit row numbers in one pass
+  if (h % kVec == 0 && row % 16 == 0 && at16(a.x) && at16(a.dy) && at16(a.dx) && at16(a.weight)) {
+    const int acc = h / kVec;
+    if (acc <= 32) return norm_backward_rows<T, kVec, 1, 1>(a, slices);
+    if (acc <= 64) return norm_backward_rows<T, kVec, 2, 1>(a, slices);
+    if (acc <= 128) return norm_backward_rows<T, kVec, 4, 1>(a, slices);
+    if (acc <= 256) return norm_backward_rows<T, kVec, 8, 1>(a, slices);
+    if (acc <= 512) return norm_backward_rows<T, kVec, 16, 1>(a, slices);
+    if (acc <= 1024) return norm_backward_rows<T, kVec, 16, 2>(a, slices);
+    if (acc <= 2048) return norm_backward_rows<T, kVec, 16, 4>(a, slices);
+  } else {
+    if (h <= 128) return norm_backward_rows<T, 1, 1, 4>(a, slices);
+    if (h <= 512) return norm_backward_rows<T, 1, 4, 4>(a, slices);
+    if (h <= 1024) return norm_backward_rows<T, 1, 8, 4>(a, slices);
+    if (h <= 2048) return norm_backward_rows<T, 1, 8, 8>(a, slices);
+    if (h <= 4096) return norm_backward_rows<T, 1, 16, 8>(a, slices);
+  }
+  return norm_backward_wide<T>(a, slices);
 }
 
 }  // namespace
 
-int norm_slices(int64_t n) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(128, n / 32))); }
+int norm_slices(int64_t n) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNormSlices, n))); }
 
 cudaError_t launch_norm_forward(const NormParams& q, const void* x, const void* weight, const void* bias, void* y,
                                 float* mean, float* rstd, cudaStream_t stream) {
@@ -387,13 +704,16 @@ cudaError_t launch_norm_forward(const NormParams& q, const void* x, const void* 
 cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void* x, const void* weight,
                                  const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
                                  float* part, cudaStream_t stream) {
-  if (q.x_f32)
-    return q.w_f32
-               ? norm_backward<float, float>(q, dy, x, weight, mean, rstd, dx, dweight, dbias, part, stream)
-               : norm_backward<float, __nv_bfloat16>(q, dy, x, weight, mean, rstd, dx, dweight, dbias, part, stream);
-  return q.w_f32 ? norm_backward<__nv_bfloat16, float>(q, dy, x, weight, mean, rstd, dx, dweight, dbias, part, stream)
-                 : norm_backward<__nv_bfloat16, __nv_bfloat16>(q, dy, x, weight, mean, rstd, dx, dweight, dbias, part,
-                                                               stream);
+  const NormBackwardArgs a{q, dy, x, weight, mean, rstd, dx, part, stream};
+  int slices = 0;
+  cudaError_t e = q.x_f32 ? norm_backward<float>(a, &slices) : norm_backward<__nv_bfloat16>(a, &slices);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>((2 * static_cast<int64_t>(q.h) + 31) / 32));
+  if (q.w_f32)
+    return launch_k(norm_dw_final_kernel<float>, grid, dim3(32 * kFinalWarps), 0, stream, q.h, slices, part,
+                    static_cast<float*>(dweight), static_cast<float*>(dbias));
+  return launch_k(norm_dw_final_kernel<__nv_bfloat16>, grid, dim3(32 * kFinalWarps), 0, stream, q.h, slices, part,
+                  static_cast<__nv_bfloat16*>(dweight), static_cast<__nv_bfloat16*>(dbias));
 }
 
 }  // namespace flce
