@@ -868,8 +868,71 @@ ScoreLayout score_layout(const flce_problem_t& p, int k) {
   L.cand_val = off;
   L.cand_idx = (off += cand);
   L.total = off + cand;
-  if (p.n == 0) L.total = kAlign;
   return L;
+}
+
+// A few rows: see flce_decode.cu.  Workspace: the header (status word), the CTAs' error
+// words, then per (row, part) the partials and candidates.
+struct DecodeLayout {
+  size_t err, part_m, part_l, part_s, tgt, cand, total;
+};
+
+DecodeLayout decode_layout(const flce_problem_t& p, int k) {
+  DecodeLayout L{};
+  const size_t n = static_cast<size_t>(p.n);
+  const size_t parts = n * kDecodeCtas * (p.n <= 32 ? 4 : 1);
+  size_t off = kAlign;
+  L.err = off;
+  L.part_m = (off += align_up(sizeof(int) * kDecodeCtas));
+  L.part_l = (off += align_up(sizeof(float) * parts));
+  L.part_s = (off += align_up(sizeof(float) * parts));
+  L.tgt = (off += align_up(sizeof(float) * parts));
+  L.cand = (off += align_up(sizeof(float) * n));
+  L.total = off + align_up(sizeof(uint64_t) * parts * static_cast<size_t>(k));
+  return L;
+}
+
+flce_status_t run_decode(const flce_problem_t& p, int k, float inv_temp, const void* X, const void* W,
+                         const int32_t* tokens, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                         float* top_logprobs, uint8_t* ws, cudaStream_t stream, const Device& dev) {
+  const DecodeLayout L = decode_layout(p, k);
+  if (cudaMemsetAsync(ws, 0, kAlign, stream) != cudaSuccess) return FLCE_ERR_CUDA;  // status word
+  DecodeParams dp{};
+  dp.n = static_cast<int>(p.n);
+  dp.h = static_cast<int>(p.h);
+  dp.v = static_cast<int>(p.v);
+  dp.k = k;
+  dp.a_rows = (dp.n + 7) / 8 * 8;
+  const int ctas = static_cast<int>(std::min<int64_t>(std::min(dev.sms, kDecodeCtas), (p.v + 15) / 16));
+  dp.parts = p.n <= 32 ? 4 * ctas : ctas;
+  dp.ignore_index = p.ignore_index;
+  dp.shift = p.shift;
+  dp.seq_len = p.shift ? p.seq_len : 1;
+  dp.zscale = kLog2e * inv_temp;
+  dp.timeout_ns = timeout_ns();
+  dp.tokens = tokens;
+  dp.part_m = reinterpret_cast<float*>(ws + L.part_m);
+  dp.part_l = reinterpret_cast<float*>(ws + L.part_l);
+  dp.part_s = reinterpret_cast<float*>(ws + L.part_s);
+  dp.cand = reinterpret_cast<uint64_t*>(ws + L.cand);
+  dp.tgt = reinterpret_cast<float*>(ws + L.tgt);
+  dp.err = reinterpret_cast<int*>(ws + L.err);
+  dp.status = reinterpret_cast<int*>(ws);
+  dp.part_count = p.n * dp.parts;
+  DecodeMaps maps;
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!make_map(&maps.x, X, bf16, p.h, p.n, p.h * 2, kBK, dp.a_rows)) return FLCE_ERR_CUDA;
+  if (!make_map(&maps.w, W, bf16, p.h, p.v, p.h * 2, kBK, 256)) return FLCE_ERR_CUDA;
+  if (!make_map(&maps.w_sub, W, bf16, p.h, p.v, p.h * 2, kBK, 16)) return FLCE_ERR_CUDA;
+  const double flops = 2.0 * static_cast<double>(p.n) * static_cast<double>(p.v) * static_cast<double>(p.h);
+  return cuda_status(timed(0, flops, stream, [&] {
+    return launch_decode(maps, dp, ctas, logprob, entropy, lse, top_ids, top_logprobs, stream);
+  }));
+}
+
+size_t score_bytes(const flce_problem_t& p, int k) {
+  if (p.n == 0) return kAlign;
+  return p.n <= kDecodeRows ? decode_layout(p, k).total : score_layout(p, k).total;
 }
 
 flce_status_t run_score(const flce_problem_t& p, int k, float inv_temp, const void* X, const void* W,
@@ -1302,7 +1365,7 @@ bool temperature_ok(float t) { return t > 0.f && t <= 1e30f && 1.f / t <= 1e30f;
 
 size_t flce_token_logprobs_workspace_bytes(const flce_problem_t* p, int32_t k) {
   if (check_problem(p) != FLCE_OK || k < 0 || k > kTopkMax) return 0;
-  return score_layout(*p, k).total;
+  return score_bytes(*p, k);
 }
 
 flce_status_t flce_token_logprobs(const flce_problem_t* p, int32_t k, float temperature, const void* X, const void* W,
@@ -1318,13 +1381,14 @@ flce_status_t flce_token_logprobs(const flce_problem_t* p, int32_t k, float temp
   flce_status_t st = check_problem(p);
   if (st != FLCE_OK) return st;
   if (p->n == 0) return run_empty(p, nullptr, nullptr, ws, ws_bytes, stream);
-  if (ws_bytes < score_layout(*p, k).total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < score_bytes(*p, k)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   Device dev;
   st = device_info(&dev);
   if (st != FLCE_OK) return st;
   if (!encode_fn()) return FLCE_ERR_CUDA;
-  return run_score(*p, k, 1.f / temperature, X, W, tokens, logprob, entropy, lse, top_ids, top_logprobs,
-                   static_cast<uint8_t*>(ws), reinterpret_cast<cudaStream_t>(stream), dev);
+  auto* run = p->n <= kDecodeRows ? run_decode : run_score;
+  return run(*p, k, 1.f / temperature, X, W, tokens, logprob, entropy, lse, top_ids, top_logprobs,
+             static_cast<uint8_t*>(ws), reinterpret_cast<cudaStream_t>(stream), dev);
 }
 
 flce_status_t flce_token_logprobs_backward(const flce_problem_t* p, float temperature, const void* X, const void* W,

@@ -238,6 +238,32 @@ cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv,
                                   const int32_t* cand_idx, float* logprob, float* entropy, float* lse,
                                   int32_t* top_ids, float* top_logprobs, int* status, cudaStream_t stream);
 
+// The same for a few rows (flce_decode.cu): CTAs own vocabulary ranges, at most kDecodeCtas
+// of them; with n <= 32 each reports four parts.  X and W are read through K-major maps: x
+// with a_rows (n rounded up to a multiple of 8) rows a box, w with 256, w_sub with 16.
+constexpr int kDecodeRows = 128;  // most rows
+constexpr int kDecodeCtas = 160;
+struct DecodeMaps {
+  CUtensorMap x, w, w_sub;
+};
+struct DecodeParams {
+  int n, h, v, k;
+  int a_rows;
+  int parts;  // per token
+  int ignore_index, shift, seq_len;
+  float zscale;
+  uint64_t timeout_ns;
+  const int32_t* tokens;
+  float *part_m, *part_l, *part_s;  // [n][parts]
+  uint64_t* cand;                   // [n][parts][k]
+  float* tgt;                       // [n]
+  int* err;                         // [CTAs] error codes
+  int* status;
+  int64_t part_count;               // elements of each part array (debug builds)
+};
+cudaError_t launch_decode(const DecodeMaps& maps, const DecodeParams& p, int ctas, float* logprob, float* entropy,
+                          float* lse, int32_t* top_ids, float* top_logprobs, cudaStream_t stream);
+
 // Vocabulary shards.  A shard's kernels read labels in shard-local form: -1 for an
 // ignored row (the shard calls run with ignore_index -1), y - v0 for a label the
 // shard holds, kNotOwned for a valid label held by another shard (it never equals

@@ -1,0 +1,101 @@
+// What the epilogues that walk a row of logits share: the candidates of its largest
+// values, and the arithmetic of its softmax in log2 units.
+#pragma once
+
+#include <stdint.h>
+
+#include "flce_device.cuh"
+
+namespace flce {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Below every finite logit's distance from the maximum, in log2 units: 2^it is 0, and 0
+// times it is 0, where a logit of minus infinity (a column past V, an infinite weight)
+// would make 0 * infinity.
+constexpr float kNoLogit = -1e30f;
+
+// max(a, b) that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// ----------------------------------------------------------------------------- top-k candidates
+// Each epilogue thread (one row) appends (logit, id) candidates that beat its
+// row's threshold to a buffer in the warp's shared-memory staging area (entry e
+// of lane l at topk_slot(e, l)).  Whenever a lane holds more than
+// kTopkCand - 8, the whole warp ranks that lane's entries (one per lane) and
+// keeps the best k; the threshold becomes the smallest kept.
+
+constexpr int kTopkCand = 32;
+
+struct TopkBuf {
+  float* val;    // [kTopkCand][32]
+  int* idx;      // [kTopkCand][32]
+  int count;
+  float thr;
+  unsigned* shared_thr;  // the row's threshold shared by all its vocabulary ranges (global memory), or null
+};
+
+// Word of entry e of lane l's buffer.  Rows of 32 words, the lane index XORed
+// with the entry: a warp appending at equal counts, and a warp reading one
+// lane's whole buffer (entry e by lane e), both touch 32 different banks.
+__device__ __forceinline__ int topk_slot(int e, int l) { return e * 32 + (l ^ e); }
+
+// Order-preserving map of a float to an unsigned (0 stands below every float).
+__device__ __forceinline__ unsigned topk_key(float f) {
+  const unsigned b = __float_as_uint(f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float topk_unkey(unsigned u) {
+  if (u == 0u) return -INFINITY;
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+
+__device__ __forceinline__ bool topk_better(float av, int ai, float bv, int bi) {
+  return av > bv || (av == bv && static_cast<unsigned>(ai) < static_cast<unsigned>(bi));
+}
+
+// Compact the buffers of every lane in `mask` (whole-warp call), keeping each
+// row's best `keep` (= k, at most kTopkMax).  Lane e holds entry e of the
+// buffer; its rank (how many entries beat it) comes from 32 independent shuffle
+// rounds, and the best `keep` go to slots 0..keep-1 in rank order.  Entries are
+// distinct (value, id) pairs, so the ranks of the filled slots are distinct.
+__device__ __forceinline__ void topk_compact_lanes(TopkBuf& b, int lane, unsigned mask, int keep) {
+  while (mask) {
+    const int L = __ffs(mask) - 1;
+    mask &= mask - 1;
+    const int cnt = __shfl_sync(0xffffffffu, b.count, L);
+    const bool filled = lane < cnt;
+    const float v = filled ? b.val[topk_slot(lane, L)] : -INFINITY;
+    const int i = filled ? b.idx[topk_slot(lane, L)] : -1;
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float ov = __shfl_sync(0xffffffffu, v, j);
+      const int oi = __shfl_sync(0xffffffffu, i, j);
+      rank += topk_better(ov, oi, v, i) ? 1 : 0;
+    }
+    __syncwarp();  // every entry is in registers before the slots are rewritten
+    if (filled && rank < keep) {
+      b.val[topk_slot(rank, L)] = v;
+      b.idx[topk_slot(rank, L)] = i;
+    }
+    const unsigned at_k = __ballot_sync(0xffffffffu, filled && rank == keep - 1);
+    const float kth = __shfl_sync(0xffffffffu, v, at_k ? __ffs(at_k) - 1 : 0);
+    __syncwarp();
+    if (lane == L) {
+      b.count = min(cnt, keep);
+      if (cnt >= keep && at_k) {
+        b.thr = kth;
+        // `keep` values of this row are >= kth, so any value below it, in any range, is out
+        if (b.shared_thr) atomicMax(b.shared_thr, topk_key(kth));
+      }
+    }
+  }
+}
+
+}  // namespace flce
