@@ -7,7 +7,9 @@ fallback: if the library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -28,6 +30,7 @@ EXPORTED = ("flce_workspace_bytes", "flce_workspace_bytes_rowchunk", "flce_forwa
             "flce_adamw_step", "flce_token_logprobs", "flce_token_logprobs_workspace_bytes",
             "flce_token_logprobs_backward",
             "flce_debug_checks", "flce_selftest_bounds", "flce_status_string")
+_NO_CONTEXT = contextlib.nullcontext()
 KERNEL_KINDS = ("forward", "grad", "dxdw", "small")
 
 
@@ -188,15 +191,24 @@ def workspace_bytes_rowchunk(n, h, v, ignore_index=-100, reduction="mean") -> in
     return int(lib().flce_workspace_bytes_rowchunk(ctypes.byref(p)))
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream_ptr(stream):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """The cudaStream_t of a torch stream, or of the current one (asked for without building
+    a torch.cuda.Stream object, which takes 3 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _check_inputs(x, w, labels):
@@ -676,8 +688,7 @@ def _dtype(t, name):
 def _allocating(stream):
     """Allocations inside belong to ``stream`` (the current one when None): the caching
     allocator then reuses them only after that stream's work."""
-    import contextlib
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+    return _NO_CONTEXT if stream is None else _torch().cuda.stream(stream)
 
 
 def _norm(x, weight, bias, eps):
@@ -713,6 +724,7 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, stream=None):
     return y, mean, rstd
 
 
+@functools.lru_cache(maxsize=256)
 def layernorm_workspace_bytes(n, h) -> int:
     return int(lib().flce_layernorm_workspace_bytes(ctypes.byref(Norm(int(n), int(h), int(h), 0.0, 0, 0))))
 
@@ -728,8 +740,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, bias=True, ws=None, stream=Non
     _f32(rstd, (q.n,), "rstd")
     with _allocating(stream):
         if ws is None:
-            ws = torch.empty(int(lib().flce_layernorm_workspace_bytes(ctypes.byref(q))), dtype=torch.uint8,
-                             device=x.device)
+            ws = torch.empty(layernorm_workspace_bytes(q.n, q.h), dtype=torch.uint8, device=x.device)
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dweight = torch.empty_like(weight)
         dbias = torch.empty_like(weight) if bias else None
@@ -805,6 +816,7 @@ def _check_head(x, w, tokens):
             raise ValueError("tokens must be a contiguous CUDA tensor [N]")
 
 
+@functools.lru_cache(maxsize=256)
 def token_logprobs_workspace_bytes(n, h, v, top=0) -> int:
     return int(lib().flce_token_logprobs_workspace_bytes(ctypes.byref(_problem(n, h, v, -100, "none")), int(top)))
 
@@ -820,7 +832,7 @@ def logprobs_forward(x, w, tokens=None, top=0, temperature=1.0, ignore_index=-10
     top, dev, f32 = int(top), x.device, torch.float32
     with _allocating(stream):
         if ws is None:
-            nbytes = int(lib().flce_token_logprobs_workspace_bytes(ctypes.byref(p), top))
+            nbytes = token_logprobs_workspace_bytes(n, h, w.shape[0], top)
             if nbytes == 0:
                 raise FlceError(1, "flce_token_logprobs_workspace_bytes")
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)

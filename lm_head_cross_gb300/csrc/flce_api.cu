@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -206,14 +207,20 @@ struct Device {
   bool ok = false;
 };
 
+// The current device's properties, looked up once for each.
 flce_status_t device_info(Device* d) {
+  constexpr int kKept = 64;
+  static std::atomic<int> kept[kKept];  // SMs of a device that the library runs on; 0: not looked up
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FLCE_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return FLCE_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return FLCE_ERR_CUDA;
-  if (major != 10) return FLCE_ERR_CUDA;  // the binary carries sm_103a code only
-  if (cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return FLCE_ERR_CUDA;
+  if (dev < kKept) d->sms = kept[dev].load(std::memory_order_relaxed);
+  if (d->sms == 0) {
+    int major = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return FLCE_ERR_CUDA;
+    if (major != 10) return FLCE_ERR_CUDA;  // the binary carries sm_103a code only
+    if (cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return FLCE_ERR_CUDA;
+    if (dev < kKept) kept[dev].store(d->sms, std::memory_order_relaxed);
+  }
   d->ok = true;
   return FLCE_OK;
 }
@@ -896,7 +903,6 @@ flce_status_t run_decode(const flce_problem_t& p, int k, float inv_temp, const v
                          const int32_t* tokens, float* logprob, float* entropy, float* lse, int32_t* top_ids,
                          float* top_logprobs, uint8_t* ws, cudaStream_t stream, const Device& dev) {
   const DecodeLayout L = decode_layout(p, k);
-  if (cudaMemsetAsync(ws, 0, kAlign, stream) != cudaSuccess) return FLCE_ERR_CUDA;  // status word
   DecodeParams dp{};
   dp.n = static_cast<int>(p.n);
   dp.h = static_cast<int>(p.h);
@@ -922,8 +928,8 @@ flce_status_t run_decode(const flce_problem_t& p, int k, float inv_temp, const v
   DecodeMaps maps;
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   if (!make_map(&maps.x, X, bf16, p.h, p.n, p.h * 2, kBK, dp.a_rows)) return FLCE_ERR_CUDA;
-  if (!make_map(&maps.w, W, bf16, p.h, p.v, p.h * 2, kBK, 256)) return FLCE_ERR_CUDA;
-  if (!make_map(&maps.w_sub, W, bf16, p.h, p.v, p.h * 2, kBK, 16)) return FLCE_ERR_CUDA;
+  for (int i = 0; i < kDecodeBoxes; ++i)
+    if (!make_map(&maps.w[i], W, bf16, p.h, p.v, p.h * 2, kBK, 256u >> i)) return FLCE_ERR_CUDA;
   const double flops = 2.0 * static_cast<double>(p.n) * static_cast<double>(p.v) * static_cast<double>(p.h);
   return cuda_status(timed(0, flops, stream, [&] {
     return launch_decode(maps, dp, ctas, logprob, entropy, lse, top_ids, top_logprobs, stream);

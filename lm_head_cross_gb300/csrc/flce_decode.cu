@@ -26,7 +26,7 @@ namespace flce {
 namespace {
 
 constexpr int kTileV = 256;                       // vocabulary rows of a tile
-constexpr int kSub = 16;                          // rows of the small box, and of the ranges' grain
+constexpr int kSub = 16;                          // rows of the smallest box, and the ranges' grain
 constexpr int kAStageBytes = 128 * kBK * 2;       // X rows: 16 KiB
 constexpr int kBStageBytes = kTileV * kBK * 2;    // W rows: 32 KiB
 constexpr int kRingStages = 4;
@@ -82,8 +82,8 @@ __device__ void decode_producer(const DecodeMaps& maps, const DecodeParams& p, R
   uint32_t phase = 0;
   for (int n0 = r.v0; n0 < r.v1; n0 += kTileV) {
     const int rows = min(kTileV, r.v1 - n0);
-    const int subs = rows == kTileV ? 0 : (rows + kSub - 1) / kSub;  // 0: one box of the whole tile
-    const uint32_t bytes = a_bytes + (subs ? subs * kSub : kTileV) * kBK * 2;
+    const int loaded = (rows + kSub - 1) / kSub * kSub;  // (past V: zeros)
+    const uint32_t bytes = a_bytes + loaded * kBK * 2;
     for (int kb = 0; kb < kblocks; ++kb) {
       if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag)) {
         *abort_flag = 1;
@@ -94,11 +94,12 @@ __device__ void decode_producer(const DecodeMaps& maps, const DecodeParams& p, R
       uint8_t* sb = sa + kAStageBytes;
       mbar_arrive_expect_tx(&full[stage], bytes);
       const int k0 = kb * kBK;  // a multiple of 64 elements: the copies' 16-byte rule
-      if (subs == 0) {
-        tma_load_2d(sb, &maps.w, &full[stage], k0, n0);
-      } else {
-        for (int q = 0; q < subs; ++q)
-          tma_load_2d(sb + q * kSub * kBK * 2, &maps.w_sub, &full[stage], k0, n0 + q * kSub);
+      // the tile's rows as boxes of 256, 128, ... 16, one of each at most
+      for (int i = 0, at = 0; i < kDecodeBoxes; ++i) {
+        const int box = kTileV >> i;
+        if (loaded - at < box) continue;
+        tma_load_2d(sb + at * kBK * 2, &maps.w[i], &full[stage], k0, n0 + at);
+        at += box;
       }
       for (int c = 0; c < copies; ++c) tma_load_2d(sa + c * 32 * kBK * 2, &maps.x, &full[stage], k0, 0);
       if (++stage == kRingStages) {
@@ -279,7 +280,7 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
   if (row >= p.n) return;
   const int part = narrow ? blockIdx.x * 4 + quarter : blockIdx.x;
   const int64_t at = static_cast<int64_t>(row) * p.parts + part;
-  if (!in_bounds(at, p.part_count, p.status)) return;
+  if (!in_bounds(at, p.part_count, err)) return;
   p.part_m[at] = m;
   p.part_l[at] = l;
   p.part_s[at] = es;
@@ -312,8 +313,7 @@ __global__ void __launch_bounds__(192, 1) decode_kernel(const __grid_constant__ 
     mbar_fence_init();
     fence_proxy_async_smem();
     tma_prefetch_map(&maps.x);
-    tma_prefetch_map(&maps.w);
-    tma_prefetch_map(&maps.w_sub);
+    for (int i = 0; i < kDecodeBoxes; ++i) tma_prefetch_map(&maps.w[i]);
   }
   if (warp == 1) tmem_alloc_one(tmem_slot, kDecodeTmem);
   tc_fence_before_sync();
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(192, 1) decode_kernel(const __grid_constant__ 
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   griddep_begin();  // X and W may come from the kernels before
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // every call's word starts clear; only the join adds to it
   const Range r = my_range(p);
   if (warp == 0) {
     if (lane == 0) decode_producer(maps, p, r, smem, full, empty, flags, flags + 1);
@@ -463,7 +464,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
 template <bool TOP>
 cudaError_t decode_launches(const DecodeMaps& maps, const DecodeParams& p, int ctas, float* logprob, float* entropy,
                             float* lse, int32_t* top_ids, float* top_logprobs, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecodeSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(decode_kernel<TOP>, kDecodeSmem, done);
   if (e != cudaSuccess) return e;
   e = launch_k(decode_kernel<TOP>, dim3(ctas), dim3(192), kDecodeSmem, stream, maps, p);
   if (e != cudaSuccess) return e;

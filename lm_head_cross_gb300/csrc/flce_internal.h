@@ -240,11 +240,12 @@ cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv,
 
 // The same for a few rows (flce_decode.cu): CTAs own vocabulary ranges, at most kDecodeCtas
 // of them; with n <= 32 each reports four parts.  X and W are read through K-major maps: x
-// with a_rows (n rounded up to a multiple of 8) rows a box, w with 256, w_sub with 16.
+// with a_rows (n rounded up to a multiple of 8) rows a box, w[i] with 256 >> i.
 constexpr int kDecodeRows = 128;  // most rows
 constexpr int kDecodeCtas = 160;
+constexpr int kDecodeBoxes = 5;   // 256 rows to 16
 struct DecodeMaps {
-  CUtensorMap x, w, w_sub;
+  CUtensorMap x, w[kDecodeBoxes];
 };
 struct DecodeParams {
   int n, h, v, k;

@@ -637,11 +637,12 @@ cudaError_t norm_backward_rows(const NormBackwardArgs& a, int* slices) {
   const size_t join = S::kGroups > 1 ? 2 * sizeof(float) * static_cast<size_t>(a.q.h) : 0;
   const size_t smem = std::max<size_t>(S::kRingBytes + S::kWeightBytes, join);
   auto* kernel = norm_bwd_rows_kernel<T, N, GW, VPL>;
-  if (smem > 40 * 1024) {  // 48 KB with the static part needs no leave
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  // asked for at its largest: the join needs 2 h of a row that the group's lanes hold
+  constexpr size_t kMost = std::max<size_t>(S::kRingBytes + S::kWeightBytes, 8 * 32 * GW * VPL * N);
+  static_assert(kMost <= 227 * 1024, "shared memory budget");
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = kMost > 40 * 1024 ? allow_smem(kernel, kMost, done) : cudaSuccess;
+  if (e != cudaSuccess) return e;
   const int64_t blocks = (a.q.n + S::kGroups - 1) / S::kGroups;
   *slices = static_cast<int>(std::min<int64_t>(blocks, S::kBlocks * kNormSms));
   return launch_k(kernel, dim3(*slices), dim3(S::kThreads), smem, a.stream, static_cast<int>(a.q.n), a.q.h, a.q.x_pitch,
