@@ -884,10 +884,13 @@ struct DecodeLayout {
   size_t err, part_m, part_l, part_s, tgt, cand, total;
 };
 
+// A few more than k, which spares most rows an exact cut to k.
+int decode_slots(int k) { return k > 0 ? std::min(k + k / 4 + 4, kDecodeSlots) : 0; }
+
 DecodeLayout decode_layout(const flce_problem_t& p, int k) {
   DecodeLayout L{};
   const size_t n = static_cast<size_t>(p.n);
-  const size_t parts = n * kDecodeCtas * (p.n <= 32 ? 4 : 1);
+  const size_t parts = n * kDecodeCtas * static_cast<size_t>(decode_copies(p.n));
   size_t off = kAlign;
   L.err = off;
   L.part_m = (off += align_up(sizeof(int) * kDecodeCtas));
@@ -895,7 +898,7 @@ DecodeLayout decode_layout(const flce_problem_t& p, int k) {
   L.part_s = (off += align_up(sizeof(float) * parts));
   L.tgt = (off += align_up(sizeof(float) * parts));
   L.cand = (off += align_up(sizeof(float) * n));
-  L.total = off + align_up(sizeof(uint64_t) * parts * static_cast<size_t>(k));
+  L.total = off + align_up(sizeof(uint64_t) * parts * static_cast<size_t>(decode_slots(k)));
   return L;
 }
 
@@ -908,9 +911,11 @@ flce_status_t run_decode(const flce_problem_t& p, int k, float inv_temp, const v
   dp.h = static_cast<int>(p.h);
   dp.v = static_cast<int>(p.v);
   dp.k = k;
+  dp.slots = decode_slots(k);
   dp.a_rows = (dp.n + 7) / 8 * 8;
   const int ctas = static_cast<int>(std::min<int64_t>(std::min(dev.sms, kDecodeCtas), (p.v + 15) / 16));
-  dp.parts = p.n <= 32 ? 4 * ctas : ctas;
+  dp.copies = decode_copies(p.n);
+  dp.parts = dp.copies * ctas;
   dp.ignore_index = p.ignore_index;
   dp.shift = p.shift;
   dp.seq_len = p.shift ? p.seq_len : 1;

@@ -10,8 +10,9 @@
 //
 // Warp roles: warp 0 loads, warp 1 issues the MMAs, warps 2-5 drain the other of two TMEM
 // accumulators, a token a lane.  With n <= 32 X is staged four times, at rows 0, 32, 64
-// and 96: every warp then finds all tokens in the TMEM quarter it can read, and takes a
-// quarter of the tile's columns, which shortens what is exposed after the last tile.
+// and 96 (n <= 64: twice): every warp then finds tokens in the TMEM quarter it can read,
+// and takes a quarter (half) of the tile's columns for them, which shortens what is
+// exposed after the last tile.
 //
 // A second kernel, one block per token, joins the ranges' partial results.
 #include <algorithm>
@@ -76,8 +77,7 @@ __device__ __forceinline__ Range my_range(const DecodeParams& p) {
 __device__ void decode_producer(const DecodeMaps& maps, const DecodeParams& p, Range r, uint8_t* ring, uint64_t* full,
                                 uint64_t* empty, volatile int* abort_flag, int* err) {
   const int kblocks = (p.h + kBK - 1) / kBK;
-  const int copies = p.n <= 32 ? 4 : 1;
-  const uint32_t a_bytes = static_cast<uint32_t>(copies * p.a_rows * kBK * 2);
+  const uint32_t a_bytes = static_cast<uint32_t>(p.copies * p.a_rows * kBK * 2);
   int stage = 0;
   uint32_t phase = 0;
   for (int n0 = r.v0; n0 < r.v1; n0 += kTileV) {
@@ -101,7 +101,7 @@ __device__ void decode_producer(const DecodeMaps& maps, const DecodeParams& p, R
         tma_load_2d(sb + at * kBK * 2, &maps.w[i], &full[stage], k0, n0 + at);
         at += box;
       }
-      for (int c = 0; c < copies; ++c) tma_load_2d(sa + c * 32 * kBK * 2, &maps.x, &full[stage], k0, 0);
+      for (int c = 0; c < p.copies; ++c) tma_load_2d(sa + c * (128 / p.copies) * kBK * 2, &maps.x, &full[stage], k0, 0);
       if (++stage == kRingStages) {
         stage = 0;
         phase ^= 1u;
@@ -150,25 +150,71 @@ __device__ void decode_mma(const DecodeParams& p, Range r, uint8_t* ring, uint64
   }
 }
 
+// A floor under a row's best k values, from the first `valid` columns of its window of the
+// first tile, before anything is kept: with the columns in groups of GROUP neighbours (64
+// groups cover the window), k groups whose maxima reach a value hold k values that do.
+// Bisection between the least and the greatest maximum finds nearly the greatest such value,
+// in the same instructions for every row; the columns that pass it are few (kept and ranked
+// whole instead, they took 20 instructions a column and row).  Whole-warp call; minus
+// infinity where fewer than k groups hold a column.
+template <int GROUP>
+__device__ __forceinline__ float first_floor(uint32_t tbase, int valid, int k) {
+  constexpr int kPer = 32 / GROUP;  // groups of a 32-column chunk
+  float g[2][32];
+  float lo[4] = {INFINITY, INFINITY, INFINITY, INFINITY}, hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 2 * GROUP; ++c) {
+    const int left = valid - c * 32;
+    if (left > 0) {  // the same for the whole warp
+      uint32_t v[32];
+      __syncwarp();
+      tmem_ld_32x32(tbase + c * 32, v);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        float m = __uint_as_float(v[q * GROUP]);
+#pragma unroll
+        for (int j = q * GROUP + 1; j < (q + 1) * GROUP; ++j)
+          if (j < left) m = fmaxf(m, __uint_as_float(v[j]));
+        const bool in = q * GROUP < left;
+        g[(c * kPer + q) / 32][(c * kPer + q) % 32] = in ? m : -INFINITY;
+        lo[q & 3] = fminf(lo[q & 3], in ? m : INFINITY);
+        hi[q & 3] = fmaxf(hi[q & 3], in ? m : -INFINITY);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) g[(c * kPer + q) / 32][(c * kPer + q) % 32] = -INFINITY;
+    }
+  }
+  if ((valid + GROUP - 1) / GROUP < k) return -INFINITY;
+  float least = fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3]));
+  float most = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+#pragma unroll 1
+  for (int i = 0; i < 7; ++i) {
+    const float mid = 0.5f * least + 0.5f * most;
+    if (count_reaching(g[0], mid) + count_reaching(g[1], mid) >= k) least = mid;
+    else most = mid;
+  }
+  return least;
+}
+
 // TOP: also the best k logits.
 template <bool TOP>
 __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, uint64_t* tfull, uint64_t* tempty,
                                 uint32_t tmem_base, volatile int* abort_flag, int* err) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;  // the TMEM lanes this warp may read
-  const bool narrow = p.n <= 32;
-  const int row = narrow ? lane : quarter * 32 + lane;       // token
-  const int c0 = narrow ? 2 * quarter : 0;                   // 32-column chunks of a tile this warp takes
-  const int c1 = narrow ? c0 + 2 : kTileV / 32;
-  const bool idle = !narrow && quarter * 32 >= p.n;          // a warp without a token only frees accumulators
+  const int copies = p.copies;
+  const int share = quarter / (4 / copies);                  // which of the copies it reads
+  const int row = quarter % (4 / copies) * 32 + lane;        // token
+  const int c0 = share * (8 / copies);                       // 32-column chunks of a tile this warp takes
+  const int c1 = c0 + 8 / copies;
+  const bool idle = row - lane >= p.n;                       // a warp without a token only frees accumulators
   const int y = (row < p.n) ? label_at(p.tokens, row, p.shift, p.seq_len, p.ignore_index) : p.ignore_index;
 
-  TopkBuf tk;
-  tk.val = reinterpret_cast<float*>(cand + (warp - 2) * kCandBytes);
-  tk.idx = reinterpret_cast<int*>(cand + (warp - 2) * kCandBytes + kTopkCand * 32 * sizeof(float));
-  tk.count = 0;
-  tk.thr = -INFINITY;
-  tk.shared_thr = nullptr;
+  float* val = reinterpret_cast<float*>(cand + (warp - 2) * kCandBytes);
+  int* idx = reinterpret_cast<int*>(cand + (warp - 2) * kCandBytes + kTopkCand * 32 * sizeof(float));
+  int count = 0;
+  float thr = -INFINITY;        // the range's own k-th best, once it is known: ids grow, so an equal later value is out
   float floor_thr = -INFINITY;  // nothing below it is among the row's best
   float m = -INFINITY, l = 0.f, es = 0.f;
   int acc = 0;
@@ -183,32 +229,10 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
     }
     tc_fence_after_sync();
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kTileV);
-    if (TOP && !idle && n0 == r.v0 && cols >= c1 * 32) {
-      // Before the first tile fills the buffer from nothing: each of 16 disjoint column groups
-      // holds its maximum, so nothing below the least of those is among the best 16.
-      float t0 = INFINITY;
-#pragma unroll 1
-      for (int c = c0; c < c1; ++c) {
-        __syncwarp();
-        uint32_t v[32];
-        tmem_ld_32x32(tbase + c * 32, v);
-        if (narrow) {  // groups of 4
-#pragma unroll
-          for (int g = 0; g < 8; ++g)
-            t0 = fminf(t0, fmaxf(fmaxf(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1])),
-                                 fmaxf(__uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]))));
-        } else {  // groups of 16
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float mx = __uint_as_float(v[16 * g]);
-#pragma unroll
-            for (int j = 1; j < 16; ++j) mx = fmaxf(mx, __uint_as_float(v[16 * g + j]));
-            t0 = fminf(t0, mx);
-          }
-        }
-      }
-      floor_thr = t0;
-    }
+    if (TOP && !idle && n0 == r.v0)
+      floor_thr = copies == 4   ? first_floor<1>(tbase + c0 * 32, cols - c0 * 32, p.k)
+                  : copies == 2 ? first_floor<2>(tbase + c0 * 32, cols - c0 * 32, p.k)
+                                : first_floor<4>(tbase, cols, p.k);
 #pragma unroll 1
     for (int c = c0; c < c1 && !idle; ++c) {
       if (c * 32 >= cols) break;  // the same for the whole warp
@@ -250,43 +274,60 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
       es = f * fmaf(l, d, es) + ((e4[0] + e4[1]) + (e4[2] + e4[3]));
       l = l * f + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
       m = new_m;
-      if (TOP && __any_sync(0xffffffffu, row < p.n && cmax > tk.thr && cmax >= floor_thr)) {
+      if (TOP && __any_sync(0xffffffffu, row < p.n && cmax > thr && cmax >= floor_thr)) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          if (!__any_sync(0xffffffffu, row < p.n && gmax[g] > tk.thr && gmax[g] >= floor_thr)) continue;
+          if (!__any_sync(0xffffffffu, row < p.n && gmax[g] > thr && gmax[g] >= floor_thr)) continue;
 #pragma unroll
           for (int j = 8 * g; j < 8 * g + 8; ++j) {
             const float x = __uint_as_float(v[j]);
             // ids grow along the range: an equal later value ranks after the kept one
-            const bool keep = row < p.n && x > tk.thr && x >= floor_thr;
-            const int at = topk_slot(tk.count, lane);
+            const bool keep = row < p.n && x > thr && x >= floor_thr;
+            const int at = topk_slot(count, lane);
             if (keep) {
-              tk.val[at] = x;
-              tk.idx[at] = col0 + j;
+              val[at] = x;
+              idx[at] = col0 + j;
             }
-            tk.count += keep ? 1 : 0;
+            count += keep ? 1 : 0;
           }
-          topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > kTopkCand - 8), p.k);
+          if (__any_sync(0xffffffffu, count > kTopkCand - 8)) {
+            Trimmed t = topk_trim(val, idx, count, lane, p.k, floor_thr);
+            floor_thr = t.thr;
+            t = topk_cut(val, idx, t.count, thr, lane, p.k, kTopkCand - 8);  // (many equal values: ranked)
+            count = t.count;
+            thr = t.thr;
+          }
         }
       }
     }
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&tempty[acc]);
+    // Room for the next tile's, made while that one loads.
+    if (TOP && n0 + kTileV < r.v1 && __any_sync(0xffffffffu, count > p.k + 2)) {
+      const Trimmed t = topk_trim(val, idx, count, lane, p.k, floor_thr);
+      count = t.count;
+      floor_thr = t.thr;
+    }
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
   }
-  if (TOP) topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > p.k), p.k);
+  if (TOP && __any_sync(0xffffffffu, count > p.slots)) {
+    count = topk_trim(val, idx, count, lane, p.k, floor_thr).count;
+    count = topk_cut(val, idx, count, thr, lane, p.k, p.slots).count;
+  }
   if (row >= p.n) return;
-  const int part = narrow ? blockIdx.x * 4 + quarter : blockIdx.x;
+  const int part = blockIdx.x * copies + share;
   const int64_t at = static_cast<int64_t>(row) * p.parts + part;
   if (!in_bounds(at, p.part_count, err)) return;
   p.part_m[at] = m;
   p.part_l[at] = l;
   p.part_s[at] = es;
-  if (TOP)
-    for (int e = 0; e < p.k; ++e)
-      p.cand[at * p.k + e] = e < tk.count ? candidate_key(tk.val[topk_slot(e, lane)], tk.idx[topk_slot(e, lane)]) : 0;
+  if (TOP) {
+#pragma unroll 4
+    for (int e = 0; e < p.slots; ++e)
+      p.cand[at * p.slots + e] = e < count ? candidate_key(val[topk_slot(e, lane)], idx[topk_slot(e, lane)]) : 0;
+  }
 }
 
 template <bool TOP>
@@ -347,51 +388,67 @@ __global__ void __launch_bounds__(192, 1) decode_kernel(const __grid_constant__ 
 
 // ----------------------------------------------------------------------------- joining the ranges
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 512;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
 // One block per token: lse, entropy and the given token's log probability from the ranges'
-// (max, sum, entropy sum), and the best k of their candidates.  For those, each thread takes
-// every 128th range's list; the k-th largest of the threads' maxima is a bound that at least
-// k candidates reach and few pass (at most k threads' lists hold any that do); those few are
-// ranked by counting.
+// (max, sum, entropy sum), and the best k of their candidates.  Those are a few thousand
+// numbers that the threads hold in registers.  The k-th largest of the 16 warps' maxima is a
+// bound that k candidates reach and few pass; where at most a block of them does, each is
+// ranked by counting, else k rounds of a maximum over the block pick the best in order
+// (0.7 us a round).
 template <bool TOP>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeParams p, int ctas, float* logprob,
                                                                    float* entropy, float* lse, int32_t* top_ids,
                                                                    float* top_logprobs) {
   griddep_begin();
   constexpr int kMostParts = (4 * kDecodeCtas + kJoinThreads - 1) / kJoinThreads;
-  __shared__ float red[3][kJoinThreads / 32];
-  __shared__ __align__(16) uint64_t maxima[kJoinThreads];
-  __shared__ uint64_t kept[TOP ? kTopkMax * kMostParts * kTopkMax : 1];
-  __shared__ uint64_t bound;
+  constexpr int kMostCands = TOP ? (4 * kDecodeCtas * kDecodeSlots + kJoinThreads - 1) / kJoinThreads : 1;
+  __shared__ float red[3][kJoinWarps];
+  __shared__ __align__(16) uint64_t round_best[2][kJoinWarps];
+  __shared__ uint64_t kept[TOP ? kJoinThreads : 1];
   __shared__ int kept_count;
   const int row = blockIdx.x, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int64_t base = static_cast<int64_t>(row) * p.parts;
-  uint64_t best = 0;
-  float m = -INFINITY;
-  for (int s = t; s < p.parts; s += kJoinThreads) {
-    m = fmaxf(m, p.part_m[base + s]);
-    if (TOP)
-      for (int e = 0; e < p.k; ++e) best = max(best, p.cand[(base + s) * p.k + e]);
+  // this thread's parts and candidates, loads first
+  float pm[kMostParts], pl[kMostParts], ps[kMostParts];
+#pragma unroll
+  for (int i = 0; i < kMostParts; ++i) {
+    const int s = t + i * kJoinThreads;
+    const bool in = s < p.parts;
+    pm[i] = in ? p.part_m[base + s] : -INFINITY;
+    pl[i] = in ? p.part_l[base + s] : 0.f;
+    ps[i] = in ? p.part_s[base + s] : 0.f;
   }
+  uint64_t key[kMostCands], best = 0;
+  if (TOP) {
+    const uint64_t* cand = p.cand + base * p.slots;
+    const int cands = p.parts * p.slots;
+#pragma unroll
+    for (int i = 0; i < kMostCands; ++i) {
+      const int c = t + i * kJoinThreads;
+      key[i] = c < cands ? cand[c] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kMostCands; ++i)
+      if (key[i] > best) best = key[i];
+  }
+  float m = pm[0];
+#pragma unroll
+  for (int i = 1; i < kMostParts; ++i) m = fmaxf(m, pm[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red[0][warp] = m;
-  if (TOP) {
-    maxima[t] = best;
-    if (t == 0) {
-      bound = 0;
-      kept_count = 0;
-    }
-  }
   __syncthreads();
-  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[0][w]);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red[0][w]);
   float l = 0.f, es = 0.f;
-  for (int s = t; s < p.parts; s += kJoinThreads) {
-    const float d = max_nan(p.part_m[base + s] - m, kNoLogit), pl = p.part_l[base + s];
+#pragma unroll
+  for (int i = 0; i < kMostParts; ++i) {
+    const float d = max_nan(pm[i] - m, kNoLogit);
     const float f = exp2f(d);
-    l += pl * f;
-    es += f * fmaf(pl, d, p.part_s[base + s]);
+    l += pl[i] * f;
+    es += f * fmaf(pl[i], d, ps[i]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -402,18 +459,10 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
     red[1][warp] = l;
     red[2][warp] = es;
   }
-  if (TOP && best != 0) {  // distinct non-zero numbers: one thread has this rank, if that many are non-zero
-    int rank = 0;
-#pragma unroll 8
-    for (int q = 0; q < kJoinThreads; q += 2) {
-      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&maxima[q]);
-      rank += (o.x > best) + (o.y > best);
-    }
-    if (rank == p.k - 1) bound = best;
-  }
   __syncthreads();
   l = es = 0.f;
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
     l += red[1][w];
     es += red[2][w];
   }
@@ -421,43 +470,82 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
   if (t == 0) {
     lse[row] = (m + log2l) * kLn2;
     if (entropy) entropy[row] = (log2l - es / l) * kLn2;
-  }
-  int code = 0;
-  if (t == 0 && p.tokens) {
-    const int y = label_at(p.tokens, row, p.shift, p.seq_len, p.ignore_index);
-    float lp = 0.f;
-    if (y != p.ignore_index) {
-      if (y >= 0 && y < p.v) lp = (fmaf(p.tgt[row], p.zscale, -m) - log2l) * kLn2;
-      else code = kErrLabel;
-    }
-    if (logprob) logprob[row] = lp;
-  }
-  if (code) atomicCAS(p.status, 0, code);
-  if (row == 0)
-    for (int c = t; c < ctas; c += kJoinThreads)
-      if (p.err[c]) atomicCAS(p.status, 0, p.err[c]);
-  if (!TOP) return;
-  if (best >= bound && best != 0)
-    for (int s = t; s < p.parts; s += kJoinThreads)
-      for (int e = 0; e < p.k; ++e) {
-        const uint64_t key = p.cand[(base + s) * p.k + e];
-        if (key != 0 && key >= bound) kept[atomicAdd(&kept_count, 1)] = key;
+    if (p.tokens) {
+      const int y = label_at(p.tokens, row, p.shift, p.seq_len, p.ignore_index);
+      float lp = 0.f;
+      if (y != p.ignore_index) {
+        // relative to the same m as l: exact where the token holds the largest logit
+        if (y >= 0 && y < p.v) lp = (fmaf(p.tgt[row], p.zscale, -m) - log2l) * kLn2;
+        else atomicCAS(p.status, 0, kErrLabel);
       }
-  __syncthreads();
-  const int count = kept_count;
-  for (int i = t; i < count; i += kJoinThreads) {
-    const uint64_t key = kept[i];
-    int rank = 0;
-    for (int q = 0; q < count; ++q) rank += kept[q] > key;
-    if (rank < p.k) {
-      const float z = topk_unkey(static_cast<unsigned>(key >> 32));
-      top_ids[static_cast<int64_t>(row) * p.k + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key));
-      top_logprobs[static_cast<int64_t>(row) * p.k + rank] = (fmaf(z, p.zscale, -m) - log2l) * kLn2;
+      if (logprob) logprob[row] = lp;
     }
   }
-  for (int i = count + t; i < p.k; i += kJoinThreads) {  // fewer than k ids
-    top_ids[static_cast<int64_t>(row) * p.k + i] = -1;
-    top_logprobs[static_cast<int64_t>(row) * p.k + i] = -INFINITY;
+  if (row == 0 && t < ctas && p.err[t]) atomicCAS(p.status, 0, p.err[t]);
+  if (!TOP) return;
+  const auto put = [&](int rank, uint64_t won) {
+    const float z = topk_unkey(static_cast<unsigned>(won >> 32));
+    top_ids[static_cast<int64_t>(row) * p.k + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(won));
+    top_logprobs[static_cast<int64_t>(row) * p.k + rank] = (fmaf(z, p.zscale, -m) - log2l) * kLn2;
+  };
+  {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
+    if (lane == 0) round_best[0][warp] = (static_cast<uint64_t>(hi) << 32) | lo;
+    if (t == 0) kept_count = 0;
+    __syncthreads();
+    uint64_t bound = 0;  // 0: fewer than k warps hold a candidate
+    const uint64_t mine = lane < kJoinWarps ? round_best[0][lane] : 0;
+    int rank = 0;
+    for (int w = 0; w < kJoinWarps; ++w) rank += round_best[0][w] > mine;
+    const unsigned at = __ballot_sync(0xffffffffu, mine != 0 && rank == p.k - 1);
+    if (at) bound = round_best[0][__ffs(at) - 1];
+    if (best >= bound) {
+#pragma unroll
+      for (int i = 0; i < kMostCands; ++i)
+        if (key[i] != 0 && key[i] >= bound) {
+          const int slot = atomicAdd(&kept_count, 1);
+          if (slot < kJoinThreads) kept[slot] = key[i];
+        }
+    }
+    __syncthreads();
+    const int count = kept_count;
+    if (count <= kJoinThreads) {
+      if (t < count) {
+        const uint64_t won = kept[t];
+        int place = 0;
+        for (int q = 0; q < count; ++q) place += kept[q] > won;
+        if (place < p.k) put(place, won);
+      } else if (t < p.k) {  // fewer than k ids
+        top_ids[static_cast<int64_t>(row) * p.k + t] = -1;
+        top_logprobs[static_cast<int64_t>(row) * p.k + t] = -INFINITY;
+      }
+      return;
+    }
+  }
+  for (int r = 0; r < p.k; ++r) {
+    __syncthreads();  // the words of two rounds ago, and the filter's, have been read
+    // the warp's best: the largest value, then the largest id word among its holders
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
+    if (lane == 0) round_best[r & 1][warp] = (static_cast<uint64_t>(hi) << 32) | lo;
+    __syncthreads();
+    uint64_t win = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; w += 2) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&round_best[r & 1][w]);
+      if (o.x > win) win = o.x;
+      if (o.y > win) win = o.y;
+    }
+    if (win == best && win != 0) {  // its holder (candidates are distinct)
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < kMostCands; ++i) {
+        if (key[i] == win) key[i] = 0;
+        if (key[i] > best) best = key[i];
+      }
+      put(r, win);
+    }
   }
 }
 

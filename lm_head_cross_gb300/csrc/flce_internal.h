@@ -239,24 +239,28 @@ cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv,
                                   int32_t* top_ids, float* top_logprobs, int* status, cudaStream_t stream);
 
 // The same for a few rows (flce_decode.cu): CTAs own vocabulary ranges, at most kDecodeCtas
-// of them; with n <= 32 each reports four parts.  X and W are read through K-major maps: x
+// of them.  X and W are read through K-major maps: x
 // with a_rows (n rounded up to a multiple of 8) rows a box, w[i] with 256 >> i.
 constexpr int kDecodeRows = 128;  // most rows
+inline int decode_copies(int64_t n) { return n <= 32 ? 4 : n <= 64 ? 2 : 1; }
 constexpr int kDecodeCtas = 160;
 constexpr int kDecodeBoxes = 5;   // 256 rows to 16
+constexpr int kDecodeSlots = 24;  // most candidates of a part
 struct DecodeMaps {
   CUtensorMap x, w[kDecodeBoxes];
 };
 struct DecodeParams {
   int n, h, v, k;
   int a_rows;
-  int parts;  // per token
+  int copies;  // of X on the MMA's 128 rows: 4, 2 or 1; each reports a part of the CTA's range
+  int parts;   // per token
+  int slots;   // candidates a part may report, at least k
   int ignore_index, shift, seq_len;
   float zscale;
   uint64_t timeout_ns;
   const int32_t* tokens;
   float *part_m, *part_l, *part_s;  // [n][parts]
-  uint64_t* cand;                   // [n][parts][k]
+  uint64_t* cand;                   // [n][parts][slots]
   float* tgt;                       // [n]
   int* err;                         // [CTAs] error codes
   int* status;

@@ -59,6 +59,14 @@ __device__ __forceinline__ bool topk_better(float av, int ai, float bv, int bi) 
   return av > bv || (av == bv && static_cast<unsigned>(ai) < static_cast<unsigned>(bi));
 }
 
+// How many of 32 values reach `at`, in four independent chains.
+__device__ __forceinline__ int count_reaching(const float (&v)[32], float at) {
+  int n[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 32; ++e) n[e & 3] += v[e] >= at ? 1 : 0;
+  return (n[0] + n[1]) + (n[2] + n[3]);
+}
+
 // Compact the buffers of every lane in `mask` (whole-warp call), keeping each
 // row's best `keep` (= k, at most kTopkMax).  Lane e holds entry e of the
 // buffer; its rank (how many entries beat it) comes from 32 independent shuffle
@@ -96,6 +104,69 @@ __device__ __forceinline__ void topk_compact_lanes(TopkBuf& b, int lane, unsigne
       }
     }
   }
+}
+
+// Drops what cannot be among a row's best k from every lane's buffer at once (whole-warp
+// call): bisection between the least and the greatest entry of a lane that holds more than
+// k finds a value that k entries reach and few others do; those stay, in their order, and
+// the value is returned as the row's new floor (the old one for other lanes).  About 900
+// instructions for the warp, where ranking takes 220 for each lane; out of line, as is the
+// ranking behind it, so that the code that every chunk runs through stays short.
+struct Trimmed {
+  int count;
+  float thr;
+};
+static __device__ __noinline__ Trimmed topk_trim(float* val, int* idx, int count, int lane, int k, float floor_thr) {
+  float v[kTopkCand];
+  float lo4[4], hi4[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo4[i] = INFINITY;
+    hi4[i] = -INFINITY;
+  }
+#pragma unroll
+  for (int e = 0; e < kTopkCand; ++e) {
+    v[e] = e < count ? val[topk_slot(e, lane)] : -INFINITY;
+    if (e < count) lo4[e & 3] = fminf(lo4[e & 3], v[e]);
+    hi4[e & 3] = fmaxf(hi4[e & 3], v[e]);
+  }
+  float lo = fminf(fminf(lo4[0], lo4[1]), fminf(lo4[2], lo4[3]));
+  float hi = fmaxf(fmaxf(hi4[0], hi4[1]), fmaxf(hi4[2], hi4[3]));
+  if (count <= k) lo = -INFINITY;  // everything stays
+#pragma unroll 1
+  for (int i = 0; i < 7; ++i) {
+    const float mid = 0.5f * lo + 0.5f * hi;
+    const bool up = count_reaching(v, mid) >= k && count > k;
+    lo = up ? mid : lo;
+    hi = up ? hi : mid;
+  }
+  int id[kTopkCand];  // read whole before anything is rewritten
+#pragma unroll
+  for (int e = 0; e < kTopkCand; ++e) id[e] = idx[topk_slot(e, lane)];
+  int at = 0;
+#pragma unroll
+  for (int e = 0; e < kTopkCand; ++e) {
+    const bool keep = e < count && v[e] >= lo;
+    if (keep) {
+      val[topk_slot(at, lane)] = v[e];
+      idx[topk_slot(at, lane)] = id[e];
+    }
+    at += keep ? 1 : 0;
+  }
+  __syncwarp();
+  return Trimmed{at, fmaxf(floor_thr, lo)};
+}
+
+// topk_compact_lanes for the lanes that hold more than `most`: their new count and threshold.
+static __device__ __noinline__ Trimmed topk_cut(float* val, int* idx, int count, float thr, int lane, int k, int most) {
+  TopkBuf b;
+  b.val = val;
+  b.idx = idx;
+  b.count = count;
+  b.thr = thr;
+  b.shared_thr = nullptr;
+  topk_compact_lanes(b, lane, __ballot_sync(0xffffffffu, count > most), k);
+  return Trimmed{b.count, b.thr};
 }
 
 }  // namespace flce
