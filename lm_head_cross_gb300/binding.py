@@ -677,10 +677,10 @@ def sparse_kl_divergence(x, w, tgt_idx, tgt_prob, reduction: str = "mean", rowch
 
 def _dtype(t, name):
     """flce_dtype_t of a tensor: 0 bf16, 1 fp32."""
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
+    torch, kind = _torch(), t.dtype
+    if kind is torch.bfloat16:
         return 0
-    if t.dtype == torch.float32:
+    if kind is torch.float32:
         return 1
     raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
@@ -692,20 +692,20 @@ def _allocating(stream):
 
 
 def _norm(x, weight, bias, eps):
-    if x.dim() != 2 or weight.dim() != 1 or weight.shape[0] != x.shape[1]:
+    if x.dim() != 2 or weight.dim() != 1:
         raise ValueError(f"x must be [N, H] and weight [H], got {tuple(x.shape)} and {tuple(weight.shape)}")
-    if bias is not None and (bias.shape != weight.shape or bias.dtype != weight.dtype):
-        raise ValueError("bias must have weight's shape and dtype")
     n, h = x.shape
-    if h < 1:
-        raise ValueError("x has no columns")
-    if not (x.is_cuda and weight.is_cuda and (bias is None or bias.is_cuda)):
-        raise ValueError("x, weight and bias must be CUDA tensors")
-    if (h > 1 and x.stride(1) != 1) or (n > 1 and x.stride(0) < h):
+    if h < 1 or weight.numel() != h:
+        raise ValueError(f"x must be [N, H] and weight [H], H >= 1, got {tuple(x.shape)} and {tuple(weight.shape)}")
+    if not (x.is_cuda and weight.is_cuda and weight.is_contiguous()):
+        raise ValueError("x and weight must be CUDA tensors, weight contiguous")
+    if bias is not None and (bias.shape != weight.shape or bias.dtype != weight.dtype or not bias.is_cuda
+                             or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous CUDA tensor of weight's shape and dtype")
+    pitch, along = x.stride()
+    if (h > 1 and along != 1) or (n > 1 and pitch < h):
         raise ValueError("the rows of x must be contiguous and must not overlap")
-    if not (weight.is_contiguous() and (bias is None or bias.is_contiguous())):
-        raise ValueError("weight and bias must be contiguous")
-    return Norm(n, h, x.stride(0) if n > 1 else h, float(eps), _dtype(x, "x"), _dtype(weight, "weight"))
+    return Norm(n, h, pitch if n > 1 else h, eps, _dtype(x, "x"), _dtype(weight, "weight"))
 
 
 def layernorm_forward(x, weight, bias=None, eps=1e-5, stream=None):
@@ -715,9 +715,9 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, stream=None):
     torch = _torch()
     q = _norm(x, weight, bias, eps)
     with _allocating(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
         mean = torch.empty(q.n, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(q.n, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
     _call("flce_layernorm_forward", lib().flce_layernorm_forward(
         ctypes.byref(q), x.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(), y.data_ptr(),
         mean.data_ptr(), rstd.data_ptr(), _stream_ptr(stream)))
@@ -741,7 +741,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, bias=True, ws=None, stream=Non
     with _allocating(stream):
         if ws is None:
             ws = torch.empty(layernorm_workspace_bytes(q.n, q.h), dtype=torch.uint8, device=x.device)
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(dy)
         dweight = torch.empty_like(weight)
         dbias = torch.empty_like(weight) if bias else None
     _call("flce_layernorm_backward", lib().flce_layernorm_backward(
@@ -805,14 +805,14 @@ def _check_head(x, w, tokens):
     torch = _torch()
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise ValueError(f"x must be [N, H] and w [V, H], got {tuple(x.shape)} and {tuple(w.shape)}")
-    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+    if x.dtype is not torch.bfloat16 or w.dtype is not torch.bfloat16:
         raise TypeError("x and w must be bfloat16")
     if not (x.is_cuda and w.is_cuda and x.is_contiguous() and w.is_contiguous()):
         raise ValueError("x and w must be contiguous CUDA tensors")
     if tokens is not None:
-        if tokens.dtype != torch.int32:
+        if tokens.dtype is not torch.int32:
             raise TypeError("tokens must be int32")
-        if tokens.shape != (x.shape[0],) or not tokens.is_cuda or not tokens.is_contiguous():
+        if tokens.dim() != 1 or tokens.numel() != x.shape[0] or not tokens.is_cuda or not tokens.is_contiguous():
             raise ValueError("tokens must be a contiguous CUDA tensor [N]")
 
 
@@ -836,8 +836,9 @@ def logprobs_forward(x, w, tokens=None, top=0, temperature=1.0, ignore_index=-10
             if nbytes == 0:
                 raise FlceError(1, "flce_token_logprobs_workspace_bytes")
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        lp = None if tokens is None else torch.empty(n, dtype=f32, device=dev)
-        entropy, lse = torch.empty(n, dtype=f32, device=dev), torch.empty(n, dtype=f32, device=dev)
+        lse = torch.empty(n, dtype=f32, device=dev)
+        entropy = torch.empty_like(lse)
+        lp = None if tokens is None else torch.empty_like(lse)
         ids = torch.empty(n, top, dtype=torch.int32, device=dev) if top > 0 else None
         tlp = torch.empty(n, top, dtype=f32, device=dev) if top > 0 else None
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
