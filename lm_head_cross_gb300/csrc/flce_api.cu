@@ -855,7 +855,7 @@ flce_status_t run_topk(const Ctx& c, int k, const void* X, const void* W, int32_
 // (split, row) the partial maximum, sum and entropy sum, the rows' target logits and, for
 // the alternatives, shared thresholds and the splits' candidates.
 struct ScoreLayout {
-  size_t part_m, part_l, part_s, tgt, thr, cand_val, cand_idx, total;
+  size_t part_m, part_l, part_s, tgt, thr, cand, total;
   int splits;
 };
 
@@ -871,10 +871,8 @@ ScoreLayout score_layout(const flce_problem_t& p, int k) {
   L.tgt = (off += part);
   L.thr = (off += align_up(sizeof(float) * n));
   if (k > 0) off += align_up(sizeof(unsigned) * n);
-  const size_t cand = k > 0 ? align_up(sizeof(float) * static_cast<size_t>(L.splits) * n * kTopkMax) : 0;
-  L.cand_val = off;
-  L.cand_idx = (off += cand);
-  L.total = off + cand;
+  L.cand = off;
+  L.total = off + align_up(sizeof(uint64_t) * static_cast<size_t>(L.splits) * n * static_cast<size_t>(k));
   return L;
 }
 
@@ -982,10 +980,9 @@ flce_status_t run_score(const flce_problem_t& p, int k, float inv_temp, const vo
   tp.part_count = static_cast<int64_t>(L.splits) * p.n;
   if (k > 0) {
     tp.topk_thr = reinterpret_cast<unsigned*>(ws + L.thr);
-    tp.topk_val = reinterpret_cast<float*>(ws + L.cand_val);
-    tp.topk_idx = reinterpret_cast<int32_t*>(ws + L.cand_idx);
+    tp.topk_keys = reinterpret_cast<uint64_t*>(ws + L.cand);
     tp.topk_k = k;
-    tp.topk_count = static_cast<int64_t>(L.splits) * p.n * kTopkMax;
+    tp.topk_count = static_cast<int64_t>(L.splits) * p.n * k;
   }
   const double flops = 2.0 * static_cast<double>(p.n) * static_cast<double>(p.v) * static_cast<double>(p.h);
   const int grid = pair_grid(dev.sms, static_cast<long long>(tp.row_tiles) * tp.vsplit);
@@ -996,8 +993,7 @@ flce_status_t run_score(const flce_problem_t& p, int k, float inv_temp, const vo
   const LabelView lv{tokens, p.ignore_index, p.shift, p.shift ? p.seq_len : 1, nullptr, nullptr, 0};
   return cuda_status(timed(3, 0.0, stream, [&] {
     return launch_score_finalize(tp.n, tp.v, tp.vsplit, k, lv, tp.zscale, tp.part_m, tp.part_l, tp.part_s, tp.tgt,
-                                 tp.topk_val, tp.topk_idx, logprob, entropy, lse, top_ids, top_logprobs, tp.status,
-                                 stream);
+                                 tp.topk_keys, logprob, entropy, lse, top_ids, top_logprobs, tp.status, stream);
   }));
 }
 

@@ -59,11 +59,6 @@ __device__ __forceinline__ void umma_commit_one(uint64_t* bar) {
                : "memory");
 }
 
-// (value, id) as one number that grows with the value and, among equal ones, as the id falls; 0: none.
-__device__ __forceinline__ uint64_t candidate_key(float v, int id) {
-  return (static_cast<uint64_t>(topk_key(v + 0.f)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
-}
-
 struct Range {
   int v0, v1;  // vocabulary rows [v0, v1)
 };
@@ -148,53 +143,6 @@ __device__ void decode_mma(const DecodeParams& p, Range r, uint8_t* ring, uint64
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
   }
-}
-
-// A floor under a row's best k values, from the first `valid` columns of its window of the
-// first tile, before anything is kept: with the columns in groups of GROUP neighbours (64
-// groups cover the window), k groups whose maxima reach a value hold k values that do.
-// Bisection between the least and the greatest maximum finds nearly the greatest such value,
-// in the same instructions for every row; the columns that pass it are few (kept and ranked
-// whole instead, they took 20 instructions a column and row).  Whole-warp call; minus
-// infinity where fewer than k groups hold a column.
-template <int GROUP>
-__device__ __forceinline__ float first_floor(uint32_t tbase, int valid, int k) {
-  constexpr int kPer = 32 / GROUP;  // groups of a 32-column chunk
-  float g[2][32];
-  float lo[4] = {INFINITY, INFINITY, INFINITY, INFINITY}, hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int c = 0; c < 2 * GROUP; ++c) {
-    const int left = valid - c * 32;
-    if (left > 0) {  // the same for the whole warp
-      uint32_t v[32];
-      __syncwarp();
-      tmem_ld_32x32(tbase + c * 32, v);
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        float m = __uint_as_float(v[q * GROUP]);
-#pragma unroll
-        for (int j = q * GROUP + 1; j < (q + 1) * GROUP; ++j)
-          if (j < left) m = fmaxf(m, __uint_as_float(v[j]));
-        const bool in = q * GROUP < left;
-        g[(c * kPer + q) / 32][(c * kPer + q) % 32] = in ? m : -INFINITY;
-        lo[q & 3] = fminf(lo[q & 3], in ? m : INFINITY);
-        hi[q & 3] = fmaxf(hi[q & 3], in ? m : -INFINITY);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) g[(c * kPer + q) / 32][(c * kPer + q) % 32] = -INFINITY;
-    }
-  }
-  if ((valid + GROUP - 1) / GROUP < k) return -INFINITY;
-  float least = fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3]));
-  float most = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
-#pragma unroll 1
-  for (int i = 0; i < 7; ++i) {
-    const float mid = 0.5f * least + 0.5f * most;
-    if (count_reaching(g[0], mid) + count_reaching(g[1], mid) >= k) least = mid;
-    else most = mid;
-  }
-  return least;
 }
 
 // TOP: also the best k logits.

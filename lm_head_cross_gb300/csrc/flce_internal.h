@@ -106,6 +106,7 @@ struct TcParams {
   float* topk_val;
   int32_t* topk_idx;
   int topk_k;
+  uint64_t* topk_keys;  // score modes: the same as candidate keys, [n][vsplit][topk_k]
   unsigned* topk_thr;   // top-k: per row the best 16th-best value any range has reached (ordered key), zeroed
   int units_group;      // forward modes: row tiles per unit group (see units_group_rows)
   // element counts of the buffers above that are indexed by computed offsets (checked in
@@ -234,8 +235,8 @@ inline int score_splits(int64_t n) {
   return static_cast<int>(s < 16 ? 16 : s > kScoreSplitMax ? kScoreSplitMax : s);
 }
 cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv, float zscale, const float* part_m,
-                                  const float* part_l, const float* part_s, const float* tgt, const float* cand_val,
-                                  const int32_t* cand_idx, float* logprob, float* entropy, float* lse,
+                                  const float* part_l, const float* part_s, const float* tgt,
+                                  const uint64_t* cand_keys, float* logprob, float* entropy, float* lse,
                                   int32_t* top_ids, float* top_logprobs, int* status, cudaStream_t stream);
 
 // The same for a few rows (flce_decode.cu): CTAs own vocabulary ranges, at most kDecodeCtas

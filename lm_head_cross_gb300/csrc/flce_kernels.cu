@@ -543,7 +543,14 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
         }
       }
       if (kTop<MODE> && tk.shared_thr) gthr = topk_unkey(thr_key);
-      if (kTop<MODE> && t.first) {
+      if (MODE == kModeScoreTop && t.first) {
+        const float t0 = first_floor<4>(tbase, min(kBN, p.v - t.n0), p.topk_k);
+        if (t0 > gthr) {
+          gthr = t0;
+          if (tk.shared_thr) atomicMax(tk.shared_thr, topk_key(t0));
+        }
+      }
+      if (MODE == kModeTopk && t.first) {
         // Before a range's first tile fills the candidate buffer from nothing: each of
         // the tile's 16 disjoint 16-column groups holds its max, so at least kTopkMax
         // values of the row are >= the smallest of those maxima, and nothing below it
@@ -654,7 +661,21 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
                   }
                   tk.count += keep ? 1 : 0;
                 }
-                topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > kTopkCand - 8), p.topk_k);
+                if constexpr (MODE == kModeScoreTop) {
+                  if (__any_sync(0xffffffffu, tk.count > kTopkCand - 8)) {
+                    Trimmed tr = topk_trim(tk.val, tk.idx, tk.count, lane, p.topk_k, gthr);
+                    if (tr.thr > gthr) {
+                      gthr = tr.thr;
+                      if (tk.shared_thr) atomicMax(tk.shared_thr, topk_key(gthr));
+                    }
+                    // (many equal values: ranked)
+                    tr = topk_cut(tk.val, tk.idx, tr.count, tk.thr, lane, p.topk_k, kTopkCand - 8);
+                    tk.count = tr.count;
+                    tk.thr = tr.thr;
+                  }
+                } else {
+                  topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > kTopkCand - 8), p.topk_k);
+                }
               }
             }
           }
@@ -730,8 +751,12 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
         run_l = run_l * fast_exp2(run_m - new_m) + sum * fast_exp2(ref - new_m);
         run_m = new_m;
       }
-      if (kTop<MODE> && t.last)
+      if (MODE == kModeTopk && t.last)
         topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > p.topk_k), p.topk_k);
+      if (MODE == kModeScoreTop && t.last && __any_sync(0xffffffffu, tk.count > p.topk_k)) {
+        tk.count = topk_trim(tk.val, tk.idx, tk.count, lane, p.topk_k, gthr).count;
+        tk.count = topk_cut(tk.val, tk.idx, tk.count, tk.thr, lane, p.topk_k, p.topk_k).count;
+      }
       if (t.last && row < row_end) {
         const int osplit = (Cfg<MODE>::kEpiWarps == 8) ? 2 * t.split + ehalf : t.split;
         const int64_t pi = static_cast<int64_t>(osplit) * p.n + row;
@@ -741,7 +766,15 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
           if (kScoring<MODE>) p.part_s[pi] = run_s;
         }
         if (found && in_bounds(row, p.n, p.status)) p.tgt[row] = z_tgt;
-        if (kTop<MODE>) {
+        if (MODE == kModeScoreTop) {
+          const int64_t base = (static_cast<int64_t>(row) * p.vsplit + t.split) * p.topk_k;
+          for (int i = 0; i < p.topk_k; ++i) {
+            if (!in_bounds(base + i, p.topk_count, p.status)) break;
+            p.topk_keys[base + i] =
+                i < tk.count ? candidate_key(tk.val[topk_slot(i, lane)], tk.idx[topk_slot(i, lane)]) : 0;
+          }
+        }
+        if (MODE == kModeTopk) {
           const int kept = tk.count;  // at most k (the merge does not need them sorted)
           const int64_t base = (static_cast<int64_t>(osplit) * p.n + row) * kTopkMax;
           for (int i = 0; i < kTopkMax; ++i) {
@@ -1635,10 +1668,12 @@ template <int kPer>
 __global__ void __launch_bounds__(256) score_finalize_kernel(
     int n, int v, int nsplit, int k, LabelView lv, float zscale, const float* __restrict__ part_m,
     const float* __restrict__ part_l, const float* __restrict__ part_s, const float* __restrict__ tgt,
-    const float* __restrict__ cand_val, const int32_t* __restrict__ cand_idx, float* __restrict__ logprob,
-    float* __restrict__ entropy, float* __restrict__ lse_out, int32_t* __restrict__ top_ids,
-    float* __restrict__ top_logprobs, int* __restrict__ status) {
+    const uint64_t* __restrict__ cand_keys, float* __restrict__ logprob, float* __restrict__ entropy,
+    float* __restrict__ lse_out, int32_t* __restrict__ top_ids, float* __restrict__ top_logprobs,
+    int* __restrict__ status) {
   griddep_begin();
+  constexpr int kKept = 96;
+  __shared__ uint64_t kept[8][kKept];  // each warp's
   const int row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (row >= n) return;  // whole warps
@@ -1675,49 +1710,60 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(
     }
   }
   if (k == 0) return;
-  const int total = nsplit * kTopkMax;
-  float cv[kPer];
-  int ci[kPer];
+  const uint64_t* cand = cand_keys + static_cast<int64_t>(row) * nsplit * k;
+  const int total = nsplit * k;
+  uint64_t key[kPer], best = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) key[q] = lane + 32 * q < total ? cand[lane + 32 * q] : 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q)
+    if (key[q] > best) best = key[q];
+  const auto put = [&](int rank, uint64_t won) {
+    const float z = topk_unkey(static_cast<unsigned>(won >> 32));
+    top_ids[static_cast<int64_t>(row) * k + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(won));
+    top_logprobs[static_cast<int64_t>(row) * k + rank] = (fmaf(z, zscale, -m) - log2l) * kLn2;
+  };
+  // The k-th largest of the lanes' maxima is a bound that k candidates reach and few pass.
+  int rank = 0;
+#pragma unroll 8
+  for (int o = 0; o < 32; ++o) rank += __shfl_sync(0xffffffffu, best, o) > best;
+  const unsigned at_k = __ballot_sync(0xffffffffu, best != 0 && rank == k - 1);
+  const uint64_t bound = at_k ? __shfl_sync(0xffffffffu, best, __ffs(at_k) - 1) : 1;
+  int count = 0;
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
-    const int c = lane + 32 * q;
-    const bool ok = c < total;
-    const int64_t at = (static_cast<int64_t>(c / kTopkMax) * n + row) * kTopkMax + c % kTopkMax;
-    cv[q] = ok ? cand_val[at] : -INFINITY;
-    ci[q] = ok ? cand_idx[at] : -1;
+    const bool in = key[q] >= bound;
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    const int slot = count + __popc(who & ((1u << lane) - 1));
+    if (in && slot < kKept) kept[threadIdx.x >> 5][slot] = key[q];
+    count += __popc(who);
   }
-  for (int r = 0; r < k; ++r) {
-    float bv = -INFINITY;
-    int bi = -1, bq = -1;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q)
-      if (topk_better(cv[q], ci[q], bv, bi)) {
-        bv = cv[q];
-        bi = ci[q];
-        bq = q;
-      }
-    float wv = bv;
-    int wi = bi;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, wv, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, wi, o);
-      if (topk_better(ov, oi, wv, wi)) {
-        wv = ov;
-        wi = oi;
-      }
+  __syncwarp();
+  if (count <= kKept) {  // ranked by counting
+    for (int i = lane; i < count; i += 32) {
+      const uint64_t won = kept[threadIdx.x >> 5][i];
+      int place = 0;
+      for (int q = 0; q < count; ++q) place += kept[threadIdx.x >> 5][q] > won;
+      if (place < k) put(place, won);
     }
-    if (bq >= 0 && wi >= 0 && bi == wi) {  // ids are unique within a row: one lane holds the winner
-#pragma unroll
-      for (int q = 0; q < kPer; ++q)
-        if (q == bq) {
-          cv[q] = -INFINITY;
-          ci[q] = -1;
-        }
+    for (int i = count + lane; i < k; i += 32) {  // fewer than k ids
+      top_ids[static_cast<int64_t>(row) * k + i] = -1;
+      top_logprobs[static_cast<int64_t>(row) * k + i] = -INFINITY;
     }
-    if (lane == 0) {
-      top_ids[static_cast<int64_t>(row) * k + r] = wi;
-      top_logprobs[static_cast<int64_t>(row) * k + r] = (fmaf(wv, zscale, -m) - log2l) * kLn2;
+    return;
+  }
+  for (int r = 0; r < k; ++r) {  // k rounds of a maximum over the warp (more than k ids: each finds one)
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
+    const uint64_t win = (static_cast<uint64_t>(hi) << 32) | lo;
+    if (win == best) {  // its holder (candidates are distinct)
+      best = 0;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        if (key[q] == win) key[q] = 0;
+        if (key[q] > best) best = key[q];
+      }
+      put(r, win);
     }
   }
 }
@@ -2061,13 +2107,16 @@ cudaError_t launch_topk_finalize(int n, int nsub, int k, const float* part_m, co
 }
 
 cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv, float zscale, const float* part_m,
-                                  const float* part_l, const float* part_s, const float* tgt, const float* cand_val,
-                                  const int32_t* cand_idx, float* logprob, float* entropy, float* lse,
+                                  const float* part_l, const float* part_s, const float* tgt,
+                                  const uint64_t* cand_keys, float* logprob, float* entropy, float* lse,
                                   int32_t* top_ids, float* top_logprobs, int* status, cudaStream_t stream) {
-  auto* kernel = nsplit <= 16 ? score_finalize_kernel<16 * kTopkMax / 32>
-                              : score_finalize_kernel<kScoreSplitMax * kTopkMax / 32>;
+  const int per = (nsplit * k + 31) / 32;  // candidates of a lane
+  auto* kernel = per <= 4    ? score_finalize_kernel<4>
+                 : per <= 8  ? score_finalize_kernel<8>
+                 : per <= 20 ? score_finalize_kernel<20>
+                             : score_finalize_kernel<kScoreSplitMax * kTopkMax / 32>;
   return launch_k(kernel, dim3((n + 7) / 8), dim3(256), 0, stream, n, v, nsplit, k, lv, zscale, part_m, part_l, part_s,
-                  tgt, cand_val, cand_idx, logprob, entropy, lse, top_ids, top_logprobs, status);
+                  tgt, cand_keys, logprob, entropy, lse, top_ids, top_logprobs, status);
 }
 
 cudaError_t launch_scale_bf16(void* x, int64_t count, const float* g, cudaStream_t stream) {
