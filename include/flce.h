@@ -410,7 +410,7 @@ flce_status_t flce_layernorm_forward(const flce_norm_t* q, const void* x, const 
                                      void* y, float* mean, float* rstd, flce_stream_t stream);
 
 /* Workspace of flce_layernorm_backward (0 if q is invalid): fp32 partial sums of
- * dweight and dbias, one row of 2h for each slice of rows.  256-byte aligned. */
+ * dweight and dbias, a row for each thread block.  256-byte aligned. */
 size_t flce_layernorm_workspace_bytes(const flce_norm_t* q);
 flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, const void* x, const void* weight,
                                       const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,

@@ -1639,7 +1639,7 @@ flce_status_t flce_layernorm_forward(const flce_norm_t* q, const void* x, const 
 size_t flce_layernorm_workspace_bytes(const flce_norm_t* q) {
   NormParams np;
   if (check_norm(q, &np) != FLCE_OK) return 0;
-  return align_up(static_cast<size_t>(norm_slices(np.n)) * 2 * static_cast<size_t>(np.h) * sizeof(float));
+  return align_up(norm_partial_floats(np.n, np.h) * sizeof(float));
 }
 
 flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, const void* x, const void* weight,

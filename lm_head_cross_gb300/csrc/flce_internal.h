@@ -300,7 +300,7 @@ struct NormParams {
   float eps;
   bool x_f32, w_f32;  // else bf16
 };
-int norm_slices(int64_t n);  // rows of partial sums the backward pass keeps in its workspace
+size_t norm_partial_floats(int64_t n, int64_t h);  // of the backward pass's workspace
 cudaError_t launch_norm_forward(const NormParams& q, const void* x, const void* weight, const void* bias, void* y,
                                 float* mean, float* rstd, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void* x, const void* weight,

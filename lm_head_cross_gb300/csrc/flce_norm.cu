@@ -11,8 +11,7 @@ namespace flce {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormSms = 152;                // SMs of the GPU this is written for
-constexpr int kNormSlices = 3 * kNormSms;    // most blocks of the one-pass backward
+constexpr int kNormSms = 152;  // SMs of the GPU this is written for
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -287,31 +286,37 @@ __global__ void __launch_bounds__(kNormThreads) norm_dw_partial_kernel(int64_t n
   out[h + j] = b;
 }
 
-// dweight, dbias: column sums of `slices` rows of partial sums.  32 columns a block, the rows
-// dealt over its 32 warps (about ten loads each, all in flight) and joined in warp order.
+// dweight, dbias: sums of `slices` rows of 2 `half` partial sums each.  32 sums a block, the
+// rows dealt over its 32 warps (about ten loads each, all in flight) and joined in warp
+// order.  Sum p of a half belongs to column (p / (n lanes)) n lanes + (p % lanes) n + (p /
+// lanes) % n: value p / lanes of lane p % lanes, n columns an access.
 constexpr int kFinalWarps = 32;
 template <typename W>
-__global__ void __launch_bounds__(32 * kFinalWarps) norm_dw_final_kernel(int h, int slices,
+__global__ void __launch_bounds__(32 * kFinalWarps) norm_dw_final_kernel(int h, int slices, int half, int lanes, int n,
                                                                          const float* __restrict__ part,
                                                                          W* __restrict__ dweight,
                                                                          W* __restrict__ dbias) {
   griddep_begin();
   __shared__ float red[kFinalWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t j = blockIdx.x * int64_t{32} + lane;  // column of [dweight | dbias]
+  const int64_t j = blockIdx.x * int64_t{32} + lane;  // of [dweight | dbias]
+  const bool in = j < 2 * static_cast<int64_t>(half);
   float a = 0.f;
-  if (j < 2 * static_cast<int64_t>(h)) {
+  if (in) {
 #pragma unroll 10
-    for (int s = warp; s < slices; s += kFinalWarps) a += part[static_cast<int64_t>(s) * 2 * h + j];
+    for (int s = warp; s < slices; s += kFinalWarps) a += part[static_cast<int64_t>(s) * 2 * half + j];
   }
   red[warp][lane] = a;
   __syncthreads();
-  if (warp != 0 || j >= 2 * static_cast<int64_t>(h)) return;
+  if (warp != 0 || !in) return;
   float t = 0.f;
 #pragma unroll
   for (int w = 0; w < kFinalWarps; ++w) t += red[w][lane];
-  if (j < h) dweight[j] = from_f32<W>(t);
-  else if (dbias) dbias[j - h] = from_f32<W>(t);
+  const int p = static_cast<int>(j < half ? j : j - half);
+  const int column = lanes == 1 ? p : p / (n * lanes) * n * lanes + p % lanes * n + p / lanes % n;
+  if (column >= h) return;
+  if (j < half) dweight[column] = from_f32<W>(t);
+  else if (dbias) dbias[column] = from_f32<W>(t);
 }
 
 // ----------------------------------------------------------------------------- backward in one pass
@@ -359,14 +364,16 @@ struct BwdShape {
   static constexpr int kWarps = N == 1 && GW <= 8 ? 8 : 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kGroups = kWarps / GW;
-  static constexpr int kPairs = N * VPL / 2;  // column pairs of a lane
+  static constexpr int kColumns = 32 * GW * VPL * N;  // the widest row
+  static constexpr int kPairs = N * VPL / 2;          // column pairs of a lane
   static constexpr int kBlocks = N == 1 ? (GW <= 8 ? 3 : 1) : kPairs <= 4 ? 2 : 1;  // on one SM
-  static constexpr int kStages = N == 1 ? 4 : VPL == 1 ? 5 : VPL == 2 ? 3 : 2;  // rows in flight for each group
+  static constexpr int kStages = N == 1 ? 4 : VPL == 1 ? 5 : VPL == 2 && N == 8 ? 3 : 2;  // rows in flight for each group
   static constexpr int kStageBytes = kThreads * VPL * 2 * kAccess;  // x and dy
   static constexpr int kRingBytes = kRing ? kStages * kStageBytes : 0;
   static constexpr int kStatsBytes = kStages * kWarps * 8;  // mean and rstd of the rows in flight, for each warp
-  static constexpr int kWeightBytes = N == 1 ? 0 : 32 * GW * VPL * N * 4;  // fp32, in the lanes' order
-  static constexpr int kSmemBytes = kRingBytes + kStatsBytes + kWeightBytes;
+  static constexpr int kWeightBytes = N == 1 ? 0 : 4 * kColumns;  // fp32, in the lanes' order
+  static constexpr int kJoinBytes = kGroups > 1 ? 8 * kColumns : 0;
+  static constexpr int kSmemBytes = std::max(kRingBytes + kStatsBytes + kWeightBytes, kJoinBytes);
 };
 
 // dx, and the rows' share of dweight and dbias, in one pass over x and dy.  A lane owns the
@@ -559,8 +566,10 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
     }
   }
 
-  // one row of partial sums a block; its groups join in order
-  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * h;
+  // one row of partial sums a block, in the lanes' order (value i of lane l at i * 32 GW + l);
+  // its groups join in order
+  constexpr int kHalf = S::kColumns;
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * kHalf;
   float* to = out;
   if constexpr (S::kGroups > 1) {
     cp_async_wait<0>();
@@ -572,15 +581,14 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
     if (g != group) continue;
 #pragma unroll
     for (int i = 0; i < VPL * N; ++i) {
-      const int j = column(i / N) + i % N;
-      if (j >= h) continue;
+      const int j = i * 32 * GW + lane;
       to[j] = (g ? to[j] : 0.f) + reinterpret_cast<const float*>(aw)[i];
-      to[h + j] = (g ? to[h + j] : 0.f) + reinterpret_cast<const float*>(ab)[i];
+      to[kHalf + j] = (g ? to[kHalf + j] : 0.f) + reinterpret_cast<const float*>(ab)[i];
     }
   }
   if constexpr (S::kGroups > 1) {
     __syncthreads();
-    for (int j = threadIdx.x; j < 2 * h; j += S::kThreads) out[j] = to[j];
+    for (int j = threadIdx.x; j < 2 * kHalf; j += S::kThreads) out[j] = to[j];
   }
 }
 
@@ -652,73 +660,79 @@ struct NormBackwardArgs {
   cudaStream_t stream;
 };
 
-// The one-pass backward; returns the rows of partial sums it leaves through *slices.
+// The partial sums that a backward pass leaves (see norm_dw_final_kernel).
+struct PartialLayout {
+  int slices, half;
+  int lanes, n;
+};
+
 template <typename T, int N, int GW, int VPL>
-cudaError_t norm_backward_rows(const NormBackwardArgs& a, int* slices) {
+cudaError_t norm_backward_rows(const NormBackwardArgs& a, PartialLayout* left) {
   using S = BwdShape<T, N, GW, VPL>;
-  // the ring (N > 1), or the joining of the groups' column sums
-  const size_t join = S::kGroups > 1 ? 2 * sizeof(float) * static_cast<size_t>(a.q.h) : 0;
-  const size_t smem = std::max<size_t>(S::kSmemBytes, join);
+  static_assert(S::kSmemBytes <= 227 * 1024 / S::kBlocks - 1536, "shared memory budget");
   auto* kernel = norm_bwd_rows_kernel<T, N, GW, VPL>;
-  // asked for at its largest: the join needs 2 h of a row that the group's lanes hold
-  constexpr size_t kMost = std::max<size_t>(S::kSmemBytes, S::kGroups > 1 ? 8 * 32 * GW * VPL * N : 0);
-  static_assert(kMost <= 227 * 1024, "shared memory budget");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = kMost > 40 * 1024 ? allow_smem(kernel, kMost, done) : cudaSuccess;
+  cudaError_t e = S::kSmemBytes > 40 * 1024 ? allow_smem(kernel, S::kSmemBytes, done) : cudaSuccess;
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.q.n + S::kGroups - 1) / S::kGroups;
-  *slices = static_cast<int>(std::min<int64_t>(blocks, S::kBlocks * kNormSms));
-  return launch_k(kernel, dim3(*slices), dim3(S::kThreads), smem, a.stream, static_cast<int>(a.q.n), a.q.h, a.q.x_pitch,
-                  static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.weight, a.q.w_f32, a.mean, a.rstd,
-                  static_cast<T*>(a.dx), a.part);
+  *left = PartialLayout{static_cast<int>(std::min<int64_t>(blocks, S::kBlocks * kNormSms)), S::kColumns, 32 * GW, N};
+  return launch_k(kernel, dim3(left->slices), dim3(S::kThreads), S::kSmemBytes, a.stream, static_cast<int>(a.q.n),
+                  a.q.h, a.q.x_pitch, static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.weight, a.q.w_f32,
+                  a.mean, a.rstd, static_cast<T*>(a.dx), a.part);
 }
 
 // Two passes for rows past every one-pass shape: dx row by row, then the column sums over
 // slices of rows.
 template <typename T>
-cudaError_t norm_backward_wide(const NormBackwardArgs& a, int* slices) {
+cudaError_t norm_backward_wide(const NormBackwardArgs& a, PartialLayout* left) {
   const int grid = static_cast<int>(std::min<int64_t>(a.q.n, 1 << 20));
   cudaError_t e = launch_k(norm_dx_kernel<T>, dim3(grid), dim3(kNormThreads), 0, a.stream, a.q.n, a.q.h, a.q.x_pitch,
                            static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.weight, a.q.w_f32, a.mean,
                            a.rstd, static_cast<T*>(a.dx));
   if (e != cudaSuccess) return e;
-  *slices = std::min(norm_slices(a.q.n), 128);
-  const int64_t rows = (a.q.n + *slices - 1) / *slices;
+  const int slices = static_cast<int>(std::min<int64_t>(a.q.n, 128));
+  *left = PartialLayout{slices, a.q.h, 1, 1};
+  const int64_t rows = (a.q.n + slices - 1) / slices;
   const int cols = (a.q.h + kNormThreads - 1) / kNormThreads;
-  return launch_k(norm_dw_partial_kernel<T>, dim3(cols, *slices), dim3(kNormThreads), 0, a.stream, a.q.n, a.q.h,
+  return launch_k(norm_dw_partial_kernel<T>, dim3(cols, slices), dim3(kNormThreads), 0, a.stream, a.q.n, a.q.h,
                   a.q.x_pitch, rows, static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.mean, a.rstd, a.part);
 }
 
 template <typename T>
-cudaError_t norm_backward(const NormBackwardArgs& a, int* slices) {
+cudaError_t norm_backward(const NormBackwardArgs& a, PartialLayout* left) {
   constexpr int kVec = 16 / sizeof(T);
   const size_t row = sizeof(T) * static_cast<size_t>(a.q.x_pitch);
   const auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   const int h = a.q.h;
-  if (a.q.n > (1 << 30)) return norm_backward_wide<T>(a, slices);  // 32-bit row numbers in one pass
+  if (a.q.n > (1 << 30)) return norm_backward_wide<T>(a, left);  // 32-bit row numbers in one pass
   if (h % kVec == 0 && row % 16 == 0 && at16(a.x) && at16(a.dy) && at16(a.dx) && at16(a.weight)) {
     const int acc = h / kVec;
-    if (acc <= 32) return norm_backward_rows<T, kVec, 1, 1>(a, slices);
-    if (acc <= 64) return norm_backward_rows<T, kVec, 2, 1>(a, slices);
-    if (acc <= 128) return norm_backward_rows<T, kVec, 4, 1>(a, slices);
-    if (acc <= 256) return norm_backward_rows<T, kVec, 8, 1>(a, slices);
-    if (acc <= 512) return norm_backward_rows<T, kVec, 16, 1>(a, slices);
-    if (acc <= 1024) return norm_backward_rows<T, kVec, 16, 2>(a, slices);
-    if (acc <= 2048) return norm_backward_rows<T, kVec, 16, 4>(a, slices);
+    if (acc <= 32) return norm_backward_rows<T, kVec, 1, 1>(a, left);
+    if (acc <= 64) return norm_backward_rows<T, kVec, 2, 1>(a, left);
+    if (acc <= 128) return norm_backward_rows<T, kVec, 4, 1>(a, left);
+    if (acc <= 256) return norm_backward_rows<T, kVec, 8, 1>(a, left);
+    if (acc <= 512) return norm_backward_rows<T, kVec, 16, 1>(a, left);
+    if (acc <= 1024) return norm_backward_rows<T, kVec, 16, 2>(a, left);
+    if (acc <= 2048) return norm_backward_rows<T, kVec, 16, 4>(a, left);
   } else {
-    if (h <= 128) return norm_backward_rows<T, 1, 1, 4>(a, slices);
-    if (h <= 512) return norm_backward_rows<T, 1, 4, 4>(a, slices);
-    if (h <= 1024) return norm_backward_rows<T, 1, 8, 4>(a, slices);
-    if (h <= 1536) return norm_backward_rows<T, 1, 8, 6>(a, slices);
-    if (h <= 2048) return norm_backward_rows<T, 1, 8, 8>(a, slices);
-    if (h <= 4096) return norm_backward_rows<T, 1, 16, 8>(a, slices);
+    if (h <= 128) return norm_backward_rows<T, 1, 1, 4>(a, left);
+    if (h <= 512) return norm_backward_rows<T, 1, 4, 4>(a, left);
+    if (h <= 1024) return norm_backward_rows<T, 1, 8, 4>(a, left);
+    if (h <= 1536) return norm_backward_rows<T, 1, 8, 6>(a, left);
+    if (h <= 2048) return norm_backward_rows<T, 1, 8, 8>(a, left);
+    if (h <= 4096) return norm_backward_rows<T, 1, 16, 8>(a, left);
   }
-  return norm_backward_wide<T>(a, slices);
+  return norm_backward_wide<T>(a, left);
 }
 
 }  // namespace
 
-int norm_slices(int64_t n) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNormSlices, n))); }
+// Every shape: at most 512 or twice h columns, and blocks for three on an SM only for single
+// elements of narrow rows.
+size_t norm_partial_floats(int64_t n, int64_t h) {
+  const int64_t slices = std::min<int64_t>(std::max<int64_t>(n, 1), (h <= 2048 ? 3 : 2) * kNormSms);
+  return static_cast<size_t>(slices) * 2 * static_cast<size_t>(std::max<int64_t>(512, 2 * h));
+}
 
 cudaError_t launch_norm_forward(const NormParams& q, const void* x, const void* weight, const void* bias, void* y,
                                 float* mean, float* rstd, cudaStream_t stream) {
@@ -730,15 +744,16 @@ cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void
                                  const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
                                  float* part, cudaStream_t stream) {
   const NormBackwardArgs a{q, dy, x, weight, mean, rstd, dx, part, stream};
-  int slices = 0;
-  cudaError_t e = q.x_f32 ? norm_backward<float>(a, &slices) : norm_backward<__nv_bfloat16>(a, &slices);
+  PartialLayout left{};
+  cudaError_t e = q.x_f32 ? norm_backward<float>(a, &left) : norm_backward<__nv_bfloat16>(a, &left);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>((2 * static_cast<int64_t>(q.h) + 31) / 32));
+  const dim3 grid(static_cast<unsigned>((2 * static_cast<int64_t>(left.half) + 31) / 32));
   if (q.w_f32)
-    return launch_k(norm_dw_final_kernel<float>, grid, dim3(32 * kFinalWarps), 0, stream, q.h, slices, part,
-                    static_cast<float*>(dweight), static_cast<float*>(dbias));
-  return launch_k(norm_dw_final_kernel<__nv_bfloat16>, grid, dim3(32 * kFinalWarps), 0, stream, q.h, slices, part,
-                  static_cast<__nv_bfloat16*>(dweight), static_cast<__nv_bfloat16*>(dbias));
+    return launch_k(norm_dw_final_kernel<float>, grid, dim3(32 * kFinalWarps), 0, stream, q.h, left.slices, left.half,
+                    left.lanes, left.n, part, static_cast<float*>(dweight), static_cast<float*>(dbias));
+  return launch_k(norm_dw_final_kernel<__nv_bfloat16>, grid, dim3(32 * kFinalWarps), 0, stream, q.h, left.slices,
+                  left.half, left.lanes, left.n, part, static_cast<__nv_bfloat16*>(dweight),
+                  static_cast<__nv_bfloat16*>(dbias));
 }
 
 }  // namespace flce
