@@ -72,6 +72,12 @@ __device__ __forceinline__ float element(const Pack<T, N>& p, int e) {
   return to_f32(p.v[e]);
 }
 
+// Elements 2e and 2e + 1.
+template <typename T, int N>
+__device__ __forceinline__ float2 element2(const Pack<T, N>& p, int e) {
+  return make_float2(element(p, 2 * e), element(p, 2 * e + 1));
+}
+
 template <typename T, int N>
 __device__ __forceinline__ void pack_f32(Pack<T, N>& p, const float (&o)[N]) {
   if (sizeof(T) == 2 && N > 1) {
@@ -82,6 +88,26 @@ __device__ __forceinline__ void pack_f32(Pack<T, N>& p, const float (&o)[N]) {
     for (int e = 0; e < N; ++e) p.v[e] = from_f32<T>(o[e]);
   }
 }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t as_u64(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
+__device__ __forceinline__ float2 as_f2(uint64_t v) { return *reinterpret_cast<float2*>(&v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // N elements of a vector of either type, as fp32 (f32 is the same for the whole grid).
 template <int N>
@@ -149,26 +175,30 @@ __global__ void __launch_bounds__(kFwdThreads<WARPS, VPL>) norm_fwd_rows_kernel(
     const int j = (lane + k * kLanes) * N;
     if (j < h) v[k] = *reinterpret_cast<const Pack<T, N>*>(xr + j);
   }
-  float s = 0.f;
+  float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < VPL; ++k)
     if ((lane + k * kLanes) * N < h) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) s += element(v[k], e);
+      for (int e = 0; e < N / 2; ++e) s2 = add2(s2, element2(v[k], e));
+      if (N == 1) s2.x += element(v[k], 0);
     }
+  const float s = s2.x + s2.y;
 #pragma unroll
   for (int k = 0; k < VPL; ++k) keep_packed(v[k]);
   const float mu = row_sum<WARPS>(s, red[0]) / h;
-  float q = 0.f;
+  float2 q2 = make_float2(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < VPL; ++k)
     if ((lane + k * kLanes) * N < h) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float d = element(v[k], e) - mu;
-        q = fmaf(d, d, q);
+      for (int e = 0; e < N / 2; ++e) {
+        const float2 d = add2(element2(v[k], e), both(-mu));
+        q2 = fma2(d, d, q2);
       }
+      if (N == 1) q2.x = fmaf(element(v[k], 0) - mu, element(v[k], 0) - mu, q2.x);
     }
+  const float q = q2.x + q2.y;
 #pragma unroll
   for (int k = 0; k < VPL; ++k) keep_packed(v[k]);
   const float rs = 1.f / sqrtf(row_sum<WARPS>(q, red[1]) / h + eps);
@@ -179,11 +209,19 @@ __global__ void __launch_bounds__(kFwdThreads<WARPS, VPL>) norm_fwd_rows_kernel(
     if (j >= h) continue;
     float w[N], b[N];
     load_w<N>(weight, w_f32, j, w);
-    if (bias) load_w<N>(bias, w_f32, j, b);
+    if (bias) {
+      load_w<N>(bias, w_f32, j, b);
+    } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float o = (element(v[k], e) - mu) * rs;
-      w[e] = bias ? fmaf(o, w[e], b[e]) : o * w[e];
+      for (int e = 0; e < N; ++e) b[e] = 0.f;
+    }
+    if (N == 1) w[0] = fmaf((element(v[k], 0) - mu) * rs, w[0], b[0]);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      const float2 o = fma2(mul2(add2(element2(v[k], e), both(-mu)), both(rs)), make_float2(w[2 * e], w[2 * e + 1]),
+                            make_float2(b[2 * e], b[2 * e + 1]));
+      w[2 * e] = o.x;
+      w[2 * e + 1] = o.y;
     }
     pack_f32(v[k], w);
     *reinterpret_cast<Pack<T, N>*>(yr + j) = v[k];
@@ -334,26 +372,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t as_u64(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
-__device__ __forceinline__ float2 as_f2(uint64_t v) { return *reinterpret_cast<float2*>(&v); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
-  return as_f2(d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
-  return as_f2(d);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
-  return as_f2(d);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Shape of the one-pass backward: GW warps share a row, VPL accesses of N elements a lane,
 // kGroups rows in a block at a time.
