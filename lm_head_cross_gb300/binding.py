@@ -850,6 +850,14 @@ def logprobs_forward(x, w, tokens=None, top=0, temperature=1.0, ignore_index=-10
     return TokenLogprobs(lp, entropy, lse, ids, tlp), ws
 
 
+@functools.lru_cache(maxsize=256)
+def _bounded_bytes(n, h, v) -> int:
+    nbytes = workspace_bytes(n, h, v, reduction="none")
+    if nbytes == 0:
+        raise FlceError(1, "workspace_bytes")
+    return nbytes
+
+
 def logprobs_backward(x, w, tokens, lse, entropy, grad_logprob=None, grad_entropy=None, temperature=1.0,
                       ignore_index=-100, shift=0, seq_len=0, ws=None, stream=None, check=False):
     """Gradients of sum(grad_logprob * logprob + grad_entropy * entropy) given logprobs_forward's
@@ -871,7 +879,7 @@ def logprobs_backward(x, w, tokens, lse, entropy, grad_logprob=None, grad_entrop
     p = _problem(n, h, w.shape[0], ignore_index, "none", shift, seq_len)
     with _allocating(stream):
         if ws is None:
-            ws = _alloc_ws(n, h, w.shape[0], ignore_index, "none", x.device)
+            ws = torch.empty(_bounded_bytes(n, h, w.shape[0]), dtype=torch.uint8, device=x.device)
         dX, dW = torch.empty_like(x), torch.empty_like(w)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     _call("flce_token_logprobs_backward", lib().flce_token_logprobs_backward(

@@ -19,6 +19,7 @@ namespace flce {
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int kChunkCounters = 48;  // header words from byte 64 on
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int32_t kMaxShardParts = 1 << 16;  // most vocabulary shards flce_shard_combine takes
 #ifdef FLCE_DEBUG_CHECKS
@@ -34,6 +35,7 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 struct Layout {
   size_t status, n_valid, scale;  // header words
   size_t counter;                 // tile counter of the dynamically scheduled launches
+  size_t chunk_counters;          // those of the bounded backward's first kChunkCounters chunks
   size_t fix_count;               // fused path: rows listed for the full fix-up in the current chunk
   size_t ticket;                  // fused path: blocks of the label pass done (its last block resets it)
   size_t fcount;                  // unit counters of the forward launches: one header word, or one per row
@@ -96,6 +98,7 @@ Layout make_layout(const flce_problem_t& p, bool fused, bool shard = false) {
   L.fix_count = off + 20;
   L.ticket = off + 24;
   L.fcount = off + 28;
+  L.chunk_counters = off + 64;
   off += kAlign;
   const size_t nblk_alloc = std::max<size_t>(L.nblk, (n + kRefRowsPerBlock - 1) / kRefRowsPerBlock);
   L.blk_loss = off;
@@ -295,6 +298,7 @@ struct Ctx {
   int* n_valid() const { return reinterpret_cast<int*>(ws + L.n_valid); }
   float* scale() const { return reinterpret_cast<float*>(ws + L.scale); }
   int* counter() const { return reinterpret_cast<int*>(ws + L.counter); }
+  int* chunk_counter(int i) const { return reinterpret_cast<int*>(ws + L.chunk_counters) + i; }
   double* blk_loss() const { return reinterpret_cast<double*>(ws + L.blk_loss); }
   int* blk_valid() const { return reinterpret_cast<int*>(ws + L.blk_valid); }
   float* part_m() const { return reinterpret_cast<float*>(ws + L.part_m); }
@@ -556,7 +560,11 @@ flce_status_t run_backward(const Ctx& c, const void* X, const void* W, const int
   if (!make_map(&bm.b, W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.v, p.h * 2, 64, kBK)) return FLCE_ERR_CUDA;
   if (!make_map(&bm.b2, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.n, p.h * 2, 64, kBK)) return FLCE_ERR_CUDA;
   if (!make_map(&bm.out2, dW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.v, p.h * 2, 64, 32)) return FLCE_ERR_CUDA;
-  bm.out = bm.out2;  // unused by these tiles (a valid map for the prologue's prefetch)
+  // a vocabulary of one chunk: dX needs no accumulator and leaves the tiles as bf16
+  const bool one_chunk = dX && p.v <= chunk;
+  bm.out = bm.out2;  // with an accumulator unused (a valid map for the prologue's prefetch)
+  if (one_chunk && !make_map(&bm.out, dX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.n, p.h * 2, 64, 32))
+    return FLCE_ERR_CUDA;
 
   for (int64_t c0 = 0; c0 < p.v; c0 += chunk) {
     const int cw = static_cast<int>(std::min<int64_t>(chunk, p.v - c0));
@@ -588,22 +596,29 @@ flce_status_t run_backward(const Ctx& c, const void* X, const void* W, const int
     tp.dw_m_tiles = (cw + kPairRows - 1) / kPairRows;
     tp.dw_tiles = tp.dw_m_tiles * tp.h_tiles;
     tp.dx_tiles = tp.row_tiles * tp.h_tiles;
-    tp.dx_out = c0 > 0 ? kOutF32Add : kOutF32Store;
+    tp.dx_out = one_chunk ? kOutBF16 : c0 > 0 ? kOutF32Add : kOutF32Store;
     tp.dx_f32 = dx_acc;
     tp.dw_out = kOutBF16;
     tp.dx_k = cw;
     tp.dw_k = tp.n;
     tp.dx_first = 0;
-    tp.tile_counter = c.counter();
-    st = cuda_status(cudaMemsetAsync(c.counter(), 0, sizeof(int), c.stream));
-    if (st != FLCE_OK) return st;
+    // each of the first chunks draws its tiles from a header word of its own, zero since the
+    // call started; later ones reset the shared word
+    const int64_t chunk_no = c0 / chunk;
+    if (chunk_no < kChunkCounters) {
+      tp.tile_counter = c.chunk_counter(static_cast<int>(chunk_no));
+    } else {
+      tp.tile_counter = c.counter();
+      st = cuda_status(cudaMemsetAsync(c.counter(), 0, sizeof(int), c.stream));
+      if (st != FLCE_OK) return st;
+    }
     const long long btiles = static_cast<long long>(tp.dw_tiles) + tp.dx_tiles;
     st = cuda_status(timed(2, 2.0 * gflops, c.stream, [&] {
       return launch_tc(kModeBwd, bm, tp, pair_grid(c.dev.sms, btiles), c.stream);
     }));
     if (st != FLCE_OK) return st;
   }
-  if (!dX) return FLCE_OK;
+  if (!dX || one_chunk) return FLCE_OK;
   return cuda_status(timed(3, 0.0, c.stream, [&] { return launch_convert_bf16(dx_acc, dX, p.n * p.h, c.stream); }));
 }
 
@@ -1414,13 +1429,6 @@ flce_status_t flce_token_logprobs_backward(const flce_problem_t* p, float temper
   Ctx c;
   st = prepare(&c, p, ws, ws_bytes, stream);
   if (st != FLCE_OK) return st;
-  if (tokens) {  // out-of-range tokens are reported as in the forward pass
-    st = cuda_status(timed(3, 0.0, c.stream, [&] {
-      return launch_label_scan_view(static_cast<int>(p->n), static_cast<int>(p->v), c.labels_of(tokens), c.blk_loss(),
-                                    c.blk_valid(), c.status(), c.stream);
-    }));
-    if (st != FLCE_OK) return st;
-  }
   const ScoreGrad sg{1.f / temperature, grad_entropy, entropy};
   return run_backward(c, X, W, tokens, lse, grad_logprob, dX, dW, c.dx_acc(), nullptr, &sg);
 }

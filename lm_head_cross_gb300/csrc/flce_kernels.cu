@@ -820,6 +820,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
       // to bf16 for the two contractions that follow, like every G.
       const int row = t.m0 + r;
       const int y = (row >= p.n) ? p.ignore_index : label_at(p.labels, row, p.shift, p.seq_len, p.ignore_index);
+      if (p.c0 + t.n0 == 0 && y != p.ignore_index && (y < 0 || y >= p.v)) atomicCAS(p.status, 0, kErrLabel);
       const float gl = (y != p.ignore_index && p.grad_rows) ? p.grad_rows[row] * p.inv_temp : 0.f;
       const float ge = (row < p.n && p.grad_ent) ? p.grad_ent[row] * p.inv_temp : 0.f;
       const float a = (row < p.n && p.grad_ent) ? -fmaf(ge, p.entropy[row], gl) : -gl;
