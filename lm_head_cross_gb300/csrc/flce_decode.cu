@@ -12,7 +12,7 @@
 // accumulators, a token a lane.  With n <= 32 X is staged four times, at rows 0, 32, 64
 // and 96 (n <= 64: twice): every warp then finds tokens in the TMEM quarter it can read,
 // and takes a quarter (half) of the tile's columns for them, which shortens what is
-// exposed after the last tile.
+// exposed after the last tile.  With n <= 8 see decode_epilogue_few.
 //
 // A second kernel, one block per token, joins the ranges' partial results.
 #include <algorithm>
@@ -26,17 +26,43 @@ namespace flce {
 
 namespace {
 
-constexpr int kTileV = 256;                       // vocabulary rows of a tile
+constexpr int kTileV = 256;                       // vocabulary rows of a tile, at most
 constexpr int kSub = 16;                          // rows of the smallest box, and the ranges' grain
 constexpr int kAStageBytes = 128 * kBK * 2;       // X rows: 16 KiB
 constexpr int kBStageBytes = kTileV * kBK * 2;    // W rows: 32 KiB
-constexpr int kRingStages = 4;
-constexpr int kCandOff = kRingStages * (kAStageBytes + kBStageBytes);
+constexpr int kMostStages = 4;
 constexpr int kCandBytes = kTopkCand * 32 * 8;    // one warp's candidates
-constexpr int kBarOff = kCandOff + 4 * kCandBytes;
-constexpr int kDecodeSmem = kBarOff + 256 + 1024;  // barriers; 1 KiB to align the ring
-static_assert(kDecodeSmem <= 232448, "shared memory budget");
+constexpr int kDecodeSmem = 232448 - 512;         // what the kernel takes; barriers in its last 512 bytes
+constexpr int kBarOff = kDecodeSmem - 1024 - 512; // (1 KiB aligns the ring)
 constexpr uint32_t kDecodeTmem = 2 * kTileV;
+
+// Shared memory, in order: W stages (32 KiB: a tile's block of K), X, then the warps'
+// candidates or the few tokens' logits.
+//   X streams beside W, 16 KiB a stage, or, for n <= 8 and as far as it fits, stays in shared
+//   memory from the first tile on, 1 KiB (8 rows) for each block of K.  Every SM reads the
+//   same X: streamed, its few lines were asked for by 152 SMs at a time, which held the whole
+//   stream to 5.6 TB/s at H = 4096 (6.3 with X resident).  The MMA's rows 8 to 127 are then
+//   the blocks that follow, and past the last one a margin: products in TMEM lanes nobody
+//   reads.
+constexpr int kFewRows = 8;
+constexpr int kFewPitch = kTileV + 4;                    // floats of a token's logits
+constexpr int kFewBytes = kFewRows * kFewPitch * 4;
+constexpr int kResidentMargin = kAStageBytes - 1024;
+struct SmemPlan {
+  bool few;  // X resident, and the epilogue of few tokens
+  int stages;
+  int x_off, cand_off;
+};
+__host__ __device__ inline SmemPlan smem_plan(int n, int h) {
+  const int x = (h + kBK - 1) / kBK * 1024 + kResidentMargin;
+  const int left = (kBarOff - kFewBytes - x) / kBStageBytes;
+  if (n <= kFewRows && left >= 3) {
+    const int stages = left < 4 ? left : 4;
+    return SmemPlan{true, stages, stages * kBStageBytes, stages * kBStageBytes + x};
+  }
+  return SmemPlan{false, 4, 4 * kBStageBytes, 4 * (kBStageBytes + kAStageBytes)};
+}
+static_assert(4 * (kBStageBytes + kAStageBytes) + 4 * kCandBytes <= kBarOff, "shared memory budget");
 
 __device__ __forceinline__ void tmem_alloc_one(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
@@ -69,24 +95,26 @@ __device__ __forceinline__ Range my_range(const DecodeParams& p) {
   return Range{static_cast<int>(u0 * kSub), static_cast<int>(end < p.v ? end : p.v)};
 }
 
-__device__ void decode_producer(const DecodeMaps& maps, const DecodeParams& p, Range r, uint8_t* ring, uint64_t* full,
-                                uint64_t* empty, volatile int* abort_flag, int* err) {
+__device__ void decode_producer(const DecodeMaps& maps, const DecodeParams& p, const SmemPlan& plan, Range r,
+                                uint8_t* smem, uint64_t* full, uint64_t* empty, volatile int* abort_flag,
+                                int* err) {
   const int kblocks = (p.h + kBK - 1) / kBK;
   const uint32_t a_bytes = static_cast<uint32_t>(p.copies * p.a_rows * kBK * 2);
+  uint8_t* const x = smem + plan.x_off;
   int stage = 0;
   uint32_t phase = 0;
   for (int n0 = r.v0; n0 < r.v1; n0 += kTileV) {
     const int rows = min(kTileV, r.v1 - n0);
     const int loaded = (rows + kSub - 1) / kSub * kSub;  // (past V: zeros)
-    const uint32_t bytes = a_bytes + loaded * kBK * 2;
+    const bool load_x = !plan.few || n0 == r.v0;  // resident: with the first tile
+    const uint32_t bytes = (load_x ? a_bytes : 0) + loaded * kBK * 2;
     for (int kb = 0; kb < kblocks; ++kb) {
       if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag)) {
         *abort_flag = 1;
         *err = kErrTimeout;
         return;
       }
-      uint8_t* sa = ring + stage * (kAStageBytes + kBStageBytes);
-      uint8_t* sb = sa + kAStageBytes;
+      uint8_t* sb = smem + stage * kTileV * kBK * 2;
       mbar_arrive_expect_tx(&full[stage], bytes);
       const int k0 = kb * kBK;  // a multiple of 64 elements: the copies' 16-byte rule
       // the tile's rows as boxes of 256, 128, ... 16, one of each at most
@@ -96,8 +124,12 @@ __device__ void decode_producer(const DecodeMaps& maps, const DecodeParams& p, R
         tma_load_2d(sb + at * kBK * 2, &maps.w[i], &full[stage], k0, n0 + at);
         at += box;
       }
-      for (int c = 0; c < p.copies; ++c) tma_load_2d(sa + c * (128 / p.copies) * kBK * 2, &maps.x, &full[stage], k0, 0);
-      if (++stage == kRingStages) {
+      if (load_x) {
+        uint8_t* sa = x + (plan.few ? kb * 1024 : stage * kAStageBytes);
+        for (int c = 0; c < p.copies; ++c)
+          tma_load_2d(sa + c * (128 / p.copies) * kBK * 2, &maps.x, &full[stage], k0, 0);
+      }
+      if (++stage == plan.stages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -105,43 +137,45 @@ __device__ void decode_producer(const DecodeMaps& maps, const DecodeParams& p, R
   }
 }
 
-__device__ void decode_mma(const DecodeParams& p, Range r, uint8_t* ring, uint64_t* full, uint64_t* empty,
-                           uint64_t* tfull, uint64_t* tempty, uint32_t tmem_base, volatile int* abort_flag, int* err) {
+__device__ void decode_mma(const DecodeParams& p, const SmemPlan& plan, Range r, uint8_t* smem, uint64_t* full,
+                           uint64_t* empty, uint64_t* tfull, uint64_t* tempty, uint32_t tmem_base,
+                           volatile int* abort_flag, int* err) {
   const int kblocks = (p.h + kBK - 1) / kBK;
+  const uint32_t x = smem_u32(smem + plan.x_off);
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
-  for (int n0 = r.v0; n0 < r.v1; n0 += kTileV) {
+  bool ok = true;
+  for (int n0 = r.v0; ok && n0 < r.v1; n0 += kTileV) {
     const int cols = (min(kTileV, r.v1 - n0) + 15) / 16 * 16;
     const uint32_t idesc = instr_desc_bf16(128, cols, false, false);
-    if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, p.timeout_ns, abort_flag)) {
-      *abort_flag = 1;
-      *err = kErrTimeout;
-      return;
-    }
+    ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, p.timeout_ns, abort_flag);
+    if (!ok) break;
     tc_fence_after_sync();
     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTileV);
     for (int kb = 0; kb < kblocks; ++kb) {
-      if (!mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag)) {
-        *abort_flag = 1;
-        *err = kErrTimeout;
-        return;
-      }
+      ok = mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag);
+      if (!ok) break;
       tc_fence_after_sync();
-      const uint32_t sa = smem_u32(ring + stage * (kAStageBytes + kBStageBytes));
-      const uint32_t sb = sa + kAStageBytes;
+      const uint32_t sa = plan.few ? x + kb * 1024 : x + stage * kAStageBytes;
+      const uint32_t sb = smem_u32(smem + stage * kTileV * kBK * 2);
 #pragma unroll
       for (int k = 0; k < kBK / 16; ++k)
         umma_bf16_one(d_tmem, smem_desc_sw128(sa + k * 32, 16, 1024), smem_desc_sw128(sb + k * 32, 16, 1024), idesc,
                       (kb | k) != 0 ? 1u : 0u);
       umma_commit_one(&empty[stage]);
-      if (++stage == kRingStages) {
+      if (++stage == plan.stages) {
         stage = 0;
         phase ^= 1u;
       }
     }
+    if (!ok) break;
     umma_commit_one(&tfull[acc]);
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
+  }
+  if (!ok) {
+    *abort_flag = 1;
+    *err = kErrTimeout;
   }
 }
 
@@ -154,13 +188,13 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
   const int copies = p.copies;
   const int share = quarter / (4 / copies);                  // which of the copies it reads
   const int row = quarter % (4 / copies) * 32 + lane;        // token
-  const int c0 = share * (8 / copies);                       // 32-column chunks of a tile this warp takes
-  const int c1 = c0 + 8 / copies;
+  const int chunks = kTileV / 32 / copies;                   // 32-column chunks of a tile this warp takes
+  const int c0 = share * chunks, c1 = c0 + chunks;
   const bool idle = row - lane >= p.n;                       // a warp without a token only frees accumulators
   const int y = (row < p.n) ? label_at(p.tokens, row, p.shift, p.seq_len, p.ignore_index) : p.ignore_index;
 
-  float* val = reinterpret_cast<float*>(cand + (warp - 2) * kCandBytes);
-  int* idx = reinterpret_cast<int*>(cand + (warp - 2) * kCandBytes + kTopkCand * 32 * sizeof(float));
+  float* val = reinterpret_cast<float*>(cand + quarter * kCandBytes);
+  int* idx = reinterpret_cast<int*>(val + kTopkCand * 32);
   int count = 0;
   float thr = -INFINITY;        // the range's own k-th best, once it is known: ids grow, so an equal later value is out
   float floor_thr = -INFINITY;  // nothing below it is among the row's best
@@ -177,10 +211,12 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
     }
     tc_fence_after_sync();
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kTileV);
-    if (TOP && !idle && n0 == r.v0)
-      floor_thr = copies == 4   ? first_floor<1>(tbase + c0 * 32, cols - c0 * 32, p.k)
-                  : copies == 2 ? first_floor<2>(tbase + c0 * 32, cols - c0 * 32, p.k)
-                                : first_floor<4>(tbase, cols, p.k);
+    if (TOP && !idle && n0 == r.v0) {
+      const int valid = min(cols - c0 * 32, chunks * 32);
+      floor_thr = chunks <= 2   ? first_floor<1>(tbase + c0 * 32, valid, p.k)
+                  : chunks == 4 ? first_floor<2>(tbase + c0 * 32, valid, p.k)
+                                : first_floor<4>(tbase, valid, p.k);
+    }
 #pragma unroll 1
     for (int c = c0; c < c1 && !idle; ++c) {
       if (c * 32 >= cols) break;  // the same for the whole warp
@@ -278,19 +314,171 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
   }
 }
 
+// The epilogue of at most 8 tokens, which are 8 lanes of TMEM: the one warp that can read
+// them copies the tile's logits to shared memory, and each token is a whole warp's, eight
+// neighbouring columns a lane.  Its best k are rounds of a maximum over the warp: as many as
+// k in the first tile, then only where a value beats the k-th so far.
+template <bool TOP>
+__device__ void decode_epilogue_few(const DecodeParams& p, Range r, float* logits, uint64_t* tfull, uint64_t* tempty,
+                                    uint32_t tmem_base, volatile int* abort_flag, int* err, volatile int* go) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool reader = (warp & 3) == 0;  // TMEM lanes 0-31
+  const auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };  // the four epilogue warps
+  constexpr int kTokens = kFewRows / 4;  // of a warp: warp - 2, warp + 2
+  float m[kTokens], l[kTokens], es[kTokens];
+  uint64_t best[kTokens];      // lane i: the i-th kept
+  uint64_t least[kTokens];     // the least of k kept (0: fewer)
+  int kept[kTokens], y[kTokens];
+#pragma unroll
+  for (int q = 0; q < kTokens; ++q) {
+    const int row = warp - 2 + 4 * q;
+    m[q] = -INFINITY;
+    l[q] = es[q] = 0.f;
+    best[q] = least[q] = 0;
+    kept[q] = 0;
+    y[q] = (row < p.n) ? label_at(p.tokens, row, p.shift, p.seq_len, p.ignore_index) : p.ignore_index;
+  }
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  for (int n0 = r.v0; n0 < r.v1; n0 += kTileV) {
+    const int cols = min(kTileV, r.v1 - n0);
+    if (reader) {
+      // (the whole warp goes on or gives up, and with it the other three)
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, p.timeout_ns, abort_flag));
+      if (ok) {
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c * 32 < cols; ++c) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld_32x32(tmem_base + static_cast<uint32_t>(acc * kTileV + c * 32), v);
+          if (lane < p.n) {
+            float4* o = reinterpret_cast<float4*>(logits + lane * kFewPitch + c * 32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              o[j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                 __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+          }
+        }
+        tc_fence_before_sync();
+      } else {
+        *abort_flag = 1;
+        *err = kErrTimeout;
+      }
+      if (lane == 0) *go = ok;
+    }
+    sync();
+    if (!*go) return;
+    if (lane == 0) mbar_arrive(&tempty[acc]);
+#pragma unroll
+    for (int q = 0; q < kTokens; ++q) {
+      const int row = warp - 2 + 4 * q;
+      if (row >= p.n) break;
+      const float4* in = reinterpret_cast<const float4*>(logits + row * kFewPitch + lane * 8);
+      const float4 lo = in[0], hi = in[1];
+      float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      const int yi = y[q] - n0 - lane * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (lane * 8 + j >= cols) v[j] = -INFINITY;  // past the range (not loaded)
+        else if (j == yi && y[q] != p.ignore_index) p.tgt[row] = v[j];
+      }
+      float top = v[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = fmaxf(top, v[j]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float new_m = fmaxf(m[q], top * p.zscale);
+      float sl = 0.f, se = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = max_nan(fmaf(v[j], p.zscale, -new_m), kNoLogit);
+        const float w = fast_exp2(u);
+        sl += w;
+        se = fmaf(w, u, se);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sl += __shfl_xor_sync(0xffffffffu, sl, o);
+        se += __shfl_xor_sync(0xffffffffu, se, o);
+      }
+      const float d = max_nan(m[q] - new_m, kNoLogit);
+      const float f = fast_exp2(d);
+      es[q] = f * fmaf(l[q], d, es[q]) + se;
+      l[q] = l[q] * f + sl;
+      m[q] = new_m;
+      if (!TOP) continue;
+      uint32_t key[8], mine = 0;  // 0: none (neither a NaN nor minus infinity is an alternative)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        key[j] = v[j] > -INFINITY ? topk_key(v[j] + 0.f) : 0u;
+        mine = max(mine, key[j]);
+      }
+      while (true) {
+        const uint32_t won = __reduce_max_sync(0xffffffffu, mine);
+        // ids grow along the range: an equal value ranks after those kept
+        if (won == 0 || won <= static_cast<uint32_t>(least[q] >> 32)) break;
+        const int owner = __ffs(__ballot_sync(0xffffffffu, mine == won)) - 1;
+        int at = 8;
+        if (lane == owner) {
+          mine = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (at == 8 && key[j] == won) {
+              at = j;
+              key[j] = 0;
+            }
+            mine = max(mine, key[j]);
+          }
+        }
+        const int id = n0 + owner * 8 + __shfl_sync(0xffffffffu, at, owner);
+        const uint64_t entry = (static_cast<uint64_t>(won) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+        if (kept[q] < p.k) {
+          if (lane == kept[q]) best[q] = entry;
+          ++kept[q];
+        } else if (best[q] == least[q]) {
+          best[q] = entry;  // in the place of the least (one lane holds it: entries are distinct)
+        }
+        if (kept[q] == p.k) {
+          const uint32_t vk = lane < p.k ? static_cast<uint32_t>(best[q] >> 32) : 0xffffffffu;
+          const uint32_t vmin = __reduce_min_sync(0xffffffffu, vk);
+          const uint32_t ik = lane < p.k && vk == vmin ? static_cast<uint32_t>(best[q]) : 0xffffffffu;
+          least[q] = (static_cast<uint64_t>(vmin) << 32) | __reduce_min_sync(0xffffffffu, ik);
+        }
+      }
+    }
+    sync();  // the logits have been read
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+  }
+#pragma unroll
+  for (int q = 0; q < kTokens; ++q) {
+    const int row = warp - 2 + 4 * q;
+    if (row >= p.n) break;
+    const int64_t at = static_cast<int64_t>(row) * p.parts + blockIdx.x;
+    if (!in_bounds(at, p.part_count, err)) return;
+    if (lane == 0) {
+      p.part_m[at] = m[q];
+      p.part_l[at] = l[q];
+      p.part_s[at] = es[q];
+    }
+    if (TOP && lane < p.slots) p.cand[at * p.slots + lane] = best[q];
+  }
+}
+
 template <bool TOP>
 __global__ void __launch_bounds__(192, 1) decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
-  uint64_t* empty = full + kRingStages;
-  uint64_t* tfull = empty + kRingStages;
+  uint64_t* empty = full + kMostStages;
+  uint64_t* tfull = empty + kMostStages;
   uint64_t* tempty = tfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
-  int* flags = reinterpret_cast<int*>(tempty + 3);  // [0] abort, [1] error code
+  int* flags = reinterpret_cast<int*>(tempty + 3);  // [0] abort, [1] error code, [2] go on
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRingStages; ++i) {
+    for (int i = 0; i < kMostStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -312,12 +500,17 @@ __global__ void __launch_bounds__(192, 1) decode_kernel(const __grid_constant__ 
   griddep_begin();  // X and W may come from the kernels before
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // every call's word starts clear; only the join adds to it
   const Range r = my_range(p);
+  const SmemPlan plan = smem_plan(p.n, p.h);
   if (warp == 0) {
-    if (lane == 0) decode_producer(maps, p, r, smem, full, empty, flags, flags + 1);
+    if (lane == 0) decode_producer(maps, p, plan, r, smem, full, empty, flags, flags + 1);
   } else if (warp == 1) {
-    if (lane == 0) decode_mma(p, r, smem, full, empty, tfull, tempty, tmem_base, flags, flags + 1);
+    if (lane == 0)
+      decode_mma(p, plan, r, smem, full, empty, tfull, tempty, tmem_base, flags, flags + 1);
+  } else if (plan.few) {
+    decode_epilogue_few<TOP>(p, r, reinterpret_cast<float*>(smem + plan.cand_off), tfull, tempty, tmem_base, flags,
+                             flags + 1, flags + 2);
   } else {
-    decode_epilogue<TOP>(p, r, smem + kCandOff, tfull, tempty, tmem_base, flags, flags + 1);
+    decode_epilogue<TOP>(p, r, smem + plan.cand_off, tfull, tempty, tmem_base, flags, flags + 1);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -417,13 +610,13 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
   const float log2l = log2f(l);
   if (t == 0) {
     lse[row] = (m + log2l) * kLn2;
-    if (entropy) entropy[row] = (log2l - es / l) * kLn2;
+    if (entropy) entropy[row] = at_least_zero((log2l - es / l) * kLn2);
     if (p.tokens) {
       const int y = label_at(p.tokens, row, p.shift, p.seq_len, p.ignore_index);
       float lp = 0.f;
       if (y != p.ignore_index) {
         // relative to the same m as l: exact where the token holds the largest logit
-        if (y >= 0 && y < p.v) lp = (fmaf(p.tgt[row], p.zscale, -m) - log2l) * kLn2;
+        if (y >= 0 && y < p.v) lp = at_most_zero((fmaf(p.tgt[row], p.zscale, -m) - log2l) * kLn2);
         else atomicCAS(p.status, 0, kErrLabel);
       }
       if (logprob) logprob[row] = lp;
@@ -434,7 +627,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
   const auto put = [&](int rank, uint64_t won) {
     const float z = topk_unkey(static_cast<unsigned>(won >> 32));
     top_ids[static_cast<int64_t>(row) * p.k + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(won));
-    top_logprobs[static_cast<int64_t>(row) * p.k + rank] = (fmaf(z, p.zscale, -m) - log2l) * kLn2;
+    top_logprobs[static_cast<int64_t>(row) * p.k + rank] = at_most_zero((fmaf(z, p.zscale, -m) - log2l) * kLn2);
   };
   {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
@@ -510,6 +703,11 @@ cudaError_t decode_launches(const DecodeMaps& maps, const DecodeParams& p, int c
 }
 
 }  // namespace
+
+int decode_copies(int64_t n, int64_t h) {
+  if (smem_plan(static_cast<int>(n), static_cast<int>(h)).few) return 1;
+  return n <= 32 ? 4 : n <= 64 ? 2 : 1;
+}
 
 cudaError_t launch_decode(const DecodeMaps& maps, const DecodeParams& p, int ctas, float* logprob, float* entropy,
                           float* lse, int32_t* top_ids, float* top_logprobs, cudaStream_t stream) {

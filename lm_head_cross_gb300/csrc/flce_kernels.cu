@@ -1698,13 +1698,13 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(
   const float log2l = log2f(l);
   if (lane == 0) {
     lse_out[row] = (m + log2l) * kLn2;
-    if (entropy) entropy[row] = (log2l - es / l) * kLn2;
+    if (entropy) entropy[row] = at_least_zero((log2l - es / l) * kLn2);
     if (lv.labels) {
       const int y = label_at(lv.labels, row, lv.shift, lv.seq_len, lv.ignore_index);
       float lp = 0.f;
       if (y != lv.ignore_index) {
         // relative to the same m as l: exact where the label holds the largest logit
-        if (y >= 0 && y < v) lp = (fmaf(tgt[row], zscale, -m) - log2l) * kLn2;
+        if (y >= 0 && y < v) lp = at_most_zero((fmaf(tgt[row], zscale, -m) - log2l) * kLn2);
         else atomicCAS(status, 0, kErrLabel);
       }
       if (logprob) logprob[row] = lp;
@@ -1722,7 +1722,7 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(
   const auto put = [&](int rank, uint64_t won) {
     const float z = topk_unkey(static_cast<unsigned>(won >> 32));
     top_ids[static_cast<int64_t>(row) * k + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(won));
-    top_logprobs[static_cast<int64_t>(row) * k + rank] = (fmaf(z, zscale, -m) - log2l) * kLn2;
+    top_logprobs[static_cast<int64_t>(row) * k + rank] = at_most_zero((fmaf(z, zscale, -m) - log2l) * kLn2);
   };
   // The k-th largest of the lanes' maxima is a bound that k candidates reach and few pass.
   int rank = 0;

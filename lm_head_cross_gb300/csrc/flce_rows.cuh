@@ -23,6 +23,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// A log probability and an entropy are kept on their side of 0, which rounding can cross by
+// 1e-7 (a NaN stays one).
+__device__ __forceinline__ float at_most_zero(float v) { return v > 0.f ? 0.f : v; }
+__device__ __forceinline__ float at_least_zero(float v) { return v < 0.f ? 0.f : v; }
+
 // ----------------------------------------------------------------------------- top-k candidates
 // Each epilogue thread (one row) appends (logit, id) candidates that beat its
 // row's threshold to a buffer in the warp's shared-memory staging area (entry e

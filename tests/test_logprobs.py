@@ -174,6 +174,20 @@ def test_peaked_and_flat(n, temperature):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 60, 300])
+def test_certain_tokens_stay_on_their_side_of_zero(n):
+    """One logit far above all others, at scales whose product with log2 e rounds: log
+    probability at most 0, entropy at least 0, both within rounding of it."""
+    v = 700
+    x = torch.linspace(1, 9, n, device="cuda")[:, None].expand(n, 64).to(BF16).contiguous()
+    w = torch.zeros(v, 64, dtype=BF16, device="cuda")
+    w[123] = 0.77
+    r, _ = flce.logprobs_forward(x, w, torch.full((n,), 123, dtype=torch.int32, device="cuda"), top=2, check=True)
+    assert (r.logprob <= 0).all() and (r.top_logprobs <= 0).all() and (r.entropy >= 0).all()
+    check(r, x, w, torch.full((n,), 123, dtype=torch.int32, device="cuda"), 2, 1.0)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [1, 90, 500])
 def test_inputs_off_the_grid(n):
     """Ordinary bf16 values: the logits' own fp32 sums are within the library's promise."""
