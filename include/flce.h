@@ -369,9 +369,12 @@ flce_status_t flce_token_logprobs(const flce_problem_t* p, int32_t k, float temp
  * above on the same X, W, tokens and temperature:
  *   dz_ij = gl_i ([j = t_i] - p_ij) - ge_i p_ij (log p_ij + entropy_i),
  *   dX = dz W / T,  dW = dz^T X / T   (bf16, fp32 accumulation).
- * Rows whose token is ignored take gl_i = 0.  Runs on the bounded workspace of
- * flce_workspace_bytes(p): the logits are recomputed chunk by chunk, dz is held in
- * bf16.  entropy may be NULL where grad_entropy is. */
+ * Rows whose token is ignored take gl_i = 0.  The logits are recomputed chunk by
+ * chunk of the vocabulary, dz is held in bf16.  entropy may be NULL where
+ * grad_entropy is.  The workspace holds the O(N) words of flce_workspace_bytes(p), a
+ * chunk of dz (as wide as there, or wider up to 128 MiB) and fp32 dX, where the rows
+ * are few in up to 64 MiB of parts; it does not grow with V beyond that. */
+size_t flce_token_logprobs_backward_workspace_bytes(const flce_problem_t* p);
 flce_status_t flce_token_logprobs_backward(const flce_problem_t* p, float temperature, const void* X, const void* W,
                                            const int32_t* tokens, const float* lse, const float* entropy,
                                            const float* grad_logprob, const float* grad_entropy, void* dX, void* dW,

@@ -28,7 +28,7 @@ EXPORTED = ("flce_workspace_bytes", "flce_workspace_bytes_rowchunk", "flce_forwa
             "flce_shard_forward", "flce_shard_combine", "flce_shard_backward", "flce_valid_count",
             "flce_f32_to_bf16", "flce_layernorm_forward", "flce_layernorm_workspace_bytes", "flce_layernorm_backward",
             "flce_adamw_step", "flce_token_logprobs", "flce_token_logprobs_workspace_bytes",
-            "flce_token_logprobs_backward",
+            "flce_token_logprobs_backward", "flce_token_logprobs_backward_workspace_bytes",
             "flce_debug_checks", "flce_selftest_bounds", "flce_status_string")
 _NO_CONTEXT = contextlib.nullcontext()
 KERNEL_KINDS = ("forward", "grad", "dxdw", "small")
@@ -114,6 +114,8 @@ def lib():
     L.flce_token_logprobs_workspace_bytes.restype = sz
     L.flce_token_logprobs.argtypes = [P, ctypes.c_int32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.flce_token_logprobs.restype = ctypes.c_int
+    L.flce_token_logprobs_backward_workspace_bytes.argtypes = [P]
+    L.flce_token_logprobs_backward_workspace_bytes.restype = sz
     L.flce_token_logprobs_backward.argtypes = [P, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.flce_token_logprobs_backward.restype = ctypes.c_int
     L.flce_forward_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp]
@@ -851,11 +853,9 @@ def logprobs_forward(x, w, tokens=None, top=0, temperature=1.0, ignore_index=-10
 
 
 @functools.lru_cache(maxsize=256)
-def _bounded_bytes(n, h, v) -> int:
-    nbytes = workspace_bytes(n, h, v, reduction="none")
-    if nbytes == 0:
-        raise FlceError(1, "workspace_bytes")
-    return nbytes
+def logprobs_backward_workspace_bytes(n, h, v) -> int:
+    p = _problem(n, h, v, -100, "none")
+    return int(lib().flce_token_logprobs_backward_workspace_bytes(ctypes.byref(p)))
 
 
 def logprobs_backward(x, w, tokens, lse, entropy, grad_logprob=None, grad_entropy=None, temperature=1.0,
@@ -879,7 +879,10 @@ def logprobs_backward(x, w, tokens, lse, entropy, grad_logprob=None, grad_entrop
     p = _problem(n, h, w.shape[0], ignore_index, "none", shift, seq_len)
     with _allocating(stream):
         if ws is None:
-            ws = torch.empty(_bounded_bytes(n, h, w.shape[0]), dtype=torch.uint8, device=x.device)
+            nbytes = logprobs_backward_workspace_bytes(n, h, w.shape[0])
+            if nbytes == 0:
+                raise FlceError(1, "flce_token_logprobs_backward_workspace_bytes")
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
         dX, dW = torch.empty_like(x), torch.empty_like(w)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     _call("flce_token_logprobs_backward", lib().flce_token_logprobs_backward(

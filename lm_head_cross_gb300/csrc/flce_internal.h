@@ -94,6 +94,9 @@ struct TcParams {
   float* dw_f32;        // bwd: the fp32 dW accumulator [v, h] for kOutF32Store / kOutF32Add dW tiles (else null)
   int dx_k, dw_k;       // K extents: dX tiles run over dx_k vocabulary ids, dW tiles over dw_k rows
   int dx_first;         // 1: dX tiles are listed first (they are the long ones)
+  // bwd with dx_splits > 1: each dX tile's K is cut into that many parts of dx_split_k ids (a
+  // multiple of kBK), part s a tile of its own that goes to dx_f32 + s n h
+  int dx_splits, dx_split_k;
   int* tile_counter;    // bwd: global tile counter, zero at launch
   // row chunk of the forward-store pass: rows [r0, row_end) (row_end 0 means n)
   int r0, row_end;
@@ -212,6 +215,8 @@ cudaError_t launch_reduce_final(int nblk, const double* blk_loss, const int* blk
                                 const float* grad_loss, float* loss_out, int* n_valid_out, float* scale_out,
                                 cudaStream_t stream);
 cudaError_t launch_convert_bf16(const float* src, void* dst, int64_t count, cudaStream_t stream);
+// dX from its parts: dst[i] = bf16(sum of src[s * count + i] in the order of s); count a multiple of 8.
+cudaError_t launch_sum_parts_bf16(const float* src, int parts, void* dst, int64_t count, cudaStream_t stream);
 // fp32 -> bf16 (round to nearest even) of any count; src and dst 16-byte aligned.
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, int64_t count, cudaStream_t stream);
 

@@ -178,18 +178,23 @@ __device__ __forceinline__ bool sched_get(const TcParams& p, const Pair& pr, con
     if (s.t >= p.dw_tiles + p.dx_tiles) return false;
     // the long tiles come first (dW when K = N, dX when K = V)
     const bool is_dx = p.dx_first ? (s.t < p.dx_tiles) : (s.t >= p.dw_tiles);
-    const int u = p.dx_first ? (is_dx ? s.t : s.t - p.dx_tiles) : (is_dx ? s.t - p.dw_tiles : s.t);
+    int u = p.dx_first ? (is_dx ? s.t : s.t - p.dx_tiles) : (is_dx ? s.t - p.dw_tiles : s.t);
+    t.split = 0;
+    if (is_dx && p.dx_splits > 1) {
+      const int whole = p.dx_tiles / p.dx_splits;
+      t.split = u / whole;
+      u -= t.split * whole;
+    }
     t.m0 = (u / p.h_tiles) * kPairM + half;  // dX: row of the G buffer; dW: column (vocabulary id) of the G buffer
     t.n0 = (u % p.h_tiles) * kBN;            // hidden column
     if (is_dx) {
-      t.kblocks = ceil_div(p.dx_k, kBK);
+      t.kblocks = ceil_div(p.dx_splits > 1 ? min(p.dx_split_k, p.dx_k - t.split * p.dx_split_k) : p.dx_k, kBK);
       t.kind = 2;
     } else {
       t.kblocks = ceil_div(p.dw_k, kBK);
       t.kind = 3;
     }
     t.first = t.last = 0;
-    t.split = 0;
     return true;
   }
 }
@@ -307,7 +312,7 @@ __device__ void run_producer(const TcMaps& maps, const TcParams& p, const Pair& 
       uint8_t* sb = sa + kAStage;
       const uint32_t bar = full_even + 8u * stage;
       if (pr.rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
-      const int k0 = kb * kBK;
+      const int k0 = kb * kBK + (MODE == kModeBwd && p.dx_splits > 1 ? t.split * p.dx_split_k : 0);  // (dW: split 0)
       // (debug builds: a load whose inner coordinate breaks the 16-byte rule is skipped and
       // recorded; the stage's transaction count then stays short and the bounded wait ends)
       if (t.kind <= 1 || t.kind == 4) {  // A = X [N,H] K-major, B = W [V,H] K-major
@@ -924,7 +929,8 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
         // added at L2 with 16-byte accesses from the epilogue warps, which keeps this
         // traffic (a tile's 128 KiB per CTA, every 64 K steps for the bounded path's dX
         // tiles) off the TMA unit that feeds the operand stages
-        float* const fbase = is_dx ? p.dx_f32 : p.dw_f32;
+        float* const part0 = is_dx ? p.dx_f32 : p.dw_f32;
+        float* const fbase = part0 ? part0 + static_cast<int64_t>(t.split) * p.n * p.h : nullptr;  // (dW: split 0)
         const int frows = fbase ? (is_dx ? p.n : p.v) : 0;  // no address: nothing written, error recorded
         if (!fbase && lane == 0) atomicCAS(p.status, 0, kErrBounds);
         if (lane == 0) bulk_wait_group_read<0>();  // earlier TMA stores are done with the staging buffers
@@ -1769,6 +1775,25 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(
   }
 }
 
+// Eight elements a thread; the parts' loads are independent, their sum is in order.
+__global__ void __launch_bounds__(256) sum_parts_bf16_kernel(const float* __restrict__ src, int parts,
+                                                             __nv_bfloat16* __restrict__ dst, int64_t count8) {
+  griddep_begin();
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < count8;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(src) + 2 * (s * count8 + i);
+      const float4 x = p[0], y = p[1];
+      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+    }
+    reinterpret_cast<uint4*>(dst)[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                                                  pack_bf16x2(b.z, b.w));
+  }
+}
+
 __global__ void convert_bf16_kernel(const float* __restrict__ src, __nv_bfloat16* __restrict__ dst, int64_t count8) {
   griddep_begin();
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < count8;
@@ -2056,6 +2081,13 @@ cudaError_t launch_convert_bf16(const float* src, void* dst, int64_t count, cuda
   if (blocks < 1) blocks = 1;
   return launch_k(convert_bf16_kernel, dim3(static_cast<int>(blocks)), dim3(256), 0, stream, src,
                   static_cast<__nv_bfloat16*>(dst), count8);
+}
+
+cudaError_t launch_sum_parts_bf16(const float* src, int parts, void* dst, int64_t count, cudaStream_t stream) {
+  const int64_t count8 = count / 8;
+  const int64_t blocks = std::min<int64_t>((count8 + 255) / 256, 1 << 16);
+  return launch_k(sum_parts_bf16_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(blocks, 1))), dim3(256), 0, stream,
+                  src, parts, static_cast<__nv_bfloat16*>(dst), count8);
 }
 
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, int64_t count, cudaStream_t stream) {

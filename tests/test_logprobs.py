@@ -320,6 +320,23 @@ def test_gradients(n, h, v, temperature, which):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,h,v", [(8000, 72, 20000), (1000, 64, 70000), (20, 1032, 60000), (17000, 8, 9000)])
+def test_gradients_over_several_chunks_and_parts(n, h, v):
+    """Vocabularies of several chunks (the last a narrow one), with dX in parts and without."""
+    x, w, tok = grid_inputs(n, h, v, seed=n)
+    g = torch.Generator().manual_seed(3)
+    gl, ge = (torch.randn(n, generator=g).cuda() / n for _ in range(2))
+    r, _ = flce.logprobs_forward(x, w, tok)
+    dX, dW, ws = flce.logprobs_backward(x, w, tok, r.lse, r.entropy, gl, ge, check=True)
+    rX, rW, mX, mW = gradients64(x, w, tok, gl, ge, 1.0)
+    for got, ref, mag, name in ((dX, rX, mX, "dX"), (dW, rW, mW, "dW")):
+        within(got, ref, 2.0 ** -8 * (mag * (1 + 2.0 ** -8) + ref.abs()) + 1e-5 * mag.max() + 1e-30, name)
+        assert (got.double() - ref).norm() <= 2.0 ** -8 * math.sqrt(2) * ref.norm() + 1e-20, name
+    again = flce.logprobs_backward(x, w, tok, r.lse, r.entropy, gl, ge, ws=ws)
+    assert torch.equal(dX, again[0]) and torch.equal(dW, again[1])  # parts join in a fixed order
+
+
+@pytest.mark.gpu
 def test_gradients_agree_with_the_cross_entropy():
     """-logprob summed is the cross-entropy: its gradients come from the same products."""
     x, w, tok = grid_inputs(500, 256, 5000, seed=1)
