@@ -771,6 +771,7 @@ class _LayerNorm:
                     return y
 
                 @staticmethod
+                @torch.autograd.function.once_differentiable
                 def backward(ctx, dy):
                     x2, weight, mean, rstd = ctx.saved_tensors
                     dx, dweight, dbias, _ = layernorm_backward(dy.contiguous(), x2, weight, mean, rstd,
@@ -915,6 +916,7 @@ class _TokenLogprobs:
                     return tuple(r)
 
                 @staticmethod
+                @torch.autograd.function.once_differentiable
                 def backward(ctx, g_logprob, g_entropy, *_):
                     x2, w, lse, entropy, *rest = ctx.saved_tensors
                     if g_logprob is None and g_entropy is None:

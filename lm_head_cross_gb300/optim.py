@@ -174,12 +174,15 @@ class AdamW:
         return [g[key] for g in self.groups for _ in g["params"]]
 
     def step(self, grad_scale=None, stream=None):
-        """One step from the parameters' .grad (see adamw_step)."""
+        """One step from the parameters' .grad (see adamw_step); without any gradient, none."""
         self.plan.set_lr(self._per_param("lr"))
         for i, p in enumerate(self.params):  # a parameter may have been given new storage
             if p.data_ptr() != self.plan.table[i].param:
                 self.plan.set_param(i, p.detach())
-        adamw_step(self.plan, [p.grad for p in self.params], self.steps + 1, grad_scale, stream)
+        grads = [p.grad for p in self.params]
+        if all(g is None for g in grads):
+            return
+        adamw_step(self.plan, grads, self.steps + 1, grad_scale, stream)
         self.steps += 1
 
     def zero_grad(self):
