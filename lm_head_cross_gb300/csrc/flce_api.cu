@@ -946,7 +946,7 @@ int decode_slots(int k) { return k > 0 ? std::min(k + k / 4 + 4, kDecodeSlots) :
 DecodeLayout decode_layout(const flce_problem_t& p, int k) {
   DecodeLayout L{};
   const size_t n = static_cast<size_t>(p.n);
-  const size_t parts = n * kDecodeCtas * static_cast<size_t>(decode_copies(p.n, p.h));
+  const size_t parts = n * kDecodeCtas * static_cast<size_t>(decode_copies(p.n, p.h, p.v, k));
   size_t off = kAlign;
   L.err = off;
   L.part_m = (off += align_up(sizeof(int) * kDecodeCtas));
@@ -970,7 +970,7 @@ flce_status_t run_decode(const flce_problem_t& p, int k, float inv_temp, const v
   dp.slots = decode_slots(k);
   dp.a_rows = (dp.n + 7) / 8 * 8;
   const int ctas = static_cast<int>(std::min<int64_t>(std::min(dev.sms, kDecodeCtas), (p.v + 15) / 16));
-  dp.copies = decode_copies(p.n, p.h);
+  dp.copies = decode_copies(p.n, p.h, p.v, k);
   dp.parts = dp.copies * ctas;
   dp.ignore_index = p.ignore_index;
   dp.shift = p.shift;

@@ -12,7 +12,7 @@
 // accumulators, a token a lane.  With n <= 32 X is staged four times, at rows 0, 32, 64
 // and 96 (n <= 64: twice): every warp then finds tokens in the TMEM quarter it can read,
 // and takes a quarter (half) of the tile's columns for them, which shortens what is
-// exposed after the last tile.  With n <= 8 see decode_epilogue_few.
+// exposed after the last tile, where that pays (decode_copies).  n <= 8: decode_epilogue_few.
 //
 // A second kernel, one block per token, joins the ranges' partial results.
 #include <algorithm>
@@ -27,6 +27,7 @@ namespace flce {
 namespace {
 
 constexpr int kTileV = 256;                       // vocabulary rows of a tile, at most
+constexpr int kSms = 152;                         // CTAs of a launch on a whole device
 constexpr int kSub = 16;                          // rows of the smallest box, and the ranges' grain
 constexpr int kAStageBytes = 128 * kBK * 2;       // X rows: 16 KiB
 constexpr int kBStageBytes = kTileV * kBK * 2;    // W rows: 32 KiB
@@ -704,8 +705,15 @@ cudaError_t decode_launches(const DecodeMaps& maps, const DecodeParams& p, int c
 
 }  // namespace
 
-int decode_copies(int64_t n, int64_t h) {
+// Copies of X in a stage.  They shorten the epilogue, of which the last tile's is exposed,
+// and cost the reads of X, the same lines for all SMs, with every tile.  So one copy where
+// a CTA has several tiles and either the epilogue is short (no candidates) or a tile's
+// K loop long enough to cover it.  One copy and four (us): 16 x 4096 x 128256, k = 0 and 8:
+// 171 and 179, 181 and 189; 32 x 2048 x 64000, k = 0 and 16: 48 and 51, 69 and 68;
+// 32 x 1024 x 100000, k = 16: 73 and 57; with a tile a CTA, 32 x 2048 x 32000, k = 16: 54 and 39.
+int decode_copies(int64_t n, int64_t h, int64_t v, int k) {
   if (smem_plan(static_cast<int>(n), static_cast<int>(h)).few) return 1;
+  if (v > kSms * kTileV && (k == 0 || h >= 4096)) return 1;
   return n <= 32 ? 4 : n <= 64 ? 2 : 1;
 }
 

@@ -248,7 +248,7 @@ cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv,
 // of them.  X and W are read through K-major maps: x
 // with a_rows (n rounded up to a multiple of 8) rows a box, w[i] with 256 >> i.
 constexpr int kDecodeRows = 128;  // most rows
-int decode_copies(int64_t n, int64_t h);
+int decode_copies(int64_t n, int64_t h, int64_t v, int k);
 constexpr int kDecodeCtas = 160;
 constexpr int kDecodeBoxes = 5;   // 256 rows to 16
 constexpr int kDecodeSlots = 24;  // most candidates of a part
