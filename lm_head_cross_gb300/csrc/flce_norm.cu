@@ -232,6 +232,238 @@ __global__ void __launch_bounds__(kFwdThreads<WARPS, VPL>) norm_fwd_rows_kernel(
   }
 }
 
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* smem, const void* gmem) {
+  static_assert(BYTES == 16 || BYTES == 4, "sizes used");
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+// 16 bytes, of which the first `bytes` are read and the others are zeros.
+__device__ __forceinline__ void cp_async_part(void* smem, const void* gmem, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem)), "l"(gmem), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ----------------------------------------------------------------------------- rows at any 16-byte phase
+
+// Rows whose length no 16-byte access divides start at every phase of one, but row r + 8's
+// is row r's.  So a block takes rows a multiple of 8 apart, and its lanes' accesses start
+// where the 16-byte lines do: `phase` elements before each row, the same for all of the
+// block's rows.  The lanes then own the same columns of every row as in the aligned
+// kernels; only a row's first and last access are cut.
+__device__ __forceinline__ int row_phase(int h, int n) {
+  return static_cast<int>((blockIdx.x * static_cast<unsigned>(h)) & static_cast<unsigned>(n - 1));
+}
+
+// Blocks of a launch whose blocks keep to one phase: `most` is a multiple of 8.
+int phase_blocks(int64_t blocks, int most) {
+  return static_cast<int>(std::min<int64_t>((blocks + 7) / 8 * 8, most));
+}
+
+// Copies an access that starts at column c of its row (column 0 at `row`), zeros past h.
+template <typename T, int N>
+__device__ __forceinline__ void cp_async_row(void* smem, const T* row, int c, int h) {
+  cp_async_part(smem, row + c, (h - c < N ? h - c : N) * static_cast<int>(sizeof(T)));
+}
+
+// Columns [c, c + N) of a row, of which those in [0, h) exist.
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* row, int c, int h, const Pack<T, N>& p) {
+  if (c >= 0 && c + N <= h) {
+    *reinterpret_cast<Pack<T, N>*>(row + c) = p;
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (c + e >= 0 && c + e < h) row[c + e] = p.v[e];
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void load_w_row(const void* w, bool f32, int c, int h, float (&o)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    o[e] = 0.f;
+    if (c + e < 0 || c + e >= h) continue;
+    o[e] = f32 ? static_cast<const float*>(w)[c + e] : to_f32(static_cast<const __nv_bfloat16*>(w)[c + e]);
+  }
+}
+
+template <typename T, int N, int GW, int VPL>
+struct FwdPhaseShape {
+  static constexpr int kWarps = 16;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kGroups = kWarps / GW;
+  static constexpr int kColumns = 32 * GW * VPL * N;               // the widest row, with its phase
+  static constexpr int kStages = VPL <= 1 ? 4 : VPL <= 2 ? 3 : 2;  // rows in flight for each group
+  static constexpr int kStageBytes = kThreads * VPL * 16;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kSmemBytes = kRingBytes + 8 * kColumns;  // weight and bias in fp32
+  static constexpr int kBlocks = kSmemBytes <= 112 * 1024 && VPL <= 4 ? 2 : 1;  // on one SM
+};
+
+// Forward at any phase.  GW warps share a row, kGroups rows in a block at a time; blocks stay,
+// because no vector access fits the weight and bias here: a block lays them out once, in
+// fp32 and in the lanes' order, and its rows stream through a ring of asynchronous copies, of
+// which a lane reads back only its own.
+template <typename T, int N, int GW, int VPL>
+__global__ void __launch_bounds__(FwdPhaseShape<T, N, GW, VPL>::kThreads, FwdPhaseShape<T, N, GW, VPL>::kBlocks)
+    norm_fwd_phase_kernel(int n, int h, int64_t pitch, float eps, const T* __restrict__ x,
+                          const void* __restrict__ weight, const void* __restrict__ bias, bool w_f32,
+                          T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
+  using S = FwdPhaseShape<T, N, GW, VPL>;
+  static_assert(VPL * N <= 32 && N % 4 == 0, "a bit for each of a lane's columns");
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][S::kWarps];
+  griddep_begin();
+  const int group = static_cast<int>(threadIdx.x) / (32 * GW);
+  const int lane = static_cast<int>(threadIdx.x) % (32 * GW);
+  const int first = blockIdx.x + group * gridDim.x;
+  const int step = gridDim.x * S::kGroups;  // (row + step fits 32 bits: see norm_forward)
+  const int phase = row_phase(h, N);
+  const auto column = [&](int k) { return (k * 32 * GW + lane) * N - phase; };
+  const auto slot = [&](int stage, int k) { return ring + stage * S::kStageBytes + (k * S::kThreads + threadIdx.x) * 16; };
+  const auto fetch = [&](int row, int stage) {
+    if (row < n) {
+      const T* xr = x + row * pitch;
+#pragma unroll
+      for (int k = 0; k < VPL; ++k)
+        if (column(k) < h) cp_async_row<T, N>(slot(stage, k), xr, column(k), h);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S::kStages; ++s) fetch(first + s * step, s);
+
+  // Which of the lane's columns exist (bit k N + e), and for each access: whether the warp
+  // has any (bit 2k), and whether some are missing (bit 2k + 1).
+  constexpr uint32_t kFull = (1u << N) - 1;
+  uint32_t valid = 0, uses = 0;
+#pragma unroll
+  for (int k = 0; k < VPL; ++k) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) m |= (column(k) + e >= 0 && column(k) + e < h ? 1u : 0u) << e;
+    valid |= m << (k * N);
+    uses |= (__any_sync(0xffffffffu, m != 0) ? 1u : 0u) << (2 * k);
+    uses |= (__any_sync(0xffffffffu, m != kFull) ? 2u : 0u) << (2 * k);
+    if (column(k) >= h)  // zeros throughout
+      for (int s = 0; s < S::kStages; ++s) *reinterpret_cast<uint4*>(slot(s, k)) = make_uint4(0, 0, 0, 0);
+  }
+  float4* const wb = reinterpret_cast<float4*>(ring + S::kRingBytes);
+  constexpr int kBias = S::kColumns / 4;  // where the bias starts
+  if (group == 0) {
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) {
+      float w[N], b[N] = {};
+      load_w_row<N>(weight, w_f32, column(k), h, w);
+      if (bias) load_w_row<N>(bias, w_f32, column(k), h, b);
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const int at = (k * (N / 4) + q) * 32 * GW + lane;
+        wb[at] = make_float4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        wb[kBias + at] = make_float4(b[4 * q], b[4 * q + 1], b[4 * q + 2], b[4 * q + 3]);
+      }
+    }
+  }
+  __syncthreads();
+  const auto group_sum = [&](float v, float* at) {
+    v = warp_sum(v);
+    if constexpr (GW > 1) {
+      // (either half of red[] is rewritten only after the other's next barrier)
+      if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = v;
+      if constexpr (S::kGroups == 1) __syncthreads();
+      else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * GW) : "memory");
+      v = 0.f;
+#pragma unroll
+      for (int q = 0; q < GW; ++q) v += at[group * GW + q];
+    }
+    return v;
+  };
+  int stage = 0;
+  for (int row = first; row < n; row += step) {
+    cp_async_wait<S::kStages - 1>();
+    Pack<T, N> v[VPL];
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) v[k] = *reinterpret_cast<const Pack<T, N>*>(slot(stage, k));
+    __syncwarp();
+    fetch(row + S::kStages * step, stage);
+    if (++stage == S::kStages) stage = 0;
+    if (lane == 0 && phase > 0) {  // the row before
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < phase) v[0].v[e] = from_f32<T>(0.f);
+    }
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) {
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) s2 = add2(s2, element2(v[k], e));
+    }
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) keep_packed(v[k]);
+    const float mu = group_sum(s2.x + s2.y, red[0]) / h;
+    float2 q2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) {
+      if ((uses >> (2 * k) & 2u) == 0) {
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          const float2 d = add2(element2(v[k], e), both(-mu));
+          q2 = fma2(d, d, q2);
+        }
+      } else if (uses >> (2 * k) & 1u) {
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          float2 d = add2(element2(v[k], e), both(-mu));
+          if (!(valid >> (k * N + 2 * e) & 1u)) d.x = 0.f;
+          if (!(valid >> (k * N + 2 * e + 1) & 1u)) d.y = 0.f;
+          q2 = fma2(d, d, q2);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) keep_packed(v[k]);
+    const float rs = 1.f / sqrtf(group_sum(q2.x + q2.y, red[1]) / h + eps);
+    T* yr = y + static_cast<int64_t>(row) * h;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) {
+      if (!(uses >> (2 * k) & 1u)) continue;
+      float o[N];
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const int at = (k * (N / 4) + q) * 32 * GW + lane;
+        const float4 w = wb[at], b = wb[kBias + at];
+        const float2 t0 = fma2(mul2(add2(element2(v[k], 2 * q), both(-mu)), both(rs)), make_float2(w.x, w.y),
+                               make_float2(b.x, b.y));
+        const float2 t1 = fma2(mul2(add2(element2(v[k], 2 * q + 1), both(-mu)), both(rs)), make_float2(w.z, w.w),
+                               make_float2(b.z, b.w));
+        o[4 * q] = t0.x;
+        o[4 * q + 1] = t0.y;
+        o[4 * q + 2] = t1.x;
+        o[4 * q + 3] = t1.y;
+      }
+      pack_f32(v[k], o);
+      if ((valid >> (k * N) & kFull) == kFull) {
+        *reinterpret_cast<Pack<T, N>*>(yr + column(k)) = v[k];
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (valid >> (k * N + e) & 1u) yr[column(k) + e] = v[k].v[e];
+      }
+    }
+    if (lane == 0) {
+      mean[row] = mu;
+      rstd[row] = rs;
+    }
+  }
+}
+
 // Rows too wide for registers: one block per row, the row read three times (the second
 // and third time from L2).
 template <typename T>
@@ -359,27 +591,13 @@ __global__ void __launch_bounds__(32 * kFinalWarps) norm_dw_final_kernel(int h, 
 
 // ----------------------------------------------------------------------------- backward in one pass
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(void* smem, const void* gmem) {
-  static_assert(BYTES == 16 || BYTES == 4, "sizes used");
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Shape of the one-pass backward: GW warps share a row, VPL accesses of N elements a lane,
 // kGroups rows in a block at a time.
 template <typename T, int N, int GW, int VPL>
 struct BwdShape {
   static constexpr int kAccess = sizeof(T) * N;             // bytes of an access
   static constexpr bool kRing = kAccess >= 4;               // what an asynchronous copy can move
-  static constexpr int kWarps = N == 1 && GW <= 8 ? 8 : 16;
+  static constexpr int kWarps = N == 1 && GW <= 8 ? 8 : GW % 3 == 0 ? 12 : 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kGroups = kWarps / GW;
   static constexpr int kColumns = 32 * GW * VPL * N;  // the widest row
@@ -390,7 +608,7 @@ struct BwdShape {
   static constexpr int kRingBytes = kRing ? kStages * kStageBytes : 0;
   static constexpr int kStatsBytes = kStages * kWarps * 8;  // mean and rstd of the rows in flight, for each warp
   static constexpr int kWeightBytes = N == 1 ? 0 : 4 * kColumns;  // fp32, in the lanes' order
-  static constexpr int kJoinBytes = kGroups > 1 ? 8 * kColumns : 0;
+  static constexpr int kJoinBytes = kRing ? 8 * kColumns : kGroups > 1 ? 8 * kColumns : 0;
   static constexpr int kSmemBytes = std::max(kRingBytes + kStatsBytes + kWeightBytes, kJoinBytes);
 };
 
@@ -405,7 +623,7 @@ struct BwdShape {
 // Columns past h are zeros throughout.  Bound by its three streams: 131072 x 2048 bf16 in
 // 267 us, 6.0 TB/s; its 190 instructions for each warp and row, 55% of the issue slots,
 // come next.
-template <typename T, int N, int GW, int VPL>
+template <typename T, int N, int GW, int VPL, bool PHASE>
 __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T, N, GW, VPL>::kBlocks)
     norm_bwd_rows_kernel(int n, int h, int64_t pitch, const T* __restrict__ dy, const T* __restrict__ x,
                          const void* __restrict__ weight, bool w_f32, const float* __restrict__ mean,
@@ -413,6 +631,7 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
   using S = BwdShape<T, N, GW, VPL>;
   constexpr int kPairs = S::kPairs;
   static_assert(N > 1 || VPL % 2 == 0, "columns come in pairs");
+  static_assert(N > 1 || !PHASE, "single elements have no phase");
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) float2 red[2][S::kWarps];
   griddep_begin();
@@ -421,7 +640,8 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
   const int first = blockIdx.x + group * gridDim.x;
   const int step = gridDim.x * S::kGroups;  // (row + step fits 32 bits: see norm_backward)
   constexpr int kAcross = 32 * GW * N;  // columns one access of the group covers
-  const auto column = [&](int k) { return k * kAcross + lane * N; };
+  const int phase = PHASE ? row_phase(h, N) : 0;
+  const auto column = [&](int k) { return k * kAcross + lane * N - phase; };
 
   const auto slot = [&](int stage, int k, int which) {  // this lane's x or dy of one access
     return ring + stage * S::kStageBytes + ((2 * k + which) * S::kThreads + threadIdx.x) * S::kAccess;
@@ -435,7 +655,10 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
 #pragma unroll
       for (int k = 0; k < VPL; ++k) {
         if (column(k) >= h) continue;
-        if constexpr (S::kRing) {
+        if constexpr (PHASE) {
+          cp_async_row<T, N>(slot(stage, k, 0), xr - lane * N, column(k), h);
+          cp_async_row<T, N>(slot(stage, k, 1), dr - lane * N, column(k), h);
+        } else if constexpr (S::kRing) {
           cp_async<S::kAccess>(slot(stage, k, 0), xr + k * kAcross);
           cp_async<S::kAccess>(slot(stage, k, 1), dr + k * kAcross);
         } else {
@@ -476,7 +699,8 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
 #pragma unroll
   for (int k = 0; k < VPL; ++k) {
     float t[N] = {};
-    if (column(k) < h) load_w<N>(weight, w_f32, column(k), t);
+    if constexpr (PHASE) load_w_row<N>(weight, w_f32, column(k), h, t);
+    else if (column(k) < h) load_w<N>(weight, w_f32, column(k), t);
     if constexpr (N == 1) {
       reinterpret_cast<float*>(w)[k] = t[0];
     } else if (group == 0) {
@@ -507,6 +731,11 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
           xh[k * (N / 2) + e] = make_float2(element(vx, 2 * e), element(vx, 2 * e + 1));
           u[k * (N / 2) + e] = make_float2(element(vd, 2 * e), element(vd, 2 * e + 1));
         }
+      }
+      if (PHASE && lane == 0) {  // the row before
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (e < phase) reinterpret_cast<float*>(xh)[e] = reinterpret_cast<float*>(u)[e] = 0.f;
       }
     } else {
 #pragma unroll
@@ -552,10 +781,15 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
       if constexpr (S::kGroups == 1) __syncthreads();
       else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * GW) : "memory");
       sum = make_float2(0.f, 0.f);
+      if constexpr (GW % 2 == 0) {
 #pragma unroll
-      for (int q = 0; q < GW; q += 2) {
-        const float4 t = *reinterpret_cast<const float4*>(&red[parity][group * GW + q]);
-        sum = add2(sum, add2(make_float2(t.x, t.y), make_float2(t.z, t.w)));
+        for (int q = 0; q < GW; q += 2) {
+          const float4 t = *reinterpret_cast<const float4*>(&red[parity][group * GW + q]);
+          sum = add2(sum, add2(make_float2(t.x, t.y), make_float2(t.z, t.w)));
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < GW; ++q) sum = add2(sum, red[parity][group * GW + q]);
       }
       parity ^= 1;
     }
@@ -575,7 +809,11 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
         }
         Pack<T, N> out;
         pack_f32(out, o);
-        if (column(k) < h) *reinterpret_cast<Pack<T, N>*>(or_ + k * kAcross) = out;
+        if constexpr (PHASE) {
+          if (column(k) < h) store_row<T, N>(or_ - lane * N, column(k), h, out);
+        } else {
+          if (column(k) < h) *reinterpret_cast<Pack<T, N>*>(or_ + k * kAcross) = out;
+        }
       } else if (k % 2 == 0) {
         const float2 d = fma2(xh[k / 2], c1, fma2(u[k / 2], both(rs), c0));
         if (column(k) < h) or_[k * kAcross] = from_f32<T>(d.x);
@@ -584,18 +822,19 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
     }
   }
 
-  // one row of partial sums a block, in the lanes' order (value i of lane l at i * 32 GW + l);
-  // its groups join in order
+  // one row of partial sums a block, in the lanes' order (value i of lane l at i * 32 GW + l),
+  // or with a phase, which differs by block, in the columns'; its groups join in order
   constexpr int kHalf = S::kColumns;
-  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * kHalf;
+  constexpr bool kJoin = PHASE || S::kGroups > 1;
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * (PHASE ? h : kHalf);
   float* to = out;
-  if constexpr (S::kGroups > 1) {
+  if constexpr (kJoin) {
     cp_async_wait<0>();
     to = reinterpret_cast<float*>(ring);
   }
 #pragma unroll 1
   for (int g = 0; g < S::kGroups; ++g) {
-    if constexpr (S::kGroups > 1) __syncthreads();
+    if constexpr (kJoin) __syncthreads();
     if (g != group) continue;
 #pragma unroll
     for (int i = 0; i < VPL * N; ++i) {
@@ -604,9 +843,18 @@ __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T,
       to[kHalf + j] = (g ? to[kHalf + j] : 0.f) + reinterpret_cast<const float*>(ab)[i];
     }
   }
-  if constexpr (S::kGroups > 1) {
+  if constexpr (kJoin) {
     __syncthreads();
-    for (int j = threadIdx.x; j < 2 * kHalf; j += S::kThreads) out[j] = to[j];
+    if constexpr (PHASE) {
+      for (int j = threadIdx.x; j < h; j += S::kThreads) {
+        const int p = j + phase;
+        const int at = (p / kAcross * N + p % N) * 32 * GW + p % kAcross / N;
+        out[j] = to[at];
+        out[h + j] = to[kHalf + at];
+      }
+    } else {
+      for (int j = threadIdx.x; j < 2 * kHalf; j += S::kThreads) out[j] = to[j];
+    }
   }
 }
 
@@ -633,6 +881,8 @@ cudaError_t norm_forward_vpl(const NormForwardArgs& a, int accesses) {
   if (per <= 1) return norm_forward_rows<T, N, WARPS, 1>(a);
   if (per <= 2) return norm_forward_rows<T, N, WARPS, 2>(a);
   if (per <= 4) return norm_forward_rows<T, N, WARPS, 4>(a);
+  if (per <= 5) return norm_forward_rows<T, N, WARPS, 5>(a);
+  if (per <= 6) return norm_forward_rows<T, N, WARPS, 6>(a);
   if (per <= 8) return norm_forward_rows<T, N, WARPS, 8>(a);
   return norm_forward_rows<T, N, WARPS, 16>(a);
 }
@@ -653,17 +903,57 @@ cudaError_t norm_forward_warps(const NormForwardArgs& a) {
   return norm_forward_vpl<T, N, 16>(a, accesses);
 }
 
+template <typename T, int N, int GW, int VPL>
+cudaError_t norm_forward_phase(const NormForwardArgs& a) {
+  using S = FwdPhaseShape<T, N, GW, VPL>;
+  auto* kernel = norm_fwd_phase_kernel<T, N, GW, VPL>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = S::kSmemBytes > 40 * 1024 ? allow_smem(kernel, S::kSmemBytes, done) : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  const int blocks = phase_blocks((a.q.n + S::kGroups - 1) / S::kGroups, S::kBlocks * kNormSms);
+  return launch_k(kernel, dim3(blocks), dim3(S::kThreads), S::kSmemBytes, a.stream, static_cast<int>(a.q.n), a.q.h,
+                  a.q.x_pitch, a.q.eps, static_cast<const T*>(a.x), a.weight, a.bias, a.q.w_f32,
+                  static_cast<T*>(a.y), a.mean, a.rstd);
+}
+
+bool at16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Rows of x and of the contiguous tensors start at the same phase of a 16-byte access.
+template <int N>
+bool same_phase(const NormParams& q) {
+  return (q.x_pitch - q.h) % N == 0;
+}
+
 template <typename T>
 cudaError_t norm_forward(const NormForwardArgs& a) {
   constexpr int kVec = 16 / sizeof(T);
-  const size_t row = sizeof(T) * static_cast<size_t>(a.q.x_pitch);
-  const auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-  const bool vec = a.q.h % kVec == 0 && row % 16 == 0 && at16(a.x) && at16(a.y) && at16(a.weight) && at16(a.bias);
   constexpr int kMost = 32 * 16 * 16;  // accesses of the widest row held in registers
-  if (a.q.n <= 0x7fffffff) {
-    if (vec && a.q.h <= kMost * kVec) return norm_forward_warps<T, kVec>(a);
-    if (!vec && a.q.h <= kMost) return norm_forward_warps<T, 1>(a);
+  if (at16(a.x) && at16(a.y)) {
+    const bool vec = a.q.h % kVec == 0 && a.q.x_pitch % kVec == 0 && at16(a.weight) && at16(a.bias);
+    if (vec && a.q.n <= 0x7fffffff && a.q.h <= kMost * kVec) return norm_forward_warps<T, kVec>(a);
+    // Accesses at a phase against single elements (us): bf16 65536 x 2049 126 and 246, 65536 x
+    // 999 49 and 74, 131072 x 250 43 and 66, but 131072 x 100 35 and 31, where a row is less than
+    // a warp's worth; fp32 65536 x 1031 92 and 111, 32768 x 2050 90 and 130, but 65536 x 501 48
+    // and 41, where single elements need no barrier.  Laying out the weight takes 2 us, which
+    // smaller calls do not earn back (bf16 2048 x 1001 4.8 and 4.0, 2048 x 1501 5.7 and 6.1).
+    const bool earns = a.q.n * a.q.h >= (3 << 20) && a.q.h > (sizeof(T) == 2 ? 128 : 1024);
+    if (!vec && same_phase<kVec>(a.q) && a.q.n <= (1 << 30) && (earns || a.q.h > kMost)) {
+      const int accesses = (a.q.h + 2 * kVec - 2) / kVec;
+      if (accesses <= 32) return norm_forward_phase<T, kVec, 1, 1>(a);
+      if (accesses <= 64) return norm_forward_phase<T, kVec, 1, 2>(a);
+      if (accesses <= 96) return norm_forward_phase<T, kVec, 1, 3>(a);
+      if (accesses <= 128) return norm_forward_phase<T, kVec, 1, 4>(a);
+      if (accesses <= 192) return norm_forward_phase<T, kVec, 2, 3>(a);
+      if (accesses <= 256) return norm_forward_phase<T, kVec, 2, 4>(a);
+      if (accesses <= 384) return norm_forward_phase<T, kVec, 4, 3>(a);
+      if (accesses <= 512) return norm_forward_phase<T, kVec, 4, 4>(a);
+      if (accesses <= 768) return norm_forward_phase<T, kVec, 8, 3>(a);
+      if (accesses <= 1024) return norm_forward_phase<T, kVec, 8, 4>(a);
+      if (accesses <= 1536) return norm_forward_phase<T, kVec, 16, 3>(a);
+      if (accesses <= 2048) return norm_forward_phase<T, kVec, 16, 4>(a);
+    }
   }
+  if (a.q.n <= 0x7fffffff && a.q.h <= kMost) return norm_forward_warps<T, 1>(a);
   const int grid = static_cast<int>(std::min<int64_t>(a.q.n, 1 << 20));
   return launch_k(norm_fwd_kernel<T>, dim3(grid), dim3(kNormThreads), 0, a.stream, a.q.n, a.q.h, a.q.x_pitch, a.q.eps,
                   static_cast<const T*>(a.x), a.weight, a.bias, a.q.w_f32, static_cast<T*>(a.y), a.mean, a.rstd);
@@ -684,16 +974,17 @@ struct PartialLayout {
   int lanes, n;
 };
 
-template <typename T, int N, int GW, int VPL>
+template <typename T, int N, int GW, int VPL, bool PHASE>
 cudaError_t norm_backward_rows(const NormBackwardArgs& a, PartialLayout* left) {
   using S = BwdShape<T, N, GW, VPL>;
   static_assert(S::kSmemBytes <= 227 * 1024 / S::kBlocks - 1536, "shared memory budget");
-  auto* kernel = norm_bwd_rows_kernel<T, N, GW, VPL>;
+  auto* kernel = norm_bwd_rows_kernel<T, N, GW, VPL, PHASE>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = S::kSmemBytes > 40 * 1024 ? allow_smem(kernel, S::kSmemBytes, done) : cudaSuccess;
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.q.n + S::kGroups - 1) / S::kGroups;
-  *left = PartialLayout{static_cast<int>(std::min<int64_t>(blocks, S::kBlocks * kNormSms)), S::kColumns, 32 * GW, N};
+  if (PHASE) *left = PartialLayout{phase_blocks(blocks, S::kBlocks * kNormSms), a.q.h, 1, 1};
+  else *left = PartialLayout{static_cast<int>(std::min<int64_t>(blocks, S::kBlocks * kNormSms)), S::kColumns, 32 * GW, N};
   return launch_k(kernel, dim3(left->slices), dim3(S::kThreads), S::kSmemBytes, a.stream, static_cast<int>(a.q.n),
                   a.q.h, a.q.x_pitch, static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.weight, a.q.w_f32,
                   a.mean, a.rstd, static_cast<T*>(a.dx), a.part);
@@ -716,30 +1007,47 @@ cudaError_t norm_backward_wide(const NormBackwardArgs& a, PartialLayout* left) {
                   a.q.x_pitch, rows, static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.mean, a.rstd, a.part);
 }
 
+// The narrowest shape that holds `accesses` accesses of 16 bytes (2048 at most).
+template <typename T, bool PHASE>
+cudaError_t norm_backward_vec(const NormBackwardArgs& a, PartialLayout* left, int accesses) {
+  constexpr int kVec = 16 / sizeof(T);
+  if (accesses <= 32) return norm_backward_rows<T, kVec, 1, 1, PHASE>(a, left);
+  if (accesses <= 64) return norm_backward_rows<T, kVec, 2, 1, PHASE>(a, left);
+  if (accesses <= 96) return norm_backward_rows<T, kVec, 3, 1, PHASE>(a, left);
+  if (accesses <= 128) return norm_backward_rows<T, kVec, 4, 1, PHASE>(a, left);
+  if (accesses <= 192) return norm_backward_rows<T, kVec, 6, 1, PHASE>(a, left);
+  if (accesses <= 256) return norm_backward_rows<T, kVec, 8, 1, PHASE>(a, left);
+  if (accesses <= 384) return norm_backward_rows<T, kVec, 12, 1, PHASE>(a, left);
+  if (accesses <= 512) return norm_backward_rows<T, kVec, 16, 1, PHASE>(a, left);
+  if (accesses <= 768) return norm_backward_rows<T, kVec, 12, 2, PHASE>(a, left);
+  if (accesses <= 1024) return norm_backward_rows<T, kVec, 16, 2, PHASE>(a, left);
+  return norm_backward_rows<T, kVec, 16, 4, PHASE>(a, left);
+}
+
 template <typename T>
 cudaError_t norm_backward(const NormBackwardArgs& a, PartialLayout* left) {
   constexpr int kVec = 16 / sizeof(T);
-  const size_t row = sizeof(T) * static_cast<size_t>(a.q.x_pitch);
-  const auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   const int h = a.q.h;
   if (a.q.n > (1 << 30)) return norm_backward_wide<T>(a, left);  // 32-bit row numbers in one pass
-  if (h % kVec == 0 && row % 16 == 0 && at16(a.x) && at16(a.dy) && at16(a.dx) && at16(a.weight)) {
-    const int acc = h / kVec;
-    if (acc <= 32) return norm_backward_rows<T, kVec, 1, 1>(a, left);
-    if (acc <= 64) return norm_backward_rows<T, kVec, 2, 1>(a, left);
-    if (acc <= 128) return norm_backward_rows<T, kVec, 4, 1>(a, left);
-    if (acc <= 256) return norm_backward_rows<T, kVec, 8, 1>(a, left);
-    if (acc <= 512) return norm_backward_rows<T, kVec, 16, 1>(a, left);
-    if (acc <= 1024) return norm_backward_rows<T, kVec, 16, 2>(a, left);
-    if (acc <= 2048) return norm_backward_rows<T, kVec, 16, 4>(a, left);
-  } else {
-    if (h <= 128) return norm_backward_rows<T, 1, 1, 4>(a, left);
-    if (h <= 512) return norm_backward_rows<T, 1, 4, 4>(a, left);
-    if (h <= 1024) return norm_backward_rows<T, 1, 8, 4>(a, left);
-    if (h <= 1536) return norm_backward_rows<T, 1, 8, 6>(a, left);
-    if (h <= 2048) return norm_backward_rows<T, 1, 8, 8>(a, left);
-    if (h <= 4096) return norm_backward_rows<T, 1, 16, 8>(a, left);
+  const int most = 2048 * kVec;  // columns of the widest vector shape
+  if (at16(a.x) && at16(a.dy) && at16(a.dx)) {
+    if (h % kVec == 0 && a.q.x_pitch % kVec == 0 && at16(a.weight) && h <= most)
+      return norm_backward_vec<T, false>(a, left, h / kVec);
+    // Accesses at a phase against single elements (us): bf16 65536 x 2049 206 and 350, 32768 x
+    // 8001 256 and 1289, 131072 x 250 72 and 123, but 131072 x 100 46 and 33; fp32 65536 x 501 69
+    // and 104.  The weight's and the partial sums' own order take 1 to 2 us more (bf16 2048 x
+    // 1501 12.8 and 11.0, 8192 x 1501 23.1 and 22.4; fp32 8192 x 1001 23.9 and 30.5), so only for
+    // many rows, or rows for which single elements are slow (bf16 2048 x 2049 15.1 and 16.6).
+    const bool earns = h > 4096 || (h > 2048 && a.q.n >= 1024) || (h > 16 * kVec && a.q.n >= 8192);
+    if (same_phase<kVec>(a.q) && h + kVec - 1 <= most && earns)
+      return norm_backward_vec<T, true>(a, left, (h + 2 * kVec - 2) / kVec);
   }
+  if (h <= 128) return norm_backward_rows<T, 1, 1, 4, false>(a, left);
+  if (h <= 512) return norm_backward_rows<T, 1, 4, 4, false>(a, left);
+  if (h <= 1024) return norm_backward_rows<T, 1, 8, 4, false>(a, left);
+  if (h <= 1536) return norm_backward_rows<T, 1, 8, 6, false>(a, left);
+  if (h <= 2048) return norm_backward_rows<T, 1, 8, 8, false>(a, left);
+  if (h <= 4096) return norm_backward_rows<T, 1, 16, 8, false>(a, left);
   return norm_backward_wide<T>(a, left);
 }
 
@@ -748,7 +1056,7 @@ cudaError_t norm_backward(const NormBackwardArgs& a, PartialLayout* left) {
 // Every shape: at most 512 or twice h columns, and blocks for three on an SM only for single
 // elements of narrow rows.
 size_t norm_partial_floats(int64_t n, int64_t h) {
-  const int64_t slices = std::min<int64_t>(std::max<int64_t>(n, 1), (h <= 2048 ? 3 : 2) * kNormSms);
+  const int64_t slices = phase_blocks(std::max<int64_t>(n, 1), (h <= 2048 ? 3 : 2) * kNormSms);
   return static_cast<size_t>(slices) * 2 * static_cast<size_t>(std::max<int64_t>(512, 2 * h));
 }
 

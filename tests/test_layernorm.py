@@ -102,7 +102,8 @@ def check_backward(x, w, dy, mean, rstd, got):
 TYPES = [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (torch.float32, torch.float32),
          (torch.float32, torch.bfloat16)]
 SIZES = [(1, 1), (1, 8), (3, 7), (2, 16), (5, 1000), (257, 2048), (33, 4096), (64, 8192), (17, 16392), (9, 20001),
-         (300, 1031), (2, 65536), (4099, 24), (1000, 520), (777, 1544), (2500, 4096)]
+         (300, 1031), (2, 65536), (4099, 24), (1000, 520), (777, 1544), (2500, 4096),
+         (7000, 1), (5000, 33), (3000, 250), (2000, 999), (1500, 2049), (900, 4100), (700, 4089), (400, 8185), (300, 16377)]
 
 
 @pytest.mark.gpu
