@@ -148,7 +148,8 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 
 // Forward: the row stays in registers between its three uses (mean, squares about the
 // mean, y), so memory sees one read of x and one write of y: bound by their bytes, 131072 x
-// 4096 bf16 in 313 us, 6.85 TB/s.  WARPS warps share a row, VPL accesses of N elements a
+// 4096 bf16 in 307 us, 7.0 TB/s (with fp32 weights, whose loads fill the first-level cache's
+// ports, 352).  WARPS warps share a row, VPL accesses of N elements a
 // lane, all in flight at once; a row each with WARPS = 1, whose sums are shuffles alone, and
 // then several rows a block where they are short (the device starts about one block a
 // nanosecond).
@@ -310,7 +311,9 @@ struct FwdPhaseShape {
 // Forward at any phase.  GW warps share a row, kGroups rows in a block at a time; blocks stay,
 // because no vector access fits the weight and bias here: a block lays them out once, in
 // fp32 and in the lanes' order, and its rows stream through a ring of asynchronous copies, of
-// which a lane reads back only its own.
+// which a lane reads back only its own.  Bound by issue and the exchange of the row's two sums:
+// bf16 65536 x 2049 in 126 us, 4.3 TB/s (246 by single elements), fp32 32768 x 2050 in 90 us,
+// 6.0 TB/s.
 template <typename T, int N, int GW, int VPL>
 __global__ void __launch_bounds__(FwdPhaseShape<T, N, GW, VPL>::kThreads, FwdPhaseShape<T, N, GW, VPL>::kBlocks)
     norm_fwd_phase_kernel(int n, int h, int64_t pitch, float eps, const T* __restrict__ x,
@@ -621,8 +624,8 @@ struct BwdShape {
 //   guards the ring.  Single bf16 elements (rows that no 16-byte access fits) are too small
 //   to copy: there the next row waits in registers.
 // Columns past h are zeros throughout.  Bound by its three streams: 131072 x 2048 bf16 in
-// 267 us, 6.0 TB/s; its 190 instructions for each warp and row, 55% of the issue slots,
-// come next.
+// 244 us, 6.6 TB/s; its instructions, 58% of the issue slots, come next.  At 8192 x 2048 (24
+// us, 4.2 TB/s) the start, the partial sums and the launch that adds them show.
 template <typename T, int N, int GW, int VPL, bool PHASE>
 __global__ void __launch_bounds__(BwdShape<T, N, GW, VPL>::kThreads, BwdShape<T, N, GW, VPL>::kBlocks)
     norm_bwd_rows_kernel(int n, int h, int64_t pitch, const T* __restrict__ dy, const T* __restrict__ x,
@@ -874,17 +877,31 @@ cudaError_t norm_forward_rows(const NormForwardArgs& a) {
                   a.weight, a.bias, a.q.w_f32, static_cast<T*>(a.y), a.mean, a.rstd);
 }
 
-// The narrowest VPL whose WARPS warps hold a row of `accesses` accesses.
+// Accesses of a lane that a row of many is dealt in: 64 or 128 bytes, single elements 16.
+template <typename T, int N>
+constexpr int kFwdWant = sizeof(T) * N == 16 ? 8 : 16;
+
+// The narrowest VPL whose WARPS warps hold a row of `accesses` accesses, of those that
+// norm_forward_warps asks for (two warps or more hold over half of kFwdWant, or one).
 template <typename T, int N, int WARPS>
 cudaError_t norm_forward_vpl(const NormForwardArgs& a, int accesses) {
   const int per = (accesses + 32 * WARPS - 1) / (32 * WARPS);
+  constexpr bool kAny = WARPS == 1 || WARPS == 16;
+  constexpr int kWant = kFwdWant<T, N>;
   if (per <= 1) return norm_forward_rows<T, N, WARPS, 1>(a);
-  if (per <= 2) return norm_forward_rows<T, N, WARPS, 2>(a);
-  if (per <= 4) return norm_forward_rows<T, N, WARPS, 4>(a);
-  if (per <= 5) return norm_forward_rows<T, N, WARPS, 5>(a);
-  if (per <= 6) return norm_forward_rows<T, N, WARPS, 6>(a);
-  if (per <= 8) return norm_forward_rows<T, N, WARPS, 8>(a);
-  return norm_forward_rows<T, N, WARPS, 16>(a);
+  if constexpr (kAny) {
+    if (per <= 2) return norm_forward_rows<T, N, WARPS, 2>(a);
+    if (per <= 4) return norm_forward_rows<T, N, WARPS, 4>(a);
+  }
+  if constexpr (kAny || kWant == 8) {
+    if (per <= 6) return norm_forward_rows<T, N, WARPS, 6>(a);
+    if (per <= 8) return norm_forward_rows<T, N, WARPS, 8>(a);
+  }
+  if constexpr (WARPS == 16 || kWant == 16) {
+    if (per <= 12) return norm_forward_rows<T, N, WARPS, 12>(a);
+    return norm_forward_rows<T, N, WARPS, 16>(a);
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <typename T, int N>
@@ -895,7 +912,7 @@ cudaError_t norm_forward_warps(const NormForwardArgs& a) {
   // 5341, h 8192 5793 / 5709 / 6836 / 5781), or 16 of a single element (fp32, h 1031, 4 warps
   // 4870, 8 warps 3731).  Few rows leave SMs idle, and a row is done sooner by more warps (4 x
   // 4096 as timed with its launch, 1 / 4 / 16 warps: 21 / 10 / 7 us).
-  const int want = a.q.n < 1024 ? 1 : N == 1 ? 16 : 8;
+  const int want = a.q.n < 1024 ? 1 : kFwdWant<T, N>;
   if (accesses <= 32 * want) return norm_forward_vpl<T, N, 1>(a, accesses);
   if (accesses <= 64 * want) return norm_forward_vpl<T, N, 2>(a, accesses);
   if (accesses <= 128 * want) return norm_forward_vpl<T, N, 4>(a, accesses);
@@ -916,7 +933,8 @@ cudaError_t norm_forward_phase(const NormForwardArgs& a) {
                   static_cast<T*>(a.y), a.mean, a.rstd);
 }
 
-bool at16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool at16(const void* p) { return aligned(p, 16); }
 
 // Rows of x and of the contiguous tensors start at the same phase of a 16-byte access.
 template <int N>
@@ -928,16 +946,25 @@ template <typename T>
 cudaError_t norm_forward(const NormForwardArgs& a) {
   constexpr int kVec = 16 / sizeof(T);
   constexpr int kMost = 32 * 16 * 16;  // accesses of the widest row held in registers
+  const auto fits = [&](int n) {       // rows, weight and bias in accesses of n elements
+    const int size = n * static_cast<int>(sizeof(T)), w_size = a.q.w_f32 ? 16 : 2 * n;
+    return a.q.h % n == 0 && a.q.x_pitch % n == 0 && aligned(a.x, size) && aligned(a.y, size) &&
+           aligned(a.weight, w_size) && aligned(a.bias, w_size) && a.q.n <= 0x7fffffff && a.q.h <= kMost * n;
+  };
+  // bf16 rows with fp32 weights go by 4 elements: a warp's weights are then 512 consecutive
+  // bytes, where 8 would be every other 16 of 1024, and the first-level cache's rate bounds
+  // (65536 x 768 38 us, by 8 41; 65536 x 5120 228 and 234).
+  if constexpr (kVec == 8)
+    if ((a.q.w_f32 || !fits(8)) && fits(4)) return norm_forward_warps<T, 4>(a);
+  if (fits(kVec)) return norm_forward_warps<T, kVec>(a);
   if (at16(a.x) && at16(a.y)) {
-    const bool vec = a.q.h % kVec == 0 && a.q.x_pitch % kVec == 0 && at16(a.weight) && at16(a.bias);
-    if (vec && a.q.n <= 0x7fffffff && a.q.h <= kMost * kVec) return norm_forward_warps<T, kVec>(a);
     // Accesses at a phase against single elements (us): bf16 65536 x 2049 126 and 246, 65536 x
     // 999 49 and 74, 131072 x 250 43 and 66, but 131072 x 100 35 and 31, where a row is less than
     // a warp's worth; fp32 65536 x 1031 92 and 111, 32768 x 2050 90 and 130, but 65536 x 501 48
     // and 41, where single elements need no barrier.  Laying out the weight takes 2 us, which
     // smaller calls do not earn back (bf16 2048 x 1001 4.8 and 4.0, 2048 x 1501 5.7 and 6.1).
     const bool earns = a.q.n * a.q.h >= (3 << 20) && a.q.h > (sizeof(T) == 2 ? 128 : 1024);
-    if (!vec && same_phase<kVec>(a.q) && a.q.n <= (1 << 30) && (earns || a.q.h > kMost)) {
+    if (same_phase<kVec>(a.q) && a.q.n <= (1 << 30) && (earns || a.q.h > kMost)) {
       const int accesses = (a.q.h + 2 * kVec - 2) / kVec;
       if (accesses <= 32) return norm_forward_phase<T, kVec, 1, 1>(a);
       if (accesses <= 64) return norm_forward_phase<T, kVec, 1, 2>(a);
