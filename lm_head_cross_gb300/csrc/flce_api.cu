@@ -921,7 +921,7 @@ ScoreLayout score_layout(const flce_problem_t& p, int k) {
   ScoreLayout L{};
   const size_t n = static_cast<size_t>(p.n);
   L.splits = score_splits(p.n);
-  const size_t part = align_up(sizeof(float) * static_cast<size_t>(L.splits) * n);
+  const size_t parts = static_cast<size_t>(L.splits * kScoreSub) * n, part = align_up(sizeof(float) * parts);
   size_t off = kAlign;
   L.part_m = off;
   L.part_l = (off += part);
@@ -930,7 +930,7 @@ ScoreLayout score_layout(const flce_problem_t& p, int k) {
   L.thr = (off += align_up(sizeof(float) * n));
   if (k > 0) off += align_up(sizeof(unsigned) * n);
   L.cand = off;
-  L.total = off + align_up(sizeof(uint64_t) * static_cast<size_t>(L.splits) * n * static_cast<size_t>(k));
+  L.total = off + align_up(sizeof(uint64_t) * parts * static_cast<size_t>(k));
   return L;
 }
 
@@ -1035,12 +1035,12 @@ flce_status_t run_score(const flce_problem_t& p, int k, float inv_temp, const vo
   tp.zscale = kLog2e * inv_temp;
   tp.inv_temp = inv_temp;
   tp.tile_counter = reinterpret_cast<int*>(ws) + 1;
-  tp.part_count = static_cast<int64_t>(L.splits) * p.n;
+  tp.part_count = static_cast<int64_t>(L.splits) * kScoreSub * p.n;
   if (k > 0) {
     tp.topk_thr = reinterpret_cast<unsigned*>(ws + L.thr);
     tp.topk_keys = reinterpret_cast<uint64_t*>(ws + L.cand);
     tp.topk_k = k;
-    tp.topk_count = static_cast<int64_t>(L.splits) * p.n * k;
+    tp.topk_count = static_cast<int64_t>(L.splits) * kScoreSub * p.n * k;
   }
   const double flops = 2.0 * static_cast<double>(p.n) * static_cast<double>(p.v) * static_cast<double>(p.h);
   const int grid = pair_grid(dev.sms, static_cast<long long>(tp.row_tiles) * tp.vsplit);
@@ -1050,7 +1050,7 @@ flce_status_t run_score(const flce_problem_t& p, int k, float inv_temp, const vo
   if (st != FLCE_OK) return st;
   const LabelView lv{tokens, p.ignore_index, p.shift, p.shift ? p.seq_len : 1, nullptr, nullptr, 0};
   return cuda_status(timed(3, 0.0, stream, [&] {
-    return launch_score_finalize(tp.n, tp.v, tp.vsplit, k, lv, tp.zscale, tp.part_m, tp.part_l, tp.part_s, tp.tgt,
+    return launch_score_finalize(tp.n, tp.v, kScoreSub * tp.vsplit, k, lv, tp.zscale, tp.part_m, tp.part_l, tp.part_s, tp.tgt,
                                  tp.topk_keys, logprob, entropy, lse, top_ids, top_logprobs, tp.status, stream);
   }));
 }

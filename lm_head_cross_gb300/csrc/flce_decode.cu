@@ -194,12 +194,14 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
   const bool idle = row - lane >= p.n;                       // a warp without a token only frees accumulators
   const int y = (row < p.n) ? label_at(p.tokens, row, p.shift, p.seq_len, p.ignore_index) : p.ignore_index;
 
-  float* val = reinterpret_cast<float*>(cand + quarter * kCandBytes);
-  int* idx = reinterpret_cast<int*>(val + kTopkCand * 32);
-  int count = 0;
-  float thr = -INFINITY;        // the range's own k-th best, once it is known: ids grow, so an equal later value is out
-  float floor_thr = -INFINITY;  // nothing below it is among the row's best
-  float m = -INFINITY, l = 0.f, es = 0.f;
+  RowBest best;
+  best.val = reinterpret_cast<float*>(cand + quarter * kCandBytes);
+  best.idx = reinterpret_cast<int*>(best.val + kTopkCand * 32);
+  best.at = best_slot(0, lane);
+  best.thr = row < p.n ? -INFINITY : INFINITY;  // (a lane without a token keeps nothing)
+  best.floor = -INFINITY;
+  set_bar(best);
+  RowSum sum{-INFINITY, 0.f, 0.f};
   int acc = 0;
   uint32_t acc_phase = 0;
   for (int n0 = r.v0; n0 < r.v1; n0 += kTileV) {
@@ -214,9 +216,10 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kTileV);
     if (TOP && !idle && n0 == r.v0) {
       const int valid = min(cols - c0 * 32, chunks * 32);
-      floor_thr = chunks <= 2   ? first_floor<1>(tbase + c0 * 32, valid, p.k)
-                  : chunks == 4 ? first_floor<2>(tbase + c0 * 32, valid, p.k)
-                                : first_floor<4>(tbase, valid, p.k);
+      best.floor = chunks <= 2   ? first_floor<1>(tbase + c0 * 32, valid, p.k)
+                   : chunks == 4 ? first_floor<2>(tbase + c0 * 32, valid, p.k)
+                                 : first_floor<4>(tbase, valid, p.k);
+      set_bar(best);
     }
 #pragma unroll 1
     for (int c = c0; c < c1 && !idle; ++c) {
@@ -237,81 +240,34 @@ __device__ void decode_epilogue(const DecodeParams& p, Range r, uint8_t* cand, u
         for (int j = 0; j < 32; ++j)
           if (j >= nv) v[j] = __float_as_uint(-INFINITY);
       }
-      float gmax[4];  // maxima of the chunk's 8-column blocks
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        gmax[g] = __uint_as_float(v[8 * g]);
-#pragma unroll
-        for (int j = 8 * g + 1; j < 8 * g + 8; ++j) gmax[g] = fmaxf(gmax[g], __uint_as_float(v[j]));
-      }
-      const float cmax = fmaxf(fmaxf(gmax[0], gmax[1]), fmaxf(gmax[2], gmax[3]));
-      const float new_m = fmaxf(m, cmax * p.zscale);
-      float s4[4] = {0.f, 0.f, 0.f, 0.f}, e4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float u = max_nan(fmaf(__uint_as_float(v[j]), p.zscale, -new_m), kNoLogit);
-        const float w = fast_exp2(u);
-        s4[j & 3] += w;
-        e4[j & 3] = fmaf(w, u, e4[j & 3]);
-      }
-      const float d = max_nan(m - new_m, kNoLogit);
-      const float f = fast_exp2(d);
-      es = f * fmaf(l, d, es) + ((e4[0] + e4[1]) + (e4[2] + e4[3]));
-      l = l * f + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-      m = new_m;
-      if (TOP && __any_sync(0xffffffffu, row < p.n && cmax > thr && cmax >= floor_thr)) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if (!__any_sync(0xffffffffu, row < p.n && gmax[g] > thr && gmax[g] >= floor_thr)) continue;
-#pragma unroll
-          for (int j = 8 * g; j < 8 * g + 8; ++j) {
-            const float x = __uint_as_float(v[j]);
-            // ids grow along the range: an equal later value ranks after the kept one
-            const bool keep = row < p.n && x > thr && x >= floor_thr;
-            const int at = topk_slot(count, lane);
-            if (keep) {
-              val[at] = x;
-              idx[at] = col0 + j;
-            }
-            count += keep ? 1 : 0;
-          }
-          if (__any_sync(0xffffffffu, count > kTopkCand - 8)) {
-            Trimmed t = topk_trim(val, idx, count, lane, p.k, floor_thr);
-            floor_thr = t.thr;
-            t = topk_cut(val, idx, t.count, thr, lane, p.k, kTopkCand - 8);  // (many equal values: ranked)
-            count = t.count;
-            thr = t.thr;
-          }
-        }
-      }
+      float gmax[4];
+      const float cmax = block_maxima(v, gmax);
+      add_chunk(sum, v, cmax, p.zscale);
+      if (TOP) append_chunk(best, v, gmax, cmax, col0, lane, p.k);
     }
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&tempty[acc]);
     // Room for the next tile's, made while that one loads.
-    if (TOP && n0 + kTileV < r.v1 && __any_sync(0xffffffffu, count > p.k + 2)) {
-      const Trimmed t = topk_trim(val, idx, count, lane, p.k, floor_thr);
-      count = t.count;
-      floor_thr = t.thr;
-    }
+    if (TOP && n0 + kTileV < r.v1 && __any_sync(0xffffffffu, best.at >= 32 * (p.k + 3)))
+      trim_best(best, lane, p.k, kTopkCand - 8);
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
   }
-  if (TOP && __any_sync(0xffffffffu, count > p.slots)) {
-    count = topk_trim(val, idx, count, lane, p.k, floor_thr).count;
-    count = topk_cut(val, idx, count, thr, lane, p.k, p.slots).count;
-  }
+  if (TOP && __any_sync(0xffffffffu, best.at >= 32 * (p.slots + 1))) trim_best(best, lane, p.k, p.slots);
   if (row >= p.n) return;
   const int part = blockIdx.x * copies + share;
   const int64_t at = static_cast<int64_t>(row) * p.parts + part;
   if (!in_bounds(at, p.part_count, err)) return;
-  p.part_m[at] = m;
-  p.part_l[at] = l;
-  p.part_s[at] = es;
+  p.part_m[at] = sum.m;
+  p.part_l[at] = sum.l;
+  p.part_s[at] = sum.es;
   if (TOP) {
+    const int count = best.at >> 5;
 #pragma unroll 4
     for (int e = 0; e < p.slots; ++e)
-      p.cand[at * p.slots + e] = e < count ? candidate_key(val[topk_slot(e, lane)], idx[topk_slot(e, lane)]) : 0;
+      p.cand[at * p.slots + e] =
+          e < count ? candidate_key(best.val[best_slot(e, lane)], best.idx[best_slot(e, lane)]) : 0;
   }
 }
 

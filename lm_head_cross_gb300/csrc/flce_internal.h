@@ -234,6 +234,7 @@ cudaError_t launch_soft_chunk_targets(int n, int k, const int32_t* soft_idx, con
 //
 // Most splits of an n-row score pass: enough that one row tile's ranges occupy every CTA
 // pair (76 on this GPU), 16 (as for the top-k pass) from ten row tiles on.
+constexpr int kScoreSub = 2;  // sub-ranges that a score launch reports for each vocabulary split
 inline int score_splits(int64_t n) {
   const int64_t row_tiles = (n + kPairRows - 1) / kPairRows;
   const int64_t s = row_tiles > 0 ? 2 * kScoreSplitMax / row_tiles : kScoreSplitMax;

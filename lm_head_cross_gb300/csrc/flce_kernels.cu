@@ -64,11 +64,12 @@ constexpr uint16_t kPairMask = 0x3;
 // slower at H = 4096.
 template <int MODE>
 struct Cfg {
-  static constexpr int kEpiWarps = 4;
+  static constexpr bool kScore = MODE == kModeScore || MODE == kModeScoreTop;
+  static constexpr int kEpiWarps = kScore ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kStages = flce::kStages;
+  static constexpr int kStages = MODE == kModeScoreTop ? flce::kStages - 1 : flce::kStages;
   static constexpr int kSmemStagingOff = kStages * kStageBytes;
-  static constexpr int kSmemBarOff = kSmemStagingOff + kEpiWarps * kStagingPerWarp;
+  static constexpr int kSmemBarOff = kSmemStagingOff + (MODE == kModeScore ? 0 : kEpiWarps * kStagingPerWarp);
   static constexpr int kSmemBytes = kSmemBarOff + 512 + 1024;  // barriers, ring, slot, flag; 1 KiB alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(2 * kStages + 6 + 2 * 8 + 4 + kEpiWarps <= 512 / 8, "barrier area");
@@ -90,9 +91,10 @@ struct Sched {
 };
 
 constexpr int kRing = 8;
-// Readers of each ring slot: the even CTA's MMA thread and 4 epilogue warps,
-// the odd CTA's producer and 4 epilogue warps.
-constexpr int kRingReaders = 10;
+// Readers of each ring slot: the even CTA's MMA thread and epilogue warps, the
+// odd CTA's producer and epilogue warps.
+template <int MODE>
+constexpr int kRingReaders = 2 + 2 * Cfg<MODE>::kEpiWarps;
 
 struct TileRing {
   volatile int* slot;  // [kRing]
@@ -507,7 +509,14 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
   tk.shared_thr = nullptr;
   float gthr = -INFINITY;  // top-k: the row's shared threshold as last read
   static_assert(kTopkCand * 32 * 8 <= kStagingPerWarp, "top-k candidates fit the staging area");
-  float run_m = -INFINITY, run_l = 0.f, run_s = 0.f, z_tgt = 0.f;
+  RowBest best;  // score passes with alternatives
+  best.val = tk.val;
+  best.idx = tk.idx;
+  best.at = best_slot(0, lane);
+  best.thr = best.floor = best.bar = -INFINITY;
+  RowSum sums{-INFINITY, 0.f, 0.f};  // score passes
+  unsigned thr_seen = 0u;  // the row's shared threshold, a tile old
+  float run_m = -INFINITY, run_l = 0.f, z_tgt = 0.f;
   bool found = false;
   int y_fwd = p.ignore_index;
   float ref_row = 0.f;  // forward-store: the row's reference exponent, log2 units
@@ -521,7 +530,9 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
     unsigned thr_key = 0u;
     if (kTop<MODE>) {
       const int row = p.r0 + t.m0 + r;
-      if (p.topk_thr && row < row_end) thr_key = *reinterpret_cast<volatile unsigned*>(p.topk_thr + row);
+      asm volatile("" : "+r"(thr_seen));  // (used from here on: on its way since the last tile)
+      if (MODE == kModeScoreTop && !t.first) thr_key = thr_seen;
+      else if (p.topk_thr && row < row_end) thr_key = *reinterpret_cast<volatile unsigned*>(p.topk_thr + row);
     }
     if (!mbar_wait(&tfull[acc], acc_phase, p.timeout_ns, abort_flag)) {
       record_timeout(p, pr, abort_flag);
@@ -537,7 +548,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
       if (t.first) {
         run_m = -INFINITY;
         run_l = 0.f;
-        if (kScoring<MODE>) run_s = 0.f;
+        if (kScoring<MODE>) sums = RowSum{-INFINITY, 0.f, 0.f};
         found = false;
         y_fwd = (row < row_end) ? label_at(p.labels, row, p.shift, p.seq_len, p.ignore_index) : p.ignore_index;
         if (MODE == kModeFwdStore) ref_row = (row < p.n) ? p.mref[row] : 0.f;
@@ -546,12 +557,27 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
           tk.thr = -INFINITY;
           tk.shared_thr = (p.topk_thr && row < row_end) ? p.topk_thr + row : nullptr;
         }
+        if (MODE == kModeScoreTop) {
+          best.at = best_slot(0, lane);
+          best.floor = -INFINITY;
+          // (a row past the end is all zeros: equal values, each of which would be ranked)
+          best.thr = row < row_end ? -INFINITY : INFINITY;
+        }
       }
-      if (kTop<MODE> && tk.shared_thr) gthr = topk_unkey(thr_key);
+      if (MODE == kModeTopk && tk.shared_thr) gthr = topk_unkey(thr_key);
+      if (MODE == kModeScoreTop) {
+        if (tk.shared_thr) {
+          best.floor = fmaxf(best.floor, topk_unkey(thr_key));
+          thr_seen = *reinterpret_cast<volatile unsigned*>(tk.shared_thr);  // for the next tile
+        }
+        set_bar(best);
+      }
       if (MODE == kModeScoreTop && t.first) {
-        const float t0 = first_floor<4>(tbase, min(kBN, p.v - t.n0), p.topk_k);
-        if (t0 > gthr) {
-          gthr = t0;
+        const int at = ehalf * kChunkCols * 32;  // this warp's columns
+        const float t0 = first_floor<kChunkCols / 2>(tbase + at, min(kChunkCols * 32, p.v - t.n0 - at), p.topk_k);
+        if (t0 > best.floor) {
+          best.floor = t0;
+          set_bar(best);
           if (tk.shared_thr) atomicMax(tk.shared_thr, topk_key(t0));
         }
       }
@@ -560,7 +586,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
         // the tile's 16 disjoint 16-column groups holds its max, so at least kTopkMax
         // values of the row are >= the smallest of those maxima, and nothing below it
         // can be among the row's best kTopkMax.  Raise the row's threshold to it.
-        static_assert(kChunkCols * 2 >= kTopkMax, "one warp sees kTopkMax column groups of a tile");
+        static_assert(MODE != kModeTopk || kChunkCols * 2 >= kTopkMax, "one warp sees kTopkMax column groups of a tile");
         float t0 = INFINITY;
 #pragma unroll 1
         for (int c = ehalf * kChunkCols; c < ehalf * kChunkCols + kTopkMax / 2; ++c) {
@@ -611,6 +637,14 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
             for (int j = 0; j < kW; ++j)
               if (j >= nv) v[j] = __float_as_uint(-INFINITY);
           }
+          if constexpr (kScoring<MODE>) {
+            float gmax[4];
+            const float cmax = block_maxima(v, gmax);
+            add_chunk(sums, v, cmax, zs);
+            if (MODE == kModeScoreTop && append_chunk(best, v, gmax, cmax, col0, lane, p.topk_k) && tk.shared_thr)
+              atomicMax(tk.shared_thr, topk_key(best.floor));
+            continue;
+          }
           constexpr int kBlocks = kW / 8;
           float gmax[kBlocks];  // maxima of the group's 8-column blocks
 #pragma unroll
@@ -622,30 +656,13 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
           float cmax = gmax[0];
 #pragma unroll
           for (int hh = 1; hh < kBlocks; ++hh) cmax = fmaxf(cmax, gmax[hh]);
-          const float new_m = fmaxf(run_m, cmax * zs);
+          const float new_m = fmaxf(run_m, cmax * kLog2e);
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
-          if (kScoring<MODE>) {
-            // beside sum e = sum 2^(t - m), the entropy's sum e (t - m): entropy = ln l - ln 2 (that / l),
-            // two terms of like sign, where lse - sum p z would cancel
-            float e4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < kW; ++j) {
-              const float u = max_nan(fmaf(__uint_as_float(v[j]), zs, -new_m), kNoLogit);
-              const float w = fast_exp2(u);
-              s4[j & 3] += w;
-              e4[j & 3] = fmaf(w, u, e4[j & 3]);
-            }
-            const float d = max_nan(run_m - new_m, kNoLogit);
-            const float f = fast_exp2(d);
-            run_s = f * fmaf(run_l, d, run_s) + ((e4[0] + e4[1]) + (e4[2] + e4[3]));
-            run_l = run_l * f + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-          } else {
-#pragma unroll
-            for (int j = 0; j < kW; ++j) s4[j & 3] += fast_exp2(fmaf(__uint_as_float(v[j]), kLog2e, -new_m));
-            run_l = run_l * fast_exp2(run_m - new_m) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-          }
+          for (int j = 0; j < kW; ++j) s4[j & 3] += fast_exp2(fmaf(__uint_as_float(v[j]), kLog2e, -new_m));
+          run_l = run_l * fast_exp2(run_m - new_m) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
           run_m = new_m;
-          if (kTop<MODE>) {
+          if (MODE == kModeTopk) {
             // blocks of 8: a buffer holding at most kTopkCand - 8 never overflows, and a
             // lane is compacted only once it has gathered more than that
             // a value must beat this range's own 16th best (ids grow along the range, so an
@@ -666,21 +683,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
                   }
                   tk.count += keep ? 1 : 0;
                 }
-                if constexpr (MODE == kModeScoreTop) {
-                  if (__any_sync(0xffffffffu, tk.count > kTopkCand - 8)) {
-                    Trimmed tr = topk_trim(tk.val, tk.idx, tk.count, lane, p.topk_k, gthr);
-                    if (tr.thr > gthr) {
-                      gthr = tr.thr;
-                      if (tk.shared_thr) atomicMax(tk.shared_thr, topk_key(gthr));
-                    }
-                    // (many equal values: ranked)
-                    tr = topk_cut(tk.val, tk.idx, tr.count, tk.thr, lane, p.topk_k, kTopkCand - 8);
-                    tk.count = tr.count;
-                    tk.thr = tr.thr;
-                  }
-                } else {
-                  topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > kTopkCand - 8), p.topk_k);
-                }
+                topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > kTopkCand - 8), p.topk_k);
               }
             }
           }
@@ -758,25 +761,23 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
       }
       if (MODE == kModeTopk && t.last)
         topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > p.topk_k), p.topk_k);
-      if (MODE == kModeScoreTop && t.last && __any_sync(0xffffffffu, tk.count > p.topk_k)) {
-        tk.count = topk_trim(tk.val, tk.idx, tk.count, lane, p.topk_k, gthr).count;
-        tk.count = topk_cut(tk.val, tk.idx, tk.count, tk.thr, lane, p.topk_k, p.topk_k).count;
-      }
+      if (MODE == kModeScoreTop && t.last && __any_sync(0xffffffffu, best.at >= 32 * (p.topk_k + 1)))
+        trim_best(best, lane, p.topk_k, p.topk_k);
       if (t.last && row < row_end) {
         const int osplit = (Cfg<MODE>::kEpiWarps == 8) ? 2 * t.split + ehalf : t.split;
         const int64_t pi = static_cast<int64_t>(osplit) * p.n + row;
         if (in_bounds(pi, p.part_count, p.status)) {
-          p.part_m[pi] = run_m;
-          p.part_l[pi] = run_l;
-          if (kScoring<MODE>) p.part_s[pi] = run_s;
+          p.part_m[pi] = kScoring<MODE> ? sums.m : run_m;
+          p.part_l[pi] = kScoring<MODE> ? sums.l : run_l;
+          if (kScoring<MODE>) p.part_s[pi] = sums.es;
         }
         if (found && in_bounds(row, p.n, p.status)) p.tgt[row] = z_tgt;
         if (MODE == kModeScoreTop) {
-          const int64_t base = (static_cast<int64_t>(row) * p.vsplit + t.split) * p.topk_k;
+          const int64_t base = (static_cast<int64_t>(row) * (Cfg<MODE>::kEpiWarps / 4 * p.vsplit) + osplit) * p.topk_k;
           for (int i = 0; i < p.topk_k; ++i) {
             if (!in_bounds(base + i, p.topk_count, p.status)) break;
             p.topk_keys[base + i] =
-                i < tk.count ? candidate_key(tk.val[topk_slot(i, lane)], tk.idx[topk_slot(i, lane)]) : 0;
+                i < best.at >> 5 ? candidate_key(best.val[best_slot(i, lane)], best.idx[best_slot(i, lane)]) : 0;
           }
         }
         if (MODE == kModeTopk) {
@@ -1017,7 +1018,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<MODE>::kThreads,
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&ring.full[i], 1);
-      mbar_init(&ring.empty[i], kRingReaders);
+      mbar_init(&ring.empty[i], kRingReaders<MODE>);
     }
     for (int i = 0; i < Cfg<MODE>::kEpiWarps; ++i) mbar_init(&ebar[i], 1);
     *abort_flag = 0;
@@ -1991,6 +1992,8 @@ __global__ void bounds_selftest_kernel(int* status) {
 
 int tc_smem_bytes() { return Cfg<kModeForward>::kSmemBytes; }
 int tc_topk_subranges() { return Cfg<kModeTopk>::kEpiWarps / 4; }
+static_assert(Cfg<kModeScore>::kEpiWarps == 4 * kScoreSub && Cfg<kModeScoreTop>::kEpiWarps == 4 * kScoreSub,
+              "sub-ranges of a score launch");
 
 template <int MODE>
 static cudaError_t launch_mode(const TcMaps& maps, const TcParams& p, int grid, cudaStream_t stream) {
@@ -2147,7 +2150,8 @@ cudaError_t launch_score_finalize(int n, int v, int nsplit, int k, LabelView lv,
   auto* kernel = per <= 4    ? score_finalize_kernel<4>
                  : per <= 8  ? score_finalize_kernel<8>
                  : per <= 20 ? score_finalize_kernel<20>
-                             : score_finalize_kernel<kScoreSplitMax * kTopkMax / 32>;
+                 : per <= 40 ? score_finalize_kernel<40>
+                             : score_finalize_kernel<kScoreSub * kScoreSplitMax * kTopkMax / 32>;
   return launch_k(kernel, dim3((n + 7) / 8), dim3(256), 0, stream, n, v, nsplit, k, lv, zscale, part_m, part_l, part_s,
                   tgt, cand_keys, logprob, entropy, lse, top_ids, top_logprobs, status);
 }

@@ -50,6 +50,14 @@ struct TopkBuf {
 // lane's whole buffer (entry e by lane e), both touch 32 different banks.
 __device__ __forceinline__ int topk_slot(int e, int l) { return e * 32 + (l ^ e); }
 
+// The same word where lanes append at their own pace and hardly ever read each other's buffer
+// (the score passes): lane l's entries stay in bank l.
+__device__ __forceinline__ int best_slot(int e, int l) { return e * 32 + l; }
+template <bool OWN_BANK>
+__device__ __forceinline__ int buffer_slot(int e, int l) {
+  return OWN_BANK ? best_slot(e, l) : topk_slot(e, l);
+}
+
 // Order-preserving map of a float to an unsigned (0 stands below every float).
 __device__ __forceinline__ unsigned topk_key(float f) {
   const unsigned b = __float_as_uint(f);
@@ -82,14 +90,15 @@ __device__ __forceinline__ int count_reaching(const float (&v)[32], float at) {
 // buffer; its rank (how many entries beat it) comes from 32 independent shuffle
 // rounds, and the best `keep` go to slots 0..keep-1 in rank order.  Entries are
 // distinct (value, id) pairs, so the ranks of the filled slots are distinct.
+template <bool OWN_BANK = false>
 __device__ __forceinline__ void topk_compact_lanes(TopkBuf& b, int lane, unsigned mask, int keep) {
   while (mask) {
     const int L = __ffs(mask) - 1;
     mask &= mask - 1;
     const int cnt = __shfl_sync(0xffffffffu, b.count, L);
     const bool filled = lane < cnt;
-    const float v = filled ? b.val[topk_slot(lane, L)] : -INFINITY;
-    const int i = filled ? b.idx[topk_slot(lane, L)] : -1;
+    const float v = filled ? b.val[buffer_slot<OWN_BANK>(lane, L)] : -INFINITY;
+    const int i = filled ? b.idx[buffer_slot<OWN_BANK>(lane, L)] : -1;
     int rank = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -99,8 +108,8 @@ __device__ __forceinline__ void topk_compact_lanes(TopkBuf& b, int lane, unsigne
     }
     __syncwarp();  // every entry is in registers before the slots are rewritten
     if (filled && rank < keep) {
-      b.val[topk_slot(rank, L)] = v;
-      b.idx[topk_slot(rank, L)] = i;
+      b.val[buffer_slot<OWN_BANK>(rank, L)] = v;
+      b.idx[buffer_slot<OWN_BANK>(rank, L)] = i;
     }
     const unsigned at_k = __ballot_sync(0xffffffffu, filled && rank == keep - 1);
     const float kth = __shfl_sync(0xffffffffu, v, at_k ? __ffs(at_k) - 1 : 0);
@@ -183,7 +192,7 @@ static __device__ __noinline__ Trimmed topk_trim(float* val, int* idx, int count
   }
 #pragma unroll
   for (int e = 0; e < kTopkCand; ++e) {
-    v[e] = e < count ? val[topk_slot(e, lane)] : -INFINITY;
+    v[e] = e < count ? val[best_slot(e, lane)] : -INFINITY;
     if (e < count) lo4[e & 3] = fminf(lo4[e & 3], v[e]);
     hi4[e & 3] = fmaxf(hi4[e & 3], v[e]);
   }
@@ -199,14 +208,14 @@ static __device__ __noinline__ Trimmed topk_trim(float* val, int* idx, int count
   }
   int id[kTopkCand];  // read whole before anything is rewritten
 #pragma unroll
-  for (int e = 0; e < kTopkCand; ++e) id[e] = idx[topk_slot(e, lane)];
+  for (int e = 0; e < kTopkCand; ++e) id[e] = idx[best_slot(e, lane)];
   int at = 0;
 #pragma unroll
   for (int e = 0; e < kTopkCand; ++e) {
     const bool keep = e < count && v[e] >= lo;
     if (keep) {
-      val[topk_slot(at, lane)] = v[e];
-      idx[topk_slot(at, lane)] = id[e];
+      val[best_slot(at, lane)] = v[e];
+      idx[best_slot(at, lane)] = id[e];
     }
     at += keep ? 1 : 0;
   }
@@ -222,8 +231,113 @@ static __device__ __noinline__ Trimmed topk_cut(float* val, int* idx, int count,
   b.count = count;
   b.thr = thr;
   b.shared_thr = nullptr;
-  topk_compact_lanes(b, lane, __ballot_sync(0xffffffffu, count > most), k);
+  topk_compact_lanes<true>(b, lane, __ballot_sync(0xffffffffu, count > most), k);
   return Trimmed{b.count, b.thr};
+}
+
+// ----------------------------------------------------------------------------- a row's walk over its logits
+
+// Softmax statistics of the logits seen so far, in log2 units: the maximum m, l = sum 2^(t - m)
+// and es = sum 2^(t - m) (t - m).  entropy = ln l - ln 2 (es / l): two terms of like sign, where
+// lse - sum p z would cancel.
+struct RowSum {
+  float m, l, es;
+};
+
+// Maxima of 32 logits' blocks of 8, and of all.
+__device__ __forceinline__ float block_maxima(const uint32_t (&v)[32], float (&gmax)[4]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const auto x = [&](int j) { return __uint_as_float(v[8 * g + j]); };
+    gmax[g] = fmaxf(fmaxf(fmaxf(fmaxf(x(0), x(1)), x(2)), fmaxf(fmaxf(x(3), x(4)), x(5))), fmaxf(x(6), x(7)));
+  }
+  return fmaxf(fmaxf(gmax[0], gmax[1]), fmaxf(gmax[2], gmax[3]));
+}
+
+// 32 logits, the largest of them cmax (in their own units), zs log2 units each.  3 instructions
+// a logit (two at a time but for 2^u), where logits of minus infinity would make 0 * infinity:
+// the NaN that it leaves is the sign to take them one by one.
+__device__ __forceinline__ void add_chunk(RowSum& r, const uint32_t (&v)[32], float cmax, float zs) {
+  const float new_m = fmaxf(r.m, cmax * zs);
+  const float2 scale = both(zs), back = both(-new_m);
+  float2 s2[2] = {}, e2[2] = {};
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float2 u = fma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), scale, back);
+    const float2 w = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+    s2[j & 1] = add2(s2[j & 1], w);
+    e2[j & 1] = fma2(w, u, e2[j & 1]);
+  }
+  const float2 st = add2(s2[0], s2[1]), et = add2(e2[0], e2[1]);
+  float s = st.x + st.y, e = et.x + et.y;
+  if (!(e == e)) {
+    const float from = new_m == -INFINITY ? 0.f : new_m;  // nothing but minus infinity so far: adds 0
+    s = e = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float u = max_nan(fmaf(__uint_as_float(v[j]), zs, -from), kNoLogit);
+      const float w = fast_exp2(u);
+      s += w;
+      e = fmaf(w, u, e);
+    }
+  }
+  const float d = fmaxf(r.m - new_m, kNoLogit);  // (minus infinity twice: the sums are 0 or NaN)
+  const float f = fast_exp2(d);
+  r.es = f * fmaf(r.l, d, r.es) + e;
+  r.l = r.l * f + s;
+  r.m = new_m;
+}
+
+// The float below f: x > it exactly where x >= f.
+__device__ __forceinline__ float float_below(float f) {
+  if (f == -INFINITY) return f;
+  return topk_unkey(topk_key(f == 0.f ? -0.f : f) - 1u);
+}
+
+// A lane's candidates for its row's best k.
+struct RowBest {
+  float* val;  // [kTopkCand][32], the warp's
+  int* idx;
+  int at;       // count * 32 + lane: where the next one goes
+  float thr;    // the range's own k-th best, once it is known: ids grow, so an equal later value is out
+  float floor;  // nothing below it is among the row's best
+  float bar;    // what a candidate passes: both in one
+};
+__device__ __forceinline__ void set_bar(RowBest& b) { b.bar = b.floor > b.thr ? float_below(b.floor) : b.thr; }
+
+// Trims every lane to about k, and ranks the lanes that stay above `most`.
+__device__ __forceinline__ void trim_best(RowBest& b, int lane, int k, int most) {
+  Trimmed t = topk_trim(b.val, b.idx, b.at >> 5, lane, k, b.floor);
+  b.floor = t.thr;
+  t = topk_cut(b.val, b.idx, t.count, b.thr, lane, k, most);  // (many equal values)
+  b.at = best_slot(t.count, lane);
+  b.thr = t.thr;
+  set_bar(b);
+}
+
+// Appends what passes the bar of 32 logits that start at id col0 (whole-warp call): 5
+// instructions a logit in the blocks of 8 where any lane's passes.  A buffer that holds at
+// most kTopkCand - 8 does not overflow.  Returns whether the lane's floor rose.
+__device__ __forceinline__ bool append_chunk(RowBest& b, const uint32_t (&v)[32], const float (&gmax)[4], float cmax,
+                                             int col0, int lane, int k) {
+  const float floor0 = b.floor;
+  if (!__any_sync(0xffffffffu, cmax > b.bar)) return false;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (!__any_sync(0xffffffffu, gmax[g] > b.bar)) continue;
+#pragma unroll
+    for (int j = 8 * g; j < 8 * g + 8; ++j) {
+      const float x = __uint_as_float(v[j]);
+      const bool keep = x > b.bar;
+      if (keep) {  // predicated stores, no branch
+        b.val[b.at] = x;
+        b.idx[b.at] = col0 + j;
+      }
+      b.at += keep ? 32 : 0;
+    }
+    if (__any_sync(0xffffffffu, b.at >= 32 * (kTopkCand - 7))) trim_best(b, lane, k, kTopkCand - 8);
+  }
+  return b.floor > floor0;
 }
 
 }  // namespace flce
