@@ -346,10 +346,11 @@ __device__ void decode_epilogue_few(const DecodeParams& p, Range r, float* logit
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const float new_m = fmaxf(m[q], top * p.zscale);
+      const float from = new_m == -INFINITY ? 0.f : new_m;  // nothing but minus infinity so far: adds 0
       float sl = 0.f, se = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float u = max_nan(fmaf(v[j], p.zscale, -new_m), kNoLogit);
+        const float u = max_nan(fmaf(v[j], p.zscale, -from), kNoLogit);
         const float w = fast_exp2(u);
         sl += w;
         se = fmaf(w, u, se);
@@ -359,7 +360,7 @@ __device__ void decode_epilogue_few(const DecodeParams& p, Range r, float* logit
         sl += __shfl_xor_sync(0xffffffffu, sl, o);
         se += __shfl_xor_sync(0xffffffffu, se, o);
       }
-      const float d = max_nan(m[q] - new_m, kNoLogit);
+      const float d = fmaxf(m[q] - new_m, kNoLogit);  // (minus infinity twice: the sums are 0 or NaN)
       const float f = fast_exp2(d);
       es[q] = f * fmaf(l[q], d, es[q]) + se;
       l[q] = l[q] * f + sl;

@@ -236,6 +236,24 @@ def test_an_infinite_weight_bans_its_token(n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 8, 40, 100, 260])
+@pytest.mark.parametrize("v,banned", [(3000, 700), (90000, 40000)])
+def test_whole_ranges_of_banned_tokens(n, v, banned):
+    """Blocks of logits that are all minus infinity, first or last in a range: they add nothing."""
+    x, w, tok = grid_inputs(n, 64, v, seed=3, ties=False)
+    x[:, 0] = 1.0
+    w2 = w.clone()
+    w2[:banned, 0] = w2[v - 300:, 0] = -float("inf")
+    tok[:] = banned + 5
+    r, _ = flce.logprobs_forward(x, w2, tok, top=4, check=True)
+    ref = reference(x, w[banned:v - 300], tok - banned, 4, 1.0)
+    base = (v / 128 + 116) * U
+    within(r.lse, ref["lse"], base + 6 * U * ref["lse"].abs(), "lse")
+    within(r.entropy, ref["entropy"], base * (1 + ref["dist"]) + 8 * U * (ref["entropy"] + ref["dist"]), "entropy")
+    assert torch.equal(r.top_ids.long(), ref["ids"] + banned)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [4, 100, 600])
 @pytest.mark.parametrize("bad", [3000, -1, -101, 2 ** 31 - 1])
 def test_tokens_out_of_range_are_reported(n, bad):
