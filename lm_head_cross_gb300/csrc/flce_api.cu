@@ -1036,6 +1036,7 @@ flce_status_t run_score(const flce_problem_t& p, int k, float inv_temp, const vo
   tp.inv_temp = inv_temp;
   tp.tile_counter = reinterpret_cast<int*>(ws) + 1;
   tp.part_count = static_cast<int64_t>(L.splits) * kScoreSub * p.n;
+  const int sub = score_subranges(p.h, k);
   if (k > 0) {
     tp.topk_thr = reinterpret_cast<unsigned*>(ws + L.thr);
     tp.topk_keys = reinterpret_cast<uint64_t*>(ws + L.cand);
@@ -1045,12 +1046,12 @@ flce_status_t run_score(const flce_problem_t& p, int k, float inv_temp, const vo
   const double flops = 2.0 * static_cast<double>(p.n) * static_cast<double>(p.v) * static_cast<double>(p.h);
   const int grid = pair_grid(dev.sms, static_cast<long long>(tp.row_tiles) * tp.vsplit);
   flce_status_t st = cuda_status(timed(0, flops, stream, [&] {
-    return launch_tc(k > 0 ? kModeScoreTop : kModeScore, maps, tp, grid, stream);
+    return launch_tc(k == 0 ? kModeScore : sub == 2 ? kModeScoreTopWide : kModeScoreTop, maps, tp, grid, stream);
   }));
   if (st != FLCE_OK) return st;
   const LabelView lv{tokens, p.ignore_index, p.shift, p.shift ? p.seq_len : 1, nullptr, nullptr, 0};
   return cuda_status(timed(3, 0.0, stream, [&] {
-    return launch_score_finalize(tp.n, tp.v, kScoreSub * tp.vsplit, k, lv, tp.zscale, tp.part_m, tp.part_l, tp.part_s, tp.tgt,
+    return launch_score_finalize(tp.n, tp.v, sub * tp.vsplit, k, lv, tp.zscale, tp.part_m, tp.part_l, tp.part_s, tp.tgt,
                                  tp.topk_keys, logprob, entropy, lse, top_ids, top_logprobs, tp.status, stream);
   }));
 }

@@ -47,6 +47,7 @@ enum Mode : int {
   kModeScore = 5,      // forward with the entropy's sum, at a temperature
   kModeScoreTop = 6,   // the same with each row's best logits
   kModeGradScore = 7,  // G of the gradients of token log probabilities and entropies
+  kModeScoreTopWide = 8,  // kModeScoreTop with eight epilogue warps (see score_subranges)
 };
 
 // Forward-store: a row's p~ is stored relative to its reference logit (log2
@@ -234,7 +235,12 @@ cudaError_t launch_soft_chunk_targets(int n, int k, const int32_t* soft_idx, con
 //
 // Most splits of an n-row score pass: enough that one row tile's ranges occupy every CTA
 // pair (76 on this GPU), 16 (as for the top-k pass) from ten row tiles on.
-constexpr int kScoreSub = 2;  // sub-ranges that a score launch reports for each vocabulary split
+constexpr int kScoreSub = 2;  // most sub-ranges that a score launch reports for each vocabulary split
+// Those that it does: two, of eight epilogue warps, but with alternatives only where a tile's
+// contraction is too short to hide the epilogue of four.  Four warps and eight (us), 777 rows x
+// 40009 ids, k = 16: H = 256 101 and 94, 1024 110 and 103, 1544 123 and 128, 4096 206 and 214;
+// 8192 x 32000, k = 8: H = 256 360 and 300, 1024 398 and 382, 2048 626 and 634, 4096 1227 and 1253.
+inline int score_subranges(int64_t h, int k) { return k == 0 || h <= 1024 ? 2 : 1; }
 inline int score_splits(int64_t n) {
   const int64_t row_tiles = (n + kPairRows - 1) / kPairRows;
   const int64_t s = row_tiles > 0 ? 2 * kScoreSplitMax / row_tiles : kScoreSplitMax;

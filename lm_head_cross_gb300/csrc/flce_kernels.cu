@@ -59,15 +59,15 @@ constexpr uint16_t kPairMask = 0x3;
 
 // Per-mode shape of a CTA: epilogue warps (4, or 8 as two per TMEM lane
 // quarter, each on half of a tile's columns, reported as two vocabulary
-// sub-ranges) and ring stages.  Every mode runs 4 and the full ring: eight
-// top-k epilogue warps with five stages were 5% faster at H = 2048 and 5%
-// slower at H = 4096.
+// sub-ranges) and ring stages.  Most run 4 and the full ring: eight top-k
+// epilogue warps with five stages were 5% faster at H = 2048 and 5% slower at
+// H = 4096.  The score pass, which needs no staging, runs 8; with alternatives,
+// whose buffers take a stage for 8 warps, there are both (see score_subranges).
 template <int MODE>
 struct Cfg {
-  static constexpr bool kScore = MODE == kModeScore || MODE == kModeScoreTop;
-  static constexpr int kEpiWarps = kScore ? 8 : 4;
+  static constexpr int kEpiWarps = MODE == kModeScore || MODE == kModeScoreTopWide ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kStages = MODE == kModeScoreTop ? flce::kStages - 1 : flce::kStages;
+  static constexpr int kStages = MODE == kModeScoreTopWide ? flce::kStages - 1 : flce::kStages;
   static constexpr int kSmemStagingOff = kStages * kStageBytes;
   static constexpr int kSmemBarOff = kSmemStagingOff + (MODE == kModeScore ? 0 : kEpiWarps * kStagingPerWarp);
   static constexpr int kSmemBytes = kSmemBarOff + 512 + 1024;  // barriers, ring, slot, flag; 1 KiB alignment slack
@@ -109,9 +109,11 @@ struct Pair {
 };
 
 template <int MODE>
-constexpr bool kScoring = (MODE == kModeScore || MODE == kModeScoreTop);
+constexpr bool kScoreTop = (MODE == kModeScoreTop || MODE == kModeScoreTopWide);
 template <int MODE>
-constexpr bool kTop = (MODE == kModeTopk || MODE == kModeScoreTop);
+constexpr bool kScoring = (MODE == kModeScore || kScoreTop<MODE>);
+template <int MODE>
+constexpr bool kTop = (MODE == kModeTopk || kScoreTop<MODE>);
 template <int MODE>
 constexpr bool kGrad = (MODE == kModeGrad || MODE == kModeGradScore);
 template <int MODE>
@@ -531,7 +533,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
     if (kTop<MODE>) {
       const int row = p.r0 + t.m0 + r;
       asm volatile("" : "+r"(thr_seen));  // (used from here on: on its way since the last tile)
-      if (MODE == kModeScoreTop && !t.first) thr_key = thr_seen;
+      if (kScoreTop<MODE> && !t.first) thr_key = thr_seen;
       else if (p.topk_thr && row < row_end) thr_key = *reinterpret_cast<volatile unsigned*>(p.topk_thr + row);
     }
     if (!mbar_wait(&tfull[acc], acc_phase, p.timeout_ns, abort_flag)) {
@@ -557,7 +559,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
           tk.thr = -INFINITY;
           tk.shared_thr = (p.topk_thr && row < row_end) ? p.topk_thr + row : nullptr;
         }
-        if (MODE == kModeScoreTop) {
+        if (kScoreTop<MODE>) {
           best.at = best_slot(0, lane);
           best.floor = -INFINITY;
           // (a row past the end is all zeros: equal values, each of which would be ranked)
@@ -565,14 +567,14 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
         }
       }
       if (MODE == kModeTopk && tk.shared_thr) gthr = topk_unkey(thr_key);
-      if (MODE == kModeScoreTop) {
+      if (kScoreTop<MODE>) {
         if (tk.shared_thr) {
           best.floor = fmaxf(best.floor, topk_unkey(thr_key));
           thr_seen = *reinterpret_cast<volatile unsigned*>(tk.shared_thr);  // for the next tile
         }
         set_bar(best);
       }
-      if (MODE == kModeScoreTop && t.first) {
+      if (kScoreTop<MODE> && t.first) {
         const int at = ehalf * kChunkCols * 32;  // this warp's columns
         const float t0 = first_floor<kChunkCols / 2>(tbase + at, min(kChunkCols * 32, p.v - t.n0 - at), p.topk_k);
         if (t0 > best.floor) {
@@ -641,7 +643,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
             float gmax[4];
             const float cmax = block_maxima(v, gmax);
             add_chunk(sums, v, cmax, zs);
-            if (MODE == kModeScoreTop && append_chunk(best, v, gmax, cmax, col0, lane, p.topk_k) && tk.shared_thr)
+            if (kScoreTop<MODE> && append_chunk(best, v, gmax, cmax, col0, lane, p.topk_k) && tk.shared_thr)
               atomicMax(tk.shared_thr, topk_key(best.floor));
             continue;
           }
@@ -761,7 +763,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
       }
       if (MODE == kModeTopk && t.last)
         topk_compact_lanes(tk, lane, __ballot_sync(0xffffffffu, tk.count > p.topk_k), p.topk_k);
-      if (MODE == kModeScoreTop && t.last && __any_sync(0xffffffffu, best.at >= 32 * (p.topk_k + 1)))
+      if (kScoreTop<MODE> && t.last && __any_sync(0xffffffffu, best.at >= 32 * (p.topk_k + 1)))
         trim_best(best, lane, p.topk_k, p.topk_k);
       if (t.last && row < row_end) {
         const int osplit = (Cfg<MODE>::kEpiWarps == 8) ? 2 * t.split + ehalf : t.split;
@@ -772,7 +774,7 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
           if (kScoring<MODE>) p.part_s[pi] = sums.es;
         }
         if (found && in_bounds(row, p.n, p.status)) p.tgt[row] = z_tgt;
-        if (MODE == kModeScoreTop) {
+        if (kScoreTop<MODE>) {
           const int64_t base = (static_cast<int64_t>(row) * (Cfg<MODE>::kEpiWarps / 4 * p.vsplit) + osplit) * p.topk_k;
           for (int i = 0; i < p.topk_k; ++i) {
             if (!in_bounds(base + i, p.topk_count, p.status)) break;
@@ -1992,7 +1994,8 @@ __global__ void bounds_selftest_kernel(int* status) {
 
 int tc_smem_bytes() { return Cfg<kModeForward>::kSmemBytes; }
 int tc_topk_subranges() { return Cfg<kModeTopk>::kEpiWarps / 4; }
-static_assert(Cfg<kModeScore>::kEpiWarps == 4 * kScoreSub && Cfg<kModeScoreTop>::kEpiWarps == 4 * kScoreSub,
+static_assert(Cfg<kModeScore>::kEpiWarps == 8 && Cfg<kModeScoreTop>::kEpiWarps == 4 &&
+                  Cfg<kModeScoreTopWide>::kEpiWarps == 8 && kScoreSub == 2,
               "sub-ranges of a score launch");
 
 template <int MODE>
@@ -2018,6 +2021,7 @@ cudaError_t launch_tc(int mode, const TcMaps& maps, const TcParams& p, int grid,
     case kModeTopk: return launch_mode<kModeTopk>(maps, p, grid, stream);
     case kModeScore: return launch_mode<kModeScore>(maps, p, grid, stream);
     case kModeScoreTop: return launch_mode<kModeScoreTop>(maps, p, grid, stream);
+    case kModeScoreTopWide: return launch_mode<kModeScoreTopWide>(maps, p, grid, stream);
     case kModeGradScore: return launch_mode<kModeGradScore>(maps, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }

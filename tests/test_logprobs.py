@@ -107,6 +107,7 @@ CASES = [
     (128, 512, 257, 5, 1.0), (129, 512, 4097, 16, 0.7), (200, 256, 40009, 7, 1.0), (256, 128, 1024, 16, 1.0),
     (257, 512, 4099, 16, 2.0), (513, 128, 777, 0, 1.0), (777, 264, 40009, 16, 1.3), (1000, 64, 2050, 1, 1.0),
     (2600, 72, 5001, 16, 1.0), (3000, 2048, 1023, 0, 0.7),
+    (300, 2056, 5003, 16, 1.0), (700, 1032, 9001, 8, 1.3), (135, 4096, 3001, 3, 1.0),
     (20, 72, 50001, 0, 1.0), (40, 72, 50001, 16, 1.0), (20, 4104, 39001, 16, 0.7), (60, 4096, 39001, 0, 1.0),
 ]
 
