@@ -263,7 +263,12 @@ __device__ __noinline__ void step_unit_scalar(const AdamwTensor& t, const StepSc
 }
 
 // One block per chunk of 16 units, two units a warp; a unit is 256 elements, the block of
-// one 8-bit scale, so its largest magnitudes are two warp reductions.
+// one 8-bit scale, so its largest magnitudes are two warp reductions.  All of a warp's loads
+// (two units: 96 to 160 bytes a lane) go out before its first operation.  Bound by its
+// streams, each byte once: 525 M parameters in bf16 with fp32 masters and 8-bit moments (16
+// bytes each) in 1257 us, 6.7 TB/s; 149 tensors of 56 M parameters with 32-bit moments (28
+// bytes each) in 227 us, 6.9 TB/s.  With 8-bit moments the arithmetic takes 85% of the issue
+// slots, with 32-bit ones 27%.
 template <int N, int BITS>
 __global__ void __launch_bounds__(kAdamwThreads) adamw_kernel(const __grid_constant__ AdamwArgs<N> a) {
   griddep_begin();

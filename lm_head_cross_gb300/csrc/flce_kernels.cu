@@ -15,6 +15,9 @@
 //                  and their ids per vocabulary range.
 //   kModeScore     the forward with the entropy's sum beside the sum of exponentials,
 //                  at a temperature; kModeScoreTop also keeps each row's best logits.
+//                  Bound by the contraction from H = 2048 (8192 x 2048 x 32000 552 us, 1.95
+//                  PFLOP/s; with 8 alternatives 1.72), by the epilogue below H = 1024 (8192 x
+//                  256 x 32000 138 us without alternatives, 300 with 8; the contraction is 69).
 //   kModeGrad      recomputes S for one vocabulary chunk and writes
 //                  G = s (exp(S - lse) - onehot) valid as bf16; kModeGradScore the G of
 //                  token log probabilities and entropies.
@@ -1671,6 +1674,7 @@ __global__ void __launch_bounds__(256) topk_finalize_kernel(int n, int nsub, int
   }
 }
 
+// Latency of two rounds of loads, 6 to 10 us for 777 to 8192 rows.
 // One warp per row: merges the splits' (max, sum, entropy sum), reads off the label's log
 // probability, and for k > 0 picks the best k of the splits' candidates (kPer of them in
 // each lane's registers).
