@@ -285,7 +285,7 @@ struct FwdPhaseShape {
   static constexpr int kStageBytes = kThreads * VPL * 16;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kSmemBytes = kRingBytes + 8 * kColumns;  // weight and bias in fp32
-  static constexpr int kBlocks = kSmemBytes <= 112 * 1024 && VPL <= 4 ? 2 : 1;  // on one SM
+  static constexpr int kBlocks = kSmemBytes <= 112 * 1024 ? 2 : 1;  // on one SM
 };
 
 // Forward at any phase.  GW warps share a row, kGroups rows in a block at a time; blocks stay,
@@ -946,12 +946,14 @@ cudaError_t norm_forward(const NormForwardArgs& a) {
     const bool earns = a.q.n * a.q.h >= (3 << 20) && a.q.h > (sizeof(T) == 2 ? 128 : 1024);
     if (same_phase<kVec>(a.q) && a.q.n <= (1 << 30) && (earns || a.q.h > kMost)) {
       const int accesses = (a.q.h + 2 * kVec - 2) / kVec;
-      if (accesses <= 32) return norm_forward_phase<T, kVec, 1, 1>(a);
-      if (accesses <= 64) return norm_forward_phase<T, kVec, 1, 2>(a);
-      if (accesses <= 96) return norm_forward_phase<T, kVec, 1, 3>(a);
-      if (accesses <= 128) return norm_forward_phase<T, kVec, 1, 4>(a);
-      if (accesses <= 192) return norm_forward_phase<T, kVec, 2, 3>(a);
-      if (accesses <= 256) return norm_forward_phase<T, kVec, 2, 4>(a);
+      if constexpr (kVec == 8) {  // (fp32 rows are wider)
+        if (accesses <= 32) return norm_forward_phase<T, kVec, 1, 1>(a);
+        if (accesses <= 64) return norm_forward_phase<T, kVec, 1, 2>(a);
+        if (accesses <= 96) return norm_forward_phase<T, kVec, 1, 3>(a);
+        if (accesses <= 128) return norm_forward_phase<T, kVec, 1, 4>(a);
+        if (accesses <= 192) return norm_forward_phase<T, kVec, 2, 3>(a);
+        if (accesses <= 256) return norm_forward_phase<T, kVec, 2, 4>(a);
+      }
       if (accesses <= 384) return norm_forward_phase<T, kVec, 4, 3>(a);
       if (accesses <= 512) return norm_forward_phase<T, kVec, 4, 4>(a);
       if (accesses <= 768) return norm_forward_phase<T, kVec, 8, 3>(a);

@@ -137,7 +137,8 @@ class AdamW:
 
     params: tensors, or groups {"params": [...], "lr": ..., "weight_decay": ...}.  state_bits 32
     or 8.  master_weights: keep fp32 master weights for bf16 parameters (their own rounding
-    would swallow updates smaller than 2^-9 of a weight).  Gradients are read from ``.grad``;
+    would swallow updates smaller than 2^-9 of a weight); the next step overwrites what was
+    written to such a parameter from outside.  Gradients are read from ``.grad``;
     a parameter without one is left alone.
     """
 

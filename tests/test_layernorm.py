@@ -147,6 +147,52 @@ def test_rows_of_a_larger_tensor(dtype, h, pitch, at):
     check_backward(x, w, dy, got[1], got[2], (dx, dweight, dbias))
 
 
+# many rows whose length no 16-byte access divides, at every width of the kernels that take them
+PHASES = [(13000, 250), (8000, 501), (6500, 761), (8193, 137), (8200, 999), (8201, 1501), (9000, 2041), (1600, 2060),
+          (1600, 3001), (1100, 4003), (1027, 5001), (500, 7001)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,h", PHASES)
+@pytest.mark.parametrize("dtype,wdtype", TYPES)
+def test_rows_at_every_phase(n, h, dtype, wdtype):
+    test_forward_and_backward(n, h, dtype, wdtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_of_a_larger_tensor_at_every_phase(dtype):
+    """A pitch that leaves x's rows at the phases of contiguous ones."""
+    n, h, pitch, at = 2100, 2051, 2067, 8
+    _, w, b, dy = (t.cuda() for t in make(n, h, dtype, torch.float32, seed=pitch))
+    big = torch.randn(n, pitch, generator=torch.Generator().manual_seed(at)).to(dtype).cuda()
+    x = big[:, at:at + h]
+    got = flce.layernorm_forward(x, w, b)
+    check_forward(x, w, b, 1e-5, got)
+    dx, dweight, dbias, _ = flce.layernorm_backward(dy, x, w, got[1], got[2])
+    check_backward(x, w, dy, got[1], got[2], (dx, dweight, dbias))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,h", [(2100, 2051), (9000, 509)])
+def test_non_finite_rows_do_not_reach_their_neighbours(dtype, n, h):
+    """An access at a row's start may hold the end of the row before."""
+    x, w, b, dy = (t.cuda() for t in make(n, h, dtype, torch.float32))
+    clean = flce.layernorm_forward(x, w, b)
+    clean_dx = flce.layernorm_backward(dy, x, w, clean[1], clean[2])[0]
+    bad = torch.arange(3, n, 17, device="cuda")
+    x2, dy2 = x.clone(), dy.clone()
+    x2[bad], dy2[bad] = float("nan"), float("inf")
+    got = flce.layernorm_forward(x2, w, b)
+    dx = flce.layernorm_backward(dy2, x2, w, clean[1], clean[2])[0]
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    for a, c in zip(got, clean):
+        assert torch.equal(a[keep], c[keep])
+    assert torch.equal(dx[keep], clean_dx[keep])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("which", ["weight", "dy"])
 def test_unaligned_vectors(which):
