@@ -431,32 +431,11 @@ cudaError_t timed(int kind, double flops, cudaStream_t stream, F&& launch) {
   return e;
 }
 
-// Token log probabilities' backward: chunk width and dX parts.  A wide chunk while its G
-// (n x chunk bf16) stays within 128 MiB, so that few rows need few launches; and where the
-// dX tiles are too few for the GPU's 76 CTA pairs, each tile's sum over the vocabulary cut
-// into parts (at least 512 ids, 64 MiB together), added up in order at the end: 256 x 4096 x
-// 128256 in 753 us, 1424 without either; 100 x 512 x 60000 in 87, 385 without.
-struct ScorePlan {
-  int chunk, parts;
-};
-ScorePlan score_plan(const flce_problem_t& p) {
-  constexpr int64_t kPairs = 76;
-  const int64_t whole = (p.v + 255) / 256 * 256;
-  const int64_t fit = (int64_t{1} << 26) / std::max<int64_t>(p.n, 1) / 256 * 256;
-  const int64_t wide = std::min<int64_t>({fit, int64_t{1} << 17, whole});
-  const int64_t chunk = std::max<int64_t>(std::min<int64_t>(chunk_width(p.n), whole), wide);
-  const int64_t tiles = (p.n + kPairRows - 1) / kPairRows * ((p.h + kBN - 1) / kBN);
-  int64_t parts = tiles < kPairs ? (2 * kPairs + tiles - 1) / tiles : 1;
-  parts = std::min<int64_t>({parts, std::min(chunk, p.v) / 512, (int64_t{1} << 24) / std::max<int64_t>(p.n * p.h, 1)});
-  // fewer than 4 parts save less than the launch that adds them up costs
-  return ScorePlan{static_cast<int>(chunk), static_cast<int>(parts < 4 ? 1 : parts)};
-}
-
 // The bounded layout with that chunk and those parts in place of its last two regions.
 Layout score_backward_layout(const flce_problem_t& p) {
   Layout L = make_layout(p, false);
   if (p.n == 0) return L;
-  const ScorePlan plan = score_plan(p);
+  const ScorePlan plan = score_plan(p.n, p.h, p.v);
   const size_t n = static_cast<size_t>(p.n);
   L.chunk = plan.chunk;
   L.dx_acc = align_up(L.g + 2 * n * static_cast<size_t>(plan.chunk));
@@ -547,7 +526,7 @@ flce_status_t run_forward(const Ctx& c, const void* X, const void* W, const int3
 // Gradients of token log probabilities and entropies: what the grad launches need besides
 // the log probabilities' upstream gradients (grad_rows).
 struct ScoreGrad {
-  int parts;  // of dX
+  ScorePlan plan;
   float inv_temp;
   const float* grad_ent;
   const float* entropy;
@@ -595,13 +574,13 @@ flce_status_t run_backward(const Ctx& c, const void* X, const void* W, const int
   if (!make_map(&bm.b2, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.n, p.h * 2, 64, kBK)) return FLCE_ERR_CUDA;
   if (!make_map(&bm.out2, dW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.v, p.h * 2, 64, 32)) return FLCE_ERR_CUDA;
   // a vocabulary of one chunk: dX needs no accumulator and leaves the tiles as bf16
-  const int parts = score ? score->parts : 1;
+  const ScorePlan plan = score ? score->plan : ScorePlan{chunk, 1, chunk};
+  const int parts = plan.parts;
   const bool one_chunk = dX && p.v <= chunk && parts == 1;
   bm.out = bm.out2;  // with an accumulator unused (a valid map for the prologue's prefetch)
   if (one_chunk && !make_map(&bm.out, dX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.h, p.n, p.h * 2, 64, 32))
     return FLCE_ERR_CUDA;
 
-  int used_parts = 0;  // the first chunk's, which stores; later ones add to as many or fewer
   for (int64_t c0 = 0; c0 < p.v; c0 += chunk) {
     const int cw = static_cast<int>(std::min<int64_t>(chunk, p.v - c0));
     tp.c0 = static_cast<int>(c0);
@@ -631,9 +610,8 @@ flce_status_t run_backward(const Ctx& c, const void* X, const void* W, const int
       return FLCE_ERR_CUDA;
     tp.dw_m_tiles = (cw + kPairRows - 1) / kPairRows;
     tp.dw_tiles = tp.dw_m_tiles * tp.h_tiles;
-    tp.dx_split_k = static_cast<int>((cw + int64_t{kBK} * parts - 1) / (int64_t{kBK} * parts)) * kBK;
-    tp.dx_splits = (cw + tp.dx_split_k - 1) / tp.dx_split_k;  // (a narrow chunk fills fewer)
-    used_parts = std::max(used_parts, tp.dx_splits);
+    tp.dx_split_k = plan.part_k;
+    tp.dx_splits = plan.splits(cw);  // the first chunk's are `parts` and store; a narrower one adds to fewer
     tp.dx_tiles = tp.row_tiles * tp.h_tiles * tp.dx_splits;
     tp.dx_out = one_chunk ? kOutBF16 : c0 > 0 ? kOutF32Add : kOutF32Store;
     tp.dx_f32 = dx_acc;
@@ -660,7 +638,7 @@ flce_status_t run_backward(const Ctx& c, const void* X, const void* W, const int
   if (!dX || one_chunk) return FLCE_OK;
   if (parts > 1)
     return cuda_status(timed(3, 0.0, c.stream, [&] {
-      return launch_sum_parts_bf16(dx_acc, used_parts, dX, p.n * p.h, c.stream);
+      return launch_sum_parts_bf16(dx_acc, parts, dX, p.n * p.h, c.stream);
     }));
   return cuda_status(timed(3, 0.0, c.stream, [&] { return launch_convert_bf16(dx_acc, dX, p.n * p.h, c.stream); }));
 }
@@ -1168,7 +1146,6 @@ flce_status_t adamw_launches(const flce_adamw_tensor_t* tensors, int count, cons
 
 }  // namespace
 
-int chunk_width(int64_t n) { return n <= 16384 ? 8192 : 4096; }
 
 }  // namespace flce
 
@@ -1478,7 +1455,7 @@ flce_status_t flce_token_logprobs_backward(const flce_problem_t* p, float temper
   Ctx c;
   st = prepare(&c, p, ws, ws_bytes, stream, Lay::kScore);
   if (st != FLCE_OK) return st;
-  const ScoreGrad sg{score_plan(*p).parts, 1.f / temperature, grad_entropy, entropy};
+  const ScoreGrad sg{score_plan(p->n, p->h, p->v), 1.f / temperature, grad_entropy, entropy};
   return run_backward(c, X, W, tokens, lse, grad_logprob, dX, dW, c.dx_acc(), nullptr, &sg);
 }
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #if defined(__CUDACC__)
 #define FLCE_HOST_DEVICE __host__ __device__
 #else
@@ -36,7 +38,35 @@ inline int pair_grid(int sms, long long pair_work) {
 
 // Vocabulary chunk width of the backward pass (a multiple of kBN).  The
 // workspace holds one chunk of G, N x chunk bf16.
-int chunk_width(int64_t n);
+inline int chunk_width(int64_t n) { return n <= 16384 ? 8192 : 4096; }
+
+// Token log probabilities' backward: chunk width and dX parts.  A wide chunk while its G
+// (n x chunk bf16) stays within 128 MiB, so that few rows need few launches; and where the
+// dX tiles are too few for the GPU's 76 CTA pairs, each tile's sum over the vocabulary cut
+// into parts (at least 512 ids, 64 MiB together), added up in order at the end: 256 x 4096 x
+// 128256 in 753 us, 1424 without either; 100 x 512 x 60000 in 87, 385 without.
+//   A part is `part_k` ids in every chunk.  The first chunk is the widest: it fills all
+// `parts`, the ones that exist, and stores them; a later chunk adds to as many or fewer.
+struct ScorePlan {
+  int chunk, parts, part_k;
+  // of a chunk of cw ids
+  int splits(int cw) const { return (cw + part_k - 1) / part_k; }
+};
+inline ScorePlan score_plan(int64_t n, int64_t h, int64_t v) {
+  constexpr int64_t kPairs = 76;
+  const int64_t whole = (v + 255) / 256 * 256;
+  const int64_t fit = (int64_t{1} << 26) / std::max<int64_t>(n, 1) / 256 * 256;
+  const int64_t wide = std::min<int64_t>({fit, int64_t{1} << 17, whole});
+  const int64_t chunk = std::max<int64_t>(std::min<int64_t>(chunk_width(n), whole), wide);
+  const int64_t first = std::min(chunk, v);
+  const int64_t tiles = (n + kPairRows - 1) / kPairRows * ((h + kBN - 1) / kBN);
+  int64_t parts = tiles < kPairs ? (2 * kPairs + tiles - 1) / std::max<int64_t>(tiles, 1) : 1;
+  parts = std::min<int64_t>({parts, first / 512, (int64_t{1} << 24) / std::max<int64_t>(n * h, 1)});
+  // fewer than 4 parts save less than the launch that adds them up costs
+  if (parts < 4) return ScorePlan{static_cast<int>(chunk), 1, static_cast<int>(chunk)};
+  const int part_k = static_cast<int>((first + kBK * parts - 1) / (kBK * parts)) * kBK;
+  return ScorePlan{static_cast<int>(chunk), static_cast<int>((first + part_k - 1) / part_k), part_k};
+}
 
 enum Mode : int {
   kModeForward = 0,
