@@ -355,7 +355,11 @@ flce_status_t flce_forward_noalloc(const flce_problem_t* p, const void* X, const
  *   entropy_i = -sum_j p_ij log p_ij   (of every row, ignored or not)
  *   top_ids[i, :]: the k ids with the largest x_i . w_j, high to low (equal: lower
  *   id first), top_logprobs[i, :] = z_ij - lse_i there.  0 <= k <= 16.  With k > V the
- *   ids past V are -1 and their log probabilities minus infinity.
+ *   ids past V are -1 and their log probabilities minus infinity.  A logit of minus
+ *   infinity (a banned token) ranks below the others and has log probability minus
+ *   infinity, unless the whole row is banned: those are NaN.  A row with a NaN logit
+ *   has NaN log probabilities; its ids are ids of the vocabulary, which ones is not
+ *   specified.
  * p->shift scores row i against tokens[i + 1] as labels are; p->reduction is not
  * used.  tokens NULL: no token is given (logprob must be NULL too).  logprob and
  * entropy may be NULL; top_ids and top_logprobs are not used when k = 0. */

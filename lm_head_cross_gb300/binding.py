@@ -937,7 +937,8 @@ def token_logprobs(x, w, tokens=None, top: int = 0, temperature: float = 1.0, ig
     x: [..., H] bf16 CUDA, w: [V, H] bf16, tokens: [...] integer (same leading shape as x), or
     None.  Rows whose token is ignore_index have log probability 0 and pass no gradient through
     it; their entropy and alternatives are those of any row.  top: alternatives per row (at most
-    16), by logit, the lower id first among equals.  shift=1 scores position t of each sequence
+    16), by logit, the lower id first among equals (so too among banned tokens, logits of minus
+    infinity, where fewer others are left); -1 only past the vocabulary's end.  shift=1 scores position t of each sequence
     against the token at t + 1.  Returns TokenLogprobs shaped like x's leading dimensions;
     autograd flows from logprob and entropy to x and w.
     """

@@ -371,7 +371,7 @@ __device__ void decode_epilogue_few(const DecodeParams& p, Range r, float* logit
       l[q] = l[q] * f + sl;
       m[q] = new_m;
       if (!TOP) continue;
-      uint32_t key[8], mine = 0;  // 0: none (neither a NaN nor minus infinity is an alternative)
+      uint32_t key[8], mine = 0;  // 0: none (a NaN, or minus infinity, which the join puts in)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         key[j] = v[j] > -INFINITY ? topk_key(v[j] + 0.f) : 0u;
@@ -620,9 +620,14 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
         int place = 0;
         for (int q = 0; q < count; ++q) place += kept[q] > won;
         if (place < p.k) put(place, won);
-      } else if (t < p.k) {  // fewer than k ids
-        top_ids[static_cast<int64_t>(row) * p.k + t] = -1;
-        top_logprobs[static_cast<int64_t>(row) * p.k + t] = -INFINITY;
+      } else if (t < p.k) {  // fewer than k logits above minus infinity
+        const int id = nth_other_id(kept, count, t - count);
+        if (id < p.v) {
+          put(t, other_key(id));
+        } else {  // fewer than k ids
+          top_ids[static_cast<int64_t>(row) * p.k + t] = -1;
+          top_logprobs[static_cast<int64_t>(row) * p.k + t] = -INFINITY;
+        }
       }
       return;
     }

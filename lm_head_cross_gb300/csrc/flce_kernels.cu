@@ -1760,9 +1760,14 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(
       for (int q = 0; q < count; ++q) place += kept[threadIdx.x >> 5][q] > won;
       if (place < k) put(place, won);
     }
-    for (int i = count + lane; i < k; i += 32) {  // fewer than k ids
-      top_ids[static_cast<int64_t>(row) * k + i] = -1;
-      top_logprobs[static_cast<int64_t>(row) * k + i] = -INFINITY;
+    for (int i = count + lane; i < k; i += 32) {  // fewer than k logits above minus infinity
+      const int id = nth_other_id(kept[threadIdx.x >> 5], count, i - count);
+      if (id < v) {
+        put(i, other_key(id));
+      } else {  // fewer than k ids
+        top_ids[static_cast<int64_t>(row) * k + i] = -1;
+        top_logprobs[static_cast<int64_t>(row) * k + i] = -INFINITY;
+      }
     }
     return;
   }

@@ -73,6 +73,22 @@ __device__ __forceinline__ uint64_t candidate_key(float v, int id) {
   return (static_cast<uint64_t>(topk_key(v + 0.f)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
 }
 
+// The nth (from 0) of the ids that are not among `count` candidates: the alternatives that
+// follow where a row has fewer logits above minus infinity than are asked for.  Those are all
+// candidates, the other ids are equal, and the lowest goes first.  (Each round moves the answer
+// past the candidates that are not above it: at most count + 1.)
+__device__ __forceinline__ int nth_other_id(const uint64_t* cand, int count, int nth) {
+  int id = nth;
+  while (true) {
+    int past = 0;
+    for (int q = 0; q < count; ++q) past += 0xffffffffu - static_cast<uint32_t>(cand[q]) <= static_cast<uint32_t>(id);
+    if (nth + past == id) return id;
+    id = nth + past;
+  }
+}
+// Its key: minus infinity, which topk_unkey makes of 0.
+__device__ __forceinline__ uint64_t other_key(int id) { return 0xffffffffu - static_cast<uint32_t>(id); }
+
 __device__ __forceinline__ bool topk_better(float av, int ai, float bv, int bi) {
   return av > bv || (av == bv && static_cast<unsigned>(ai) < static_cast<unsigned>(bi));
 }
