@@ -130,6 +130,10 @@ def adamw_step(plan, grads, step, grad_scale=None, stream=None):
     _call("flce_adamw_step", lib().flce_adamw_step(
         table, len(plan), ctypes.byref(plan.options), None if grad_scale is None else grad_scale.data_ptr(),
         _stream_ptr(stream)))
+    # autograd learns of the writes: a graph that saved the old weights refuses its backward pass
+    params, masters = plan._held[0], plan._held[3]
+    torch.autograd.graph.increment_version(
+        [t for i, g in enumerate(grads) if g is not None for t in (params[i], masters[i]) if t is not None])
 
 
 class AdamW:

@@ -1,0 +1,64 @@
+"""The AdamW calls' own work on the host, on CPU tensors and with a stand-in for the library's
+step (which writes nothing): what they tell autograd, what they hand to the step, and on what
+they refuse to run.  With a GPU, the same through the step itself."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import lm_head_cross_gb300 as flce  # noqa: E402
+from lm_head_cross_gb300 import optim  # noqa: E402
+
+
+class Steps:
+    """Stands in for the library: keeps what each step was given."""
+
+    def __init__(self):
+        self.rows = []
+
+    def flce_adamw_step(self, table, count, options, grad_scale, stream):
+        self.rows.append([{name: getattr(table[i], name) for name, _ in table[i]._fields_} for i in range(count)])
+        return 0
+
+
+@pytest.fixture
+def steps(monkeypatch):
+    s = Steps()
+    monkeypatch.setattr(optim, "lib", lambda: s)
+    monkeypatch.setattr(optim, "_check", lambda *a, **k: None)  # (CPU tensors)
+    monkeypatch.setattr(optim, "_stream_ptr", lambda stream: None)
+    return s
+
+
+def params(device="cpu"):
+    return [torch.nn.Parameter(torch.linspace(-1, 1, n, device=device)) for n in (6, 5)]
+
+
+def graphs_refuse(ps):
+    """A step moves a weight that a graph has saved: its backward pass must not use the new one."""
+    opt = flce.AdamW(ps, lr=0.1)
+    losses = [(p * p).sum() for p in ps]
+    ps[0].grad = torch.ones_like(ps[0])
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        losses[0].backward()
+    losses[1].backward()  # no gradient: left alone
+    assert torch.equal(ps[1].grad, 2 * ps[1].detach())
+
+
+def test_graphs_of_old_weights_refuse_their_backward_pass(steps):
+    graphs_refuse(params())
+
+
+@pytest.mark.gpu
+def test_graphs_of_old_weights_refuse_their_backward_pass_on_gpu():
+    graphs_refuse(params("cuda"))
+
+
+def test_master_weights_count_as_written(steps):
+    w = torch.zeros(8, dtype=torch.bfloat16)
+    master = torch.zeros(8, requires_grad=True)
+    loss = (master * master).sum()
+    plan = flce.adamw_plan([w], [torch.zeros(8)], [torch.zeros(8)], masters=[master])
+    flce.adamw_step(plan, [torch.ones(8)], step=1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
