@@ -86,11 +86,18 @@ class AdamWPlan:
 
     def set_lr(self, lr):
         """A number for every tensor, or one number per tensor, used from the next step on."""
-        lrs = list(lr) if isinstance(lr, (list, tuple)) else [lr] * len(self)
-        if len(lrs) != len(self):
-            raise ValueError("lr is a number, or one number per parameter")
-        for i, v in enumerate(lrs):
-            self.table[i].lr = v
+        self._set("lr", lr)
+
+    def set_weight_decay(self, weight_decay):
+        """A number for every tensor, or one number per tensor, used from the next step on."""
+        self._set("weight_decay", weight_decay)
+
+    def _set(self, name, value):
+        values = list(value) if isinstance(value, (list, tuple)) else [value] * len(self)
+        if len(values) != len(self):
+            raise ValueError(f"{name} is a number, or one number per parameter")
+        for i, v in enumerate(values):
+            setattr(self.table[i], name, v)
 
 
 def adamw_plan(params, exp_avgs, exp_avg_sqs, masters=None, scales=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
@@ -179,8 +186,10 @@ class AdamW:
         return [g[key] for g in self.groups for _ in g["params"]]
 
     def step(self, grad_scale=None, stream=None):
-        """One step from the parameters' .grad (see adamw_step); without any gradient, none."""
+        """One step from the parameters' .grad (see adamw_step), at the groups' present lr and
+        weight_decay; without any gradient, none."""
         self.plan.set_lr(self._per_param("lr"))
+        self.plan.set_weight_decay(self._per_param("weight_decay"))
         for i, p in enumerate(self.params):  # a parameter may have been given new storage
             if p.data_ptr() != self.plan.table[i].param:
                 self.plan.set_param(i, p.detach())

@@ -62,3 +62,34 @@ def test_master_weights_count_as_written(steps):
     flce.adamw_step(plan, [torch.ones(8)], step=1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_a_schedule_of_lr_and_weight_decay_is_followed(steps):
+    ps = params()
+    opt = flce.AdamW([{"params": ps[:1]}, {"params": ps[1:], "weight_decay": 0.5}], lr=0.1, weight_decay=0.25)
+    for p in ps:
+        p.grad = torch.ones_like(p)
+    opt.step()
+    opt.groups[0]["lr"], opt.groups[1]["weight_decay"] = 0.5, 0.125
+    opt.step()
+    got = [[(r["lr"], r["weight_decay"]) for r in rows] for rows in steps.rows]
+    tenth = float(torch.tensor(0.1))
+    assert got == [[(tenth, 0.25), (tenth, 0.5)], [(0.5, 0.25), (tenth, 0.125)]]
+    opt.plan.set_weight_decay(0.0)
+    flce.adamw_step(opt.plan, [p.grad for p in ps], step=3)
+    assert [r["weight_decay"] for r in steps.rows[-1]] == [0.0, 0.0]
+    for set_one in (opt.plan.set_lr, opt.plan.set_weight_decay):
+        with pytest.raises(ValueError):
+            set_one([0.1])
+
+
+@pytest.mark.gpu
+def test_weight_decay_changed_between_steps():
+    """Zero gradients from zero moments: only the decay moves a weight, by 1 - lr wd."""
+    p = torch.nn.Parameter(torch.full((300,), 2.0, device="cuda"))
+    opt = flce.AdamW([p], lr=0.5, weight_decay=0.5)
+    p.grad = torch.zeros_like(p)
+    opt.step()
+    opt.groups[0]["weight_decay"] = 0.25
+    opt.step()
+    assert torch.equal(p.detach(), torch.full_like(p, 2.0 * 0.75 * 0.875))  # exact in fp32
