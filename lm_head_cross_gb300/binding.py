@@ -213,6 +213,20 @@ def _stream_ptr(stream):
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+def _current_device():
+    return _torch()._C._cuda_getDevice()
+
+
+def _check_device(device, stream, *tensors):
+    """Kernels start on the current device and read every pointer there: it must be the one that
+    holds the call's tensors (None: not given) and the stream, if one is given."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on one device, got {device} and {t.device}")
+    if device.index != _current_device() or (stream is not None and stream.device != device):
+        raise ValueError(f"the tensors are on {device}, which is not the current device, or not the stream's")
+
+
 def _check_inputs(x, w, labels):
     torch = _torch()
     if x.dim() != 2 or w.dim() != 2 or labels.dim() != 1:
@@ -716,6 +730,7 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, stream=None):
     rstd [N] fp32)."""
     torch = _torch()
     q = _norm(x, weight, bias, eps)
+    _check_device(x.device, stream, weight, bias)
     with _allocating(stream):
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
         mean = torch.empty(q.n, dtype=torch.float32, device=x.device)
@@ -740,6 +755,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, bias=True, ws=None, stream=Non
         raise ValueError("dy must be a contiguous CUDA tensor of x's shape and dtype")
     _f32(mean, (q.n,), "mean")
     _f32(rstd, (q.n,), "rstd")
+    _check_device(x.device, stream, dy, weight, mean, rstd, ws)
     with _allocating(stream):
         if ws is None:
             ws = torch.empty(layernorm_workspace_bytes(q.n, q.h), dtype=torch.uint8, device=x.device)
@@ -830,6 +846,7 @@ def logprobs_forward(x, w, tokens=None, top=0, temperature=1.0, ignore_index=-10
     row's entropy, log-sum-exp and ``top`` (at most 16) alternatives.  Returns (TokenLogprobs, ws)."""
     torch = _torch()
     _check_head(x, w, tokens)
+    _check_device(x.device, stream, w, tokens, ws)
     n, h = x.shape
     p = _problem(n, h, w.shape[0], ignore_index, "none", shift, seq_len)
     top, dev, f32 = int(top), x.device, torch.float32
@@ -877,6 +894,7 @@ def logprobs_backward(x, w, tokens, lse, entropy, grad_logprob=None, grad_entrop
             raise ValueError("grad_entropy needs entropy")
     if entropy is not None:
         _f32(entropy, (n,), "entropy")
+    _check_device(x.device, stream, w, tokens, lse, entropy, grad_logprob, grad_entropy, ws)
     p = _problem(n, h, w.shape[0], ignore_index, "none", shift, seq_len)
     with _allocating(stream):
         if ws is None:

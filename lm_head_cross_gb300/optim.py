@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import AdamwOptions, AdamwTensor, _call, _stream_ptr, _torch, lib
+from .binding import AdamwOptions, AdamwTensor, _call, _check_device, _stream_ptr, _torch, lib
 
 BLOCK = 256  # elements that share one scale of an 8-bit moment
 
@@ -133,6 +133,8 @@ def adamw_step(plan, grads, step, grad_scale=None, stream=None):
     if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                    or not grad_scale.is_cuda):
         raise ValueError("grad_scale must be a one-element fp32 CUDA tensor")
+    if plan.device is not None:
+        _check_device(plan.device, stream, grad_scale)
     plan.options.step = int(step)
     _call("flce_adamw_step", lib().flce_adamw_step(
         table, len(plan), ctypes.byref(plan.options), None if grad_scale is None else grad_scale.data_ptr(),

@@ -25,6 +25,7 @@ def steps(monkeypatch):
     s = Steps()
     monkeypatch.setattr(optim, "lib", lambda: s)
     monkeypatch.setattr(optim, "_check", lambda *a, **k: None)  # (CPU tensors)
+    monkeypatch.setattr(optim, "_check_device", lambda *a: None)
     monkeypatch.setattr(optim, "_stream_ptr", lambda stream: None)
     return s
 
