@@ -71,6 +71,7 @@ class AdamWPlan:
             self.table[i] = AdamwTensor(*ptr, p.numel(), lrs[i], wds[i], code, 0)
         self.options = AdamwOptions(betas[0], betas[1], eps, 1, self.state_bits)
         self._held = (list(params), *(list(x) for x in lists))  # the table holds their addresses
+        self._recorded = set()  # streams that _held's memory is known to be used on
 
     def __len__(self):
         return len(self.numels)
@@ -83,6 +84,7 @@ class AdamWPlan:
             raise ValueError("all tensors of a plan must be on one device")
         self._held[0][i] = p
         self.table[i].param = p.data_ptr()
+        self._recorded.clear()
 
     def set_lr(self, lr):
         """A number for every tensor, or one number per tensor, used from the next step on."""
@@ -113,7 +115,8 @@ def adamw_plan(params, exp_avgs, exp_avg_sqs, masters=None, scales=None, lr=1e-3
 def adamw_step(plan, grads, step, grad_scale=None, stream=None):
     """One step (number ``step``, from 1) in place.  grads: one contiguous bf16 or fp32 CUDA tensor
     per parameter, or None for a parameter that is left alone.  grad_scale: a one-element fp32 CUDA
-    tensor that multiplies every gradient (clipping, loss scaling)."""
+    tensor that multiplies every gradient (clipping, loss scaling).  stream: the torch stream to
+    run on, else the current one; the tensors may be freed once the call has returned."""
     torch = _torch()
     if len(grads) != len(plan):
         raise ValueError(f"{len(plan)} gradients are needed, got {len(grads)}")
@@ -139,6 +142,14 @@ def adamw_step(plan, grads, step, grad_scale=None, stream=None):
     _call("flce_adamw_step", lib().flce_adamw_step(
         table, len(plan), ctypes.byref(plan.options), None if grad_scale is None else grad_scale.data_ptr(),
         _stream_ptr(stream)))
+    if stream is not None:  # what is freed after the call is reused only once the stream is done with it
+        used = [*grads, grad_scale]
+        if stream.cuda_stream not in plan._recorded:
+            used += [t for held in plan._held for t in held]
+            plan._recorded.add(stream.cuda_stream)
+        for t in used:
+            if t is not None:
+                t.record_stream(stream)
     # autograd learns of the writes: a graph that saved the old weights refuses its backward pass
     params, masters = plan._held[0], plan._held[3]
     torch.autograd.graph.increment_version(

@@ -94,3 +94,67 @@ def test_weight_decay_changed_between_steps():
     opt.groups[0]["weight_decay"] = 0.25
     opt.step()
     assert torch.equal(p.detach(), torch.full_like(p, 2.0 * 0.75 * 0.875))  # exact in fp32
+
+
+class Recorded(torch.Tensor):
+    """A CPU tensor that says it is on a GPU and keeps the streams its memory is recorded on."""
+    __torch_function__ = torch._C._disabled_torch_function_impl
+    is_cuda = True
+
+    def record_stream(self, stream):
+        self.__dict__.setdefault("streams", []).append(stream)
+
+
+class Stream:
+    cuda_stream = 7
+
+
+def test_a_foreign_stream_is_recorded_on_what_it_uses(steps):
+    """Every step: the gradients and grad_scale; once: what the plan holds, and a parameter's
+    new storage."""
+    def make(n):
+        return torch.zeros(n).as_subclass(Recorded)
+
+    held = [make(6) for _ in range(4)]
+    plan = flce.adamw_plan(held[:1], held[1:2], held[2:3], masters=held[3:])
+    s = Stream()
+    for k in range(2):
+        grad, scale = make(6), make(1)
+        flce.adamw_step(plan, [grad], step=k + 1, grad_scale=scale, stream=s)
+        assert [t.streams for t in (grad, scale, *held)] == [[s]] * 6
+    moved = make(6)
+    plan.set_param(0, moved)
+    flce.adamw_step(plan, [None], step=3, stream=s)
+    assert moved.streams == [s]
+    grad = make(6)
+    flce.adamw_step(plan, [grad], step=4)  # the current stream
+    assert not hasattr(grad, "streams")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_freed_right_after_a_step_on_another_stream(bits):
+    """The step waits on its stream while the caller frees the gradients and writes to memory
+    of the same size: the weights are those of a step that was waited for."""
+    n = 1 << 20
+    g = torch.Generator().manual_seed(0)
+    start, grad = torch.randn(n, generator=g).cuda(), torch.randn(n, generator=g).cuda()
+    ends = []
+    for early in (False, True):
+        p = torch.nn.Parameter(start.clone())
+        opt = flce.AdamW([p], lr=0.1, state_bits=bits)
+        p.grad = grad.clone()
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        if early:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(20_000_000)  # about 10 ms
+        opt.step(stream=s)
+        if not early:
+            s.synchronize()
+        opt.zero_grad()
+        for _ in range(4):
+            torch.full((n,), 1e6, device="cuda")
+        torch.cuda.synchronize()
+        ends.append(p.detach().clone())
+    assert torch.equal(*ends)
