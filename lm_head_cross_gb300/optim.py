@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import AdamwOptions, AdamwTensor, _call, _check_device, _stream_ptr, _torch, lib
+from .binding import AdamwOptions, AdamwTensor, _allocating, _call, _check_device, _stream_ptr, _torch, lib
 
 BLOCK = 256  # elements that share one scale of an 8-bit moment
 
@@ -162,8 +162,8 @@ class AdamW:
     params: tensors, or groups {"params": [...], "lr": ..., "weight_decay": ...}.  state_bits 32
     or 8.  master_weights: keep fp32 master weights for bf16 parameters (their own rounding
     would swallow updates smaller than 2^-9 of a weight); the next step overwrites what was
-    written to such a parameter from outside.  Gradients are read from ``.grad``;
-    a parameter without one is left alone.
+    written to such a parameter from outside.  Gradients are read from ``.grad`` (copied first
+    where they are not contiguous); a parameter without one is left alone.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32,
@@ -209,6 +209,9 @@ class AdamW:
         grads = [p.grad for p in self.params]
         if all(g is None for g in grads):
             return
+        if any(g is not None and not g.is_contiguous() for g in grads):
+            with _allocating(stream):  # copied on the step's stream
+                grads = [None if g is None else g.contiguous() for g in grads]
         adamw_step(self.plan, grads, self.steps + 1, grad_scale, stream)
         self.steps += 1
 

@@ -158,3 +158,28 @@ def test_gradients_freed_right_after_a_step_on_another_stream(bits):
         torch.cuda.synchronize()
         ends.append(p.detach().clone())
     assert torch.equal(*ends)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("foreign", [False, True])
+def test_gradients_of_other_layouts_are_taken(foreign):
+    """A transposed and an expanded gradient step as their contiguous copies do."""
+    g = torch.Generator().manual_seed(0)
+    start, grad = torch.randn(40, 24, generator=g).cuda(), torch.randn(24, 40, generator=g).cuda().t()
+    row = torch.randn(24, generator=g).cuda().expand(40, 24)
+    ends = []
+    for copy in (True, False):
+        ps = [torch.nn.Parameter(start.clone()) for _ in range(3)]
+        opt = flce.AdamW(ps, lr=0.1)
+        s = torch.cuda.Stream() if foreign else None
+        for k, p in enumerate(ps[:2]):
+            p.grad = (grad, row)[k].contiguous() if copy else (grad, row)[k]
+            assert p.grad.is_contiguous() is copy
+        if foreign:
+            s.wait_stream(torch.cuda.current_stream())
+        opt.step(stream=s)
+        torch.cuda.synchronize()
+        ends.append([p.detach().clone() for p in ps])
+    for a, b in zip(*ends):
+        assert torch.equal(a, b)
+    assert torch.equal(ends[1][2], start)  # without a gradient
