@@ -204,27 +204,30 @@ def _torch():
     return _TORCH
 
 
-def _stream_ptr(stream):
+def _stream_ptr(stream, device=None):
     """The cudaStream_t of a torch stream, or of the current one (asked for without building
-    a torch.cuda.Stream object, which takes 3 us)."""
+    a torch.cuda.Stream object, which takes 3 us) of the current device, whose index a caller
+    may know."""
     if stream is not None:
         return stream.cuda_stream
-    c = _torch()._C
-    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return _torch()._C._cuda_getCurrentRawStream(_current_device() if device is None else device)
 
 
 def _current_device():
     return _torch()._C._cuda_getDevice()
 
 
-def _check_device(device, stream, *tensors):
+def _check_device(x, stream, *tensors):
     """Kernels start on the current device and read every pointer there: it must be the one that
-    holds the call's tensors (None: not given) and the stream, if one is given."""
+    holds x, the call's other tensors (None: not given) and the stream, if one is given.  Returns
+    its index (by number: comparing torch.device objects took 3 us a call)."""
+    device = x.get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on one device, got {device} and {t.device}")
-    if device.index != _current_device() or (stream is not None and stream.device != device):
-        raise ValueError(f"the tensors are on {device}, which is not the current device, or not the stream's")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors must be on one device, got {x.device} and {t.device}")
+    if device != _current_device() or (stream is not None and stream.device.index != device):
+        raise ValueError(f"the tensors are on {x.device}, which is not the current device, or not the stream's")
+    return device
 
 
 def _check_inputs(x, w, labels):
@@ -730,14 +733,14 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, stream=None):
     rstd [N] fp32)."""
     torch = _torch()
     q = _norm(x, weight, bias, eps)
-    _check_device(x.device, stream, weight, bias)
+    device = _check_device(x, stream, weight, bias)
     with _allocating(stream):
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
         mean = torch.empty(q.n, dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
     _call("flce_layernorm_forward", lib().flce_layernorm_forward(
         ctypes.byref(q), x.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(), y.data_ptr(),
-        mean.data_ptr(), rstd.data_ptr(), _stream_ptr(stream)))
+        mean.data_ptr(), rstd.data_ptr(), _stream_ptr(stream, device)))
     return y, mean, rstd
 
 
@@ -755,7 +758,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, bias=True, ws=None, stream=Non
         raise ValueError("dy must be a contiguous CUDA tensor of x's shape and dtype")
     _f32(mean, (q.n,), "mean")
     _f32(rstd, (q.n,), "rstd")
-    _check_device(x.device, stream, dy, weight, mean, rstd, ws)
+    device = _check_device(x, stream, dy, weight, mean, rstd, ws)
     with _allocating(stream):
         if ws is None:
             ws = torch.empty(layernorm_workspace_bytes(q.n, q.h), dtype=torch.uint8, device=x.device)
@@ -765,7 +768,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, bias=True, ws=None, stream=Non
     _call("flce_layernorm_backward", lib().flce_layernorm_backward(
         ctypes.byref(q), dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
         dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr() if bias else None, ws.data_ptr(), ws.numel(),
-        _stream_ptr(stream)))
+        _stream_ptr(stream, device)))
     return dx, dweight, dbias, ws
 
 
@@ -846,7 +849,7 @@ def logprobs_forward(x, w, tokens=None, top=0, temperature=1.0, ignore_index=-10
     row's entropy, log-sum-exp and ``top`` (at most 16) alternatives.  Returns (TokenLogprobs, ws)."""
     torch = _torch()
     _check_head(x, w, tokens)
-    _check_device(x.device, stream, w, tokens, ws)
+    device = _check_device(x, stream, w, tokens, ws)
     n, h = x.shape
     p = _problem(n, h, w.shape[0], ignore_index, "none", shift, seq_len)
     top, dev, f32 = int(top), x.device, torch.float32
@@ -864,7 +867,7 @@ def logprobs_forward(x, w, tokens=None, top=0, temperature=1.0, ignore_index=-10
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     _call("flce_token_logprobs", lib().flce_token_logprobs(
         ctypes.byref(p), top, float(temperature), x.data_ptr(), w.data_ptr(), ptr(tokens), ptr(lp), entropy.data_ptr(),
-        lse.data_ptr(), ptr(ids), ptr(tlp), ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
+        lse.data_ptr(), ptr(ids), ptr(tlp), ws.data_ptr(), ws.numel(), _stream_ptr(stream, device)))
     if check:
         _call("device", read_device_status(ws, stream))
     return TokenLogprobs(lp, entropy, lse, ids, tlp), ws
@@ -894,7 +897,7 @@ def logprobs_backward(x, w, tokens, lse, entropy, grad_logprob=None, grad_entrop
             raise ValueError("grad_entropy needs entropy")
     if entropy is not None:
         _f32(entropy, (n,), "entropy")
-    _check_device(x.device, stream, w, tokens, lse, entropy, grad_logprob, grad_entropy, ws)
+    device = _check_device(x, stream, w, tokens, lse, entropy, grad_logprob, grad_entropy, ws)
     p = _problem(n, h, w.shape[0], ignore_index, "none", shift, seq_len)
     with _allocating(stream):
         if ws is None:
@@ -907,7 +910,7 @@ def logprobs_backward(x, w, tokens, lse, entropy, grad_logprob=None, grad_entrop
     _call("flce_token_logprobs_backward", lib().flce_token_logprobs_backward(
         ctypes.byref(p), float(temperature), x.data_ptr(), w.data_ptr(), ptr(tokens), lse.data_ptr(), ptr(entropy),
         ptr(grad_logprob), ptr(grad_entropy), dX.data_ptr(), dW.data_ptr(), ws.data_ptr(), ws.numel(),
-        _stream_ptr(stream)))
+        _stream_ptr(stream, device)))
     if check:
         _call("device", read_device_status(ws, stream))
     return dX, dW, ws

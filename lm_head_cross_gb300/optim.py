@@ -136,12 +136,11 @@ def adamw_step(plan, grads, step, grad_scale=None, stream=None):
     if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                    or not grad_scale.is_cuda):
         raise ValueError("grad_scale must be a one-element fp32 CUDA tensor")
-    if plan.device is not None:
-        _check_device(plan.device, stream, grad_scale)
+    device = _check_device(plan._held[0][0], stream, grad_scale) if len(plan) else None
     plan.options.step = int(step)
     _call("flce_adamw_step", lib().flce_adamw_step(
         table, len(plan), ctypes.byref(plan.options), None if grad_scale is None else grad_scale.data_ptr(),
-        _stream_ptr(stream)))
+        _stream_ptr(stream, device)))
     if stream is not None:  # what is freed after the call is reused only once the stream is done with it
         used = [*grads, grad_scale]
         if stream.cuda_stream not in plan._recorded:

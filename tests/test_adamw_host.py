@@ -26,7 +26,7 @@ def steps(monkeypatch):
     monkeypatch.setattr(optim, "lib", lambda: s)
     monkeypatch.setattr(optim, "_check", lambda *a, **k: None)  # (CPU tensors)
     monkeypatch.setattr(optim, "_check_device", lambda *a: None)
-    monkeypatch.setattr(optim, "_stream_ptr", lambda stream: None)
+    monkeypatch.setattr(optim, "_stream_ptr", lambda *a: None)
     return s
 
 

@@ -21,6 +21,9 @@ class On(torch.Tensor):
     def device(self):
         return torch.device("cuda", self.index)
 
+    def get_device(self):
+        return self.index
+
 
 def on(index, *shape, dtype=F32):
     t = torch.zeros(*shape, dtype=dtype).as_subclass(On)
@@ -75,7 +78,7 @@ def current(monkeypatch):
     monkeypatch.setattr(binding, "lib", lambda: pytest.fail("not refused"))
     monkeypatch.setattr(optim, "lib", lambda: pytest.fail("not refused"))
     for mod in (binding, optim):
-        monkeypatch.setattr(mod, "_stream_ptr", lambda stream: None)
+        monkeypatch.setattr(mod, "_stream_ptr", lambda *a: None)
     real = torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: real(*a, **k))
 
