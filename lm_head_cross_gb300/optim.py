@@ -1,4 +1,4 @@
-"""AdamW over many tensors in one launch (flce_adamw_step).
+"""AdamW over many tensors, one launch for each 400 of them (flce_adamw_step).
 
 ``adamw_plan`` describes the tensors once (parameters, moments, optional fp32 master
 weights); ``adamw_step`` takes one step with the current gradients.  ``AdamW`` is the
@@ -156,7 +156,7 @@ def adamw_step(plan, grads, step, grad_scale=None, stream=None):
 
 
 class AdamW:
-    """AdamW with moments in 32 or 8 bits, over all parameters in one launch.
+    """AdamW with moments in 32 or 8 bits, one launch for each 400 parameters.
 
     params: tensors, or groups {"params": [...], "lr": ..., "weight_decay": ...}.  state_bits 32
     or 8.  master_weights: keep fp32 master weights for bf16 parameters (their own rounding
