@@ -424,6 +424,44 @@ flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, cons
                                       void* ws, size_t ws_bytes, flce_stream_t stream);
 
 /* ----------------------------------------------------------------------------
+ * Embedding: rows of a vocabulary matrix, which may be the head's own, scaled,
+ * and its gradient.  For n tokens,
+ *   y_i = scale W[id_i],
+ *   dW_v = scale sum_{i : id_i = v} dy_i   (0 for v = padding_idx).
+ *   - W and dW share one type, y and dy another (flce_dtype_t each; the forward
+ *     pass needs them equal).  Sums are fp32, in the order of the tokens'
+ *     positions (an id with more than 32 tokens: in parts, themselves in order),
+ *     and rounded once: the same inputs give the same bits.
+ *   - add = 0: all v rows of dW are written.  add = 1: dW receives dW + the
+ *     gradient, rounded once; rows without a token are neither read nor written.
+ *     So the gradient that the head's backward pass left for a shared matrix is
+ *     completed in place.
+ *   - padding_idx: tokens with this id pass no gradient; -1 for none.
+ *   - Any n >= 0, h >= 1, v >= 1 (n, v up to 2^30, h up to 2^20).  ids is int32
+ *     [n].  Pointers need the alignment of their type.  An id outside [0, v)
+ *     (the padding id aside) records FLCE_ERR_LABEL_OUT_OF_RANGE in the
+ *     workspace's status word; its token reads and adds nothing.
+ *   - n = 0: dW is zeros (add = 0) or left alone. */
+typedef struct {
+  int64_t n;            /* tokens */
+  int64_t h;            /* elements of a row */
+  int64_t v;            /* rows of W */
+  float scale;
+  int32_t padding_idx;  /* in [0, v), or -1 */
+  int32_t w_dtype;      /* flce_dtype_t of W and dW */
+  int32_t y_dtype;      /* flce_dtype_t of y and dy */
+} flce_embedding_t;
+
+/* The forward pass needs 256 bytes of workspace (the status word), the backward
+ * pass flce_embedding_workspace_bytes(q) (0 if q is invalid): the sorted tokens
+ * (4 (v + 2 n) bytes) and, from 33 tokens on, two fp32 rows for each 32. */
+flce_status_t flce_embedding_forward(const flce_embedding_t* q, const int32_t* ids, const void* W, void* y, void* ws,
+                                     size_t ws_bytes, flce_stream_t stream);
+size_t flce_embedding_workspace_bytes(const flce_embedding_t* q);
+flce_status_t flce_embedding_backward(const flce_embedding_t* q, const void* dy, const int32_t* ids, void* dW,
+                                      int32_t add, void* ws, size_t ws_bytes, flce_stream_t stream);
+
+/* ----------------------------------------------------------------------------
  * AdamW: one step over many tensors.  For every element, with the gradient
  * g = grad * grad_scale (a device fp32 scalar; NULL: 1),
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,

@@ -12,7 +12,8 @@ from .binding import (  # noqa: F401
     profile_enable, profile_read, KERNEL_KINDS, scale_grads, topk, topk_workspace_bytes, soft_fwd_bwd,
     host_buffer_bytes, fwd_bwd_host, sparse_kl_divergence, shard_workspace_bytes, shard_forward, shard_combine,
     shard_backward, valid_count, f32_to_bf16, layer_norm, layernorm_forward, layernorm_backward,
-    layernorm_workspace_bytes, TokenLogprobs, token_logprobs, logprobs_forward, logprobs_backward,
+    layernorm_workspace_bytes, embedding, embedding_forward, embedding_backward, embedding_workspace_bytes,
+    TokenLogprobs, token_logprobs, logprobs_forward, logprobs_backward,
     token_logprobs_workspace_bytes, logprobs_backward_workspace_bytes,
 )
 from .optim import AdamW, adamw_plan, adamw_step  # noqa: F401

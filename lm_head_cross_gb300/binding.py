@@ -27,6 +27,7 @@ EXPORTED = ("flce_workspace_bytes", "flce_workspace_bytes_rowchunk", "flce_forwa
             "flce_soft_fwd_bwd", "flce_soft_fwd_bwd_rowchunk", "flce_host_buffer_bytes", "flce_fwd_bwd_host", "flce_shard_workspace_bytes",
             "flce_shard_forward", "flce_shard_combine", "flce_shard_backward", "flce_valid_count",
             "flce_f32_to_bf16", "flce_layernorm_forward", "flce_layernorm_workspace_bytes", "flce_layernorm_backward",
+            "flce_embedding_forward", "flce_embedding_workspace_bytes", "flce_embedding_backward",
             "flce_adamw_step", "flce_token_logprobs", "flce_token_logprobs_workspace_bytes",
             "flce_token_logprobs_backward", "flce_token_logprobs_backward_workspace_bytes",
             "flce_debug_checks", "flce_selftest_bounds", "flce_status_string")
@@ -54,6 +55,11 @@ class VocabShard(ctypes.Structure):
 class Norm(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("h", ctypes.c_int64), ("x_pitch", ctypes.c_int64), ("eps", ctypes.c_float),
                 ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32)]
+
+
+class Embedding(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("h", ctypes.c_int64), ("v", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("padding_idx", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32)]
 
 
 class AdamwTensor(ctypes.Structure):
@@ -108,6 +114,13 @@ def lib():
     L.flce_layernorm_workspace_bytes.restype = sz
     L.flce_layernorm_backward.argtypes = [Q, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.flce_layernorm_backward.restype = ctypes.c_int
+    E = ctypes.POINTER(Embedding)
+    L.flce_embedding_forward.argtypes = [E, vp, vp, vp, vp, sz, vp]
+    L.flce_embedding_forward.restype = ctypes.c_int
+    L.flce_embedding_workspace_bytes.argtypes = [E]
+    L.flce_embedding_workspace_bytes.restype = sz
+    L.flce_embedding_backward.argtypes = [E, vp, vp, vp, ctypes.c_int32, vp, sz, vp]
+    L.flce_embedding_backward.restype = ctypes.c_int
     L.flce_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), ctypes.c_int32, ctypes.POINTER(AdamwOptions), vp, vp]
     L.flce_adamw_step.restype = ctypes.c_int
     L.flce_token_logprobs_workspace_bytes.argtypes = [P, ctypes.c_int32]
@@ -810,6 +823,116 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5):
         x2 = x2.contiguous()
     y = _LayerNorm.get().apply(x2, weight.contiguous(), None if bias is None else bias.contiguous(), float(eps))
     return y.reshape(x.shape)
+
+
+def _check_ids(ids):
+    if ids.dtype is not _torch().int32:
+        raise TypeError("ids must be int32")
+    if ids.dim() != 1 or not ids.is_cuda or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous CUDA tensor [N]")
+
+
+def embedding_forward(ids, weight, scale=1.0, ws=None, stream=None, check=False):
+    """scale * weight[ids] for ids [N] int32 and weight [V, H], bf16 or fp32.  Returns (y [N, H] of
+    weight's type, ws).  ws: 256 bytes or more, for the device status."""
+    torch = _torch()
+    _check_ids(ids)
+    if weight.dim() != 2 or not weight.is_cuda or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous CUDA tensor [V, H]")
+    code = _dtype(weight, "weight")
+    device = _check_device(weight, stream, ids, ws)
+    (v, h), n = weight.shape, ids.numel()
+    q = Embedding(n, h, v, scale, -1, code, code)
+    with _allocating(stream):
+        if ws is None:
+            ws = torch.empty(256, dtype=torch.uint8, device=weight.device)
+        y = torch.empty(n, h, dtype=weight.dtype, device=weight.device)
+    _call("flce_embedding_forward", lib().flce_embedding_forward(
+        ctypes.byref(q), ids.data_ptr(), weight.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream_ptr(stream, device)))
+    if check:
+        _call("device", read_device_status(ws, stream))
+    return y, ws
+
+
+@functools.lru_cache(maxsize=256)
+def embedding_workspace_bytes(n, h, v) -> int:
+    return int(lib().flce_embedding_workspace_bytes(ctypes.byref(Embedding(int(n), int(h), int(v), 1.0, -1, 0, 0))))
+
+
+def embedding_backward(dy, ids, v, scale=1.0, padding_idx=None, add_to=None, dtype=None, ws=None, stream=None,
+                       check=False):
+    """The gradient of embedding_forward's weight [v, H] for dy [N, H]: a new tensor (of type dtype,
+    else dy's), or added in place to ``add_to``, the gradient that the head's backward pass left
+    for a matrix that both share.  Tokens equal to padding_idx add nothing.  Returns (dweight, ws)."""
+    torch = _torch()
+    _check_ids(ids)
+    n, v = ids.numel(), int(v)
+    if dy.dim() != 2 or dy.shape[0] != n or not dy.is_cuda or not dy.is_contiguous():
+        raise ValueError(f"dy must be a contiguous CUDA tensor [N, H] for ids [N], got {tuple(dy.shape)}")
+    h = dy.shape[1]
+    if add_to is not None:
+        if add_to.shape != (v, h) or not add_to.is_cuda or not add_to.is_contiguous():
+            raise ValueError(f"add_to must be a contiguous CUDA tensor {(v, h)}")
+        if dtype is not None and dtype != add_to.dtype:
+            raise TypeError("dtype is add_to's where it is given")
+    device = _check_device(dy, stream, ids, add_to, ws)
+    with _allocating(stream):
+        dw = torch.empty(v, h, dtype=dtype or dy.dtype, device=dy.device) if add_to is None else add_to
+        q = Embedding(n, h, v, scale, -1 if padding_idx is None else int(padding_idx), _dtype(dw, "dweight"),
+                      _dtype(dy, "dy"))
+        if ws is None:
+            nbytes = embedding_workspace_bytes(n, h, v)
+            if nbytes == 0:
+                raise FlceError(1, "flce_embedding_workspace_bytes")
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
+    _call("flce_embedding_backward", lib().flce_embedding_backward(
+        ctypes.byref(q), dy.data_ptr(), ids.data_ptr(), dw.data_ptr(), int(add_to is not None), ws.data_ptr(),
+        ws.numel(), _stream_ptr(stream, device)))
+    if add_to is not None:  # autograd learns of the write
+        torch.autograd.graph.increment_version([add_to])
+    if check:
+        _call("device", read_device_status(ws, stream))
+    return dw, ws
+
+
+class _Embedding:
+    """torch.autograd.Function over embedding_forward / embedding_backward."""
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            torch = _torch()
+
+            class Fn(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, ids, weight, scale, padding_idx):
+                    y, _ = embedding_forward(ids, weight, scale)
+                    ctx.save_for_backward(ids)
+                    ctx.args = (weight.shape[0], scale, padding_idx)
+                    return y
+
+                @staticmethod
+                @torch.autograd.function.once_differentiable
+                def backward(ctx, dy):
+                    ids, = ctx.saved_tensors
+                    dw, _ = embedding_backward(dy.contiguous(), ids, *ctx.args)
+                    return None, dw, None, None
+
+            cls.fn = Fn
+        return cls.fn
+
+
+def embedding(ids, weight, scale: float = 1.0, padding_idx=None):
+    """scale * weight[ids] for ids [...] (integer CUDA) and weight [V, H] (bf16 or fp32): [..., H].
+    Autograd flows to weight, except from tokens equal to padding_idx."""
+    v = weight.shape[0]
+    if padding_idx is not None and not 0 <= padding_idx < v:
+        raise ValueError(f"padding_idx must be in [0, {v}), got {padding_idx}")
+    flat = ids.reshape(-1).to(_torch().int32).contiguous()
+    y = _Embedding.get().apply(flat, weight.contiguous(), float(scale), padding_idx)
+    return y.reshape(*ids.shape, weight.shape[1])
 
 
 class TokenLogprobs(NamedTuple):

@@ -1704,6 +1704,93 @@ flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, cons
   }));
 }
 
+// ----------------------------------------------------------------------------- embedding
+
+namespace {
+
+flce_status_t check_embedding(const flce_embedding_t* q, EmbedParams* out) {
+  if (!q || q->n < 0 || q->h < 1 || q->v < 1 || !std::isfinite(q->scale)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!known_dtype(q->w_dtype) || !known_dtype(q->y_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (q->padding_idx < -1 || q->padding_idx >= q->v) return FLCE_ERR_INVALID_ARGUMENT;
+  // positions, ids and columns are 32-bit; element offsets are 64-bit
+  if (q->n > (int64_t{1} << 30) || q->v > (int64_t{1} << 30) || q->h > (int64_t{1} << 20))
+    return FLCE_ERR_UNSUPPORTED_SHAPE;
+  *out = EmbedParams{q->n, static_cast<int>(q->h), q->v, q->scale, q->w_dtype == FLCE_F32, q->y_dtype == FLCE_F32};
+  return FLCE_OK;
+}
+
+struct EmbedLayout {
+  size_t start, order, sorted_id, part, total;
+};
+EmbedLayout embed_layout(const EmbedParams& q) {
+  EmbedLayout L{};
+  const size_t n = static_cast<size_t>(q.n);
+  L.start = kAlign;  // after the status word
+  L.order = align_up(L.start + sizeof(int32_t) * (static_cast<size_t>(q.v) + 1));
+  L.sorted_id = align_up(L.order + sizeof(int32_t) * n);
+  L.part = align_up(L.sorted_id + sizeof(int32_t) * n);
+  // (a row's chunks where its start may lie anywhere between two 8-element boundaries)
+  L.total = align_up(L.part + sizeof(float) * static_cast<size_t>(embed_part_floats(q.n, (q.h + 14) / 8 * 8)));
+  return L;
+}
+
+}  // namespace
+
+flce_status_t flce_embedding_forward(const flce_embedding_t* q, const int32_t* ids, const void* W, void* y, void* ws,
+                                     size_t ws_bytes, flce_stream_t stream) {
+  EmbedParams ep;
+  flce_status_t st = check_embedding(q, &ep);
+  if (st != FLCE_OK) return st;
+  if (q->y_dtype != q->w_dtype || !W || !ws || (q->n > 0 && (!ids || !y))) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(W, dtype_bytes(q->w_dtype)) || !aligned(y, dtype_bytes(q->y_dtype)) || !aligned(ids, 4) ||
+      !aligned(ws, kAlign))
+    return FLCE_ERR_MISALIGNED;
+  if (ws_bytes < kAlign) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (q->n == 0) return cuda_status(cudaMemsetAsync(ws, 0, kAlign, s));
+  Device dev;
+  st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  return cuda_status(
+      timed(3, 0.0, s, [&] { return launch_embed_forward(ep, ids, W, y, static_cast<int*>(ws), s); }));
+}
+
+size_t flce_embedding_workspace_bytes(const flce_embedding_t* q) {
+  EmbedParams ep;
+  if (check_embedding(q, &ep) != FLCE_OK) return 0;
+  return embed_layout(ep).total;
+}
+
+flce_status_t flce_embedding_backward(const flce_embedding_t* q, const void* dy, const int32_t* ids, void* dW,
+                                      int32_t add, void* ws, size_t ws_bytes, flce_stream_t stream) {
+  EmbedParams ep;
+  flce_status_t st = check_embedding(q, &ep);
+  if (st != FLCE_OK) return st;
+  if (!dW || !ws || (q->n > 0 && (!dy || !ids)) || (add != 0 && add != 1)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(dW, dtype_bytes(q->w_dtype)) || !aligned(dy, dtype_bytes(q->y_dtype)) || !aligned(ids, 4) ||
+      !aligned(ws, kAlign))
+    return FLCE_ERR_MISALIGNED;
+  const EmbedLayout L = embed_layout(ep);
+  if (ws_bytes < L.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (q->n == 0) {
+    const size_t bytes = dtype_bytes(q->w_dtype) * static_cast<size_t>(q->v) * static_cast<size_t>(q->h);
+    if (!add && cudaMemsetAsync(dW, 0, bytes, s) != cudaSuccess) return FLCE_ERR_CUDA;
+    return cuda_status(cudaMemsetAsync(ws, 0, kAlign, s));
+  }
+  Device dev;
+  st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const EmbedSorted o{reinterpret_cast<int32_t*>(base + L.start), reinterpret_cast<int32_t*>(base + L.order),
+                      reinterpret_cast<int32_t*>(base + L.sorted_id), reinterpret_cast<float*>(base + L.part),
+                      reinterpret_cast<int*>(base)};
+  st = cuda_status(timed(3, 0.0, s, [&] { return launch_embed_sort(ep, q->padding_idx, ids, o, dev.sms, s); }));
+  if (st != FLCE_OK) return st;
+  return cuda_status(
+      timed(3, 0.0, s, [&] { return launch_embed_backward(ep, dy, o, dW, add != 0, dev.sms, s); }));
+}
+
 // ----------------------------------------------------------------------------- AdamW
 
 flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count, const flce_adamw_t* opt,

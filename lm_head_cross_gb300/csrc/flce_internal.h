@@ -349,6 +349,35 @@ cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void
                                  const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
                                  float* part, cudaStream_t stream);
 
+// Embedding (flce_embed.cu).
+constexpr int kEmbedTile = 32;  // most tokens of an id that one thread sums; more are cut into parts
+struct EmbedParams {
+  int64_t n;
+  int h;
+  int64_t v;
+  float scale;
+  bool w_f32, y_f32;  // else bf16
+};
+// The tokens other than the padding id in the order of (id, position): their positions and
+// ids, start[v + 1] of each id's, and the parts of the rows that are summed in several.
+struct EmbedSorted {
+  int32_t* start;
+  int32_t* order;
+  int32_t* sorted_id;
+  float* part;
+  int* status;
+};
+// Parts of n tokens whose rows take `row` floats: two for each tile of the sorted order.
+FLCE_HOST_DEVICE inline int64_t embed_part_floats(int64_t n, int64_t row) {
+  return n > kEmbedTile ? 2 * ((n + kEmbedTile - 1) / kEmbedTile) * row : 0;
+}
+cudaError_t launch_embed_forward(const EmbedParams& q, const int32_t* ids, const void* w, void* y, int* status,
+                                 cudaStream_t stream);
+cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, int sms,
+                              cudaStream_t stream);
+cudaError_t launch_embed_backward(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, bool add,
+                                  int sms, cudaStream_t stream);
+
 // AdamW (flce_adamw.cu).  The tensors travel as a kernel argument, so a step needs no
 // table in device memory; an argument holds at most 32764 bytes.
 constexpr int kAdamwBlock = 256;   // elements of one 8-bit scale
