@@ -512,6 +512,73 @@ typedef struct {
 flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count, const flce_adamw_t* opt,
                               const float* grad_scale, flce_stream_t stream);
 
+/* ----------------------------------------------------------------------------
+ * Muon: updates orthogonalised by Newton-Schulz products, for the matrices of a
+ * model's hidden layers (AdamW takes its embedding, head, norms and biases).
+ * A matrix u [rows, cols] becomes
+ *   X = u / (|u|_F + eps), then `steps` times
+ *   X <- a X + (b X X^T + c (X X^T)^2) X,
+ * the same odd polynomial of each singular value; (a, b, c) is given for each
+ * step.  (3.4445, -4.7750, 2.0315) five times brings singular values above
+ * about 1e-3 of the norm to between 0.7 and 1.2.
+ *   flce_orthogonalize: u is given, X is written as bf16.
+ *   flce_muon_step: with the gradient g = grad * grad_scale (a device fp32
+ *   scalar; NULL: 1) and momentum mu,
+ *     m <- mu m + (1 - mu) g,   u = mu m + (1 - mu) g (nesterov) or m,
+ *     w <- w (1 - lr weight_decay) - lr scale X.
+ *   `scale` is the caller's factor for the shape, e.g. sqrt(max(1, rows / cols)).
+ *   - Products take fp16 operands with power-of-two scales and accumulate in
+ *     fp32; rounding leaves about 1e-3 of X's norm, less than bf16's own (up to
+ *     6e-3 where most singular values are equal, so that all roundings agree).
+ *     Matrices of at most 128 rows or columns carry 22 bits.  Momentum, norm and the weights' update are fp32.
+ *   - The coefficients must keep singular values in [0, 1] within 1.95 at every
+ *     step (FLCE_ERR_INVALID_ARGUMENT otherwise).
+ *   - A matrix of zeros becomes zeros.  One with a non-finite element, or whose
+ *     squares sum past fp32's range, becomes NaN as a whole, no other does.
+ *   - Matrices are dense row-major, any number of rows and columns (the smaller
+ *     up to 65536, the larger up to 2^24; empty ones are skipped).  Pointers need the
+ *     alignment of their type.  Outputs must not overlap one another or inputs
+ *     (but out may be x where x is bf16).  Tensors are updated in place.
+ *   - matrices and tensors are HOST arrays, read before the call returns.
+ *   - ws: the workspace size below (0 if an entry is invalid), 256-byte aligned,
+ *     status word at its start: the operands of a round of matrices, about 10
+ *     bytes an element (16 up to 128 rows), up to 4 GiB unless one matrix alone
+ *     takes more. */
+#define FLCE_MUON_MAX_STEPS 16
+
+typedef struct {
+  const void* x;
+  void* out;           /* bf16 [rows, cols] */
+  int64_t rows, cols;
+  int32_t x_dtype;     /* flce_dtype_t */
+} flce_matrix_t;
+
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;       /* fp32 weights that take the step, param their rounding; or NULL */
+  float* momentum;     /* m */
+  int64_t rows, cols;
+  float lr, weight_decay, scale;
+  int32_t param_dtype; /* flce_dtype_t */
+  int32_t grad_dtype;
+} flce_muon_tensor_t;
+
+typedef struct {
+  double momentum;      /* in [0, 1); of flce_muon_step */
+  double eps;           /* >= 1e-30 */
+  const double* coefficients;  /* [steps][3]: a, b, c */
+  int32_t steps;        /* 1 to FLCE_MUON_MAX_STEPS */
+  int32_t nesterov;     /* 0 or 1; of flce_muon_step */
+} flce_muon_t;
+
+size_t flce_orthogonalize_workspace_bytes(const flce_matrix_t* matrices, int32_t count);
+flce_status_t flce_orthogonalize(const flce_matrix_t* matrices, int32_t count, const flce_muon_t* opt, void* ws,
+                                 size_t ws_bytes, flce_stream_t stream);
+size_t flce_muon_workspace_bytes(const flce_muon_tensor_t* tensors, int32_t count);
+flce_status_t flce_muon_step(const flce_muon_tensor_t* tensors, int32_t count, const flce_muon_t* opt,
+                             const float* grad_scale, void* ws, size_t ws_bytes, flce_stream_t stream);
+
 /* Static description of a status code. */
 const char* flce_status_string(flce_status_t s);
 

@@ -3,7 +3,7 @@
 Python binding over the C-ABI library ``libflce.so`` (declared in
 ``include/flce.h``).  Every step of the computation runs in the library's CUDA
 kernels; this module only marshals arguments.  See ``binding`` for the calls,
-``optim`` for AdamW and ``sharded`` for the vocabulary- and sequence-sharded loss
+``optim`` for AdamW, ``muon`` for Muon and ``sharded`` for the vocabulary- and sequence-sharded loss
 across ranks.
 """
 from .binding import (  # noqa: F401
@@ -16,5 +16,6 @@ from .binding import (  # noqa: F401
     TokenLogprobs, token_logprobs, logprobs_forward, logprobs_backward,
     token_logprobs_workspace_bytes, logprobs_backward_workspace_bytes,
 )
+from .muon import Muon, muon_plan, muon_step, orthogonalize  # noqa: F401
 from .optim import AdamW, adamw_plan, adamw_step  # noqa: F401
 from .sharded import sharded_cross_entropy  # noqa: F401

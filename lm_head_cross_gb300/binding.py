@@ -28,7 +28,8 @@ EXPORTED = ("flce_workspace_bytes", "flce_workspace_bytes_rowchunk", "flce_forwa
             "flce_shard_forward", "flce_shard_combine", "flce_shard_backward", "flce_valid_count",
             "flce_f32_to_bf16", "flce_layernorm_forward", "flce_layernorm_workspace_bytes", "flce_layernorm_backward",
             "flce_embedding_forward", "flce_embedding_workspace_bytes", "flce_embedding_backward",
-            "flce_adamw_step", "flce_token_logprobs", "flce_token_logprobs_workspace_bytes",
+            "flce_adamw_step", "flce_orthogonalize_workspace_bytes", "flce_orthogonalize", "flce_muon_workspace_bytes",
+            "flce_muon_step", "flce_token_logprobs", "flce_token_logprobs_workspace_bytes",
             "flce_token_logprobs_backward", "flce_token_logprobs_backward_workspace_bytes",
             "flce_debug_checks", "flce_selftest_bounds", "flce_status_string")
 _NO_CONTEXT = contextlib.nullcontext()
@@ -72,6 +73,24 @@ class AdamwTensor(ctypes.Structure):
 class AdamwOptions(ctypes.Structure):
     _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
                 ("step", ctypes.c_int64), ("state_bits", ctypes.c_int32)]
+
+
+class Matrix(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32)]
+
+
+class MuonTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("momentum", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("lr", ctypes.c_float), ("weight_decay", ctypes.c_float), ("scale", ctypes.c_float),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class MuonOptions(ctypes.Structure):
+    _fields_ = [("momentum", ctypes.c_double), ("eps", ctypes.c_double),
+                ("coefficients", ctypes.POINTER(ctypes.c_double)), ("steps", ctypes.c_int32),
+                ("nesterov", ctypes.c_int32)]
 
 
 def lib_path() -> str:
@@ -123,6 +142,14 @@ def lib():
     L.flce_embedding_backward.restype = ctypes.c_int
     L.flce_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), ctypes.c_int32, ctypes.POINTER(AdamwOptions), vp, vp]
     L.flce_adamw_step.restype = ctypes.c_int
+    for name, entry in (("orthogonalize", Matrix), ("muon", MuonTensor)):
+        size = getattr(L, f"flce_{name}_workspace_bytes")
+        size.argtypes, size.restype = [ctypes.POINTER(entry), ctypes.c_int32], sz
+    O = ctypes.POINTER(MuonOptions)
+    L.flce_orthogonalize.argtypes = [ctypes.POINTER(Matrix), ctypes.c_int32, O, vp, sz, vp]
+    L.flce_orthogonalize.restype = ctypes.c_int
+    L.flce_muon_step.argtypes = [ctypes.POINTER(MuonTensor), ctypes.c_int32, O, vp, vp, sz, vp]
+    L.flce_muon_step.restype = ctypes.c_int
     L.flce_token_logprobs_workspace_bytes.argtypes = [P, ctypes.c_int32]
     L.flce_token_logprobs_workspace_bytes.restype = sz
     L.flce_token_logprobs.argtypes = [P, ctypes.c_int32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]

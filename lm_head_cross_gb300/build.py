@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libflce.so")
 DEBUG_LIB = os.path.join(HERE, "libflce_debug.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["flce_kernels.cu", "flce_api.cu", "flce_noalloc.cu", "flce_norm.cu", "flce_adamw.cu",
-           "flce_decode.cu", "flce_embed.cu"]
+           "flce_decode.cu", "flce_embed.cu", "flce_muon.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

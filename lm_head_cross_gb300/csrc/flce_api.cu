@@ -172,6 +172,20 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same over [batch, outer, inner], matrices batch_bytes apart.
+bool make_map3(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t outer,
+               uint64_t batch, uint64_t pitch_bytes, uint64_t batch_bytes, uint32_t box_inner, uint32_t box_outer) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, outer, batch};
+  cuuint64_t strides[2] = {pitch_bytes, batch_bytes};
+  cuuint32_t box[3] = {box_inner, box_outer, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 uint64_t timeout_ns() {
@@ -1813,6 +1827,396 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return live <= kAdamwFewTensors ? adamw_launches<kAdamwFewTensors>(tensors, count, *opt, grad_scale, s)
                                   : adamw_launches<kAdamwManyTensors>(tensors, count, *opt, grad_scale, s);
+}
+
+// ----------------------------------------------------------------------------- Muon
+
+extern "C++" {
+namespace {
+
+// A matrix of a call, whichever entry point it came by.
+struct MuonItem {
+  int64_t rows, cols;
+  MuonMatrix to;
+  const void* grad;
+  float* momentum;
+  uint32_t flags;  // kMuonParamF32, kMuonGradF32
+  int64_t r() const { return std::min(rows, cols); }
+  int64_t c() const { return std::max(rows, cols); }
+};
+
+// Groups of one round and where their buffers lie: X (two: a product reads one and writes the
+// other) with what rounding left of it, A and P.
+struct MuonPlanGroup {
+  int64_t r, c;
+  std::vector<int> items;
+  bool exact() const { return r <= kMuonExactRows; }
+  int64_t xp() const { return (c + 7) / 8 * 8; }
+  int64_t ap() const { return (r + 7) / 8 * 8; }
+  size_t x[2], xlo[2], a, alo, p, plo;
+};
+struct MuonRound {
+  std::vector<MuonPlanGroup> groups;
+  int matrices = 0;
+  int64_t chunks = 0;
+  size_t part = 0, total = 0;
+};
+
+size_t muon_matrix_bytes(int64_t r, int64_t c) {
+  const size_t x = 2 * static_cast<size_t>(r) * static_cast<size_t>((c + 7) / 8 * 8);
+  const size_t a = 2 * static_cast<size_t>(r) * static_cast<size_t>((r + 7) / 8 * 8);
+  return r <= kMuonExactRows ? 4 * x + 4 * a : 3 * x + 2 * a;
+}
+
+constexpr size_t kMuonRoundBytes = size_t{4} << 30;  // of a round of several matrices
+
+int64_t muon_chunks(const MuonItem& m) { return (m.rows * m.cols + kMuonChunk - 1) / kMuonChunk; }
+
+// The call's matrices by shape, the largest first, cut into rounds.
+std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
+  std::vector<int> by(items.size());
+  for (size_t i = 0; i < by.size(); ++i) by[i] = static_cast<int>(i);
+  std::stable_sort(by.begin(), by.end(), [&](int i, int j) {
+    const MuonItem &x = items[i], &y = items[j];
+    return x.r() != y.r() ? x.r() > y.r() : x.c() > y.c();
+  });
+  std::vector<MuonRound> rounds;
+  size_t bytes = 0;
+  for (int i : by) {
+    const MuonItem& m = items[i];
+    if (m.rows == 0 || m.cols == 0) continue;
+    const size_t more = muon_matrix_bytes(m.r(), m.c());
+    bool same = !rounds.empty() && rounds.back().groups.back().r == m.r() && rounds.back().groups.back().c == m.c();
+    if (rounds.empty() || rounds.back().matrices == kMuonMatrices || bytes + more > kMuonRoundBytes ||
+        (!same && static_cast<int>(rounds.back().groups.size()) == kMuonGroups)) {
+      rounds.emplace_back();
+      bytes = 0;
+      same = false;
+    }
+    MuonRound& r = rounds.back();
+    if (!same) {
+      r.groups.emplace_back();
+      r.groups.back().r = m.r();
+      r.groups.back().c = m.c();
+    }
+    r.groups.back().items.push_back(i);
+    ++r.matrices;
+    r.chunks += muon_chunks(m);
+    bytes += more;
+  }
+  for (MuonRound& r : rounds) {
+    size_t off = kAlign;  // after the status word
+    auto take = [&](size_t n) {
+      const size_t at = off;
+      off = align_up(off + n);
+      return at;
+    };
+    r.part = take(sizeof(float) * static_cast<size_t>(r.chunks));
+    for (MuonPlanGroup& g : r.groups) {
+      const size_t count = g.items.size();
+      const size_t xb = 2 * count * static_cast<size_t>(g.r * g.xp()), ab = 2 * count * static_cast<size_t>(g.r * g.ap());
+      g.x[0] = take(xb);
+      g.x[1] = take(xb);
+      g.xlo[0] = take(xb);
+      g.xlo[1] = g.exact() ? take(xb) : g.xlo[0];
+      g.a = take(ab);
+      g.p = take(ab);
+      g.alo = g.exact() ? take(ab) : 0;
+      g.plo = g.exact() ? take(ab) : 0;
+    }
+    r.total = off;
+  }
+  return rounds;
+}
+
+size_t muon_bytes(const std::vector<MuonRound>& rounds) {
+  size_t most = kAlign;
+  for (const MuonRound& r : rounds) most = std::max(most, r.total);
+  return most;
+}
+
+flce_status_t check_muon_shape(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0) return FLCE_ERR_INVALID_ARGUMENT;
+  // 32-bit coordinates, tile and chunk counts
+  if (std::min(rows, cols) > 65536 || std::max(rows, cols) > (int64_t{1} << 24)) return FLCE_ERR_UNSUPPORTED_SHAPE;
+  return FLCE_OK;
+}
+
+// Scale of P in fp16: a power of two that keeps its entries, at most the largest value of
+// |a + b s^2 + c s^4| for a singular value s of X, below 2^16.  False where some step could take a
+// singular value past 1.95, beyond which A's would not fit theirs.
+bool muon_scales(const flce_muon_t& o, float* p_scale) {
+  double top = 1.0 + 1.0 / 256, p_most = 0.0;
+  for (int k = 0; k < o.steps; ++k) {
+    const double a = o.coefficients[3 * k], b = o.coefficients[3 * k + 1], c = o.coefficients[3 * k + 2];
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+    double next = 0.0;
+    constexpr int kGrid = 4096;
+    for (int i = 0; i <= kGrid; ++i) {
+      const double s = top * i / kGrid, p = std::abs(a + s * s * (b + s * s * c));
+      p_most = std::max(p_most, p);
+      next = std::max(next, p * s);
+    }
+    top = next * (1.0 + 1.0 / 256);
+    if (!(top <= 1.95) || !(p_most <= 1e4)) return false;
+  }
+  *p_scale = static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(p_most, 1e-3)))));
+  return true;
+}
+
+struct MuonMaps {
+  CUtensorMap xk[2], xlok[2], xmn[2], xlomn[2], xst[2], xlost[2];
+  CUtensorMap ak, alok, ast, alost, pk, plok, pst, plost;
+};
+
+bool muon_maps(const MuonPlanGroup& g, uint8_t* ws, MuonMaps* m) {
+  const uint64_t r = g.r, c = g.c, n = g.items.size();
+  const uint64_t xp = 2 * static_cast<uint64_t>(g.xp()), ap = 2 * static_cast<uint64_t>(g.ap());
+  auto x = [&](CUtensorMap* t, size_t at, uint32_t rows) {
+    return make_map3(t, ws + at, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c, r, n, xp, xp * r, 64, rows);
+  };
+  auto a = [&](CUtensorMap* t, size_t at, uint32_t rows) {
+    return make_map3(t, ws + at, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, r, r, n, ap, ap * r, 64, rows);
+  };
+  for (int i = 0; i < 2; ++i) {
+    if (!x(&m->xk[i], g.x[i], 128) || !x(&m->xmn[i], g.x[i], 64) || !x(&m->xst[i], g.x[i], 32)) return false;
+    if (!x(&m->xlost[i], g.xlo[i], 32)) return false;
+    if (g.exact() && (!x(&m->xlok[i], g.xlo[i], 128) || !x(&m->xlomn[i], g.xlo[i], 64))) return false;
+  }
+  if (!a(&m->ak, g.a, 128) || !a(&m->ast, g.a, 32) || !a(&m->pk, g.p, 128) || !a(&m->pst, g.p, 32)) return false;
+  return !g.exact() || (a(&m->alok, g.alo, 128) && a(&m->alost, g.alo, 32) && a(&m->plok, g.plo, 128) &&
+                        a(&m->plost, g.plo, 32));
+}
+
+// One launch's groups: product `mode` of step k.
+void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mode, int k, const flce_muon_t& o,
+               float p_scale, uint8_t* ws, MuonArgs* out) {
+  const double ca = o.coefficients[3 * k], cb = o.coefficients[3 * k + 1], cc = o.coefficients[3 * k + 2];
+  const double xs = kMuonXScale, as = kMuonAScale, ps = p_scale;
+  const int cur = k & 1;
+  out->groups = static_cast<int>(round.groups.size());
+  int tiles = 0, matrix0 = 0;
+  for (int i = 0; i < out->groups; ++i) {
+    const MuonPlanGroup& g = round.groups[i];
+    const MuonMaps& m = maps[i];
+    MuonGroup& t = out->g[i];
+    t = MuonGroup{};
+    auto half = [&](size_t at) { return reinterpret_cast<__half*>(ws + at); };
+    const int row_tiles = static_cast<int>((g.r + kPairRows - 1) / kPairRows);
+    t.r = static_cast<int>(g.r);
+    t.segments = g.exact() ? 3 : 1;
+    t.row_tiles = row_tiles;
+    if (mode == kMuonGram || mode == kMuonPoly) {
+      t.n = t.r;
+      t.tiles_each = row_tiles * (row_tiles + 1) / 2;
+      t.mir_pitch = g.ap();
+      t.mir_size = g.ap() * g.r;
+      t.write_lo = g.exact();
+      if (mode == kMuonGram) {
+        t.a = t.b = m.xk[cur];
+        if (g.exact()) t.a_lo = t.b_lo = m.xlok[cur], t.out_lo = m.alost;
+        t.out = m.ast;
+        t.kblocks = static_cast<int>((g.c + kBK - 1) / kBK);
+        t.alpha = static_cast<float>(as / (xs * xs));
+        t.mir_hi = half(g.a);
+        t.mir_lo = half(g.alo);
+      } else {
+        t.a = t.b = m.ak;
+        if (g.exact()) t.a_lo = t.b_lo = m.alok, t.out_lo = m.plost;
+        t.out = m.pst;
+        t.kblocks = static_cast<int>((g.r + kBK - 1) / kBK);
+        t.alpha = static_cast<float>(cc * ps / (as * as));
+        t.beta = static_cast<float>(cb * ps / as);
+        t.gamma = static_cast<float>(ca * ps);
+        t.in_hi = half(g.a);
+        t.in_lo = g.exact() ? half(g.alo) : nullptr;
+        t.in_pitch = g.ap();
+        t.in_size = g.ap() * g.r;
+        t.mir_hi = half(g.p);
+        t.mir_lo = half(g.plo);
+      }
+    } else {
+      t.n = static_cast<int>(g.c);
+      t.tiles_each = row_tiles * static_cast<int>((g.c + kBN - 1) / kBN);
+      t.a = m.pk;
+      t.b = m.xmn[cur];
+      if (g.exact()) t.a_lo = m.plok, t.b_lo = m.xlomn[cur];
+      t.out = m.xst[cur ^ 1];
+      t.out_lo = m.xlost[cur ^ 1];
+      t.kblocks = static_cast<int>((g.r + kBK - 1) / kBK);
+      const double unit = mode == kMuonFinal ? 1.0 / xs : 1.0;
+      t.alpha = static_cast<float>(unit / ps);
+      t.beta = static_cast<float>(unit * ca);
+      t.in_lo = !g.exact() && k < kMuonPairSteps ? half(g.xlo[0]) : nullptr;
+      t.in_pitch = g.xp();
+      t.in_size = g.xp() * g.r;
+      t.write_lo = g.exact() || k + 1 < kMuonPairSteps;
+    }
+    t.tile0 = tiles;
+    t.matrix0 = matrix0;
+    tiles += t.tiles_each * static_cast<int>(g.items.size());
+    matrix0 += static_cast<int>(g.items.size());
+  }
+  out->tiles = tiles;
+}
+
+flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o, const float* grad_scale, void* ws,
+                       size_t ws_bytes, cudaStream_t s) {
+  float p_scale = 1.f;
+  if (!muon_scales(o, &p_scale)) return FLCE_ERR_INVALID_ARGUMENT;
+  const std::vector<MuonRound> rounds = muon_rounds(items);
+  if (ws_bytes < muon_bytes(rounds)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  if (rounds.empty()) return cuda_status(cudaMemsetAsync(ws, 0, kAlign, s));
+  Device dev;
+  flce_status_t st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  for (size_t n = 0; n < rounds.size(); ++n) {
+    const MuonRound& round = rounds[n];
+    MuonSources src{};
+    MuonMatrices to{};
+    src.mu = static_cast<float>(o.momentum);
+    src.omm = static_cast<float>(1.0 - o.momentum);
+    src.nesterov = o.nesterov;
+    src.eps = static_cast<float>(o.eps);
+    src.grad_scale = grad_scale;
+    src.part = reinterpret_cast<float*>(base + round.part);
+    src.status = n == 0 ? reinterpret_cast<int*>(base) : nullptr;
+    int64_t chunks = 0, strips = 0;
+    std::vector<MuonMaps> maps(round.groups.size());
+    for (size_t i = 0; i < round.groups.size(); ++i) {
+      const MuonPlanGroup& g = round.groups[i];
+      if (!muon_maps(g, base, &maps[i])) return FLCE_ERR_CUDA;
+      for (size_t j = 0; j < g.items.size(); ++j) {
+        const MuonItem& m = items[g.items[j]];
+        MuonSource& t = src.s[src.count];
+        const int64_t size = g.r * g.xp();
+        t.grad = m.grad;
+        t.momentum = m.momentum;
+        t.hi = reinterpret_cast<__half*>(base + g.x[0]) + static_cast<int64_t>(j) * size;
+        t.lo = reinterpret_cast<__half*>(base + g.xlo[0]) + static_cast<int64_t>(j) * size;
+        t.rows = static_cast<int>(m.rows);
+        t.cols = static_cast<int>(m.cols);
+        t.pitch = static_cast<int>(g.xp());
+        t.flags = m.flags | (m.rows > m.cols ? kMuonTall : 0u);
+        t.chunk0 = static_cast<uint32_t>(chunks);
+        t.strip0 = static_cast<uint32_t>(strips);
+        chunks += muon_chunks(m);
+        strips += muon_strips(m.rows, m.cols);
+        to.m[src.count] = m.to;
+        to.m[src.count].flags = t.flags;
+        ++src.count;
+      }
+    }
+    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_momentum(src, static_cast<uint32_t>(chunks), s); }));
+    if (st != FLCE_OK) return st;
+    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_scale(src, static_cast<uint32_t>(strips), s); }));
+    if (st != FLCE_OK) return st;
+    MuonArgs args{};
+    args.timeout_ns = timeout_ns();
+    args.status = reinterpret_cast<int*>(base);
+    for (int k = 0; k < o.steps; ++k) {
+      for (int mode : {kMuonGram, kMuonPoly, k + 1 < o.steps ? kMuonApply : kMuonFinal}) {
+        muon_args(round, maps, mode, k, o, p_scale, base, &args);
+        st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_product(mode, args, to, dev.sms, s); }));
+        if (st != FLCE_OK) return st;
+      }
+    }
+  }
+  return FLCE_OK;
+}
+
+bool muon_options_ok(const flce_muon_t* o) {
+  return o && o->coefficients && o->momentum >= 0.0 && o->momentum < 1.0 && (o->nesterov == 0 || o->nesterov == 1) && o->steps >= 1 &&
+         o->steps <= FLCE_MUON_MAX_STEPS && o->eps >= 1e-30 && std::isfinite(o->eps);
+}
+
+flce_status_t muon_items(const flce_matrix_t* x, int32_t count, std::vector<MuonItem>* items) {
+  for (int i = 0; i < count; ++i) {
+    const flce_matrix_t& t = x[i];
+    flce_status_t st = check_muon_shape(t.rows, t.cols);
+    if (st != FLCE_OK) return st;
+    if (!known_dtype(t.x_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
+    MuonItem m{t.rows, t.cols, MuonMatrix{t.out, nullptr, nullptr, 0.f, 0.f, 0u}, t.x, nullptr,
+               t.x_dtype == FLCE_F32 ? kMuonGradF32 : 0u};
+    items->push_back(m);
+  }
+  return FLCE_OK;
+}
+
+flce_status_t muon_items(const flce_muon_tensor_t* x, int32_t count, std::vector<MuonItem>* items) {
+  for (int i = 0; i < count; ++i) {
+    const flce_muon_tensor_t& t = x[i];
+    flce_status_t st = check_muon_shape(t.rows, t.cols);
+    if (st != FLCE_OK) return st;
+    if (!known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
+    MuonItem m{t.rows, t.cols,
+               MuonMatrix{nullptr, t.param, t.master, static_cast<float>(1.0 - static_cast<double>(t.lr) * t.weight_decay),
+                          static_cast<float>(static_cast<double>(t.lr) * t.scale), 0u},
+               t.grad, t.momentum,
+               (t.grad_dtype == FLCE_F32 ? kMuonGradF32 : 0u) | (t.param_dtype == FLCE_F32 ? kMuonParamF32 : 0u)};
+    items->push_back(m);
+  }
+  return FLCE_OK;
+}
+
+template <typename T>
+size_t muon_workspace(const T* x, int32_t count) try {
+  std::vector<MuonItem> items;
+  if (count < 0 || (count > 0 && !x) || muon_items(x, count, &items) != FLCE_OK) return 0;
+  return muon_bytes(muon_rounds(items));
+} catch (...) {
+  return 0;
+}
+
+}  // namespace
+}  // extern "C++"
+
+size_t flce_orthogonalize_workspace_bytes(const flce_matrix_t* matrices, int32_t count) {
+  return muon_workspace(matrices, count);
+}
+size_t flce_muon_workspace_bytes(const flce_muon_tensor_t* tensors, int32_t count) {
+  return muon_workspace(tensors, count);
+}
+
+flce_status_t flce_orthogonalize(const flce_matrix_t* matrices, int32_t count, const flce_muon_t* opt, void* ws,
+                                 size_t ws_bytes, flce_stream_t stream) try {
+  if (!muon_options_ok(opt) || count < 0 || (count > 0 && !matrices) || !ws) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(ws, kAlign)) return FLCE_ERR_MISALIGNED;
+  std::vector<MuonItem> items;
+  flce_status_t st = muon_items(matrices, count, &items);
+  if (st != FLCE_OK) return st;
+  for (int i = 0; i < count; ++i) {
+    if (matrices[i].rows == 0 || matrices[i].cols == 0) continue;
+    if (!matrices[i].x || !matrices[i].out) return FLCE_ERR_INVALID_ARGUMENT;
+    if (!aligned(matrices[i].x, dtype_bytes(matrices[i].x_dtype)) || !aligned(matrices[i].out, 2))
+      return FLCE_ERR_MISALIGNED;
+  }
+  return run_muon(items, *opt, nullptr, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+} catch (...) {
+  return FLCE_ERR_CUDA;  // (host memory)
+}
+
+flce_status_t flce_muon_step(const flce_muon_tensor_t* tensors, int32_t count, const flce_muon_t* opt,
+                             const float* grad_scale, void* ws, size_t ws_bytes, flce_stream_t stream) try {
+  if (!muon_options_ok(opt) || count < 0 || (count > 0 && !tensors) || !ws) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(ws, kAlign) || !aligned(grad_scale, 4)) return FLCE_ERR_MISALIGNED;
+  std::vector<MuonItem> items;
+  flce_status_t st = muon_items(tensors, count, &items);
+  if (st != FLCE_OK) return st;
+  for (int i = 0; i < count; ++i) {
+    const flce_muon_tensor_t& t = tensors[i];
+    if (t.rows == 0 || t.cols == 0) continue;
+    if (!t.param || !t.grad || !t.momentum || !std::isfinite(t.lr) || !std::isfinite(t.weight_decay) ||
+        !std::isfinite(t.scale))
+      return FLCE_ERR_INVALID_ARGUMENT;
+    if (!aligned(t.param, dtype_bytes(t.param_dtype)) || !aligned(t.grad, dtype_bytes(t.grad_dtype)) ||
+        !aligned(t.momentum, 4) || !aligned(t.master, 4))
+      return FLCE_ERR_MISALIGNED;
+  }
+  return run_muon(items, *opt, grad_scale, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+} catch (...) {
+  return FLCE_ERR_CUDA;  // (host memory)
 }
 
 flce_status_t flce_profile_enable(int mask) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -413,6 +414,73 @@ struct AdamwArgs {
 static_assert(sizeof(AdamwArgs<kAdamwManyTensors>) <= 32764, "kernel argument limit");
 template <int N>
 cudaError_t launch_adamw(const AdamwArgs<N>& a, int state_bits, cudaStream_t stream);
+
+// Muon (flce_muon.cu).  Matrices of one shape form a group, [matrix][r][pitch] in the workspace; a
+// call runs in rounds of as many groups and matrices as the kernels' arguments hold.
+constexpr int kMuonGroups = 12;
+constexpr int kMuonMatrices = 256;
+constexpr int kMuonChunk = 8192;     // elements of one block of the momentum's pass
+constexpr int kMuonExactRows = 128;  // up to this many rows, pairs of fp16 everywhere
+constexpr int kMuonPairSteps = 3;    // else for the first iterates alone
+constexpr float kMuonXScale = 16384.f, kMuonAScale = 16384.f;
+enum MuonMode : int { kMuonGram, kMuonPoly, kMuonApply, kMuonFinal };
+enum : uint32_t { kMuonTall = 1, kMuonParamF32 = 2, kMuonGradF32 = 4 };
+// One launch's view of a group: out = alpha a b + beta in + gamma on the diagonal, [r, n].
+struct MuonGroup {
+  CUtensorMap a, b, a_lo, b_lo;  // operands, and what their rounding to fp16 left
+  CUtensorMap out, out_lo;
+  const __half *in_hi, *in_lo;   // what the epilogue adds, element by element (either may be null)
+  int64_t in_pitch, in_size;     // from one row, one matrix to the next
+  __half *mir_hi, *mir_lo;       // the output, for its tiles' other side of the diagonal
+  int64_t mir_pitch, mir_size;
+  float alpha, beta, gamma;
+  int r, n;
+  int kblocks, segments;  // 64-element steps of the contraction; 3 for hi hi + hi lo + lo hi, else 1
+  int tile0, tiles_each, row_tiles;
+  int matrix0;            // the group's first in the round's matrices
+  int write_lo;
+};
+struct MuonArgs {
+  MuonGroup g[kMuonGroups];
+  int groups, tiles;
+  uint64_t timeout_ns;
+  int* status;
+};
+// Where the last product goes: out (bf16), or w <- w decay - rate X on the weights.
+struct MuonMatrix {
+  void* out;
+  void* param;
+  float* master;
+  float decay, rate;
+  uint32_t flags;
+};
+struct MuonMatrices {
+  MuonMatrix m[kMuonMatrices];
+};
+static_assert(sizeof(MuonArgs) + sizeof(MuonMatrices) <= 32764, "kernel argument limit");
+struct MuonSource {
+  const void* grad;
+  float* momentum;  // or null: the gradient itself is what is orthogonalised
+  __half *hi, *lo;  // the internal matrix
+  int rows, cols, pitch;
+  uint32_t flags;
+  uint32_t chunk0, strip0;
+};
+struct MuonSources {
+  MuonSource s[kMuonMatrices];
+  int count;
+  float mu, omm;  // momentum and 1 - momentum
+  int nesterov;
+  float eps;
+  const float* grad_scale;
+  float* part;   // a sum of squares for each chunk
+  int* status;   // set to 0 by the momentum's pass (null: left alone)
+};
+static_assert(sizeof(MuonSources) <= 32764, "kernel argument limit");
+int64_t muon_strips(int64_t rows, int64_t cols);  // blocks of launch_muon_scale for one matrix
+cudaError_t launch_muon_momentum(const MuonSources& a, uint32_t chunks, cudaStream_t stream);
+cudaError_t launch_muon_scale(const MuonSources& a, uint32_t strips, cudaStream_t stream);
+cudaError_t launch_muon_product(int mode, const MuonArgs& a, const MuonMatrices& m, int sms, cudaStream_t stream);
 
 // Limit of every bounded wait in the kernels, in nanoseconds: FLCE_TIMEOUT_NS
 // from the environment (read once), else 4 s.
