@@ -532,7 +532,7 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
  *     6e-3 where most singular values are equal, so that all roundings agree).
  *     Matrices of at most 128 rows or columns carry 22 bits.  Momentum, norm and the weights' update are fp32.
  *   - The coefficients must keep singular values in [0, 1] within 1.95 at every
- *     step (FLCE_ERR_INVALID_ARGUMENT otherwise).
+ *     step, and c must be 0 or |b| <= 6 |c| (FLCE_ERR_INVALID_ARGUMENT otherwise).
  *   - A matrix of zeros becomes zeros.  One with a non-finite element, or whose
  *     squares sum past fp32's range, becomes NaN as a whole, no other does.
  *   - Matrices are dense row-major, any number of rows and columns (the smaller

@@ -1837,7 +1837,9 @@ namespace {
 // A matrix of a call, whichever entry point it came by.
 struct MuonItem {
   int64_t rows, cols;
-  MuonMatrix to;
+  void *out, *param;
+  float* master;
+  float decay, rate;
   const void* grad;
   float* momentum;
   uint32_t flags;  // kMuonParamF32, kMuonGradF32
@@ -1853,7 +1855,7 @@ struct MuonPlanGroup {
   bool exact() const { return r <= kMuonExactRows; }
   int64_t xp() const { return (c + 7) / 8 * 8; }
   int64_t ap() const { return (r + 7) / 8 * 8; }
-  size_t x[2], xlo[2], a, alo, p, plo;
+  size_t x[2], xlo[2], a, alo, p, plo, diag;
 };
 struct MuonRound {
   std::vector<MuonPlanGroup> groups;
@@ -1923,6 +1925,7 @@ std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
       g.p = take(ab);
       g.alo = g.exact() ? take(ab) : 0;
       g.plo = g.exact() ? take(ab) : 0;
+      g.diag = g.exact() ? 0 : take(sizeof(float) * count * static_cast<size_t>(g.r));
     }
     r.total = off;
   }
@@ -1944,12 +1947,14 @@ flce_status_t check_muon_shape(int64_t rows, int64_t cols) {
 
 // Scale of P in fp16: a power of two that keeps its entries, at most the largest value of
 // |a + b s^2 + c s^4| for a singular value s of X, below 2^16.  False where some step could take a
-// singular value past 1.95, beyond which A's would not fit theirs.
+// singular value past 1.95, or shift A's diagonal by more than 3 (b / 2c), beyond which A would
+// not fit its scale.
 bool muon_scales(const flce_muon_t& o, float* p_scale) {
   double top = 1.0 + 1.0 / 256, p_most = 0.0;
   for (int k = 0; k < o.steps; ++k) {
     const double a = o.coefficients[3 * k], b = o.coefficients[3 * k + 1], c = o.coefficients[3 * k + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+    if (c != 0.0 && std::abs(b) > 6.0 * std::abs(c)) return false;
     double next = 0.0;
     constexpr int kGrid = 4096;
     for (int i = 0; i <= kGrid; ++i) {
@@ -1964,98 +1969,99 @@ bool muon_scales(const flce_muon_t& o, float* p_scale) {
   return true;
 }
 
+// Boxes of 64 columns by 128, 64 (operands) and 32 rows (outputs) of a buffer.
+struct MuonMap {
+  CUtensorMap b128, b64, b32;
+};
 struct MuonMaps {
-  CUtensorMap xk[2], xlok[2], xmn[2], xlomn[2], xst[2], xlost[2];
-  CUtensorMap ak, alok, ast, alost, pk, plok, pst, plost;
+  MuonMap x[2], xlo[2], a, alo, p, plo;
 };
 
 bool muon_maps(const MuonPlanGroup& g, uint8_t* ws, MuonMaps* m) {
   const uint64_t r = g.r, c = g.c, n = g.items.size();
   const uint64_t xp = 2 * static_cast<uint64_t>(g.xp()), ap = 2 * static_cast<uint64_t>(g.ap());
-  auto x = [&](CUtensorMap* t, size_t at, uint32_t rows) {
-    return make_map3(t, ws + at, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c, r, n, xp, xp * r, 64, rows);
+  auto all = [&](MuonMap* t, size_t at, uint64_t cols, uint64_t pitch, bool operand) {
+    auto one = [&](CUtensorMap* q, uint32_t rows) {
+      return make_map3(q, ws + at, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, cols, r, n, pitch, pitch * r, 64, rows);
+    };
+    return one(&t->b32, 32) && (!operand || (one(&t->b128, 128) && one(&t->b64, 64)));
   };
-  auto a = [&](CUtensorMap* t, size_t at, uint32_t rows) {
-    return make_map3(t, ws + at, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, r, r, n, ap, ap * r, 64, rows);
-  };
-  for (int i = 0; i < 2; ++i) {
-    if (!x(&m->xk[i], g.x[i], 128) || !x(&m->xmn[i], g.x[i], 64) || !x(&m->xst[i], g.x[i], 32)) return false;
-    if (!x(&m->xlost[i], g.xlo[i], 32)) return false;
-    if (g.exact() && (!x(&m->xlok[i], g.xlo[i], 128) || !x(&m->xlomn[i], g.xlo[i], 64))) return false;
-  }
-  if (!a(&m->ak, g.a, 128) || !a(&m->ast, g.a, 32) || !a(&m->pk, g.p, 128) || !a(&m->pst, g.p, 32)) return false;
-  return !g.exact() || (a(&m->alok, g.alo, 128) && a(&m->alost, g.alo, 32) && a(&m->plok, g.plo, 128) &&
-                        a(&m->plost, g.plo, 32));
+  for (int i = 0; i < 2; ++i)
+    if (!all(&m->x[i], g.x[i], c, xp, true) || !all(&m->xlo[i], g.xlo[i], c, xp, g.exact())) return false;
+  if (!all(&m->a, g.a, r, ap, true) || !all(&m->p, g.p, r, ap, true)) return false;
+  return !g.exact() || (all(&m->alo, g.alo, r, ap, true) && all(&m->plo, g.plo, r, ap, true));
+}
+
+int64_t muon_tiles_each(const MuonPlanGroup& g, int mode, int bn) {
+  const int64_t rows = (g.r + kPairRows - 1) / kPairRows, per = kPairRows / bn;
+  if (mode == kMuonApply) return rows * ((g.c + bn - 1) / bn);
+  const int64_t cols = (g.r + bn - 1) / bn;  // the tiles from the diagonal on
+  return rows * cols - per * rows * (rows - 1) / 2;
+}
+
+// Columns of a launch's tiles: 128 where there are fewer 256-wide ones than CTA pairs.
+int muon_tile_width(const MuonRound& round, int mode, int sms) {
+  int64_t tiles = 0;
+  for (const MuonPlanGroup& g : round.groups) tiles += muon_tiles_each(g, mode, 256) * static_cast<int64_t>(g.items.size());
+  return tiles < sms / 2 ? 128 : 256;
 }
 
 // One launch's groups: product `mode` of step k.
-void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mode, int k, const flce_muon_t& o,
-               float p_scale, uint8_t* ws, MuonArgs* out) {
+void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mode, int k, int bn,
+               const flce_muon_t& o, float p_scale, uint8_t* ws, MuonArgs* out) {
   const double ca = o.coefficients[3 * k], cb = o.coefficients[3 * k + 1], cc = o.coefficients[3 * k + 2];
   const double xs = kMuonXScale, as = kMuonAScale, ps = p_scale;
   const int cur = k & 1;
   out->groups = static_cast<int>(round.groups.size());
-  int tiles = 0, matrix0 = 0;
+  int tiles = 0;
   for (int i = 0; i < out->groups; ++i) {
     const MuonPlanGroup& g = round.groups[i];
     const MuonMaps& m = maps[i];
     MuonGroup& t = out->g[i];
     t = MuonGroup{};
-    auto half = [&](size_t at) { return reinterpret_cast<__half*>(ws + at); };
-    const int row_tiles = static_cast<int>((g.r + kPairRows - 1) / kPairRows);
+    auto operand = [&](CUtensorMap* b128, CUtensorMap* b64, const MuonMap& from) {
+      *b128 = from.b128;
+      *b64 = from.b64;
+    };
+    auto operands = [&](const MuonMap& a, const MuonMap& alo, const MuonMap& b, const MuonMap& blo) {
+      operand(&t.a128, &t.a64, a);
+      operand(&t.b128, &t.b64, b);
+      if (!g.exact()) return;
+      operand(&t.a_lo128, &t.a_lo64, alo);
+      operand(&t.b_lo128, &t.b_lo64, blo);
+    };
     t.r = static_cast<int>(g.r);
+    t.n = static_cast<int>(mode == kMuonApply ? g.c : g.r);
     t.segments = g.exact() ? 3 : 1;
-    t.row_tiles = row_tiles;
-    if (mode == kMuonGram || mode == kMuonPoly) {
-      t.n = t.r;
-      t.tiles_each = row_tiles * (row_tiles + 1) / 2;
-      t.mir_pitch = g.ap();
-      t.mir_size = g.ap() * g.r;
-      t.write_lo = g.exact();
-      if (mode == kMuonGram) {
-        t.a = t.b = m.xk[cur];
-        if (g.exact()) t.a_lo = t.b_lo = m.xlok[cur], t.out_lo = m.alost;
-        t.out = m.ast;
-        t.kblocks = static_cast<int>((g.c + kBK - 1) / kBK);
-        t.alpha = static_cast<float>(as / (xs * xs));
-        t.mir_hi = half(g.a);
-        t.mir_lo = half(g.alo);
-      } else {
-        t.a = t.b = m.ak;
-        if (g.exact()) t.a_lo = t.b_lo = m.alok, t.out_lo = m.plost;
-        t.out = m.pst;
-        t.kblocks = static_cast<int>((g.r + kBK - 1) / kBK);
-        t.alpha = static_cast<float>(cc * ps / (as * as));
-        t.beta = static_cast<float>(cb * ps / as);
-        t.gamma = static_cast<float>(ca * ps);
-        t.in_hi = half(g.a);
-        t.in_lo = g.exact() ? half(g.alo) : nullptr;
-        t.in_pitch = g.ap();
-        t.in_size = g.ap() * g.r;
-        t.mir_hi = half(g.p);
-        t.mir_lo = half(g.plo);
-      }
+    t.row_tiles = static_cast<int>((g.r + kPairRows - 1) / kPairRows);
+    t.kblocks = static_cast<int>(((mode == kMuonGram ? g.c : g.r) + kBK - 1) / kBK);
+    t.write_lo = g.exact();
+    t.diag = g.exact() || cc == 0.0 ? nullptr : reinterpret_cast<float*>(ws + g.diag);
+    if (mode == kMuonGram) {
+      operands(m.x[cur], m.xlo[cur], m.x[cur], m.xlo[cur]);
+      const bool poly = cc != 0.0;
+      t.out = poly ? m.a.b32 : m.p.b32;
+      t.out_lo = poly ? m.alo.b32 : m.plo.b32;
+      t.alpha = static_cast<float>((poly ? as : cb * ps) / (xs * xs));
+      t.gamma = static_cast<float>(poly ? as * cb / (2.0 * cc) : ca * ps);
+    } else if (mode == kMuonPoly) {
+      operands(m.a, m.alo, m.a, m.alo);
+      t.out = m.p.b32;
+      t.out_lo = m.plo.b32;
+      t.alpha = static_cast<float>(cc * ps / (as * as));
+      t.gamma = static_cast<float>((ca - cb * cb / (4.0 * cc)) * ps);
     } else {
-      t.n = static_cast<int>(g.c);
-      t.tiles_each = row_tiles * static_cast<int>((g.c + kBN - 1) / kBN);
-      t.a = m.pk;
-      t.b = m.xmn[cur];
-      if (g.exact()) t.a_lo = m.plok, t.b_lo = m.xlomn[cur];
-      t.out = m.xst[cur ^ 1];
-      t.out_lo = m.xlost[cur ^ 1];
-      t.kblocks = static_cast<int>((g.r + kBK - 1) / kBK);
-      const double unit = mode == kMuonFinal ? 1.0 / xs : 1.0;
-      t.alpha = static_cast<float>(unit / ps);
-      t.beta = static_cast<float>(unit * ca);
-      t.in_lo = !g.exact() && k < kMuonPairSteps ? half(g.xlo[0]) : nullptr;
-      t.in_pitch = g.xp();
-      t.in_size = g.xp() * g.r;
-      t.write_lo = g.exact() || k + 1 < kMuonPairSteps;
+      operands(m.p, m.plo, m.x[cur], m.xlo[cur]);
+      t.out = m.x[cur ^ 1].b32;
+      t.out_lo = m.xlo[cur ^ 1].b32;
+      t.alpha = static_cast<float>(1.0 / ps);
+      t.beta = static_cast<float>(ca);
+      t.lo_in = !g.exact() && k < kMuonPairSteps;
+      t.write_lo = g.exact() || (k + 1 < kMuonPairSteps && k + 1 < o.steps);
     }
+    t.tiles_each = static_cast<int>(muon_tiles_each(g, mode, bn));
     t.tile0 = tiles;
-    t.matrix0 = matrix0;
     tiles += t.tiles_each * static_cast<int>(g.items.size());
-    matrix0 += static_cast<int>(g.items.size());
   }
   out->tiles = tiles;
 }
@@ -2074,7 +2080,7 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
   for (size_t n = 0; n < rounds.size(); ++n) {
     const MuonRound& round = rounds[n];
     MuonSources src{};
-    MuonMatrices to{};
+    MuonTargets to{};
     src.mu = static_cast<float>(o.momentum);
     src.omm = static_cast<float>(1.0 - o.momentum);
     src.nesterov = o.nesterov;
@@ -2089,25 +2095,43 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
       if (!muon_maps(g, base, &maps[i])) return FLCE_ERR_CUDA;
       for (size_t j = 0; j < g.items.size(); ++j) {
         const MuonItem& m = items[g.items[j]];
+        const size_t at = j * static_cast<size_t>(g.r * g.xp());
+        auto half = [&](size_t buf) { return reinterpret_cast<__half*>(base + buf) + at; };
+        const size_t ga = m.flags & kMuonGradF32 ? 16 : 8, pa = m.flags & kMuonParamF32 ? 16 : 8;
+        const bool source4 = aligned(m.grad, ga) && aligned(m.momentum, 16);
+        const bool target4 = aligned(m.out, 8) && aligned(m.param, pa) && aligned(m.master, 16);
+        const uint32_t flags = m.flags | (m.rows > m.cols ? kMuonTall : 0u);
         MuonSource& t = src.s[src.count];
-        const int64_t size = g.r * g.xp();
         t.grad = m.grad;
         t.momentum = m.momentum;
-        t.hi = reinterpret_cast<__half*>(base + g.x[0]) + static_cast<int64_t>(j) * size;
-        t.lo = reinterpret_cast<__half*>(base + g.xlo[0]) + static_cast<int64_t>(j) * size;
+        t.hi = half(g.x[0]);
+        t.lo = half(g.xlo[0]);
         t.rows = static_cast<int>(m.rows);
         t.cols = static_cast<int>(m.cols);
         t.pitch = static_cast<int>(g.xp());
-        t.flags = m.flags | (m.rows > m.cols ? kMuonTall : 0u);
+        t.flags = flags | (source4 ? kMuonAligned : 0u) | (source4 && m.cols % 4 == 0 ? kMuonAlignedRows : 0u);
         t.chunk0 = static_cast<uint32_t>(chunks);
         t.strip0 = static_cast<uint32_t>(strips);
+        MuonTarget& w = to.t[src.count];
+        w.hi = half(g.x[o.steps & 1]);
+        w.lo = g.exact() ? half(g.xlo[o.steps & 1]) : nullptr;
+        w.out = m.out;
+        w.param = m.param;
+        w.master = m.master;
+        w.decay = m.decay;
+        w.rate = m.rate;
+        w.rows = t.rows;
+        w.cols = t.cols;
+        w.pitch = t.pitch;
+        w.flags = flags | (target4 && m.cols % 4 == 0 ? kMuonAlignedRows : 0u);
+        w.strip0 = t.strip0;
         chunks += muon_chunks(m);
         strips += muon_strips(m.rows, m.cols);
-        to.m[src.count] = m.to;
-        to.m[src.count].flags = t.flags;
         ++src.count;
       }
     }
+    to.count = src.count;
+    if (chunks > INT32_MAX || strips > INT32_MAX) return FLCE_ERR_UNSUPPORTED_SHAPE;
     st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_momentum(src, static_cast<uint32_t>(chunks), s); }));
     if (st != FLCE_OK) return st;
     st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_scale(src, static_cast<uint32_t>(strips), s); }));
@@ -2116,12 +2140,16 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
     args.timeout_ns = timeout_ns();
     args.status = reinterpret_cast<int*>(base);
     for (int k = 0; k < o.steps; ++k) {
-      for (int mode : {kMuonGram, kMuonPoly, k + 1 < o.steps ? kMuonApply : kMuonFinal}) {
-        muon_args(round, maps, mode, k, o, p_scale, base, &args);
-        st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_product(mode, args, to, dev.sms, s); }));
+      for (int mode : {kMuonGram, kMuonPoly, kMuonApply}) {
+        if (mode == kMuonPoly && o.coefficients[3 * k + 2] == 0.0) continue;  // (kGram wrote P)
+        const int bn = muon_tile_width(round, mode, dev.sms);
+        muon_args(round, maps, mode, k, bn, o, p_scale, base, &args);
+        st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_product(mode, bn, args, dev.sms, s); }));
         if (st != FLCE_OK) return st;
       }
     }
+    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_weights(to, static_cast<uint32_t>(strips), s); }));
+    if (st != FLCE_OK) return st;
   }
   return FLCE_OK;
 }
@@ -2137,8 +2165,7 @@ flce_status_t muon_items(const flce_matrix_t* x, int32_t count, std::vector<Muon
     flce_status_t st = check_muon_shape(t.rows, t.cols);
     if (st != FLCE_OK) return st;
     if (!known_dtype(t.x_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
-    MuonItem m{t.rows, t.cols, MuonMatrix{t.out, nullptr, nullptr, 0.f, 0.f, 0u}, t.x, nullptr,
-               t.x_dtype == FLCE_F32 ? kMuonGradF32 : 0u};
+    MuonItem m{t.rows, t.cols, t.out, nullptr, nullptr, 0.f, 0.f, t.x, nullptr, t.x_dtype == FLCE_F32 ? kMuonGradF32 : 0u};
     items->push_back(m);
   }
   return FLCE_OK;
@@ -2150,10 +2177,9 @@ flce_status_t muon_items(const flce_muon_tensor_t* x, int32_t count, std::vector
     flce_status_t st = check_muon_shape(t.rows, t.cols);
     if (st != FLCE_OK) return st;
     if (!known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
-    MuonItem m{t.rows, t.cols,
-               MuonMatrix{nullptr, t.param, t.master, static_cast<float>(1.0 - static_cast<double>(t.lr) * t.weight_decay),
-                          static_cast<float>(static_cast<double>(t.lr) * t.scale), 0u},
-               t.grad, t.momentum,
+    MuonItem m{t.rows, t.cols, nullptr, t.param, t.master,
+               static_cast<float>(1.0 - static_cast<double>(t.lr) * t.weight_decay),
+               static_cast<float>(static_cast<double>(t.lr) * t.scale), t.grad, t.momentum,
                (t.grad_dtype == FLCE_F32 ? kMuonGradF32 : 0u) | (t.param_dtype == FLCE_F32 ? kMuonParamF32 : 0u)};
     items->push_back(m);
   }

@@ -422,23 +422,27 @@ constexpr int kMuonMatrices = 256;
 constexpr int kMuonChunk = 8192;     // elements of one block of the momentum's pass
 constexpr int kMuonExactRows = 128;  // up to this many rows, pairs of fp16 everywhere
 constexpr int kMuonPairSteps = 3;    // else for the first iterates alone
-constexpr float kMuonXScale = 16384.f, kMuonAScale = 16384.f;
-enum MuonMode : int { kMuonGram, kMuonPoly, kMuonApply, kMuonFinal };
-enum : uint32_t { kMuonTall = 1, kMuonParamF32 = 2, kMuonGradF32 = 4 };
-// One launch's view of a group: out = alpha a b + beta in + gamma on the diagonal, [r, n].
+constexpr float kMuonXScale = 16384.f, kMuonAScale = 8192.f;
+enum MuonMode : int { kMuonGram, kMuonPoly, kMuonApply };
+enum : uint32_t {
+  kMuonTall = 1,
+  kMuonParamF32 = 2,
+  kMuonGradF32 = 4,
+  kMuonAligned = 8,      // gradient and momentum: four elements at a time from the start on
+  kMuonAlignedRows = 16  // every tensor of the matrix, and its rows are whole numbers of four
+};
+// One launch's view of a group: out = alpha a b, + gamma (and in kPoly alpha diag) on the diagonal,
+// + beta lo; [r, n].  Operands in boxes of 64 columns by 128 and by 64 rows.
 struct MuonGroup {
-  CUtensorMap a, b, a_lo, b_lo;  // operands, and what their rounding to fp16 left
+  CUtensorMap a128, a64, b128, b64;
+  CUtensorMap a_lo128, a_lo64, b_lo128, b_lo64;  // what their rounding to fp16 left (segments = 3)
   CUtensorMap out, out_lo;
-  const __half *in_hi, *in_lo;   // what the epilogue adds, element by element (either may be null)
-  int64_t in_pitch, in_size;     // from one row, one matrix to the next
-  __half *mir_hi, *mir_lo;       // the output, for its tiles' other side of the diagonal
-  int64_t mir_pitch, mir_size;
+  float* diag;  // [matrix][r], for the square: what rounding the diagonal left (null: nothing)
   float alpha, beta, gamma;
   int r, n;
   int kblocks, segments;  // 64-element steps of the contraction; 3 for hi hi + hi lo + lo hi, else 1
   int tile0, tiles_each, row_tiles;
-  int matrix0;            // the group's first in the round's matrices
-  int write_lo;
+  int lo_in, write_lo;    // add beta times out_lo's old values; write out_lo
 };
 struct MuonArgs {
   MuonGroup g[kMuonGroups];
@@ -446,18 +450,7 @@ struct MuonArgs {
   uint64_t timeout_ns;
   int* status;
 };
-// Where the last product goes: out (bf16), or w <- w decay - rate X on the weights.
-struct MuonMatrix {
-  void* out;
-  void* param;
-  float* master;
-  float decay, rate;
-  uint32_t flags;
-};
-struct MuonMatrices {
-  MuonMatrix m[kMuonMatrices];
-};
-static_assert(sizeof(MuonArgs) + sizeof(MuonMatrices) <= 32764, "kernel argument limit");
+static_assert(sizeof(MuonArgs) <= 32764, "kernel argument limit");
 struct MuonSource {
   const void* grad;
   float* momentum;  // or null: the gradient itself is what is orthogonalised
@@ -477,10 +470,27 @@ struct MuonSources {
   int* status;   // set to 0 by the momentum's pass (null: left alone)
 };
 static_assert(sizeof(MuonSources) <= 32764, "kernel argument limit");
-int64_t muon_strips(int64_t rows, int64_t cols);  // blocks of launch_muon_scale for one matrix
+// Where X goes: out (bf16), or w <- w decay - rate X on the weights.
+struct MuonTarget {
+  const __half *hi, *lo;  // (lo may be null)
+  void* out;
+  void* param;
+  float* master;
+  float decay, rate;
+  int rows, cols, pitch;
+  uint32_t flags, strip0;
+};
+struct MuonTargets {
+  MuonTarget t[kMuonMatrices];
+  int count;
+};
+static_assert(sizeof(MuonTargets) <= 32764, "kernel argument limit");
+int64_t muon_strips(int64_t rows, int64_t cols);  // blocks of the scale's and the weights' launch for one matrix
 cudaError_t launch_muon_momentum(const MuonSources& a, uint32_t chunks, cudaStream_t stream);
 cudaError_t launch_muon_scale(const MuonSources& a, uint32_t strips, cudaStream_t stream);
-cudaError_t launch_muon_product(int mode, const MuonArgs& a, const MuonMatrices& m, int sms, cudaStream_t stream);
+cudaError_t launch_muon_weights(const MuonTargets& a, uint32_t strips, cudaStream_t stream);
+// bn: columns of a tile, 256 or 128.
+cudaError_t launch_muon_product(int mode, int bn, const MuonArgs& a, int sms, cudaStream_t stream);
 
 // Limit of every bounded wait in the kernels, in nanoseconds: FLCE_TIMEOUT_NS
 // from the environment (read once), else 4 s.

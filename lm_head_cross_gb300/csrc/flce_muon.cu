@@ -9,23 +9,31 @@
 // above about 1e-3 of the norm to between 0.7 and 1.2.
 //
 // Products: tcgen05 on CTA pairs, 256 x 256 tiles of fp16 operands with fp32 accumulators, three
-// launches a step (kGram, kPoly, kApply), each over every matrix of the call.  A and P are
-// symmetric: tiles on and above the diagonal are computed and written to both sides, half the
-// operations of two of the three products.
+// launches a step (kGram, kPoly, kApply), each over every matrix of the call.
+//
+// A and P are symmetric: half the operations of two of the three products are done, the tiles on
+// and above the diagonal, and only they are stored.  A step of a contraction that needs a block
+// below it loads the block above as the transposed operand it is (MN-major), so nothing is written
+// twice.
+//
+// kGram stores A + (b / 2c) I, whose square gives P without another look at A:
+//   P = c (A + (b / 2c) I)^2 + (a - b^2 / 4c) I   (c = 0: kGram stores P = a I + b A itself).
+// What rounding the diagonal to fp16 leaves, up to 2^-11 of b / 2c where A's own is far smaller, is
+// kept in fp32 for P's diagonal.
 //
 // fp16, not bf16: singular values stay below 2 whatever the input, so that every scale is a power
-// of two known beforehand (X 2^14, A 2^14, P by its polynomial's largest value) and the 3 bits
+// of two known beforehand (X 2^14, A 2^13, P by its polynomial's largest value) and the 3 bits
 // more are free: rounding errors, which the steps amplify, leave 1e-3 of the result's norm, less
 // than its own rounding to bf16 (1.7e-3); bf16 operands would leave 1e-2.
 //
 // A rounded X also carries noise of 2^-12 of its strong directions into its weak ones, which then
 // grow faster, by up to a in each step (|u| of rank 8 with 2% of noise: 1.4e-2 of the result).
-// So the first kMuonPairSteps iterates are kept as a pair hi + lo of fp16, 22 bits.  The products use
-// hi alone and the epilogue adds a lo: what P lo - a lo would add lies along the strong directions
-// themselves, where it does no harm (1.0e-3 of the result then).
+// So the first kMuonPairSteps iterates are kept as a pair hi + lo of fp16, 22 bits.  The products
+// use hi alone and the epilogue adds a lo: what P lo - a lo would add lies along the strong
+// directions themselves, where it does no harm (1.0e-3 of the result then).
 //
-// Matrices of at most kMuonExactRows rows average few rounding errors (8 x 8: 4e-3) and cost little:
-// all of X, A and P are pairs there, each product hi hi + hi lo + lo hi.
+// Matrices of at most kMuonExactRows rows average few rounding errors (8 x 8: 4e-3) and cost
+// little: all of X, A and P are pairs there, each product hi hi + hi lo + lo hi.
 #include <cuda_fp16.h>
 
 #include "flce_device.cuh"
@@ -37,25 +45,29 @@ namespace flce {
 namespace {
 
 constexpr int kPairM = 2 * kBM;
-constexpr int kHalfN = kBN / 2;
 constexpr int kAStage = kBM * kBK * 2;
-constexpr int kBStage = kHalfN * kBK * 2;
-constexpr int kStageBytes = kAStage + kBStage;
 constexpr int kMnBlock = 64 * kBK * 2;  // 64 columns of 64 K rows
 constexpr int kStagingBuf = 32 * 128;
 constexpr int kStagingPerWarp = 2 * kStagingBuf;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;  // two for each quarter of the TMEM lanes, each half of a tile's columns
 constexpr int kProductThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr uint16_t kPairMask = 0x3;
-constexpr int kSmemStagingOff = kStages * kStageBytes;
-constexpr int kSmemBarOff = kSmemStagingOff + kEpiWarps * kStagingPerWarp;
-constexpr int kSmemBytes = kSmemBarOff + 256 + 1024;
-static_assert(kSmemBytes <= 232448 && (2 * kStages + 6) * 8 <= 256, "shared memory budget");
+
+// Tiles of 256 x BN.  BN = 128 where 256 x 256 tiles are fewer than the CTA pairs.
+template <int BN>
+struct Shape {
+  static constexpr int kHalfN = BN / 2;  // B rows that each CTA stages
+  static constexpr int kStageBytes = kAStage + kHalfN * kBK * 2;
+  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr int kSmemStagingOff = kStages * kStageBytes;
+  static constexpr int kSmemBarOff = kSmemStagingOff + kEpiWarps * kStagingPerWarp;
+  static constexpr int kSmemBytes = kSmemBarOff + 256 + 1024;
+  static_assert(kSmemBytes <= 232448 && (2 * kStages + 6 + kEpiWarps) * 8 <= 256, "shared memory budget");
+};
 
 // fp16 operands: formats 0 (see instr_desc_bf16).
-__host__ __device__ constexpr uint32_t instr_desc_f16(int m, int n, bool b_mn) {
-  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+__host__ __device__ constexpr uint32_t instr_desc_f16(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 
@@ -65,6 +77,14 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
       "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t x, int32_t y, int32_t z) {
@@ -84,15 +104,13 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t w) {
 
 // ----------------------------------------------------------------------------- products
 
-// A tile of the launch: which group, which of its matrices, this CTA's first row, the tile's first
-// column, and whether it is written to the other side of the diagonal as well.
+// A tile of the launch: its group, which of its matrices, this CTA's first row, the first column.
 struct Tile {
   const MuonGroup* g;
   int matrix, m0, n0;
-  bool mirror;
 };
 
-template <int MODE>
+template <int MODE, int BN>
 __device__ __forceinline__ bool find_tile(const MuonArgs& a, int t, uint32_t rank, Tile& o) {
   if (t >= a.tiles) return false;
   int gi = 0;
@@ -102,25 +120,27 @@ __device__ __forceinline__ bool find_tile(const MuonArgs& a, int t, uint32_t ran
   o.g = &g;
   o.matrix = t / g.tiles_each;
   t -= o.matrix * g.tiles_each;
-  int ti, tj;
-  if (MODE == kMuonGram || MODE == kMuonPoly) {  // (ti, tj) with ti <= tj, tj (tj + 1) / 2 + ti = t
-    tj = static_cast<int>((sqrtf(8.f * static_cast<float>(t) + 1.f) - 1.f) * 0.5f);
-    while (tj * (tj + 1) / 2 > t) --tj;
-    while ((tj + 1) * (tj + 2) / 2 <= t) ++tj;
-    ti = t - tj * (tj + 1) / 2;
-    o.mirror = ti != tj;
-  } else {  // a column of tiles shares its part of X
+  int ti = 0, tj;
+  if (MODE == kMuonApply) {  // a column of tiles shares its part of X
     ti = t % g.row_tiles;
     tj = t / g.row_tiles;
-    o.mirror = false;
+  } else {  // the tiles of row ti from the diagonal on
+    constexpr int kPer = kPairM / BN;
+    const int cols = (g.r + BN - 1) / BN;
+    while (t >= cols - kPer * ti) t -= cols - kPer * ti++;
+    tj = kPer * ti + t;
   }
   o.m0 = ti * kPairM + static_cast<int>(rank) * kBM;
-  o.n0 = tj * kBN;
+  o.n0 = tj * BN;
   return true;
 }
 
+// Whether rows of the 256-row block that holds `row` are stored at column k0 of a symmetric
+// matrix; else the block's transpose is.
+__device__ __forceinline__ bool stored(int row, int k0) { return k0 >= (row & ~(kPairM - 1)); }
+
 struct Bars {
-  uint64_t *full, *empty, *tfull, *tempty;
+  uint64_t *full, *empty, *tfull, *tempty, *ebar;
   volatile int* abort_flag;
 };
 
@@ -130,37 +150,47 @@ __device__ __forceinline__ void record_timeout(const MuonArgs& a, uint32_t rank,
   atomicCAS(a.status, 0, kErrTimeout);
 }
 
-template <int MODE>
+// Inner coordinates are multiples of 64 elements: every copy starts on a 128-byte boundary.
+template <int MODE, int BN>
 __device__ void run_producer(const MuonArgs& a, uint32_t rank, int pair, int pairs, uint8_t* smem, const Bars& b) {
+  using S = Shape<BN>;
   const uint32_t full_even = mapa_shared(smem_u32(b.full), 0);
-  const int bhalf = static_cast<int>(rank) * kHalfN;
+  const int bhalf = static_cast<int>(rank) * S::kHalfN;
   int stage = 0;
   uint32_t phase = 0;
   Tile t;
-  for (int i = pair; find_tile<MODE>(a, i, rank, t); i += pairs) {
+  for (int i = pair; find_tile<MODE, BN>(a, i, rank, t); i += pairs) {
     const MuonGroup& g = *t.g;
+    const int n0 = t.n0 + bhalf;
     for (int seg = 0; seg < g.segments; ++seg) {  // hi hi, hi lo, lo hi
-      const CUtensorMap* ma = seg == 2 ? &g.a_lo : &g.a;
-      const CUtensorMap* mb = seg == 1 ? &g.b_lo : &g.b;
+      const CUtensorMap* a128 = seg == 2 ? &g.a_lo128 : &g.a128;
+      const CUtensorMap* a64 = seg == 2 ? &g.a_lo64 : &g.a64;
+      const CUtensorMap* b128 = seg == 1 ? &g.b_lo128 : &g.b128;
+      const CUtensorMap* b64 = seg == 1 ? &g.b_lo64 : &g.b64;
       for (int kb = 0; kb < g.kblocks; ++kb) {
         if (!mbar_wait(&b.empty[stage], phase ^ 1u, a.timeout_ns, b.abort_flag)) {
           record_timeout(a, rank, b.abort_flag);
           return;
         }
-        uint8_t* sa = smem + stage * kStageBytes;
+        uint8_t* sa = smem + stage * S::kStageBytes;
         uint8_t* sb = sa + kAStage;
         const uint32_t bar = full_even + 8u * stage;
-        if (rank == 0) mbar_arrive_expect_tx(&b.full[stage], 2 * kStageBytes);
-        const int k0 = kb * kBK;  // (64-element steps, so every inner coordinate is on a 128-byte boundary)
-        tma_load_3d_pair(sa, ma, bar, k0, t.m0, t.matrix);
-        if (MODE == kMuonGram || MODE == kMuonPoly) {
-          tma_load_3d_pair(sb, mb, bar, k0, t.n0 + bhalf, t.matrix);
+        if (rank == 0) mbar_arrive_expect_tx(&b.full[stage], 2 * S::kStageBytes);
+        const int k0 = kb * kBK;
+        if (MODE == kMuonGram || stored(t.m0, k0)) {
+          tma_load_3d_pair(sa, a128, bar, k0, t.m0, t.matrix);
+        } else {
+          tma_load_3d_pair(sa, a64, bar, t.m0, k0, t.matrix);
+          tma_load_3d_pair(sa + kMnBlock, a64, bar, t.m0 + 64, k0, t.matrix);
+        }
+        if (MODE == kMuonGram || (MODE == kMuonPoly && stored(t.n0, k0))) {
+          tma_load_3d_pair(sb, BN == 256 ? b128 : b64, bar, k0, n0, t.matrix);
         } else {
 #pragma unroll
-          for (int j = 0; j < kHalfN / 64; ++j)
-            tma_load_3d_pair(sb + j * kMnBlock, mb, bar, t.n0 + bhalf + 64 * j, k0, t.matrix);
+          for (int j = 0; j < S::kHalfN / 64; ++j)
+            tma_load_3d_pair(sb + j * kMnBlock, b64, bar, n0 + 64 * j, k0, t.matrix);
         }
-        if (++stage == kStages) {
+        if (++stage == S::kStages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -169,39 +199,44 @@ __device__ void run_producer(const MuonArgs& a, uint32_t rank, int pair, int pai
   }
 }
 
-template <int MODE>
+template <int MODE, int BN>
 __device__ void run_mma(const MuonArgs& a, int pair, int pairs, uint8_t* smem, uint32_t tmem_base, const Bars& b) {
-  constexpr bool b_mn = MODE == kMuonApply || MODE == kMuonFinal;
-  constexpr uint32_t idesc = instr_desc_f16(kPairM, kBN, b_mn);
+  using S = Shape<BN>;
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
   Tile t;
-  for (int i = pair; find_tile<MODE>(a, i, 0, t); i += pairs) {
+  for (int i = pair; find_tile<MODE, BN>(a, i, 0, t); i += pairs) {
     if (!mbar_wait(&b.tempty[acc], acc_phase ^ 1u, a.timeout_ns, b.abort_flag)) {
       record_timeout(a, 0, b.abort_flag);
       return;
     }
     tc_fence_after_sync();
-    const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
-    const int steps = t.g->segments * t.g->kblocks;
-    for (int kb = 0; kb < steps; ++kb) {
-      if (!mbar_wait(&b.full[stage], phase, a.timeout_ns, b.abort_flag)) {
-        record_timeout(a, 0, b.abort_flag);
-        return;
-      }
-      tc_fence_after_sync();
-      const uint32_t sa = smem_u32(smem + stage * kStageBytes);
-      const uint32_t sb = sa + kAStage;
+    const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+    uint32_t more = 0;
+    for (int seg = 0; seg < t.g->segments; ++seg) {
+      for (int kb = 0; kb < t.g->kblocks; ++kb) {
+        const bool a_mn = MODE != kMuonGram && !stored(t.m0, kb * kBK);
+        const bool b_mn = MODE == kMuonApply || (MODE == kMuonPoly && !stored(t.n0, kb * kBK));
+        const uint32_t idesc = instr_desc_f16(kPairM, BN, a_mn, b_mn);
+        if (!mbar_wait(&b.full[stage], phase, a.timeout_ns, b.abort_flag)) {
+          record_timeout(a, 0, b.abort_flag);
+          return;
+        }
+        tc_fence_after_sync();
+        const uint32_t sa = smem_u32(smem + stage * S::kStageBytes);
+        const uint32_t sb = sa + kAStage;
 #pragma unroll
-      for (int k = 0; k < kBK / 16; ++k) {
-        const uint64_t ad = smem_desc_sw128(sa + k * 32, 16, 1024);
-        const uint64_t bd = b_mn ? smem_desc_sw128(sb + k * 2048, kMnBlock, 1024) : smem_desc_sw128(sb + k * 32, 16, 1024);
-        umma_bf16_pair(d, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);  // (kind::f16: idesc names the type)
-      }
-      umma_commit_pair(&b.empty[stage], kPairMask);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1u;
+        for (int k = 0; k < kBK / 16; ++k) {
+          const uint64_t ad = a_mn ? smem_desc_sw128(sa + k * 2048, kMnBlock, 1024) : smem_desc_sw128(sa + k * 32, 16, 1024);
+          const uint64_t bd = b_mn ? smem_desc_sw128(sb + k * 2048, kMnBlock, 1024) : smem_desc_sw128(sb + k * 32, 16, 1024);
+          umma_bf16_pair(d, ad, bd, idesc, more);  // (kind::f16: idesc names the type)
+          more = 1;
+        }
+        umma_commit_pair(&b.empty[stage], kPairMask);
+        if (++stage == S::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     umma_commit_pair(&b.tfull[acc], kPairMask);
@@ -210,203 +245,128 @@ __device__ void run_mma(const MuonArgs& a, int pair, int pairs, uint8_t* smem, u
   }
 }
 
-// 32 rows x 64 fp16 of this warp to the tensor of `map`.
-__device__ __forceinline__ void stage_and_store(const CUtensorMap* map, uint8_t* stg, int& sbuf, int lane,
-                                                const uint32_t (&w)[32], int x, int y, int z) {
-  uint8_t* buf = stg + sbuf * kStagingBuf;
-  if (lane == 0) bulk_wait_group_read<1>();
-  __syncwarp();
-  uint8_t* row = buf + lane * 128;
+// A lane's row of 64 fp16 in a staging buffer of 32, laid out as a 128-byte-swizzled box.
+__device__ __forceinline__ uint4* staged(uint8_t* buf, int lane, int c) {
+  return reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4));
+}
+__device__ __forceinline__ void stage_and_store(const CUtensorMap* map, uint8_t* buf, int lane, const uint32_t (&w)[32],
+                                                int x, int y, int z) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  for (int c = 0; c < 8; ++c) *staged(buf, lane, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
     tma_store_3d(map, buf, x, y, z);
     bulk_commit_group();
   }
-  sbuf ^= 1;
 }
 
-// 64 fp16 of one row, as fp32; zeros where the row or a chunk of 8 lies outside.
-__device__ __forceinline__ void load_row64(const __half* p, int valid, float (&x)[64]) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (8 * c < valid) v = *reinterpret_cast<const uint4*>(p + 8 * c);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_half2(u[e]);
-      x[8 * c + 2 * e] = f.x;
-      x[8 * c + 2 * e + 1] = f.y;
-    }
-  }
-}
-
-// The last product's 32 columns of 32 rows (row `i0 + lane` in v): written as bf16, or taken off
-// the weights.  x is the internal matrix's element (i, j): the tensor's (j, i) where it is tall.
-__device__ __forceinline__ void emit(const MuonMatrix& m, float* buf, int lane, int i0, int j0, int r, int c,
-                                     const float (&v)[32]) {
-  const bool tall = m.flags & kMuonTall;
-  if (!tall) {  // through shared memory, so that a warp's lanes hold one row's consecutive elements
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 32; ++j) buf[lane * 33 + j] = v[j];
-    __syncwarp();
-  }
-  const int64_t pitch = tall ? r : c;
-#pragma unroll 1
-  for (int q = 0; q < 32; q += 8) {
-    int64_t at[8];
-    float x[8], p[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = tall ? i0 + lane : i0 + q + e, j = tall ? j0 + q + e : j0 + lane;
-      x[e] = 0.f;
-      if (!tall) x[e] = buf[(q + e) * 33 + lane];
-      at[e] = i < r && j < c ? (tall ? j * pitch + i : i * pitch + j) : -1;
-    }
-    if (tall) {
-#pragma unroll
-      for (int k = 0; k < 32; k += 8)
-        if (k == q)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = v[k + e];
-    }
-    if (m.out) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at[e] >= 0) static_cast<__nv_bfloat16*>(m.out)[at[e]] = __float2bfloat16_rn(x[e]);
-      continue;
-    }
-    const bool f32 = m.flags & kMuonParamF32;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      p[e] = 0.f;
-      if (at[e] < 0) continue;
-      p[e] = m.master ? m.master[at[e]]
-             : f32    ? static_cast<const float*>(m.param)[at[e]]
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(m.param)[at[e]]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (at[e] < 0) continue;
-      const float w = fmaf(-m.rate, x[e], p[e] * m.decay);
-      if (m.master) m.master[at[e]] = w;
-      if (f32) static_cast<float*>(m.param)[at[e]] = w;
-      else static_cast<__nv_bfloat16*>(m.param)[at[e]] = __float2bfloat16_rn(w);
-    }
-  }
-}
-
-template <int MODE>
-__device__ void run_epilogue(const MuonArgs& a, const MuonMatrix* mats, uint32_t rank, int pair, int pairs,
-                             uint8_t* staging, uint32_t tmem_base, const Bars& b) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3;  // TMEM lanes that this warp may read
-  uint8_t* stg = staging + (warp - 2) * kStagingPerWarp;
+template <int MODE, int BN>
+__device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pairs, uint8_t* staging,
+                             uint32_t tmem_base, const Bars& b) {
+  constexpr int kCols = BN / 2;  // of a warp
+  const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+  const int quarter = (warp + 2) & 3;  // TMEM lanes that this warp may read
+  const int half = warp >> 2;
+  uint8_t* stg = staging + warp * kStagingPerWarp;
+  uint64_t* ebar = b.ebar + warp;
   const uint32_t tempty_even = mapa_shared(smem_u32(b.tempty), 0);
-  int sbuf = 0, acc = 0;
-  uint32_t acc_phase = 0;
+  int acc = 0, sbuf = 0;
+  uint32_t acc_phase = 0, ephase = 0;
   Tile t;
-  for (int i = pair; find_tile<MODE>(a, i, rank, t); i += pairs) {
+  for (int i = pair; find_tile<MODE, BN>(a, i, rank, t); i += pairs) {
     const MuonGroup& g = *t.g;
+    const int i0 = t.m0 + quarter * 32, row = i0 + lane;
+    const int first = t.n0 + half * kCols;
+    const bool lo_in = MODE == kMuonApply && g.lo_in;
+    const bool pairs_out = g.write_lo;
+    // the second buffer takes the old lo and then the new one
+    auto fetch = [&](int j0) {
+      if (lane == 0) {
+        bulk_wait_group_read<0>();
+        mbar_arrive_expect_tx(ebar, kStagingBuf);
+        tma_load_3d(stg + kStagingBuf, &g.out_lo, ebar, j0, i0, t.matrix);
+      }
+    };
+    if (lo_in && i0 < g.r && first < g.n) fetch(first);
     if (!mbar_wait(&b.tfull[acc], acc_phase, a.timeout_ns, b.abort_flag)) {
       record_timeout(a, rank, b.abort_flag);
       break;
     }
     tc_fence_after_sync();
-    const uint32_t tbase = tmem_base + static_cast<uint32_t>(acc * kBN) + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int i0 = t.m0 + quarter * 32;
-    const int row = i0 + lane;
-    if (i0 < g.r) {
-      if (MODE == kMuonFinal) {
-        const MuonMatrix& m = mats[g.matrix0 + t.matrix];
+    const uint32_t tbase = tmem_base + static_cast<uint32_t>(acc * BN + half * kCols) + (static_cast<uint32_t>(quarter * 32) << 16);
+    bool gave_up = false;
 #pragma unroll 1
-        for (int h = 0; h < kBN / 32; ++h) {
-          const int j0 = t.n0 + h * 32;
-          if (j0 >= g.n) break;
-          __syncwarp();
-          uint32_t d[32];
-          tmem_ld_32x32(tbase + h * 32, d);
-          float v[32];
-          if (g.in_lo) {  // (at most kMuonPairSteps steps)
-            const __half* src = g.in_lo + t.matrix * g.in_size + static_cast<int64_t>(row) * g.in_pitch + j0;
+    for (int h = 0; h < kCols / 64; ++h) {
+      const int j0 = first + h * 64;
+      if (i0 >= g.r || j0 >= g.n) break;
+      __syncwarp();
+      uint32_t d[64];
+      tmem_ld_32x64(tbase + h * 64, d);
+      float v[64];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = fmaf(__uint_as_float(d[j]), g.alpha, row < g.r && j0 + j < g.n ? g.beta * __half2float(src[j]) : 0.f);
-          } else {
+      for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(d[j]) * g.alpha;
+      if (MODE != kMuonApply) {
+        const int diag = row - j0;  // in this chunk, for the lanes of one row block alone
+        if (static_cast<unsigned>(i0 - j0 + 31) < 95u) {
+          float* keep = g.diag ? g.diag + static_cast<int64_t>(t.matrix) * g.r + row : nullptr;
+          float plus = g.gamma;
+          if (MODE == kMuonPoly && keep && row < g.r) plus = fmaf(g.alpha, *keep, plus);
+          float at = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(d[j]) * g.alpha;
-          }
-          emit(m, reinterpret_cast<float*>(stg), lane, i0, j0, g.r, g.n, v);
-        }
-      } else {
-#pragma unroll 1
-        for (int h = 0; h < kBN / 64; ++h) {
-          const int j0 = t.n0 + h * 64;
-          if (j0 >= g.n) break;
-          __syncwarp();
-          uint32_t d[64];
-          tmem_ld_32x64(tbase + h * 64, d);
-          float v[64];
-#pragma unroll
-          for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(d[j]) * g.alpha;
-          const int valid = row < g.r ? g.n - j0 : 0;
-          const int64_t at = t.matrix * g.in_size + static_cast<int64_t>(row) * g.in_pitch + j0;
-          if (MODE == kMuonPoly || (MODE == kMuonApply && g.in_lo)) {
-            float x[64];
-            if (MODE == kMuonPoly) {
-              load_row64(g.in_hi + at, valid, x);
-#pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] = fmaf(x[j], g.beta, v[j]);
-            }
-            if (g.in_lo) {
-              load_row64(g.in_lo + at, valid, x);
-#pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] = fmaf(x[j], g.beta, v[j]);
-            }
-            if (MODE == kMuonPoly) {
-              const int diag = row - j0;
-#pragma unroll
-              for (int j = 0; j < 64; ++j)
-                if (j == diag) v[j] += g.gamma;
+          for (int j = 0; j < 64; ++j) {
+            if (j == diag) {
+              v[j] += plus;
+              at = v[j];
             }
           }
-          uint32_t w[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1]);
-          stage_and_store(&g.out, stg, sbuf, lane, w, j0, i0, t.matrix);
-          const int64_t mir = t.matrix * g.mir_size + static_cast<int64_t>(j0) * g.mir_pitch + row;
-          if (t.mirror && row < g.r) {
-#pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              const uint32_t u = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1];
-              if (j0 + j < g.n)
-                reinterpret_cast<uint16_t*>(g.mir_hi)[mir + static_cast<int64_t>(j) * g.mir_pitch] = static_cast<uint16_t>(u);
-            }
-          }
-          if (g.write_lo) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float2 f = unpack_half2(w[j]);
-              w[j] = pack_half2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
-            }
-            stage_and_store(&g.out_lo, stg, sbuf, lane, w, j0, i0, t.matrix);
-            if (t.mirror && row < g.r) {
-#pragma unroll
-              for (int j = 0; j < 64; ++j) {
-                const uint32_t u = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1];
-                if (j0 + j < g.n)
-                  reinterpret_cast<uint16_t*>(g.mir_lo)[mir + static_cast<int64_t>(j) * g.mir_pitch] = static_cast<uint16_t>(u);
-              }
-            }
+          if (MODE == kMuonGram && keep && diag >= 0 && diag < 64 && row < g.r) {
+            const float hi = __half2float(__float2half_rn(at)), left = at - hi;
+            *keep = fmaf(2.f, hi, left) * left;  // of the square
           }
         }
       }
+      if (lo_in) {
+        if (!mbar_wait(ebar, ephase, a.timeout_ns, b.abort_flag)) {
+          record_timeout(a, rank, b.abort_flag);
+          gave_up = true;
+          break;
+        }
+        ephase ^= 1u;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 q = *staged(stg + kStagingBuf, lane, c);
+          const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_half2(u[e]);
+            v[8 * c + 2 * e] = fmaf(f.x, g.beta, v[8 * c + 2 * e]);
+            v[8 * c + 2 * e + 1] = fmaf(f.y, g.beta, v[8 * c + 2 * e + 1]);
+          }
+        }
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1]);
+      const bool alternate = !lo_in && !pairs_out;
+      if (lane == 0) {
+        if (alternate) bulk_wait_group_read<1>();
+        else bulk_wait_group_read<0>();
+      }
+      __syncwarp();  // the old lo has been read, and the buffers' earlier stores are done with them
+      stage_and_store(&g.out, stg + (alternate ? sbuf * kStagingBuf : 0), lane, w, j0, i0, t.matrix);
+      sbuf ^= 1;
+      if (pairs_out) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float2 f = unpack_half2(w[j]);
+          w[j] = pack_half2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+        }
+        stage_and_store(&g.out_lo, stg + kStagingBuf, lane, w, j0, i0, t.matrix);
+      }
+      if (lo_in && h + 1 < kCols / 64 && j0 + 64 < g.n) fetch(j0 + 64);
     }
+    if (gave_up) break;
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive_cluster(tempty_even + 8u * acc);
@@ -417,19 +377,27 @@ __device__ void run_epilogue(const MuonArgs& a, const MuonMatrix* mats, uint32_t
   __syncwarp();
 }
 
-template <int MODE>
-__device__ __forceinline__ void product_body(const MuonArgs& a, const MuonMatrix* mats) {
+template <int MODE, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+    muon_product_kernel(const __grid_constant__ MuonArgs a) {
+  using S = Shape<BN>;
+  constexpr uint32_t kTmemCols = 2 * BN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kSmemBarOff);
-  Bars b{bars, bars + kStages, bars + 2 * kStages, bars + 2 * kStages + 2,
-         reinterpret_cast<volatile int*>(bars + 2 * kStages + 4)};
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kSmemBarOff);
+  Bars b;
+  b.full = bars;
+  b.empty = b.full + S::kStages;
+  b.tfull = b.empty + S::kStages;
+  b.tempty = b.tfull + 2;
+  b.ebar = b.tempty + 2;
+  b.abort_flag = reinterpret_cast<volatile int*>(b.ebar + kEpiWarps);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b.ebar + kEpiWarps + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&b.full[i], 1);
       mbar_init(&b.empty[i], 1);
     }
@@ -437,6 +405,7 @@ __device__ __forceinline__ void product_body(const MuonArgs& a, const MuonMatrix
       mbar_init(&b.tfull[i], 1);
       mbar_init(&b.tempty[i], 2 * kEpiWarps);
     }
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(&b.ebar[i], 1);
     *b.abort_flag = 0;
     mbar_fence_init();
     fence_proxy_async_smem();
@@ -452,11 +421,11 @@ __device__ __forceinline__ void product_body(const MuonArgs& a, const MuonMatrix
   griddep_wait();
   griddep_launch();
   if (warp == 0) {
-    if (lane == 0) run_producer<MODE>(a, rank, pair, pairs, smem, b);
+    if (lane == 0) run_producer<MODE, BN>(a, rank, pair, pairs, smem, b);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) run_mma<MODE>(a, pair, pairs, smem, tmem_base, b);
+    if (lane == 0 && rank == 0) run_mma<MODE, BN>(a, pair, pairs, smem, tmem_base, b);
   } else {
-    run_epilogue<MODE>(a, mats, rank, pair, pairs, smem + kSmemStagingOff, tmem_base, b);
+    run_epilogue<MODE, BN>(a, rank, pair, pairs, smem + S::kSmemStagingOff, tmem_base, b);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -472,24 +441,24 @@ __device__ __forceinline__ void product_body(const MuonArgs& a, const MuonMatrix
   }
 }
 
-template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
-    muon_product_kernel(const __grid_constant__ MuonArgs a) {
-  product_body<MODE>(a, nullptr);
-}
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
-    muon_final_kernel(const __grid_constant__ MuonArgs a, const __grid_constant__ MuonMatrices m) {
-  product_body<kMuonFinal>(a, m.m);
-}
+// ----------------------------------------------------------------------------- momentum, norm, weights
 
-// ----------------------------------------------------------------------------- momentum and norm
-
+template <bool F32>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  return F32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+// Four from an element that is a multiple of four.
+__device__ __forceinline__ float4 load4(const void* p, int64_t i, bool f32) {
+  if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
 __device__ __forceinline__ float load_g(const MuonSource& s, int64_t i) {
-  return (s.flags & kMuonGradF32) ? static_cast<const float*>(s.grad)[i]
-                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(s.grad)[i]);
+  return (s.flags & kMuonGradF32) ? load1<true>(s.grad, i) : load1<false>(s.grad, i);
 }
 
-// The source that holds chunk or strip c of the launch.
+// The source that holds block c of the launch.
 template <typename F>
 __device__ __forceinline__ int find_source(int count, uint32_t c, F first) {
   int lo = 0, hi = count - 1;
@@ -502,6 +471,18 @@ __device__ __forceinline__ int find_source(int count, uint32_t c, F first) {
 }
 
 constexpr int kNormThreads = 256;
+static_assert(kMuonChunk == kNormThreads * 4 * 8, "eight vectors a thread");
+
+struct Momentum {
+  float mu, omm, gs;
+  int nesterov;
+  __device__ __forceinline__ float move(float m, float g) const { return m * mu + g * gs * omm; }
+  // u, from the gradient and the momentum that has moved
+  __device__ __forceinline__ float u(float m, float g) const { return nesterov ? m * mu + g * gs * omm : m; }
+};
+__device__ __forceinline__ Momentum momentum_of(const MuonSources& a) {
+  return Momentum{a.mu, a.omm, a.grad_scale ? *a.grad_scale : 1.f, a.nesterov};
+}
 
 // One chunk of kMuonChunk elements: the momentum moves, and the squares of u are added up.
 __global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __grid_constant__ MuonSources a) {
@@ -512,17 +493,43 @@ __global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __gri
   const MuonSource& s = a.s[si];
   const int64_t begin = static_cast<int64_t>(c - s.chunk0) * kMuonChunk;
   const int64_t end = min(begin + kMuonChunk, static_cast<int64_t>(s.rows) * s.cols);
-  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+  const Momentum q = momentum_of(a);
   float sum = 0.f;
-#pragma unroll 4
-  for (int64_t i = begin + threadIdx.x; i < end; i += kNormThreads) {
-    float u = load_g(s, i) * gs;
-    if (s.momentum) {
-      const float m = s.momentum[i] * a.mu + u * a.omm;
-      s.momentum[i] = m;
-      u = a.nesterov ? m * a.mu + u * a.omm : m;
+  if ((s.flags & kMuonAligned) && end - begin == kMuonChunk) {
+    const bool f32 = s.flags & kMuonGradF32;
+#pragma unroll
+    for (int k0 = 0; k0 < 8; k0 += 4) {
+      float4 g[4], m[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = begin + ((k0 + k) * kNormThreads + threadIdx.x) * 4;
+        g[k] = load4(s.grad, i, f32);
+        m[k] = s.momentum ? *reinterpret_cast<const float4*>(s.momentum + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float4 u = make_float4(g[k].x * q.gs, g[k].y * q.gs, g[k].z * q.gs, g[k].w * q.gs);
+        if (s.momentum) {
+          const float4 n = make_float4(q.move(m[k].x, g[k].x), q.move(m[k].y, g[k].y), q.move(m[k].z, g[k].z),
+                                       q.move(m[k].w, g[k].w));
+          *reinterpret_cast<float4*>(s.momentum + begin + ((k0 + k) * kNormThreads + threadIdx.x) * 4) = n;
+          u = make_float4(q.u(n.x, g[k].x), q.u(n.y, g[k].y), q.u(n.z, g[k].z), q.u(n.w, g[k].w));
+        }
+        sum = fmaf(u.x, u.x, fmaf(u.y, u.y, fmaf(u.z, u.z, fmaf(u.w, u.w, sum))));
+      }
     }
-    sum = fmaf(u, u, sum);
+  } else {
+#pragma unroll 4
+    for (int64_t i = begin + threadIdx.x; i < end; i += kNormThreads) {
+      const float g = load_g(s, i);
+      float u = g * q.gs;
+      if (s.momentum) {
+        const float m = q.move(s.momentum[i], g);
+        s.momentum[i] = m;
+        u = q.u(m, g);
+      }
+      sum = fmaf(u, u, sum);
+    }
   }
   __shared__ float part[kNormThreads / 32];
 #pragma unroll
@@ -535,40 +542,82 @@ __global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __gri
   }
 }
 
-constexpr int kStripR = 64, kStripC = 64;
+constexpr int kStrip = 64;  // tiles of kStrip x kStrip go through shared memory, to be turned where the matrix is tall
 
-// A 64 x 64 tile of one source: u / (|u| + eps) as a pair of fp16, turned where the matrix is tall.
+struct Strip {
+  int r0, c0;    // in the tensor
+  int rr, cc;    // in the internal matrix
+  int nr, nc;    // its size
+  bool tall;
+};
+__device__ __forceinline__ Strip strip_of(const MuonSource& s, uint32_t q) {
+  Strip t;
+  const int across = (s.cols + kStrip - 1) / kStrip, k = static_cast<int>(q - s.strip0);
+  t.r0 = k / across * kStrip;
+  t.c0 = k % across * kStrip;
+  t.tall = s.flags & kMuonTall;
+  t.rr = t.tall ? t.c0 : t.r0;
+  t.cc = t.tall ? t.r0 : t.c0;
+  t.nr = t.tall ? s.cols : s.rows;
+  t.nc = t.tall ? s.rows : s.cols;
+  return t;
+}
+
+// One tile of one source: u / (|u| + eps) as a pair of fp16.  The launch runs through the sources
+// backwards: what the momentum's pass left in L2 is read first.
 __global__ void __launch_bounds__(kNormThreads) muon_scale_kernel(const __grid_constant__ MuonSources a) {
   griddep_begin();
-  __shared__ float tile[kStripR][kStripC + 1];
+  __shared__ float tile[kStrip][kStrip + 1];
   __shared__ double red[kNormThreads / 32];
-  const uint32_t q = blockIdx.x;
+  const uint32_t q = gridDim.x - 1 - blockIdx.x;
   const int si = find_source(a.count, q, [&](int i) { return a.s[i].strip0; });
   const MuonSource& s = a.s[si];
   const int tid = threadIdx.x;
+  const Strip t = strip_of(s, q);
+  const Momentum mo = momentum_of(a);
+  const bool f32 = s.flags & kMuonGradF32;
+  const bool need_g = !s.momentum || a.nesterov;
+  if (s.flags & kMuonAlignedRows) {  // four columns a thread; rows are whole numbers of them
+    float4 g[4], m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = (k * kNormThreads + tid) / (kStrip / 4), j = (k * kNormThreads + tid) % (kStrip / 4) * 4;
+      g[k] = m[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t.r0 + i < s.rows && t.c0 + j < s.cols) {
+        const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
+        if (need_g) g[k] = load4(s.grad, at, f32);
+        if (s.momentum) m[k] = *reinterpret_cast<const float4*>(s.momentum + at);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = (k * kNormThreads + tid) / (kStrip / 4), j = (k * kNormThreads + tid) % (kStrip / 4) * 4;
+      float* o = &tile[i][j];
+      const bool mom = s.momentum;
+      o[0] = mom ? mo.u(m[k].x, g[k].x) : g[k].x * mo.gs;
+      o[1] = mom ? mo.u(m[k].y, g[k].y) : g[k].y * mo.gs;
+      o[2] = mom ? mo.u(m[k].z, g[k].z) : g[k].z * mo.gs;
+      o[3] = mom ? mo.u(m[k].w, g[k].w) : g[k].w * mo.gs;
+    }
+  } else {
+#pragma unroll 8
+    for (int k = tid; k < kStrip * kStrip; k += kNormThreads) {
+      const int i = k / kStrip, j = k % kStrip;
+      float u = 0.f;
+      if (t.r0 + i < s.rows && t.c0 + j < s.cols) {
+        const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
+        const float g = need_g ? load_g(s, at) : 0.f;
+        u = s.momentum ? mo.u(s.momentum[at], g) : g * mo.gs;
+      }
+      tile[i][j] = u;
+    }
+  }
   const int64_t chunks = (static_cast<int64_t>(s.rows) * s.cols + kMuonChunk - 1) / kMuonChunk;
   double sum = 0.0;
   for (int64_t i = tid; i < chunks; i += kNormThreads) sum += static_cast<double>(a.part[s.chunk0 + i]);
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if ((tid & 31) == 0) red[tid >> 5] = sum;
-  const int across = (s.cols + kStripC - 1) / kStripC;
-  const int r0 = static_cast<int>(q - s.strip0) / across * kStripR, c0 = static_cast<int>(q - s.strip0) % across * kStripC;
-  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-#pragma unroll 4
-  for (int k = tid; k < kStripR * kStripC; k += kNormThreads) {
-    const int i = k / kStripC, j = k % kStripC;
-    float u = 0.f;
-    if (r0 + i < s.rows && c0 + j < s.cols) {
-      const int64_t at = static_cast<int64_t>(r0 + i) * s.cols + c0 + j;
-      if (!s.momentum || a.nesterov) u = load_g(s, at) * gs;
-      if (s.momentum) {
-        const float m = s.momentum[at];
-        u = a.nesterov ? m * a.mu + u * a.omm : m;
-      }
-    }
-    tile[i][j] = u;
-  }
   __syncthreads();
   sum = red[0];
 #pragma unroll
@@ -576,28 +625,127 @@ __global__ void __launch_bounds__(kNormThreads) muon_scale_kernel(const __grid_c
   // a sum of squares past fp32's range, or a non-finite element, makes the whole matrix NaN
   const float total = static_cast<float>(sum);
   const float inv = isfinite(total) ? kMuonXScale / (sqrtf(total) + a.eps) : NAN;
-  const bool tall = s.flags & kMuonTall;
-  const int rr = tall ? c0 : r0, cc = tall ? r0 : c0;  // the tile in the internal matrix
-  const int nr = tall ? s.cols : s.rows, nc = tall ? s.rows : s.cols;
-  for (int k = tid; k < kStripR * kStripC / 2; k += kNormThreads) {
-    const int i = k / (kStripC / 2), j = k % (kStripC / 2) * 2;
-    if (rr + i >= nr || cc + j >= nc) continue;
-    const float x0 = (tall ? tile[j][i] : tile[i][j]) * inv;
-    const float x1 = cc + j + 1 < nc ? (tall ? tile[j + 1][i] : tile[i][j + 1]) * inv : 0.f;  // (the pitch is even)
-    const uint32_t hi = pack_half2(x0, x1);
-    const float2 f = unpack_half2(hi);
-    const int64_t at = static_cast<int64_t>(rr + i) * s.pitch + cc + j;
-    *reinterpret_cast<uint32_t*>(s.hi + at) = hi;
-    *reinterpret_cast<uint32_t*>(s.lo + at) = pack_half2(x0 - f.x, x1 - f.y);
+#pragma unroll
+  for (int k = tid; k < kStrip * kStrip / 4; k += kNormThreads) {
+    const int i = k / (kStrip / 4), j = k % (kStrip / 4) * 4;
+    if (t.rr + i >= t.nr || t.cc + j >= t.nc) continue;  // (the pitch is a multiple of 8: four always fit)
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (t.tall ? tile[j + e][i] : tile[i][j + e]) * inv;
+    uint2 hi, lo;
+    hi.x = pack_half2(x[0], x[1]);
+    hi.y = pack_half2(x[2], x[3]);
+    const float2 f0 = unpack_half2(hi.x), f1 = unpack_half2(hi.y);
+    lo.x = pack_half2(x[0] - f0.x, x[1] - f0.y);
+    lo.y = pack_half2(x[2] - f1.x, x[3] - f1.y);
+    const int64_t at = static_cast<int64_t>(t.rr + i) * s.pitch + t.cc + j;
+    *reinterpret_cast<uint2*>(s.hi + at) = hi;
+    *reinterpret_cast<uint2*>(s.lo + at) = lo;
   }
 }
 
-template <int MODE>
-cudaError_t launch_mode(const MuonArgs& a, int grid, cudaStream_t s) {
+// One tile of one matrix: X, from the internal matrix, to out as bf16, or taken off the weights.
+__global__ void __launch_bounds__(kNormThreads) muon_weights_kernel(const __grid_constant__ MuonTargets a) {
+  griddep_begin();
+  __shared__ float tile[kStrip][kStrip + 1];
+  const uint32_t q = blockIdx.x;
+  const int si = find_source(a.count, q, [&](int i) { return a.t[i].strip0; });
+  const MuonTarget& s = a.t[si];
+  const int tid = threadIdx.x;
+  MuonSource shape{};
+  shape.rows = s.rows;
+  shape.cols = s.cols;
+  shape.flags = s.flags;
+  shape.strip0 = s.strip0;
+  const Strip t = strip_of(shape, q);
+  const bool f32 = s.flags & kMuonParamF32, vec = s.flags & kMuonAlignedRows;
+  float4 w[4];
+  if (!s.out && vec) {  // under way while X is turned
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = (k * kNormThreads + tid) / (kStrip / 4), j = (k * kNormThreads + tid) % (kStrip / 4) * 4;
+      w[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t.r0 + i < s.rows && t.c0 + j < s.cols) {
+        const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
+        w[k] = s.master ? *reinterpret_cast<const float4*>(s.master + at) : load4(s.param, at, f32);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = (k * kNormThreads + tid) / (kStrip / 8), j = (k * kNormThreads + tid) % (kStrip / 8) * 8;
+    uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+    if (t.rr + i < t.nr && t.cc + j < t.nc) {
+      const int64_t at = static_cast<int64_t>(t.rr + i) * s.pitch + t.cc + j;
+      hi = *reinterpret_cast<const uint4*>(s.hi + at);
+      if (s.lo) lo = *reinterpret_cast<const uint4*>(s.lo + at);
+    }
+    const uint32_t uh[4] = {hi.x, hi.y, hi.z, hi.w}, ul[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_half2(uh[e]), g = unpack_half2(ul[e]);
+      const float x0 = (f.x + g.x) * (1.f / kMuonXScale), x1 = (f.y + g.y) * (1.f / kMuonXScale);
+      if (t.tall) {
+        tile[j + 2 * e][i] = x0;
+        tile[j + 2 * e + 1][i] = x1;
+      } else {
+        tile[i][j + 2 * e] = x0;
+        tile[i][j + 2 * e + 1] = x1;
+      }
+    }
+  }
+  __syncthreads();
+  if (vec) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = (k * kNormThreads + tid) / (kStrip / 4), j = (k * kNormThreads + tid) % (kStrip / 4) * 4;
+      if (t.r0 + i >= s.rows || t.c0 + j >= s.cols) continue;
+      const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
+      float4 x = make_float4(tile[i][j], tile[i][j + 1], tile[i][j + 2], tile[i][j + 3]);
+      void* to = s.out;
+      if (!s.out) {
+        x = make_float4(fmaf(-s.rate, x.x, w[k].x * s.decay), fmaf(-s.rate, x.y, w[k].y * s.decay),
+                        fmaf(-s.rate, x.z, w[k].z * s.decay), fmaf(-s.rate, x.w, w[k].w * s.decay));
+        if (s.master) *reinterpret_cast<float4*>(s.master + at) = x;
+        to = s.param;
+      }
+      if (!s.out && f32) *reinterpret_cast<float4*>(static_cast<float*>(to) + at) = x;
+      else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to) + at) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    }
+  } else {
+#pragma unroll 4
+    for (int k = tid; k < kStrip * kStrip; k += kNormThreads) {
+      const int i = k / kStrip, j = k % kStrip;
+      if (t.r0 + i >= s.rows || t.c0 + j >= s.cols) continue;
+      const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
+      float x = tile[i][j];
+      if (s.out) {
+        static_cast<__nv_bfloat16*>(s.out)[at] = __float2bfloat16_rn(x);
+        continue;
+      }
+      const float p = s.master ? s.master[at] : f32 ? load1<true>(s.param, at) : load1<false>(s.param, at);
+      x = fmaf(-s.rate, x, p * s.decay);
+      if (s.master) s.master[at] = x;
+      if (f32) static_cast<float*>(s.param)[at] = x;
+      else static_cast<__nv_bfloat16*>(s.param)[at] = __float2bfloat16_rn(x);
+    }
+  }
+}
+
+template <int MODE, int BN>
+cudaError_t launch_mode(const MuonArgs& a, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(muon_product_kernel<MODE>, kSmemBytes, done);
+  cudaError_t e = allow_smem(muon_product_kernel<MODE, BN>, Shape<BN>::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_k(muon_product_kernel<MODE>, dim3(grid), dim3(kProductThreads), kSmemBytes, s, a);
+  return launch_k(muon_product_kernel<MODE, BN>, dim3(pair_grid(sms, a.tiles)), dim3(kProductThreads),
+                  Shape<BN>::kSmemBytes, s, a);
+}
+
+template <int BN>
+cudaError_t launch_width(int mode, const MuonArgs& a, int sms, cudaStream_t s) {
+  return mode == kMuonGram   ? launch_mode<kMuonGram, BN>(a, sms, s)
+         : mode == kMuonPoly ? launch_mode<kMuonPoly, BN>(a, sms, s)
+                             : launch_mode<kMuonApply, BN>(a, sms, s);
 }
 
 }  // namespace
@@ -608,21 +756,14 @@ cudaError_t launch_muon_momentum(const MuonSources& a, uint32_t chunks, cudaStre
 cudaError_t launch_muon_scale(const MuonSources& a, uint32_t strips, cudaStream_t s) {
   return launch_k(muon_scale_kernel, dim3(strips), dim3(kNormThreads), 0, s, a);
 }
-int64_t muon_strips(int64_t rows, int64_t cols) {
-  return (rows + kStripR - 1) / kStripR * ((cols + kStripC - 1) / kStripC);
+cudaError_t launch_muon_weights(const MuonTargets& a, uint32_t strips, cudaStream_t s) {
+  return launch_k(muon_weights_kernel, dim3(strips), dim3(kNormThreads), 0, s, a);
 }
-cudaError_t launch_muon_product(int mode, const MuonArgs& a, const MuonMatrices& m, int sms, cudaStream_t s) {
-  const int grid = pair_grid(sms, a.tiles);
-  switch (mode) {
-    case kMuonGram: return launch_mode<kMuonGram>(a, grid, s);
-    case kMuonPoly: return launch_mode<kMuonPoly>(a, grid, s);
-    case kMuonApply: return launch_mode<kMuonApply>(a, grid, s);
-    default: break;
-  }
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(muon_final_kernel, kSmemBytes, done);
-  if (e != cudaSuccess) return e;
-  return launch_k(muon_final_kernel, dim3(grid), dim3(kProductThreads), kSmemBytes, s, a, m);
+int64_t muon_strips(int64_t rows, int64_t cols) {
+  return (rows + kStrip - 1) / kStrip * ((cols + kStrip - 1) / kStrip);
+}
+cudaError_t launch_muon_product(int mode, int bn, const MuonArgs& a, int sms, cudaStream_t s) {
+  return bn == 256 ? launch_width<256>(mode, a, sms, s) : launch_width<128>(mode, a, sms, s);
 }
 
 }  // namespace flce

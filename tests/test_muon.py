@@ -74,10 +74,20 @@ def rounded(u, steps=5, coefficients=USUAL, eps=1e-7):
     one = torch.eye(r, dtype=torch.float64, device=u.device)
     x = pair(x, 2.0 ** 14, True)
     for k, (a, b, c) in enumerate(triples(coefficients, steps)):
-        g = pair(product(x, (x[0].mT, x[1].mT)), 2.0 ** 14, every)
-        p = pair(a * one + b * (g[0] + g[1]) + c * product(g, g), ps, every)
+        g = product(x, (x[0].mT, x[1].mT))
+        if c:  # the square completed; what rounding the diagonal left is known
+            g = g + b / (2 * c) * one
+            left = g
+            g = pair(g, 2.0 ** 13, every)
+            left = 0 if every else torch.diagonal(left - g[0], dim1=-2, dim2=-1)
+            more = left * (2 * torch.diagonal(g[0], dim1=-2, dim2=-1) + left)
+            p = c * product(g, g) + (a - b * b / (4 * c)) * one + (0 if every else c * torch.diag_embed(more))
+        else:
+            p = a * one + b * g
+        p = pair(p, ps, every)
         y = product(p, x) if every else p[0] @ x[0] + (a * x[1] if k < 3 else 0)
-        x = pair(y, 2.0 ** 14, every or k + 1 < 3)
+        x = pair(y, 2.0 ** 14, every or (k + 1 < 3 and k + 1 < steps))
+    y = x[0] + x[1]
     return y if wide else y.mT
 
 
@@ -145,7 +155,7 @@ def test_library_refuses():
                       ((0x1000, 0x2000, 8, (1 << 24) + 1, 0), 2)):
         assert ortho(row) == code, row
     for over in (dict(eps=0.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(coefficients=(4.5, -4.775, 2.03)),
-                 dict(coefficients=(float("nan"), 0.0, 0.0)), dict(coefficients=(1e5, 0.0, 0.0), steps=1),
+                 dict(coefficients=(float("nan"), 0.0, 0.0)), dict(coefficients=(1.5, -0.5, 0.05)), dict(coefficients=(1e5, 0.0, 0.0), steps=1),
                  dict(momentum=1.0), dict(momentum=-0.1)):
         assert ortho(o=options(**over)) == 1, over
     o = options()
@@ -222,6 +232,7 @@ def test_orthogonalize(shape, kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("steps,coefficients", [(1, USUAL), (2, USUAL), (3, USUAL), (4, USUAL), (12, (1.5, -0.5, 0.0)),
+                                                (1, (1.5, -0.5, 0.0)), (1, (3.9, -8.0, 4.5)),
                                                 (8, (1.875, -1.25, 0.375)),
                                                 (3, [(3.9, -8.0, 4.5), (3.0, -4.0, 1.9), (1.875, -1.25, 0.375)])])
 @pytest.mark.parametrize("shape", [(100, 60), (200, 300)])
