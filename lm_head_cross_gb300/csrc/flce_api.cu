@@ -1850,11 +1850,14 @@ struct MuonItem {
 // Groups of one round and where their buffers lie: X (two: a product reads one and writes the
 // other) with what rounding left of it, A and P.
 struct MuonPlanGroup {
-  int64_t r, c;
+  int64_t rows, cols;
   std::vector<int> items;
-  bool exact() const { return r <= kMuonExactRows; }
-  int64_t xp() const { return (c + 7) / 8 * 8; }
-  int64_t ap() const { return (r + 7) / 8 * 8; }
+  int64_t r() const { return std::min(rows, cols); }
+  int64_t c() const { return std::max(rows, cols); }
+  bool tall() const { return rows > cols; }
+  bool exact() const { return r() <= kMuonExactRows; }
+  int64_t xp() const { return (cols + 7) / 8 * 8; }
+  int64_t ap() const { return (r() + 7) / 8 * 8; }
   size_t x[2], xlo[2], a, alo, p, plo, diag;
 };
 struct MuonRound {
@@ -1864,8 +1867,9 @@ struct MuonRound {
   size_t part = 0, total = 0;
 };
 
-size_t muon_matrix_bytes(int64_t r, int64_t c) {
-  const size_t x = 2 * static_cast<size_t>(r) * static_cast<size_t>((c + 7) / 8 * 8);
+size_t muon_matrix_bytes(int64_t rows, int64_t cols) {
+  const int64_t r = std::min(rows, cols);
+  const size_t x = 2 * static_cast<size_t>(rows) * static_cast<size_t>((cols + 7) / 8 * 8);
   const size_t a = 2 * static_cast<size_t>(r) * static_cast<size_t>((r + 7) / 8 * 8);
   return r <= kMuonExactRows ? 4 * x + 4 * a : 3 * x + 2 * a;
 }
@@ -1880,15 +1884,15 @@ std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
   for (size_t i = 0; i < by.size(); ++i) by[i] = static_cast<int>(i);
   std::stable_sort(by.begin(), by.end(), [&](int i, int j) {
     const MuonItem &x = items[i], &y = items[j];
-    return x.r() != y.r() ? x.r() > y.r() : x.c() > y.c();
+    return x.r() != y.r() ? x.r() > y.r() : x.c() != y.c() ? x.c() > y.c() : x.rows > y.rows;
   });
   std::vector<MuonRound> rounds;
   size_t bytes = 0;
   for (int i : by) {
     const MuonItem& m = items[i];
     if (m.rows == 0 || m.cols == 0) continue;
-    const size_t more = muon_matrix_bytes(m.r(), m.c());
-    bool same = !rounds.empty() && rounds.back().groups.back().r == m.r() && rounds.back().groups.back().c == m.c();
+    const size_t more = muon_matrix_bytes(m.rows, m.cols);
+    bool same = !rounds.empty() && rounds.back().groups.back().rows == m.rows && rounds.back().groups.back().cols == m.cols;
     if (rounds.empty() || rounds.back().matrices == kMuonMatrices || bytes + more > kMuonRoundBytes ||
         (!same && static_cast<int>(rounds.back().groups.size()) == kMuonGroups)) {
       rounds.emplace_back();
@@ -1898,8 +1902,8 @@ std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
     MuonRound& r = rounds.back();
     if (!same) {
       r.groups.emplace_back();
-      r.groups.back().r = m.r();
-      r.groups.back().c = m.c();
+      r.groups.back().rows = m.rows;
+      r.groups.back().cols = m.cols;
     }
     r.groups.back().items.push_back(i);
     ++r.matrices;
@@ -1916,7 +1920,7 @@ std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
     r.part = take(sizeof(float) * static_cast<size_t>(r.chunks));
     for (MuonPlanGroup& g : r.groups) {
       const size_t count = g.items.size();
-      const size_t xb = 2 * count * static_cast<size_t>(g.r * g.xp()), ab = 2 * count * static_cast<size_t>(g.r * g.ap());
+      const size_t xb = 2 * count * static_cast<size_t>(g.rows * g.xp()), ab = 2 * count * static_cast<size_t>(g.r() * g.ap());
       g.x[0] = take(xb);
       g.x[1] = take(xb);
       g.xlo[0] = take(xb);
@@ -1925,7 +1929,7 @@ std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
       g.p = take(ab);
       g.alo = g.exact() ? take(ab) : 0;
       g.plo = g.exact() ? take(ab) : 0;
-      g.diag = g.exact() ? 0 : take(sizeof(float) * count * static_cast<size_t>(g.r));
+      g.diag = g.exact() ? 0 : take(sizeof(float) * count * static_cast<size_t>(g.r()));
     }
     r.total = off;
   }
@@ -1978,25 +1982,26 @@ struct MuonMaps {
 };
 
 bool muon_maps(const MuonPlanGroup& g, uint8_t* ws, MuonMaps* m) {
-  const uint64_t r = g.r, c = g.c, n = g.items.size();
+  const uint64_t r = g.r(), n = g.items.size();
   const uint64_t xp = 2 * static_cast<uint64_t>(g.xp()), ap = 2 * static_cast<uint64_t>(g.ap());
-  auto all = [&](MuonMap* t, size_t at, uint64_t cols, uint64_t pitch, bool operand) {
-    auto one = [&](CUtensorMap* q, uint32_t rows) {
-      return make_map3(q, ws + at, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, cols, r, n, pitch, pitch * r, 64, rows);
+  auto all = [&](MuonMap* t, size_t at, uint64_t rows, uint64_t cols, uint64_t pitch, bool operand) {
+    auto one = [&](CUtensorMap* q, uint32_t box) {
+      return make_map3(q, ws + at, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, cols, rows, n, pitch, pitch * rows, 64, box);
     };
     return one(&t->b32, 32) && (!operand || (one(&t->b128, 128) && one(&t->b64, 64)));
   };
   for (int i = 0; i < 2; ++i)
-    if (!all(&m->x[i], g.x[i], c, xp, true) || !all(&m->xlo[i], g.xlo[i], c, xp, g.exact())) return false;
-  if (!all(&m->a, g.a, r, ap, true) || !all(&m->p, g.p, r, ap, true)) return false;
-  return !g.exact() || (all(&m->alo, g.alo, r, ap, true) && all(&m->plo, g.plo, r, ap, true));
+    if (!all(&m->x[i], g.x[i], g.rows, g.cols, xp, true) || !all(&m->xlo[i], g.xlo[i], g.rows, g.cols, xp, g.exact()))
+      return false;
+  if (!all(&m->a, g.a, r, r, ap, true) || !all(&m->p, g.p, r, r, ap, true)) return false;
+  return !g.exact() || (all(&m->alo, g.alo, r, r, ap, true) && all(&m->plo, g.plo, r, r, ap, true));
 }
 
 int64_t muon_tiles_each(const MuonPlanGroup& g, int mode, int bn) {
-  const int64_t rows = (g.r + kPairRows - 1) / kPairRows, per = kPairRows / bn;
-  if (mode == kMuonApply) return rows * ((g.c + bn - 1) / bn);
-  const int64_t cols = (g.r + bn - 1) / bn;  // the tiles from the diagonal on
-  return rows * cols - per * rows * (rows - 1) / 2;
+  const int64_t m = mode == kMuonApply ? g.rows : g.r(), n = mode == kMuonApply ? g.cols : g.r();
+  const int64_t rows = (m + kPairRows - 1) / kPairRows, cols = (n + bn - 1) / bn;
+  if (mode == kMuonApply) return rows * cols;
+  return rows * cols - (kPairRows / bn) * rows * (rows - 1) / 2;  // the tiles from the diagonal on
 }
 
 // Columns of a launch's tiles: 128 where there are fewer 256-wide ones than CTA pairs.
@@ -2030,11 +2035,13 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mo
       operand(&t.a_lo128, &t.a_lo64, alo);
       operand(&t.b_lo128, &t.b_lo64, blo);
     };
-    t.r = static_cast<int>(g.r);
-    t.n = static_cast<int>(mode == kMuonApply ? g.c : g.r);
+    t.m = static_cast<int>(mode == kMuonApply ? g.rows : g.r());
+    t.n = static_cast<int>(mode == kMuonApply ? g.cols : g.r());
+    t.tall = g.tall();
     t.segments = g.exact() ? 3 : 1;
-    t.row_tiles = static_cast<int>((g.r + kPairRows - 1) / kPairRows);
-    t.kblocks = static_cast<int>(((mode == kMuonGram ? g.c : g.r) + kBK - 1) / kBK);
+    t.row_tiles = (t.m + kPairRows - 1) / kPairRows;
+    t.col_tiles = (t.n + bn - 1) / bn;
+    t.kblocks = static_cast<int>(((mode == kMuonGram ? g.c() : g.r()) + kBK - 1) / kBK);
     t.write_lo = g.exact();
     t.diag = g.exact() || cc == 0.0 ? nullptr : reinterpret_cast<float*>(ws + g.diag);
     if (mode == kMuonGram) {
@@ -2051,7 +2058,8 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mo
       t.alpha = static_cast<float>(cc * ps / (as * as));
       t.gamma = static_cast<float>((ca - cb * cb / (4.0 * cc)) * ps);
     } else {
-      operands(m.p, m.plo, m.x[cur], m.xlo[cur]);
+      if (g.tall()) operands(m.x[cur], m.xlo[cur], m.p, m.plo);
+      else operands(m.p, m.plo, m.x[cur], m.xlo[cur]);
       t.out = m.x[cur ^ 1].b32;
       t.out_lo = m.xlo[cur ^ 1].b32;
       t.alpha = static_cast<float>(1.0 / ps);
@@ -2087,21 +2095,27 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
     src.eps = static_cast<float>(o.eps);
     src.grad_scale = grad_scale;
     src.part = reinterpret_cast<float*>(base + round.part);
-    src.status = n == 0 ? reinterpret_cast<int*>(base) : nullptr;
-    int64_t chunks = 0, strips = 0;
+    src.status = to.status = reinterpret_cast<int*>(base);
+    src.first = n == 0;
+    int64_t chunks = 0, strips = 0, target_strips = 0;
     std::vector<MuonMaps> maps(round.groups.size());
     for (size_t i = 0; i < round.groups.size(); ++i) {
       const MuonPlanGroup& g = round.groups[i];
       if (!muon_maps(g, base, &maps[i])) return FLCE_ERR_CUDA;
       for (size_t j = 0; j < g.items.size(); ++j) {
         const MuonItem& m = items[g.items[j]];
-        const size_t at = j * static_cast<size_t>(g.r * g.xp());
+        const size_t at = j * static_cast<size_t>(g.rows * g.xp());
         auto half = [&](size_t buf) { return reinterpret_cast<__half*>(base + buf) + at; };
-        const size_t ga = m.flags & kMuonGradF32 ? 16 : 8, pa = m.flags & kMuonParamF32 ? 16 : 8;
-        const bool source4 = aligned(m.grad, ga) && aligned(m.momentum, 16);
-        const bool target4 = aligned(m.out, 8) && aligned(m.param, pa) && aligned(m.master, 16);
-        const uint32_t flags = m.flags | (m.rows > m.cols ? kMuonTall : 0u);
+        // a tensor's rows by `v` columns at a time
+        auto rows_by = [&](const void* p, bool f32, int v) { return aligned(p, v * (f32 ? 4 : 2)) && m.cols % v == 0; };
+        const bool gf = m.flags & kMuonGradF32, pf = m.flags & kMuonParamF32;
         MuonSource& t = src.s[src.count];
+        MuonTarget& w = to.t[src.count];
+        t.vec = w.vec = 1;
+        for (int v : {2, 4}) {
+          if (rows_by(m.grad, gf, v) && rows_by(m.momentum, true, v)) t.vec = v;
+          if (rows_by(m.out, false, v) && rows_by(m.param, pf, v) && rows_by(m.master, true, v)) w.vec = v;
+        }
         t.grad = m.grad;
         t.momentum = m.momentum;
         t.hi = half(g.x[0]);
@@ -2109,10 +2123,9 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
         t.rows = static_cast<int>(m.rows);
         t.cols = static_cast<int>(m.cols);
         t.pitch = static_cast<int>(g.xp());
-        t.flags = flags | (source4 ? kMuonAligned : 0u) | (source4 && m.cols % 4 == 0 ? kMuonAlignedRows : 0u);
-        t.chunk0 = static_cast<uint32_t>(chunks);
-        t.strip0 = static_cast<uint32_t>(strips);
-        MuonTarget& w = to.t[src.count];
+        t.flags = m.flags | (aligned(m.grad, gf ? 16 : 8) && aligned(m.momentum, 16) ? kMuonAligned : 0u);
+        src.chunk0[src.count] = static_cast<uint32_t>(chunks);
+        src.strip0[src.count] = static_cast<uint32_t>(strips);
         w.hi = half(g.x[o.steps & 1]);
         w.lo = g.exact() ? half(g.xlo[o.steps & 1]) : nullptr;
         w.out = m.out;
@@ -2123,18 +2136,22 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
         w.rows = t.rows;
         w.cols = t.cols;
         w.pitch = t.pitch;
-        w.flags = flags | (target4 && m.cols % 4 == 0 ? kMuonAlignedRows : 0u);
-        w.strip0 = t.strip0;
+        w.flags = m.flags;
+        to.strip0[src.count] = static_cast<uint32_t>(target_strips);
         chunks += muon_chunks(m);
-        strips += muon_strips(m.rows, m.cols);
+        strips += muon_strips(m.rows, m.cols, t.vec);
+        target_strips += muon_strips(m.rows, m.cols, w.vec);
         ++src.count;
       }
     }
     to.count = src.count;
-    if (chunks > INT32_MAX || strips > INT32_MAX) return FLCE_ERR_UNSUPPORTED_SHAPE;
-    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_momentum(src, static_cast<uint32_t>(chunks), s); }));
+    src.chunk0[src.count] = static_cast<uint32_t>(chunks);
+    src.strip0[src.count] = static_cast<uint32_t>(strips);
+    to.strip0[src.count] = static_cast<uint32_t>(target_strips);
+    if (chunks > INT32_MAX || strips > INT32_MAX || target_strips > INT32_MAX) return FLCE_ERR_UNSUPPORTED_SHAPE;
+    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_momentum(src, s); }));
     if (st != FLCE_OK) return st;
-    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_scale(src, static_cast<uint32_t>(strips), s); }));
+    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_scale(src, dev.sms, s); }));
     if (st != FLCE_OK) return st;
     MuonArgs args{};
     args.timeout_ns = timeout_ns();
@@ -2148,7 +2165,7 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
         if (st != FLCE_OK) return st;
       }
     }
-    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_weights(to, static_cast<uint32_t>(strips), s); }));
+    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_weights(to, dev.sms, s); }));
     if (st != FLCE_OK) return st;
   }
   return FLCE_OK;

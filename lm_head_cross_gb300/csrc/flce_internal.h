@@ -415,33 +415,33 @@ static_assert(sizeof(AdamwArgs<kAdamwManyTensors>) <= 32764, "kernel argument li
 template <int N>
 cudaError_t launch_adamw(const AdamwArgs<N>& a, int state_bits, cudaStream_t stream);
 
-// Muon (flce_muon.cu).  Matrices of one shape form a group, [matrix][r][pitch] in the workspace; a
+// Muon (flce_muon.cu).  Matrices of one shape form a group, [matrix][rows][pitch] in the workspace; a
 // call runs in rounds of as many groups and matrices as the kernels' arguments hold.
 constexpr int kMuonGroups = 12;
 constexpr int kMuonMatrices = 256;
 constexpr int kMuonChunk = 8192;     // elements of one block of the momentum's pass
+constexpr int kMuonStrip = 4096;     // and of the passes between a tensor and X
 constexpr int kMuonExactRows = 128;  // up to this many rows, pairs of fp16 everywhere
 constexpr int kMuonPairSteps = 3;    // else for the first iterates alone
 constexpr float kMuonXScale = 16384.f, kMuonAScale = 8192.f;
 enum MuonMode : int { kMuonGram, kMuonPoly, kMuonApply };
 enum : uint32_t {
-  kMuonTall = 1,
-  kMuonParamF32 = 2,
-  kMuonGradF32 = 4,
-  kMuonAligned = 8,      // gradient and momentum: four elements at a time from the start on
-  kMuonAlignedRows = 16  // every tensor of the matrix, and its rows are whole numbers of four
+  kMuonParamF32 = 1,
+  kMuonGradF32 = 2,
+  kMuonAligned = 4  // gradient and momentum: four elements at a time from the start on
 };
 // One launch's view of a group: out = alpha a b, + gamma (and in kPoly alpha diag) on the diagonal,
-// + beta lo; [r, n].  Operands in boxes of 64 columns by 128 and by 64 rows.
+// + beta lo; [m, n].  Operands in boxes of 64 columns by 128 and by 64 rows.
 struct MuonGroup {
   CUtensorMap a128, a64, b128, b64;
   CUtensorMap a_lo128, a_lo64, b_lo128, b_lo64;  // what their rounding to fp16 left (segments = 3)
   CUtensorMap out, out_lo;
-  float* diag;  // [matrix][r], for the square: what rounding the diagonal left (null: nothing)
+  float* diag;  // [matrix][m], for the square: what rounding the diagonal left (null: nothing)
   float alpha, beta, gamma;
-  int r, n;
+  int m, n;
   int kblocks, segments;  // 64-element steps of the contraction; 3 for hi hi + hi lo + lo hi, else 1
-  int tile0, tiles_each, row_tiles;
+  int tile0, tiles_each, row_tiles, col_tiles;
+  int tall;               // X has more rows than columns
   int lo_in, write_lo;    // add beta times out_lo's old values; write out_lo
 };
 struct MuonArgs {
@@ -454,12 +454,15 @@ static_assert(sizeof(MuonArgs) <= 32764, "kernel argument limit");
 struct MuonSource {
   const void* grad;
   float* momentum;  // or null: the gradient itself is what is orthogonalised
-  __half *hi, *lo;  // the internal matrix
+  __half *hi, *lo;  // X, rows of `pitch` elements
   int rows, cols, pitch;
   uint32_t flags;
-  uint32_t chunk0, strip0;
+  int vec;  // columns at a time that every tensor's rows allow: 4, 2 or 1
 };
 struct MuonSources {
+  // the first block of work of each source, and the number of blocks behind the last: apart from
+  // the sources, so that a search stays within a few lines of the constant cache
+  uint32_t chunk0[kMuonMatrices + 1], strip0[kMuonMatrices + 1];
   MuonSource s[kMuonMatrices];
   int count;
   float mu, omm;  // momentum and 1 - momentum
@@ -467,7 +470,8 @@ struct MuonSources {
   float eps;
   const float* grad_scale;
   float* part;   // a sum of squares for each chunk
-  int* status;   // set to 0 by the momentum's pass (null: left alone)
+  int* status;
+  int first;     // the momentum's pass clears the status word
 };
 static_assert(sizeof(MuonSources) <= 32764, "kernel argument limit");
 // Where X goes: out (bf16), or w <- w decay - rate X on the weights.
@@ -478,17 +482,20 @@ struct MuonTarget {
   float* master;
   float decay, rate;
   int rows, cols, pitch;
-  uint32_t flags, strip0;
+  uint32_t flags;
+  int vec;
 };
 struct MuonTargets {
+  uint32_t strip0[kMuonMatrices + 1];
   MuonTarget t[kMuonMatrices];
   int count;
+  int* status;
 };
 static_assert(sizeof(MuonTargets) <= 32764, "kernel argument limit");
-int64_t muon_strips(int64_t rows, int64_t cols);  // blocks of the scale's and the weights' launch for one matrix
-cudaError_t launch_muon_momentum(const MuonSources& a, uint32_t chunks, cudaStream_t stream);
-cudaError_t launch_muon_scale(const MuonSources& a, uint32_t strips, cudaStream_t stream);
-cudaError_t launch_muon_weights(const MuonTargets& a, uint32_t strips, cudaStream_t stream);
+int64_t muon_strips(int64_t rows, int64_t cols, int vec);  // blocks of the scale's or the weights' launch for one matrix
+cudaError_t launch_muon_momentum(const MuonSources& a, cudaStream_t stream);
+cudaError_t launch_muon_scale(const MuonSources& a, int sms, cudaStream_t stream);
+cudaError_t launch_muon_weights(const MuonTargets& a, int sms, cudaStream_t stream);
 // bn: columns of a tile, 256 or 128.
 cudaError_t launch_muon_product(int mode, int bn, const MuonArgs& a, int sms, cudaStream_t stream);
 

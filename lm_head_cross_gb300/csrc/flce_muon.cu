@@ -1,8 +1,9 @@
 // Muon: an update's matrix orthogonalised by Newton-Schulz products, alone or as a step.
 //
 //   m <- mu m + (1 - mu) g,   u = mu m + (1 - mu) g (Nesterov) or m         (a step's first part)
-//   X = u / (|u|_F + eps), on the side where it has fewer rows than columns [r, c]
-//   steps times:  A = X X^T,   P = a I + b A + c A^2,   X <- P X
+//   X = u / (|u|_F + eps)
+//   steps times:  A = X X^T,   P = a I + b A + c A^2,   X <- P X     (rows <= columns)
+//                 A = X^T X,   P the same,              X <- X P     (rows > columns)
 //   w <- w (1 - lr wd) - lr scale X                                         (a step's last part)
 //
 // An odd polynomial of X's singular values: with the usual coefficients five steps bring those
@@ -121,12 +122,13 @@ __device__ __forceinline__ bool find_tile(const MuonArgs& a, int t, uint32_t ran
   o.matrix = t / g.tiles_each;
   t -= o.matrix * g.tiles_each;
   int ti = 0, tj;
-  if (MODE == kMuonApply) {  // a column of tiles shares its part of X
-    ti = t % g.row_tiles;
-    tj = t / g.row_tiles;
+  if (MODE == kMuonApply) {  // the tiles that share their part of X follow one another
+    const int inner = g.tall ? g.col_tiles : g.row_tiles;
+    ti = g.tall ? t / inner : t % inner;
+    tj = g.tall ? t % inner : t / inner;
   } else {  // the tiles of row ti from the diagonal on
     constexpr int kPer = kPairM / BN;
-    const int cols = (g.r + BN - 1) / BN;
+    const int cols = g.col_tiles;
     while (t >= cols - kPer * ti) t -= cols - kPer * ti++;
     tj = kPer * ti + t;
   }
@@ -138,6 +140,17 @@ __device__ __forceinline__ bool find_tile(const MuonArgs& a, int t, uint32_t ran
 // Whether rows of the 256-row block that holds `row` are stored at column k0 of a symmetric
 // matrix; else the block's transpose is.
 __device__ __forceinline__ bool stored(int row, int k0) { return k0 >= (row & ~(kPairM - 1)); }
+
+// Whether an operand's rows run along the contraction: X does in X X^T and as the left operand of
+// X P, a symmetric matrix where the block is stored.
+template <int MODE>
+__device__ __forceinline__ bool a_k_major(const MuonGroup& g, const Tile& t, int k0) {
+  return MODE == kMuonGram ? !g.tall : (MODE == kMuonApply && g.tall) || stored(t.m0, k0);
+}
+template <int MODE>
+__device__ __forceinline__ bool b_k_major(const MuonGroup& g, const Tile& t, int k0) {
+  return MODE == kMuonGram ? !g.tall : !(MODE == kMuonApply && !g.tall) && stored(t.n0, k0);
+}
 
 struct Bars {
   uint64_t *full, *empty, *tfull, *tempty, *ebar;
@@ -177,13 +190,13 @@ __device__ void run_producer(const MuonArgs& a, uint32_t rank, int pair, int pai
         const uint32_t bar = full_even + 8u * stage;
         if (rank == 0) mbar_arrive_expect_tx(&b.full[stage], 2 * S::kStageBytes);
         const int k0 = kb * kBK;
-        if (MODE == kMuonGram || stored(t.m0, k0)) {
+        if (a_k_major<MODE>(g, t, k0)) {
           tma_load_3d_pair(sa, a128, bar, k0, t.m0, t.matrix);
         } else {
           tma_load_3d_pair(sa, a64, bar, t.m0, k0, t.matrix);
           tma_load_3d_pair(sa + kMnBlock, a64, bar, t.m0 + 64, k0, t.matrix);
         }
-        if (MODE == kMuonGram || (MODE == kMuonPoly && stored(t.n0, k0))) {
+        if (b_k_major<MODE>(g, t, k0)) {
           tma_load_3d_pair(sb, BN == 256 ? b128 : b64, bar, k0, n0, t.matrix);
         } else {
 #pragma unroll
@@ -215,8 +228,8 @@ __device__ void run_mma(const MuonArgs& a, int pair, int pairs, uint8_t* smem, u
     uint32_t more = 0;
     for (int seg = 0; seg < t.g->segments; ++seg) {
       for (int kb = 0; kb < t.g->kblocks; ++kb) {
-        const bool a_mn = MODE != kMuonGram && !stored(t.m0, kb * kBK);
-        const bool b_mn = MODE == kMuonApply || (MODE == kMuonPoly && !stored(t.n0, kb * kBK));
+        const bool a_mn = !a_k_major<MODE>(*t.g, t, kb * kBK);
+        const bool b_mn = !b_k_major<MODE>(*t.g, t, kb * kBK);
         const uint32_t idesc = instr_desc_f16(kPairM, BN, a_mn, b_mn);
         if (!mbar_wait(&b.full[stage], phase, a.timeout_ns, b.abort_flag)) {
           record_timeout(a, 0, b.abort_flag);
@@ -288,7 +301,7 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
         tma_load_3d(stg + kStagingBuf, &g.out_lo, ebar, j0, i0, t.matrix);
       }
     };
-    if (lo_in && i0 < g.r && first < g.n) fetch(first);
+    if (lo_in && i0 < g.m && first < g.n) fetch(first);
     if (!mbar_wait(&b.tfull[acc], acc_phase, a.timeout_ns, b.abort_flag)) {
       record_timeout(a, rank, b.abort_flag);
       break;
@@ -299,7 +312,7 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
 #pragma unroll 1
     for (int h = 0; h < kCols / 64; ++h) {
       const int j0 = first + h * 64;
-      if (i0 >= g.r || j0 >= g.n) break;
+      if (i0 >= g.m || j0 >= g.n) break;
       __syncwarp();
       uint32_t d[64];
       tmem_ld_32x64(tbase + h * 64, d);
@@ -309,9 +322,9 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
       if (MODE != kMuonApply) {
         const int diag = row - j0;  // in this chunk, for the lanes of one row block alone
         if (static_cast<unsigned>(i0 - j0 + 31) < 95u) {
-          float* keep = g.diag ? g.diag + static_cast<int64_t>(t.matrix) * g.r + row : nullptr;
+          float* keep = g.diag ? g.diag + static_cast<int64_t>(t.matrix) * g.m + row : nullptr;
           float plus = g.gamma;
-          if (MODE == kMuonPoly && keep && row < g.r) plus = fmaf(g.alpha, *keep, plus);
+          if (MODE == kMuonPoly && keep && row < g.m) plus = fmaf(g.alpha, *keep, plus);
           float at = 0.f;
 #pragma unroll
           for (int j = 0; j < 64; ++j) {
@@ -320,7 +333,7 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
               at = v[j];
             }
           }
-          if (MODE == kMuonGram && keep && diag >= 0 && diag < 64 && row < g.r) {
+          if (MODE == kMuonGram && keep && diag >= 0 && diag < 64 && row < g.m) {
             const float hi = __half2float(__float2half_rn(at)), left = at - hi;
             *keep = fmaf(2.f, hi, left) * left;  // of the square
           }
@@ -409,6 +422,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     *b.abort_flag = 0;
     mbar_fence_init();
     fence_proxy_async_smem();
+    Tile t;  // what the first tile needs of the arguments, before the wait for the launch before
+    if (find_tile<MODE, BN>(a, pair, rank, t)) {
+      tma_prefetch_map(&t.g->a128);
+      tma_prefetch_map(&t.g->a64);
+      tma_prefetch_map(&t.g->b128);
+      tma_prefetch_map(&t.g->b64);
+      tma_prefetch_map(&t.g->out);
+      if (t.g->write_lo || t.g->lo_in) tma_prefetch_map(&t.g->out_lo);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
@@ -443,28 +465,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 
 // ----------------------------------------------------------------------------- momentum, norm, weights
 
-template <bool F32>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  return F32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-// Four from an element that is a multiple of four.
-__device__ __forceinline__ float4 load4(const void* p, int64_t i, bool f32) {
-  if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
-__device__ __forceinline__ float load_g(const MuonSource& s, int64_t i) {
-  return (s.flags & kMuonGradF32) ? load1<true>(s.grad, i) : load1<false>(s.grad, i);
-}
+// V (4, 2 or 1) consecutive elements from a multiple of V on, as they lie in memory: loads are
+// issued together, and their words are taken apart after the last.
+template <int V>
+struct Words {
+  uint32_t u[4];
+  __device__ __forceinline__ void load(const void* p, int64_t i, bool f32) {
+    if (f32) {
+      const float* q = static_cast<const float*>(p) + i;
+      if (V == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(q);
+        u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+      } else if (V == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(q);
+        u[0] = v.x, u[1] = v.y;
+      } else {
+        u[0] = *reinterpret_cast<const uint32_t*>(q);
+      }
+    } else {
+      load16(static_cast<const uint16_t*>(p) + i);
+    }
+  }
+  // of a two-byte type
+  __device__ __forceinline__ void load16(const uint16_t* q) {
+    if (V == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      u[0] = v.x, u[1] = v.y;
+    } else if (V == 2) {
+      u[0] = *reinterpret_cast<const uint32_t*>(q);
+    } else {
+      u[0] = *q;
+    }
+  }
+  __device__ __forceinline__ void zero() { u[0] = u[1] = u[2] = u[3] = 0; }
+  __device__ __forceinline__ float value(int e, bool f32) const {  // fp32 or bf16
+    return f32 ? __uint_as_float(u[e]) : __uint_as_float((e & 1) ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+  }
+  __device__ __forceinline__ float half(int e) const {
+    const float2 f = unpack_half2(u[e >> 1]);
+    return (e & 1) ? f.y : f.x;
+  }
+};
 
 // The source that holds block c of the launch.
-template <typename F>
-__device__ __forceinline__ int find_source(int count, uint32_t c, F first) {
+__device__ __forceinline__ int find_source(const uint32_t* first, int count, uint32_t c) {
   int lo = 0, hi = count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (first(mid) <= c) lo = mid;
+    if (first[mid] <= c) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -488,45 +536,54 @@ __device__ __forceinline__ Momentum momentum_of(const MuonSources& a) {
 __global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __grid_constant__ MuonSources a) {
   griddep_begin();
   const uint32_t c = blockIdx.x;
-  if (c == 0 && threadIdx.x == 0 && a.status) *a.status = kOk;
-  const int si = find_source(a.count, c, [&](int i) { return a.s[i].chunk0; });
+  if (c == 0 && threadIdx.x == 0 && a.first) *a.status = kOk;
+  const int si = find_source(a.chunk0, a.count, c);
   const MuonSource& s = a.s[si];
-  const int64_t begin = static_cast<int64_t>(c - s.chunk0) * kMuonChunk;
-  const int64_t end = min(begin + kMuonChunk, static_cast<int64_t>(s.rows) * s.cols);
+  const int64_t size = static_cast<int64_t>(s.rows) * s.cols;
+  const int64_t begin = static_cast<int64_t>(c - a.chunk0[si]) * kMuonChunk, end = min(begin + kMuonChunk, size);
   const Momentum q = momentum_of(a);
+  const bool f32 = s.flags & kMuonGradF32, mom = s.momentum != nullptr;
   float sum = 0.f;
   if ((s.flags & kMuonAligned) && end - begin == kMuonChunk) {
-    const bool f32 = s.flags & kMuonGradF32;
 #pragma unroll
     for (int k0 = 0; k0 < 8; k0 += 4) {
-      float4 g[4], m[4];
+      const int64_t i0 = begin + (k0 * kNormThreads + static_cast<int>(threadIdx.x)) * 4;
+      Words<4> g[4], m[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int64_t i = begin + ((k0 + k) * kNormThreads + threadIdx.x) * 4;
-        g[k] = load4(s.grad, i, f32);
-        m[k] = s.momentum ? *reinterpret_cast<const float4*>(s.momentum + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int64_t i = i0 + k * (4 * kNormThreads);
+        g[k].zero();
+        m[k].zero();
+        if (!in_bounds(i + 3, size, a.status)) continue;
+        g[k].load(s.grad, i, f32);
+        if (mom) m[k].load(s.momentum, i, true);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float4 u = make_float4(g[k].x * q.gs, g[k].y * q.gs, g[k].z * q.gs, g[k].w * q.gs);
-        if (s.momentum) {
-          const float4 n = make_float4(q.move(m[k].x, g[k].x), q.move(m[k].y, g[k].y), q.move(m[k].z, g[k].z),
-                                       q.move(m[k].w, g[k].w));
-          *reinterpret_cast<float4*>(s.momentum + begin + ((k0 + k) * kNormThreads + threadIdx.x) * 4) = n;
-          u = make_float4(q.u(n.x, g[k].x), q.u(n.y, g[k].y), q.u(n.z, g[k].z), q.u(n.w, g[k].w));
+        const int64_t i = i0 + k * (4 * kNormThreads);
+        float n[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float gv = g[k].value(e, f32);
+          n[e] = q.move(m[k].value(e, true), gv);
+          const float u = mom ? q.u(n[e], gv) : gv * q.gs;
+          sum = fmaf(u, u, sum);
         }
-        sum = fmaf(u.x, u.x, fmaf(u.y, u.y, fmaf(u.z, u.z, fmaf(u.w, u.w, sum))));
+        if (mom && in_bounds(i + 3, size, a.status))
+          *reinterpret_cast<float4*>(s.momentum + i) = make_float4(n[0], n[1], n[2], n[3]);
       }
     }
   } else {
-#pragma unroll 4
     for (int64_t i = begin + threadIdx.x; i < end; i += kNormThreads) {
-      const float g = load_g(s, i);
-      float u = g * q.gs;
-      if (s.momentum) {
-        const float m = q.move(s.momentum[i], g);
+      if (!in_bounds(i, size, a.status)) continue;
+      Words<1> g;
+      g.load(s.grad, i, f32);
+      const float gv = g.value(0, f32);
+      float u = gv * q.gs;
+      if (mom) {
+        const float m = q.move(s.momentum[i], gv);
         s.momentum[i] = m;
-        u = q.u(m, g);
+        u = q.u(m, gv);
       }
       sum = fmaf(u, u, sum);
     }
@@ -542,195 +599,174 @@ __global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __gri
   }
 }
 
-constexpr int kStrip = 64;  // tiles of kStrip x kStrip go through shared memory, to be turned where the matrix is tall
+// The passes between a tensor and its X take blocks of kMuonStrip elements: a warp's lanes hold V
+// (4, 2 or 1, as the rows' alignment allows) consecutive columns each, a thread 16 / V rows.
+static_assert(kMuonStrip == kNormThreads * 16, "16 elements a thread");
 
+template <int V>
 struct Strip {
-  int r0, c0;    // in the tensor
-  int rr, cc;    // in the internal matrix
-  int nr, nc;    // its size
-  bool tall;
+  int row, col, rows, cols;
+  __device__ __forceinline__ Strip(int rows_, int cols_, uint32_t k) : rows(rows_), cols(cols_) {
+    const uint32_t across = (static_cast<uint32_t>(cols) + 32 * V - 1) / (32 * V);
+    row = static_cast<int>(k / across) * (128 / V) + static_cast<int>(threadIdx.x >> 5);
+    col = static_cast<int>(k % across) * (32 * V) + static_cast<int>(threadIdx.x & 31) * V;
+  }
+  __device__ __forceinline__ bool in(int k) const { return row + 8 * k < rows && col < cols; }
+  __device__ __forceinline__ int64_t at(int k, int pitch) const { return static_cast<int64_t>(row + 8 * k) * pitch + col; }
 };
-__device__ __forceinline__ Strip strip_of(const MuonSource& s, uint32_t q) {
-  Strip t;
-  const int across = (s.cols + kStrip - 1) / kStrip, k = static_cast<int>(q - s.strip0);
-  t.r0 = k / across * kStrip;
-  t.c0 = k % across * kStrip;
-  t.tall = s.flags & kMuonTall;
-  t.rr = t.tall ? t.c0 : t.r0;
-  t.cc = t.tall ? t.r0 : t.c0;
-  t.nr = t.tall ? s.cols : s.rows;
-  t.nc = t.tall ? s.rows : s.cols;
-  return t;
+
+template <int V>
+__device__ __forceinline__ void store_v(void* p, int64_t i, bool f32, const float (&x)[V]) {
+  if (f32) {
+    float* q = static_cast<float*>(p) + i;
+    if (V == 4) *reinterpret_cast<float4*>(q) = make_float4(x[0], x[1 % V], x[2 % V], x[3 % V]);
+    else if (V == 2) *reinterpret_cast<float2*>(q) = make_float2(x[0], x[1 % V]);
+    else *q = x[0];
+  } else {
+    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + i;
+    if (V == 4) *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16x2(x[0], x[1 % V]), pack_bf16x2(x[2 % V], x[3 % V]));
+    else if (V == 2) *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(x[0], x[1 % V]);
+    else *q = __float2bfloat16_rn(x[0]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_h(__half* p, const float (&x)[V]) {
+  if (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack_half2(x[0], x[1 % V]), pack_half2(x[2 % V], x[3 % V]));
+  else if (V == 2) *reinterpret_cast<uint32_t*>(p) = pack_half2(x[0], x[1 % V]);
+  else *p = __float2half_rn(x[0]);
 }
 
-// One tile of one source: u / (|u| + eps) as a pair of fp16.  The launch runs through the sources
-// backwards: what the momentum's pass left in L2 is read first.
-__global__ void __launch_bounds__(kNormThreads) muon_scale_kernel(const __grid_constant__ MuonSources a) {
-  griddep_begin();
-  __shared__ float tile[kStrip][kStrip + 1];
-  __shared__ double red[kNormThreads / 32];
-  const uint32_t q = gridDim.x - 1 - blockIdx.x;
-  const int si = find_source(a.count, q, [&](int i) { return a.s[i].strip0; });
-  const MuonSource& s = a.s[si];
-  const int tid = threadIdx.x;
-  const Strip t = strip_of(s, q);
-  const Momentum mo = momentum_of(a);
-  const bool f32 = s.flags & kMuonGradF32;
-  const bool need_g = !s.momentum || a.nesterov;
-  if (s.flags & kMuonAlignedRows) {  // four columns a thread; rows are whole numbers of them
-    float4 g[4], m[4];
+// X = u / (|u| + eps) as a pair of fp16.
+template <int V>
+__device__ __forceinline__ void scale_strip(const MuonSources& a, const MuonSource& s, uint32_t k0, const Momentum& mo,
+                                            float inv) {
+  constexpr int kRows = 16 / V;
+  constexpr int kBatch = kRows < 8 ? kRows : 8;
+  const Strip<V> t(s.rows, s.cols, k0);
+  const int64_t size = static_cast<int64_t>(s.rows) * s.cols, room = static_cast<int64_t>(s.rows) * s.pitch;
+  const bool f32 = s.flags & kMuonGradF32, mom = s.momentum != nullptr, need_g = !mom || a.nesterov;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = (k * kNormThreads + tid) / (kStrip / 4), j = (k * kNormThreads + tid) % (kStrip / 4) * 4;
-      g[k] = m[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t.r0 + i < s.rows && t.c0 + j < s.cols) {
-        const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
-        if (need_g) g[k] = load4(s.grad, at, f32);
-        if (s.momentum) m[k] = *reinterpret_cast<const float4*>(s.momentum + at);
-      }
+  for (int b = 0; b < kRows; b += kBatch) {
+    Words<V> g[kBatch], m[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      g[k].zero();
+      m[k].zero();
+      const int64_t at = t.at(b + k, s.cols);
+      if (!t.in(b + k) || !in_bounds(at + V - 1, size, a.status)) continue;
+      if (need_g) g[k].load(s.grad, at, f32);
+      if (mom) m[k].load(s.momentum, at, true);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = (k * kNormThreads + tid) / (kStrip / 4), j = (k * kNormThreads + tid) % (kStrip / 4) * 4;
-      float* o = &tile[i][j];
-      const bool mom = s.momentum;
-      o[0] = mom ? mo.u(m[k].x, g[k].x) : g[k].x * mo.gs;
-      o[1] = mom ? mo.u(m[k].y, g[k].y) : g[k].y * mo.gs;
-      o[2] = mom ? mo.u(m[k].z, g[k].z) : g[k].z * mo.gs;
-      o[3] = mom ? mo.u(m[k].w, g[k].w) : g[k].w * mo.gs;
-    }
-  } else {
-#pragma unroll 8
-    for (int k = tid; k < kStrip * kStrip; k += kNormThreads) {
-      const int i = k / kStrip, j = k % kStrip;
-      float u = 0.f;
-      if (t.r0 + i < s.rows && t.c0 + j < s.cols) {
-        const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
-        const float g = need_g ? load_g(s, at) : 0.f;
-        u = s.momentum ? mo.u(s.momentum[at], g) : g * mo.gs;
+    for (int k = 0; k < kBatch; ++k) {
+      float hi[V], lo[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float gv = g[k].value(e, f32);
+        hi[e] = (mom ? mo.u(m[k].value(e, true), gv) : gv * mo.gs) * inv;
+        lo[e] = hi[e] - __half2float(__float2half_rn(hi[e]));
       }
-      tile[i][j] = u;
+      const int64_t at = t.at(b + k, s.pitch);
+      if (!t.in(b + k) || !in_bounds(at + V - 1, room, a.status)) continue;
+      store_h<V>(s.hi + at, hi);
+      store_h<V>(s.lo + at, lo);
     }
   }
-  const int64_t chunks = (static_cast<int64_t>(s.rows) * s.cols + kMuonChunk - 1) / kMuonChunk;
-  double sum = 0.0;
-  for (int64_t i = tid; i < chunks; i += kNormThreads) sum += static_cast<double>(a.part[s.chunk0 + i]);
+}
+
+// 1 / (|u| + eps), times X's scale.  A sum of squares past fp32's range, or a non-finite element,
+// makes the whole matrix NaN.
+__device__ __forceinline__ float norm_factor(const MuonSources& a, int si, float* red) {
+  float sum = 0.f;
+  for (uint32_t i = a.chunk0[si] + threadIdx.x; i < a.chunk0[si + 1]; i += kNormThreads) sum += a.part[i];
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  if ((tid & 31) == 0) red[tid >> 5] = sum;
+  __syncthreads();  // (the last factor has been read)
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
   sum = red[0];
 #pragma unroll
   for (int k = 1; k < kNormThreads / 32; ++k) sum += red[k];
-  // a sum of squares past fp32's range, or a non-finite element, makes the whole matrix NaN
-  const float total = static_cast<float>(sum);
-  const float inv = isfinite(total) ? kMuonXScale / (sqrtf(total) + a.eps) : NAN;
-#pragma unroll
-  for (int k = tid; k < kStrip * kStrip / 4; k += kNormThreads) {
-    const int i = k / (kStrip / 4), j = k % (kStrip / 4) * 4;
-    if (t.rr + i >= t.nr || t.cc + j >= t.nc) continue;  // (the pitch is a multiple of 8: four always fit)
-    float x[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = (t.tall ? tile[j + e][i] : tile[i][j + e]) * inv;
-    uint2 hi, lo;
-    hi.x = pack_half2(x[0], x[1]);
-    hi.y = pack_half2(x[2], x[3]);
-    const float2 f0 = unpack_half2(hi.x), f1 = unpack_half2(hi.y);
-    lo.x = pack_half2(x[0] - f0.x, x[1] - f0.y);
-    lo.y = pack_half2(x[2] - f1.x, x[3] - f1.y);
-    const int64_t at = static_cast<int64_t>(t.rr + i) * s.pitch + t.cc + j;
-    *reinterpret_cast<uint2*>(s.hi + at) = hi;
-    *reinterpret_cast<uint2*>(s.lo + at) = lo;
+  return isfinite(sum) ? kMuonXScale / (sqrtf(sum) + a.eps) : NAN;
+}
+
+// Blocks take runs of consecutive strips, from the last source to the first: what the momentum's
+// pass left in L2 is read first.
+__global__ void __launch_bounds__(kNormThreads) muon_scale_kernel(const __grid_constant__ MuonSources a, uint32_t run) {
+  griddep_begin();
+  __shared__ float red[kNormThreads / 32];
+  const uint32_t begin = (gridDim.x - 1 - blockIdx.x) * run, end = min(begin + run, a.strip0[a.count]);
+  if (begin >= end) return;
+  int si = find_source(a.strip0, a.count, begin);
+  const Momentum mo = momentum_of(a);
+  float inv = norm_factor(a, si, red);
+  for (uint32_t q = begin; q < end; ++q) {
+    if (q >= a.strip0[si + 1]) inv = norm_factor(a, ++si, red);
+    const MuonSource& s = a.s[si];
+    const uint32_t k = q - a.strip0[si];
+    if (s.vec == 4) scale_strip<4>(a, s, k, mo, inv);
+    else if (s.vec == 2) scale_strip<2>(a, s, k, mo, inv);
+    else scale_strip<1>(a, s, k, mo, inv);
   }
 }
 
-// One tile of one matrix: X, from the internal matrix, to out as bf16, or taken off the weights.
-__global__ void __launch_bounds__(kNormThreads) muon_weights_kernel(const __grid_constant__ MuonTargets a) {
-  griddep_begin();
-  __shared__ float tile[kStrip][kStrip + 1];
-  const uint32_t q = blockIdx.x;
-  const int si = find_source(a.count, q, [&](int i) { return a.t[i].strip0; });
-  const MuonTarget& s = a.t[si];
-  const int tid = threadIdx.x;
-  MuonSource shape{};
-  shape.rows = s.rows;
-  shape.cols = s.cols;
-  shape.flags = s.flags;
-  shape.strip0 = s.strip0;
-  const Strip t = strip_of(shape, q);
-  const bool f32 = s.flags & kMuonParamF32, vec = s.flags & kMuonAlignedRows;
-  float4 w[4];
-  if (!s.out && vec) {  // under way while X is turned
+template <int V>
+__device__ __forceinline__ void weights_strip(const MuonTarget& s, uint32_t k0, int* status) {
+  constexpr int kRows = 16 / V;
+  constexpr int kBatch = kRows < 8 ? kRows : 8;
+  const Strip<V> t(s.rows, s.cols, k0);
+  const int64_t size = static_cast<int64_t>(s.rows) * s.cols, room = static_cast<int64_t>(s.rows) * s.pitch;
+  const bool f32 = s.flags & kMuonParamF32, master = s.master != nullptr;
+  const void* old = master ? s.master : s.param;  // null: X itself is the result
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = (k * kNormThreads + tid) / (kStrip / 4), j = (k * kNormThreads + tid) % (kStrip / 4) * 4;
-      w[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t.r0 + i < s.rows && t.c0 + j < s.cols) {
-        const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
-        w[k] = s.master ? *reinterpret_cast<const float4*>(s.master + at) : load4(s.param, at, f32);
-      }
-    }
-  }
+  for (int b = 0; b < kRows; b += kBatch) {
+    Words<V> x[kBatch], l[kBatch], w[kBatch];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int i = (k * kNormThreads + tid) / (kStrip / 8), j = (k * kNormThreads + tid) % (kStrip / 8) * 8;
-    uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-    if (t.rr + i < t.nr && t.cc + j < t.nc) {
-      const int64_t at = static_cast<int64_t>(t.rr + i) * s.pitch + t.cc + j;
-      hi = *reinterpret_cast<const uint4*>(s.hi + at);
-      if (s.lo) lo = *reinterpret_cast<const uint4*>(s.lo + at);
+    for (int k = 0; k < kBatch; ++k) {
+      x[k].zero();
+      l[k].zero();
+      w[k].zero();
+      const int64_t from = t.at(b + k, s.pitch), at = t.at(b + k, s.cols);
+      if (!t.in(b + k) || !in_bounds(from + V - 1, room, status) || !in_bounds(at + V - 1, size, status)) continue;
+      x[k].load16(reinterpret_cast<const uint16_t*>(s.hi) + from);
+      if (s.lo) l[k].load16(reinterpret_cast<const uint16_t*>(s.lo) + from);
+      if (old) w[k].load(old, at, f32 || master);
     }
-    const uint32_t uh[4] = {hi.x, hi.y, hi.z, hi.w}, ul[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_half2(uh[e]), g = unpack_half2(ul[e]);
-      const float x0 = (f.x + g.x) * (1.f / kMuonXScale), x1 = (f.y + g.y) * (1.f / kMuonXScale);
-      if (t.tall) {
-        tile[j + 2 * e][i] = x0;
-        tile[j + 2 * e + 1][i] = x1;
-      } else {
-        tile[i][j + 2 * e] = x0;
-        tile[i][j + 2 * e + 1] = x1;
-      }
-    }
-  }
-  __syncthreads();
-  if (vec) {
+    for (int k = 0; k < kBatch; ++k) {
+      float y[V];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = (k * kNormThreads + tid) / (kStrip / 4), j = (k * kNormThreads + tid) % (kStrip / 4) * 4;
-      if (t.r0 + i >= s.rows || t.c0 + j >= s.cols) continue;
-      const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
-      float4 x = make_float4(tile[i][j], tile[i][j + 1], tile[i][j + 2], tile[i][j + 3]);
-      void* to = s.out;
-      if (!s.out) {
-        x = make_float4(fmaf(-s.rate, x.x, w[k].x * s.decay), fmaf(-s.rate, x.y, w[k].y * s.decay),
-                        fmaf(-s.rate, x.z, w[k].z * s.decay), fmaf(-s.rate, x.w, w[k].w * s.decay));
-        if (s.master) *reinterpret_cast<float4*>(s.master + at) = x;
-        to = s.param;
+      for (int e = 0; e < V; ++e) {
+        y[e] = (x[k].half(e) + l[k].half(e)) * (1.f / kMuonXScale);
+        if (old) y[e] = fmaf(-s.rate, y[e], w[k].value(e, f32 || master) * s.decay);
       }
-      if (!s.out && f32) *reinterpret_cast<float4*>(static_cast<float*>(to) + at) = x;
-      else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to) + at) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-    }
-  } else {
-#pragma unroll 4
-    for (int k = tid; k < kStrip * kStrip; k += kNormThreads) {
-      const int i = k / kStrip, j = k % kStrip;
-      if (t.r0 + i >= s.rows || t.c0 + j >= s.cols) continue;
-      const int64_t at = static_cast<int64_t>(t.r0 + i) * s.cols + t.c0 + j;
-      float x = tile[i][j];
-      if (s.out) {
-        static_cast<__nv_bfloat16*>(s.out)[at] = __float2bfloat16_rn(x);
-        continue;
-      }
-      const float p = s.master ? s.master[at] : f32 ? load1<true>(s.param, at) : load1<false>(s.param, at);
-      x = fmaf(-s.rate, x, p * s.decay);
-      if (s.master) s.master[at] = x;
-      if (f32) static_cast<float*>(s.param)[at] = x;
-      else static_cast<__nv_bfloat16*>(s.param)[at] = __float2bfloat16_rn(x);
+      const int64_t at = t.at(b + k, s.cols);
+      if (!t.in(b + k) || !in_bounds(at + V - 1, size, status)) continue;
+      if (master) store_v<V>(s.master, at, true, y);
+      if (old) store_v<V>(s.param, at, f32, y);
+      else store_v<V>(s.out, at, false, y);
     }
   }
 }
+
+// X to out as bf16, or taken off the weights.
+__global__ void __launch_bounds__(kNormThreads) muon_weights_kernel(const __grid_constant__ MuonTargets a, uint32_t run) {
+  griddep_begin();
+  const uint32_t begin = blockIdx.x * run, end = min(begin + run, a.strip0[a.count]);
+  if (begin >= end) return;
+  int si = find_source(a.strip0, a.count, begin);
+  for (uint32_t q = begin; q < end; ++q) {
+    if (q >= a.strip0[si + 1]) ++si;
+    const MuonTarget& s = a.t[si];
+    const uint32_t k = q - a.strip0[si];
+    if (s.vec == 4) weights_strip<4>(s, k, a.status);
+    else if (s.vec == 2) weights_strip<2>(s, k, a.status);
+    else weights_strip<1>(s, k, a.status);
+  }
+}
+
+// Runs of strips for blocks of a launch: about four waves of the SMs' blocks, one strip at least.
+uint32_t run_length(uint32_t strips, int sms) { return std::max<uint32_t>(1, strips / (static_cast<uint32_t>(sms) * 16)); }
 
 template <int MODE, int BN>
 cudaError_t launch_mode(const MuonArgs& a, int sms, cudaStream_t s) {
@@ -750,17 +786,19 @@ cudaError_t launch_width(int mode, const MuonArgs& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_muon_momentum(const MuonSources& a, uint32_t chunks, cudaStream_t s) {
-  return launch_k(muon_momentum_kernel, dim3(chunks), dim3(kNormThreads), 0, s, a);
+cudaError_t launch_muon_momentum(const MuonSources& a, cudaStream_t s) {
+  return launch_k(muon_momentum_kernel, dim3(a.chunk0[a.count]), dim3(kNormThreads), 0, s, a);
 }
-cudaError_t launch_muon_scale(const MuonSources& a, uint32_t strips, cudaStream_t s) {
-  return launch_k(muon_scale_kernel, dim3(strips), dim3(kNormThreads), 0, s, a);
+cudaError_t launch_muon_scale(const MuonSources& a, int sms, cudaStream_t s) {
+  const uint32_t n = a.strip0[a.count], run = run_length(n, sms);
+  return launch_k(muon_scale_kernel, dim3((n + run - 1) / run), dim3(kNormThreads), 0, s, a, run);
 }
-cudaError_t launch_muon_weights(const MuonTargets& a, uint32_t strips, cudaStream_t s) {
-  return launch_k(muon_weights_kernel, dim3(strips), dim3(kNormThreads), 0, s, a);
+cudaError_t launch_muon_weights(const MuonTargets& a, int sms, cudaStream_t s) {
+  const uint32_t n = a.strip0[a.count], run = run_length(n, sms);
+  return launch_k(muon_weights_kernel, dim3((n + run - 1) / run), dim3(kNormThreads), 0, s, a, run);
 }
-int64_t muon_strips(int64_t rows, int64_t cols) {
-  return (rows + kStrip - 1) / kStrip * ((cols + kStrip - 1) / kStrip);
+int64_t muon_strips(int64_t rows, int64_t cols, int vec) {
+  return (rows * vec + 127) / 128 * ((cols + 32 * vec - 1) / (32 * vec));
 }
 cudaError_t launch_muon_product(int mode, int bn, const MuonArgs& a, int sms, cudaStream_t s) {
   return bn == 256 ? launch_width<256>(mode, a, sms, s) : launch_width<128>(mode, a, sms, s);
