@@ -430,7 +430,7 @@ flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, cons
  *   dW_v = scale sum_{i : id_i = v} dy_i   (0 for v = padding_idx).
  *   - W and dW share one type, y and dy another (flce_dtype_t each; the forward
  *     pass needs them equal).  Sums are fp32, in the order of the tokens'
- *     positions (an id with more than 32 tokens: in parts, themselves in order),
+ *     positions (in parts, themselves in order, where an id has several tokens),
  *     and rounded once: the same inputs give the same bits.
  *   - add = 0: all v rows of dW are written.  add = 1: dW receives dW + the
  *     gradient, rounded once; rows without a token are neither read nor written.

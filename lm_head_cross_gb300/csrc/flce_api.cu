@@ -1802,7 +1802,7 @@ flce_status_t flce_embedding_backward(const flce_embedding_t* q, const void* dy,
   st = cuda_status(timed(3, 0.0, s, [&] { return launch_embed_sort(ep, q->padding_idx, ids, o, dev.sms, s); }));
   if (st != FLCE_OK) return st;
   return cuda_status(
-      timed(3, 0.0, s, [&] { return launch_embed_backward(ep, dy, o, dW, add != 0, dev.sms, s); }));
+      timed(3, 0.0, s, [&] { return launch_embed_backward(ep, dy, o, dW, add != 0, s); }));
 }
 
 // ----------------------------------------------------------------------------- AdamW

@@ -7,13 +7,14 @@
 // gradient reads N H elements and writes V H (or reads and writes the distinct rows).
 //
 // The gradient's sums have one order, whatever the schedule: the tokens are sorted by (id,
-// position), a row of dW is the sum over its tokens in that order in fp32, in parts of at most
-// kTile tokens where it has more, the parts added in order, and rounded once.
+// position) and cut into tiles of kTile; a row of dW is the sum over its tokens in that order in
+// fp32, one part for each tile that it has tokens in, the parts added in order, and rounded once.
 //   sort   every block owns a range of the vocabulary and reads all ids twice (they stay in L2):
 //          once to count, a count for each (warp's stretch of positions, id), and once to place
 //          its tokens.  No block waits for another, no atomics in global memory, one launch.
-//   parts  tokens of frequent ids (more than kTile of them), tile by tile of the sorted order
-//   rows   every row of dW: zeros, the sum of its few tokens, or the sum of its parts
+//   tiles  every tile's tokens, 32 chunks of columns a warp: rows that lie within the tile are
+//          finished, the others leave a part; beside them, zeros for the rows without a token
+//   join   the rows with several parts
 #include "flce_device.cuh"
 #include "flce_internal.h"
 #include "flce_launch.cuh"
@@ -170,7 +171,8 @@ __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, i
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortBatch = 8;  // loads of ids in flight
+constexpr int kSortBatch = 16;  // loads of ids in flight
+constexpr int32_t kNoToken = INT32_MIN;  // behind a stretch's end: outside every range
 
 // Block b owns ids [b per, (b + 1) per).  Warp w counts and places the positions of its stretch
 // [w seg, (w + 1) seg), so that (id, warp, position) is the sorted order.
@@ -191,20 +193,27 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, 
   int32_t* row = count + warp * per;
   const int64_t p0 = static_cast<int64_t>(warp) * seg;
   const int64_t p1 = min(p0 + seg, static_cast<int64_t>(n));
+  const uint32_t ulo = static_cast<uint32_t>(lo), umine = static_cast<uint32_t>(mine);
   int below = 0, bad = 0;
   for (int64_t p = p0; p < p1; p += 32 * kSortBatch) {
     int32_t id[kSortBatch];
 #pragma unroll
     for (int k = 0; k < kSortBatch; ++k) {
       const int64_t i = p + 32 * k + lane;
-      id[k] = i < p1 ? __ldg(ids + i) : pad;
-      if (i < p1) bad |= static_cast<uint32_t>(id[k]) >= static_cast<uint32_t>(v);
+      id[k] = i < p1 ? __ldg(ids + i) : kNoToken;
     }
+    uint32_t hits = 0;  // few: the block owns a small part of the vocabulary
 #pragma unroll
     for (int k = 0; k < kSortBatch; ++k) {
-      if (id[k] == pad || static_cast<uint32_t>(id[k]) >= static_cast<uint32_t>(v)) continue;
-      below += id[k] < lo;
-      if (id[k] >= lo && id[k] - lo < mine) atomicAdd(row + (id[k] - lo), 1);
+      const uint32_t u = static_cast<uint32_t>(id[k]);  // (an id below 0 is above every range)
+      below += u < ulo && id[k] != pad;
+      hits |= (u - ulo < umine ? 1u : 0u) << k;
+      if (blockIdx.x == 0) bad |= u >= static_cast<uint32_t>(v) && p + 32 * k + lane < p1;
+    }
+    if (hits) {
+#pragma unroll
+      for (int k = 0; k < kSortBatch; ++k)
+        if ((hits >> k & 1) && id[k] != pad) atomicAdd(row + (id[k] - lo), 1);
     }
   }
   below = __reduce_add_sync(kFull, below);
@@ -249,11 +258,11 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, 
 #pragma unroll
     for (int k = 0; k < kSortBatch; ++k) {
       const int64_t i = p + 32 * k + lane;
-      id[k] = i < p1 ? __ldg(ids + i) : pad;
+      id[k] = i < p1 ? __ldg(ids + i) : kNoToken;
     }
 #pragma unroll
     for (int k = 0; k < kSortBatch; ++k) {
-      const bool in = id[k] != pad && id[k] >= lo && id[k] - lo < mine;
+      const bool in = static_cast<uint32_t>(id[k]) - ulo < umine && id[k] != pad;
       const uint32_t some = __ballot_sync(kFull, in);
       if (!some) continue;
       if (in) {
@@ -273,87 +282,6 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, 
 }
 
 // ----------------------------------------------------------------------------- sums
-
-// Adds the rows order[a .. b) of dy at columns [col, col + 8) to x, in order.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t h, const int32_t* __restrict__ order, int a,
-                                         int b, int col, float (&x)[8]) {
-  constexpr int kBatch = 4;
-  const bool whole = ALIGNED || (col >= 0 && col + 8 <= h);
-  int i = a;
-  for (; i + kBatch <= b; i += kBatch) {
-    float t[kBatch][8];
-    int64_t at[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) at[k] = static_cast<int64_t>(__ldg(order + i + k)) * h + col;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (whole) {
-        load8<ALIGNED>(dy + at[k], t[k]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[k][e] = col + e >= 0 && col + e < h ? to_f32(dy[at[k] + e]) : 0.f;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] += t[k][e];
-  }
-  for (; i < b; ++i) {
-    const int64_t at = static_cast<int64_t>(__ldg(order + i)) * h + col;
-    float t[8];
-    if (whole) {
-      load8<ALIGNED>(dy + at, t);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = col + e >= 0 && col + e < h ? to_f32(dy[at + e]) : 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += t[e];
-  }
-}
-
-// Parts are rows of 8 cpr fp32: element c of the row at c + lead (see lead_of), so that every
-// chunk is aligned.  Tile t of the sorted tokens has two: 2 t of a row that starts before it,
-// 2 t + 1 of one that starts in it and goes on.
-template <typename T, typename TW, bool ALIGNED>
-__global__ void __launch_bounds__(256) embed_parts_kernel(int n, int h, int v, const int32_t* __restrict__ start,
-                                                          const int32_t* __restrict__ order,
-                                                          const int32_t* __restrict__ sorted_id,
-                                                          const T* __restrict__ dy, const TW* __restrict__ dw,
-                                                          float* __restrict__ part, int cpr, int* status) {
-  griddep_begin();
-  const int total = start[v];
-  const int groups = (cpr + 31) / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t units = static_cast<int64_t>((total + kTile - 1) / kTile) * groups;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units;
-       u += static_cast<int64_t>(gridDim.x) * 8) {
-    const int t = static_cast<int>(u / groups);
-    const int chunk = static_cast<int>(u % groups) * 32 + lane;
-    const int s0 = t * kTile, s1 = min(s0 + kTile, total);
-    const int va = sorted_id[s0], vb = sorted_id[s1 - 1];
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      const int id = which ? vb : va;
-      const int a = start[id], b = start[id + 1];
-      if (b - a <= kTile) continue;
-      if (which ? !(a >= s0) : !(a < s0)) continue;
-      if (chunk >= cpr) continue;
-      const int col = chunk * 8 - lead_of<TW, ALIGNED>(dw + static_cast<int64_t>(id) * h);
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-      if (col < h) add_rows<T, ALIGNED>(dy, h, order, max(a, s0), min(b, s1), col, x);
-      const int64_t at = (2 * static_cast<int64_t>(t) + which) * cpr * 8 + chunk * 8;
-      if (in_bounds(at, embed_part_floats(n, cpr * 8), status)) {
-        *reinterpret_cast<float4*>(part + at) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4*>(part + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
-      }
-    }
-  }
-}
 
 template <typename TW, bool ALIGNED, bool ADD>
 __device__ __forceinline__ void finish(TW* row, int h, int col, float scale, float (&x)[8]) {
@@ -376,72 +304,154 @@ __device__ __forceinline__ void finish(TW* row, int h, int col, float scale, flo
   }
 }
 
-// Blocks below `joins` add up the parts of one tile's row that starts there, if it has more than
-// kTile tokens, at 32 chunks: each warp a run of the parts, the runs joined in order.  The others
-// take the remaining rows, a warp 32 chunks of one at a time.
+constexpr int kZeroRows = 8;    // of a warp of the zeros' blocks
+constexpr int kTokenBatch = 8;  // rows of dy in flight
+static_assert(kTile == 32, "a lane holds one of a tile's tokens");
+
+// Parts are rows of 8 cpr fp32: element c of the row at c + lead (see lead_of), so that every
+// chunk is aligned.  Tile t has two: 2 t of a row that starts before it, 2 t + 1 of one that
+// starts in it and goes on.
+//   Blocks below `tile_blocks` take tiles, the others the rows without a token.
 template <typename T, typename TW, bool ALIGNED, bool ADD>
-__global__ void __launch_bounds__(256) embed_rows_kernel(int n, int h, int v, float scale, int64_t joins,
-                                                         const int32_t* __restrict__ start,
-                                                         const int32_t* __restrict__ order,
-                                                         const int32_t* __restrict__ sorted_id,
-                                                         const T* __restrict__ dy, const float* __restrict__ part,
-                                                         TW* __restrict__ dw, int cpr, int* status) {
+__global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, float scale, int64_t tile_blocks,
+                                                          const int32_t* __restrict__ start,
+                                                          const int32_t* __restrict__ order,
+                                                          const int32_t* __restrict__ sorted_id,
+                                                          const T* __restrict__ dy, float* __restrict__ part,
+                                                          TW* __restrict__ dw, int cpr, int* status) {
   griddep_begin();
-  const int groups = (cpr + 31) / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x < joins) {
-    __shared__ float run[8][32][9];
-    const int t = static_cast<int>(blockIdx.x / groups);
-    const int chunk = static_cast<int>(blockIdx.x % groups) * 32 + lane;
-    const int total = start[v];
-    if (t * kTile >= total) return;
-    const int s1 = min((t + 1) * kTile, total);
-    const int id = sorted_id[s1 - 1];
-    const int a = start[id], b = start[id + 1];
-    if (b - a <= kTile || a < t * kTile) return;
-    const int t1 = (b - 1) / kTile;  // part 0 is 2 t + 1, part i is 2 (t + i)
-    const int parts = t1 - t + 1, each = (parts + 7) / 8;
-    const int64_t pitch = static_cast<int64_t>(cpr) * 8;
-    float x[8];
+  if (blockIdx.x >= tile_blocks) {
+    const int64_t first = ((static_cast<int64_t>(blockIdx.x) - tile_blocks) * 8 + warp) * kZeroRows;
+    const int at = first + lane <= v ? start[first + lane] : 0;  // (lane 8: where the last one ends)
+    const int to = __shfl_down_sync(kFull, at, 1);
+    const uint32_t none = __ballot_sync(kFull, lane < kZeroRows && first + lane < v && at == to);
+    for (uint32_t left = none; left; left &= left - 1) {
+      TW* row = dw + (first + __ffs(left) - 1) * h;
+      for (int chunk = lane; chunk < cpr; chunk += 32) {
+        const int col = chunk * 8 - lead_of<TW, ALIGNED>(row);
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (col < h) finish<TW, ALIGNED, false>(row, h, col, 0.f, x);
+      }
+    }
+    return;
+  }
+  const int groups = (cpr + 31) / 32;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  const int64_t t = u / groups;
+  const int chunk = static_cast<int>(u % groups) * 32 + lane;
+  const int total = start[v];
+  if (t * kTile >= total) return;
+  const int s0 = static_cast<int>(t) * kTile, tokens = min(kTile, total - s0);
+  const int my_id = lane < tokens ? sorted_id[s0 + lane] : -1;
+  const int my_at = lane < tokens ? order[s0 + lane] : 0;
+  const int before = s0 > 0 ? sorted_id[s0 - 1] : -1, after = s0 + tokens < total ? sorted_id[s0 + tokens] : -1;
+  const bool live = chunk < cpr;
+  float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (chunk < cpr) {
-#pragma unroll 4
-      for (int i = warp * each; i < min(parts, (warp + 1) * each); ++i) {
-        float q[8];
-        load8<true>(part + (2 * static_cast<int64_t>(t + i) + (i == 0)) * pitch + chunk * 8, q);
+  for (int e = 0; e < 8; ++e) x[e] = 0.f;
+#pragma unroll 1
+  for (int b = 0; b < tokens; b += kTokenBatch) {
+    float y[kTokenBatch][8];
+    int id[kTokenBatch], col[kTokenBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += q[e];
+    for (int k = 0; k < kTokenBatch; ++k) {
+      id[k] = __shfl_sync(kFull, my_id, b + k);
+      const int64_t at = static_cast<int64_t>(__shfl_sync(kFull, my_at, b + k)) * h;
+      col[k] = chunk * 8 - lead_of<TW, ALIGNED>(dw + static_cast<int64_t>(id[k]) * h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[k][e] = 0.f;
+      if (b + k >= tokens || !live || !in_bounds(at, static_cast<int64_t>(n) * h, status)) continue;
+      if (ALIGNED || (col[k] >= 0 && col[k] + 8 <= h)) {
+        load8<ALIGNED>(dy + at + col[k], y[k]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col[k] + e >= 0 && col[k] + e < h) y[k][e] = to_f32(dy[at + col[k] + e]);
       }
     }
 #pragma unroll
+    for (int k = 0; k < kTokenBatch; ++k) {
+      const int i = b + k;
+      if (i >= tokens) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += y[k][e];
+      const int next = i + 1 < tokens ? __shfl_sync(kFull, my_id, i + 1) : after;
+      if (next == id[k] && i + 1 < tokens) continue;
+      // the row's last token in this tile; it began here unless the token before the tile is its own
+      const bool began = before != id[k];
+      if (began && next != id[k]) {
+        if (live && col[k] < h) finish<TW, ALIGNED, ADD>(dw + static_cast<int64_t>(id[k]) * h, h, col[k], scale, x);
+      } else if (live) {
+        const int64_t to = (2 * t + (began ? 1 : 0)) * cpr * 8 + chunk * 8;
+        if (in_bounds(to + 7, embed_part_floats(n, cpr * 8), status)) {
+          *reinterpret_cast<float4*>(part + to) = make_float4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<float4*>(part + to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    }
+  }
+}
+
+constexpr int kJoinAlone = 16;  // parts that a warp adds up by itself; more are cut into a run for each warp
+
+// Block (t, g): 8 times 32 chunks of the row that starts in tile t and goes on, if there is one.
+template <typename TW, bool ALIGNED, bool ADD>
+__global__ void __launch_bounds__(256) embed_join_kernel(int h, int v, float scale, const int32_t* __restrict__ start,
+                                                         const int32_t* __restrict__ sorted_id,
+                                                         const float* __restrict__ part, TW* __restrict__ dw, int cpr) {
+  griddep_begin();
+  __shared__ float run[8][32][9];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = (cpr + 31) / 32, wide = (groups + 7) / 8;
+  const int64_t t = blockIdx.x / wide;
+  const int g0 = static_cast<int>(blockIdx.x % wide) * 8;
+  const int total = start[v];
+  const int64_t s0 = t * kTile, s1 = s0 + kTile;
+  if (s1 >= total) return;
+  const int id = sorted_id[s1 - 1];
+  const int a = start[id], b = start[id + 1];
+  if (a < s0 || b <= s1) return;
+  const int parts = static_cast<int>((b - 1) / kTile - t) + 1;  // part 0 is 2 t + 1, part i is 2 (t + i)
+  const int64_t pitch = static_cast<int64_t>(cpr) * 8;
+  TW* row = dw + static_cast<int64_t>(id) * h;
+  const int lead = lead_of<TW, ALIGNED>(row);
+  auto sum = [&](int chunk, int from, int to, float (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (chunk >= cpr) return;
+#pragma unroll 4
+    for (int i = from; i < to; ++i) {
+      float q[8];
+      load8<true>(part + (2 * (t + i) + (i == 0)) * pitch + chunk * 8, q);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += q[e];
+    }
+  };
+  if (parts <= kJoinAlone) {
+    const int chunk = (g0 + warp) * 32 + lane, col = chunk * 8 - lead;
+    float x[8];
+    sum(chunk, 0, parts, x);
+    if (chunk < cpr && col < h) finish<TW, ALIGNED, ADD>(row, h, col, scale, x);
+    return;
+  }
+  const int each = (parts + 7) / 8;
+  for (int g = g0; g < min(g0 + 8, groups); ++g) {
+    const int chunk = g * 32 + lane, col = chunk * 8 - lead;
+    float x[8];
+    sum(chunk, warp * each, min(parts, (warp + 1) * each), x);
+    __syncthreads();  // (the runs of the group before have been read)
+#pragma unroll
     for (int e = 0; e < 8; ++e) run[warp][lane][e] = x[e];
     __syncthreads();
-    TW* row = dw + static_cast<int64_t>(id) * h;
-    const int col = chunk * 8 - lead_of<TW, ALIGNED>(row);
     if (warp == 0 && chunk < cpr && col < h) {
       for (int k = 1; k < 8; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += run[k][lane][e];
       finish<TW, ALIGNED, ADD>(row, h, col, scale, x);
     }
-    return;
-  }
-  const int64_t units = static_cast<int64_t>(v) * groups;
-  for (int64_t u = (static_cast<int64_t>(blockIdx.x) - joins) * 8 + warp; u < units;
-       u += (static_cast<int64_t>(gridDim.x) - joins) * 8) {
-    const int id = static_cast<int>(u / groups);
-    const int chunk = static_cast<int>(u % groups) * 32 + lane;
-    const int a = __ldg(start + id), b = __ldg(start + id + 1);
-    if (b - a > kTile || (ADD && a == b) || chunk >= cpr) continue;
-    TW* row = dw + static_cast<int64_t>(id) * h;
-    const int col = chunk * 8 - lead_of<TW, ALIGNED>(row);
-    if (col >= h || !in_bounds(b, static_cast<int64_t>(n) + 1, status)) continue;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    add_rows<T, ALIGNED>(dy, h, order, a, b, col, x);
-    finish<TW, ALIGNED, ADD>(row, h, col, scale, x);
   }
 }
 
@@ -459,28 +469,29 @@ cudaError_t forward_of(const EmbedParams& q, const int32_t* ids, const void* w, 
                   static_cast<const T*>(w), static_cast<T*>(y), cpr, status);
 }
 
-template <typename T, typename TW>
-cudaError_t backward_of(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, bool add, int sms,
-                        cudaStream_t s) {
-  const bool al = q.h % 8 == 0 && aligned16(dy) && aligned16(dw);
-  const int cpr = chunks_of(q.h, al), groups = (cpr + 31) / 32;
+template <typename T, typename TW, bool ALIGNED, bool ADD>
+cudaError_t backward_as(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, cudaStream_t s) {
+  const int cpr = chunks_of(q.h, ALIGNED), groups = (cpr + 31) / 32;
   const int n = static_cast<int>(q.n), v = static_cast<int>(q.v);
-  const int64_t tiles = (q.n + kTile - 1) / kTile;
-  const unsigned most = static_cast<unsigned>(sms) * 8;  // 8 blocks of 256 threads an SM
-  if (q.n > kTile) {
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(most, (tiles * groups + 7) / 8));
-    auto* k = al ? embed_parts_kernel<T, TW, true> : embed_parts_kernel<T, TW, false>;
-    cudaError_t e = launch_k(k, dim3(grid), dim3(256), 0, s, n, q.h, v, o.start, o.order, o.sorted_id,
-                             static_cast<const T*>(dy), static_cast<const TW*>(dw), o.part, cpr, o.status);
-    if (e != cudaSuccess) return e;
-  }
-  const int64_t joins = q.n > kTile ? tiles * groups : 0;
-  const int64_t grid = joins + std::min<int64_t>(most, (q.v * groups + 7) / 8);
-  if (grid > INT_MAX) return cudaErrorInvalidValue;
-  auto* k = al ? (add ? embed_rows_kernel<T, TW, true, true> : embed_rows_kernel<T, TW, true, false>)
-               : (add ? embed_rows_kernel<T, TW, false, true> : embed_rows_kernel<T, TW, false, false>);
-  return launch_k(k, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, n, q.h, v, q.scale, joins, o.start, o.order,
-                  o.sorted_id, static_cast<const T*>(dy), o.part, static_cast<TW*>(dw), cpr, o.status);
+  const int64_t tiles = (q.n + kTile - 1) / kTile, tile_blocks = (tiles * groups + 7) / 8;
+  const int64_t zero_blocks = ADD ? 0 : (q.v + 8 * kZeroRows - 1) / (8 * kZeroRows);
+  const int64_t join_blocks = (tiles - 1) * ((groups + 7) / 8);
+  if (tile_blocks + zero_blocks > INT_MAX || join_blocks > INT_MAX) return cudaErrorInvalidValue;
+  TW* out = static_cast<TW*>(dw);
+  cudaError_t e = launch_k(embed_tiles_kernel<T, TW, ALIGNED, ADD>, dim3(static_cast<unsigned>(tile_blocks + zero_blocks)),
+                           dim3(256), 0, s, n, q.h, v, q.scale, tile_blocks, o.start, o.order, o.sorted_id,
+                           static_cast<const T*>(dy), o.part, out, cpr, o.status);
+  if (e != cudaSuccess || join_blocks == 0) return e;
+  return launch_k(embed_join_kernel<TW, ALIGNED, ADD>, dim3(static_cast<unsigned>(join_blocks)), dim3(256), 0, s, q.h, v,
+                  q.scale, o.start, o.sorted_id, o.part, out, cpr);
+}
+
+template <typename T, typename TW>
+cudaError_t backward_of(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, bool add,
+                        cudaStream_t s) {
+  if (q.h % 8 == 0 && aligned16(dy) && aligned16(dw))
+    return add ? backward_as<T, TW, true, true>(q, dy, o, dw, s) : backward_as<T, TW, true, false>(q, dy, o, dw, s);
+  return add ? backward_as<T, TW, false, true>(q, dy, o, dw, s) : backward_as<T, TW, false, false>(q, dy, o, dw, s);
 }
 
 }  // namespace
@@ -509,12 +520,12 @@ cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids,
 }
 
 cudaError_t launch_embed_backward(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, bool add,
-                                  int sms, cudaStream_t s) {
+                                  cudaStream_t s) {
   if (q.y_f32)
-    return q.w_f32 ? backward_of<float, float>(q, dy, o, dw, add, sms, s)
-                   : backward_of<float, __nv_bfloat16>(q, dy, o, dw, add, sms, s);
-  return q.w_f32 ? backward_of<__nv_bfloat16, float>(q, dy, o, dw, add, sms, s)
-                 : backward_of<__nv_bfloat16, __nv_bfloat16>(q, dy, o, dw, add, sms, s);
+    return q.w_f32 ? backward_of<float, float>(q, dy, o, dw, add, s)
+                   : backward_of<float, __nv_bfloat16>(q, dy, o, dw, add, s);
+  return q.w_f32 ? backward_of<__nv_bfloat16, float>(q, dy, o, dw, add, s)
+                 : backward_of<__nv_bfloat16, __nv_bfloat16>(q, dy, o, dw, add, s);
 }
 
 }  // namespace flce

@@ -351,7 +351,7 @@ cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void
                                  float* part, cudaStream_t stream);
 
 // Embedding (flce_embed.cu).
-constexpr int kEmbedTile = 32;  // most tokens of an id that one thread sums; more are cut into parts
+constexpr int kEmbedTile = 32;  // tokens of the sorted order that are summed at once
 struct EmbedParams {
   int64_t n;
   int h;
@@ -360,7 +360,7 @@ struct EmbedParams {
   bool w_f32, y_f32;  // else bf16
 };
 // The tokens other than the padding id in the order of (id, position): their positions and
-// ids, start[v + 1] of each id's, and the parts of the rows that are summed in several.
+// ids, start[v + 1] of each id's, and the parts of the rows whose tokens lie in several tiles.
 struct EmbedSorted {
   int32_t* start;
   int32_t* order;
@@ -377,7 +377,7 @@ cudaError_t launch_embed_forward(const EmbedParams& q, const int32_t* ids, const
 cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, int sms,
                               cudaStream_t stream);
 cudaError_t launch_embed_backward(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, bool add,
-                                  int sms, cudaStream_t stream);
+                                  cudaStream_t stream);
 
 // AdamW (flce_adamw.cu).  The tensors travel as a kernel argument, so a step needs no
 // table in device memory; an argument holds at most 32764 bytes.
