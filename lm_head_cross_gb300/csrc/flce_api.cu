@@ -1743,8 +1743,7 @@ EmbedLayout embed_layout(const EmbedParams& q) {
   L.order = align_up(L.start + sizeof(int32_t) * (static_cast<size_t>(q.v) + 1));
   L.sorted_id = align_up(L.order + sizeof(int32_t) * n);
   L.part = align_up(L.sorted_id + sizeof(int32_t) * n);
-  // (a row's chunks where its start may lie anywhere between two 8-element boundaries)
-  L.total = align_up(L.part + sizeof(float) * static_cast<size_t>(embed_part_floats(q.n, (q.h + 14) / 8 * 8)));
+  L.total = align_up(L.part + sizeof(float) * static_cast<size_t>(embed_part_floats(q.n, (int64_t{q.h} + 255) / 256 * 256)));
   return L;
 }
 

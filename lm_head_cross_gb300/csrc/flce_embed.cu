@@ -28,142 +28,127 @@ constexpr uint32_t kFull = 0xffffffffu;
 
 // ----------------------------------------------------------------------------- 8 elements of a row
 
-// 8 consecutive elements at any element alignment: two-byte elements that start at an odd one are
-// taken from aligned words and shifted.
+// A warp holds 256 columns of a row, a lane 8 of them.  Where 16-byte accesses divide the rows
+// (ALIGNED) they are 8 consecutive ones; else every 32nd, by accesses of one element each that
+// are consecutive across the lanes: a warp's access then takes 2 or 4 sectors whatever the row's
+// alignment, a fifth of what shifting the words of unaligned 16-byte chunks into place takes.
+constexpr int kCols = 256;
+
 template <bool ALIGNED>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  uint32_t w[4];
-  if (ALIGNED) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(a & ~uintptr_t{3});
-    if (a & 2) {
-      uint32_t u[5];
+struct Place {
+  int c;  // the lane's first column
+  __device__ __forceinline__ Place(int group, int lane) : c(group * kCols + (ALIGNED ? lane * 8 : lane)) {}
+  __device__ __forceinline__ bool in(int e, int h) const { return ALIGNED ? c < h : c + 32 * e < h; }
+  __device__ __forceinline__ int col(int e) const { return c + (ALIGNED ? e : 32 * e); }
+};
+
+// As they lie in memory: loads are issued together and their words taken apart after the last.
+template <typename T, bool ALIGNED>
+struct Words {
+  static constexpr bool kPacked = ALIGNED && sizeof(T) == 2;
+  uint32_t u[kPacked ? 4 : 8];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-      for (int e = 0; e < 5; ++e) u[e] = __ldg(q + e);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = __funnelshift_r(u[e], u[e + 1], 16);
+    for (int e = 0; e < (kPacked ? 4 : 8); ++e) u[e] = 0;
+  }
+  // elements outside the row are left as they are
+  __device__ __forceinline__ void load(const T* row, const Place<ALIGNED>& at, int h) {
+    if (ALIGNED) {
+      if (at.c >= h) return;
+      const uint4* p = reinterpret_cast<const uint4*>(row + at.c);
+      const uint4 a = *p;
+      u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
+      if (!kPacked) {
+        const uint4 b = p[1];
+        u[kPacked ? 0 : 4] = b.x, u[kPacked ? 0 : 5] = b.y, u[kPacked ? 0 : 6] = b.z, u[kPacked ? 0 : 7] = b.w;
+      }
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = __ldg(q + e);
+      for (int e = 0; e < 8; ++e) {
+        if (!at.in(e, h)) continue;
+        if (sizeof(T) == 2) u[kPacked ? 0 : e] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(row + at.col(e))) << 16;
+        else u[kPacked ? 0 : e] = *reinterpret_cast<const uint32_t*>(row + at.col(e));
+      }
     }
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  __device__ __forceinline__ float value(int e) const {
+    if (kPacked) return __uint_as_float((e & 1) ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+    return __uint_as_float(u[kPacked ? 0 : e]);
   }
-}
+};
 
 template <bool ALIGNED>
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* row, const Place<ALIGNED>& at, int h, const float (&x)[8]) {
   if (ALIGNED) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    if (at.c < h)
+      __stcs(reinterpret_cast<uint4*>(row + at.c), make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __ldg(p + e);
+    for (int e = 0; e < 8; ++e)
+      if (at.in(e, h)) row[at.col(e)] = __float2bfloat16_rn(x[e]);
   }
 }
-
-// 8 elements whose first is at a multiple of 8 elements (from a 16-byte boundary on).
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+template <bool ALIGNED>
+__device__ __forceinline__ void store8(float* row, const Place<ALIGNED>& at, int h, const float (&x)[8]) {
+  if (ALIGNED) {
+    if (at.c < h) {
+      __stcs(reinterpret_cast<float4*>(row + at.c), make_float4(x[0], x[1], x[2], x[3]));
+      __stcs(reinterpret_cast<float4*>(row + at.c) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (at.in(e, h)) row[at.col(e)] = x[e];
+  }
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
-}
-
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-
-// A row that is written is cut at the 8-element boundaries of its memory, so that only its first
-// and last chunk can be short: `lead` elements of the first chunk belong to the row before.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ int lead_of(const T* row) {
-  return ALIGNED ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) & 7);
-}
-
-}  // namespace
-
-// Chunks that cover any row of h elements.
-static int chunks_of(int h, bool aligned) { return aligned ? h / 8 : (h + 7 + 7) / 8; }
-
-namespace {
 
 // ----------------------------------------------------------------------------- forward
 
 constexpr int kFwdThreads = 256;
-constexpr int kFwdChunks = 4;  // of a thread: as many loads in flight
+constexpr int kFwdUnits = 4;  // of a warp, as many rows' columns in flight
 
-// Blocks 0 .. gridDim - 2 take kFwdThreads * kFwdChunks consecutive chunks of y; the last one
+// Blocks 0 .. gridDim - 2: a warp takes kFwdUnits consecutive (row, 256 columns); the last block
 // looks all ids over and writes the status word, so that nothing has to clear it first.
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, int h, int64_t v, float scale,
                                                                     const int32_t* __restrict__ ids,
                                                                     const T* __restrict__ w, T* __restrict__ y,
-                                                                    int cpr, int* status) {
+                                                                    int groups, int* status) {
   griddep_begin();
-  const int tid = threadIdx.x;
   if (blockIdx.x == gridDim.x - 1) {
     int bad = 0;
-    for (int64_t i = tid; i < n; i += kFwdThreads) bad |= static_cast<uint32_t>(ids[i]) >= static_cast<uint64_t>(v);
+    for (int64_t i = threadIdx.x; i < n; i += kFwdThreads) bad |= static_cast<uint32_t>(ids[i]) >= static_cast<uint64_t>(v);
     bad = __syncthreads_or(bad);
-    if (tid == 0) *status = bad ? kErrLabel : kOk;
+    if (threadIdx.x == 0) *status = bad ? kErrLabel : kOk;
     return;
   }
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kFwdThreads * kFwdChunks);
-  const int64_t row0 = first / cpr;
-  const uint32_t off0 = static_cast<uint32_t>(first - row0 * cpr);
-  float x[kFwdChunks][8];
-  int64_t row[kFwdChunks];
-  int col[kFwdChunks];
-  int64_t id[kFwdChunks];
+  const int lane = threadIdx.x & 31;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kFwdThreads / 32) + (threadIdx.x >> 5)) * kFwdUnits;
+  int64_t row = first / groups;
+  int group = static_cast<int>(first - row * groups);
+  int64_t rows[kFwdUnits], id[kFwdUnits];
+  int cols[kFwdUnits];
 #pragma unroll
-  for (int k = 0; k < kFwdChunks; ++k) {
-    const uint32_t at = off0 + static_cast<uint32_t>(tid + k * kFwdThreads);
-    row[k] = row0 + at / static_cast<uint32_t>(cpr);
-    col[k] = static_cast<int>(at % static_cast<uint32_t>(cpr)) * 8;
-    if (row[k] >= n) {
-      col[k] = INT_MAX;
-      continue;
-    }
-    id[k] = ids[row[k]];
-    col[k] -= lead_of<T, ALIGNED>(y + row[k] * h);
+  for (int k = 0; k < kFwdUnits; ++k) {
+    rows[k] = row;
+    cols[k] = group;
+    id[k] = row < n ? ids[row] : -1;
+    if (++group == groups) group = 0, ++row;
+  }
+  Words<T, ALIGNED> x[kFwdUnits];
+#pragma unroll
+  for (int k = 0; k < kFwdUnits; ++k) {
+    x[k].zero();
+    if (id[k] >= 0 && id[k] < v) x[k].load(w + id[k] * h, Place<ALIGNED>(cols[k], lane), h);
   }
 #pragma unroll
-  for (int k = 0; k < kFwdChunks; ++k) {
+  for (int k = 0; k < kFwdUnits; ++k) {
+    if (rows[k] >= n) return;
+    float z[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-    if (col[k] >= h || id[k] < 0 || id[k] >= v) continue;
-    const T* src = w + id[k] * h;
-    if (ALIGNED || (col[k] >= 0 && col[k] + 8 <= h)) {
-      load8<ALIGNED>(src + col[k], x[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (col[k] + e >= 0 && col[k] + e < h) x[k][e] = to_f32(src[col[k] + e]);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kFwdChunks; ++k) {
-    if (col[k] >= h) continue;
-    T* dst = y + row[k] * h;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[k][e] *= scale;
-    if (ALIGNED || (col[k] >= 0 && col[k] + 8 <= h)) {
-      store8(dst + col[k], x[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (col[k] + e >= 0 && col[k] + e < h) put(dst + col[k] + e, x[k][e]);
-    }
+    for (int e = 0; e < 8; ++e) z[e] = x[k].value(e) * scale;
+    store8<ALIGNED>(y + rows[k] * h, Place<ALIGNED>(cols[k], lane), h, z);
   }
 }
 
@@ -283,42 +268,51 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, 
 
 // ----------------------------------------------------------------------------- sums
 
+// dW's row: x scale, added to what it held where ADD.
 template <typename TW, bool ALIGNED, bool ADD>
-__device__ __forceinline__ void finish(TW* row, int h, int col, float scale, float (&x)[8]) {
-  const bool whole = ALIGNED || (col >= 0 && col + 8 <= h);
-  if (whole) {
-    float old[8];
-    if (ADD) {
-      load8<true>(row + col, old);  // (chunks are cut at dW's own boundaries)
+__device__ __forceinline__ void finish(TW* row, const Place<ALIGNED>& at, int h, float scale,
+                                       const Words<TW, ALIGNED>& old, float (&x)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], scale, old[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= scale;
-    }
-    store8(row + col, x);
+  for (int e = 0; e < 8; ++e) x[e] = ADD ? fmaf(x[e], scale, old.value(e)) : x[e] * scale;
+  store8<ALIGNED>(row, at, h, x);
+}
+
+// A part is a row of `groups` times 256 fp32, in the order of the lanes' elements.
+template <bool ALIGNED>
+__device__ __forceinline__ void part_store(float* p, int lane, const float (&x)[8]) {
+  if (ALIGNED) {
+    reinterpret_cast<float4*>(p)[2 * lane] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[2 * lane + 1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (col + e >= 0 && col + e < h) put(row + col + e, ADD ? fmaf(x[e], scale, to_f32(row[col + e])) : x[e] * scale);
+    for (int e = 0; e < 8; ++e) p[32 * e + lane] = x[e];
+  }
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void part_load(const float* p, int lane, float (&x)[8]) {
+  if (ALIGNED) {
+    const float4 a = reinterpret_cast<const float4*>(p)[2 * lane], b = reinterpret_cast<const float4*>(p)[2 * lane + 1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = p[32 * e + lane];
   }
 }
 
-constexpr int kZeroRows = 8;    // of a warp of the zeros' blocks
-constexpr int kTokenBatch = 8;  // rows of dy in flight
-static_assert(kTile == 32, "a lane holds one of a tile's tokens");
+constexpr int kZeroRows = 8;  // of a warp of the zeros' blocks
 
-// Parts are rows of 8 cpr fp32: element c of the row at c + lead (see lead_of), so that every
-// chunk is aligned.  Tile t has two: 2 t of a row that starts before it, 2 t + 1 of one that
-// starts in it and goes on.
-//   Blocks below `tile_blocks` take tiles, the others the rows without a token.
+// Tile t has two parts: 2 t of a row that starts before it, 2 t + 1 of one that starts in it and
+// goes on.
+//   Blocks below `tile_blocks` take tiles, the others the rows without a token.  A batch of
+// tokens' rows is in flight at once, with the rows of dW that they complete.
 template <typename T, typename TW, bool ALIGNED, bool ADD>
 __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, float scale, int64_t tile_blocks,
                                                           const int32_t* __restrict__ start,
                                                           const int32_t* __restrict__ order,
                                                           const int32_t* __restrict__ sorted_id,
                                                           const T* __restrict__ dy, float* __restrict__ part,
-                                                          TW* __restrict__ dw, int cpr, int* status) {
+                                                          TW* __restrict__ dw, int groups, int* status) {
+  constexpr int kBatch = Words<T, ALIGNED>::kPacked && !ADD ? 8 : 4;
   griddep_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x >= tile_blocks) {
@@ -326,68 +320,74 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, f
     const int at = first + lane <= v ? start[first + lane] : 0;  // (lane 8: where the last one ends)
     const int to = __shfl_down_sync(kFull, at, 1);
     const uint32_t none = __ballot_sync(kFull, lane < kZeroRows && first + lane < v && at == to);
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (uint32_t left = none; left; left &= left - 1) {
       TW* row = dw + (first + __ffs(left) - 1) * h;
-      for (int chunk = lane; chunk < cpr; chunk += 32) {
-        const int col = chunk * 8 - lead_of<TW, ALIGNED>(row);
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (col < h) finish<TW, ALIGNED, false>(row, h, col, 0.f, x);
-      }
+      for (int g = 0; g < groups; ++g) store8<ALIGNED>(row, Place<ALIGNED>(g, lane), h, zero);
     }
     return;
   }
-  const int groups = (cpr + 31) / 32;
   const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + warp;
   const int64_t t = u / groups;
-  const int chunk = static_cast<int>(u % groups) * 32 + lane;
+  const int group = static_cast<int>(u % groups);
+  const Place<ALIGNED> place(group, lane);
   const int total = start[v];
   if (t * kTile >= total) return;
   const int s0 = static_cast<int>(t) * kTile, tokens = min(kTile, total - s0);
-  const int my_id = lane < tokens ? sorted_id[s0 + lane] : -1;
-  const int my_at = lane < tokens ? order[s0 + lane] : 0;
+  int my_id[kTile / 32], my_at[kTile / 32];
+#pragma unroll
+  for (int k = 0; k < kTile / 32; ++k) {
+    const int i = 32 * k + lane;
+    my_id[k] = i < tokens ? sorted_id[s0 + i] : -1;
+    my_at[k] = i < tokens ? order[s0 + i] : 0;
+  }
   const int before = s0 > 0 ? sorted_id[s0 - 1] : -1, after = s0 + tokens < total ? sorted_id[s0 + tokens] : -1;
-  const bool live = chunk < cpr;
   float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = 0.f;
 #pragma unroll 1
-  for (int b = 0; b < tokens; b += kTokenBatch) {
-    float y[kTokenBatch][8];
-    int id[kTokenBatch], col[kTokenBatch];
+  for (int b = 0; b < tokens; b += kBatch) {
+    Words<T, ALIGNED> y[kBatch];
+    Words<TW, ALIGNED> old[ADD ? kBatch : 1];
+    int id[kBatch + 1];
+    const int half = b / 32;
 #pragma unroll
-    for (int k = 0; k < kTokenBatch; ++k) {
-      id[k] = __shfl_sync(kFull, my_id, b + k);
-      const int64_t at = static_cast<int64_t>(__shfl_sync(kFull, my_at, b + k)) * h;
-      col[k] = chunk * 8 - lead_of<TW, ALIGNED>(dw + static_cast<int64_t>(id[k]) * h);
+    for (int k = 0; k <= kBatch; ++k) {  // ids of the batch and of the token behind it
+      int held = my_id[0];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[k][e] = 0.f;
-      if (b + k >= tokens || !live || !in_bounds(at, static_cast<int64_t>(n) * h, status)) continue;
-      if (ALIGNED || (col[k] >= 0 && col[k] + 8 <= h)) {
-        load8<ALIGNED>(dy + at + col[k], y[k]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (col[k] + e >= 0 && col[k] + e < h) y[k][e] = to_f32(dy[at + col[k] + e]);
-      }
+      for (int j = 1; j < kTile / 32; ++j)
+        if ((b + k) / 32 == j) held = my_id[j];
+      id[k] = __shfl_sync(kFull, held, (b + k) & 31);
+      if (b + k >= tokens) id[k] = after;
     }
 #pragma unroll
-    for (int k = 0; k < kTokenBatch; ++k) {
-      const int i = b + k;
-      if (i >= tokens) break;
+    for (int k = 0; k < kBatch; ++k) {
+      int held = my_at[0];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] += y[k][e];
-      const int next = i + 1 < tokens ? __shfl_sync(kFull, my_id, i + 1) : after;
-      if (next == id[k] && i + 1 < tokens) continue;
+      for (int j = 1; j < kTile / 32; ++j)
+        if (half == j) held = my_at[j];
+      const int64_t at = static_cast<int64_t>(__shfl_sync(kFull, held, (b + k) & 31)) * h;
+      y[k].zero();
+      if (ADD) old[ADD ? k : 0].zero();
+      if (b + k >= tokens || !in_bounds(at, static_cast<int64_t>(n) * h, status)) continue;
+      y[k].load(dy + at, place, h);
+      if (ADD && id[k + 1] != id[k] && id[k] != before) old[ADD ? k : 0].load(dw + static_cast<int64_t>(id[k]) * h, place, h);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (b + k >= tokens) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += y[k].value(e);
+      const bool ends = id[k + 1] != id[k];
+      if (!ends && b + k + 1 < tokens) continue;
       // the row's last token in this tile; it began here unless the token before the tile is its own
       const bool began = before != id[k];
-      if (began && next != id[k]) {
-        if (live && col[k] < h) finish<TW, ALIGNED, ADD>(dw + static_cast<int64_t>(id[k]) * h, h, col[k], scale, x);
-      } else if (live) {
-        const int64_t to = (2 * t + (began ? 1 : 0)) * cpr * 8 + chunk * 8;
-        if (in_bounds(to + 7, embed_part_floats(n, cpr * 8), status)) {
-          *reinterpret_cast<float4*>(part + to) = make_float4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<float4*>(part + to + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        }
+      if (began && ends) {
+        finish<TW, ALIGNED, ADD>(dw + static_cast<int64_t>(id[k]) * h, place, h, scale, old[ADD ? k : 0], x);
+      } else {
+        const int64_t to = ((2 * t + (began ? 1 : 0)) * groups + group) * kCols;
+        if (in_bounds(to + kCols - 1, embed_part_floats(n, static_cast<int64_t>(groups) * kCols), status))
+          part_store<ALIGNED>(part + to, lane, x);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = 0.f;
@@ -397,15 +397,15 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, f
 
 constexpr int kJoinAlone = 16;  // parts that a warp adds up by itself; more are cut into a run for each warp
 
-// Block (t, g): 8 times 32 chunks of the row that starts in tile t and goes on, if there is one.
+// Block (t, g): 8 times 256 columns of the row that starts in tile t and goes on, if there is one.
 template <typename TW, bool ALIGNED, bool ADD>
 __global__ void __launch_bounds__(256) embed_join_kernel(int h, int v, float scale, const int32_t* __restrict__ start,
                                                          const int32_t* __restrict__ sorted_id,
-                                                         const float* __restrict__ part, TW* __restrict__ dw, int cpr) {
+                                                         const float* __restrict__ part, TW* __restrict__ dw, int groups) {
   griddep_begin();
   __shared__ float run[8][32][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (cpr + 31) / 32, wide = (groups + 7) / 8;
+  const int wide = (groups + 7) / 8;
   const int64_t t = blockIdx.x / wide;
   const int g0 = static_cast<int>(blockIdx.x % wide) * 8;
   const int total = start[v];
@@ -415,63 +415,69 @@ __global__ void __launch_bounds__(256) embed_join_kernel(int h, int v, float sca
   const int a = start[id], b = start[id + 1];
   if (a < s0 || b <= s1) return;
   const int parts = static_cast<int>((b - 1) / kTile - t) + 1;  // part 0 is 2 t + 1, part i is 2 (t + i)
-  const int64_t pitch = static_cast<int64_t>(cpr) * 8;
   TW* row = dw + static_cast<int64_t>(id) * h;
-  const int lead = lead_of<TW, ALIGNED>(row);
-  auto sum = [&](int chunk, int from, int to, float (&x)[8]) {
+  auto sum = [&](int g, int from, int to, float (&x)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (chunk >= cpr) return;
 #pragma unroll 4
     for (int i = from; i < to; ++i) {
       float q[8];
-      load8<true>(part + (2 * (t + i) + (i == 0)) * pitch + chunk * 8, q);
+      part_load<ALIGNED>(part + ((2 * (t + i) + (i == 0)) * groups + g) * kCols, lane, q);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] += q[e];
     }
   };
+  Words<TW, ALIGNED> old;
   if (parts <= kJoinAlone) {
-    const int chunk = (g0 + warp) * 32 + lane, col = chunk * 8 - lead;
+    const int g = g0 + warp;
+    if (g >= groups) return;
+    const Place<ALIGNED> place(g, lane);
     float x[8];
-    sum(chunk, 0, parts, x);
-    if (chunk < cpr && col < h) finish<TW, ALIGNED, ADD>(row, h, col, scale, x);
+    old.zero();
+    if (ADD) old.load(row, place, h);
+    sum(g, 0, parts, x);
+    finish<TW, ALIGNED, ADD>(row, place, h, scale, old, x);
     return;
   }
   const int each = (parts + 7) / 8;
   for (int g = g0; g < min(g0 + 8, groups); ++g) {
-    const int chunk = g * 32 + lane, col = chunk * 8 - lead;
     float x[8];
-    sum(chunk, warp * each, min(parts, (warp + 1) * each), x);
+    sum(g, warp * each, min(parts, (warp + 1) * each), x);
     __syncthreads();  // (the runs of the group before have been read)
 #pragma unroll
     for (int e = 0; e < 8; ++e) run[warp][lane][e] = x[e];
     __syncthreads();
-    if (warp == 0 && chunk < cpr && col < h) {
+    if (warp == 0) {
+      const Place<ALIGNED> place(g, lane);
+      old.zero();
+      if (ADD) old.load(row, place, h);
       for (int k = 1; k < 8; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += run[k][lane][e];
-      finish<TW, ALIGNED, ADD>(row, h, col, scale, x);
+      finish<TW, ALIGNED, ADD>(row, place, h, scale, old, x);
     }
   }
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+int groups_of(int h) { return (h + kCols - 1) / kCols; }
+
 template <typename T>
 cudaError_t forward_of(const EmbedParams& q, const int32_t* ids, const void* w, void* y, int* status, cudaStream_t s) {
   const bool al = q.h % 8 == 0 && aligned16(w) && aligned16(y);
-  const int cpr = chunks_of(q.h, al);
-  const int64_t per_block = kFwdThreads * kFwdChunks;
-  const int64_t blocks = (q.n * cpr + per_block - 1) / per_block + 1;
+  const int groups = groups_of(q.h);
+  constexpr int kPerBlock = kFwdThreads / 32 * kFwdUnits;
+  const int64_t blocks = (q.n * groups + kPerBlock - 1) / kPerBlock + 1;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
   auto* k = al ? embed_forward_kernel<T, true> : embed_forward_kernel<T, false>;
   return launch_k(k, dim3(static_cast<unsigned>(blocks)), dim3(kFwdThreads), 0, s, q.n, q.h, q.v, q.scale, ids,
-                  static_cast<const T*>(w), static_cast<T*>(y), cpr, status);
+                  static_cast<const T*>(w), static_cast<T*>(y), groups, status);
 }
 
 template <typename T, typename TW, bool ALIGNED, bool ADD>
 cudaError_t backward_as(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, cudaStream_t s) {
-  const int cpr = chunks_of(q.h, ALIGNED), groups = (cpr + 31) / 32;
+  const int groups = groups_of(q.h);
   const int n = static_cast<int>(q.n), v = static_cast<int>(q.v);
   const int64_t tiles = (q.n + kTile - 1) / kTile, tile_blocks = (tiles * groups + 7) / 8;
   const int64_t zero_blocks = ADD ? 0 : (q.v + 8 * kZeroRows - 1) / (8 * kZeroRows);
@@ -480,10 +486,10 @@ cudaError_t backward_as(const EmbedParams& q, const void* dy, const EmbedSorted&
   TW* out = static_cast<TW*>(dw);
   cudaError_t e = launch_k(embed_tiles_kernel<T, TW, ALIGNED, ADD>, dim3(static_cast<unsigned>(tile_blocks + zero_blocks)),
                            dim3(256), 0, s, n, q.h, v, q.scale, tile_blocks, o.start, o.order, o.sorted_id,
-                           static_cast<const T*>(dy), o.part, out, cpr, o.status);
+                           static_cast<const T*>(dy), o.part, out, groups, o.status);
   if (e != cudaSuccess || join_blocks == 0) return e;
   return launch_k(embed_join_kernel<TW, ALIGNED, ADD>, dim3(static_cast<unsigned>(join_blocks)), dim3(256), 0, s, q.h, v,
-                  q.scale, o.start, o.sorted_id, o.part, out, cpr);
+                  q.scale, o.start, o.sorted_id, o.part, out, groups);
 }
 
 template <typename T, typename TW>

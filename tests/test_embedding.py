@@ -93,7 +93,7 @@ def test_workspace_size_rules():
     assert ws(-1, 8, 8) == ws(1, 0, 8) == ws(1, 8, 0) == 0
     assert ws(32, 4096, 100) < ws(33, 4096, 100)  # up to 32 tokens need no parts
     n, h, v = 131072, 4096, 131072
-    assert 4 * (v + 2 * n) + 2 * (n // 32) * 4 * h <= ws(n, h, v) <= 4 * (v + 2 * n) + 2 * (n // 32) * 4 * (h + 14) + 2048
+    assert 4 * (v + 2 * n) + 2 * (n // 32) * 4 * h <= ws(n, h, v) <= 4 * (v + 2 * n) + 2 * (n // 32) * 4 * h + 2048
 
 
 def test_python_refuses_on_cpu():
