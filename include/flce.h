@@ -437,7 +437,7 @@ flce_status_t flce_layernorm_backward(const flce_norm_t* q, const void* dy, cons
  *     So the gradient that the head's backward pass left for a shared matrix is
  *     completed in place.
  *   - padding_idx: tokens with this id pass no gradient; -1 for none.
- *   - Any n >= 0, h >= 1, v >= 1 (n, v up to 2^30, h up to 2^20).  ids is int32
+ *   - Any n >= 0, h >= 1, v >= 1 (n up to 2^30, h and v up to 2^20).  ids is int32
  *     [n].  Pointers need the alignment of their type.  An id outside [0, v)
  *     (the padding id aside) records FLCE_ERR_LABEL_OUT_OF_RANGE in the
  *     workspace's status word; its token reads and adds nothing.
@@ -454,7 +454,8 @@ typedef struct {
 
 /* The forward pass needs 256 bytes of workspace (the status word), the backward
  * pass flce_embedding_workspace_bytes(q) (0 if q is invalid): the sorted tokens
- * (4 (v + 2 n) bytes) and, from 33 tokens on, two fp32 rows for each 32. */
+ * (4 (v + 4 n) bytes), a table of 0.6 MB and two fp32 rows for each 32 of the
+ * tokens (64, from 32768 tokens on). */
 flce_status_t flce_embedding_forward(const flce_embedding_t* q, const int32_t* ids, const void* W, void* y, void* ws,
                                      size_t ws_bytes, flce_stream_t stream);
 size_t flce_embedding_workspace_bytes(const flce_embedding_t* q);

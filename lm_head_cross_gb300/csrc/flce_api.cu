@@ -1727,14 +1727,13 @@ flce_status_t check_embedding(const flce_embedding_t* q, EmbedParams* out) {
   if (!known_dtype(q->w_dtype) || !known_dtype(q->y_dtype)) return FLCE_ERR_INVALID_ARGUMENT;
   if (q->padding_idx < -1 || q->padding_idx >= q->v) return FLCE_ERR_INVALID_ARGUMENT;
   // positions, ids and columns are 32-bit; element offsets are 64-bit
-  if (q->n > (int64_t{1} << 30) || q->v > (int64_t{1} << 30) || q->h > (int64_t{1} << 20))
-    return FLCE_ERR_UNSUPPORTED_SHAPE;
+  if (q->n > (int64_t{1} << 30) || q->v > kEmbedIdsMost || q->h > (int64_t{1} << 20)) return FLCE_ERR_UNSUPPORTED_SHAPE;
   *out = EmbedParams{q->n, static_cast<int>(q->h), q->v, q->scale, q->w_dtype == FLCE_F32, q->y_dtype == FLCE_F32};
   return FLCE_OK;
 }
 
 struct EmbedLayout {
-  size_t start, order, sorted_id, part, total;
+  size_t start, order, sorted_id, tokens, off, bad, part, total;
 };
 EmbedLayout embed_layout(const EmbedParams& q) {
   EmbedLayout L{};
@@ -1742,7 +1741,10 @@ EmbedLayout embed_layout(const EmbedParams& q) {
   L.start = kAlign;  // after the status word
   L.order = align_up(L.start + sizeof(int32_t) * (static_cast<size_t>(q.v) + 1));
   L.sorted_id = align_up(L.order + sizeof(int32_t) * n);
-  L.part = align_up(L.sorted_id + sizeof(int32_t) * n);
+  L.tokens = align_up(L.sorted_id + sizeof(int32_t) * n);
+  L.off = align_up(L.tokens + 2 * sizeof(int32_t) * n);
+  L.bad = align_up(L.off + sizeof(int32_t) * (kEmbedRanges + 1) * kEmbedStretches);
+  L.part = align_up(L.bad + sizeof(int32_t) * kEmbedStretches);
   L.total = align_up(L.part + sizeof(float) * static_cast<size_t>(embed_part_floats(q.n, (int64_t{q.h} + 255) / 256 * 256)));
   return L;
 }
@@ -1796,9 +1798,10 @@ flce_status_t flce_embedding_backward(const flce_embedding_t* q, const void* dy,
   if (st != FLCE_OK) return st;
   uint8_t* base = static_cast<uint8_t*>(ws);
   const EmbedSorted o{reinterpret_cast<int32_t*>(base + L.start), reinterpret_cast<int32_t*>(base + L.order),
-                      reinterpret_cast<int32_t*>(base + L.sorted_id), reinterpret_cast<float*>(base + L.part),
-                      reinterpret_cast<int*>(base)};
-  st = cuda_status(timed(3, 0.0, s, [&] { return launch_embed_sort(ep, q->padding_idx, ids, o, dev.sms, s); }));
+                      reinterpret_cast<int32_t*>(base + L.sorted_id), base + L.tokens,
+                      reinterpret_cast<int32_t*>(base + L.off), reinterpret_cast<int32_t*>(base + L.bad),
+                      reinterpret_cast<float*>(base + L.part), reinterpret_cast<int*>(base)};
+  st = cuda_status(timed(3, 0.0, s, [&] { return launch_embed_sort(ep, q->padding_idx, ids, o, s); }));
   if (st != FLCE_OK) return st;
   return cuda_status(
       timed(3, 0.0, s, [&] { return launch_embed_backward(ep, dy, o, dW, add != 0, s); }));

@@ -7,14 +7,15 @@
 // gradient reads N H elements and writes V H (or reads and writes the distinct rows).
 //
 // The gradient's sums have one order, whatever the schedule: the tokens are sorted by (id,
-// position) and cut into tiles of kTile; a row of dW is the sum over its tokens in that order in
-// fp32, one part for each tile that it has tokens in, the parts added in order, and rounded once.
-//   sort   every block owns a range of the vocabulary and reads all ids twice (they stay in L2):
-//          once to count, a count for each (warp's stretch of positions, id), and once to place
-//          its tokens.  No block waits for another, no atomics in global memory, one launch.
-//   tiles  every tile's tokens, 32 chunks of columns a warp: rows that lie within the tile are
-//          finished, the others leave a part; beside them, zeros for the rows without a token
-//   join   the rows with several parts
+// position) and cut into tiles; a row of dW is the sum over its tokens in that order in fp32, one
+// part for each tile that it has tokens in, the parts added in order, and rounded once.
+//   bucket  every block sorts its stretch of positions by range of the vocabulary
+//   sort    every block gathers one range's tokens, which the stretches hold in order, and sorts
+//           them by id.  No block waits for another, no atomics in global memory.  (Blocks that
+//           each read all ids and kept their range's took 9 us for 8192 tokens and 55 for 131072.)
+//   tiles   every tile's tokens, 256 columns a warp: rows that lie within the tile are finished,
+//           the others leave a part; beside them, zeros for the rows without a token
+//   join    the rows with several parts
 #include "flce_device.cuh"
 #include "flce_internal.h"
 #include "flce_launch.cuh"
@@ -23,7 +24,6 @@ namespace flce {
 
 namespace {
 
-constexpr int kTile = kEmbedTile;
 constexpr uint32_t kFull = 0xffffffffu;
 
 // ----------------------------------------------------------------------------- 8 elements of a row
@@ -154,115 +154,198 @@ __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, i
 
 // ----------------------------------------------------------------------------- sort
 
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortBatch = 16;  // loads of ids in flight
-constexpr int32_t kNoToken = INT32_MIN;  // behind a stretch's end: outside every range
+constexpr int kSortRound = 4096;  // tokens of a block's shared memory; a range with more takes several rounds
+constexpr int kPerMost = kEmbedIdsMost / kEmbedRanges;  // ids of a range
 
-// Block b owns ids [b per, (b + 1) per).  Warp w counts and places the positions of its stretch
-// [w seg, (w + 1) seg), so that (id, warp, position) is the sorted order.
-__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, int per, int seg, int pad,
-                                                                  const int32_t* __restrict__ ids,
+// Inclusive sum over the block's threads; *all gets the total.  `part` holds a word for each warp.
+__device__ __forceinline__ int block_scan(int x, int* part, int* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(kFull, x, d);
+    if (lane >= d) x += up;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  const int w = lane < kSortWarps ? part[lane] : 0;
+  const int before = __reduce_add_sync(kFull, lane < warp ? w : 0);
+  *all = __reduce_add_sync(kFull, w);
+  return x + before;
+}
+
+// The lane's place among the warp's lanes with its key, behind row[key] earlier ones; row[key]
+// moves on.  Lanes of `some` alone call it.
+__device__ __forceinline__ int take_rank(uint32_t some, int key, int32_t* row, int lane) {
+  const uint32_t same = __match_any_sync(some, key);
+  const int rank = row[key] + __popc(same & ((1u << lane) - 1));
+  __syncwarp(some);
+  if ((same >> lane) == 1u) row[key] = rank + 1;  // the highest of them
+  __syncwarp(some);
+  return rank;
+}
+
+// Block s: positions [s len, (s + 1) len), sorted by range (stable) into tokens[s len ..] as (id,
+// position); off[r stretches + s] is where range r starts in it, the last entry how many tokens
+// it holds.  Padding and ids outside the vocabulary are left out.
+__global__ void __launch_bounds__(kSortThreads) embed_bucket_kernel(int n, int v, int per, int ranges, int len, int pad,
+                                                                    const int32_t* __restrict__ ids,
+                                                                    int2* __restrict__ tokens,
+                                                                    int32_t* __restrict__ off, int32_t* __restrict__ bad) {
+  __shared__ int32_t count[kSortWarps][kEmbedRanges];
+  __shared__ int part[kSortWarps];
+  griddep_begin();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int stretches = static_cast<int>(gridDim.x);
+  for (int i = tid; i < kSortWarps * kEmbedRanges; i += kSortThreads) (&count[0][0])[i] = 0;
+  __syncthreads();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * len;
+  const int mine = static_cast<int>(min(static_cast<int64_t>(len), n - first));
+  const int each = (mine + kSortThreads - 1) / kSortThreads * 32;  // of a warp
+  const int w0 = warp * each, w1 = min(w0 + each, mine);
+  int32_t* row = count[warp];
+  int outside = 0;
+  for (int i0 = w0; i0 < w1; i0 += 32) {  // count
+    const int id = i0 + lane < w1 ? ids[first + i0 + lane] : -1;
+    const bool in = static_cast<uint32_t>(id) < static_cast<uint32_t>(v);
+    outside |= i0 + lane < w1 && !in;
+    if (in && id != pad) atomicAdd(row + id / per, 1);
+  }
+  outside = __syncthreads_or(outside);
+  if (tid == 0) bad[blockIdx.x] = outside;
+  // exclusive sums over (range, warp)
+  int base = 0;
+  for (int r0 = 0; r0 < kEmbedRanges; r0 += kSortThreads) {
+    const int r = r0 + tid;
+    int total = 0, all;
+    if (r < kEmbedRanges)
+      for (int k = 0; k < kSortWarps; ++k) total += count[k][r];
+    int at = base + block_scan(total, part, &all) - total;
+    base += all;
+    if (r < ranges) off[static_cast<int64_t>(r) * stretches + blockIdx.x] = at;
+    if (r < kEmbedRanges)
+      for (int k = 0; k < kSortWarps; ++k) {
+        const int c = count[k][r];
+        count[k][r] = at;
+        at += c;
+      }
+  }
+  if (tid == 0) off[static_cast<int64_t>(ranges) * stretches + blockIdx.x] = base;
+  __syncthreads();
+  for (int i0 = w0; i0 < w1; i0 += 32) {  // place
+    const int id = i0 + lane < w1 ? ids[first + i0 + lane] : -1;
+    const bool in = static_cast<uint32_t>(id) < static_cast<uint32_t>(v) && id != pad;
+    const uint32_t some = __ballot_sync(kFull, in);
+    if (in) {
+      const int at = take_rank(some, id / per, row, lane);
+      tokens[first + at] = make_int2(id, static_cast<int>(first) + i0 + lane);
+    }
+    __syncwarp();
+  }
+}
+
+// Block r: range r's ids [r per, (r + 1) per).
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, int per, int stretches, int len,
+                                                                  const int2* __restrict__ tokens,
+                                                                  const int32_t* __restrict__ off,
+                                                                  const int32_t* __restrict__ bad,
                                                                   int32_t* __restrict__ start,
                                                                   int32_t* __restrict__ order,
                                                                   int32_t* __restrict__ sorted_id, int* status) {
-  extern __shared__ int32_t count[];  // [kSortWarps][per]
-  __shared__ int32_t warp_sum[kSortWarps];
-  __shared__ int32_t below_sum[kSortWarps];
+  extern __shared__ __align__(16) int32_t sort_smem[];
+  __shared__ int part[kSortWarps];
+  __shared__ int32_t seg_first[kEmbedStretches], seg_off[kEmbedStretches];  // of the range's tokens, of the stretch's
+  int2* list = reinterpret_cast<int2*>(sort_smem);
+  int32_t* running = sort_smem + 2 * kSortRound;  // [per]: where an id's next token goes
+  int32_t* count = running + per;                 // [kSortWarps][per]
   griddep_begin();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int lo = blockIdx.x * per;
-  const int mine = min(per, v - lo);
-  for (int i = tid; i < kSortWarps * per; i += kSortThreads) count[i] = 0;
-  __syncthreads();
-  int32_t* row = count + warp * per;
-  const int64_t p0 = static_cast<int64_t>(warp) * seg;
-  const int64_t p1 = min(p0 + seg, static_cast<int64_t>(n));
-  const uint32_t ulo = static_cast<uint32_t>(lo), umine = static_cast<uint32_t>(mine);
-  int below = 0, bad = 0;
-  for (int64_t p = p0; p < p1; p += 32 * kSortBatch) {
-    int32_t id[kSortBatch];
-#pragma unroll
-    for (int k = 0; k < kSortBatch; ++k) {
-      const int64_t i = p + 32 * k + lane;
-      id[k] = i < p1 ? __ldg(ids + i) : kNoToken;
-    }
-    uint32_t hits = 0;  // few: the block owns a small part of the vocabulary
-#pragma unroll
-    for (int k = 0; k < kSortBatch; ++k) {
-      const uint32_t u = static_cast<uint32_t>(id[k]);  // (an id below 0 is above every range)
-      below += u < ulo && id[k] != pad;
-      hits |= (u - ulo < umine ? 1u : 0u) << k;
-      if (blockIdx.x == 0) bad |= u >= static_cast<uint32_t>(v) && p + 32 * k + lane < p1;
-    }
-    if (hits) {
-#pragma unroll
-      for (int k = 0; k < kSortBatch; ++k)
-        if ((hits >> k & 1) && id[k] != pad) atomicAdd(row + (id[k] - lo), 1);
-    }
+  const int r = blockIdx.x, lo = r * per, mine = min(per, v - lo);
+  int all, wrong = 0;
+  // the range's tokens of each stretch, and all tokens of the ranges before
+  static_assert(kEmbedStretches <= kSortThreads, "a thread for each stretch");
+  const int at = tid < stretches ? off[static_cast<int64_t>(r) * stretches + tid] : 0;
+  const int to = tid < stretches ? off[static_cast<int64_t>(r + 1) * stretches + tid] : 0;
+  if (r == 0 && tid < stretches) wrong = bad[tid];
+  const int incl = block_scan(to - at, part, &all);
+  const int m = all;
+  if (tid < stretches) {
+    seg_first[tid] = incl - (to - at);
+    seg_off[tid] = at;
   }
-  below = __reduce_add_sync(kFull, below);
-  if (lane == 0) below_sum[warp] = below;
-  bad = __syncthreads_or(bad);
-  if (blockIdx.x == 0 && tid == 0) *status = bad ? kErrLabel : kOk;
-  below = __reduce_add_sync(kFull, below_sum[lane]);
-  // exclusive sums: of an id's counts over the warps, then of the ids (in turns of a block's threads)
+  block_scan(at, part, &all);
+  int begin = all;
+  wrong = __syncthreads_or(wrong);
+  if (r == 0 && tid == 0) *status = wrong ? kErrLabel : kOk;
+  auto token = [&](int i) {  // the range's i-th, in the order of positions
+    int a = 0, b = stretches - 1;
+    while (a < b) {
+      const int mid = (a + b + 1) >> 1;
+      if (seg_first[mid] <= i) a = mid;
+      else b = mid - 1;
+    }
+    return tokens[static_cast<int64_t>(a) * len + seg_off[a] + (i - seg_first[a])];
+  };
+  // ids' totals, and where each one's tokens start
+  for (int j = tid; j < per; j += kSortThreads) running[j] = 0;
+  __syncthreads();
+  for (int i = tid; i < m; i += kSortThreads) {
+    const int2 t = token(i);
+    if (i < kSortRound) list[i] = t;
+    atomicAdd(running + (t.x - lo), 1);
+  }
+  __syncthreads();
   for (int j0 = 0; j0 < mine; j0 += kSortThreads) {
-    const int j = j0 + tid;
-    int total = 0;
-    if (j < mine) {
-      for (int k = 0; k < kSortWarps; ++k) {
-        const int c = count[k * per + j];
-        count[k * per + j] = total;
-        total += c;
-      }
-    }
-    int incl = total;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(kFull, incl, d);
-      if (lane >= d) incl += up;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    const int ws = warp_sum[lane];
-    int before = __reduce_add_sync(kFull, lane < warp ? ws : 0);
-    const int all = __reduce_add_sync(kFull, ws);
-    const int first = below + before + incl - total;
-    if (j < mine) {
-      start[lo + j] = first;
-      for (int k = 0; k < kSortWarps; ++k) count[k * per + j] += first;
-    }
-    below += all;
-    __syncthreads();
+    const int j = j0 + tid, c = j < mine ? running[j] : 0;
+    const int first = begin + block_scan(c, part, &all) - c;
+    begin += all;
+    if (j < mine) start[lo + j] = running[j] = first;
   }
-  if (lo + mine == v && tid == 0) start[v] = below;
+  if (lo + mine == v && tid == 0) start[v] = begin;
   __syncthreads();
-  for (int64_t p = p0; p < p1; p += 32 * kSortBatch) {
-    int32_t id[kSortBatch];
+  for (int i0 = 0; i0 < m; i0 += kSortRound) {
+    const int here = min(kSortRound, m - i0);
+    for (int j = tid; j < kSortWarps * per; j += kSortThreads) count[j] = 0;
+    if (i0 > 0)
+      for (int i = tid; i < here; i += kSortThreads) list[i] = token(i0 + i);
+    __syncthreads();
+    // each token's rank among its warp's with its id
+    const int each = (here + kSortThreads - 1) / kSortThreads * 32;
+    const int w0 = warp * each, w1 = min(w0 + each, here);
+    int32_t* row = count + warp * per;
+    int rank[kSortRound / kSortThreads];
 #pragma unroll
-    for (int k = 0; k < kSortBatch; ++k) {
-      const int64_t i = p + 32 * k + lane;
-      id[k] = i < p1 ? __ldg(ids + i) : kNoToken;
-    }
-#pragma unroll
-    for (int k = 0; k < kSortBatch; ++k) {
-      const bool in = static_cast<uint32_t>(id[k]) - ulo < umine && id[k] != pad;
-      const uint32_t some = __ballot_sync(kFull, in);
-      if (!some) continue;
-      if (in) {
-        const int j = id[k] - lo;
-        const uint32_t same = __match_any_sync(some, j);
-        const int at = row[j] + __popc(same & ((1u << lane) - 1));
-        __syncwarp(some);
-        if ((same >> lane) == 1u) row[j] = at + 1;  // the highest of them
-        if (in_bounds(at, n, status)) {
-          order[at] = static_cast<int32_t>(p + 32 * k + lane);
-          sorted_id[at] = id[k];
-        }
-      }
+    for (int k = 0; k < kSortRound / kSortThreads; ++k) {
+      const int i = w0 + 32 * k + lane;
+      const uint32_t some = __ballot_sync(kFull, i < w1);
+      rank[k] = i < w1 ? take_rank(some, list[i].x - lo, row, lane) : 0;
       __syncwarp();
     }
+    __syncthreads();
+    for (int j = tid; j < mine; j += kSortThreads) {  // (warp, id) counts to places
+      int next = running[j];
+      for (int k = 0; k < kSortWarps; ++k) {
+        const int c = count[k * per + j];
+        count[k * per + j] = next;
+        next += c;
+      }
+      running[j] = next;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSortRound / kSortThreads; ++k) {
+      const int i = w0 + 32 * k + lane;
+      if (i >= w1) continue;
+      const int2 t = list[i];
+      const int where = row[t.x - lo] + rank[k];
+      if (in_bounds(where, n, status)) {
+        order[where] = t.y;
+        sorted_id[where] = t.x;
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -305,7 +388,7 @@ constexpr int kZeroRows = 8;  // of a warp of the zeros' blocks
 // goes on.
 //   Blocks below `tile_blocks` take tiles, the others the rows without a token.  A batch of
 // tokens' rows is in flight at once, with the rows of dW that they complete.
-template <typename T, typename TW, bool ALIGNED, bool ADD>
+template <typename T, typename TW, bool ALIGNED, bool ADD, int kTile>
 __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, float scale, int64_t tile_blocks,
                                                           const int32_t* __restrict__ start,
                                                           const int32_t* __restrict__ order,
@@ -350,7 +433,6 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, f
     Words<T, ALIGNED> y[kBatch];
     Words<TW, ALIGNED> old[ADD ? kBatch : 1];
     int id[kBatch + 1];
-    const int half = b / 32;
 #pragma unroll
     for (int k = 0; k <= kBatch; ++k) {  // ids of the batch and of the token behind it
       int held = my_id[0];
@@ -365,7 +447,7 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, f
       int held = my_at[0];
 #pragma unroll
       for (int j = 1; j < kTile / 32; ++j)
-        if (half == j) held = my_at[j];
+        if ((b + k) / 32 == j) held = my_at[j];
       const int64_t at = static_cast<int64_t>(__shfl_sync(kFull, held, (b + k) & 31)) * h;
       y[k].zero();
       if (ADD) old[ADD ? k : 0].zero();
@@ -398,7 +480,7 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, f
 constexpr int kJoinAlone = 16;  // parts that a warp adds up by itself; more are cut into a run for each warp
 
 // Block (t, g): 8 times 256 columns of the row that starts in tile t and goes on, if there is one.
-template <typename TW, bool ALIGNED, bool ADD>
+template <typename TW, bool ALIGNED, bool ADD, int kTile>
 __global__ void __launch_bounds__(256) embed_join_kernel(int h, int v, float scale, const int32_t* __restrict__ start,
                                                          const int32_t* __restrict__ sorted_id,
                                                          const float* __restrict__ part, TW* __restrict__ dw, int groups) {
@@ -475,21 +557,28 @@ cudaError_t forward_of(const EmbedParams& q, const int32_t* ids, const void* w, 
                   static_cast<const T*>(w), static_cast<T*>(y), groups, status);
 }
 
-template <typename T, typename TW, bool ALIGNED, bool ADD>
-cudaError_t backward_as(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, cudaStream_t s) {
+template <typename T, typename TW, bool ALIGNED, bool ADD, int TILE>
+cudaError_t backward_by(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, cudaStream_t s) {
   const int groups = groups_of(q.h);
   const int n = static_cast<int>(q.n), v = static_cast<int>(q.v);
-  const int64_t tiles = (q.n + kTile - 1) / kTile, tile_blocks = (tiles * groups + 7) / 8;
+  const int64_t tiles = (q.n + TILE - 1) / TILE, tile_blocks = (tiles * groups + 7) / 8;
   const int64_t zero_blocks = ADD ? 0 : (q.v + 8 * kZeroRows - 1) / (8 * kZeroRows);
   const int64_t join_blocks = (tiles - 1) * ((groups + 7) / 8);
   if (tile_blocks + zero_blocks > INT_MAX || join_blocks > INT_MAX) return cudaErrorInvalidValue;
   TW* out = static_cast<TW*>(dw);
-  cudaError_t e = launch_k(embed_tiles_kernel<T, TW, ALIGNED, ADD>, dim3(static_cast<unsigned>(tile_blocks + zero_blocks)),
-                           dim3(256), 0, s, n, q.h, v, q.scale, tile_blocks, o.start, o.order, o.sorted_id,
-                           static_cast<const T*>(dy), o.part, out, groups, o.status);
+  cudaError_t e = launch_k(embed_tiles_kernel<T, TW, ALIGNED, ADD, TILE>,
+                           dim3(static_cast<unsigned>(tile_blocks + zero_blocks)), dim3(256), 0, s, n, q.h, v, q.scale,
+                           tile_blocks, o.start, o.order, o.sorted_id, static_cast<const T*>(dy), o.part, out, groups,
+                           o.status);
   if (e != cudaSuccess || join_blocks == 0) return e;
-  return launch_k(embed_join_kernel<TW, ALIGNED, ADD>, dim3(static_cast<unsigned>(join_blocks)), dim3(256), 0, s, q.h, v,
-                  q.scale, o.start, o.sorted_id, o.part, out, groups);
+  return launch_k(embed_join_kernel<TW, ALIGNED, ADD, TILE>, dim3(static_cast<unsigned>(join_blocks)), dim3(256), 0, s,
+                  q.h, v, q.scale, o.start, o.sorted_id, o.part, out, groups);
+}
+
+template <typename T, typename TW, bool ALIGNED, bool ADD>
+cudaError_t backward_as(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, cudaStream_t s) {
+  return q.n < kEmbedMany ? backward_by<T, TW, ALIGNED, ADD, kEmbedTile>(q, dy, o, dw, s)
+                          : backward_by<T, TW, ALIGNED, ADD, kEmbedTileMany>(q, dy, o, dw, s);
 }
 
 template <typename T, typename TW>
@@ -508,21 +597,23 @@ cudaError_t launch_embed_forward(const EmbedParams& q, const int32_t* ids, const
                  : forward_of<__nv_bfloat16>(q, ids, w, y, status, s);
 }
 
-cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, int sms,
-                              cudaStream_t s) {
-  // a range for each SM, or as many as keep a block's counts within its shared memory
-  constexpr int kMostPer = 1536;
-  const int64_t blocks0 = std::max<int64_t>(std::min<int64_t>(sms, q.v), (q.v + kMostPer - 1) / kMostPer);
-  const int per = static_cast<int>((q.v + blocks0 - 1) / blocks0);
-  const int64_t blocks = (q.v + per - 1) / per;
-  const int seg = static_cast<int>((q.n + kSortThreads - 1) / kSortThreads) * 32;
-  const size_t smem = sizeof(int32_t) * kSortWarps * static_cast<size_t>(per);
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(embed_sort_kernel, sizeof(int32_t) * kSortWarps * kMostPer, done);
+cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, cudaStream_t s) {
+  const int per = static_cast<int>((q.v + kEmbedRanges - 1) / kEmbedRanges);
+  const int ranges = static_cast<int>((q.v + per - 1) / per);
+  const int len = static_cast<int>((q.n + kEmbedStretches - 1) / kEmbedStretches);
+  const int stretches = static_cast<int>((q.n + len - 1) / len);
+  const int n = static_cast<int>(q.n), v = static_cast<int>(q.v);
+  cudaError_t e = launch_k(embed_bucket_kernel, dim3(stretches), dim3(kSortThreads), 0, s, n, v, per, ranges, len, pad,
+                           ids, static_cast<int2*>(o.tokens), o.off, o.bad);
   if (e != cudaSuccess) return e;
-  return launch_k(embed_sort_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kSortThreads), smem, s,
-                  static_cast<int>(q.n), static_cast<int>(q.v), per, seg, pad, ids, o.start, o.order, o.sorted_id,
-                  o.status);
+  auto smem = [](int ids_of_range) {
+    return sizeof(int32_t) * (2 * kSortRound + static_cast<size_t>(kSortWarps + 1) * static_cast<size_t>(ids_of_range));
+  };
+  static std::atomic<uint64_t> done{0};
+  e = allow_smem(embed_sort_kernel, smem(kPerMost), done);
+  if (e != cudaSuccess) return e;
+  return launch_k(embed_sort_kernel, dim3(ranges), dim3(kSortThreads), smem(per), s, n, v, per, stretches, len,
+                  static_cast<const int2*>(o.tokens), o.off, o.bad, o.start, o.order, o.sorted_id, o.status);
 }
 
 cudaError_t launch_embed_backward(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, bool add,

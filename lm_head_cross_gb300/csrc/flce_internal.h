@@ -351,7 +351,14 @@ cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void
                                  float* part, cudaStream_t stream);
 
 // Embedding (flce_embed.cu).
-constexpr int kEmbedTile = 32;  // tokens of the sorted order that are summed at once
+constexpr int kEmbedRanges = 512;            // of the vocabulary, a block's each in the sort
+constexpr int64_t kEmbedIdsMost = 1 << 20;   // rows of a matrix
+constexpr int kEmbedStretches = 304;         // of the positions: two blocks for each SM
+// Tokens of the sorted order that are summed at once, and the tokens of a call from which on the
+// larger number serves: few tokens need small tiles to occupy the GPU, many leave fewer parts in
+// large ones (131072 x 4096: parts joined in 72 us with 32, 42 with 64).
+constexpr int kEmbedTile = 32, kEmbedTileMany = 64;
+constexpr int64_t kEmbedMany = 32768;
 struct EmbedParams {
   int64_t n;
   int h;
@@ -365,16 +372,20 @@ struct EmbedSorted {
   int32_t* start;
   int32_t* order;
   int32_t* sorted_id;
+  void* tokens;    // [n] (id, position), by stretch and range
+  int32_t* off;    // [kEmbedRanges + 1][kEmbedStretches]
+  int32_t* bad;    // [kEmbedStretches]
   float* part;
   int* status;
 };
 // Parts of n tokens whose rows take `row` floats: two for each tile of the sorted order.
 FLCE_HOST_DEVICE inline int64_t embed_part_floats(int64_t n, int64_t row) {
-  return n > kEmbedTile ? 2 * ((n + kEmbedTile - 1) / kEmbedTile) * row : 0;
+  const int64_t tile = n < kEmbedMany ? kEmbedTile : kEmbedTileMany;
+  return n > tile ? 2 * ((n + tile - 1) / tile) * row : 0;
 }
 cudaError_t launch_embed_forward(const EmbedParams& q, const int32_t* ids, const void* w, void* y, int* status,
                                  cudaStream_t stream);
-cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, int sms,
+cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o,
                               cudaStream_t stream);
 cudaError_t launch_embed_backward(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, bool add,
                                   cudaStream_t stream);
