@@ -1801,7 +1801,7 @@ flce_status_t flce_embedding_backward(const flce_embedding_t* q, const void* dy,
                       reinterpret_cast<int32_t*>(base + L.sorted_id), base + L.tokens,
                       reinterpret_cast<int32_t*>(base + L.off), reinterpret_cast<int32_t*>(base + L.bad),
                       reinterpret_cast<float*>(base + L.part), reinterpret_cast<int*>(base)};
-  st = cuda_status(timed(3, 0.0, s, [&] { return launch_embed_sort(ep, q->padding_idx, ids, o, s); }));
+  st = cuda_status(timed(3, 0.0, s, [&] { return launch_embed_sort(ep, q->padding_idx, ids, o, dev.sms, s); }));
   if (st != FLCE_OK) return st;
   return cuda_status(
       timed(3, 0.0, s, [&] { return launch_embed_backward(ep, dy, o, dW, add != 0, s); }));

@@ -11,8 +11,10 @@
 // part for each tile that it has tokens in, the parts added in order, and rounded once.
 //   bucket  every block sorts its stretch of positions by range of the vocabulary
 //   sort    every block gathers one range's tokens, which the stretches hold in order, and sorts
-//           them by id.  No block waits for another, no atomics in global memory.  (Blocks that
-//           each read all ids and kept their range's took 9 us for 8192 tokens and 55 for 131072.)
+//           them by id.  No block waits for another, no atomics in global memory.
+//           Few tokens are sorted in one launch, whose blocks each read all ids and keep their
+//           range's: 8 us for 5003 and 9 for 8192, where the two launches take 12 and 13; 48 for
+//           131072, where they take 28.
 //   tiles   every tile's tokens, 256 columns a warp: rows that lie within the tile are finished,
 //           the others leave a part; beside them, zeros for the rows without a token
 //   join    the rows with several parts
@@ -349,6 +351,119 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, 
   }
 }
 
+constexpr int kFewThreads = 1024;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewBatch = 16;  // loads of ids in flight
+constexpr int kFewMostPer = 1536;  // ids of a block: their counts fit its shared memory
+constexpr int32_t kNoToken = INT32_MIN;  // behind a stretch's end: outside every range
+
+// Block b owns ids [b per, (b + 1) per).  Warp w counts and places the positions of its stretch
+// [w seg, (w + 1) seg), so that (id, warp, position) is the sorted order.
+__global__ void __launch_bounds__(kFewThreads) embed_sort_few_kernel(int n, int v, int per, int seg, int pad,
+                                                                  const int32_t* __restrict__ ids,
+                                                                  int32_t* __restrict__ start,
+                                                                  int32_t* __restrict__ order,
+                                                                  int32_t* __restrict__ sorted_id, int* status) {
+  extern __shared__ int32_t count[];  // [kFewWarps][per]
+  __shared__ int32_t warp_sum[kFewWarps];
+  __shared__ int32_t below_sum[kFewWarps];
+  griddep_begin();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int lo = blockIdx.x * per;
+  const int mine = min(per, v - lo);
+  for (int i = tid; i < kFewWarps * per; i += kFewThreads) count[i] = 0;
+  __syncthreads();
+  int32_t* row = count + warp * per;
+  const int64_t p0 = static_cast<int64_t>(warp) * seg;
+  const int64_t p1 = min(p0 + seg, static_cast<int64_t>(n));
+  const uint32_t ulo = static_cast<uint32_t>(lo), umine = static_cast<uint32_t>(mine);
+  int below = 0, bad = 0;
+  for (int64_t p = p0; p < p1; p += 32 * kFewBatch) {
+    int32_t id[kFewBatch];
+#pragma unroll
+    for (int k = 0; k < kFewBatch; ++k) {
+      const int64_t i = p + 32 * k + lane;
+      id[k] = i < p1 ? __ldg(ids + i) : kNoToken;
+    }
+    uint32_t hits = 0;  // few: the block owns a small part of the vocabulary
+#pragma unroll
+    for (int k = 0; k < kFewBatch; ++k) {
+      const uint32_t u = static_cast<uint32_t>(id[k]);  // (an id below 0 is above every range)
+      below += u < ulo && id[k] != pad;
+      hits |= (u - ulo < umine ? 1u : 0u) << k;
+      if (blockIdx.x == 0) bad |= u >= static_cast<uint32_t>(v) && p + 32 * k + lane < p1;
+    }
+    if (hits) {
+#pragma unroll
+      for (int k = 0; k < kFewBatch; ++k)
+        if ((hits >> k & 1) && id[k] != pad) atomicAdd(row + (id[k] - lo), 1);
+    }
+  }
+  below = __reduce_add_sync(kFull, below);
+  if (lane == 0) below_sum[warp] = below;
+  bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0 && tid == 0) *status = bad ? kErrLabel : kOk;
+  below = __reduce_add_sync(kFull, below_sum[lane]);
+  // exclusive sums: of an id's counts over the warps, then of the ids (in turns of a block's threads)
+  for (int j0 = 0; j0 < mine; j0 += kFewThreads) {
+    const int j = j0 + tid;
+    int total = 0;
+    if (j < mine) {
+      for (int k = 0; k < kFewWarps; ++k) {
+        const int c = count[k * per + j];
+        count[k * per + j] = total;
+        total += c;
+      }
+    }
+    int incl = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += up;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    const int ws = warp_sum[lane];
+    int before = __reduce_add_sync(kFull, lane < warp ? ws : 0);
+    const int all = __reduce_add_sync(kFull, ws);
+    const int first = below + before + incl - total;
+    if (j < mine) {
+      start[lo + j] = first;
+      for (int k = 0; k < kFewWarps; ++k) count[k * per + j] += first;
+    }
+    below += all;
+    __syncthreads();
+  }
+  if (lo + mine == v && tid == 0) start[v] = below;
+  __syncthreads();
+  for (int64_t p = p0; p < p1; p += 32 * kFewBatch) {
+    int32_t id[kFewBatch];
+#pragma unroll
+    for (int k = 0; k < kFewBatch; ++k) {
+      const int64_t i = p + 32 * k + lane;
+      id[k] = i < p1 ? __ldg(ids + i) : kNoToken;
+    }
+#pragma unroll
+    for (int k = 0; k < kFewBatch; ++k) {
+      const bool in = static_cast<uint32_t>(id[k]) - ulo < umine && id[k] != pad;
+      const uint32_t some = __ballot_sync(kFull, in);
+      if (!some) continue;
+      if (in) {
+        const int j = id[k] - lo;
+        const uint32_t same = __match_any_sync(some, j);
+        const int at = row[j] + __popc(same & ((1u << lane) - 1));
+        __syncwarp(some);
+        if ((same >> lane) == 1u) row[j] = at + 1;  // the highest of them
+        if (in_bounds(at, n, status)) {
+          order[at] = static_cast<int32_t>(p + 32 * k + lane);
+          sorted_id[at] = id[k];
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
 // ----------------------------------------------------------------------------- sums
 
 // dW's row: x scale, added to what it held where ADD.
@@ -484,17 +599,22 @@ template <typename TW, bool ALIGNED, bool ADD, int kTile>
 __global__ void __launch_bounds__(256) embed_join_kernel(int h, int v, float scale, const int32_t* __restrict__ start,
                                                          const int32_t* __restrict__ sorted_id,
                                                          const float* __restrict__ part, TW* __restrict__ dw, int groups) {
-  griddep_begin();
   __shared__ float run[8][32][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wide = (groups + 7) / 8;
   const int64_t t = blockIdx.x / wide;
   const int g0 = static_cast<int>(blockIdx.x % wide) * 8;
+  // The sorted order is older than the launch before, which waited for it: it is read ahead of the
+  // wait.  Every block waits before it leaves, so that whatever follows this launch follows that one.
   const int total = start[v];
   const int64_t s0 = t * kTile, s1 = s0 + kTile;
-  if (s1 >= total) return;
-  const int id = sorted_id[s1 - 1];
-  const int a = start[id], b = start[id + 1];
+  int id = 0, a = 0, b = 0;
+  if (s1 < total) {
+    id = sorted_id[s1 - 1];
+    a = start[id];
+    b = start[id + 1];
+  }
+  griddep_begin();
   if (a < s0 || b <= s1) return;
   const int parts = static_cast<int>((b - 1) / kTile - t) + 1;  // part 0 is 2 t + 1, part i is 2 (t + i)
   TW* row = dw + static_cast<int64_t>(id) * h;
@@ -597,7 +717,24 @@ cudaError_t launch_embed_forward(const EmbedParams& q, const int32_t* ids, const
                  : forward_of<__nv_bfloat16>(q, ids, w, y, status, s);
 }
 
-cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, cudaStream_t s) {
+static cudaError_t sort_few(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, int sms,
+                            cudaStream_t s) {
+  // a range for each SM, or as many as keep a block's counts within its shared memory
+  const int64_t ranges = std::max<int64_t>(std::min<int64_t>(sms, q.v), (q.v + kFewMostPer - 1) / kFewMostPer);
+  const int per = static_cast<int>((q.v + ranges - 1) / ranges);
+  const int64_t blocks = (q.v + per - 1) / per;
+  const int seg = static_cast<int>((q.n + kFewThreads - 1) / kFewThreads) * 32;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(embed_sort_few_kernel, sizeof(int32_t) * kFewWarps * kFewMostPer, done);
+  if (e != cudaSuccess) return e;
+  return launch_k(embed_sort_few_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads),
+                  sizeof(int32_t) * kFewWarps * static_cast<size_t>(per), s, static_cast<int>(q.n), static_cast<int>(q.v),
+                  per, seg, pad, ids, o.start, o.order, o.sorted_id, o.status);
+}
+
+cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, int sms,
+                              cudaStream_t s) {
+  if (q.n <= kEmbedFew) return sort_few(q, pad, ids, o, sms, s);
   const int per = static_cast<int>((q.v + kEmbedRanges - 1) / kEmbedRanges);
   const int ranges = static_cast<int>((q.v + per - 1) / per);
   const int len = static_cast<int>((q.n + kEmbedStretches - 1) / kEmbedStretches);

@@ -354,6 +354,7 @@ cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void
 constexpr int kEmbedRanges = 512;            // of the vocabulary, a block's each in the sort
 constexpr int64_t kEmbedIdsMost = 1 << 20;   // rows of a matrix
 constexpr int kEmbedStretches = 304;         // of the positions: two blocks for each SM
+constexpr int64_t kEmbedFew = 16384;         // tokens up to which one launch sorts them
 // Tokens of the sorted order that are summed at once, and the tokens of a call from which on the
 // larger number serves: few tokens need small tiles to occupy the GPU, many leave fewer parts in
 // large ones (131072 x 4096: parts joined in 72 us with 32, 42 with 64).
@@ -385,7 +386,7 @@ FLCE_HOST_DEVICE inline int64_t embed_part_floats(int64_t n, int64_t row) {
 }
 cudaError_t launch_embed_forward(const EmbedParams& q, const int32_t* ids, const void* w, void* y, int* status,
                                  cudaStream_t stream);
-cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o,
+cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, int sms,
                               cudaStream_t stream);
 cudaError_t launch_embed_backward(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, bool add,
                                   cudaStream_t stream);
