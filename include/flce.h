@@ -531,7 +531,9 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
  *   - Products take fp16 operands with power-of-two scales and accumulate in
  *     fp32; rounding leaves about 1e-3 of X's norm, less than bf16's own (up to
  *     6e-3 where most singular values are equal, so that all roundings agree).
- *     Matrices of at most 128 rows or columns carry 22 bits.  Momentum, norm and the weights' update are fp32.
+ *     Matrices of at most 128 rows or columns carry 22 bits (1e-4 of X's norm, up
+ *     to 2e-3 where strong directions outweigh weak ones 1000 to 1).  Momentum,
+ *     norm and the weights' update are fp32.
  *   - The coefficients must keep singular values in [0, 1] within 1.95 at every
  *     step, and c must be 0 or |b| <= 6 |c| (FLCE_ERR_INVALID_ARGUMENT otherwise).
  *   - A matrix of zeros becomes zeros.  One with a non-finite element, or whose

@@ -1860,10 +1860,21 @@ struct MuonPlanGroup {
   bool exact() const { return r() <= kMuonExactRows; }
   int64_t xp() const { return (cols + 7) / 8 * 8; }
   int64_t ap() const { return (r() + 7) / 8 * 8; }
-  size_t x[2], xlo[2], a, alo, p, plo, diag;
+  // parts of X X^T of the exact ones
+  int64_t split_blocks() const {
+    const int64_t all = (c() + kBK - 1) / kBK;
+    return std::max<int64_t>(kMuonSplitBlocks, (all + kMuonSplitsMost - 1) / kMuonSplitsMost);
+  }
+  int64_t splits() const { return ((c() + kBK - 1) / kBK + split_blocks() - 1) / split_blocks(); }
+  size_t x[2], xlo[2], a, p, plo, diag, part;
 };
 struct MuonRound {
-  std::vector<MuonPlanGroup> groups;
+  std::vector<MuonPlanGroup> groups;  // the exact ones last
+  int plain() const {
+    int n = 0;
+    while (n < static_cast<int>(groups.size()) && !groups[n].exact()) ++n;
+    return n;
+  }
   int matrices = 0;
   int64_t chunks = 0;
   size_t part = 0, total = 0;
@@ -1873,7 +1884,7 @@ size_t muon_matrix_bytes(int64_t rows, int64_t cols) {
   const int64_t r = std::min(rows, cols);
   const size_t x = 2 * static_cast<size_t>(rows) * static_cast<size_t>((cols + 7) / 8 * 8);
   const size_t a = 2 * static_cast<size_t>(r) * static_cast<size_t>((r + 7) / 8 * 8);
-  return r <= kMuonExactRows ? 4 * x + 4 * a : 3 * x + 2 * a;
+  return r <= kMuonExactRows ? 4 * x + 2 * a + 65536 : 3 * x + 2 * a;  // (and more parts: they grow slower than x)
 }
 
 constexpr size_t kMuonRoundBytes = size_t{4} << 30;  // of a round of several matrices
@@ -1927,11 +1938,11 @@ std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
       g.x[1] = take(xb);
       g.xlo[0] = take(xb);
       g.xlo[1] = g.exact() ? take(xb) : g.xlo[0];
-      g.a = take(ab);
       g.p = take(ab);
-      g.alo = g.exact() ? take(ab) : 0;
-      g.plo = g.exact() ? take(ab) : 0;
+      g.a = g.exact() ? 0 : take(ab);
       g.diag = g.exact() ? 0 : take(sizeof(float) * count * static_cast<size_t>(g.r()));
+      g.plo = g.exact() ? take(ab) : 0;
+      g.part = g.exact() ? take(sizeof(float) * count * static_cast<size_t>(g.splits()) * kMuonExactRows * kMuonExactRows) : 0;
     }
     r.total = off;
   }
@@ -1955,21 +1966,31 @@ flce_status_t check_muon_shape(int64_t rows, int64_t cols) {
 // |a + b s^2 + c s^4| for a singular value s of X, below 2^16.  False where some step could take a
 // singular value past 1.95, or shift A's diagonal by more than 3 (b / 2c), beyond which A would
 // not fit its scale.
-bool muon_scales(const flce_muon_t& o, float* p_scale) {
+//   q_scale: the same for the product of the first steps' P, X's factor after them, whose largest
+// value the same grid finds.
+bool muon_scales(const flce_muon_t& o, float* p_scale, float* q_scale) {
+  constexpr int kGrid = 4096;
   double top = 1.0 + 1.0 / 256, p_most = 0.0;
+  std::vector<double> value(kGrid + 1), factor(kGrid + 1, 1.0);
+  for (int i = 0; i <= kGrid; ++i) value[i] = top * i / kGrid;
   for (int k = 0; k < o.steps; ++k) {
     const double a = o.coefficients[3 * k], b = o.coefficients[3 * k + 1], c = o.coefficients[3 * k + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     if (c != 0.0 && std::abs(b) > 6.0 * std::abs(c)) return false;
-    double next = 0.0;
-    constexpr int kGrid = 4096;
+    double next = 0.0, q_most = 0.0;
     for (int i = 0; i <= kGrid; ++i) {
       const double s = top * i / kGrid, p = std::abs(a + s * s * (b + s * s * c));
       p_most = std::max(p_most, p);
       next = std::max(next, p * s);
+      const double at = value[i], q = a + at * at * (b + at * at * c);
+      value[i] = at * q;
+      factor[i] *= q;
+      q_most = std::max(q_most, std::abs(factor[i]));
     }
     top = next * (1.0 + 1.0 / 256);
     if (!(top <= 1.95) || !(p_most <= 1e4)) return false;
+    // (between the grid's points a factor moves by less than a third)
+    q_scale[k] = static_cast<float>(std::exp2(std::floor(std::log2(45000.0 / std::max(q_most, 1e-3)))));
   }
   *p_scale = static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(p_most, 1e-3)))));
   return true;
@@ -1980,7 +2001,7 @@ struct MuonMap {
   CUtensorMap b128, b64, b32;
 };
 struct MuonMaps {
-  MuonMap x[2], xlo[2], a, alo, p, plo;
+  MuonMap x[2], xlo[2], a, p, plo;
 };
 
 bool muon_maps(const MuonPlanGroup& g, uint8_t* ws, MuonMaps* m) {
@@ -1995,11 +2016,11 @@ bool muon_maps(const MuonPlanGroup& g, uint8_t* ws, MuonMaps* m) {
   for (int i = 0; i < 2; ++i)
     if (!all(&m->x[i], g.x[i], g.rows, g.cols, xp, true) || !all(&m->xlo[i], g.xlo[i], g.rows, g.cols, xp, g.exact()))
       return false;
-  if (!all(&m->a, g.a, r, r, ap, true) || !all(&m->p, g.p, r, r, ap, true)) return false;
-  return !g.exact() || (all(&m->alo, g.alo, r, r, ap, true) && all(&m->plo, g.plo, r, r, ap, true));
+  return all(&m->p, g.p, r, r, ap, true) && all(g.exact() ? &m->plo : &m->a, g.exact() ? g.plo : g.a, r, r, ap, true);
 }
 
 int64_t muon_tiles_each(const MuonPlanGroup& g, int mode, int bn) {
+  if (mode == kMuonGram && g.exact()) return g.splits();
   const int64_t m = mode == kMuonApply ? g.rows : g.r(), n = mode == kMuonApply ? g.cols : g.r();
   const int64_t rows = (m + kPairRows - 1) / kPairRows, cols = (n + bn - 1) / bn;
   if (mode == kMuonApply) return rows * cols;
@@ -2007,19 +2028,20 @@ int64_t muon_tiles_each(const MuonPlanGroup& g, int mode, int bn) {
 }
 
 // Columns of a launch's tiles: 128 where there are fewer 256-wide ones than CTA pairs.
-int muon_tile_width(const MuonRound& round, int mode, int sms) {
+int muon_tile_width(const MuonRound& round, int groups, int mode, int sms) {
   int64_t tiles = 0;
-  for (const MuonPlanGroup& g : round.groups) tiles += muon_tiles_each(g, mode, 256) * static_cast<int64_t>(g.items.size());
+  for (int i = 0; i < groups; ++i)
+    tiles += muon_tiles_each(round.groups[i], mode, 256) * static_cast<int64_t>(round.groups[i].items.size());
   return tiles < sms / 2 ? 128 : 256;
 }
 
 // One launch's groups: product `mode` of step k.
-void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mode, int k, int bn,
-               const flce_muon_t& o, float p_scale, uint8_t* ws, MuonArgs* out) {
+void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int groups, int mode, int k, int bn,
+               const flce_muon_t& o, float p_scale, float q_scale, uint8_t* ws, MuonArgs* out) {
   const double ca = o.coefficients[3 * k], cb = o.coefficients[3 * k + 1], cc = o.coefficients[3 * k + 2];
   const double xs = kMuonXScale, as = kMuonAScale, ps = p_scale;
   const int cur = k & 1;
-  out->groups = static_cast<int>(round.groups.size());
+  out->groups = groups;
   int tiles = 0;
   for (int i = 0; i < out->groups; ++i) {
     const MuonPlanGroup& g = round.groups[i];
@@ -2044,19 +2066,18 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mo
     t.row_tiles = (t.m + kPairRows - 1) / kPairRows;
     t.col_tiles = (t.n + bn - 1) / bn;
     t.kblocks = static_cast<int>(((mode == kMuonGram ? g.c() : g.r()) + kBK - 1) / kBK);
-    t.write_lo = g.exact();
     t.diag = g.exact() || cc == 0.0 ? nullptr : reinterpret_cast<float*>(ws + g.diag);
     if (mode == kMuonGram) {
-      operands(m.x[cur], m.xlo[cur], m.x[cur], m.xlo[cur]);
       const bool poly = cc != 0.0;
-      t.out = poly ? m.a.b32 : m.p.b32;
-      t.out_lo = poly ? m.alo.b32 : m.plo.b32;
-      t.alpha = static_cast<float>((poly ? as : cb * ps) / (xs * xs));
+      operands(m.x[cur], m.xlo[cur], m.x[cur], m.xlo[cur]);
+      t.out = poly && !g.exact() ? m.a.b32 : m.p.b32;
+      t.alpha = static_cast<float>((poly || g.exact() ? as : cb * ps) / (xs * xs));
       t.gamma = static_cast<float>(poly ? as * cb / (2.0 * cc) : ca * ps);
+      t.part = g.exact() ? reinterpret_cast<float*>(ws + g.part) : nullptr;
+      t.split_blocks = static_cast<int>(g.split_blocks());
     } else if (mode == kMuonPoly) {
-      operands(m.a, m.alo, m.a, m.alo);
+      operands(m.a, m.a, m.a, m.a);
       t.out = m.p.b32;
-      t.out_lo = m.plo.b32;
       t.alpha = static_cast<float>(cc * ps / (as * as));
       t.gamma = static_cast<float>((ca - cb * cb / (4.0 * cc)) * ps);
     } else {
@@ -2064,7 +2085,7 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mo
       else operands(m.p, m.plo, m.x[cur], m.xlo[cur]);
       t.out = m.x[cur ^ 1].b32;
       t.out_lo = m.xlo[cur ^ 1].b32;
-      t.alpha = static_cast<float>(1.0 / ps);
+      t.alpha = static_cast<float>(1.0 / (g.exact() ? q_scale : ps));
       t.beta = static_cast<float>(ca);
       t.lo_in = !g.exact() && k < kMuonPairSteps;
       t.write_lo = g.exact() || (k + 1 < kMuonPairSteps && k + 1 < o.steps);
@@ -2076,10 +2097,37 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int mo
   out->tiles = tiles;
 }
 
+// The steps of the groups from `first` on.
+void muon_chain(const MuonRound& round, int first, const flce_muon_t& o, float p_scale, const float* q_scale,
+                uint8_t* ws, MuonChain* out) {
+  for (int k = 0; k < o.steps; ++k) {
+    out->a[k] = static_cast<float>(o.coefficients[3 * k]);
+    out->b[k] = static_cast<float>(o.coefficients[3 * k + 1]);
+    out->c[k] = static_cast<float>(o.coefficients[3 * k + 2]);
+    out->q_scale[k] = q_scale[k];
+  }
+  out->p_scale = p_scale;
+  out->steps = o.steps;
+  out->timeout_ns = timeout_ns();
+  out->status = reinterpret_cast<int*>(ws);
+  for (size_t i = first; i < round.groups.size(); ++i) {
+    const MuonPlanGroup& g = round.groups[i];
+    MuonChainGroup& t = out->g[out->groups++];
+    t.part = reinterpret_cast<const float*>(ws + g.part);
+    t.splits = static_cast<int>(g.splits());
+    t.q = reinterpret_cast<__half*>(ws + g.p);
+    t.q_lo = reinterpret_cast<__half*>(ws + g.plo);
+    t.r = static_cast<int>(g.r());
+    t.pitch = static_cast<int>(g.ap());
+    t.block0 = out->blocks;
+    out->blocks += static_cast<int>(g.items.size());
+  }
+}
+
 flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o, const float* grad_scale, void* ws,
                        size_t ws_bytes, cudaStream_t s) {
-  float p_scale = 1.f;
-  if (!muon_scales(o, &p_scale)) return FLCE_ERR_INVALID_ARGUMENT;
+  float p_scale = 1.f, q_scale[FLCE_MUON_MAX_STEPS] = {};
+  if (!muon_scales(o, &p_scale, q_scale)) return FLCE_ERR_INVALID_ARGUMENT;
   const std::vector<MuonRound> rounds = muon_rounds(items);
   if (ws_bytes < muon_bytes(rounds)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -2128,8 +2176,8 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
         t.flags = m.flags | (aligned(m.grad, gf ? 16 : 8) && aligned(m.momentum, 16) ? kMuonAligned : 0u);
         src.chunk0[src.count] = static_cast<uint32_t>(chunks);
         src.strip0[src.count] = static_cast<uint32_t>(strips);
-        w.hi = half(g.x[o.steps & 1]);
-        w.lo = g.exact() ? half(g.xlo[o.steps & 1]) : nullptr;
+        w.hi = half(g.x[g.exact() ? 1 : o.steps & 1]);  // (the exact ones' X is multiplied once)
+        w.lo = g.exact() ? half(g.xlo[1]) : nullptr;
         w.out = m.out;
         w.param = m.param;
         w.master = m.master;
@@ -2158,11 +2206,20 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
     MuonArgs args{};
     args.timeout_ns = timeout_ns();
     args.status = reinterpret_cast<int*>(base);
+    const int all = static_cast<int>(round.groups.size()), plain = round.plain();
     for (int k = 0; k < o.steps; ++k) {
       for (int mode : {kMuonGram, kMuonPoly, kMuonApply}) {
+        if (mode == kMuonApply && k == 0 && plain < all) {
+          MuonChain chain{};
+          muon_chain(round, plain, o, p_scale, q_scale, base, &chain);
+          st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_chain(chain, s); }));
+          if (st != FLCE_OK) return st;
+        }
         if (mode == kMuonPoly && o.coefficients[3 * k + 2] == 0.0) continue;  // (kGram wrote P)
-        const int bn = muon_tile_width(round, mode, dev.sms);
-        muon_args(round, maps, mode, k, bn, o, p_scale, base, &args);
+        const int groups = k == 0 && mode != kMuonPoly ? all : plain;  // the exact ones take part once
+        if (groups == 0) continue;
+        const int bn = muon_tile_width(round, groups, mode, dev.sms);
+        muon_args(round, maps, groups, mode, k, bn, o, p_scale, q_scale[o.steps - 1], base, &args);
         st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_product(mode, bn, args, dev.sms, s); }));
         if (st != FLCE_OK) return st;
       }

@@ -433,7 +433,9 @@ constexpr int kMuonGroups = 12;
 constexpr int kMuonMatrices = 256;
 constexpr int kMuonChunk = 8192;     // elements of one block of the momentum's pass
 constexpr int kMuonStrip = 4096;     // and of the passes between a tensor and X
-constexpr int kMuonExactRows = 128;  // up to this many rows, pairs of fp16 everywhere
+constexpr int kMuonExactRows = 128;  // up to this many rows or columns: pairs of fp16, steps on X X^T alone
+constexpr int kMuonSplitBlocks = 8;  // of 64 elements, of one part of their X X^T
+constexpr int kMuonSplitsMost = 64;
 constexpr int kMuonPairSteps = 3;    // else for the first iterates alone
 constexpr float kMuonXScale = 16384.f, kMuonAScale = 8192.f;
 enum MuonMode : int { kMuonGram, kMuonPoly, kMuonApply };
@@ -450,8 +452,10 @@ struct MuonGroup {
   CUtensorMap out, out_lo;
   float* diag;  // [matrix][m], for the square: what rounding the diagonal left (null: nothing)
   float alpha, beta, gamma;
+  float* part;  // kGram of a matrix of few rows: alpha a b of each split of the contraction, [matrix][split][128][128]
   int m, n;
   int kblocks, segments;  // 64-element steps of the contraction; 3 for hi hi + hi lo + lo hi, else 1
+  int split_blocks;       // of one split of kGram's parts
   int tile0, tiles_each, row_tiles, col_tiles;
   int tall;               // X has more rows than columns
   int lo_in, write_lo;    // add beta times out_lo's old values; write out_lo
@@ -463,6 +467,23 @@ struct MuonArgs {
   int* status;
 };
 static_assert(sizeof(MuonArgs) <= 32764, "kernel argument limit");
+// The steps of the matrices of at most kMuonExactRows rows, from X X^T to the product Q of all
+// steps' P, a block each.
+struct MuonChainGroup {
+  const float* part;   // X X^T in kGram's parts, in units of 1 / kMuonAScale
+  int splits;
+  __half *q, *q_lo;    // [matrix][r][pitch]
+  int r, pitch;
+  int block0;
+};
+struct MuonChain {
+  MuonChainGroup g[kMuonGroups];
+  float a[16], b[16], c[16];  // of each step
+  float p_scale, q_scale[16];
+  int groups, blocks, steps;
+  uint64_t timeout_ns;
+  int* status;
+};
 struct MuonSource {
   const void* grad;
   float* momentum;  // or null: the gradient itself is what is orthogonalised
@@ -508,6 +529,7 @@ int64_t muon_strips(int64_t rows, int64_t cols, int vec);  // blocks of the scal
 cudaError_t launch_muon_momentum(const MuonSources& a, cudaStream_t stream);
 cudaError_t launch_muon_scale(const MuonSources& a, int sms, cudaStream_t stream);
 cudaError_t launch_muon_weights(const MuonTargets& a, int sms, cudaStream_t stream);
+cudaError_t launch_muon_chain(const MuonChain& a, cudaStream_t stream);
 // bn: columns of a tile, 256 or 128.
 cudaError_t launch_muon_product(int mode, int bn, const MuonArgs& a, int sms, cudaStream_t stream);
 

@@ -33,8 +33,12 @@
 // use hi alone and the epilogue adds a lo: what P lo - a lo would add lies along the strong
 // directions themselves, where it does no harm (1.0e-3 of the result then).
 //
-// Matrices of at most kMuonExactRows rows average few rounding errors (8 x 8: 4e-3) and cost
-// little: all of X, A and P are pairs there, each product hi hi + hi lo + lo hi.
+// Matrices of at most kMuonExactRows rows (or columns) average few rounding errors (8 x 8: 4e-3),
+// and one block holds all of A, P and the product Q of the P: there every operand is a pair, each
+// product hi hi + hi lo + lo hi, and the steps run on A alone,
+//   P = a I + b A + c A^2,   Q <- P Q,   A <- P A P,
+// X being read twice, for X X^T and for Q X: 1e-4 of the result, up to 2e-3 where strong
+// directions outweigh weak ones 1000 to 1.
 #include <cuda_fp16.h>
 
 #include "flce_device.cuh"
@@ -109,6 +113,8 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t w) {
 struct Tile {
   const MuonGroup* g;
   int matrix, m0, n0;
+  int kb0, kb1;  // steps of the contraction
+  int split;
 };
 
 template <int MODE, int BN>
@@ -121,8 +127,14 @@ __device__ __forceinline__ bool find_tile(const MuonArgs& a, int t, uint32_t ran
   o.g = &g;
   o.matrix = t / g.tiles_each;
   t -= o.matrix * g.tiles_each;
-  int ti = 0, tj;
-  if (MODE == kMuonApply) {  // the tiles that share their part of X follow one another
+  int ti = 0, tj = 0;
+  o.kb0 = o.split = 0;
+  o.kb1 = g.kblocks;
+  if (MODE == kMuonGram && g.part) {
+    o.split = t;
+    o.kb0 = t * g.split_blocks;
+    o.kb1 = min(o.kb0 + g.split_blocks, g.kblocks);
+  } else if (MODE == kMuonApply) {  // the tiles that share their part of X follow one another
     const int inner = g.tall ? g.col_tiles : g.row_tiles;
     ti = g.tall ? t / inner : t % inner;
     tj = g.tall ? t % inner : t / inner;
@@ -180,7 +192,7 @@ __device__ void run_producer(const MuonArgs& a, uint32_t rank, int pair, int pai
       const CUtensorMap* a64 = seg == 2 ? &g.a_lo64 : &g.a64;
       const CUtensorMap* b128 = seg == 1 ? &g.b_lo128 : &g.b128;
       const CUtensorMap* b64 = seg == 1 ? &g.b_lo64 : &g.b64;
-      for (int kb = 0; kb < g.kblocks; ++kb) {
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
         if (!mbar_wait(&b.empty[stage], phase ^ 1u, a.timeout_ns, b.abort_flag)) {
           record_timeout(a, rank, b.abort_flag);
           return;
@@ -227,7 +239,7 @@ __device__ void run_mma(const MuonArgs& a, int pair, int pairs, uint8_t* smem, u
     const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
     uint32_t more = 0;
     for (int seg = 0; seg < t.g->segments; ++seg) {
-      for (int kb = 0; kb < t.g->kblocks; ++kb) {
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
         const bool a_mn = !a_k_major<MODE>(*t.g, t, kb * kBK);
         const bool b_mn = !b_k_major<MODE>(*t.g, t, kb * kBK);
         const uint32_t idesc = instr_desc_f16(kPairM, BN, a_mn, b_mn);
@@ -319,6 +331,15 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
       float v[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(d[j]) * g.alpha;
+      if (MODE == kMuonGram && g.part) {
+        const int splits = g.tiles_each;
+        float* to = g.part + ((static_cast<int64_t>(t.matrix) * splits + t.split) * kMuonExactRows + row) * kMuonExactRows + j0;
+        if (row < g.m) {
+#pragma unroll
+          for (int j = 0; j < 64; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        continue;
+      }
       if (MODE != kMuonApply) {
         const int diag = row - j0;  // in this chunk, for the lanes of one row block alone
         if (static_cast<unsigned>(i0 - j0 + 31) < 95u) {
@@ -460,6 +481,222 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------------------------- the steps of small matrices
+
+constexpr int kChainThreads = 256;
+constexpr int kChainHalf = kMuonExactRows * kMuonExactRows * 2;  // one fp16 matrix: two blocks of 64 columns
+constexpr int kChainBlock = kChainHalf / 2;
+constexpr int kChainBarOff = 6 * kChainHalf;                      // A (then P A), P, Q, each hi and lo
+constexpr int kChainSmem = kChainBarOff + 64 + 1024;
+static_assert(kChainSmem <= 232448, "shared memory budget");
+
+__device__ __forceinline__ void umma_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t more) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(more)
+      : "memory");
+}
+
+// 8 fp16 of (row, columns 8 c .. 8 c + 7) of a matrix of the block.
+__device__ __forceinline__ uint4* chain_at(uint8_t* m, int row, int c) {
+  return reinterpret_cast<uint4*>(m + (c >> 3) * kChainBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void chain_store(uint8_t* m, int row, int c0, const float (&v)[64]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = v[8 * c + 2 * e], y = v[8 * c + 2 * e + 1];
+      hi[e] = pack_half2(x, y);
+      const float2 f = unpack_half2(hi[e]);
+      lo[e] = pack_half2(x - f.x, y - f.y);
+    }
+    *chain_at(m, row, c0 + c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *chain_at(m + kChainHalf, row, c0 + c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
+
+// All of a matrix's steps in one block: operands in shared memory, one thread issues the products,
+// a thread of the eight warps holds half a row of their results.  Symmetric operands are K-major
+// on either side.
+__global__ void __launch_bounds__(kChainThreads, 1) muon_chain_kernel(const __grid_constant__ MuonChain a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *ma = smem, *mp = smem + 2 * kChainHalf, *mq = smem + 4 * kChainHalf;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kChainBarOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 1);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(256) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *slot;
+  griddep_begin();
+  int gi = 0;
+  while (gi + 1 < a.groups && a.g[gi + 1].block0 <= blockIdx.x) ++gi;
+  const MuonChainGroup& g = a.g[gi];
+  const int64_t matrix = blockIdx.x - g.block0;
+  const int r = g.r;
+  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 8;  // of the thread: columns 8 c0 .. 8 c0 + 63
+  const bool live = 8 * c0 < r;
+  const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(8 * c0);
+  {
+    float v[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) v[j] = 0.f;
+    if (row < r && live) {
+      const float* from = g.part + (matrix * g.splits * kMuonExactRows + row) * kMuonExactRows + 8 * c0;
+      for (int k = 0; k < g.splits; ++k, from += kMuonExactRows * kMuonExactRows) {
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(from + j);
+          v[j] += q.x, v[j + 1] += q.y, v[j + 2] += q.z, v[j + 3] += q.w;
+        }
+      }
+    }
+    chain_store(ma, row, c0, v);
+    if (!live) {  // columns that no product writes
+#pragma unroll
+      for (int j = 0; j < 64; ++j) v[j] = 0.f;
+      chain_store(mp, row, c0, v);
+      chain_store(mq, row, c0, v);
+    }
+  }
+  uint32_t phase = 0;
+  const uint32_t idesc = instr_desc_f16(kMuonExactRows, (r + 15) / 16 * 16, false, false);
+  const int ksteps = (r + 15) / 16;
+  auto multiply = [&](uint32_t d, uint8_t* x, uint8_t* y) {  // one thread
+    for (int seg = 0; seg < 3; ++seg) {
+      const uint32_t sx = smem_u32(x + (seg == 2 ? kChainHalf : 0)), sy = smem_u32(y + (seg == 1 ? kChainHalf : 0));
+      for (int k = 0; k < ksteps; ++k) {
+        const uint32_t at = (k >> 2) * kChainBlock + (k & 3) * 32;
+        umma_one(d, smem_desc_sw128(sx + at, 16, 1024), smem_desc_sw128(sy + at, 16, 1024), idesc, (seg | k) != 0 ? 1u : 0u);
+      }
+    }
+  };
+  // operands written by all threads; up to two products; their results ready for all threads
+  auto products = [&](uint8_t* x, uint8_t* y, uint8_t* z) {
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after_sync();
+      if (y) multiply(tmem, x, y);
+      if (z) multiply(tmem + kMuonExactRows, x, z);
+      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    }
+    const bool done = __syncthreads_and(mbar_wait(bar, phase, a.timeout_ns, abort_flag));  // one answer for all
+    phase ^= 1u;
+    tc_fence_after_sync();
+    return done;
+  };
+  auto result = [&](uint32_t at, float (&v)[64]) {
+    uint32_t d[64];
+    __syncwarp();
+    tmem_ld_32x64(at, d);
+#pragma unroll
+    for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(d[j]);
+  };
+  bool ok = true;
+  for (int k = 0; k < a.steps && ok; ++k) {
+    const bool last = k + 1 == a.steps;
+    const float ps = a.p_scale;
+    // P = a I + b A + c A^2
+    if (a.c[k] != 0.f) ok = products(ma, ma, nullptr);
+    if (live) {
+      float v[64];
+      if (a.c[k] != 0.f) {
+        result(mine, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] = 0.f;
+      }
+      const float alpha = a.c[k] * ps / (kMuonAScale * kMuonAScale), beta = a.b[k] * ps / kMuonAScale;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 h = *chain_at(ma, row, c0 + c), l = *chain_at(ma + kChainHalf, row, c0 + c);
+        const uint32_t uh[4] = {h.x, h.y, h.z, h.w}, ul[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_half2(uh[e]), q = unpack_half2(ul[e]);
+          const int j = 8 * c + 2 * e, col = 8 * c0 + j;
+          v[j] = fmaf(v[j], alpha, fmaf(f.x + q.x, beta, col == row && row < r ? a.a[k] * ps : 0.f));
+          v[j + 1] = fmaf(v[j + 1], alpha, fmaf(f.y + q.y, beta, col + 1 == row && row < r ? a.a[k] * ps : 0.f));
+        }
+      }
+      chain_store(mp, row, c0, v);
+      if (k == 0) {
+        const float to_q = a.q_scale[0] / ps;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] *= to_q;
+        chain_store(mq, row, c0, v);
+      }
+    }
+    if (last && k == 0) break;
+    // P A and P Q, then (P A) P
+    if (ok) ok = products(mp, last ? nullptr : ma, k == 0 ? nullptr : mq);
+    if (live) {
+      float v[64];
+      if (!last) {
+        result(mine, v);
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] *= 1.f / ps;
+        chain_store(ma, row, c0, v);
+      }
+      if (k > 0) {
+        result(mine + kMuonExactRows, v);
+        const float to_q = a.q_scale[k] / (ps * a.q_scale[k - 1]);
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] *= to_q;
+        chain_store(mq, row, c0, v);
+      }
+    }
+    if (last) break;
+    if (ok) ok = products(ma, mp, nullptr);
+    if (live) {
+      float v[64];
+      result(mine, v);
+#pragma unroll
+      for (int j = 0; j < 64; ++j) v[j] *= 1.f / ps;
+      chain_store(ma, row, c0, v);
+    }
+  }
+  if (!ok && tid == 0) {
+    *abort_flag = 1;
+    atomicCAS(a.status, 0, kErrTimeout);
+  }
+  if (live && row < r) {
+    const int64_t to = (matrix * r + row) * g.pitch;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (8 * (c0 + c) >= g.pitch) continue;  // (rows end at a multiple of 8)
+      *reinterpret_cast<uint4*>(g.q + to + 8 * (c0 + c)) = *chain_at(mq, row, c0 + c);
+      *reinterpret_cast<uint4*>(g.q_lo + to + 8 * (c0 + c)) = *chain_at(mq + kChainHalf, row, c0 + c);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (*abort_flag) {  // products that are still under way land before shared memory and TMEM go
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 2000000ull) {
+    }
+  }
+  if (warp == 0) {
+    tc_fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
   }
 }
 
@@ -786,6 +1023,12 @@ cudaError_t launch_width(int mode, const MuonArgs& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t launch_muon_chain(const MuonChain& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(muon_chain_kernel, kChainSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_k(muon_chain_kernel, dim3(a.blocks), dim3(kChainThreads), kChainSmem, s, a);
+}
 cudaError_t launch_muon_momentum(const MuonSources& a, cudaStream_t s) {
   return launch_k(muon_momentum_kernel, dim3(a.chunk0[a.count]), dim3(kNormThreads), 0, s, a);
 }
