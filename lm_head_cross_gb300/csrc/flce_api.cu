@@ -1969,10 +1969,13 @@ flce_status_t check_muon_shape(int64_t rows, int64_t cols) {
 //   q_scale: the same for the product of the first steps' P, X's factor after them, whose largest
 // value the same grid finds.
 bool muon_scales(const flce_muon_t& o, float* p_scale, float* q_scale) {
-  constexpr int kGrid = 4096;
+  constexpr int kGrid = 256;  // (4096 points took 10 us a step)
   double top = 1.0 + 1.0 / 256, p_most = 0.0;
-  std::vector<double> value(kGrid + 1), factor(kGrid + 1, 1.0);
-  for (int i = 0; i <= kGrid; ++i) value[i] = top * i / kGrid;
+  double value[kGrid + 1], factor[kGrid + 1];
+  for (int i = 0; i <= kGrid; ++i) {
+    value[i] = top * i / kGrid;
+    factor[i] = 1.0;
+  }
   for (int k = 0; k < o.steps; ++k) {
     const double a = o.coefficients[3 * k], b = o.coefficients[3 * k + 1], c = o.coefficients[3 * k + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
@@ -1989,7 +1992,7 @@ bool muon_scales(const flce_muon_t& o, float* p_scale, float* q_scale) {
     }
     top = next * (1.0 + 1.0 / 256);
     if (!(top <= 1.95) || !(p_most <= 1e4)) return false;
-    // (between the grid's points a factor moves by less than a third)
+    // (between the grid's points; the largest factors are those of 0)
     q_scale[k] = static_cast<float>(std::exp2(std::floor(std::log2(45000.0 / std::max(q_most, 1e-3)))));
   }
   *p_scale = static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(p_most, 1e-3)))));

@@ -500,6 +500,24 @@ __device__ __forceinline__ void umma_one(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+// mbar_wait without suspending the thread.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+      if (ok) return true;
+    }
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // 8 fp16 of (row, columns 8 c .. 8 c + 7) of a matrix of the block.
 __device__ __forceinline__ uint4* chain_at(uint8_t* m, int row, int c) {
   return reinterpret_cast<uint4*>(m + (c >> 3) * kChainBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4));
@@ -579,11 +597,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) muon_chain_kernel(const __gr
   const uint32_t idesc = instr_desc_f16(kMuonExactRows, (r + 15) / 16 * 16, false, false);
   const int ksteps = (r + 15) / 16;
   auto multiply = [&](uint32_t d, uint8_t* x, uint8_t* y) {  // one thread
+    const uint64_t dx = smem_desc_sw128(smem_u32(x), 16, 1024), dy = smem_desc_sw128(smem_u32(y), 16, 1024);
+#pragma unroll
     for (int seg = 0; seg < 3; ++seg) {
-      const uint32_t sx = smem_u32(x + (seg == 2 ? kChainHalf : 0)), sy = smem_u32(y + (seg == 1 ? kChainHalf : 0));
-      for (int k = 0; k < ksteps; ++k) {
-        const uint32_t at = (k >> 2) * kChainBlock + (k & 3) * 32;
-        umma_one(d, smem_desc_sw128(sx + at, 16, 1024), smem_desc_sw128(sy + at, 16, 1024), idesc, (seg | k) != 0 ? 1u : 0u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k >= ksteps) break;
+        const int at = ((k >> 2) * kChainBlock + (k & 3) * 32) >> 4;  // (addresses are in units of 16 bytes)
+        umma_one(d, dx + (at + (seg == 2 ? kChainHalf >> 4 : 0)), dy + (at + (seg == 1 ? kChainHalf >> 4 : 0)), idesc,
+                 (seg | k) != 0 ? 1u : 0u);
       }
     }
   };
@@ -598,7 +620,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) muon_chain_kernel(const __gr
       if (z) multiply(tmem + kMuonExactRows, x, z);
       asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
     }
-    const bool done = __syncthreads_and(mbar_wait(bar, phase, a.timeout_ns, abort_flag));  // one answer for all
+    // one answer for all.  The products take about a microsecond: asking again finds their end
+    // sooner than sleeping on it does.
+    const bool done = __syncthreads_and(warp != 0 || mbar_poll(bar, phase, a.timeout_ns));
     phase ^= 1u;
     tc_fence_after_sync();
     return done;
