@@ -53,17 +53,20 @@ constexpr int kPairM = 2 * kBM;
 constexpr int kAStage = kBM * kBK * 2;
 constexpr int kMnBlock = 64 * kBK * 2;  // 64 columns of 64 K rows
 constexpr int kStagingBuf = 32 * 128;
-constexpr int kStagingPerWarp = 2 * kStagingBuf;
 constexpr int kEpiWarps = 8;  // two for each quarter of the TMEM lanes, each half of a tile's columns
 constexpr int kProductThreads = 64 + 32 * kEpiWarps;
 constexpr uint16_t kPairMask = 0x3;
 
-// Tiles of 256 x BN.  BN = 128 where 256 x 256 tiles are fewer than the CTA pairs.
+// Tiles of 256 x BN.  With BN = 256 a warp of the epilogue has two staging buffers for its two
+// groups of 64 columns; with 128 it has one of each, and three stages more hide the latency of
+// loads that few tiles are bound by.
 template <int BN>
 struct Shape {
   static constexpr int kHalfN = BN / 2;  // B rows that each CTA stages
   static constexpr int kStageBytes = kAStage + kHalfN * kBK * 2;
-  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr int kStages = BN == 256 ? 5 : 8;
+  static constexpr int kBuffers = BN == 256 ? 2 : 1;
+  static constexpr int kStagingPerWarp = kBuffers * kStagingBuf;
   static constexpr int kSmemStagingOff = kStages * kStageBytes;
   static constexpr int kSmemBarOff = kSmemStagingOff + kEpiWarps * kStagingPerWarp;
   static constexpr int kSmemBytes = kSmemBarOff + 256 + 1024;
@@ -293,7 +296,9 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
   const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
   const int quarter = (warp + 2) & 3;  // TMEM lanes that this warp may read
   const int half = warp >> 2;
-  uint8_t* stg = staging + warp * kStagingPerWarp;
+  using S = Shape<BN>;
+  uint8_t* stg = staging + warp * S::kStagingPerWarp;
+  uint8_t* stg_lo = stg + (S::kBuffers - 1) * kStagingBuf;  // takes the old lo and then the new one
   uint64_t* ebar = b.ebar + warp;
   const uint32_t tempty_even = mapa_shared(smem_u32(b.tempty), 0);
   int acc = 0, sbuf = 0;
@@ -305,15 +310,16 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
     const int first = t.n0 + half * kCols;
     const bool lo_in = MODE == kMuonApply && g.lo_in;
     const bool pairs_out = g.write_lo;
-    // the second buffer takes the old lo and then the new one
     auto fetch = [&](int j0) {
       if (lane == 0) {
         bulk_wait_group_read<0>();
         mbar_arrive_expect_tx(ebar, kStagingBuf);
-        tma_load_3d(stg + kStagingBuf, &g.out_lo, ebar, j0, i0, t.matrix);
+        tma_load_3d(stg_lo, &g.out_lo, ebar, j0, i0, t.matrix);
       }
     };
     if (lo_in && i0 < g.m && first < g.n) fetch(first);
+    float* keep = MODE != kMuonApply && g.diag ? g.diag + static_cast<int64_t>(t.matrix) * g.m + row : nullptr;
+    const float kept = MODE == kMuonPoly && keep && row < g.m ? *keep : 0.f;  // (under way while the tile is)
     if (!mbar_wait(&b.tfull[acc], acc_phase, a.timeout_ns, b.abort_flag)) {
       record_timeout(a, rank, b.abort_flag);
       break;
@@ -343,9 +349,7 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
       if (MODE != kMuonApply) {
         const int diag = row - j0;  // in this chunk, for the lanes of one row block alone
         if (static_cast<unsigned>(i0 - j0 + 31) < 95u) {
-          float* keep = g.diag ? g.diag + static_cast<int64_t>(t.matrix) * g.m + row : nullptr;
-          float plus = g.gamma;
-          if (MODE == kMuonPoly && keep && row < g.m) plus = fmaf(g.alpha, *keep, plus);
+          const float plus = fmaf(g.alpha, kept, g.gamma);
           float at = 0.f;
 #pragma unroll
           for (int j = 0; j < 64; ++j) {
@@ -369,7 +373,7 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
         ephase ^= 1u;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint4 q = *staged(stg + kStagingBuf, lane, c);
+          const uint4 q = *staged(stg_lo, lane, c);
           const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -382,7 +386,7 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
       uint32_t w[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1]);
-      const bool alternate = !lo_in && !pairs_out;
+      const bool alternate = S::kBuffers == 2 && !lo_in && !pairs_out;
       if (lane == 0) {
         if (alternate) bulk_wait_group_read<1>();
         else bulk_wait_group_read<0>();
@@ -391,12 +395,16 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
       stage_and_store(&g.out, stg + (alternate ? sbuf * kStagingBuf : 0), lane, w, j0, i0, t.matrix);
       sbuf ^= 1;
       if (pairs_out) {
+        if (S::kBuffers == 1) {  // the same buffer again
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const float2 f = unpack_half2(w[j]);
           w[j] = pack_half2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
         }
-        stage_and_store(&g.out_lo, stg + kStagingBuf, lane, w, j0, i0, t.matrix);
+        stage_and_store(&g.out_lo, stg_lo, lane, w, j0, i0, t.matrix);
       }
       if (lo_in && h + 1 < kCols / 64 && j0 + 64 < g.n) fetch(j0 + 64);
     }
@@ -862,7 +870,7 @@ __global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __gri
 
 // The passes between a tensor and its X take blocks of kMuonStrip elements: a warp's lanes hold V
 // (4, 2 or 1, as the rows' alignment allows) consecutive columns each, a thread 16 / V rows.
-static_assert(kMuonStrip == kNormThreads * 16, "16 elements a thread");
+static_assert(kMuonStrip == kNormThreads * 16, "16 elements a thread (32 leave too few warps: 401 us for 319)");
 
 template <int V>
 struct Strip {
@@ -953,7 +961,7 @@ __device__ __forceinline__ float norm_factor(const MuonSources& a, int si, float
 
 // Blocks take runs of consecutive strips, from the last source to the first: what the momentum's
 // pass left in L2 is read first.
-__global__ void __launch_bounds__(kNormThreads) muon_scale_kernel(const __grid_constant__ MuonSources a, uint32_t run) {
+__global__ void __launch_bounds__(kNormThreads, 5) muon_scale_kernel(const __grid_constant__ MuonSources a, uint32_t run) {
   griddep_begin();
   __shared__ float red[kNormThreads / 32];
   const uint32_t begin = (gridDim.x - 1 - blockIdx.x) * run, end = min(begin + run, a.strip0[a.count]);
@@ -1011,7 +1019,7 @@ __device__ __forceinline__ void weights_strip(const MuonTarget& s, uint32_t k0, 
 }
 
 // X to out as bf16, or taken off the weights.
-__global__ void __launch_bounds__(kNormThreads) muon_weights_kernel(const __grid_constant__ MuonTargets a, uint32_t run) {
+__global__ void __launch_bounds__(kNormThreads, 4) muon_weights_kernel(const __grid_constant__ MuonTargets a, uint32_t run) {
   griddep_begin();
   const uint32_t begin = blockIdx.x * run, end = min(begin + run, a.strip0[a.count]);
   if (begin >= end) return;
@@ -1026,8 +1034,12 @@ __global__ void __launch_bounds__(kNormThreads) muon_weights_kernel(const __grid
   }
 }
 
-// Runs of strips for blocks of a launch: about four waves of the SMs' blocks, one strip at least.
-uint32_t run_length(uint32_t strips, int sms) { return std::max<uint32_t>(1, strips / (static_cast<uint32_t>(sms) * 16)); }
+// Strips of a block's run, so that a launch has up to `blocks` blocks for each SM: 32 for the scale's
+// pass (135M elements in 314 us, with 16 in 323, with one strip a block in 463), 64 for the
+// weights' (178 us; with 16 203).
+uint32_t run_length(uint32_t strips, int sms, int blocks) {
+  return std::max<uint32_t>(1, strips / static_cast<uint32_t>(sms * blocks));
+}
 
 template <int MODE, int BN>
 cudaError_t launch_mode(const MuonArgs& a, int sms, cudaStream_t s) {
@@ -1057,11 +1069,11 @@ cudaError_t launch_muon_momentum(const MuonSources& a, cudaStream_t s) {
   return launch_k(muon_momentum_kernel, dim3(a.chunk0[a.count]), dim3(kNormThreads), 0, s, a);
 }
 cudaError_t launch_muon_scale(const MuonSources& a, int sms, cudaStream_t s) {
-  const uint32_t n = a.strip0[a.count], run = run_length(n, sms);
+  const uint32_t n = a.strip0[a.count], run = run_length(n, sms, 32);
   return launch_k(muon_scale_kernel, dim3((n + run - 1) / run), dim3(kNormThreads), 0, s, a, run);
 }
 cudaError_t launch_muon_weights(const MuonTargets& a, int sms, cudaStream_t s) {
-  const uint32_t n = a.strip0[a.count], run = run_length(n, sms);
+  const uint32_t n = a.strip0[a.count], run = run_length(n, sms, 64);
   return launch_k(muon_weights_kernel, dim3((n + run - 1) / run), dim3(kNormThreads), 0, s, a, run);
 }
 int64_t muon_strips(int64_t rows, int64_t cols, int vec) {
