@@ -298,10 +298,9 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
   const int half = warp >> 2;
   using S = Shape<BN>;
   uint8_t* stg = staging + warp * S::kStagingPerWarp;
-  uint8_t* stg_lo = stg + (S::kBuffers - 1) * kStagingBuf;  // takes the old lo and then the new one
   uint64_t* ebar = b.ebar + warp;
   const uint32_t tempty_even = mapa_shared(smem_u32(b.tempty), 0);
-  int acc = 0, sbuf = 0;
+  int acc = 0;
   uint32_t acc_phase = 0, ephase = 0;
   Tile t;
   for (int i = pair; find_tile<MODE, BN>(a, i, rank, t); i += pairs) {
@@ -310,14 +309,14 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
     const int first = t.n0 + half * kCols;
     const bool lo_in = MODE == kMuonApply && g.lo_in;
     const bool pairs_out = g.write_lo;
-    auto fetch = [&](int j0) {
-      if (lane == 0) {
-        bulk_wait_group_read<0>();
-        mbar_arrive_expect_tx(ebar, kStagingBuf);
-        tma_load_3d(stg_lo, &g.out_lo, ebar, j0, i0, t.matrix);
-      }
-    };
-    if (lo_in && i0 < g.m && first < g.n) fetch(first);
+    // of 64 columns, one in each staging buffer
+    const int chunks = i0 < g.m && first < g.n ? min(S::kBuffers, (g.n - first + 63) / 64) : 0;
+    if (lo_in && chunks > 0 && lane == 0) {  // the old lo, while the tile is under way
+      bulk_wait_group_read<0>();
+      mbar_arrive_expect_tx(ebar, chunks * kStagingBuf);
+      for (int h = 0; h < chunks; ++h)
+        tma_load_3d(stg + h * kStagingBuf, &g.out_lo, ebar, first + 64 * h, i0, t.matrix);
+    }
     float* keep = MODE != kMuonApply && g.diag ? g.diag + static_cast<int64_t>(t.matrix) * g.m + row : nullptr;
     const float kept = MODE == kMuonPoly && keep && row < g.m ? *keep : 0.f;  // (under way while the tile is)
     if (!mbar_wait(&b.tfull[acc], acc_phase, a.timeout_ns, b.abort_flag)) {
@@ -326,11 +325,17 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
     }
     tc_fence_after_sync();
     const uint32_t tbase = tmem_base + static_cast<uint32_t>(acc * BN + half * kCols) + (static_cast<uint32_t>(quarter * 32) << 16);
-    bool gave_up = false;
+    if (lo_in && chunks > 0) {
+      if (!mbar_wait(ebar, ephase, a.timeout_ns, b.abort_flag)) {
+        record_timeout(a, rank, b.abort_flag);
+        break;
+      }
+      ephase ^= 1u;
+    }
 #pragma unroll 1
-    for (int h = 0; h < kCols / 64; ++h) {
+    for (int h = 0; h < chunks; ++h) {
       const int j0 = first + h * 64;
-      if (i0 >= g.m || j0 >= g.n) break;
+      uint8_t* buf = stg + h * kStagingBuf;
       __syncwarp();
       uint32_t d[64];
       tmem_ld_32x64(tbase + h * 64, d);
@@ -365,15 +370,9 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
         }
       }
       if (lo_in) {
-        if (!mbar_wait(ebar, ephase, a.timeout_ns, b.abort_flag)) {
-          record_timeout(a, rank, b.abort_flag);
-          gave_up = true;
-          break;
-        }
-        ephase ^= 1u;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint4 q = *staged(stg_lo, lane, c);
+          const uint4 q = *staged(buf, lane, c);
           const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -386,29 +385,21 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
       uint32_t w[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1]);
-      const bool alternate = S::kBuffers == 2 && !lo_in && !pairs_out;
-      if (lane == 0) {
-        if (alternate) bulk_wait_group_read<1>();
-        else bulk_wait_group_read<0>();
-      }
-      __syncwarp();  // the old lo has been read, and the buffers' earlier stores are done with them
-      stage_and_store(&g.out, stg + (alternate ? sbuf * kStagingBuf : 0), lane, w, j0, i0, t.matrix);
-      sbuf ^= 1;
+      // the last tile's stores are done with the buffers (the wait before the old lo's copies was the same)
+      if (lane == 0 && h == 0 && !lo_in) bulk_wait_group_read<0>();
+      __syncwarp();
+      stage_and_store(&g.out, buf, lane, w, j0, i0, t.matrix);
       if (pairs_out) {
-        if (S::kBuffers == 1) {  // the same buffer again
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
-        }
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const float2 f = unpack_half2(w[j]);
           w[j] = pack_half2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
         }
-        stage_and_store(&g.out_lo, stg_lo, lane, w, j0, i0, t.matrix);
+        stage_and_store(&g.out_lo, buf, lane, w, j0, i0, t.matrix);
       }
-      if (lo_in && h + 1 < kCols / 64 && j0 + 64 < g.n) fetch(j0 + 64);
     }
-    if (gave_up) break;
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive_cluster(tempty_even + 8u * acc);
