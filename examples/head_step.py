@@ -4,10 +4,10 @@
 A small bigram model (an embedding in place of a transformer's trunk) runs the calls that
 surround the LM head as a program would use them together:
 
-  training   layer_norm -> token_logprobs (log probabilities and entropies of the next
+  training   embedding -> layer_norm -> token_logprobs (log probabilities and entropies of the next
              tokens) -> backward through both -> AdamW over every parameter, moments in 8
              bits, gradients clipped by their global norm through grad_scale;
-  serving    layernorm_forward -> logprobs_forward for single tokens with the top
+  serving    embedding_forward -> layernorm_forward -> logprobs_forward for single tokens with the top
              alternatives, sampling the next token from them.
 
     python examples/head_step.py [--steps 60] [--hidden 256] [--vocab 1024] [--state-bits 8]
@@ -42,7 +42,7 @@ class Bigram:
                 {"params": [self.norm_weight, self.norm_bias], "weight_decay": 0.0}]
 
     def hidden(self, tokens):
-        return flce.layer_norm(self.embed[tokens], self.norm_weight, self.norm_bias)
+        return flce.layer_norm(flce.embedding(tokens, self.embed), self.norm_weight, self.norm_bias)
 
 
 def train(model, batch, steps, lr=2e-2, entropy_bonus=1e-3, clip=1.0, state_bits=8):
@@ -70,7 +70,8 @@ def generate(model, prompt, length, top=8, temperature=0.8, seed=0):
     g = torch.Generator(device=prompt.device).manual_seed(seed)
     token, tokens, logprobs, ws = prompt, [], [], None
     for _ in range(length):
-        y, _, _ = flce.layernorm_forward(model.embed[token], model.norm_weight, model.norm_bias)
+        x, _ = flce.embedding_forward(token.to(torch.int32), model.embed)
+        y, _, _ = flce.layernorm_forward(x, model.norm_weight, model.norm_bias)
         r, ws = flce.logprobs_forward(y, model.head, top=top, temperature=temperature, ws=ws)
         pick = torch.multinomial(r.top_logprobs.exp(), 1, generator=g)
         token = r.top_ids.gather(1, pick)[:, 0].long()

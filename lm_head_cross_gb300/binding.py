@@ -953,11 +953,16 @@ class _Embedding:
 
 def embedding(ids, weight, scale: float = 1.0, padding_idx=None):
     """scale * weight[ids] for ids [...] (integer CUDA) and weight [V, H] (bf16 or fp32): [..., H].
-    Autograd flows to weight, except from tokens equal to padding_idx."""
+    Autograd flows to weight, except from tokens equal to padding_idx.  An id outside [0, V) gives a
+    row of zeros and passes no gradient (embedding_forward reports it)."""
+    torch = _torch()
     v = weight.shape[0]
     if padding_idx is not None and not 0 <= padding_idx < v:
         raise ValueError(f"padding_idx must be in [0, {v}), got {padding_idx}")
-    flat = ids.reshape(-1).to(_torch().int32).contiguous()
+    flat = ids.reshape(-1)
+    if flat.dtype is torch.int64:  # those beyond 32 bits stay outside
+        flat = flat.clamp(-1, v)
+    flat = flat.to(torch.int32).contiguous()
     y = _Embedding.get().apply(flat, weight.contiguous(), float(scale), padding_idx)
     return y.reshape(*ids.shape, weight.shape[1])
 

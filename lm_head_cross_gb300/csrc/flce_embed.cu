@@ -605,14 +605,15 @@ __global__ void __launch_bounds__(256) embed_join_kernel(int h, int v, float sca
   const int64_t t = blockIdx.x / wide;
   const int g0 = static_cast<int>(blockIdx.x % wide) * 8;
   // The sorted order is older than the launch before, which waited for it: it is read ahead of the
-  // wait.  Every block waits before it leaves, so that whatever follows this launch follows that one.
-  const int total = start[v];
+  // wait, from L2.  Every block waits before it leaves, so that whatever follows this launch follows
+  // that one.
+  const int total = __ldcg(start + v);
   const int64_t s0 = t * kTile, s1 = s0 + kTile;
   int id = 0, a = 0, b = 0;
   if (s1 < total) {
-    id = sorted_id[s1 - 1];
-    a = start[id];
-    b = start[id + 1];
+    id = __ldcg(sorted_id + s1 - 1);
+    a = __ldcg(start + id);
+    b = __ldcg(start + id + 1);
   }
   griddep_begin();
   if (a < s0 || b <= s1) return;
