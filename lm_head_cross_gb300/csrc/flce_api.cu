@@ -2007,19 +2007,27 @@ struct MuonMaps {
   MuonMap x[2], xlo[2], a, p, plo;
 };
 
-bool muon_maps(const MuonPlanGroup& g, uint8_t* ws, MuonMaps* m) {
+// (Only those that some launch takes: an encoding costs 0.4 us.)
+bool muon_maps(const MuonPlanGroup& g, int steps, uint8_t* ws, MuonMaps* m) {
   const uint64_t r = g.r(), n = g.items.size();
   const uint64_t xp = 2 * static_cast<uint64_t>(g.xp()), ap = 2 * static_cast<uint64_t>(g.ap());
-  auto all = [&](MuonMap* t, size_t at, uint64_t rows, uint64_t cols, uint64_t pitch, bool operand) {
+  auto all = [&](MuonMap* t, size_t at, uint64_t rows, uint64_t cols, uint64_t pitch, bool operand, bool output) {
     auto one = [&](CUtensorMap* q, uint32_t box) {
       return make_map3(q, ws + at, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, cols, rows, n, pitch, pitch * rows, 64, box);
     };
-    return one(&t->b32, 32) && (!operand || (one(&t->b128, 128) && one(&t->b64, 64)));
+    return (!output || one(&t->b32, 32)) && (!operand || (one(&t->b128, 128) && one(&t->b64, 64)));
   };
-  for (int i = 0; i < 2; ++i)
-    if (!all(&m->x[i], g.x[i], g.rows, g.cols, xp, true) || !all(&m->xlo[i], g.xlo[i], g.rows, g.cols, xp, g.exact()))
-      return false;
-  return all(&m->p, g.p, r, r, ap, true) && all(g.exact() ? &m->plo : &m->a, g.exact() ? g.plo : g.a, r, r, ap, true);
+  const bool exact = g.exact(), again = !exact && steps > 1;
+  if (!all(&m->x[0], g.x[0], g.rows, g.cols, xp, true, again) || !all(&m->x[1], g.x[1], g.rows, g.cols, xp, again, true))
+    return false;
+  // the exact ones' lo is an operand and an output of its own, the others' is replaced in place
+  if (!all(&m->xlo[0], g.xlo[0], g.rows, g.cols, xp, exact, !exact)) return false;
+  if (exact) {
+    if (!all(&m->xlo[1], g.xlo[1], g.rows, g.cols, xp, false, true)) return false;
+    return all(&m->p, g.p, r, r, ap, true, false) && all(&m->plo, g.plo, r, r, ap, true, false);
+  }
+  m->xlo[1] = m->xlo[0];
+  return all(&m->p, g.p, r, r, ap, true, true) && all(&m->a, g.a, r, r, ap, true, true);
 }
 
 int64_t muon_tiles_each(const MuonPlanGroup& g, int mode, int bn) {
@@ -2045,8 +2053,9 @@ int muon_tile_width(const MuonRound& round, int groups, int mode, int sms) {
 }
 
 // One launch's groups: product `mode` of step k.
+template <int G>
 void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int groups, int mode, int k, int bn,
-               const flce_muon_t& o, float p_scale, float q_scale, uint8_t* ws, MuonArgs* out) {
+               const flce_muon_t& o, float p_scale, float q_scale, uint8_t* ws, MuonArgs<G>* out) {
   const double ca = o.coefficients[3 * k], cb = o.coefficients[3 * k + 1], cc = o.coefficients[3 * k + 2];
   const double xs = kMuonXScale, as = kMuonAScale, ps = p_scale;
   const int cur = k & 1;
@@ -2079,7 +2088,7 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int gr
     if (mode == kMuonGram) {
       const bool poly = cc != 0.0;
       operands(m.x[cur], m.xlo[cur], m.x[cur], m.xlo[cur]);
-      t.out = poly && !g.exact() ? m.a.b32 : m.p.b32;
+      t.out = poly && !g.exact() ? m.a.b32 : m.p.b32;  // (the exact ones write parts)
       t.alpha = static_cast<float>((poly || g.exact() ? as : cb * ps) / (xs * xs));
       t.gamma = static_cast<float>(poly ? as * cb / (2.0 * cc) : ca * ps);
       t.part = g.exact() ? reinterpret_cast<float*>(ws + g.part) : nullptr;
@@ -2133,6 +2142,105 @@ void muon_chain(const MuonRound& round, int first, const flce_muon_t& o, float p
   }
 }
 
+// One round's launches; `first`: of the call.
+template <int N, int G>
+flce_status_t run_muon_round(const std::vector<MuonItem>& items, const MuonRound& round, const flce_muon_t& o,
+                             float p_scale, const float* q_scale, const float* grad_scale, uint8_t* base, bool first,
+                             const Device& dev, cudaStream_t s) {
+  flce_status_t st = FLCE_OK;
+  MuonSources<N> src;
+  MuonTargets<N> to;
+  src.count = 0;
+  src.mu = static_cast<float>(o.momentum);
+  src.omm = static_cast<float>(1.0 - o.momentum);
+  src.nesterov = o.nesterov;
+  src.eps = static_cast<float>(o.eps);
+  src.grad_scale = grad_scale;
+  src.part = reinterpret_cast<float*>(base + round.part);
+  src.status = to.status = reinterpret_cast<int*>(base);
+  src.first = first;
+  int64_t chunks = 0, strips = 0, target_strips = 0;
+  std::vector<MuonMaps> maps(round.groups.size());
+  for (size_t i = 0; i < round.groups.size(); ++i) {
+    const MuonPlanGroup& g = round.groups[i];
+    if (!muon_maps(g, o.steps, base, &maps[i])) return FLCE_ERR_CUDA;
+    for (size_t j = 0; j < g.items.size(); ++j) {
+      const MuonItem& m = items[g.items[j]];
+      const size_t at = j * static_cast<size_t>(g.rows * g.xp());
+      auto half = [&](size_t buf) { return reinterpret_cast<__half*>(base + buf) + at; };
+      // a tensor's rows by `v` columns at a time
+      auto rows_by = [&](const void* p, bool f32, int v) { return aligned(p, v * (f32 ? 4 : 2)) && m.cols % v == 0; };
+      const bool gf = m.flags & kMuonGradF32, pf = m.flags & kMuonParamF32;
+      MuonSource& t = src.s[src.count];
+      MuonTarget& w = to.t[src.count];
+      t.vec = w.vec = 1;
+      for (int v : {2, 4}) {
+        if (rows_by(m.grad, gf, v) && rows_by(m.momentum, true, v)) t.vec = v;
+        if (rows_by(m.out, false, v) && rows_by(m.param, pf, v) && rows_by(m.master, true, v)) w.vec = v;
+      }
+      t.grad = m.grad;
+      t.momentum = m.momentum;
+      t.hi = half(g.x[0]);
+      t.lo = half(g.xlo[0]);
+      t.rows = static_cast<int>(m.rows);
+      t.cols = static_cast<int>(m.cols);
+      t.pitch = static_cast<int>(g.xp());
+      t.flags = m.flags | (aligned(m.grad, gf ? 16 : 8) && aligned(m.momentum, 16) ? kMuonAligned : 0u);
+      src.chunk0[src.count] = static_cast<uint32_t>(chunks);
+      src.strip0[src.count] = static_cast<uint32_t>(strips);
+      w.hi = half(g.x[g.exact() ? 1 : o.steps & 1]);  // (the exact ones' X is multiplied once)
+      w.lo = g.exact() ? half(g.xlo[1]) : nullptr;
+      w.out = m.out;
+      w.param = m.param;
+      w.master = m.master;
+      w.decay = m.decay;
+      w.rate = m.rate;
+      w.rows = t.rows;
+      w.cols = t.cols;
+      w.pitch = t.pitch;
+      w.flags = m.flags;
+      to.strip0[src.count] = static_cast<uint32_t>(target_strips);
+      chunks += muon_chunks(m);
+      strips += muon_strips(m.rows, m.cols, t.vec);
+      target_strips += muon_strips(m.rows, m.cols, w.vec);
+      ++src.count;
+    }
+  }
+  to.count = src.count;
+  src.chunk0[src.count] = static_cast<uint32_t>(chunks);
+  src.strip0[src.count] = static_cast<uint32_t>(strips);
+  to.strip0[src.count] = static_cast<uint32_t>(target_strips);
+  if (chunks > INT32_MAX || strips > INT32_MAX || target_strips > INT32_MAX) return FLCE_ERR_UNSUPPORTED_SHAPE;
+  st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_momentum(src, s); }));
+  if (st != FLCE_OK) return st;
+  st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_scale(src, dev.sms, s); }));
+  if (st != FLCE_OK) return st;
+  MuonArgs<G> args;
+  args.timeout_ns = timeout_ns();
+  args.status = reinterpret_cast<int*>(base);
+  const int all = static_cast<int>(round.groups.size()), plain = round.plain();
+  for (int k = 0; k < o.steps; ++k) {
+    for (int mode : {kMuonGram, kMuonPoly, kMuonApply}) {
+      if (mode == kMuonApply && k == 0 && plain < all) {
+        MuonChain chain{};
+        muon_chain(round, plain, o, p_scale, q_scale, base, &chain);
+        st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_chain(chain, s); }));
+        if (st != FLCE_OK) return st;
+      }
+      if (mode == kMuonPoly && o.coefficients[3 * k + 2] == 0.0) continue;  // (kGram wrote P)
+      const int groups = k == 0 && mode != kMuonPoly ? all : plain;  // the exact ones take part once
+      if (groups == 0) continue;
+      const int bn = muon_tile_width(round, groups, mode, dev.sms);
+      muon_args(round, maps, groups, mode, k, bn, o, p_scale, q_scale[o.steps - 1], base, &args);
+      st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_product(mode, bn, args, dev.sms, s); }));
+      if (st != FLCE_OK) return st;
+    }
+  }
+  st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_weights(to, dev.sms, s); }));
+  if (st != FLCE_OK) return st;
+  return FLCE_OK;
+}
+
 flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o, const float* grad_scale, void* ws,
                        size_t ws_bytes, cudaStream_t s) {
   float p_scale = 1.f, q_scale[FLCE_MUON_MAX_STEPS] = {};
@@ -2146,94 +2254,9 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
   if (st != FLCE_OK) return st;
   for (size_t n = 0; n < rounds.size(); ++n) {
     const MuonRound& round = rounds[n];
-    MuonSources src{};
-    MuonTargets to{};
-    src.mu = static_cast<float>(o.momentum);
-    src.omm = static_cast<float>(1.0 - o.momentum);
-    src.nesterov = o.nesterov;
-    src.eps = static_cast<float>(o.eps);
-    src.grad_scale = grad_scale;
-    src.part = reinterpret_cast<float*>(base + round.part);
-    src.status = to.status = reinterpret_cast<int*>(base);
-    src.first = n == 0;
-    int64_t chunks = 0, strips = 0, target_strips = 0;
-    std::vector<MuonMaps> maps(round.groups.size());
-    for (size_t i = 0; i < round.groups.size(); ++i) {
-      const MuonPlanGroup& g = round.groups[i];
-      if (!muon_maps(g, base, &maps[i])) return FLCE_ERR_CUDA;
-      for (size_t j = 0; j < g.items.size(); ++j) {
-        const MuonItem& m = items[g.items[j]];
-        const size_t at = j * static_cast<size_t>(g.rows * g.xp());
-        auto half = [&](size_t buf) { return reinterpret_cast<__half*>(base + buf) + at; };
-        // a tensor's rows by `v` columns at a time
-        auto rows_by = [&](const void* p, bool f32, int v) { return aligned(p, v * (f32 ? 4 : 2)) && m.cols % v == 0; };
-        const bool gf = m.flags & kMuonGradF32, pf = m.flags & kMuonParamF32;
-        MuonSource& t = src.s[src.count];
-        MuonTarget& w = to.t[src.count];
-        t.vec = w.vec = 1;
-        for (int v : {2, 4}) {
-          if (rows_by(m.grad, gf, v) && rows_by(m.momentum, true, v)) t.vec = v;
-          if (rows_by(m.out, false, v) && rows_by(m.param, pf, v) && rows_by(m.master, true, v)) w.vec = v;
-        }
-        t.grad = m.grad;
-        t.momentum = m.momentum;
-        t.hi = half(g.x[0]);
-        t.lo = half(g.xlo[0]);
-        t.rows = static_cast<int>(m.rows);
-        t.cols = static_cast<int>(m.cols);
-        t.pitch = static_cast<int>(g.xp());
-        t.flags = m.flags | (aligned(m.grad, gf ? 16 : 8) && aligned(m.momentum, 16) ? kMuonAligned : 0u);
-        src.chunk0[src.count] = static_cast<uint32_t>(chunks);
-        src.strip0[src.count] = static_cast<uint32_t>(strips);
-        w.hi = half(g.x[g.exact() ? 1 : o.steps & 1]);  // (the exact ones' X is multiplied once)
-        w.lo = g.exact() ? half(g.xlo[1]) : nullptr;
-        w.out = m.out;
-        w.param = m.param;
-        w.master = m.master;
-        w.decay = m.decay;
-        w.rate = m.rate;
-        w.rows = t.rows;
-        w.cols = t.cols;
-        w.pitch = t.pitch;
-        w.flags = m.flags;
-        to.strip0[src.count] = static_cast<uint32_t>(target_strips);
-        chunks += muon_chunks(m);
-        strips += muon_strips(m.rows, m.cols, t.vec);
-        target_strips += muon_strips(m.rows, m.cols, w.vec);
-        ++src.count;
-      }
-    }
-    to.count = src.count;
-    src.chunk0[src.count] = static_cast<uint32_t>(chunks);
-    src.strip0[src.count] = static_cast<uint32_t>(strips);
-    to.strip0[src.count] = static_cast<uint32_t>(target_strips);
-    if (chunks > INT32_MAX || strips > INT32_MAX || target_strips > INT32_MAX) return FLCE_ERR_UNSUPPORTED_SHAPE;
-    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_momentum(src, s); }));
-    if (st != FLCE_OK) return st;
-    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_scale(src, dev.sms, s); }));
-    if (st != FLCE_OK) return st;
-    MuonArgs args{};
-    args.timeout_ns = timeout_ns();
-    args.status = reinterpret_cast<int*>(base);
-    const int all = static_cast<int>(round.groups.size()), plain = round.plain();
-    for (int k = 0; k < o.steps; ++k) {
-      for (int mode : {kMuonGram, kMuonPoly, kMuonApply}) {
-        if (mode == kMuonApply && k == 0 && plain < all) {
-          MuonChain chain{};
-          muon_chain(round, plain, o, p_scale, q_scale, base, &chain);
-          st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_chain(chain, s); }));
-          if (st != FLCE_OK) return st;
-        }
-        if (mode == kMuonPoly && o.coefficients[3 * k + 2] == 0.0) continue;  // (kGram wrote P)
-        const int groups = k == 0 && mode != kMuonPoly ? all : plain;  // the exact ones take part once
-        if (groups == 0) continue;
-        const int bn = muon_tile_width(round, groups, mode, dev.sms);
-        muon_args(round, maps, groups, mode, k, bn, o, p_scale, q_scale[o.steps - 1], base, &args);
-        st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_product(mode, bn, args, dev.sms, s); }));
-        if (st != FLCE_OK) return st;
-      }
-    }
-    st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_weights(to, dev.sms, s); }));
+    const bool few = round.matrices <= kMuonFewMatrices && round.groups.size() <= kMuonFewGroups;
+    st = few ? run_muon_round<kMuonFewMatrices, kMuonFewGroups>(items, round, o, p_scale, q_scale, grad_scale, base, n == 0, dev, s)
+             : run_muon_round<kMuonMatrices, kMuonGroups>(items, round, o, p_scale, q_scale, grad_scale, base, n == 0, dev, s);
     if (st != FLCE_OK) return st;
   }
   return FLCE_OK;

@@ -429,8 +429,10 @@ cudaError_t launch_adamw(const AdamwArgs<N>& a, int state_bits, cudaStream_t str
 
 // Muon (flce_muon.cu).  Matrices of one shape form a group, [matrix][rows][pitch] in the workspace; a
 // call runs in rounds of as many groups and matrices as the kernels' arguments hold.
-constexpr int kMuonGroups = 12;
-constexpr int kMuonMatrices = 256;
+constexpr int kMuonGroups = 12, kMuonMatrices = 256;
+// Most calls of latency's kind have one or a few matrices: kernels whose arguments hold no more
+// take 1 KB where the others take 17 KB, which cost 2 us a launch to copy.
+constexpr int kMuonFewGroups = 2, kMuonFewMatrices = 16;
 constexpr int kMuonChunk = 8192;     // elements of one block of the momentum's pass
 constexpr int kMuonStrip = 4096;     // and of the passes between a tensor and X
 constexpr int kMuonExactRows = 128;  // up to this many rows or columns: pairs of fp16, steps on X X^T alone
@@ -460,13 +462,14 @@ struct MuonGroup {
   int tall;               // X has more rows than columns
   int lo_in, write_lo;    // add beta times out_lo's old values; write out_lo
 };
+template <int G>
 struct MuonArgs {
-  MuonGroup g[kMuonGroups];
+  MuonGroup g[G];
   int groups, tiles;
   uint64_t timeout_ns;
   int* status;
 };
-static_assert(sizeof(MuonArgs) <= 32764, "kernel argument limit");
+static_assert(sizeof(MuonArgs<kMuonGroups>) <= 32764, "kernel argument limit");
 // The steps of the matrices of at most kMuonExactRows rows, from X X^T to the product Q of all
 // steps' P, a block each.
 struct MuonChainGroup {
@@ -492,11 +495,12 @@ struct MuonSource {
   uint32_t flags;
   int vec;  // columns at a time that every tensor's rows allow: 4, 2 or 1
 };
+template <int N>
 struct MuonSources {
   // the first block of work of each source, and the number of blocks behind the last: apart from
   // the sources, so that a search stays within a few lines of the constant cache
-  uint32_t chunk0[kMuonMatrices + 1], strip0[kMuonMatrices + 1];
-  MuonSource s[kMuonMatrices];
+  uint32_t chunk0[N + 1], strip0[N + 1];
+  MuonSource s[N];
   int count;
   float mu, omm;  // momentum and 1 - momentum
   int nesterov;
@@ -506,7 +510,7 @@ struct MuonSources {
   int* status;
   int first;     // the momentum's pass clears the status word
 };
-static_assert(sizeof(MuonSources) <= 32764, "kernel argument limit");
+static_assert(sizeof(MuonSources<kMuonMatrices>) <= 32764, "kernel argument limit");
 // Where X goes: out (bf16), or w <- w decay - rate X on the weights.
 struct MuonTarget {
   const __half *hi, *lo;  // (lo may be null)
@@ -518,20 +522,26 @@ struct MuonTarget {
   uint32_t flags;
   int vec;
 };
+template <int N>
 struct MuonTargets {
-  uint32_t strip0[kMuonMatrices + 1];
-  MuonTarget t[kMuonMatrices];
+  uint32_t strip0[N + 1];
+  MuonTarget t[N];
   int count;
   int* status;
 };
-static_assert(sizeof(MuonTargets) <= 32764, "kernel argument limit");
+static_assert(sizeof(MuonTargets<kMuonMatrices>) <= 32764, "kernel argument limit");
 int64_t muon_strips(int64_t rows, int64_t cols, int vec);  // blocks of the scale's or the weights' launch for one matrix
-cudaError_t launch_muon_momentum(const MuonSources& a, cudaStream_t stream);
-cudaError_t launch_muon_scale(const MuonSources& a, int sms, cudaStream_t stream);
-cudaError_t launch_muon_weights(const MuonTargets& a, int sms, cudaStream_t stream);
+// N: kMuonMatrices or kMuonFewMatrices; G: kMuonGroups or kMuonFewGroups.
+template <int N>
+cudaError_t launch_muon_momentum(const MuonSources<N>& a, cudaStream_t stream);
+template <int N>
+cudaError_t launch_muon_scale(const MuonSources<N>& a, int sms, cudaStream_t stream);
+template <int N>
+cudaError_t launch_muon_weights(const MuonTargets<N>& a, int sms, cudaStream_t stream);
 cudaError_t launch_muon_chain(const MuonChain& a, cudaStream_t stream);
 // bn: columns of a tile, 256 or 128.
-cudaError_t launch_muon_product(int mode, int bn, const MuonArgs& a, int sms, cudaStream_t stream);
+template <int G>
+cudaError_t launch_muon_product(int mode, int bn, const MuonArgs<G>& a, int sms, cudaStream_t stream);
 
 // Limit of every bounded wait in the kernels, in nanoseconds: FLCE_TIMEOUT_NS
 // from the environment (read once), else 4 s.

@@ -120,8 +120,8 @@ struct Tile {
   int split;
 };
 
-template <int MODE, int BN>
-__device__ __forceinline__ bool find_tile(const MuonArgs& a, int t, uint32_t rank, Tile& o) {
+template <int MODE, int BN, int G>
+__device__ __forceinline__ bool find_tile(const MuonArgs<G>& a, int t, uint32_t rank, Tile& o) {
   if (t >= a.tiles) return false;
   int gi = 0;
   while (gi + 1 < a.groups && a.g[gi + 1].tile0 <= t) ++gi;
@@ -172,15 +172,16 @@ struct Bars {
   volatile int* abort_flag;
 };
 
-__device__ __forceinline__ void record_timeout(const MuonArgs& a, uint32_t rank, volatile int* abort_flag) {
+template <int G>
+__device__ __forceinline__ void record_timeout(const MuonArgs<G>& a, uint32_t rank, volatile int* abort_flag) {
   *abort_flag = 1;
   st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1u);
   atomicCAS(a.status, 0, kErrTimeout);
 }
 
 // Inner coordinates are multiples of 64 elements: every copy starts on a 128-byte boundary.
-template <int MODE, int BN>
-__device__ void run_producer(const MuonArgs& a, uint32_t rank, int pair, int pairs, uint8_t* smem, const Bars& b) {
+template <int MODE, int BN, int G>
+__device__ void run_producer(const MuonArgs<G>& a, uint32_t rank, int pair, int pairs, uint8_t* smem, const Bars& b) {
   using S = Shape<BN>;
   const uint32_t full_even = mapa_shared(smem_u32(b.full), 0);
   const int bhalf = static_cast<int>(rank) * S::kHalfN;
@@ -227,8 +228,8 @@ __device__ void run_producer(const MuonArgs& a, uint32_t rank, int pair, int pai
   }
 }
 
-template <int MODE, int BN>
-__device__ void run_mma(const MuonArgs& a, int pair, int pairs, uint8_t* smem, uint32_t tmem_base, const Bars& b) {
+template <int MODE, int BN, int G>
+__device__ void run_mma(const MuonArgs<G>& a, int pair, int pairs, uint8_t* smem, uint32_t tmem_base, const Bars& b) {
   using S = Shape<BN>;
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
@@ -289,8 +290,8 @@ __device__ __forceinline__ void stage_and_store(const CUtensorMap* map, uint8_t*
   }
 }
 
-template <int MODE, int BN>
-__device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pairs, uint8_t* staging,
+template <int MODE, int BN, int G>
+__device__ void run_epilogue(const MuonArgs<G>& a, uint32_t rank, int pair, int pairs, uint8_t* staging,
                              uint32_t tmem_base, const Bars& b) {
   constexpr int kCols = BN / 2;  // of a warp
   const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
@@ -410,9 +411,9 @@ __device__ void run_epilogue(const MuonArgs& a, uint32_t rank, int pair, int pai
   __syncwarp();
 }
 
-template <int MODE, int BN>
+template <int MODE, int BN, int G>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
-    muon_product_kernel(const __grid_constant__ MuonArgs a) {
+    muon_product_kernel(const __grid_constant__ MuonArgs<G> a) {
   using S = Shape<BN>;
   constexpr uint32_t kTmemCols = 2 * BN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -448,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       tma_prefetch_map(&t.g->a64);
       tma_prefetch_map(&t.g->b128);
       tma_prefetch_map(&t.g->b64);
-      tma_prefetch_map(&t.g->out);
+      if (!t.g->part) tma_prefetch_map(&t.g->out);
       if (t.g->write_lo || t.g->lo_in) tma_prefetch_map(&t.g->out_lo);
     }
   }
@@ -788,12 +789,14 @@ struct Momentum {
   // u, from the gradient and the momentum that has moved
   __device__ __forceinline__ float u(float m, float g) const { return nesterov ? m * mu + g * gs * omm : m; }
 };
-__device__ __forceinline__ Momentum momentum_of(const MuonSources& a) {
+template <int N>
+__device__ __forceinline__ Momentum momentum_of(const MuonSources<N>& a) {
   return Momentum{a.mu, a.omm, a.grad_scale ? *a.grad_scale : 1.f, a.nesterov};
 }
 
 // One chunk of kMuonChunk elements: the momentum moves, and the squares of u are added up.
-__global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __grid_constant__ MuonSources a) {
+template <int N>
+__global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __grid_constant__ MuonSources<N> a) {
   griddep_begin();
   const uint32_t c = blockIdx.x;
   if (c == 0 && threadIdx.x == 0 && a.first) *a.status = kOk;
@@ -897,8 +900,8 @@ __device__ __forceinline__ void store_h(__half* p, const float (&x)[V]) {
 }
 
 // X = u / (|u| + eps) as a pair of fp16.
-template <int V>
-__device__ __forceinline__ void scale_strip(const MuonSources& a, const MuonSource& s, uint32_t k0, const Momentum& mo,
+template <int V, int N>
+__device__ __forceinline__ void scale_strip(const MuonSources<N>& a, const MuonSource& s, uint32_t k0, const Momentum& mo,
                                             float inv) {
   constexpr int kRows = 16 / V;
   constexpr int kBatch = kRows < 8 ? kRows : 8;
@@ -936,7 +939,8 @@ __device__ __forceinline__ void scale_strip(const MuonSources& a, const MuonSour
 
 // 1 / (|u| + eps), times X's scale.  A sum of squares past fp32's range, or a non-finite element,
 // makes the whole matrix NaN.
-__device__ __forceinline__ float norm_factor(const MuonSources& a, int si, float* red) {
+template <int N>
+__device__ __forceinline__ float norm_factor(const MuonSources<N>& a, int si, float* red) {
   float sum = 0.f;
   for (uint32_t i = a.chunk0[si] + threadIdx.x; i < a.chunk0[si + 1]; i += kNormThreads) sum += a.part[i];
 #pragma unroll
@@ -952,7 +956,8 @@ __device__ __forceinline__ float norm_factor(const MuonSources& a, int si, float
 
 // Blocks take runs of consecutive strips, from the last source to the first: what the momentum's
 // pass left in L2 is read first.
-__global__ void __launch_bounds__(kNormThreads, 5) muon_scale_kernel(const __grid_constant__ MuonSources a, uint32_t run) {
+template <int N>
+__global__ void __launch_bounds__(kNormThreads, 5) muon_scale_kernel(const __grid_constant__ MuonSources<N> a, uint32_t run) {
   griddep_begin();
   __shared__ float red[kNormThreads / 32];
   const uint32_t begin = (gridDim.x - 1 - blockIdx.x) * run, end = min(begin + run, a.strip0[a.count]);
@@ -1010,7 +1015,8 @@ __device__ __forceinline__ void weights_strip(const MuonTarget& s, uint32_t k0, 
 }
 
 // X to out as bf16, or taken off the weights.
-__global__ void __launch_bounds__(kNormThreads, 4) muon_weights_kernel(const __grid_constant__ MuonTargets a, uint32_t run) {
+template <int N>
+__global__ void __launch_bounds__(kNormThreads, 4) muon_weights_kernel(const __grid_constant__ MuonTargets<N> a, uint32_t run) {
   griddep_begin();
   const uint32_t begin = blockIdx.x * run, end = min(begin + run, a.strip0[a.count]);
   if (begin >= end) return;
@@ -1032,20 +1038,20 @@ uint32_t run_length(uint32_t strips, int sms, int blocks) {
   return std::max<uint32_t>(1, strips / static_cast<uint32_t>(sms * blocks));
 }
 
-template <int MODE, int BN>
-cudaError_t launch_mode(const MuonArgs& a, int sms, cudaStream_t s) {
+template <int MODE, int BN, int G>
+cudaError_t launch_mode(const MuonArgs<G>& a, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(muon_product_kernel<MODE, BN>, Shape<BN>::kSmemBytes, done);
+  cudaError_t e = allow_smem(muon_product_kernel<MODE, BN, G>, Shape<BN>::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_k(muon_product_kernel<MODE, BN>, dim3(pair_grid(sms, a.tiles)), dim3(kProductThreads),
+  return launch_k(muon_product_kernel<MODE, BN, G>, dim3(pair_grid(sms, a.tiles)), dim3(kProductThreads),
                   Shape<BN>::kSmemBytes, s, a);
 }
 
-template <int BN>
-cudaError_t launch_width(int mode, const MuonArgs& a, int sms, cudaStream_t s) {
-  return mode == kMuonGram   ? launch_mode<kMuonGram, BN>(a, sms, s)
-         : mode == kMuonPoly ? launch_mode<kMuonPoly, BN>(a, sms, s)
-                             : launch_mode<kMuonApply, BN>(a, sms, s);
+template <int BN, int G>
+cudaError_t launch_width(int mode, const MuonArgs<G>& a, int sms, cudaStream_t s) {
+  return mode == kMuonGram   ? launch_mode<kMuonGram, BN, G>(a, sms, s)
+         : mode == kMuonPoly ? launch_mode<kMuonPoly, BN, G>(a, sms, s)
+                             : launch_mode<kMuonApply, BN, G>(a, sms, s);
 }
 
 }  // namespace
@@ -1056,22 +1062,34 @@ cudaError_t launch_muon_chain(const MuonChain& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_k(muon_chain_kernel, dim3(a.blocks), dim3(kChainThreads), kChainSmem, s, a);
 }
-cudaError_t launch_muon_momentum(const MuonSources& a, cudaStream_t s) {
-  return launch_k(muon_momentum_kernel, dim3(a.chunk0[a.count]), dim3(kNormThreads), 0, s, a);
+template <int N>
+cudaError_t launch_muon_momentum(const MuonSources<N>& a, cudaStream_t s) {
+  return launch_k(muon_momentum_kernel<N>, dim3(a.chunk0[a.count]), dim3(kNormThreads), 0, s, a);
 }
-cudaError_t launch_muon_scale(const MuonSources& a, int sms, cudaStream_t s) {
+template <int N>
+cudaError_t launch_muon_scale(const MuonSources<N>& a, int sms, cudaStream_t s) {
   const uint32_t n = a.strip0[a.count], run = run_length(n, sms, 32);
-  return launch_k(muon_scale_kernel, dim3((n + run - 1) / run), dim3(kNormThreads), 0, s, a, run);
+  return launch_k(muon_scale_kernel<N>, dim3((n + run - 1) / run), dim3(kNormThreads), 0, s, a, run);
 }
-cudaError_t launch_muon_weights(const MuonTargets& a, int sms, cudaStream_t s) {
+template <int N>
+cudaError_t launch_muon_weights(const MuonTargets<N>& a, int sms, cudaStream_t s) {
   const uint32_t n = a.strip0[a.count], run = run_length(n, sms, 64);
-  return launch_k(muon_weights_kernel, dim3((n + run - 1) / run), dim3(kNormThreads), 0, s, a, run);
+  return launch_k(muon_weights_kernel<N>, dim3((n + run - 1) / run), dim3(kNormThreads), 0, s, a, run);
 }
+template cudaError_t launch_muon_momentum<kMuonFewMatrices>(const MuonSources<kMuonFewMatrices>&, cudaStream_t);
+template cudaError_t launch_muon_momentum<kMuonMatrices>(const MuonSources<kMuonMatrices>&, cudaStream_t);
+template cudaError_t launch_muon_scale<kMuonFewMatrices>(const MuonSources<kMuonFewMatrices>&, int, cudaStream_t);
+template cudaError_t launch_muon_scale<kMuonMatrices>(const MuonSources<kMuonMatrices>&, int, cudaStream_t);
+template cudaError_t launch_muon_weights<kMuonFewMatrices>(const MuonTargets<kMuonFewMatrices>&, int, cudaStream_t);
+template cudaError_t launch_muon_weights<kMuonMatrices>(const MuonTargets<kMuonMatrices>&, int, cudaStream_t);
 int64_t muon_strips(int64_t rows, int64_t cols, int vec) {
   return (rows * vec + 127) / 128 * ((cols + 32 * vec - 1) / (32 * vec));
 }
-cudaError_t launch_muon_product(int mode, int bn, const MuonArgs& a, int sms, cudaStream_t s) {
-  return bn == 256 ? launch_width<256>(mode, a, sms, s) : launch_width<128>(mode, a, sms, s);
+template <int G>
+cudaError_t launch_muon_product(int mode, int bn, const MuonArgs<G>& a, int sms, cudaStream_t s) {
+  return bn == 256 ? launch_width<256, G>(mode, a, sms, s) : launch_width<128, G>(mode, a, sms, s);
 }
+template cudaError_t launch_muon_product<kMuonFewGroups>(int, int, const MuonArgs<kMuonFewGroups>&, int, cudaStream_t);
+template cudaError_t launch_muon_product<kMuonGroups>(int, int, const MuonArgs<kMuonGroups>&, int, cudaStream_t);
 
 }  // namespace flce
