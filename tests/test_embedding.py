@@ -147,6 +147,25 @@ def test_forward_of_nothing_and_of_ids_outside():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [16383, 16384, 16385, 40000])
+def test_forward_finds_an_id_outside_wherever_it_stands(n):
+    w = torch.randn(50, 8, device="cuda")
+    ids = torch.randint(0, 50, (n,), device="cuda", dtype=torch.int32)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    y, _ = flce.embedding_forward(ids, w, ws=ws, check=True)
+    assert torch.equal(y, w[ids.long()])
+    for at in {0, min(16383, n - 1), min(16384, n - 1), n // 2, n - 1}:
+        bad = ids.clone()
+        bad[at] = 50
+        ws.fill_(255)
+        y, _ = flce.embedding_forward(bad, w, ws=ws)
+        assert flce.read_device_status(ws) == 5
+        want = w[ids.long()]
+        want[at] = 0
+        assert torch.equal(y, want)
+
+
+@pytest.mark.gpu
 def test_forward_of_offsets_beyond_32_bits():
     v, h = 70000, 40000  # 2.8e9 elements
     w = torch.empty(v, h, dtype=BF16, device="cuda")
