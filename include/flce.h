@@ -545,8 +545,8 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
  *   - matrices and tensors are HOST arrays, read before the call returns.
  *   - ws: the workspace size below (0 if an entry is invalid), 256-byte aligned,
  *     status word at its start: the operands of a round of matrices, about 10
- *     bytes an element (16 up to 128 rows), up to 4 GiB unless one matrix alone
- *     takes more. */
+ *     bytes an element (up to 128 rows: 8 to 16, and a 64 KB part for every 512
+ *     columns, 64 parts at most), up to 4 GiB unless one matrix alone takes more. */
 #define FLCE_MUON_MAX_STEPS 16
 
 typedef struct {
@@ -569,7 +569,7 @@ typedef struct {
 
 typedef struct {
   double momentum;      /* in [0, 1); of flce_muon_step */
-  double eps;           /* >= 1e-30 */
+  double eps;           /* >= 1e-15: squares of elements below 4e-23 add up to 0 in fp32 */
   const double* coefficients;  /* [steps][3]: a, b, c */
   int32_t steps;        /* 1 to FLCE_MUON_MAX_STEPS */
   int32_t nesterov;     /* 0 or 1; of flce_muon_step */

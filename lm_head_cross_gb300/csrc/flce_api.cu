@@ -1849,6 +1849,17 @@ struct MuonItem {
   int64_t c() const { return std::max(rows, cols); }
 };
 
+// Parts of X X^T of the exact ones, and the steps of a part's contraction, for c columns.
+int64_t muon_split_blocks(int64_t c) {
+  const int64_t all = (c + kBK - 1) / kBK;
+  return std::max<int64_t>(kMuonSplitBlocks, (all + kMuonSplitsMost - 1) / kMuonSplitsMost);
+}
+int64_t muon_splits(int64_t c) { return ((c + kBK - 1) / kBK + muon_split_blocks(c) - 1) / muon_split_blocks(c); }
+
+size_t muon_part_bytes(int64_t c) {
+  return sizeof(float) * static_cast<size_t>(muon_splits(c)) * kMuonExactRows * kMuonExactRows;
+}
+
 // Groups of one round and where their buffers lie: X (two: a product reads one and writes the
 // other) with what rounding left of it, A and P.
 struct MuonPlanGroup {
@@ -1860,12 +1871,8 @@ struct MuonPlanGroup {
   bool exact() const { return r() <= kMuonExactRows; }
   int64_t xp() const { return (cols + 7) / 8 * 8; }
   int64_t ap() const { return (r() + 7) / 8 * 8; }
-  // parts of X X^T of the exact ones
-  int64_t split_blocks() const {
-    const int64_t all = (c() + kBK - 1) / kBK;
-    return std::max<int64_t>(kMuonSplitBlocks, (all + kMuonSplitsMost - 1) / kMuonSplitsMost);
-  }
-  int64_t splits() const { return ((c() + kBK - 1) / kBK + split_blocks() - 1) / split_blocks(); }
+  int64_t split_blocks() const { return muon_split_blocks(c()); }
+  int64_t splits() const { return muon_splits(c()); }
   size_t x[2], xlo[2], a, p, plo, diag, part;
 };
 struct MuonRound {
@@ -1884,7 +1891,7 @@ size_t muon_matrix_bytes(int64_t rows, int64_t cols) {
   const int64_t r = std::min(rows, cols);
   const size_t x = 2 * static_cast<size_t>(rows) * static_cast<size_t>((cols + 7) / 8 * 8);
   const size_t a = 2 * static_cast<size_t>(r) * static_cast<size_t>((r + 7) / 8 * 8);
-  return r <= kMuonExactRows ? 4 * x + 2 * a + 65536 : 3 * x + 2 * a;  // (and more parts: they grow slower than x)
+  return r <= kMuonExactRows ? 4 * x + 2 * a + muon_part_bytes(std::max(rows, cols)) : 3 * x + 2 * a;
 }
 
 constexpr size_t kMuonRoundBytes = size_t{4} << 30;  // of a round of several matrices
@@ -1942,7 +1949,7 @@ std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
       g.a = g.exact() ? 0 : take(ab);
       g.diag = g.exact() ? 0 : take(sizeof(float) * count * static_cast<size_t>(g.r()));
       g.plo = g.exact() ? take(ab) : 0;
-      g.part = g.exact() ? take(sizeof(float) * count * static_cast<size_t>(g.splits()) * kMuonExactRows * kMuonExactRows) : 0;
+      g.part = g.exact() ? take(count * muon_part_bytes(g.c())) : 0;
     }
     r.total = off;
   }
@@ -2262,9 +2269,11 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
   return FLCE_OK;
 }
 
+// eps: squares of elements below 4e-23 are 0 in fp32, and of those X = u / eps: matrices of up to
+// 2^40 elements, the most there are, then stay below a norm of 0.04.
 bool muon_options_ok(const flce_muon_t* o) {
   return o && o->coefficients && o->momentum >= 0.0 && o->momentum < 1.0 && (o->nesterov == 0 || o->nesterov == 1) && o->steps >= 1 &&
-         o->steps <= FLCE_MUON_MAX_STEPS && o->eps >= 1e-30 && std::isfinite(o->eps);
+         o->steps <= FLCE_MUON_MAX_STEPS && o->eps >= 1e-15 && std::isfinite(o->eps);
 }
 
 flce_status_t muon_items(const flce_matrix_t* x, int32_t count, std::vector<MuonItem>* items) {

@@ -202,6 +202,27 @@ def test_workspace_size_rules():
     assert workspace(*((200 + i, 300) for i in range(12))) >= workspace(*((200 + i, 300) for i in range(11)))
 
 
+def test_workspace_of_long_thin_matrices():
+    """Their parts of X X^T count towards a round's size."""
+    assert workspace(*[(1, 1 << 22)] * 300) <= (4 << 30) + (1 << 20)
+    assert workspace((2, 1 << 24)) >= 8 * 2 * (1 << 24) + 64 * 65536
+
+
+def test_eps_that_fp32_squares_pass_by_is_refused():
+    assert ortho(o=options(eps=9e-16)) == 1 and ortho(o=options(eps=1.1e-15)) == 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [1e-21, 1e-24, 1e-38])
+def test_elements_whose_squares_are_lost(size):
+    """Each X is u / eps or nearly so.  fp16 ends at 2^-24 / 2^14 = 2^-38: half of that an element."""
+    x = torch.randn(100, 200, device="cuda") * size
+    for y in (x, x.repeat(2, 1)):
+        got = flce.orthogonalize(y, steps=1, eps=1e-15).double()
+        near = exact(y.cpu(), steps=1, eps=1e-15).to(got)
+        assert (got - near).norm() <= 2.0 ** -6 * near.norm() + 3.4445 * 2.0 ** -39 * x.numel() ** 0.5 * 2
+
+
 def test_python_refuses_on_cpu():
     for x in (torch.zeros(4, 4), [torch.zeros(4, 4)], torch.zeros(4)):
         with pytest.raises(ValueError):
