@@ -750,6 +750,14 @@ def _allocating(stream):
     return _NO_CONTEXT if stream is None else _torch().cuda.stream(stream)
 
 
+def _record(stream, *tensors):
+    """What is freed after the call is reused only once ``stream`` is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _norm(x, weight, bias, eps):
     if x.dim() != 2 or weight.dim() != 1:
         raise ValueError(f"x must be [N, H] and weight [H], got {tuple(x.shape)} and {tuple(weight.shape)}")
@@ -877,6 +885,7 @@ def embedding_forward(ids, weight, scale=1.0, ws=None, stream=None, check=False)
     _call("flce_embedding_forward", lib().flce_embedding_forward(
         ctypes.byref(q), ids.data_ptr(), weight.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel(),
         _stream_ptr(stream, device)))
+    _record(stream, ids, weight, ws)
     if check:
         _call("device", read_device_status(ws, stream))
     return y, ws
@@ -895,6 +904,8 @@ def embedding_backward(dy, ids, v, scale=1.0, padding_idx=None, add_to=None, dty
     torch = _torch()
     _check_ids(ids)
     n, v = ids.numel(), int(v)
+    if padding_idx is not None and padding_idx < 0:
+        raise ValueError(f"padding_idx must be None or in [0, {v}), got {padding_idx}")
     if dy.dim() != 2 or dy.shape[0] != n or not dy.is_cuda or not dy.is_contiguous():
         raise ValueError(f"dy must be a contiguous CUDA tensor [N, H] for ids [N], got {tuple(dy.shape)}")
     h = dy.shape[1]
@@ -916,6 +927,7 @@ def embedding_backward(dy, ids, v, scale=1.0, padding_idx=None, add_to=None, dty
     _call("flce_embedding_backward", lib().flce_embedding_backward(
         ctypes.byref(q), dy.data_ptr(), ids.data_ptr(), dw.data_ptr(), int(add_to is not None), ws.data_ptr(),
         ws.numel(), _stream_ptr(stream, device)))
+    _record(stream, dy, ids, add_to, ws)
     if add_to is not None:  # autograd learns of the write
         torch.autograd.graph.increment_version([add_to])
     if check:
@@ -959,6 +971,8 @@ def embedding(ids, weight, scale: float = 1.0, padding_idx=None):
     v = weight.shape[0]
     if padding_idx is not None and not 0 <= padding_idx < v:
         raise ValueError(f"padding_idx must be in [0, {v}), got {padding_idx}")
+    if ids.dtype not in (torch.int32, torch.int64, torch.int16, torch.int8, torch.uint8):
+        raise TypeError(f"ids must be integers, got {ids.dtype}")
     flat = ids.reshape(-1)
     if flat.dtype is torch.int64:  # those beyond 32 bits stay outside
         flat = flat.clamp(-1, v)

@@ -11,7 +11,7 @@ import ctypes
 import math
 
 from .binding import (FlceError, Matrix, MuonOptions, MuonTensor, _allocating, _call, _check_device, _dtype,
-                      _stream_ptr, _torch, lib, read_device_status)
+                      _record, _stream_ptr, _torch, lib, read_device_status)
 from .optim import _check
 
 #: Newton-Schulz coefficients (a, b, c) of X <- a X + (b X X^T + c (X X^T)^2) X, for every step
@@ -75,6 +75,7 @@ def orthogonalize(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, ws=
             ws = torch.empty(nbytes, dtype=torch.uint8, device=xs[0].device)
     _call("flce_orthogonalize", lib().flce_orthogonalize(table, len(rows), ctypes.byref(options), ws.data_ptr(),
                                                          ws.numel(), _stream_ptr(stream, device)))
+    _record(stream, *xs, *outs, ws)
     given = [o for o in (out if listed else [out]) if o is not None] if out is not None else []
     if given:  # autograd learns of the writes
         torch.autograd.graph.increment_version(given)
@@ -214,14 +215,11 @@ def muon_step(plan, grads, grad_scale=None, ws=None, stream=None, check=False):
     _call("flce_muon_step", lib().flce_muon_step(
         table, len(plan), ctypes.byref(plan.options), None if grad_scale is None else grad_scale.data_ptr(),
         ws.data_ptr(), ws.numel(), _stream_ptr(stream, device)))
-    if stream is not None:  # what is freed after the call is reused only once the stream is done with it
-        used = [*grads, grad_scale]
+    if stream is not None:
+        _record(stream, *grads, grad_scale, ws)
         if stream.cuda_stream not in plan._recorded:
-            used += [t for held in plan._held for t in held]
+            _record(stream, *(t for held in plan._held for t in held))
             plan._recorded.add(stream.cuda_stream)
-        for t in used:
-            if t is not None:
-                t.record_stream(stream)
     # autograd learns of the writes: a graph that saved the old weights refuses its backward pass
     params, _, masters = plan._held
     torch.autograd.graph.increment_version(

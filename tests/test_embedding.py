@@ -110,6 +110,23 @@ def test_python_refuses_on_cpu():
         flce.embedding_backward(torch.zeros(4, 8), ids, 10)
 
 
+def test_ids_that_are_no_integers_are_refused():
+    """(Converted, 1.9 would be row 1, and an unsigned 2^32 + 1 too.)"""
+    for dtype in (F32, BF16, torch.bool, torch.uint64):
+        with pytest.raises(TypeError, match="integers"):
+            flce.embedding(torch.zeros(4).to(dtype), torch.zeros(10, 8))
+
+
+def test_a_padding_id_from_the_end_is_refused():
+    class Device(torch.Tensor):
+        __torch_function__ = torch._C._disabled_torch_function_impl
+        is_cuda = True
+
+    ids, dy = torch.zeros(4, dtype=torch.int32).as_subclass(Device), torch.zeros(4, 8).as_subclass(Device)
+    with pytest.raises(ValueError, match="padding_idx"):
+        flce.embedding_backward(dy, ids, 10, padding_idx=-1)
+
+
 # ----------------------------------------------------------------------------- forward
 
 

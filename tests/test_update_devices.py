@@ -1,13 +1,15 @@
 """The embedding's and Muon's calls run on the current device alone, like the others around the
 head: tensors or a stream of another one are refused on the host (stand-ins as in
 test_ops_devices)."""
+import contextlib
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import lm_head_cross_gb300 as flce  # noqa: E402
 from lm_head_cross_gb300 import binding, muon  # noqa: E402
-from test_ops_devices import BF16, I32, H, N, Stream, V, on  # noqa: E402
+from test_ops_devices import BF16, F32, I32, H, N, On, Stream, V, on  # noqa: E402
 
 U8 = torch.uint8
 
@@ -77,6 +79,42 @@ def test_the_current_device_is_taken(current, monkeypatch, call):
         monkeypatch.setattr(mod, "lib", reached)
     with pytest.raises(KeyError):
         call(lambda which: 0, None)()
+
+
+class Recorded(On):
+    """One that keeps the streams its memory is recorded on."""
+
+    def record_stream(self, stream):
+        self.__dict__.setdefault("streams", []).append(stream)
+
+
+def recorded(*shape, dtype=F32):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(Recorded)
+    t.index = 0
+    return t
+
+
+@pytest.mark.parametrize("stream", [None, Stream(0)], ids=["current", "given"])
+def test_a_given_stream_is_recorded_on_what_it_uses(current, monkeypatch, stream):
+    """What is freed after a call on another stream than its own must not be reused before its end."""
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    for mod in (binding, muon):
+        monkeypatch.setattr(mod, "lib", Library)
+        monkeypatch.setattr(mod, "_allocating", lambda s: contextlib.nullcontext())
+    ids, w, dy, dw, ws, x, y, g, m, p, gs = used = [
+        recorded(N, dtype=I32), recorded(V, H), recorded(N, H), recorded(V, H), recorded(256, dtype=U8), recorded(H, H),
+        recorded(H, H, dtype=BF16), *(recorded(H, H) for _ in range(3)), recorded(1)]
+    new = flce.embedding_forward(ids, w, ws=ws, stream=stream)[0]
+    flce.embedding_backward(dy, ids, V, add_to=dw, ws=ws, stream=stream)
+    flce.orthogonalize([x], out=[y], ws=ws, stream=stream)
+    flce.muon_step(flce.muon_plan([p], [m]), [g], grad_scale=gs, ws=ws, stream=stream)
+    for t in used:
+        assert bool(getattr(t, "streams", None)) == (stream is not None)
+        assert all(s is stream for s in getattr(t, "streams", []))
+    assert not hasattr(new, "streams")  # (allocated on it)
 
 
 def test_gradients_of_another_device_are_refused(current):
