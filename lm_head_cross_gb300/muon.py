@@ -19,6 +19,14 @@ COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 MAX_STEPS = 16
 
 
+def _distinct(names, tensors):
+    """A call writes each of its tensors: none may be there twice."""
+    seen = {}
+    for name, t in zip(names, tensors):
+        if t is not None and t.numel() and seen.setdefault(t.data_ptr(), name) != name:
+            raise ValueError(f"{name} and {seen[t.data_ptr()]} are the same memory")
+
+
 def _options(momentum, nesterov, steps, coefficients, eps):
     """MuonOptions, which keeps its coefficients alive."""
     steps = int(steps)
@@ -38,7 +46,8 @@ def orthogonalize(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, ws=
 
     x: [..., R, C], or a list of matrices [R, C] of any shapes; bf16 or fp32, contiguous CUDA.
     out: where to write (bf16, shaped like x; may be x itself), else it is allocated.
-    coefficients: (a, b, c), or a list of them for the steps.  Returns out."""
+    coefficients: (a, b, c), or a list of them for the steps.  Returns out, without a
+    gradient.  stream: the torch stream to run on, else the current one."""
     torch = _torch()
     listed = isinstance(x, (list, tuple))
     xs = list(x) if listed else [x]
@@ -56,6 +65,8 @@ def orthogonalize(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, ws=
         if o is not None and (o.shape != t.shape or o.dtype is not torch.bfloat16 or not o.is_contiguous()
                               or not o.is_cuda):
             raise ValueError("out must be contiguous bf16 CUDA tensors shaped like x")
+    if out is not None:
+        _distinct([f"out[{i}]" for i in range(len(outs))], outs)
     device = _check_device(xs[0], stream, *xs[1:], *outs, ws)
     options = _options(0.0, False, steps, coefficients, eps)
     with _allocating(stream):
@@ -125,6 +136,8 @@ class MuonPlan:
             self.table[i] = MuonTensor(p.data_ptr(), None, None if masters[i] is None else masters[i].data_ptr(),
                                        momenta[i].data_ptr(), rows, cols, 0.0, 0.0, shape_factor(rows, cols, adjust),
                                        _dtype(p, f"params[{i}]"), 0)
+        _distinct([f"{name}[{i}]" for name in ("params", "momenta", "masters") for i in range(n)],
+                  [*params, *momenta, *masters])
         self._held = (list(params), list(momenta), list(masters))  # the table holds their addresses
         self._recorded = set()  # streams that _held's memory is known to be used on
         self._bytes = {}        # workspace size by which parameters have a gradient
@@ -170,6 +183,8 @@ class MuonPlan:
             nbytes = int(lib().flce_muon_workspace_bytes(table, len(self)))
             if nbytes == 0:
                 raise FlceError(2, "flce_muon_workspace_bytes")
+            if len(self._bytes) >= 64:  # (experts that come and go)
+                self._bytes.clear()
             self._bytes[key] = nbytes
         return self._bytes[key]
 
@@ -244,6 +259,9 @@ class Muon:
         torch = _torch()
         params = list(params)
         groups = params if params and isinstance(params[0], dict) else [{"params": params}]
+        for g in groups:
+            if not {"params"} <= set(g) <= {"params", "lr", "weight_decay"}:
+                raise ValueError(f"a group is params, lr and weight_decay, got {sorted(g)}")
         self.groups = [{"lr": lr, "weight_decay": weight_decay, **g, "params": list(g["params"])} for g in groups]
         self.params = [p for g in self.groups for p in g["params"]]
         if len({id(p) for p in self.params}) != len(self.params):

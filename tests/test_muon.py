@@ -240,6 +240,41 @@ def test_python_refuses_on_cpu():
     assert muon.shape_factor(4, 16, "match_rms_adamw") == 0.8
 
 
+class Device(torch.Tensor):
+    """A CPU tensor that says it is on a GPU."""
+    __torch_function__ = torch._C._disabled_torch_function_impl
+    is_cuda = True
+
+
+def test_memory_that_is_written_twice_is_refused():
+    a, b, c = (torch.zeros(4, 6).as_subclass(Device) for _ in range(3))
+    for lists in (([a, a], [b, c]), ([a, c], [b, b]), ([a], [a]), ([a], [b], [a]), ([a], [b], [b])):
+        with pytest.raises(ValueError, match="same memory"):
+            flce.muon_plan(*lists)
+    flce.muon_plan([a], [b], [c])
+    empty = [torch.zeros(0, 6).as_subclass(Device) for _ in range(4)]
+    flce.muon_plan(empty[:2], empty[2:])
+    y = torch.zeros(4, 6, dtype=BF16).as_subclass(Device)
+    with pytest.raises(ValueError, match="same memory"):
+        flce.orthogonalize([a, b], out=[y, y])
+
+
+def test_a_group_of_other_options_is_refused():
+    for group in ({"params": [], "momentum": 0.9}, {"lr": 0.1}):
+        with pytest.raises(ValueError, match="group"):
+            flce.Muon([group])
+
+
+def test_sizes_of_many_sets_of_gradients_are_not_kept():
+    plan = flce.muon_plan(*([torch.zeros(2, 3).as_subclass(Device) for _ in range(8)] for _ in range(2)))
+    want = {}
+    for k in range(1, 256):
+        live = [bool(k >> i & 1) for i in range(8)]
+        want[k] = plan.workspace_bytes(live)
+        assert len(plan._bytes) <= 64
+    assert want[1] == plan.workspace_bytes([True] + 7 * [False]) and want[255] == plan.workspace_bytes()
+
+
 # ----------------------------------------------------------------------------- orthogonalize
 
 
