@@ -532,15 +532,15 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
  *     fp32; rounding leaves about 1e-3 of X's norm, less than bf16's own (up to
  *     6e-3 where most singular values are equal, so that all roundings agree).
  *     Matrices of at most 128 rows or columns carry 22 bits (1e-4 of X's norm, up
- *     to 2e-3 where strong directions outweigh weak ones 1000 to 1).  Momentum,
- *     norm and the weights' update are fp32.
+ *     to 2e-3 where strong directions outweigh weak ones 1000 to 1, or with 2^24
+ *     columns).  Momentum, norm and the weights' update are fp32.
  *   - The coefficients must keep singular values in [0, 1] within 1.95 at every
  *     step, and c must be 0 or |b| <= 6 |c| (FLCE_ERR_INVALID_ARGUMENT otherwise).
  *   - A matrix of zeros becomes zeros.  One with a non-finite element, or whose
  *     squares sum past fp32's range, becomes NaN as a whole, no other does.
  *   - Matrices are dense row-major, any number of rows and columns (the smaller
- *     up to 65536, the larger up to 2^24; empty ones are skipped).  Pointers need the
- *     alignment of their type.  Outputs must not overlap one another or inputs
+ *     up to 65536, the larger up to 2^20, or 2^24 where the smaller is at most 128;
+ *     empty ones are skipped).  Pointers need the alignment of their type.  Outputs must not overlap one another or inputs
  *     (but out may be x where x is bf16).  Tensors are updated in place.
  *   - matrices and tensors are HOST arrays, read before the call returns.
  *   - ws: the workspace size below (0 if an entry is invalid), 256-byte aligned,

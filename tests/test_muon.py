@@ -240,6 +240,27 @@ def test_python_refuses_on_cpu():
     assert muon.shape_factor(4, 16, "match_rms_adamw") == 0.8
 
 
+def test_longer_sums_than_the_accumulator_holds_are_refused():
+    for rows, cols, code in ((129, (1 << 20) + 1, 2), ((1 << 20) + 1, 129, 2), (129, 1 << 20, 4), (128, 1 << 24, 4),
+                             (1 << 24, 128, 4), ((1 << 24) + 1, 128, 2)):
+        assert ortho((0x1000, 0x2000, rows, cols, 0)) == code, (rows, cols)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(2100, 1 << 20), (128, 1 << 24), (1 << 24, 128)])
+def test_offsets_beyond_32_bits(rows, cols):
+    """A matrix beside itself n times: its singular vectors, n times over, so X's blocks / sqrt(n)."""
+    r, n = min(rows, cols), max(rows, cols) // 4096
+    x = torch.randn(r, 4096, device="cuda").bfloat16()
+    near = exact(x) / n ** 0.5
+    big = x.repeat(1, n) if rows < cols else x.t().contiguous().repeat(n, 1)
+    got = flce.orthogonalize(big, out=big)
+    blocks = [got[:, k:k + 4096] if rows < cols else got[k:k + 4096].t() for k in (0, 4096, n // 2 * 4096, 4096 * (n - 1))]
+    for b in blocks:
+        assert torch.equal(b, blocks[0])
+        assert (b.double() - near).norm() <= 2.0 ** -6 * near.norm()
+
+
 class Device(torch.Tensor):
     """A CPU tensor that says it is on a GPU."""
     __torch_function__ = torch._C._disabled_torch_function_impl
