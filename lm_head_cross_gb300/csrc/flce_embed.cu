@@ -36,12 +36,13 @@ constexpr uint32_t kFull = 0xffffffffu;
 // alignment, a fifth of what shifting the words of unaligned 16-byte chunks into place takes.
 constexpr int kCols = 256;
 
-template <bool ALIGNED>
+//   LANES: of a row's group of columns, 32 but where the forward pass has several rows in a warp.
+template <bool ALIGNED, int LANES = 32>
 struct Place {
   int c;  // the lane's first column
-  __device__ __forceinline__ Place(int group, int lane) : c(group * kCols + (ALIGNED ? lane * 8 : lane)) {}
-  __device__ __forceinline__ bool in(int e, int h) const { return ALIGNED ? c < h : c + 32 * e < h; }
-  __device__ __forceinline__ int col(int e) const { return c + (ALIGNED ? e : 32 * e); }
+  __device__ __forceinline__ Place(int group, int lane) : c(group * (8 * LANES) + (ALIGNED ? lane * 8 : lane)) {}
+  __device__ __forceinline__ bool in(int e, int h) const { return ALIGNED ? c < h : c + LANES * e < h; }
+  __device__ __forceinline__ int col(int e) const { return c + (ALIGNED ? e : LANES * e); }
 };
 
 // As they lie in memory: loads are issued together and their words taken apart after the last.
@@ -54,7 +55,8 @@ struct Words {
     for (int e = 0; e < (kPacked ? 4 : 8); ++e) u[e] = 0;
   }
   // elements outside the row are left as they are
-  __device__ __forceinline__ void load(const T* row, const Place<ALIGNED>& at, int h) {
+  template <int LANES>
+  __device__ __forceinline__ void load(const T* row, const Place<ALIGNED, LANES>& at, int h) {
     if (ALIGNED) {
       if (at.c >= h) return;
       const uint4* p = reinterpret_cast<const uint4*>(row + at.c);
@@ -79,8 +81,8 @@ struct Words {
   }
 };
 
-template <bool ALIGNED>
-__device__ __forceinline__ void store8(__nv_bfloat16* row, const Place<ALIGNED>& at, int h, const float (&x)[8]) {
+template <bool ALIGNED, int LANES>
+__device__ __forceinline__ void store8(__nv_bfloat16* row, const Place<ALIGNED, LANES>& at, int h, const float (&x)[8]) {
   if (ALIGNED) {
     if (at.c < h)
       __stcs(reinterpret_cast<uint4*>(row + at.c), make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
@@ -91,8 +93,8 @@ __device__ __forceinline__ void store8(__nv_bfloat16* row, const Place<ALIGNED>&
       if (at.in(e, h)) row[at.col(e)] = __float2bfloat16_rn(x[e]);
   }
 }
-template <bool ALIGNED>
-__device__ __forceinline__ void store8(float* row, const Place<ALIGNED>& at, int h, const float (&x)[8]) {
+template <bool ALIGNED, int LANES>
+__device__ __forceinline__ void store8(float* row, const Place<ALIGNED, LANES>& at, int h, const float (&x)[8]) {
   if (ALIGNED) {
     if (at.c < h) {
       __stcs(reinterpret_cast<float4*>(row + at.c), make_float4(x[0], x[1], x[2], x[3]));
@@ -113,10 +115,11 @@ constexpr int64_t kScanIds = 16384;  // of a block
 
 // Blocks below `scans` look the ids over, ahead of the rows so that none of it is left at the end:
 // one writes the status word, several (for many ids) record errors in a word that was cleared.  In
-// the others a warp takes kFwdUnits consecutive (row, 256 columns).
+// the others LANES threads take kFwdUnits consecutive (row, 8 LANES columns).
+//   Several rows in a warp where they are short: 131072 x 64 in 13 us for 18, 2^20 x 64 in 30 for 89.
 //   Times with one scanning block behind the rows, one ahead of them, and with these: 131072 x 512
 // in 55, 39, 38 us, 131072 x 64 in 31, 33, 18, 131072 x 4096 in 338, 317, 318; 20000 x 512 in 14, 12, 13.
-template <typename T, bool ALIGNED>
+template <typename T, bool ALIGNED, int LANES>
 __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, int h, int64_t v, float scale,
                                                                     const int32_t* __restrict__ ids,
                                                                     const T* __restrict__ w, T* __restrict__ y,
@@ -136,8 +139,8 @@ __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, i
     if (threadIdx.x == 0 && (bad || scans == 1)) *status = bad ? kErrLabel : kOk;
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x - scans) * (kFwdThreads / 32) + (threadIdx.x >> 5)) * kFwdUnits;
+  const int lane = threadIdx.x % LANES;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x - scans) * (kFwdThreads / LANES) + threadIdx.x / LANES) * kFwdUnits;
   int64_t row = first / groups;
   int group = static_cast<int>(first - row * groups);
   int64_t rows[kFwdUnits], id[kFwdUnits];
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, i
 #pragma unroll
   for (int k = 0; k < kFwdUnits; ++k) {
     x[k].zero();
-    if (id[k] >= 0 && id[k] < v) x[k].load(w + id[k] * h, Place<ALIGNED>(cols[k], lane), h);
+    if (id[k] >= 0 && id[k] < v) x[k].load(w + id[k] * h, Place<ALIGNED, LANES>(cols[k], lane), h);
   }
 #pragma unroll
   for (int k = 0; k < kFwdUnits; ++k) {
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, i
     float z[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = x[k].value(e) * scale;
-    store8<ALIGNED>(y + rows[k] * h, Place<ALIGNED>(cols[k], lane), h, z);
+    store8<ALIGNED, LANES>(y + rows[k] * h, Place<ALIGNED, LANES>(cols[k], lane), h, z);
   }
 }
 
@@ -677,11 +680,11 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 int groups_of(int h) { return (h + kCols - 1) / kCols; }
 
-template <typename T>
-cudaError_t forward_of(const EmbedParams& q, const int32_t* ids, const void* w, void* y, int* status, cudaStream_t s) {
+template <typename T, int LANES>
+cudaError_t forward_by(const EmbedParams& q, const int32_t* ids, const void* w, void* y, int* status, cudaStream_t s) {
   const bool al = q.h % 8 == 0 && aligned16(w) && aligned16(y);
-  const int groups = groups_of(q.h);
-  constexpr int kPerBlock = kFwdThreads / 32 * kFwdUnits;
+  const int groups = (q.h + 8 * LANES - 1) / (8 * LANES);
+  constexpr int kPerBlock = kFwdThreads / LANES * kFwdUnits;
   const int64_t scans = (q.n + kScanIds - 1) / kScanIds;
   const int64_t blocks = (q.n * groups + kPerBlock - 1) / kPerBlock + scans;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
@@ -689,9 +692,16 @@ cudaError_t forward_of(const EmbedParams& q, const int32_t* ids, const void* w, 
     const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), s);
     if (e != cudaSuccess) return e;
   }
-  auto* k = al ? embed_forward_kernel<T, true> : embed_forward_kernel<T, false>;
+  auto* k = al ? embed_forward_kernel<T, true, LANES> : embed_forward_kernel<T, false, LANES>;
   return launch_k(k, dim3(static_cast<unsigned>(blocks)), dim3(kFwdThreads), 0, s, q.n, q.h, q.v, q.scale, ids,
                   static_cast<const T*>(w), static_cast<T*>(y), groups, static_cast<int>(scans), status);
+}
+
+template <typename T>
+cudaError_t forward_of(const EmbedParams& q, const int32_t* ids, const void* w, void* y, int* status, cudaStream_t s) {
+  return q.h <= 64    ? forward_by<T, 8>(q, ids, w, y, status, s)
+         : q.h <= 128 ? forward_by<T, 16>(q, ids, w, y, status, s)
+                      : forward_by<T, 32>(q, ids, w, y, status, s);
 }
 
 template <typename T, typename TW, bool ALIGNED, bool ADD, int TILE>
