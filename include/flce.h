@@ -454,8 +454,8 @@ typedef struct {
 
 /* The forward pass needs 256 bytes of workspace (the status word), the backward
  * pass flce_embedding_workspace_bytes(q) (0 if q is invalid): the sorted tokens
- * (4 (v + 4 n) bytes), a table of 0.6 MB and two fp32 rows for each 32 of the
- * tokens (64, from 32768 tokens on). */
+ * (4 (v + 4 n) bytes), a table of 0.6 MB and two fp32 rows, of whole multiples of
+ * 256 elements, for each 32 of the tokens (64 where there are many). */
 flce_status_t flce_embedding_forward(const flce_embedding_t* q, const int32_t* ids, const void* W, void* y, void* ws,
                                      size_t ws_bytes, flce_stream_t stream);
 size_t flce_embedding_workspace_bytes(const flce_embedding_t* q);

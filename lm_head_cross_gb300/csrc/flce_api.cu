@@ -1739,13 +1739,13 @@ EmbedLayout embed_layout(const EmbedParams& q) {
   EmbedLayout L{};
   const size_t n = static_cast<size_t>(q.n);
   L.start = kAlign;  // after the status word
-  L.order = align_up(L.start + sizeof(int32_t) * (static_cast<size_t>(q.v) + 1));
+  L.order = align_up(L.start + sizeof(int32_t) * (static_cast<size_t>(embed_keys(q.n, q.v).count()) + 1));
   L.sorted_id = align_up(L.order + sizeof(int32_t) * n);
   L.tokens = align_up(L.sorted_id + sizeof(int32_t) * n);
   L.off = align_up(L.tokens + 2 * sizeof(int32_t) * n);
   L.bad = align_up(L.off + sizeof(int32_t) * (kEmbedRanges + 1) * kEmbedStretches);
   L.part = align_up(L.bad + sizeof(int32_t) * kEmbedStretches);
-  L.total = align_up(L.part + sizeof(float) * static_cast<size_t>(embed_part_floats(q.n, (int64_t{q.h} + 255) / 256 * 256)));
+  L.total = align_up(L.part + sizeof(float) * static_cast<size_t>(embed_part_floats(q.n, q.h)));
   return L;
 }
 

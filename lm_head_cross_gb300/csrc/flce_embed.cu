@@ -6,12 +6,13 @@
 // Both are bound by memory: the forward pass reads the distinct rows and writes N H elements, the
 // gradient reads N H elements and writes V H (or reads and writes the distinct rows).
 //
-// The gradient's sums have one order, whatever the schedule: the tokens are sorted by (id,
-// position) and cut into tiles; a row of dW is the sum over its tokens in that order in fp32, one
-// part for each tile that it has tokens in, the parts added in order, and rounded once.
-//   bucket  every block sorts its stretch of positions by range of the vocabulary
+// The gradient's sums have one order, whatever the schedule: the tokens are sorted by (key,
+// position), the key a permutation of the id, and cut into tiles; a row of dW is the sum over its
+// tokens in that order in fp32, one part for each tile that it has tokens in, the parts added in
+// order, and rounded once.
+//   bucket  every block sorts its stretch of positions by range of the vocabulary (every 512th id)
 //   sort    every block gathers one range's tokens, which the stretches hold in order, and sorts
-//           them by id.  No block waits for another, no atomics in global memory.
+//           them by key.  No block waits for another, no atomics in global memory.
 //           Few tokens are sorted in one launch, whose blocks each read all ids and keep their
 //           range's: 8 us for 5003 and 9 for 8192, where the two launches take 12 and 13; 48 for
 //           131072, where they take 28.
@@ -173,6 +174,8 @@ __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, i
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRound = 4096;  // tokens of a block's shared memory; a range with more takes several rounds
+constexpr int kEmbedStretchSteps = 256;  // the first step of a search among the stretches
+static_assert(2 * kEmbedStretchSteps > kEmbedStretches, "steps of 256, 128, ... reach each");
 constexpr int kPerMost = kEmbedIdsMost / kEmbedRanges;  // ids of a range
 
 // Inclusive sum over the block's threads; *all gets the total.  `part` holds a word for each warp.
@@ -206,7 +209,7 @@ __device__ __forceinline__ int take_rank(uint32_t some, int key, int32_t* row, i
 // Block s: positions [s len, (s + 1) len), sorted by range (stable) into tokens[s len ..] as (id,
 // position); off[r stretches + s] is where range r starts in it, the last entry how many tokens
 // it holds.  Padding and ids outside the vocabulary are left out.
-__global__ void __launch_bounds__(kSortThreads) embed_bucket_kernel(int n, int v, int per, int ranges, int len, int pad,
+__global__ void __launch_bounds__(kSortThreads) embed_bucket_kernel(int n, int v, int len, int pad,
                                                                     const int32_t* __restrict__ ids,
                                                                     int2* __restrict__ tokens,
                                                                     int32_t* __restrict__ off, int32_t* __restrict__ bad) {
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_bucket_kernel(int n, int v
     const int id = i0 + lane < w1 ? ids[first + i0 + lane] : -1;
     const bool in = static_cast<uint32_t>(id) < static_cast<uint32_t>(v);
     outside |= i0 + lane < w1 && !in;
-    if (in && id != pad) atomicAdd(row + id / per, 1);
+    if (in && id != pad) atomicAdd(row + (id & (kEmbedRanges - 1)), 1);
   }
   outside = __syncthreads_or(outside);
   if (tid == 0) bad[blockIdx.x] = outside;
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_bucket_kernel(int n, int v
       for (int k = 0; k < kSortWarps; ++k) total += count[k][r];
     int at = base + block_scan(total, part, &all) - total;
     base += all;
-    if (r < ranges) off[static_cast<int64_t>(r) * stretches + blockIdx.x] = at;
+    if (r < kEmbedRanges) off[static_cast<int64_t>(r) * stretches + blockIdx.x] = at;
     if (r < kEmbedRanges)
       for (int k = 0; k < kSortWarps; ++k) {
         const int c = count[k][r];
@@ -248,22 +251,22 @@ __global__ void __launch_bounds__(kSortThreads) embed_bucket_kernel(int n, int v
         at += c;
       }
   }
-  if (tid == 0) off[static_cast<int64_t>(ranges) * stretches + blockIdx.x] = base;
+  if (tid == 0) off[static_cast<int64_t>(kEmbedRanges) * stretches + blockIdx.x] = base;
   __syncthreads();
   for (int i0 = w0; i0 < w1; i0 += 32) {  // place
     const int id = i0 + lane < w1 ? ids[first + i0 + lane] : -1;
     const bool in = static_cast<uint32_t>(id) < static_cast<uint32_t>(v) && id != pad;
     const uint32_t some = __ballot_sync(kFull, in);
     if (in) {
-      const int at = take_rank(some, id / per, row, lane);
+      const int at = take_rank(some, id & (kEmbedRanges - 1), row, lane);
       tokens[first + at] = make_int2(id, static_cast<int>(first) + i0 + lane);
     }
     __syncwarp();
   }
 }
 
-// Block r: range r's ids [r per, (r + 1) per).
-__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, int per, int stretches, int len,
+// Block r: range r's ids, r and every kEmbedRanges-th after it.
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int per, int stretches, int len,
                                                                   const int2* __restrict__ tokens,
                                                                   const int32_t* __restrict__ off,
                                                                   const int32_t* __restrict__ bad,
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, 
   int32_t* count = running + per;                 // [kSortWarps][per]
   griddep_begin();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = blockIdx.x, lo = r * per, mine = min(per, v - lo);
+  const int r = blockIdx.x, lo = r * per;
   int all, wrong = 0;
   // the range's tokens of each stretch, and all tokens of the ranges before
   static_assert(kEmbedStretches <= kSortThreads, "a thread for each stretch");
@@ -295,52 +298,71 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, 
   int begin = all;
   wrong = __syncthreads_or(wrong);
   if (r == 0 && tid == 0) *status = wrong ? kErrLabel : kOk;
-  auto token = [&](int i) {  // the range's i-th, in the order of positions
-    int a = 0, b = stretches - 1;
-    while (a < b) {
-      const int mid = (a + b + 1) >> 1;
-      if (seg_first[mid] <= i) a = mid;
-      else b = mid - 1;
+  constexpr int kEach = kSortRound / kSortThreads;
+  // the range's tokens from i0 on, in the order of positions: the thread's are tid, tid + kSortThreads, ...
+  auto fetch = [&](int i0, int2 (&t)[kEach]) {
+    int a[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) a[k] = 0;
+#pragma unroll
+    for (int step = kEmbedStretchSteps; step; step >>= 1) {  // the last stretch that starts at or before it
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (i0 + k * kSortThreads < m && a[k] + step < stretches && seg_first[a[k] + step] <= i0 + k * kSortThreads + tid) a[k] += step;
     }
-    return tokens[static_cast<int64_t>(a) * len + seg_off[a] + (i - seg_first[a])];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = i0 + k * kSortThreads + tid;
+      t[k] = i < m ? tokens[static_cast<int64_t>(a[k]) * len + seg_off[a[k]] + (i - seg_first[a[k]])] : make_int2(-1, 0);
+    }
   };
   // ids' totals, and where each one's tokens start
   for (int j = tid; j < per; j += kSortThreads) running[j] = 0;
   __syncthreads();
-  for (int i = tid; i < m; i += kSortThreads) {
-    const int2 t = token(i);
-    if (i < kSortRound) list[i] = t;
-    atomicAdd(running + (t.x - lo), 1);
+  for (int i0 = 0; i0 < m; i0 += kSortRound) {
+    int2 t[kEach];
+    fetch(i0, t);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      if (i0 + k * kSortThreads >= m) break;
+      if (i0 == 0) list[k * kSortThreads + tid] = t[k];
+      const uint32_t same = __match_any_sync(kFull, t[k].x);
+      if (t[k].x >= 0 && (same >> lane) == 1u) atomicAdd(running + (t[k].x >> kEmbedRangeBits), __popc(same));
+    }
   }
   __syncthreads();
-  for (int j0 = 0; j0 < mine; j0 += kSortThreads) {
-    const int j = j0 + tid, c = j < mine ? running[j] : 0;
+  for (int j0 = 0; j0 < per; j0 += kSortThreads) {
+    const int j = j0 + tid, c = j < per ? running[j] : 0;
     const int first = begin + block_scan(c, part, &all) - c;
     begin += all;
-    if (j < mine) start[lo + j] = running[j] = first;
+    if (j < per) start[lo + j] = running[j] = first;
   }
-  if (lo + mine == v && tid == 0) start[v] = begin;
+  if (r == kEmbedRanges - 1 && tid == 0) start[lo + per] = begin;
   __syncthreads();
   for (int i0 = 0; i0 < m; i0 += kSortRound) {
     const int here = min(kSortRound, m - i0);
     for (int j = tid; j < kSortWarps * per; j += kSortThreads) count[j] = 0;
-    if (i0 > 0)
-      for (int i = tid; i < here; i += kSortThreads) list[i] = token(i0 + i);
+    if (i0 > 0) {
+      int2 t[kEach];
+      fetch(i0, t);
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) list[k * kSortThreads + tid] = t[k];
+    }
     __syncthreads();
     // each token's rank among its warp's with its id
     const int each = (here + kSortThreads - 1) / kSortThreads * 32;
     const int w0 = warp * each, w1 = min(w0 + each, here);
     int32_t* row = count + warp * per;
-    int rank[kSortRound / kSortThreads];
+    int rank[kEach];
 #pragma unroll
-    for (int k = 0; k < kSortRound / kSortThreads; ++k) {
+    for (int k = 0; k < kEach; ++k) {
       const int i = w0 + 32 * k + lane;
       const uint32_t some = __ballot_sync(kFull, i < w1);
-      rank[k] = i < w1 ? take_rank(some, list[i].x - lo, row, lane) : 0;
+      rank[k] = i < w1 ? take_rank(some, list[i].x >> kEmbedRangeBits, row, lane) : 0;
       __syncwarp();
     }
     __syncthreads();
-    for (int j = tid; j < mine; j += kSortThreads) {  // (warp, id) counts to places
+    for (int j = tid; j < per; j += kSortThreads) {  // (warp, id) counts to places
       int next = running[j];
       for (int k = 0; k < kSortWarps; ++k) {
         const int c = count[k * per + j];
@@ -351,11 +373,11 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int v, 
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSortRound / kSortThreads; ++k) {
+    for (int k = 0; k < kEach; ++k) {
       const int i = w0 + 32 * k + lane;
       if (i >= w1) continue;
       const int2 t = list[i];
-      const int where = row[t.x - lo] + rank[k];
+      const int where = row[t.x >> kEmbedRangeBits] + rank[k];
       if (in_bounds(where, n, status)) {
         order[where] = t.y;
         sorted_id[where] = t.x;
@@ -518,7 +540,7 @@ constexpr int kZeroRows = 8;  // of a warp of the zeros' blocks
 //   Blocks below `tile_blocks` take tiles, the others the rows without a token.  A batch of
 // tokens' rows is in flight at once, with the rows of dW that they complete.
 template <typename T, typename TW, bool ALIGNED, bool ADD, int kTile>
-__global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, float scale, int64_t tile_blocks,
+__global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, EmbedKeys keys, float scale, int64_t tile_blocks,
                                                           const int32_t* __restrict__ start,
                                                           const int32_t* __restrict__ order,
                                                           const int32_t* __restrict__ sorted_id,
@@ -529,12 +551,13 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, f
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x >= tile_blocks) {
     const int64_t first = ((static_cast<int64_t>(blockIdx.x) - tile_blocks) * 8 + warp) * kZeroRows;
-    const int at = first + lane <= v ? start[first + lane] : 0;  // (lane 8: where the last one ends)
+    const int key = static_cast<int>(first) + lane, id = keys.id(min(key, keys.count() - 1));
+    const int at = key <= keys.count() ? start[key] : 0;  // (lane 8: where the last one ends)
     const int to = __shfl_down_sync(kFull, at, 1);
-    const uint32_t none = __ballot_sync(kFull, lane < kZeroRows && first + lane < v && at == to);
+    const uint32_t none = __ballot_sync(kFull, lane < kZeroRows && key < keys.count() && id < v && at == to);
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (uint32_t left = none; left; left &= left - 1) {
-      TW* row = dw + (first + __ffs(left) - 1) * h;
+      TW* row = dw + static_cast<int64_t>(__shfl_sync(kFull, id, __ffs(left) - 1)) * h;
       for (int g = 0; g < groups; ++g) store8<ALIGNED>(row, Place<ALIGNED>(g, lane), h, zero);
     }
     return;
@@ -543,7 +566,7 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, f
   const int64_t t = u / groups;
   const int group = static_cast<int>(u % groups);
   const Place<ALIGNED> place(group, lane);
-  const int total = start[v];
+  const int total = start[keys.count()];
   if (t * kTile >= total) return;
   const int s0 = static_cast<int>(t) * kTile, tokens = min(kTile, total - s0);
   int my_id[kTile / 32], my_at[kTile / 32];
@@ -597,7 +620,7 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, f
         finish<TW, ALIGNED, ADD>(dw + static_cast<int64_t>(id[k]) * h, place, h, scale, old[ADD ? k : 0], x);
       } else {
         const int64_t to = ((2 * t + (began ? 1 : 0)) * groups + group) * kCols;
-        if (in_bounds(to + kCols - 1, embed_part_floats(n, static_cast<int64_t>(groups) * kCols), status))
+        if (in_bounds(to + kCols - 1, embed_part_floats(n, h), status))
           part_store<ALIGNED>(part + to, lane, x);
       }
 #pragma unroll
@@ -610,7 +633,7 @@ constexpr int kJoinAlone = 16;  // parts that a warp adds up by itself; more are
 
 // Block (t, g): 8 times 256 columns of the row that starts in tile t and goes on, if there is one.
 template <typename TW, bool ALIGNED, bool ADD, int kTile>
-__global__ void __launch_bounds__(256) embed_join_kernel(int h, int v, float scale, const int32_t* __restrict__ start,
+__global__ void __launch_bounds__(256) embed_join_kernel(int h, EmbedKeys keys, float scale, const int32_t* __restrict__ start,
                                                          const int32_t* __restrict__ sorted_id,
                                                          const float* __restrict__ part, TW* __restrict__ dw, int groups) {
   __shared__ float run[8][32][9];
@@ -621,13 +644,13 @@ __global__ void __launch_bounds__(256) embed_join_kernel(int h, int v, float sca
   // The sorted order is older than the launch before, which waited for it: it is read ahead of the
   // wait, from L2.  Every block waits before it leaves, so that whatever follows this launch follows
   // that one.
-  const int total = __ldcg(start + v);
+  const int total = __ldcg(start + keys.count());
   const int64_t s0 = t * kTile, s1 = s0 + kTile;
   int id = 0, a = 0, b = 0;
   if (s1 < total) {
     id = __ldcg(sorted_id + s1 - 1);
-    a = __ldcg(start + id);
-    b = __ldcg(start + id + 1);
+    a = __ldcg(start + keys.of(id));
+    b = __ldcg(start + keys.of(id) + 1);
   }
   griddep_begin();
   if (a < s0 || b <= s1) return;
@@ -708,24 +731,25 @@ template <typename T, typename TW, bool ALIGNED, bool ADD, int TILE>
 cudaError_t backward_by(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, cudaStream_t s) {
   const int groups = groups_of(q.h);
   const int n = static_cast<int>(q.n), v = static_cast<int>(q.v);
+  const EmbedKeys keys = embed_keys(q.n, q.v);
   const int64_t tiles = (q.n + TILE - 1) / TILE, tile_blocks = (tiles * groups + 7) / 8;
-  const int64_t zero_blocks = ADD ? 0 : (q.v + 8 * kZeroRows - 1) / (8 * kZeroRows);
+  const int64_t zero_blocks = ADD ? 0 : (keys.count() + 8 * kZeroRows - 1) / (8 * kZeroRows);
   const int64_t join_blocks = (tiles - 1) * ((groups + 7) / 8);
   if (tile_blocks + zero_blocks > INT_MAX || join_blocks > INT_MAX) return cudaErrorInvalidValue;
   TW* out = static_cast<TW*>(dw);
   cudaError_t e = launch_k(embed_tiles_kernel<T, TW, ALIGNED, ADD, TILE>,
-                           dim3(static_cast<unsigned>(tile_blocks + zero_blocks)), dim3(256), 0, s, n, q.h, v, q.scale,
+                           dim3(static_cast<unsigned>(tile_blocks + zero_blocks)), dim3(256), 0, s, n, q.h, v, keys, q.scale,
                            tile_blocks, o.start, o.order, o.sorted_id, static_cast<const T*>(dy), o.part, out, groups,
                            o.status);
   if (e != cudaSuccess || join_blocks == 0) return e;
   return launch_k(embed_join_kernel<TW, ALIGNED, ADD, TILE>, dim3(static_cast<unsigned>(join_blocks)), dim3(256), 0, s,
-                  q.h, v, q.scale, o.start, o.sorted_id, o.part, out, groups);
+                  q.h, keys, q.scale, o.start, o.sorted_id, o.part, out, groups);
 }
 
 template <typename T, typename TW, bool ALIGNED, bool ADD>
 cudaError_t backward_as(const EmbedParams& q, const void* dy, const EmbedSorted& o, void* dw, cudaStream_t s) {
-  return q.n < kEmbedMany ? backward_by<T, TW, ALIGNED, ADD, kEmbedTile>(q, dy, o, dw, s)
-                          : backward_by<T, TW, ALIGNED, ADD, kEmbedTileMany>(q, dy, o, dw, s);
+  return embed_tile(q.n, q.h) == kEmbedTile ? backward_by<T, TW, ALIGNED, ADD, kEmbedTile>(q, dy, o, dw, s)
+                                            : backward_by<T, TW, ALIGNED, ADD, kEmbedTileMany>(q, dy, o, dw, s);
 }
 
 template <typename T, typename TW>
@@ -762,12 +786,11 @@ static cudaError_t sort_few(const EmbedParams& q, int pad, const int32_t* ids, c
 cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids, const EmbedSorted& o, int sms,
                               cudaStream_t s) {
   if (q.n <= kEmbedFew) return sort_few(q, pad, ids, o, sms, s);
-  const int per = static_cast<int>((q.v + kEmbedRanges - 1) / kEmbedRanges);
-  const int ranges = static_cast<int>((q.v + per - 1) / per);
+  const int per = embed_keys(q.n, q.v).per;
   const int len = static_cast<int>((q.n + kEmbedStretches - 1) / kEmbedStretches);
   const int stretches = static_cast<int>((q.n + len - 1) / len);
   const int n = static_cast<int>(q.n), v = static_cast<int>(q.v);
-  cudaError_t e = launch_k(embed_bucket_kernel, dim3(stretches), dim3(kSortThreads), 0, s, n, v, per, ranges, len, pad,
+  cudaError_t e = launch_k(embed_bucket_kernel, dim3(stretches), dim3(kSortThreads), 0, s, n, v, len, pad,
                            ids, static_cast<int2*>(o.tokens), o.off, o.bad);
   if (e != cudaSuccess) return e;
   auto smem = [](int ids_of_range) {
@@ -776,7 +799,7 @@ cudaError_t launch_embed_sort(const EmbedParams& q, int pad, const int32_t* ids,
   static std::atomic<uint64_t> done{0};
   e = allow_smem(embed_sort_kernel, smem(kPerMost), done);
   if (e != cudaSuccess) return e;
-  return launch_k(embed_sort_kernel, dim3(ranges), dim3(kSortThreads), smem(per), s, n, v, per, stretches, len,
+  return launch_k(embed_sort_kernel, dim3(kEmbedRanges), dim3(kSortThreads), smem(per), s, n, per, stretches, len,
                   static_cast<const int2*>(o.tokens), o.off, o.bad, o.start, o.order, o.sorted_id, o.status);
 }
 

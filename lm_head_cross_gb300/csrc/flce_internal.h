@@ -351,15 +351,34 @@ cudaError_t launch_norm_backward(const NormParams& q, const void* dy, const void
                                  float* part, cudaStream_t stream);
 
 // Embedding (flce_embed.cu).
-constexpr int kEmbedRanges = 512;            // of the vocabulary, a block's each in the sort
+constexpr int kEmbedRangeBits = 9;
+constexpr int kEmbedRanges = 1 << kEmbedRangeBits;  // of the vocabulary, a block's each in the sort
 constexpr int64_t kEmbedIdsMost = 1 << 20;   // rows of a matrix
 constexpr int kEmbedStretches = 304;         // of the positions: two blocks for each SM
 constexpr int64_t kEmbedFew = 16384;         // tokens up to which one launch sorts them
-// Tokens of the sorted order that are summed at once, and the tokens of a call from which on the
-// larger number serves: few tokens need small tiles to occupy the GPU, many leave fewer parts in
-// large ones (131072 x 4096: parts joined in 72 us with 32, 42 with 64).
+// Tokens of the sorted order that a warp sums at once.  Few tokens or short rows need small tiles to
+// occupy the GPU, many leave fewer parts in large ones: 131072 x 4096 in 339 us with 64, 355 with 32
+// (most ids alike: 609, 724), 32768 x 512 in 42, 36 (81, 79).  Rows that no 16-byte access divides
+// take many more loads for each token: 131072 x 1001 in 431, 271.
 constexpr int kEmbedTile = 32, kEmbedTileMany = 64;
-constexpr int64_t kEmbedMany = 32768;
+FLCE_HOST_DEVICE inline int embed_tile(int64_t n, int64_t h) {
+  return n >= 32768 && n * ((h + 255) / 256) >= 131072 && h % 8 == 0 ? kEmbedTileMany : kEmbedTile;
+}
+// The sorted order is one of ids' keys.  One launch's blocks take consecutive ids; in two launches a
+// range is every kEmbedRanges-th id: vocabularies put their frequent ids side by side, and a block
+// with all of them was the end of the sort (131072 tokens, the first 98 of 50000 ids a third of
+// them: 168 us).
+struct EmbedKeys {
+  int bits;  // range: the id's low bits
+  int per;   // ids of a range
+  FLCE_HOST_DEVICE int of(int id) const { return (id & ((1 << bits) - 1)) * per + (id >> bits); }
+  FLCE_HOST_DEVICE int id(int key) const { return (key % per << bits) + key / per; }
+  FLCE_HOST_DEVICE int count() const { return per << bits; }  // some of ids past the vocabulary's end
+};
+FLCE_HOST_DEVICE inline EmbedKeys embed_keys(int64_t n, int64_t v) {
+  const int bits = n <= kEmbedFew ? 0 : kEmbedRangeBits;
+  return EmbedKeys{bits, static_cast<int>((v + (int64_t{1} << bits) - 1) >> bits)};
+}
 struct EmbedParams {
   int64_t n;
   int h;
@@ -367,8 +386,8 @@ struct EmbedParams {
   float scale;
   bool w_f32, y_f32;  // else bf16
 };
-// The tokens other than the padding id in the order of (id, position): their positions and
-// ids, start[v + 1] of each id's, and the parts of the rows whose tokens lie in several tiles.
+// The tokens other than the padding id in the order of (key, position): their positions and
+// ids, start[keys + 1] of each key's, and the parts of the rows whose tokens lie in several tiles.
 struct EmbedSorted {
   int32_t* start;
   int32_t* order;
@@ -379,10 +398,11 @@ struct EmbedSorted {
   float* part;
   int* status;
 };
-// Parts of n tokens whose rows take `row` floats: two for each tile of the sorted order.
-FLCE_HOST_DEVICE inline int64_t embed_part_floats(int64_t n, int64_t row) {
-  const int64_t tile = n < kEmbedMany ? kEmbedTile : kEmbedTileMany;
-  return n > tile ? 2 * ((n + tile - 1) / tile) * row : 0;
+// Parts of n tokens with rows of h elements: two, of whole groups of 256, for each tile of the
+// sorted order.
+FLCE_HOST_DEVICE inline int64_t embed_part_floats(int64_t n, int64_t h) {
+  const int64_t tile = embed_tile(n, h);
+  return n > tile ? 2 * ((n + tile - 1) / tile) * ((h + 255) / 256 * 256) : 0;
 }
 cudaError_t launch_embed_forward(const EmbedParams& q, const int32_t* ids, const void* w, void* y, int* status,
                                  cudaStream_t stream);
