@@ -19,6 +19,8 @@
 //   tiles   every tile's tokens, 256 columns a warp: rows that lie within the tile are finished,
 //           the others leave a part; beside them, zeros for the rows without a token
 //   join    the rows with several parts
+#include <type_traits>
+
 #include "flce_device.cuh"
 #include "flce_internal.h"
 #include "flce_launch.cuh"
@@ -174,8 +176,8 @@ __global__ void __launch_bounds__(kFwdThreads) embed_forward_kernel(int64_t n, i
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRound = 4096;  // tokens of a block's shared memory; a range with more takes several rounds
-constexpr int kEmbedStretchSteps = 256;  // the first step of a search among the stretches
-static_assert(2 * kEmbedStretchSteps > kEmbedStretches, "steps of 256, 128, ... reach each");
+constexpr int kSearchStep = 256;  // the first of a search among the stretches
+static_assert(2 * kSearchStep > kEmbedStretches, "steps of 256, 128, ... reach each");
 constexpr int kPerMost = kEmbedIdsMost / kEmbedRanges;  // ids of a range
 
 // Inclusive sum over the block's threads; *all gets the total.  `part` holds a word for each warp.
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int per
                                                                   int32_t* __restrict__ sorted_id, int* status) {
   extern __shared__ __align__(16) int32_t sort_smem[];
   __shared__ int part[kSortWarps];
-  __shared__ int32_t seg_first[kEmbedStretches], seg_off[kEmbedStretches];  // of the range's tokens, of the stretch's
+  __shared__ int32_t seg_first[2 * kSearchStep], seg_off[kEmbedStretches];  // of the range's tokens, of the stretch's
   int2* list = reinterpret_cast<int2*>(sort_smem);
   int32_t* running = sort_smem + 2 * kSortRound;  // [per]: where an id's next token goes
   int32_t* count = running + per;                 // [kSortWarps][per]
@@ -290,10 +292,9 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int per
   if (r == 0 && tid < stretches) wrong = bad[tid];
   const int incl = block_scan(to - at, part, &all);
   const int m = all;
-  if (tid < stretches) {
-    seg_first[tid] = incl - (to - at);
-    seg_off[tid] = at;
-  }
+  static_assert(2 * kSearchStep <= kSortThreads, "a thread for each entry");
+  if (tid < 2 * kSearchStep) seg_first[tid] = tid < stretches ? incl - (to - at) : INT32_MAX;
+  if (tid < stretches) seg_off[tid] = at;
   block_scan(at, part, &all);
   int begin = all;
   wrong = __syncthreads_or(wrong);
@@ -301,20 +302,26 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(int n, int per
   constexpr int kEach = kSortRound / kSortThreads;
   // the range's tokens from i0 on, in the order of positions: the thread's are tid, tid + kSortThreads, ...
   auto fetch = [&](int i0, int2 (&t)[kEach]) {
-    int a[kEach];
+    auto some = [&](auto count) {  // of the thread's
+      constexpr int number = decltype(count)::value;
+      int a[number];
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) a[k] = 0;
+      for (int k = 0; k < number; ++k) a[k] = 0;
 #pragma unroll
-    for (int step = kEmbedStretchSteps; step; step >>= 1) {  // the last stretch that starts at or before it
+      for (int step = kSearchStep; step; step >>= 1) {  // the last stretch that starts at or before it
 #pragma unroll
-      for (int k = 0; k < kEach; ++k)
-        if (i0 + k * kSortThreads < m && a[k] + step < stretches && seg_first[a[k] + step] <= i0 + k * kSortThreads + tid) a[k] += step;
-    }
+        for (int k = 0; k < number; ++k) a[k] += seg_first[a[k] + step] <= i0 + k * kSortThreads + tid ? step : 0;
+      }
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int i = i0 + k * kSortThreads + tid;
-      t[k] = i < m ? tokens[static_cast<int64_t>(a[k]) * len + seg_off[a[k]] + (i - seg_first[a[k]])] : make_int2(-1, 0);
-    }
+      for (int k = 0; k < number; ++k) {
+        const int i = i0 + k * kSortThreads + tid;
+        t[k] = i < m ? tokens[static_cast<int64_t>(a[k]) * len + seg_off[a[k]] + (i - seg_first[a[k]])] : make_int2(-1, 0);
+      }
+    };
+#pragma unroll
+    for (int k = 1; k < kEach; ++k) t[k] = make_int2(-1, 0);
+    if (m - i0 > kSortThreads) some(std::integral_constant<int, kEach>());
+    else some(std::integral_constant<int, 1>());
   };
   // ids' totals, and where each one's tokens start
   for (int j = tid; j < per; j += kSortThreads) running[j] = 0;
