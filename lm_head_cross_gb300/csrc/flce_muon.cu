@@ -112,6 +112,13 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t w) {
 
 // ----------------------------------------------------------------------------- products
 
+// What bounds them.  At 4096 x 4096 X X^T and the square, 136 tiles on 76 pairs, take 50 us, P X, 256
+// tiles, 95 and with the old lo 99: two and four waves.  Without the epilogue 44 and 84, so that a
+// wave's main loop runs at 1.9 PFLOP/s, the library's rate; the last wave's idle pairs and the last
+// tile's epilogue are the rest.  Four stages cost 7%, a sixth gives nothing.  28 matrices in one
+// launch fill their waves: 128 to 450 us, 1.4 to 1.5 PFLOP/s, with the power cap.  Three
+// of 777 x 1544 have one or two tiles for a pair: 13 to 23 us, of which the loop is 13 or 25 steps.
+
 // A tile of the launch: its group, which of its matrices, this CTA's first row, the first column.
 struct Tile {
   const MuonGroup* g;
@@ -541,6 +548,9 @@ __device__ __forceinline__ void chain_store(uint8_t* m, int row, int c0, const f
 // All of a matrix's steps in one block: operands in shared memory, one thread issues the products,
 // a thread of the eight warps holds half a row of their results.  Symmetric operands are K-major
 // on either side.
+//   128 x 128, five steps: 48 us, of which 14 rounds of products (30 of 128 x 128 x 128, three each)
+// take 18 and the results' way through registers to operands, 255 registers a thread, the others.
+// One launch in the place of 13, which took 10 us each.
 __global__ void __launch_bounds__(kChainThreads, 1) muon_chain_kernel(const __grid_constant__ MuonChain a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -794,7 +804,8 @@ __device__ __forceinline__ Momentum momentum_of(const MuonSources<N>& a) {
   return Momentum{a.mu, a.omm, a.grad_scale ? *a.grad_scale : 1.f, a.nesterov};
 }
 
-// One chunk of kMuonChunk elements: the momentum moves, and the squares of u are added up.
+// One chunk of kMuonChunk elements: the momentum moves, and the squares of u are added up.  Bound by
+// memory: 112 matrices of 40M elements in 60 us, 73% of DRAM's nominal rate.
 template <int N>
 __global__ void __launch_bounds__(kNormThreads) muon_momentum_kernel(const __grid_constant__ MuonSources<N> a) {
   griddep_begin();
@@ -955,7 +966,8 @@ __device__ __forceinline__ float norm_factor(const MuonSources<N>& a, int si, fl
 }
 
 // Blocks take runs of consecutive strips, from the last source to the first: what the momentum's
-// pass left in L2 is read first.
+// pass left in L2 is read first.  The same 40M elements in 80 us: 359 MB through DRAM, and the
+// issue slots half busy with roundings to the pair.
 template <int N>
 __global__ void __launch_bounds__(kNormThreads, 5) muon_scale_kernel(const __grid_constant__ MuonSources<N> a, uint32_t run) {
   griddep_begin();
@@ -1014,7 +1026,8 @@ __device__ __forceinline__ void weights_strip(const MuonTarget& s, uint32_t k0, 
   }
 }
 
-// X to out as bf16, or taken off the weights.
+// X to out as bf16, or taken off the weights.  Bound by memory: 40M bf16 weights in 55 us, 193 MB of
+// them through DRAM and the rest, X, from L2.
 template <int N>
 __global__ void __launch_bounds__(kNormThreads, 4) muon_weights_kernel(const __grid_constant__ MuonTargets<N> a, uint32_t run) {
   griddep_begin();
