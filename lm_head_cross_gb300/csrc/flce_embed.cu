@@ -640,19 +640,21 @@ __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, E
   }
 }
 
+constexpr int kJoinGroups = 4;  // of 256 columns, a block's: one after the other where a row has many parts
 constexpr int kJoinAlone = 16;  // parts that a warp adds up by itself; more are cut into a run for each warp
 
-// Block (t, g): 8 times 256 columns of the row that starts in tile t and goes on, if there is one.
-// 42 us of 131072 x 4096 in tiles of 64 (the parts are in L2), 10 of 8192 x 2048.
+// Block (t, g): kJoinGroups times 256 columns of the row that starts in tile t and goes on, if there
+// is one.  The row with the most parts is the end of it: 131072 x 4096 in tiles of 64, a vocabulary's
+// frequencies, 31 us, with 8 groups a block 42 (and eight parts in flight in place of four 51); 8192 x 2048 8.
 template <typename TW, bool ALIGNED, bool ADD, int kTile>
 __global__ void __launch_bounds__(256) embed_join_kernel(int h, EmbedKeys keys, float scale, const int32_t* __restrict__ start,
                                                          const int32_t* __restrict__ sorted_id,
                                                          const float* __restrict__ part, TW* __restrict__ dw, int groups) {
   __shared__ float run[8][32][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wide = (groups + 7) / 8;
+  const int wide = (groups + kJoinGroups - 1) / kJoinGroups;
   const int64_t t = blockIdx.x / wide;
-  const int g0 = static_cast<int>(blockIdx.x % wide) * 8;
+  const int g0 = static_cast<int>(blockIdx.x % wide) * kJoinGroups;
   // The sorted order is older than the launch before, which waited for it: it is read ahead of the
   // wait, from L2.  Every block waits before it leaves, so that whatever follows this launch follows
   // that one.
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(int h, EmbedKeys keys, 
   Words<TW, ALIGNED> old;
   if (parts <= kJoinAlone) {
     const int g = g0 + warp;
-    if (g >= groups) return;
+    if (warp >= kJoinGroups || g >= groups) return;
     const Place<ALIGNED> place(g, lane);
     float x[8];
     old.zero();
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(int h, EmbedKeys keys, 
     return;
   }
   const int each = (parts + 7) / 8;
-  for (int g = g0; g < min(g0 + 8, groups); ++g) {
+  for (int g = g0; g < min(g0 + kJoinGroups, groups); ++g) {
     float x[8];
     sum(g, warp * each, min(parts, (warp + 1) * each), x);
     __syncthreads();  // (the runs of the group before have been read)
@@ -746,7 +748,7 @@ cudaError_t backward_by(const EmbedParams& q, const void* dy, const EmbedSorted&
   const EmbedKeys keys = embed_keys(q.n, q.v);
   const int64_t tiles = (q.n + TILE - 1) / TILE, tile_blocks = (tiles * groups + 7) / 8;
   const int64_t zero_blocks = ADD ? 0 : (keys.count() + 8 * kZeroRows - 1) / (8 * kZeroRows);
-  const int64_t join_blocks = (tiles - 1) * ((groups + 7) / 8);
+  const int64_t join_blocks = (tiles - 1) * ((groups + kJoinGroups - 1) / kJoinGroups);
   if (tile_blocks + zero_blocks > INT_MAX || join_blocks > INT_MAX) return cudaErrorInvalidValue;
   TW* out = static_cast<TW*>(dw);
   cudaError_t e = launch_k(embed_tiles_kernel<T, TW, ALIGNED, ADD, TILE>,
