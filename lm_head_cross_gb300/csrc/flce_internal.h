@@ -357,12 +357,11 @@ constexpr int64_t kEmbedIdsMost = 1 << 20;   // rows of a matrix
 constexpr int kEmbedStretches = 304;         // of the positions: two blocks for each SM
 constexpr int64_t kEmbedFew = 16384;         // tokens up to which one launch sorts them
 // Tokens of the sorted order that a warp sums at once.  Few tokens or short rows need small tiles to
-// occupy the GPU, many leave fewer parts in large ones: 131072 x 4096 in 339 us with 64, 355 with 32
-// (most ids alike: 609, 724), 32768 x 512 in 42, 36 (81, 79).  Rows that no 16-byte access divides
-// take many more loads for each token: 131072 x 1001 in 431, 271.
+// occupy the GPU, many leave fewer parts in large ones: 131072 x 4096 in 259 us with 64, 286 with 32
+// (frequent ids: 328, 390), 131072 x 1001 in 126, 128 (235, 314), 32768 x 512 in 40, 36 (44, 46).
 constexpr int kEmbedTile = 32, kEmbedTileMany = 64;
 FLCE_HOST_DEVICE inline int embed_tile(int64_t n, int64_t h) {
-  return n >= 32768 && n * ((h + 255) / 256) >= 131072 && h % 8 == 0 ? kEmbedTileMany : kEmbedTile;
+  return n >= 32768 && n * ((h + 255) / 256) >= 131072 ? kEmbedTileMany : kEmbedTile;
 }
 // The sorted order is one of ids' keys.  One launch's blocks take consecutive ids; in two launches a
 // range is every kEmbedRanges-th id: vocabularies put their frequent ids side by side, and a block
