@@ -120,7 +120,7 @@ constexpr int64_t kScanIds = 16384;  // of a block
 // Blocks below `scans` look the ids over, ahead of the rows so that none of it is left at the end:
 // one writes the status word, several (for many ids) record errors in a word that was cleared.  In
 // the others LANES threads take kFwdUnits consecutive (row, 8 LANES columns).
-//   Bound by memory: 131072 x 4096 bf16, a vocabulary's frequencies, 224 us (1.36 GB through DRAM).
+//   Bound by memory: 131072 x 4096 bf16, a vocabulary's frequencies, 216 us (1.36 GB through DRAM).
 //   Several rows in a warp where they are short: 131072 x 64 in 13 us for 18, 2^20 x 64 in 30 for 89.
 //   Times with one scanning block behind the rows, one ahead of them, and with these: 131072 x 512
 // in 55, 39, 38 us, 131072 x 64 in 31, 33, 18, 131072 x 4096 in 338, 317, 318; 20000 x 512 in 14, 12, 13.
@@ -548,9 +548,9 @@ constexpr int kZeroRows = 8;  // of a warp of the zeros' blocks
 // goes on.
 //   Blocks below `tile_blocks` take tiles, the others the rows without a token.  A batch of
 // tokens' rows is in flight at once, with the rows of dW that they complete.
-//   Bound by memory where there is enough of it: 131072 x 4096 added to dW in 256 us (1.53 GB, 75% of
-// DRAM's nominal rate), 8192 x 2048 for 32000 rows in 31 (102 MB of them reach DRAM), 5003 x 1031 fp32
-// for 40009 rows in 32.
+//   Bound by memory where there is enough of it: 131072 x 4096 added to dW in 241 us (1.53 GB, 80% of
+// DRAM's nominal rate), 8192 x 2048 for 32000 rows in 28 (102 MB of them reach DRAM), 5003 x 1031 fp32
+// for 40009 rows in 31.
 template <typename T, typename TW, bool ALIGNED, bool ADD, int kTile>
 __global__ void __launch_bounds__(256) embed_tiles_kernel(int n, int h, int v, EmbedKeys keys, float scale, int64_t tile_blocks,
                                                           const int32_t* __restrict__ start,
@@ -650,7 +650,7 @@ constexpr int kJoinAlone = 16;  // parts that a warp adds up by itself; more are
 
 // Block (t, g): kJoinGroups times 256 columns of the row that starts in tile t and goes on, if there
 // is one.  The row with the most parts is the end of it: 131072 x 4096 in tiles of 64, a vocabulary's
-// frequencies, 31 us, with 8 groups a block 42 (and eight parts in flight in place of four 51); 8192 x 2048 8.
+// frequencies, 30 us, with 8 groups a block 42 (and eight parts in flight in place of four 51); 8192 x 2048 8.
 template <typename TW, bool ALIGNED, bool ADD, int kTile>
 __global__ void __launch_bounds__(256) embed_join_kernel(int h, EmbedKeys keys, float scale, const int32_t* __restrict__ start,
                                                          const int32_t* __restrict__ sorted_id,
