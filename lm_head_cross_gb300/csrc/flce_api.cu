@@ -1972,37 +1972,52 @@ flce_status_t check_muon_shape(int64_t rows, int64_t cols) {
   return FLCE_OK;
 }
 
+// The largest values of |p(s)| and of |s p(s)|, p(s) = a + b s^2 + c s^4, for s in [0, top]: at an end
+// or where a derivative is 0.  (A grid passes by what lies between its points.)
+struct MuonBound {
+  double p, sp;
+};
+MuonBound muon_bound(double a, double b, double c, double top) {
+  MuonBound m{0.0, 0.0};
+  auto at = [&](double x) {  // x = s^2
+    if (!(x >= 0.0 && x <= top * top)) return;
+    const double p = std::abs(a + x * (b + x * c));
+    m.p = std::max(m.p, p);
+    m.sp = std::max(m.sp, p * std::sqrt(x));
+  };
+  at(0.0);
+  at(top * top);
+  if (c != 0.0) {
+    at(-b / (2.0 * c));
+    const double d = 9.0 * b * b - 20.0 * a * c;  // a + 3 b x + 5 c x^2 = 0
+    if (d >= 0.0) {
+      at((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+      at((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+    }
+  } else if (b != 0.0) {
+    at(-a / (3.0 * b));
+  }
+  return m;
+}
+
 // Scale of P in fp16: a power of two that keeps its entries, at most the largest value of
 // |a + b s^2 + c s^4| for a singular value s of X, below 2^16.  False where some step could take a
 // singular value past 1.95, or shift A's diagonal by more than 3 (b / 2c), beyond which A would
 // not fit its scale.
-//   q_scale: the same for the product of the first steps' P, X's factor after them, whose largest
-// value the same grid finds.
+//   q_scale: the same for the product of the first steps' P, X's factor after them: at most the
+// product of their bounds.  (The factor itself may peak anywhere, and what its scale has to spare
+// costs nothing: a pair's finest step is 2^-39 of the bound.)
 bool muon_scales(const flce_muon_t& o, float* p_scale, float* q_scale) {
-  constexpr int kGrid = 256;  // (4096 points took 10 us a step)
-  double top = 1.0 + 1.0 / 256, p_most = 0.0;
-  double value[kGrid + 1], factor[kGrid + 1];
-  for (int i = 0; i <= kGrid; ++i) {
-    value[i] = top * i / kGrid;
-    factor[i] = 1.0;
-  }
+  double top = 1.0 + 1.0 / 256, p_most = 0.0, q_most = 1.0;
   for (int k = 0; k < o.steps; ++k) {
     const double a = o.coefficients[3 * k], b = o.coefficients[3 * k + 1], c = o.coefficients[3 * k + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     if (c != 0.0 && std::abs(b) > 6.0 * std::abs(c)) return false;
-    double next = 0.0, q_most = 0.0;
-    for (int i = 0; i <= kGrid; ++i) {
-      const double s = top * i / kGrid, p = std::abs(a + s * s * (b + s * s * c));
-      p_most = std::max(p_most, p);
-      next = std::max(next, p * s);
-      const double at = value[i], q = a + at * at * (b + at * at * c);
-      value[i] = at * q;
-      factor[i] *= q;
-      q_most = std::max(q_most, std::abs(factor[i]));
-    }
-    top = next * (1.0 + 1.0 / 256);
+    const MuonBound m = muon_bound(a, b, c, top);
+    p_most = std::max(p_most, m.p);
+    q_most *= m.p;
+    top = m.sp * (1.0 + 1.0 / 256);
     if (!(top <= 1.95) || !(p_most <= 1e4)) return false;
-    // (between the grid's points; the largest factors are those of 0)
     q_scale[k] = static_cast<float>(std::exp2(std::floor(std::log2(45000.0 / std::max(q_most, 1e-3)))));
   }
   *p_scale = static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(p_most, 1e-3)))));

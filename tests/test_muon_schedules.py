@@ -1,0 +1,80 @@
+"""Schedules of Newton-Schulz coefficients other than the usual five steps, against the definition
+in 64 bits.
+
+X is read from fp32 weights that start at 0 and take a step of rate -1 with a momentum of 0, so
+that no rounding of a result comes on top.  Errors are in X's norm.
+  What the header promises for the roundings of the products: PROMISE below.
+  `floor`: 22 bits of u and of what the products sum in fp32 leave a part nu of u's norm that is not
+u's.  It grows like the singular values of its directions, by at most the product G of the slopes at
+0, and until those reach order one: by 1 / the smallest of u's, times 8 for the steps from
+there on, where a slope may still exceed 1.  nu = 2^-20: pairs of fp16 are off by 2^-23 of an element, the sums
+of 24 products of 16 terms in Q X by 2^-23 of the running sum each time, 5 of those in the mean (their
+root): 6 2^-23.  Where nu grows to order one X is as large as its directions are many."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import lm_head_cross_gb300 as flce  # noqa: E402
+
+USUAL = (3.4445, -4.7750, 2.0315)
+PROMISE = 2e-3  # of up to 128 rows or columns
+
+
+def exact(u, coefficients, eps=1e-7):
+    """The definition: u [R, C] in 64 bits."""
+    x = u.double()
+    x = x / (x.square().sum().sqrt() + eps)
+    for a, b, c in coefficients:
+        if x.shape[0] <= x.shape[1]:
+            g = x @ x.mT
+            x = a * x + (b * g + c * (g @ g)) @ x
+        else:
+            g = x.mT @ x
+            x = a * x + x @ (b * g + c * (g @ g))
+    return x
+
+
+def with_values(r, c, values, seed=0):
+    """A matrix of these singular values."""
+    g = torch.Generator().manual_seed(seed)
+    m = min(r, c)
+    left, _ = torch.linalg.qr(torch.randn(r, m, generator=g, dtype=torch.float64))
+    right, _ = torch.linalg.qr(torch.randn(c, m, generator=g, dtype=torch.float64))
+    return ((left * torch.as_tensor(values, dtype=torch.float64)) @ right.mT).float()
+
+
+def x_of(u, coefficients):
+    """X in 32 bits, as the step takes it off weights of 0."""
+    w, m = torch.zeros_like(u), torch.zeros_like(u)
+    factor = math.sqrt(max(1.0, u.shape[0] / u.shape[1]))
+    plan = flce.muon_plan([w], [m], lr=-1.0 / factor, momentum=0.0, nesterov=False, steps=len(coefficients),
+                          coefficients=list(coefficients))
+    flce.muon_step(plan, [u], check=True)
+    return w
+
+
+def off(u, coefficients):
+    """The error of X, and what the floor adds to the promise, both of X's norm."""
+    near = exact(u, coefficients)
+    norm = near.norm().item()
+    least = (torch.linalg.svdvals(u.double())[-1] / u.double().norm()).item()
+    grown = min(math.prod(max(1.0, abs(a)) for a, _, _ in coefficients), 8.0 / max(least, 1e-300))
+    floor = min(2.0 ** -20 * grown, 2.0 * min(u.shape) ** 0.5) / norm
+    return ((x_of(u, coefficients).double() - near).norm() / norm).item(), floor
+
+
+#: four usual steps, then four whose product is largest for a singular value of 0.0141275, between
+#: the points of a grid of 256: 52 times X there, 1.05 at its neighbours
+PEAK = [USUAL] * 4 + [(0.3691, -0.2635, -0.4207), (0.2906, -1.0417, -0.2021), (0.2066, -0.809, 0.1765),
+                      (0.2686, -1.4555, -0.7431)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r,c", [(64, 96), (96, 64), (16, 16)])
+def test_products_of_the_steps_that_peak_anywhere(r, c):
+    m, s = min(r, c), 0.0141275
+    u = with_values(r, c, [math.sqrt(1 - (m - 1) * s * s)] + [s] * (m - 1)).cuda()
+    error, floor = off(u, PEAK)
+    assert error <= PROMISE + floor
