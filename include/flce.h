@@ -533,7 +533,10 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
  *     6e-3 where most singular values are equal, so that all roundings agree).
  *     Matrices of at most 128 rows or columns carry 22 bits (1e-4 of X's norm, up
  *     to 2e-3 where strong directions outweigh weak ones 1000 to 1, or with 2^24
- *     columns).  Momentum, norm and the weights' update are fp32.
+ *     columns), for any number of steps.  Momentum, norm and the weights' update are
+ *     fp32.  As in 32-bit arithmetic, directions that hold less than about 1e-6 of
+ *     u's norm are the rounding's, and grow like others with the product of the
+ *     slopes a (2e5 for ten usual steps, 1e6 for eleven).
  *   - The coefficients must keep singular values in [0, 1] within 1.95 at every
  *     step, and c must be 0 or |b| <= 6 |c| (FLCE_ERR_INVALID_ARGUMENT otherwise).
  *   - A matrix of zeros becomes zeros.  One with a non-finite element, or whose

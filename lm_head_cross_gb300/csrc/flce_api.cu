@@ -2000,27 +2000,42 @@ MuonBound muon_bound(double a, double b, double c, double top) {
   return m;
 }
 
-// Scale of P in fp16: a power of two that keeps its entries, at most the largest value of
-// |a + b s^2 + c s^4| for a singular value s of X, below 2^16.  False where some step could take a
-// singular value past 1.95, or shift A's diagonal by more than 3 (b / 2c), beyond which A would
-// not fit its scale.
-//   q_scale: the same for the product of the first steps' P, X's factor after them: at most the
-// product of their bounds.  (The factor itself may peak anywhere, and what its scale has to spare
-// costs nothing: a pair's finest step is 2^-39 of the bound.)
-bool muon_scales(const flce_muon_t& o, float* p_scale, float* q_scale) {
-  double top = 1.0 + 1.0 / 256, p_most = 0.0, q_most = 1.0;
+// What a call's coefficients decide.
+struct MuonSchedule {
+  // Scale of P in fp16: a power of two that keeps its entries, at most the largest value of
+  // |a + b s^2 + c s^4| for a singular value s of X, below 2^16.
+  float p_scale;
+  // The exact ones' reads of X: the n-th takes steps first[n] to first[n + 1] - 1 on X X^T.
+  int reads, first[FLCE_MUON_MAX_STEPS + 1];
+  // At each step the scale of the product of its read's P so far, X's factor: at most the product of
+  // their bounds.  (The factor itself may peak anywhere, and what its scale has to spare costs
+  // nothing: a pair's finest step is 2^-39 of the bound.)
+  float q_scale[FLCE_MUON_MAX_STEPS];
+};
+
+// False where some step could take a singular value past 1.95, or shift A's diagonal by more than 3
+// (b / 2c), beyond which A would not fit its scale.
+bool muon_schedule(const flce_muon_t& o, MuonSchedule* out) {
+  double top = 1.0 + 1.0 / 256, p_most = 0.0, q_most = 1.0, growth = 1.0;
+  out->reads = 0;
   for (int k = 0; k < o.steps; ++k) {
     const double a = o.coefficients[3 * k], b = o.coefficients[3 * k + 1], c = o.coefficients[3 * k + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     if (c != 0.0 && std::abs(b) > 6.0 * std::abs(c)) return false;
     const MuonBound m = muon_bound(a, b, c, top);
     p_most = std::max(p_most, m.p);
-    q_most *= m.p;
     top = m.sp * (1.0 + 1.0 / 256);
     if (!(top <= 1.95) || !(p_most <= 1e4)) return false;
-    q_scale[k] = static_cast<float>(std::exp2(std::floor(std::log2(45000.0 / std::max(q_most, 1e-3)))));
+    if (k == 0 || growth > kMuonReadGrowth) {
+      out->first[out->reads++] = k;
+      q_most = growth = 1.0;
+    }
+    q_most *= m.p;
+    growth *= std::max(m.p, 1.0);
+    out->q_scale[k] = static_cast<float>(std::exp2(std::floor(std::log2(45000.0 / std::max(q_most, 1e-3)))));
   }
-  *p_scale = static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(p_most, 1e-3)))));
+  out->first[out->reads] = o.steps;
+  out->p_scale = static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(p_most, 1e-3)))));
   return true;
 }
 
@@ -2033,7 +2048,7 @@ struct MuonMaps {
 };
 
 // (Only those that some launch takes: an encoding costs 0.4 us.)
-bool muon_maps(const MuonPlanGroup& g, int steps, uint8_t* ws, MuonMaps* m) {
+bool muon_maps(const MuonPlanGroup& g, int steps, int reads, uint8_t* ws, MuonMaps* m) {
   const uint64_t r = g.r(), n = g.items.size();
   const uint64_t xp = 2 * static_cast<uint64_t>(g.xp()), ap = 2 * static_cast<uint64_t>(g.ap());
   auto all = [&](MuonMap* t, size_t at, uint64_t rows, uint64_t cols, uint64_t pitch, bool operand, bool output) {
@@ -2042,13 +2057,13 @@ bool muon_maps(const MuonPlanGroup& g, int steps, uint8_t* ws, MuonMaps* m) {
     };
     return (!output || one(&t->b32, 32)) && (!operand || (one(&t->b128, 128) && one(&t->b64, 64)));
   };
-  const bool exact = g.exact(), again = !exact && steps > 1;
+  const bool exact = g.exact(), again = (exact ? reads : steps) > 1;
   if (!all(&m->x[0], g.x[0], g.rows, g.cols, xp, true, again) || !all(&m->x[1], g.x[1], g.rows, g.cols, xp, again, true))
     return false;
   // the exact ones' lo is an operand and an output of its own, the others' is replaced in place
-  if (!all(&m->xlo[0], g.xlo[0], g.rows, g.cols, xp, exact, !exact)) return false;
+  if (!all(&m->xlo[0], g.xlo[0], g.rows, g.cols, xp, exact, !exact || again)) return false;
   if (exact) {
-    if (!all(&m->xlo[1], g.xlo[1], g.rows, g.cols, xp, false, true)) return false;
+    if (!all(&m->xlo[1], g.xlo[1], g.rows, g.cols, xp, again, true)) return false;
     return all(&m->p, g.p, r, r, ap, true, false) && all(&m->plo, g.plo, r, r, ap, true, false);
   }
   m->xlo[1] = m->xlo[0];
@@ -2077,12 +2092,12 @@ int muon_tile_width(const MuonRound& round, int groups, int mode, int sms) {
   return 6 * ((narrow + pairs - 1) / pairs) < 10 * ((wide + pairs - 1) / pairs) ? 128 : 256;
 }
 
-// One launch's groups: product `mode` of step k.
+// One launch's groups: product `mode` of step k, of the exact ones' k-th read of X.
 template <int G>
 void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int groups, int mode, int k, int bn,
-               const flce_muon_t& o, float p_scale, float q_scale, uint8_t* ws, MuonArgs<G>* out) {
+               const flce_muon_t& o, const MuonSchedule& sch, uint8_t* ws, MuonArgs<G>* out) {
   const double ca = o.coefficients[3 * k], cb = o.coefficients[3 * k + 1], cc = o.coefficients[3 * k + 2];
-  const double xs = kMuonXScale, as = kMuonAScale, ps = p_scale;
+  const double xs = kMuonXScale, as = kMuonAScale, ps = sch.p_scale;
   const int cur = k & 1;
   out->groups = groups;
   int tiles = 0;
@@ -2128,7 +2143,7 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int gr
       else operands(m.p, m.plo, m.x[cur], m.xlo[cur]);
       t.out = m.x[cur ^ 1].b32;
       t.out_lo = m.xlo[cur ^ 1].b32;
-      t.alpha = static_cast<float>(1.0 / (g.exact() ? q_scale : ps));
+      t.alpha = static_cast<float>(1.0 / (g.exact() ? sch.q_scale[sch.first[k + 1] - 1] : ps));
       t.beta = static_cast<float>(ca);
       t.lo_in = !g.exact() && k < kMuonPairSteps;
       t.write_lo = g.exact() || (k + 1 < kMuonPairSteps && k + 1 < o.steps);
@@ -2140,17 +2155,19 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int gr
   out->tiles = tiles;
 }
 
-// The steps of the groups from `first` on.
-void muon_chain(const MuonRound& round, int first, const flce_muon_t& o, float p_scale, const float* q_scale,
+// The steps of one read of X, of the groups from `first` on.
+void muon_chain(const MuonRound& round, int first, const flce_muon_t& o, const MuonSchedule& sch, int read,
                 uint8_t* ws, MuonChain* out) {
-  for (int k = 0; k < o.steps; ++k) {
-    out->a[k] = static_cast<float>(o.coefficients[3 * k]);
-    out->b[k] = static_cast<float>(o.coefficients[3 * k + 1]);
-    out->c[k] = static_cast<float>(o.coefficients[3 * k + 2]);
-    out->q_scale[k] = q_scale[k];
+  const int from = sch.first[read];
+  out->steps = sch.first[read + 1] - from;
+  for (int k = 0; k < out->steps; ++k) {
+    const double* abc = o.coefficients + 3 * (from + k);
+    out->a[k] = static_cast<float>(abc[0]);
+    out->b[k] = static_cast<float>(abc[1]);
+    out->c[k] = static_cast<float>(abc[2]);
+    out->q_scale[k] = sch.q_scale[from + k];
   }
-  out->p_scale = p_scale;
-  out->steps = o.steps;
+  out->p_scale = sch.p_scale;
   out->timeout_ns = timeout_ns();
   out->status = reinterpret_cast<int*>(ws);
   for (size_t i = first; i < round.groups.size(); ++i) {
@@ -2170,7 +2187,7 @@ void muon_chain(const MuonRound& round, int first, const flce_muon_t& o, float p
 // One round's launches; `first`: of the call.
 template <int N, int G>
 flce_status_t run_muon_round(const std::vector<MuonItem>& items, const MuonRound& round, const flce_muon_t& o,
-                             float p_scale, const float* q_scale, const float* grad_scale, uint8_t* base, bool first,
+                             const MuonSchedule& sch, const float* grad_scale, uint8_t* base, bool first,
                              const Device& dev, cudaStream_t s) {
   flce_status_t st = FLCE_OK;
   MuonSources<N> src;
@@ -2188,7 +2205,7 @@ flce_status_t run_muon_round(const std::vector<MuonItem>& items, const MuonRound
   std::vector<MuonMaps> maps(round.groups.size());
   for (size_t i = 0; i < round.groups.size(); ++i) {
     const MuonPlanGroup& g = round.groups[i];
-    if (!muon_maps(g, o.steps, base, &maps[i])) return FLCE_ERR_CUDA;
+    if (!muon_maps(g, o.steps, sch.reads, base, &maps[i])) return FLCE_ERR_CUDA;
     for (size_t j = 0; j < g.items.size(); ++j) {
       const MuonItem& m = items[g.items[j]];
       const size_t at = j * static_cast<size_t>(g.rows * g.xp());
@@ -2213,8 +2230,8 @@ flce_status_t run_muon_round(const std::vector<MuonItem>& items, const MuonRound
       t.flags = m.flags | (aligned(m.grad, gf ? 16 : 8) && aligned(m.momentum, 16) ? kMuonAligned : 0u);
       src.chunk0[src.count] = static_cast<uint32_t>(chunks);
       src.strip0[src.count] = static_cast<uint32_t>(strips);
-      w.hi = half(g.x[g.exact() ? 1 : o.steps & 1]);  // (the exact ones' X is multiplied once)
-      w.lo = g.exact() ? half(g.xlo[1]) : nullptr;
+      w.hi = half(g.x[(g.exact() ? sch.reads : o.steps) & 1]);
+      w.lo = g.exact() ? half(g.xlo[sch.reads & 1]) : nullptr;
       w.out = m.out;
       w.param = m.param;
       w.master = m.master;
@@ -2246,17 +2263,18 @@ flce_status_t run_muon_round(const std::vector<MuonItem>& items, const MuonRound
   const int all = static_cast<int>(round.groups.size()), plain = round.plain();
   for (int k = 0; k < o.steps; ++k) {
     for (int mode : {kMuonGram, kMuonPoly, kMuonApply}) {
-      if (mode == kMuonApply && k == 0 && plain < all) {
+      const bool read = k < sch.reads;  // the exact ones take part
+      if (mode == kMuonApply && read && plain < all) {
         MuonChain chain{};
-        muon_chain(round, plain, o, p_scale, q_scale, base, &chain);
+        muon_chain(round, plain, o, sch, k, base, &chain);
         st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_chain(chain, s); }));
         if (st != FLCE_OK) return st;
       }
       if (mode == kMuonPoly && o.coefficients[3 * k + 2] == 0.0) continue;  // (kGram wrote P)
-      const int groups = k == 0 && mode != kMuonPoly ? all : plain;  // the exact ones take part once
+      const int groups = read && mode != kMuonPoly ? all : plain;
       if (groups == 0) continue;
       const int bn = muon_tile_width(round, groups, mode, dev.sms);
-      muon_args(round, maps, groups, mode, k, bn, o, p_scale, q_scale[o.steps - 1], base, &args);
+      muon_args(round, maps, groups, mode, k, bn, o, sch, base, &args);
       st = cuda_status(timed(3, 0.0, s, [&] { return launch_muon_product(mode, bn, args, dev.sms, s); }));
       if (st != FLCE_OK) return st;
     }
@@ -2268,8 +2286,8 @@ flce_status_t run_muon_round(const std::vector<MuonItem>& items, const MuonRound
 
 flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o, const float* grad_scale, void* ws,
                        size_t ws_bytes, cudaStream_t s) {
-  float p_scale = 1.f, q_scale[FLCE_MUON_MAX_STEPS] = {};
-  if (!muon_scales(o, &p_scale, q_scale)) return FLCE_ERR_INVALID_ARGUMENT;
+  MuonSchedule sch;
+  if (!muon_schedule(o, &sch)) return FLCE_ERR_INVALID_ARGUMENT;
   const std::vector<MuonRound> rounds = muon_rounds(items);
   if (ws_bytes < muon_bytes(rounds)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -2280,8 +2298,8 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
   for (size_t n = 0; n < rounds.size(); ++n) {
     const MuonRound& round = rounds[n];
     const bool few = round.matrices <= kMuonFewMatrices && round.groups.size() <= kMuonFewGroups;
-    st = few ? run_muon_round<kMuonFewMatrices, kMuonFewGroups>(items, round, o, p_scale, q_scale, grad_scale, base, n == 0, dev, s)
-             : run_muon_round<kMuonMatrices, kMuonGroups>(items, round, o, p_scale, q_scale, grad_scale, base, n == 0, dev, s);
+    st = few ? run_muon_round<kMuonFewMatrices, kMuonFewGroups>(items, round, o, sch, grad_scale, base, n == 0, dev, s)
+             : run_muon_round<kMuonMatrices, kMuonGroups>(items, round, o, sch, grad_scale, base, n == 0, dev, s);
     if (st != FLCE_OK) return st;
   }
   return FLCE_OK;

@@ -455,6 +455,13 @@ constexpr int kMuonFewGroups = 2, kMuonFewMatrices = 16;
 constexpr int kMuonChunk = 8192;     // elements of one block of the momentum's pass
 constexpr int kMuonStrip = 4096;     // and of the passes between a tensor and X
 constexpr int kMuonExactRows = 128;  // up to this many rows or columns: pairs of fp16, steps on X X^T alone
+// The steps on X X^T go on until singular values may have grown this much, then X is read again: an
+// error d of an eigenvalue grows with the square of what singular values do, and counts as
+// |b| / a d 144^2 then in the weakest directions' factor.  d is up to 2^-22 by its pair and 5e-8 by fp32 sums:
+// 2e-3 to 7e-3 of these directions.  The usual coefficients reach 141 before the fifth step, 485
+// before a sixth, which on 128 x 128 with strong directions is off by 1e-3, an eighth step
+// by 2e-2 and a twelfth by infinities; with reads every five steps 1e-4 for all (simulated).
+constexpr double kMuonReadGrowth = 144.0;
 constexpr int kMuonSplitBlocks = 8;  // of 64 elements, of one part of their X X^T
 constexpr int kMuonSplitsMost = 64;
 constexpr int kMuonPairSteps = 3;    // else for the first iterates alone
@@ -489,8 +496,8 @@ struct MuonArgs {
   int* status;
 };
 static_assert(sizeof(MuonArgs<kMuonGroups>) <= 32764, "kernel argument limit");
-// The steps of the matrices of at most kMuonExactRows rows, from X X^T to the product Q of all
-// steps' P, a block each.
+// The steps of the matrices of at most kMuonExactRows rows between two reads of X, from X X^T to
+// the product Q of their P, a block each.
 struct MuonChainGroup {
   const float* part;   // X X^T in kGram's parts, in units of 1 / kMuonAScale
   int splits;

@@ -38,7 +38,9 @@
 // product hi hi + hi lo + lo hi, and the steps run on A alone,
 //   P = a I + b A + c A^2,   Q <- P Q,   A <- P A P,
 // X being read twice, for X X^T and for Q X: 1e-4 of the result, up to 2e-3 where strong
-// directions outweigh weak ones 1000 to 1.
+// directions outweigh weak ones 1000 to 1.  A's rounding hides the squares of weak singular
+// values, so after as many steps as that bears (kMuonReadGrowth; the usual coefficients' five)
+// X <- Q X and the next steps start from a new X X^T.
 #include <cuda_fp16.h>
 
 #include "flce_device.cuh"
@@ -545,7 +547,7 @@ __device__ __forceinline__ void chain_store(uint8_t* m, int row, int c0, const f
   }
 }
 
-// All of a matrix's steps in one block: operands in shared memory, one thread issues the products,
+// All of a matrix's steps on one X X^T in one block: operands in shared memory, one thread issues the products,
 // a thread of the eight warps holds half a row of their results.  Symmetric operands are K-major
 // on either side.
 //   128 x 128, five steps: 48 us, of which 14 rounds of products (30 of 128 x 128 x 128, three each)

@@ -78,3 +78,40 @@ def test_products_of_the_steps_that_peak_anywhere(r, c):
     u = with_values(r, c, [math.sqrt(1 - (m - 1) * s * s)] + [s] * (m - 1)).cuda()
     error, floor = off(u, PEAK)
     assert error <= PROMISE + floor
+
+
+def matrix(r, c, kind, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    noise = torch.randn(r, c, generator=g)
+
+    def directions(k):
+        return torch.randn(r, k, generator=g) @ torch.randn(k, c, generator=g)
+    return {"noise": lambda: noise, "same": lambda: torch.eye(r, c),
+            "strong": lambda: directions(8) + 0.05 * noise,   # eight directions over noise
+            "rank8": lambda: directions(8) + 0.003 * noise,   # over a thousandth of it
+            "rank1": lambda: directions(1),                   # over nothing at all
+            "decay": lambda: with_values(r, c, torch.logspace(0, -5, min(r, c)), seed)}[kind]()
+
+
+SCHEDULES = {"usual 6": [USUAL] * 6, "usual 8": [USUAL] * 8, "usual 10": [USUAL] * 10, "usual 16": [USUAL] * 16,
+             "cubic 16": [(1.5, -0.5, 0.0)] * 16, "quintic 16": [(1.875, -1.25, 0.375)] * 16,
+             "mixed": [USUAL] * 7 + [(1.875, -1.25, 0.375)] * 3}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["noise", "strong", "rank8", "rank1", "decay"])
+@pytest.mark.parametrize("r,c", [(64, 200), (128, 128), (300, 100), (128, 1544)])
+@pytest.mark.parametrize("schedule", SCHEDULES)
+def test_few_rows_and_many_steps(r, c, kind, schedule):
+    error, floor = off(matrix(r, c, kind).cuda(), SCHEDULES[schedule])
+    assert error <= PROMISE + floor
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps", [6, 11, 16])
+def test_few_rows_beside_many_of_them(steps):
+    """One call's matrices read X a few times or at every step: the same bits as each alone."""
+    xs = [matrix(r, c, "strong", r).cuda() for r, c in ((300, 200), (40, 60), (128, 640), (200, 300), (7, 5))]
+    got = flce.orthogonalize(xs, steps=steps, check=True)
+    for x, y in zip(xs, got):
+        assert torch.equal(y, flce.orthogonalize(x, steps=steps))
