@@ -2011,18 +2011,21 @@ struct MuonSchedule {
   // their bounds.  (The factor itself may peak anywhere, and what its scale has to spare costs
   // nothing: a pair's finest step is 2^-39 of the bound.)
   float q_scale[FLCE_MUON_MAX_STEPS];
+  // The other matrices' iterates that are kept as pairs.
+  bool paired[FLCE_MUON_MAX_STEPS + 1];
 };
 
 // False where some step could take a singular value past 1.95, or shift A's diagonal by more than 3
 // (b / 2c), beyond which A would not fit its scale.
 bool muon_schedule(const flce_muon_t& o, MuonSchedule* out) {
-  double top = 1.0 + 1.0 / 256, p_most = 0.0, q_most = 1.0, growth = 1.0;
+  double top = 1.0 + 1.0 / 256, p_most = 0.0, q_most = 1.0, growth = 1.0, most[FLCE_MUON_MAX_STEPS];
   out->reads = 0;
   for (int k = 0; k < o.steps; ++k) {
     const double a = o.coefficients[3 * k], b = o.coefficients[3 * k + 1], c = o.coefficients[3 * k + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     if (c != 0.0 && std::abs(b) > 6.0 * std::abs(c)) return false;
     const MuonBound m = muon_bound(a, b, c, top);
+    most[k] = m.p;
     p_most = std::max(p_most, m.p);
     top = m.sp * (1.0 + 1.0 / 256);
     if (!(top <= 1.95) || !(p_most <= 1e4)) return false;
@@ -2035,6 +2038,14 @@ bool muon_schedule(const flce_muon_t& o, MuonSchedule* out) {
     out->q_scale[k] = static_cast<float>(std::exp2(std::floor(std::log2(45000.0 / std::max(q_most, 1e-3)))));
   }
   out->first[out->reads] = o.steps;
+  std::fill(out->paired, out->paired + FLCE_MUON_MAX_STEPS + 1, false);
+  double left = 0.0;  // by what the steps multiply roundings of the iterates from k on, added up
+  for (int k = o.steps - 1; k >= 0; --k) {
+    double own = 1.0;
+    for (int j = k; j < o.steps; ++j) own *= most[j];
+    left += own;
+    out->paired[k] = k < kMuonPairSteps || left > kMuonPairGrowth;
+  }
   out->p_scale = static_cast<float>(std::exp2(std::floor(std::log2(60000.0 / std::max(p_most, 1e-3)))));
   return true;
 }
@@ -2145,8 +2156,8 @@ void muon_args(const MuonRound& round, const std::vector<MuonMaps>& maps, int gr
       t.out_lo = m.xlo[cur ^ 1].b32;
       t.alpha = static_cast<float>(1.0 / (g.exact() ? sch.q_scale[sch.first[k + 1] - 1] : ps));
       t.beta = static_cast<float>(ca);
-      t.lo_in = !g.exact() && k < kMuonPairSteps;
-      t.write_lo = g.exact() || (k + 1 < kMuonPairSteps && k + 1 < o.steps);
+      t.lo_in = !g.exact() && sch.paired[k];
+      t.write_lo = g.exact() || sch.paired[k + 1];
     }
     t.tiles_each = static_cast<int>(muon_tiles_each(g, mode, bn));
     t.tile0 = tiles;

@@ -464,7 +464,15 @@ constexpr int kMuonExactRows = 128;  // up to this many rows or columns: pairs o
 constexpr double kMuonReadGrowth = 144.0;
 constexpr int kMuonSplitBlocks = 8;  // of 64 elements, of one part of their X X^T
 constexpr int kMuonSplitsMost = 64;
-constexpr int kMuonPairSteps = 3;    // else for the first iterates alone
+// Larger matrices' iterates are pairs too, but for the last: a rounding to one fp16 leaves 2e-4 of
+// X's norm in its weak directions, which the remaining steps multiply by up to their slopes at 0.  Iterates are
+// single from where these products add up to at most 16 (usual coefficients: the last two, 3.4 + 11.9; the
+// first three are pairs however gentle the steps).  Of 300 x 777 with eight directions over 0.2% of noise
+// the result is off by 3e-3 after five usual steps (2e-3 with all as pairs), 2e-3 after six, 7e-4 after
+// eight; with three pairs for any number of steps by 7e-3 and 9e-3, without noise 0.2 after eight
+// (simulated).  A pair costs P X 10 us of 45 more for 40M elements.
+constexpr int kMuonPairSteps = 3;
+constexpr double kMuonPairGrowth = 16.0;
 constexpr float kMuonXScale = 16384.f, kMuonAScale = 8192.f;
 enum MuonMode : int { kMuonGram, kMuonPoly, kMuonApply };
 enum : uint32_t {

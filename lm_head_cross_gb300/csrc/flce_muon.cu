@@ -29,7 +29,8 @@
 //
 // A rounded X also carries noise of 2^-12 of its strong directions into its weak ones, which then
 // grow faster, by up to a in each step (|u| of rank 8 with 2% of noise: 1.4e-2 of the result).
-// So the first kMuonPairSteps iterates are kept as a pair hi + lo of fp16, 22 bits.  The products
+// So the iterates are kept as a pair hi + lo of fp16, 22 bits, but for the last ones, whose noise few
+// steps are left to raise (kMuonPairGrowth).  The products
 // use hi alone and the epilogue adds a lo: what P lo - a lo would add lies along the strong
 // directions themselves, where it does no harm (1.0e-3 of the result then).
 //
