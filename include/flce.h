@@ -531,15 +531,15 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
  *   - Products take fp16 operands with power-of-two scales and accumulate in
  *     fp32; rounding leaves 3e-4 (one step) to 4e-3 of X's norm, 1e-3 after five
  *     usual steps of noise (bf16's own is 1.7e-3); up to 6e-3 where a few directions
- *     hold nearly all of u, and 1.2e-2 where most singular values are equal, so that
- *     all roundings agree.
+ *     hold nearly all of u, and 1.2e-2 there with slopes a beyond 4, or where most
+ *     singular values are equal, so that all roundings agree.
  *     Matrices of at most 128 rows or columns carry 22 bits: 1e-5 to 5e-4 of X's
  *     norm, up to 2e-3 with 2^24 columns or 16 usual steps, and 3e-3 where one
  *     direction holds nearly all of u.  Momentum, norm and the weights' update are
  *     fp32.  As in 32-bit arithmetic, directions that hold less than about 1e-6 of
  *     u's norm are the rounding's, and grow like others with the product of the
  *     slopes a (2e5 for ten usual steps, 1e6 for eleven).
- *   - The coefficients must keep singular values in [0, 1] within 1.95 at every
+ *   - The coefficients must keep singular values in [0, 1] within 2.1 at every
  *     step, and c must be 0 or |b| <= 6 |c| (FLCE_ERR_INVALID_ARGUMENT otherwise).
  *   - A matrix of zeros becomes zeros.  One with a non-finite element, or whose
  *     squares sum past fp32's range, becomes NaN as a whole, no other does.

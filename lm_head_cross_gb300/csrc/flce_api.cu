@@ -2015,20 +2015,20 @@ struct MuonSchedule {
   bool paired[FLCE_MUON_MAX_STEPS + 1];
 };
 
-// False where some step could take a singular value past 1.95, or shift A's diagonal by more than 3
-// (b / 2c), beyond which A would not fit its scale.
+// False where some step could take a singular value past kMuonMostX, or shift A's diagonal by more
+// than kMuonMostShift (b / 2c), beyond which A would not fit its scale.
 bool muon_schedule(const flce_muon_t& o, MuonSchedule* out) {
   double top = 1.0 + 1.0 / 256, p_most = 0.0, q_most = 1.0, growth = 1.0, most[FLCE_MUON_MAX_STEPS];
   out->reads = 0;
   for (int k = 0; k < o.steps; ++k) {
     const double a = o.coefficients[3 * k], b = o.coefficients[3 * k + 1], c = o.coefficients[3 * k + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
-    if (c != 0.0 && std::abs(b) > 6.0 * std::abs(c)) return false;
+    if (c != 0.0 && std::abs(b) > 2.0 * kMuonMostShift * std::abs(c)) return false;
     const MuonBound m = muon_bound(a, b, c, top);
     most[k] = m.p;
     p_most = std::max(p_most, m.p);
     top = m.sp * (1.0 + 1.0 / 256);
-    if (!(top <= 1.95) || !(p_most <= 1e4)) return false;
+    if (!(top <= kMuonMostX) || !(p_most <= 1e4)) return false;
     if (k == 0 || growth > kMuonReadGrowth) {
       out->first[out->reads++] = k;
       q_most = growth = 1.0;

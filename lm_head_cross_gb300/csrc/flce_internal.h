@@ -474,6 +474,10 @@ constexpr int kMuonSplitsMost = 64;
 constexpr int kMuonPairSteps = 3;
 constexpr double kMuonPairGrowth = 16.0;
 constexpr float kMuonXScale = 16384.f, kMuonAScale = 8192.f;
+// The largest singular value of X and shift of A's diagonal that coefficients may lead to: A, P A
+// and X stay below fp16's 65504.  (Schedules of steep first steps reach 2.)
+constexpr double kMuonMostX = 2.1, kMuonMostShift = 3.0;
+static_assert((kMuonMostX * kMuonMostX + kMuonMostShift) * kMuonAScale < 65000 && kMuonMostX * kMuonXScale < 65000, "fp16");
 enum MuonMode : int { kMuonGram, kMuonPoly, kMuonApply };
 enum : uint32_t {
   kMuonParamF32 = 1,

@@ -22,7 +22,7 @@
 // What rounding the diagonal to fp16 leaves, up to 2^-11 of b / 2c where A's own is far smaller, is
 // kept in fp32 for P's diagonal.
 //
-// fp16, not bf16: singular values stay below 2 whatever the input, so that every scale is a power
+// fp16, not bf16: singular values stay below 2.1 whatever the input, so that every scale is a power
 // of two known beforehand (X 2^14, A 2^13, P by its polynomial's largest value) and the 3 bits
 // more are free: rounding errors, which the steps amplify, leave 1e-3 of the result's norm, less
 // than its own rounding to bf16 (1.7e-3); bf16 operands would leave 1e-2.

@@ -10,6 +10,7 @@ u's.  It grows like the singular values of its directions, by at most the produc
 there on, where a slope may still exceed 1.  nu = 2^-20: pairs of fp16 are off by 2^-23 of an element, the sums
 of 24 products of 16 terms in Q X by 2^-23 of the running sum each time, 5 of those in the mean (their
 root): 6 2^-23.  Where nu grows to order one X is as large as its directions are many."""
+import ctypes
 import math
 
 import pytest
@@ -17,11 +18,12 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import lm_head_cross_gb300 as flce  # noqa: E402
+from lm_head_cross_gb300 import binding, muon  # noqa: E402
 
 USUAL = (3.4445, -4.7750, 2.0315)
 PROMISE = 2e-3  # of up to 128 rows or columns
 PROMISE_MANY = 6e-3  # of more
-PROMISE_EQUAL = 1.2e-2  # where most singular values are equal
+PROMISE_EQUAL = 1.2e-2  # where most singular values are equal, or slopes pass 4
 
 
 def exact(u, coefficients, eps=1e-7):
@@ -125,3 +127,47 @@ def test_few_rows_beside_many_of_them(steps):
 def test_many_rows_and_many_steps(r, c, kind, schedule):
     error, floor = off(matrix(r, c, kind).cuda(), SCHEDULES[schedule])
     assert error <= (PROMISE_EQUAL if kind == "same" else PROMISE_MANY) + floor
+
+
+#: the Polar Express schedule (Amsel, Persson, Musco, Gower 2025) with its safety factor of 1.01
+POLAR = [(a / 1.01, b / 1.01 ** 3, c / 1.01 ** 5) for a, b, c in
+         ((8.28721201814563, -23.595886519098837, 17.300387312530933),
+          (4.107059111542203, -2.9478499167379106, 0.5448431082926601),
+          (3.9486908534822946, -2.908902115962949, 0.5518191394370137),
+          (3.3184196573706015, -2.488488024314874, 0.51004894012372),
+          (2.300652019954817, -1.6689039845747493, 0.4188073119525673),
+          (1.891301407787398, -1.2679958271945868, 0.37680408948524835),
+          (1.8750014808534479, -1.2500016453999487, 0.3750001645474248))] + [(1.875, -1.25, 0.375)]
+
+
+def code(coefficients):
+    o = muon._options(0.0, False, len(coefficients), coefficients, 1e-7)
+    return flce.lib().flce_orthogonalize((binding.Matrix * 1)((0x1000, 0x2000, 8, 8, 0)), 1, ctypes.byref(o), 0x100000,
+                                         0, None)
+
+
+def test_singular_values_of_up_to_2_1_are_taken():
+    """(4: all is well but the workspace's size.)"""
+    for n in range(1, 9):
+        assert code(POLAR[:n]) == 4
+    assert code([(2.05, 0.0, 0.0)]) == 4 and code([(2.1, 0.0, 0.0)]) == 1
+    assert code([(2.05, 0.0, 0.0), (0.9, 0.0, 0.0)]) == 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["noise", "strong", "same", "rank8", "rank1", "decay"])
+@pytest.mark.parametrize("r,c", [(64, 200), (128, 128), (300, 777), (640, 400)])
+@pytest.mark.parametrize("steps", [1, 5, 8, 16])
+def test_steep_first_steps(r, c, kind, steps):
+    error, floor = off(matrix(r, c, kind).cuda(), POLAR[:steps] + POLAR[-1:] * (steps - 8))
+    assert error <= (PROMISE if min(r, c) <= 128 else PROMISE_EQUAL) + floor
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r,c", [(48, 96), (200, 300)])
+@pytest.mark.parametrize("second", [(0.9, -0.06, 0.01), (0.9, 0.06, -0.01), (0.5, 0.06, 0.01)])
+def test_the_largest_singular_value_and_shift(r, c, second):
+    """One direction at 2.05, where A and its shifted diagonal are largest."""
+    u = with_values(r, c, [1.0] + [1e-3] * (min(r, c) - 1)).cuda()
+    error, floor = off(u, [(2.05, 0.0, 0.0), second])
+    assert error <= (PROMISE if min(r, c) <= 128 else PROMISE_EQUAL) + floor
