@@ -12,7 +12,7 @@ import math
 
 from .binding import (FlceError, Matrix, MuonOptions, MuonTensor, _allocating, _call, _check_device, _dtype,
                       _record, _stream_ptr, _torch, lib, read_device_status)
-from .optim import _check
+from .optim import _check, _contiguous
 
 #: Newton-Schulz coefficients (a, b, c) of X <- a X + (b X X^T + c (X X^T)^2) X, for every step
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
@@ -285,11 +285,7 @@ class Muon:
         for i, p in enumerate(self.params):  # a parameter may have been given new storage
             if p.data_ptr() != self.plan.table[i].param:
                 self.plan.set_param(i, p.detach())
-        grads = [p.grad for p in self.params]
-        if any(g is not None and not g.is_contiguous() for g in grads):
-            with _allocating(stream):  # copied on the step's stream
-                grads = [None if g is None else g.contiguous() for g in grads]
-        muon_step(self.plan, grads, grad_scale, stream=stream)
+        muon_step(self.plan, _contiguous([p.grad for p in self.params], stream), grad_scale, stream=stream)
 
     def zero_grad(self):
         for p in self.params:

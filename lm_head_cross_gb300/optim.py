@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import AdamwOptions, AdamwTensor, _allocating, _call, _check_device, _stream_ptr, _torch, lib
+from .binding import AdamwOptions, AdamwTensor, _allocating, _call, _check_device, _record, _stream_ptr, _torch, lib
 
 BLOCK = 256  # elements that share one scale of an 8-bit moment
 
@@ -30,6 +30,17 @@ def _check(t, name, like=None, dtype=None, count=None):
     want = like.numel() if count is None else count
     if t.numel() != want:
         raise ValueError(f"{name} must have {want} elements, got {t.numel()}")
+
+
+def _contiguous(grads, stream):
+    """The gradients, those of other layouts copied on the step's stream.  That stream reads what it
+    copies, so they are recorded on it too."""
+    if all(g is None or g.is_contiguous() for g in grads):
+        return grads
+    with _allocating(stream):
+        copies = [None if g is None else g.contiguous() for g in grads]
+    _record(stream, *(g for g, c in zip(grads, copies) if c is not g))
+    return copies
 
 
 class AdamWPlan:
