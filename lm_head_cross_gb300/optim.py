@@ -219,10 +219,7 @@ class AdamW:
         grads = [p.grad for p in self.params]
         if all(g is None for g in grads):
             return
-        if any(g is not None and not g.is_contiguous() for g in grads):
-            with _allocating(stream):  # copied on the step's stream
-                grads = [None if g is None else g.contiguous() for g in grads]
-        adamw_step(self.plan, grads, self.steps + 1, grad_scale, stream)
+        adamw_step(self.plan, _contiguous(grads, stream), self.steps + 1, grad_scale, stream)
         self.steps += 1
 
     def zero_grad(self):

@@ -59,7 +59,7 @@ def fake(monkeypatch):
 
 
 @pytest.mark.parametrize("stream", [None, Stream(0)], ids=["current", "given"])
-@pytest.mark.parametrize("kind", [flce.Muon])
+@pytest.mark.parametrize("kind", [flce.Muon, flce.AdamW], ids=lambda k: k.__name__)
 def test_gradients_that_a_step_copies_are_recorded(fake, kind, stream):
     """The copy is made on the step's stream: what it reads may be freed after the call as well."""
     opt = optimizer(kind)
