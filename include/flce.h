@@ -551,7 +551,9 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
  *   - ws: the workspace size below (0 if an entry is invalid), 256-byte aligned,
  *     status word at its start: the operands of a round of matrices, about 10
  *     bytes an element (up to 128 rows: 8 to 16, and a 64 KB part for every 512
- *     columns, 64 parts at most), up to 4 GiB unless one matrix alone takes more. */
+ *     columns, 64 parts at most), up to 4 GiB unless one matrix alone takes more.
+ *     flce_muon_workspace_bytes is enough for a step that leaves any of the
+ *     tensors out (rows or cols of 0: their gradients are missing), too. */
 #define FLCE_MUON_MAX_STEPS 16
 
 typedef struct {

@@ -1898,6 +1898,30 @@ constexpr size_t kMuonRoundBytes = size_t{4} << 30;  // of a round of several ma
 
 int64_t muon_chunks(const MuonItem& m) { return (m.rows * m.cols + kMuonChunk - 1) / kMuonChunk; }
 
+void muon_layout(MuonRound* r) {
+  size_t off = kAlign;  // after the status word
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off = align_up(off + n);
+    return at;
+  };
+  r->part = take(sizeof(float) * static_cast<size_t>(r->chunks));
+  for (MuonPlanGroup& g : r->groups) {
+    const size_t count = g.items.size();
+    const size_t xb = 2 * count * static_cast<size_t>(g.rows * g.xp()), ab = 2 * count * static_cast<size_t>(g.r() * g.ap());
+    g.x[0] = take(xb);
+    g.x[1] = take(xb);
+    g.xlo[0] = take(xb);
+    g.xlo[1] = g.exact() ? take(xb) : g.xlo[0];
+    g.p = take(ab);
+    g.a = g.exact() ? 0 : take(ab);
+    g.diag = g.exact() ? 0 : take(sizeof(float) * count * static_cast<size_t>(g.r()));
+    g.plo = g.exact() ? take(ab) : 0;
+    g.part = g.exact() ? take(count * muon_part_bytes(g.c())) : 0;
+  }
+  r->total = off;
+}
+
 // The call's matrices by shape, the largest first, cut into rounds.
 std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
   std::vector<int> by(items.size());
@@ -1930,29 +1954,7 @@ std::vector<MuonRound> muon_rounds(const std::vector<MuonItem>& items) {
     r.chunks += muon_chunks(m);
     bytes += more;
   }
-  for (MuonRound& r : rounds) {
-    size_t off = kAlign;  // after the status word
-    auto take = [&](size_t n) {
-      const size_t at = off;
-      off = align_up(off + n);
-      return at;
-    };
-    r.part = take(sizeof(float) * static_cast<size_t>(r.chunks));
-    for (MuonPlanGroup& g : r.groups) {
-      const size_t count = g.items.size();
-      const size_t xb = 2 * count * static_cast<size_t>(g.rows * g.xp()), ab = 2 * count * static_cast<size_t>(g.r() * g.ap());
-      g.x[0] = take(xb);
-      g.x[1] = take(xb);
-      g.xlo[0] = take(xb);
-      g.xlo[1] = g.exact() ? take(xb) : g.xlo[0];
-      g.p = take(ab);
-      g.a = g.exact() ? 0 : take(ab);
-      g.diag = g.exact() ? 0 : take(sizeof(float) * count * static_cast<size_t>(g.r()));
-      g.plo = g.exact() ? take(ab) : 0;
-      g.part = g.exact() ? take(count * muon_part_bytes(g.c())) : 0;
-    }
-    r.total = off;
-  }
+  for (MuonRound& r : rounds) muon_layout(&r);
   return rounds;
 }
 
@@ -1960,6 +1962,37 @@ size_t muon_bytes(const std::vector<MuonRound>& rounds) {
   size_t most = kAlign;
   for (const MuonRound& r : rounds) most = std::max(most, r.total);
   return most;
+}
+
+// What a step needs that takes any of the matrices.  One that leaves some out cuts its rounds
+// elsewhere, and a round of it may be larger than any of all matrices' (not where those fit one
+// round).  A round needs at most what its matrices need in rounds of their own, buffers rounded up
+// for each: of the 256 largest, or of what the bytes that bound a round leave room for.
+size_t muon_bytes_of_any(const std::vector<MuonItem>& items) {
+  const std::vector<MuonRound> rounds = muon_rounds(items);
+  if (rounds.size() <= 1) return muon_bytes(rounds);
+  std::vector<size_t> need, beyond;  // beyond what muon_matrix_bytes counts
+  size_t largest = 0;
+  for (const MuonItem& m : items) {
+    if (m.rows == 0 || m.cols == 0) continue;
+    MuonRound one;
+    one.groups.emplace_back();
+    one.groups.back().rows = m.rows;
+    one.groups.back().cols = m.cols;
+    one.groups.back().items.push_back(0);
+    one.chunks = muon_chunks(m);
+    muon_layout(&one);
+    largest = std::max(largest, one.total);
+    need.push_back(one.total - kAlign);
+    beyond.push_back(need.back() - muon_matrix_bytes(m.rows, m.cols));
+  }
+  auto most = [](std::vector<size_t>& v) {
+    std::sort(v.begin(), v.end(), [](size_t a, size_t b) { return a > b; });
+    size_t sum = 0;
+    for (size_t i = 0; i < std::min<size_t>(v.size(), kMuonMatrices); ++i) sum += v[i];
+    return sum;
+  };
+  return std::max(largest, kAlign + std::min(most(need), kMuonRoundBytes + most(beyond)));
 }
 
 flce_status_t check_muon_shape(int64_t rows, int64_t cols) {
@@ -2351,10 +2384,10 @@ flce_status_t muon_items(const flce_muon_tensor_t* x, int32_t count, std::vector
 }
 
 template <typename T>
-size_t muon_workspace(const T* x, int32_t count) try {
+size_t muon_workspace(const T* x, int32_t count, bool any) try {
   std::vector<MuonItem> items;
   if (count < 0 || (count > 0 && !x) || muon_items(x, count, &items) != FLCE_OK) return 0;
-  return muon_bytes(muon_rounds(items));
+  return any ? muon_bytes_of_any(items) : muon_bytes(muon_rounds(items));
 } catch (...) {
   return 0;
 }
@@ -2363,10 +2396,10 @@ size_t muon_workspace(const T* x, int32_t count) try {
 }  // extern "C++"
 
 size_t flce_orthogonalize_workspace_bytes(const flce_matrix_t* matrices, int32_t count) {
-  return muon_workspace(matrices, count);
+  return muon_workspace(matrices, count, false);
 }
 size_t flce_muon_workspace_bytes(const flce_muon_tensor_t* tensors, int32_t count) {
-  return muon_workspace(tensors, count);
+  return muon_workspace(tensors, count, true);
 }
 
 flce_status_t flce_orthogonalize(const flce_matrix_t* matrices, int32_t count, const flce_muon_t* opt, void* ws,

@@ -174,7 +174,7 @@ class MuonPlan:
 
     def workspace_bytes(self, live=None):
         """Workspace of a step in which the parameters that ``live`` (truth values; None: all) names
-        have a gradient."""
+        have a gradient, or any of them."""
         key = None if live is None or all(live) else tuple(live)
         if key not in self._bytes:
             table = (MuonTensor * max(len(self), 1))()

@@ -1,5 +1,6 @@
 """What the optimizers' steps do with memory that is not theirs (stand-ins as in test_ops_devices)."""
 import contextlib
+import random
 
 import pytest
 
@@ -71,3 +72,57 @@ def test_gradients_that_a_step_copies_are_recorded(fake, kind, stream):
     opt.step(stream=stream)
     for g in grads:
         assert getattr(g, "streams", []) == ([] if stream is None else [stream])
+
+
+def step_bytes(shapes):
+    table = (binding.MuonTensor * max(len(shapes), 1))()
+    for row, (r, c) in zip(table, shapes):
+        row.rows, row.cols = r, c
+    return binding.lib().flce_muon_workspace_bytes(table, len(shapes))
+
+
+def call_bytes(shapes):
+    """What exactly these need: orthogonalize's rounds are the same."""
+    table = (binding.Matrix * max(len(shapes), 1))(*((1, 1, r, c, 0) for r, c in shapes))
+    return binding.lib().flce_orthogonalize_workspace_bytes(table, len(shapes))
+
+
+def test_a_workspace_is_enough_where_gradients_are_missing():
+    """Rounds are cut anew: without the first 200 the others share one, which all of them do not."""
+    shapes = [(300, 310)] * 200 + [(299, 8000)] * 200
+    assert call_bytes(shapes[200:]) > call_bytes(shapes)
+    assert step_bytes(shapes) >= call_bytes(shapes[200:])
+    rng = random.Random(0)
+    for _ in range(40):
+        kinds = [(rng.randint(1, 900), rng.choice([rng.randint(1, 900), rng.randint(1, 90000)])) for _ in range(rng.randint(1, 30))]
+        shapes = [rng.choice(kinds) for _ in range(rng.randint(1, 700))]
+        most = step_bytes(shapes)
+        assert most >= call_bytes(shapes)
+        for _ in range(30):
+            some = set(rng.sample(kinds, rng.randint(1, len(kinds))))
+            part = rng.random()
+            live = [s for s in shapes if s in some or rng.random() < part]
+            assert call_bytes(live) <= most
+            assert step_bytes([s if s in some else (0, 0) for s in shapes]) <= most
+
+
+def test_a_workspace_of_one_round_is_what_it_takes():
+    for shapes in ([(300, 310)] * 200, [(64, 64), (4096, 4096), (5, 9000)], [(3, 0)], []):
+        assert step_bytes(shapes) == call_bytes(shapes)
+
+
+@pytest.mark.gpu
+def test_a_step_without_some_gradients_in_the_plans_workspace():
+    """18 shapes, 12 of a round: the last 12 share one only where the first have no gradient."""
+    shapes = [(300 + i, 310) for i in range(6)] + [(200, 1000 + 8 * i) for i in range(12)]
+    assert call_bytes(shapes[6:]) > call_bytes(shapes)
+    g = torch.Generator().manual_seed(0)
+    gs = [None if i < 6 else torch.randn(s, generator=g).cuda() for i, s in enumerate(shapes)]
+    results = []
+    for given in (True, False):
+        ps, ms = ([torch.zeros(s, device="cuda") for s in shapes] for _ in range(2))
+        plan = flce.muon_plan(ps, ms)
+        ws = torch.empty(plan.workspace_bytes(), dtype=torch.uint8, device="cuda") if given else None
+        flce.muon_step(plan, gs, ws=ws, check=True)
+        results.append(ps + ms)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
