@@ -545,8 +545,9 @@ flce_status_t flce_adamw_step(const flce_adamw_tensor_t* tensors, int32_t count,
  *     squares sum past fp32's range, becomes NaN as a whole, no other does.
  *   - Matrices are dense row-major, any number of rows and columns (the smaller
  *     up to 65536, the larger up to 2^20, or 2^24 where the smaller is at most 128;
- *     empty ones are skipped).  Pointers need the alignment of their type.  Outputs must not overlap one another or inputs
- *     (but out may be x where x is bf16).  Tensors are updated in place.
+ *     empty ones are skipped).  Pointers need the alignment of their type.  Tensors
+ *     are updated in place.  What is written must not overlap anything else of the
+ *     call (FLCE_ERR_INVALID_ARGUMENT), but out may be its own x where x is bf16.
  *   - matrices and tensors are HOST arrays, read before the call returns.
  *   - ws: the workspace size below (0 if an entry is invalid), 256-byte aligned,
  *     status word at its start: the operands of a round of matrices, about 10

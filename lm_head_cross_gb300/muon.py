@@ -19,12 +19,21 @@ COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 MAX_STEPS = 16
 
 
-def _distinct(names, tensors):
-    """A call writes each of its tensors: none may be there twice."""
-    seen = {}
-    for name, t in zip(names, tensors):
-        if t is not None and t.numel() and seen.setdefault(t.data_ptr(), name) != name:
-            raise ValueError(f"{name} and {seen[t.data_ptr()]} are the same memory")
+def _apart(written, read=()):
+    """What a call writes must not overlap anything else that it writes or reads: (name, tensor)
+    pairs, those of tensors that are None left out.  (The library looks at every call's addresses;
+    here they have names.)"""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), writes, name)
+                   for writes, named in ((True, written), (False, read)) for name, t in named
+                   if t is not None and t.numel())
+    any_end = written_end = (0, "")
+    for begin, end, writes, name in spans:
+        before = any_end if writes else written_end
+        if begin < before[0]:
+            raise ValueError(f"{name} and {before[1]} are the same memory, or overlap")
+        any_end = max(any_end, (end, name))
+        if writes:
+            written_end = max(written_end, (end, name))
 
 
 def _options(momentum, nesterov, steps, coefficients, eps):
@@ -45,7 +54,7 @@ def orthogonalize(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, ws=
     """Each matrix of x, u / (|u|_F + eps), taken through `steps` Newton-Schulz products; bf16.
 
     x: [..., R, C], or a list of matrices [R, C] of any shapes; bf16 or fp32, contiguous CUDA.
-    out: where to write (bf16, shaped like x; may be x itself), else it is allocated.
+    out: where to write (bf16, shaped like x; may be x itself, but overlap nothing else), else it is allocated.
     coefficients: (a, b, c), or a list of them for the steps.  Returns out, without a
     gradient.  stream: the torch stream to run on, else the current one."""
     torch = _torch()
@@ -66,7 +75,10 @@ def orthogonalize(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, ws=
                               or not o.is_cuda):
             raise ValueError("out must be contiguous bf16 CUDA tensors shaped like x")
     if out is not None:
-        _distinct([f"out[{i}]" for i in range(len(outs))], outs)
+        # (an output may be its own input)
+        _apart([(f"out[{i}]", o) for i, o in enumerate(outs)],
+               [(f"x[{i}]", t) for i, (t, o) in enumerate(zip(xs, outs))
+                if o is None or t.data_ptr() != o.data_ptr() or t.dtype is not torch.bfloat16])
     device = _check_device(xs[0], stream, *xs[1:], *outs, ws)
     options = _options(0.0, False, steps, coefficients, eps)
     with _allocating(stream):
@@ -136,8 +148,8 @@ class MuonPlan:
             self.table[i] = MuonTensor(p.data_ptr(), None, None if masters[i] is None else masters[i].data_ptr(),
                                        momenta[i].data_ptr(), rows, cols, 0.0, 0.0, shape_factor(rows, cols, adjust),
                                        _dtype(p, f"params[{i}]"), 0)
-        _distinct([f"{name}[{i}]" for name in ("params", "momenta", "masters") for i in range(n)],
-                  [*params, *momenta, *masters])
+        _apart([(f"{name}[{i}]", t) for name, held in (("params", params), ("momenta", momenta), ("masters", masters))
+                for i, t in enumerate(held)])
         self._held = (list(params), list(momenta), list(masters))  # the table holds their addresses
         self._recorded = set()  # streams that _held's memory is known to be used on
         self._bytes = {}        # workspace size by which parameters have a gradient

@@ -1,5 +1,6 @@
 """What the optimizers' steps do with memory that is not theirs (stand-ins as in test_ops_devices)."""
 import contextlib
+import ctypes
 import random
 
 import pytest
@@ -126,3 +127,62 @@ def test_a_step_without_some_gradients_in_the_plans_workspace():
         flce.muon_step(plan, gs, ws=ws, check=True)
         results.append(ps + ms)
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def cut(base, at, *shape, dtype=None):
+    """A view of base's memory from element `at` on."""
+    n = shape[0] * shape[1]
+    t = base.view(-1)[at:at + n].view(shape)
+    t = (t if dtype is None else t.view(dtype)).as_subclass(Copied)
+    t.index = 0
+    return t
+
+
+def test_overlapping_memory_is_refused_by_name():
+    base = torch.zeros(64)
+    p, m = cut(base, 0, 4, 6), cut(base, 24, 4, 6)
+    flce.muon_plan([p], [m])
+    for first, second in ((cut(base, 23, 4, 6), p), (p, cut(base, 23, 4, 6))):
+        with pytest.raises(ValueError, match="overlap"):
+            flce.muon_plan([first], [second])
+    with pytest.raises(ValueError, match="overlap"):
+        flce.muon_plan([p, cut(base, 8, 2, 3)], [m, cut(base, 50, 2, 3)])
+
+
+def test_outputs_over_other_inputs_are_refused(fake):
+    base = torch.zeros(256, dtype=torch.bfloat16)
+    a, b, c = (cut(base, 32 * i, 4, 6) for i in range(3))
+    for x, out in (([a, b], [b, a]), ([a, b], [c, cut(base, 8, 4, 6)]), ([a, b], [a, cut(base, 33, 4, 6)]),
+                   ([a], [cut(base, 1, 4, 6)]), ([a, a], [a, c])):
+        with pytest.raises(ValueError, match="overlap"):
+            flce.orthogonalize(x, out=out)
+    for x, out in (([a, b], [a, b]), ([a, b], [a, c]), ([a, a], [b, c])):
+        flce.orthogonalize(x, out=out)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="addresses of nothing")
+def test_the_library_refuses_overlapping_memory():
+    """A call that is not refused gets as far as the device, which is missing (7)."""
+    L, o = binding.lib(), ctypes.byref(muon._options(0.9, True, 5, muon.COEFFICIENTS, 1e-7))
+    size = 8 * 8
+
+    def ortho(*rows, ws=0x1000000, nbytes=1 << 20):  # (x, out, dtype)
+        table = (binding.Matrix * len(rows))(*((x, out, 8, 8, code) for x, out, code in rows))
+        return L.flce_orthogonalize(table, len(rows), o, ws, nbytes, None)
+    x, y = 0x10000, 0x20000
+    assert ortho((x, y, 0)) == ortho((x, x, 0)) == ortho((x, x + 2 * size, 0)) == ortho((x, y, 0), (x, y + 2 * size, 0)) == 7
+    for rows in ([(x, x + 2, 0)], [(x, x + 2 * size - 2, 0)], [(x, x, 1)], [(x, y, 0), (y, x, 0)], [(x, y, 0), (x + 512, y + 2, 0)],
+                 [(x, x, 0), (x, y, 0)], [(x, 0x1000100, 0)], [(0x1000100, y, 0)]):
+        assert ortho(*rows) == 1, rows
+    # addresses past what a call needs of a larger workspace are nobody's
+    assert ortho((x, 0x1000000 + (1 << 19), 0)) == 7
+
+    def step(**over):
+        row = dict(param=0x10000, grad=0x20000, master=0x30000, momentum=0x40000, rows=8, cols=8, lr=0.1, weight_decay=0.0,
+                   scale=1.0, param_dtype=0, grad_dtype=0)
+        table = (binding.MuonTensor * 1)(tuple({**row, **over}.values()))
+        return L.flce_muon_step(table, 1, o, None, 0x1000000, 1 << 20, None)
+    assert step() == step(master=None) == step(grad=0x10080) == 7
+    for over in (dict(grad=0x10000), dict(grad=0x1007e), dict(momentum=0x10040), dict(master=0x400fc), dict(master=0x10000),
+                 dict(grad=0x40080), dict(momentum=0x1000000)):
+        assert step(**over) == 1, over
