@@ -79,7 +79,8 @@ typedef enum {
   FLCE_ERR_CUDA = 7,                /* a CUDA runtime/driver call failed, or no sm_100-family GPU */
   FLCE_ERR_NO_DEVICE_STATUS = 8,    /* flce_read_device_status could not read the word */
   FLCE_ERR_EXCEEDS_STATIC_SCRATCH = 9, /* flce_forward_noalloc: n above its fixed maximum */
-  FLCE_ERR_BOUNDS = 10              /* device, debug build only: an index or TMA coordinate failed its check */
+  FLCE_ERR_BOUNDS = 10,             /* device, debug build only: an index or TMA coordinate failed its check */
+  FLCE_ERR_HOST_MEMORY = 11         /* the call's tables of its matrices could not be allocated (Muon's calls) */
 } flce_status_t;
 
 typedef enum { FLCE_REDUCTION_MEAN = 0, FLCE_REDUCTION_SUM = 1, FLCE_REDUCTION_NONE = 2 } flce_reduction_t;

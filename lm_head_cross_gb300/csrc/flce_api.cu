@@ -2454,7 +2454,7 @@ flce_status_t flce_orthogonalize(const flce_matrix_t* matrices, int32_t count, c
   }
   return run_muon(items, *opt, nullptr, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 } catch (...) {
-  return FLCE_ERR_CUDA;  // (host memory)
+  return FLCE_ERR_HOST_MEMORY;
 }
 
 flce_status_t flce_muon_step(const flce_muon_tensor_t* tensors, int32_t count, const flce_muon_t* opt,
@@ -2476,7 +2476,7 @@ flce_status_t flce_muon_step(const flce_muon_tensor_t* tensors, int32_t count, c
   }
   return run_muon(items, *opt, grad_scale, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 } catch (...) {
-  return FLCE_ERR_CUDA;  // (host memory)
+  return FLCE_ERR_HOST_MEMORY;
 }
 
 flce_status_t flce_profile_enable(int mask) {
@@ -2519,6 +2519,7 @@ const char* flce_status_string(flce_status_t s) {
     case FLCE_ERR_NO_DEVICE_STATUS: return "could not read the device status word";
     case FLCE_ERR_EXCEEDS_STATIC_SCRATCH: return "n exceeds the fixed scratch of flce_forward_noalloc (32768 rows)";
     case FLCE_ERR_BOUNDS: return "device: an index or TMA coordinate failed a check of the debug build";
+    case FLCE_ERR_HOST_MEMORY: return "host memory for the call's tables could not be allocated";
     default: return "unknown status";
   }
 }

@@ -1,7 +1,10 @@
 """What the optimizers' steps do with memory that is not theirs (stand-ins as in test_ops_devices)."""
 import contextlib
 import ctypes
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 
@@ -186,3 +189,25 @@ def test_the_library_refuses_overlapping_memory():
     for over in (dict(grad=0x10000), dict(grad=0x1007e), dict(momentum=0x10040), dict(master=0x400fc), dict(master=0x10000),
                  dict(grad=0x40080), dict(momentum=0x1000000)):
         assert step(**over) == 1, over
+
+
+CHILD = """
+import ctypes, resource
+import lm_head_cross_gb300 as flce
+from lm_head_cross_gb300 import binding, muon
+L, o, n = binding.lib(), muon._options(0.9, True, 5, muon.COEFFICIENTS, 1e-7), 1 << 20
+matrices, tensors = (binding.Matrix * n)(), (binding.MuonTensor * n)()
+size = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (size + (32 << 20), resource.getrlimit(resource.RLIMIT_AS)[1]))
+print(L.flce_orthogonalize(matrices, n, ctypes.byref(o), 0x1000000, 256, None),
+      L.flce_muon_step(tensors, n, ctypes.byref(o), None, 0x1000000, 256, None),
+      L.flce_muon_workspace_bytes(tensors, n), binding.status_string(11))
+"""
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="where an allocation does not fail the call ends at the missing device")
+def test_host_memory_that_is_missing_is_a_status():
+    r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.startswith("11 11 0 host memory"), r.stdout
