@@ -2331,18 +2331,19 @@ flce_status_t run_muon_round(const std::vector<MuonItem>& items, const MuonRound
 // Whether what a call writes (outputs, or weights and momenta, and its workspace) overlaps nothing
 // else that it reads or writes.  An output may be its own bf16 input: that is read before it is written,
 // which of other matrices' inputs holds within a round alone.  (449 ranges in 9 us.)
-bool muon_apart(const std::vector<MuonItem>& items, const void* ws, size_t ws_bytes) {
+bool muon_apart(const std::vector<MuonItem>& items, const float* grad_scale, const void* ws, size_t ws_bytes) {
   struct Range {
     uintptr_t begin, end;
     bool written;
   };
   std::vector<Range> all;
-  all.reserve(4 * items.size() + 1);
+  all.reserve(4 * items.size() + 2);
   auto add = [&](const void* p, int64_t elements, bool f32, bool written) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
     if (p) all.push_back(Range{at, at + static_cast<uintptr_t>(elements) * (f32 ? 4 : 2), written});
   };
   all.push_back(Range{reinterpret_cast<uintptr_t>(ws), reinterpret_cast<uintptr_t>(ws) + ws_bytes, true});
+  add(grad_scale, 1, true, false);
   for (const MuonItem& m : items) {
     const int64_t n = m.rows * m.cols;
     if (n == 0) continue;
@@ -2370,7 +2371,7 @@ flce_status_t run_muon(const std::vector<MuonItem>& items, const flce_muon_t& o,
   const std::vector<MuonRound> rounds = muon_rounds(items);
   const size_t bytes = muon_bytes(rounds);
   if (ws_bytes < bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
-  if (!muon_apart(items, ws, bytes)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!muon_apart(items, grad_scale, ws, bytes)) return FLCE_ERR_INVALID_ARGUMENT;
   uint8_t* base = static_cast<uint8_t*>(ws);
   if (rounds.empty()) return cuda_status(cudaMemsetAsync(ws, 0, kAlign, s));
   Device dev;

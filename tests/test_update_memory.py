@@ -180,14 +180,14 @@ def test_the_library_refuses_overlapping_memory():
     # addresses past what a call needs of a larger workspace are nobody's
     assert ortho((x, 0x1000000 + (1 << 19), 0)) == 7
 
-    def step(**over):
+    def step(gs=None, **over):
         row = dict(param=0x10000, grad=0x20000, master=0x30000, momentum=0x40000, rows=8, cols=8, lr=0.1, weight_decay=0.0,
                    scale=1.0, param_dtype=0, grad_dtype=0)
         table = (binding.MuonTensor * 1)(tuple({**row, **over}.values()))
-        return L.flce_muon_step(table, 1, o, None, 0x1000000, 1 << 20, None)
-    assert step() == step(master=None) == step(grad=0x10080) == 7
+        return L.flce_muon_step(table, 1, o, gs, 0x1000000, 1 << 20, None)
+    assert step() == step(master=None) == step(grad=0x10080) == step(gs=0x20000) == step(gs=0x10080) == 7
     for over in (dict(grad=0x10000), dict(grad=0x1007e), dict(momentum=0x10040), dict(master=0x400fc), dict(master=0x10000),
-                 dict(grad=0x40080), dict(momentum=0x1000000)):
+                 dict(grad=0x40080), dict(momentum=0x1000000), dict(gs=0x1007c), dict(gs=0x40000)):
         assert step(**over) == 1, over
 
 
