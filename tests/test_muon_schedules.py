@@ -171,3 +171,24 @@ def test_the_largest_singular_value_and_shift(r, c, second):
     u = with_values(r, c, [1.0] + [1e-3] * (min(r, c) - 1)).cuda()
     error, floor = off(u, [(2.05, 0.0, 0.0), second])
     assert error <= (PROMISE if min(r, c) <= 128 else PROMISE_EQUAL) + floor
+
+
+@pytest.mark.gpu
+def test_many_steps_captured_and_replayed():
+    """Small matrices' further reads of X and larger ones' pairs in a graph, with a workspace of any content."""
+    xs = [matrix(r, c, "strong", r).cuda() for r, c in ((200, 300), (40, 60), (128, 640))]
+    table = (binding.Matrix * 3)(*((1, 1, *x.shape, 1) for x in xs))
+    ws = torch.full((flce.lib().flce_orthogonalize_workspace_bytes(table, 3),), 255, dtype=torch.uint8, device="cuda")
+    out = [torch.empty_like(x, dtype=torch.bfloat16) for x in xs]
+    flce.orthogonalize(xs, steps=11, out=out, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        flce.orthogonalize(xs, steps=11, out=out, ws=ws)
+    for k in range(3):
+        for x in xs:
+            x.copy_(matrix(*x.shape, "rank8", k))
+        graph.replay()
+        for y, z in zip(out, flce.orthogonalize(xs, steps=11)):
+            assert torch.equal(y, z)
+    assert flce.read_device_status(ws) == 0
