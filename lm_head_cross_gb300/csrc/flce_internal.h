@@ -455,15 +455,16 @@ constexpr int kMuonFewGroups = 2, kMuonFewMatrices = 16;
 constexpr int kMuonChunk = 8192;     // elements of one block of the momentum's pass
 constexpr int kMuonStrip = 4096;     // and of the passes between a tensor and X
 constexpr int kMuonExactRows = 128;  // up to this many rows or columns: pairs of fp16, steps on X X^T alone
+constexpr int kMuonSplitBlocks = 8;  // of 64 elements, of one part of their X X^T
+constexpr int kMuonSplitsMost = 64;
 // The steps on X X^T go on until singular values may have grown this much, then X is read again: an
 // error d of an eigenvalue grows with the square of what singular values do, and counts as
 // |b| / a d 144^2 then in the weakest directions' factor.  d is up to 2^-22 by its pair and 5e-8 by fp32 sums:
 // 2e-3 to 7e-3 of these directions.  The usual coefficients reach 141 before the fifth step, 485
 // before a sixth, which on 128 x 128 with strong directions is off by 1e-3, an eighth step
-// by 2e-2 and a twelfth by infinities; with reads every five steps 1e-4 for all (simulated).
+// by 2e-2 and a twelfth by infinities (simulated); with reads every five steps by 4e-4, 5e-4, 9e-4
+// (measured).  A read is three launches, 20 us of the 101 of 6 steps there.
 constexpr double kMuonReadGrowth = 144.0;
-constexpr int kMuonSplitBlocks = 8;  // of 64 elements, of one part of their X X^T
-constexpr int kMuonSplitsMost = 64;
 // Larger matrices' iterates are pairs too, but for the last: a rounding to one fp16 leaves 2e-4 of
 // X's norm in its weak directions, which the remaining steps multiply by up to their slopes at 0.  Iterates are
 // single from where these products add up to at most 16 (usual coefficients: the last two, 3.4 + 11.9; the

@@ -38,8 +38,8 @@
 // and one block holds all of A, P and the product Q of the P: there every operand is a pair, each
 // product hi hi + hi lo + lo hi, and the steps run on A alone,
 //   P = a I + b A + c A^2,   Q <- P Q,   A <- P A P,
-// X being read twice, for X X^T and for Q X: 1e-4 of the result, up to 2e-3 where strong
-// directions outweigh weak ones 1000 to 1.  A's rounding hides the squares of weak singular
+// X being read twice, for X X^T and for Q X: 1e-5 to 5e-4 of the result, 2e-3 where one direction
+// holds nearly all of it.  A's rounding hides the squares of weak singular
 // values, so after as many steps as that bears (kMuonReadGrowth; the usual coefficients' five)
 // X <- Q X and the next steps start from a new X X^T.
 #include <cuda_fp16.h>

@@ -55,8 +55,9 @@ def orthogonalize(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, ws=
 
     x: [..., R, C], or a list of matrices [R, C] of any shapes; bf16 or fp32, contiguous CUDA.
     out: where to write (bf16, shaped like x; may be x itself, but overlap nothing else), else it is allocated.
-    coefficients: (a, b, c), or a list of them for the steps.  Returns out, without a
-    gradient.  stream: the torch stream to run on, else the current one."""
+    coefficients: (a, b, c), or a list of them for the steps, which keep singular values within 2.1.
+    Products take fp16 operands, pairs of them up to 128 rows or columns (the header says what their
+    rounding leaves).  Returns out, without a gradient.  stream: the torch stream to run on, else the current one."""
     torch = _torch()
     listed = isinstance(x, (list, tuple))
     xs = list(x) if listed else [x]
