@@ -211,3 +211,20 @@ def test_host_memory_that_is_missing_is_a_status():
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr
     assert r.stdout.startswith("11 11 0 host memory"), r.stdout
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="memory of the host")
+def test_parameters_that_came_to_share_memory_are_refused(monkeypatch):
+    """New storage is looked at by the step: two parameters that were tied after the plan was made."""
+    monkeypatch.setattr(binding, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(muon, "_stream_ptr", lambda *a: None)
+    base = torch.zeros(96)
+    plan = flce.muon_plan([cut(base, 0, 4, 6), cut(base, 24, 4, 6)], [stand_in(4, 6), stand_in(4, 6)])
+    room = torch.zeros(plan.workspace_bytes() + 256, dtype=torch.uint8)
+    ws = room[-room.data_ptr() % 256:].as_subclass(Copied)
+    ws.index = 0
+    for second, code in ((cut(base, 48, 4, 6), 7), (cut(base, 12, 4, 6), 1), (cut(base, 0, 4, 6), 1)):
+        plan.set_param(1, second)
+        with pytest.raises(flce.FlceError) as e:
+            flce.muon_step(plan, [stand_in(4, 6), stand_in(4, 6)], ws=ws)
+        assert e.value.code == code
